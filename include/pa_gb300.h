@@ -71,6 +71,8 @@ typedef enum pa_status {
 #define PA_DEVERR_SLOT_MISMATCH 0x40u /* fused store: slot_mapping[t] >= 0 is not the cache row
                                          of token t's own position (row still written) */
 
+#define PA_DEVERR_NO_BLOCKS 0x80u /* prepare: the free list ran out (sequences end at their last block) */
+
 /* Human-readable name of a status code (static storage). */
 const char *pa_status_string(pa_status status);
 
@@ -371,6 +373,125 @@ pa_status pa_varlen_prefill_fp8(void *out, const void *q, const void *key, const
                                 int max_seqlen_k, int64_t num_blocks, int block_size,
                                 int num_heads, int num_kv_heads, int head_dim,
                                 int sliding_window, float scale, float kv_scale, void *stream);
+
+/*
+ * The serving step over a 4-bit KV cache: pa_prepare_step, pa_store_kvcache_fp4 (or the
+ * stores inside the attention calls), pa_varlen_prefill_fp4 / pa_decode_fp4 and
+ * pa_release_blocks, with pa_gather_kvcache_fp4 to read rows back.
+ *
+ * pa_prepare_step - the metadata of a step from the requests' lengths, on the GPU ("05
+ * Attention Backends", section 4: seq_len = context_len + query_len, and Q&A 2: slot =
+ * block_table[i][p / block_size] * block_size + p % block_size).  The pool's free blocks are
+ * a stack in device memory: free_blocks[0 .. *num_free) are the ids nobody holds.  With
+ * c_i = context_lens[i], q_i = query_lens[i]:
+ *     have_i = ceil(c_i / block_size), need_i = ceil((c_i + q_i) / block_size) - have_i;
+ *     the need_i new blocks of request 0, 1, ... are taken from the end of the stack, one by
+ *     one in that order, into block_table[i][have_i ..];
+ *     seq_lens[i] = c_i + q_i;  cu_seqlens_q = exclusive prefix sum of q (num_seqs + 1);
+ *     token t of request i: positions[t] = p = c_i + t - cu_seqlens_q[i] and
+ *     slot_mapping[t] = its slot; entries from the last token to max_tokens get position 0
+ *     and slot -1 (padding, which every store skips).
+ *     *num_free_out = *num_free minus the blocks taken.
+ * A request may have no new tokens (q_i = 0) or nothing cached.  No other table entry is
+ * read (but the block that holds position c_i - 1 when that block is not full) or written.
+ *
+ *   block_table   [num_seqs, max_num_blocks] int32, device, updated in place
+ *   seq_lens      [num_seqs], cu_seqlens_q [num_seqs + 1], slot_mapping [max_tokens],
+ *                 positions [max_tokens] (or NULL), num_free_out [1]: int32, device, written
+ *   context_lens, query_lens [num_seqs], free_blocks [num_blocks], num_free [1]: int32, device
+ * num_free_out may be num_free and seq_lens may be context_lens (updated in place, as a
+ * captured graph of a decode step wants it); no other buffers may overlap.
+ * Out of blocks: PA_DEVERR_NO_BLOCKS; the blocks that are left go to the first requests, the
+ * tokens without a block get slot -1, and seq_lens[i] ends with the last block the request
+ * holds (less than c_i + q_i: the caller's sign to preempt it; the attention of such a
+ * request in this step is not meaningful).  Negative or too long lengths are clamped to the
+ * row and flagged PA_DEVERR_SEQ_RANGE / PA_DEVERR_QUERY_LEN (more than max_tokens tokens
+ * too; cu_seqlens_q then ends at max_tokens); bad block ids give -1 and
+ * PA_DEVERR_BLOCK_RANGE.
+ * Supported: block_size a power of two in [1, 1024]; num_seqs <= 16384; num_blocks *
+ * block_size and max_tokens below 2^31.  No workspace.
+ *
+ * pa_release_blocks - the blocks of finished requests return to the stack: for every i with
+ * finished[i] != 0, in order, entries 0 .. ceil(seq_lens[i] / block_size) - 1 of row i are
+ * appended to free_blocks, seq_lens_out[i] = 0 (other rows: seq_lens[i]), and *num_free_out =
+ * *num_free plus their number.  The table is left as it is.  Blocks that several rows share
+ * (a common prefix) are the caller's to release once.  num_free_out may be num_free and
+ * seq_lens_out may be seq_lens.  Entries out of range, or beyond the pool's num_blocks ids,
+ * are flagged PA_DEVERR_BLOCK_RANGE.  Limits as pa_prepare_step.
+ */
+pa_status pa_prepare_step(int32_t *block_table, int32_t *seq_lens, int32_t *cu_seqlens_q,
+                          int32_t *slot_mapping, int32_t *positions, int32_t *num_free_out,
+                          const int32_t *context_lens, const int32_t *query_lens,
+                          const int32_t *free_blocks, const int32_t *num_free, int num_seqs,
+                          int max_num_blocks, int64_t max_tokens, int64_t num_blocks,
+                          int block_size, void *stream);
+pa_status pa_release_blocks(int32_t *free_blocks, int32_t *num_free_out, int32_t *seq_lens_out,
+                            const int32_t *finished, const int32_t *seq_lens,
+                            const int32_t *block_table, const int32_t *num_free, int num_seqs,
+                            int max_num_blocks, int64_t num_blocks, int block_size, void *stream);
+
+/*
+ * 4-bit KV cache.  This library's own format: E2M1 codes with an E4M3 scale for each 16 dims.
+ * k_cache and v_cache are [num_blocks, num_kv_heads, block_size, head_dim / 2 + head_dim / 16]
+ * bytes (72 at head_dim 128, 36 at 64), 16-byte aligned.  A row is one token of one kv head:
+ * head_dim / 2 bytes of codes (dim 2 i in the low four bits of byte i, dim 2 i + 1 in the high
+ * four), then head_dim / 16 scales.  An element reads
+ *     code * scale * kv_scale,
+ * code in {0, .5, 1, 1.5, 2, 3, 4, 6} with a sign (bit 3).  kv_scale is one number a cache,
+ * in [1e-30, 1e30].  The store of 16 values x with the largest magnitude a:
+ *     scale = max(E4M3(a / (6 kv_scale)), 2^-9),   code = E2M1(x / (scale * kv_scale)),
+ * each division and product one fp32 operation, each conversion to the nearest (ties to
+ * even), saturating at 448 and 6.  A NaN makes its group's scale NaN; an infinity saturates.
+ *
+ * pa_store_kvcache_fp4: as pa_store_kvcache.  Distinct slots are written by disjoint stores;
+ *     no other byte of the cache changes.
+ * pa_gather_kvcache_fp4: the rows of slot_mapping read back: key[t] / value[t] [num_kv_heads,
+ *     head_dim] bf16 (rounded to nearest); a negative slot gives zeros (one past the pool too,
+ *     flagged PA_DEVERR_SLOT_RANGE).
+ * pa_decode_fp4: as pa_decode (optional store included).  The work of all sequences is cut
+ *     evenly, so a row's last bits may depend on the other sequences' lengths; equal calls
+ *     give equal bits.  The products run in f16: every
+ *     code * scale is an f16, q is rounded to f16 once (exactly for |q| in [2^-14, 65504],
+ *     clamped beyond) and so are the softmax weights; sums are fp32.
+ * pa_varlen_prefill_fp4: as pa_varlen_prefill; single-row sequences run on the decode kernel
+ *     when seq_lens is given, in the workspace.
+ *
+ *   workspace  at least pa_decode_fp4_workspace_size(...) /
+ *              pa_varlen_prefill_fp4_workspace_size(...) bytes, 256-byte aligned (may be NULL
+ *              when that is 0); its contents on entry do not matter; two calls that may
+ *              overlap on the GPU need one each
+ * Supported: head_dim in {64, 128}; block_size a power of two in [16, 256]; num_blocks *
+ * block_size below 2^31; num_heads / num_kv_heads <= 64; batch, num_seqs <= 65535; scale
+ * positive and finite.
+ */
+pa_status pa_store_kvcache_fp4(const void *key, const void *value, void *k_cache, void *v_cache,
+                               const int32_t *slot_mapping, int64_t num_tokens,
+                               int64_t num_blocks, int block_size, int num_kv_heads,
+                               int head_dim, float kv_scale, void *stream);
+pa_status pa_gather_kvcache_fp4(void *key, void *value, const void *k_cache, const void *v_cache,
+                                const int32_t *slot_mapping, int64_t num_tokens,
+                                int64_t num_blocks, int block_size, int num_kv_heads,
+                                int head_dim, float kv_scale, void *stream);
+size_t pa_decode_fp4_workspace_size(int batch, int num_heads, int num_kv_heads, int head_dim,
+                                    int max_seq_len, int sliding_window);
+pa_status pa_decode_fp4(void *out, const void *q, const void *key, const void *value,
+                        const int32_t *slot_mapping, void *k_cache, void *v_cache,
+                        const int32_t *block_table, int max_num_blocks, const int32_t *seq_lens,
+                        int batch, int max_seq_len, int64_t num_blocks, int block_size,
+                        int num_heads, int num_kv_heads, int head_dim, int sliding_window,
+                        float scale, float kv_scale, void *workspace, size_t workspace_bytes,
+                        void *stream);
+size_t pa_varlen_prefill_fp4_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                            int head_dim, int max_seqlen_k, int sliding_window);
+pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const void *value,
+                                const int32_t *slot_mapping, void *k_cache, void *v_cache,
+                                const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                const int32_t *seq_lens, const int32_t *block_table,
+                                int max_num_blocks, int num_seqs, int total_q, int max_seqlen_q,
+                                int max_seqlen_k, int64_t num_blocks, int block_size,
+                                int num_heads, int num_kv_heads, int head_dim,
+                                int sliding_window, float scale, float kv_scale, void *workspace,
+                                size_t workspace_bytes, void *stream);
 
 /*
  * pa_read_device_error - synchronise `stream`, then return in *flags the device

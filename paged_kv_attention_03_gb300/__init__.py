@@ -8,6 +8,7 @@ does, and raises if it is missing.
 """
 from ._lib import (  # noqa: F401
     DEVERR_BLOCK_RANGE,
+    DEVERR_NO_BLOCKS,
     DEVERR_QUERY_LEN,
     DEVERR_SEQ_RANGE,
     DEVERR_SEQLENS_K,
@@ -31,7 +32,13 @@ from ._lib import (  # noqa: F401
     pa_cascade_decode,
     pa_cascade_decode_workspace_size,
     pa_common_prefix_blocks,
+    pa_decode_fp4,
+    pa_decode_fp4_workspace_size,
     pa_decode_fp8,
+    pa_gather_kvcache_fp4,
+    pa_prepare_step,
+    pa_release_blocks,
+    pa_store_kvcache_fp4,
     pa_store_kvcache_fp8,
     pa_decode_num_splits,
     pa_decode_workspace_size,
@@ -39,6 +46,8 @@ from ._lib import (  # noqa: F401
     pa_debug_prefill_stall,
     pa_store_kvcache,
     pa_varlen_prefill,
+    pa_varlen_prefill_fp4,
+    pa_varlen_prefill_fp4_workspace_size,
     pa_varlen_prefill_fp8,
     status_string,
     version,

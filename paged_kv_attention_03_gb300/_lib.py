@@ -28,6 +28,7 @@ DEVERR_QUERY_LEN = 0x8
 DEVERR_SEQLENS_K = 0x10
 DEVERR_TIMEOUT = 0x20
 DEVERR_SLOT_MISMATCH = 0x40
+DEVERR_NO_BLOCKS = 0x80
 
 EXPORTED = ("pa_status_string", "pa_version", "pa_store_kvcache", "pa_decode_num_splits",
             "pa_decode_workspace_size", "pa_decode", "pa_varlen_prefill",
@@ -35,7 +36,9 @@ EXPORTED = ("pa_status_string", "pa_version", "pa_store_kvcache", "pa_decode_num
             "pa_decode_state_workspace_size", "pa_decode_state", "pa_merge_states",
             "pa_cascade_decode_workspace_size", "pa_cascade_decode", "pa_common_prefix_blocks",
             "pa_store_kvcache_fp8", "pa_decode_fp8", "pa_debug_prefill_stall",
-            "pa_varlen_prefill_fp8")
+            "pa_varlen_prefill_fp8", "pa_prepare_step", "pa_release_blocks",
+            "pa_store_kvcache_fp4", "pa_gather_kvcache_fp4", "pa_decode_fp4_workspace_size",
+            "pa_decode_fp4", "pa_varlen_prefill_fp4_workspace_size", "pa_varlen_prefill_fp4")
 
 
 class PAError(RuntimeError):
@@ -103,6 +106,22 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.pa_decode_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i64,
                                       i32, i32, i32, i32, i32, f32, f32, i32, vp, sz, vp]
         lib.pa_decode_fp8.restype = ctypes.c_int
+        lib.pa_prepare_step.argtypes = [vp] * 10 + [i32, i32, i64, i64, i32, vp]
+        lib.pa_prepare_step.restype = ctypes.c_int
+        lib.pa_release_blocks.argtypes = [vp] * 7 + [i32, i32, i64, i32, vp]
+        lib.pa_release_blocks.restype = ctypes.c_int
+        for fn in (lib.pa_store_kvcache_fp4, lib.pa_gather_kvcache_fp4):
+            fn.argtypes = [vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, f32, vp]
+            fn.restype = ctypes.c_int
+        for fn in (lib.pa_decode_fp4_workspace_size, lib.pa_varlen_prefill_fp4_workspace_size):
+            fn.argtypes = [i32] * 6
+            fn.restype = sz
+        lib.pa_decode_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i64, i32,
+                                      i32, i32, i32, i32, f32, f32, vp, sz, vp]
+        lib.pa_decode_fp4.restype = ctypes.c_int
+        lib.pa_varlen_prefill_fp4.argtypes = [vp] * 11 + [i32, i32, i32, i32, i32, i64, i32, i32,
+                                                          i32, i32, i32, f32, f32, vp, sz, vp]
+        lib.pa_varlen_prefill_fp4.restype = ctypes.c_int
         lib.pa_read_device_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
         lib.pa_read_device_error.restype = ctypes.c_int
         _lib = lib
@@ -276,6 +295,242 @@ def pa_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                head_dim, int(sliding_window), float(scale), float(kv_scale),
                                int(num_splits), ws_ptr, ws_bytes, _stream(dev))
     _check(st, "pa_decode_fp8")
+    return out
+
+
+def _need_i32(dev: torch.device, **tensors) -> None:
+    for name, t in tensors.items():
+        _need(t, torch.int32, name, dev)
+
+
+def _one(num_free: torch.Tensor, name: str) -> None:
+    if num_free.numel() != 1:
+        raise ValueError(f"{name} must have one entry")
+
+
+def pa_prepare_step(context_lens: torch.Tensor, query_lens: torch.Tensor,
+                    block_table: torch.Tensor, free_blocks: torch.Tensor,
+                    num_free: torch.Tensor, block_size: int, max_tokens: int,
+                    seq_lens: torch.Tensor | None = None,
+                    cu_seqlens_q: torch.Tensor | None = None,
+                    slot_mapping: torch.Tensor | None = None,
+                    positions: torch.Tensor | None = None,
+                    num_free_out: torch.Tensor | None = None) -> tuple[torch.Tensor, ...]:
+    """The metadata of one step from the requests' lengths (int32 on the GPU): takes the new
+    blocks from the end of free_blocks[:num_free] into block_table (in place) and returns
+    (seq_lens [S], cu_seqlens_q [S + 1], slot_mapping [max_tokens], positions [max_tokens],
+    num_free_out [1]).  num_free_out may be num_free and seq_lens may be context_lens."""
+    lib = load()
+    dev = block_table.device
+    _need_i32(dev, context_lens=context_lens, query_lens=query_lens, block_table=block_table,
+              free_blocks=free_blocks, num_free=num_free)
+    n = context_lens.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != n or query_lens.shape != (n,) \
+            or context_lens.dim() != 1 or free_blocks.dim() != 1:
+        raise ValueError("pa_prepare_step: inconsistent shapes")
+    _one(num_free, "num_free")
+    max_tokens = int(max_tokens)
+    seq_lens = _out(seq_lens, (n,), torch.int32, dev, "seq_lens")
+    cu_seqlens_q = _out(cu_seqlens_q, (n + 1,), torch.int32, dev, "cu_seqlens_q")
+    slot_mapping = _out(slot_mapping, (max(max_tokens, 0),), torch.int32, dev, "slot_mapping")
+    positions = _out(positions, (max(max_tokens, 0),), torch.int32, dev, "positions")
+    num_free_out = _out(num_free_out, (1,), torch.int32, dev, "num_free_out")
+    with _on(dev):
+        st = lib.pa_prepare_step(_ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens_q),
+                                 _ptr(slot_mapping), _ptr(positions), _ptr(num_free_out),
+                                 _ptr(context_lens), _ptr(query_lens), _ptr(free_blocks),
+                                 _ptr(num_free), n, block_table.shape[1], max_tokens,
+                                 free_blocks.shape[0], block_size, _stream(dev))
+    _check(st, "pa_prepare_step")
+    return seq_lens, cu_seqlens_q, slot_mapping, positions, num_free_out
+
+
+def pa_release_blocks(finished: torch.Tensor, seq_lens: torch.Tensor, block_table: torch.Tensor,
+                      free_blocks: torch.Tensor, num_free: torch.Tensor, block_size: int,
+                      seq_lens_out: torch.Tensor | None = None,
+                      num_free_out: torch.Tensor | None = None
+                      ) -> tuple[torch.Tensor, torch.Tensor]:
+    """Append the blocks of the rows with finished != 0 (int32) to free_blocks[:num_free] (in
+    place) and return (seq_lens_out [S], 0 for those rows, num_free_out [1]).  The outputs may
+    be seq_lens and num_free."""
+    lib = load()
+    dev = block_table.device
+    _need_i32(dev, finished=finished, seq_lens=seq_lens, block_table=block_table,
+              free_blocks=free_blocks, num_free=num_free)
+    n = seq_lens.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != n or finished.shape != (n,) \
+            or seq_lens.dim() != 1 or free_blocks.dim() != 1:
+        raise ValueError("pa_release_blocks: inconsistent shapes")
+    _one(num_free, "num_free")
+    seq_lens_out = _out(seq_lens_out, (n,), torch.int32, dev, "seq_lens_out")
+    num_free_out = _out(num_free_out, (1,), torch.int32, dev, "num_free_out")
+    with _on(dev):
+        st = lib.pa_release_blocks(_ptr(free_blocks), _ptr(num_free_out), _ptr(seq_lens_out),
+                                   _ptr(finished), _ptr(seq_lens), _ptr(block_table),
+                                   _ptr(num_free), n, block_table.shape[1],
+                                   free_blocks.shape[0], block_size, _stream(dev))
+    _check(st, "pa_release_blocks")
+    return seq_lens_out, num_free_out
+
+
+def _fp4_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: torch.device,
+               what: str) -> tuple[int, int, int, int]:
+    """(num_blocks, num_kv_heads, block_size, head_dim) of 4-bit caches, uint8
+    [num_blocks, num_kv_heads, block_size, head_dim / 2 + head_dim / 16]."""
+    _need(k_cache, torch.uint8, "k_cache", dev)
+    _need(v_cache, torch.uint8, "v_cache", dev)
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[3] % 9:
+        raise ValueError(f"{what}: 4-bit caches are [num_blocks, num_kv_heads, block_size, "
+                         "head_dim / 2 + head_dim / 16] bytes")
+    nb, hkv, bs, row = k_cache.shape
+    return nb, hkv, bs, row // 9 * 16
+
+
+def pa_store_kvcache_fp4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor,
+                         v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                         kv_scale: float) -> None:
+    """Quantise key/value [T, Hkv, D] bf16 into 4-bit caches (uint8 [NB, Hkv, bs, D/2 + D/16]:
+    E2M1 codes, then an E4M3 scale for each 16 dims) at slot_mapping [T] (< 0: skipped)."""
+    lib = load()
+    dev = k_cache.device
+    nb, hkv, bs, d = _fp4_cache(k_cache, v_cache, dev, "pa_store_kvcache_fp4")
+    _need(key, torch.bfloat16, "key", dev)
+    _need(value, torch.bfloat16, "value", dev)
+    _need(slot_mapping, torch.int32, "slot_mapping", dev)
+    if key.dim() != 3 or key.shape != value.shape or key.shape[1:] != (hkv, d) \
+            or slot_mapping.shape != key.shape[:1]:
+        raise ValueError("pa_store_kvcache_fp4: inconsistent shapes")
+    with _on(dev):
+        st = lib.pa_store_kvcache_fp4(_ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache),
+                                      _ptr(slot_mapping), key.shape[0], nb, bs, hkv, d,
+                                      kv_scale, _stream(dev))
+    _check(st, "pa_store_kvcache_fp4")
+
+
+def pa_gather_kvcache_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          slot_mapping: torch.Tensor, kv_scale: float,
+                          key: torch.Tensor | None = None, value: torch.Tensor | None = None
+                          ) -> tuple[torch.Tensor, torch.Tensor]:
+    """Read rows of 4-bit caches back: (key, value) [T, Hkv, D] bf16 of slot_mapping [T], zeros
+    for a negative slot."""
+    lib = load()
+    dev = k_cache.device
+    nb, hkv, bs, d = _fp4_cache(k_cache, v_cache, dev, "pa_gather_kvcache_fp4")
+    _need(slot_mapping, torch.int32, "slot_mapping", dev)
+    if slot_mapping.dim() != 1:
+        raise ValueError("pa_gather_kvcache_fp4: slot_mapping must be one-dimensional")
+    n = slot_mapping.shape[0]
+    key = _out(key, (n, hkv, d), torch.bfloat16, dev, "key")
+    value = _out(value, (n, hkv, d), torch.bfloat16, dev, "value")
+    with _on(dev):
+        st = lib.pa_gather_kvcache_fp4(_ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache),
+                                       _ptr(slot_mapping), n, nb, bs, hkv, d, kv_scale,
+                                       _stream(dev))
+    _check(st, "pa_gather_kvcache_fp4")
+    return key, value
+
+
+@functools.lru_cache(maxsize=1024)
+def pa_decode_fp4_workspace_size(batch: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                                 max_seq_len: int, sliding_window: int = 0) -> int:
+    return int(load().pa_decode_fp4_workspace_size(batch, num_heads, num_kv_heads, head_dim,
+                                                   max_seq_len, sliding_window))
+
+
+@functools.lru_cache(maxsize=1024)
+def pa_varlen_prefill_fp4_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int,
+                                         head_dim: int, max_seqlen_k: int,
+                                         sliding_window: int = 0) -> int:
+    return int(load().pa_varlen_prefill_fp4_workspace_size(num_seqs, num_heads, num_kv_heads,
+                                                           head_dim, max_seqlen_k,
+                                                           sliding_window))
+
+
+def _workspace(workspace: torch.Tensor | None, need: int, dev: torch.device):
+    """(pointer, bytes) of a caller's scratch that is large enough, or of a new one; the tensor
+    is returned too, so that it lives until the call is queued."""
+    if need == 0:
+        return None, 0, None
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev:
+        raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
+    return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
+
+
+def pa_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                  block_table: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                  scale: float, kv_scale: float, sliding_window: int = 0,
+                  key: torch.Tensor | None = None, value: torch.Tensor | None = None,
+                  slot_mapping: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Paged decode over 4-bit caches (uint8 [NB, Hkv, bs, D/2 + D/16], elements
+    code * scale * kv_scale): q [B, H, D] -> out [B, H, D].  New tokens, when given, are
+    quantised into the caches in the same launch."""
+    lib = load()
+    dev = q.device
+    nb, hkv, bs, d = _fp4_cache(k_cache, v_cache, dev, "pa_decode_fp4")
+    _need(q, torch.bfloat16, "q", dev)
+    _need(block_table, torch.int32, "block_table", dev)
+    _need(seq_lens, torch.int32, "seq_lens", dev)
+    batch, num_heads, head_dim = q.shape
+    if d != head_dim or block_table.dim() != 2 or block_table.shape[0] != batch \
+            or seq_lens.shape != (batch,):
+        raise ValueError("pa_decode_fp4: inconsistent shapes")
+    _new_tokens(key, value, slot_mapping, batch, hkv, head_dim, dev, "pa_decode_fp4")
+    out = _out(out, q.shape, torch.bfloat16, dev)
+    ws, ws_bytes, workspace = _workspace(
+        workspace, pa_decode_fp4_workspace_size(batch, num_heads, hkv, head_dim, max_seq_len,
+                                                sliding_window), dev)
+    with _on(dev):
+        st = lib.pa_decode_fp4(_ptr(out), _ptr(q), _ptr(key), _ptr(value), _ptr(slot_mapping),
+                               _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
+                               block_table.shape[1], _ptr(seq_lens), batch, max_seq_len, nb, bs,
+                               num_heads, hkv, head_dim, sliding_window, scale, kv_scale, ws,
+                               ws_bytes, _stream(dev))
+    _check(st, "pa_decode_fp4")
+    return out
+
+
+def pa_varlen_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          cu_seqlens_q: torch.Tensor, seq_lens: torch.Tensor | None,
+                          block_table: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int,
+                          scale: float, kv_scale: float, sliding_window: int = 0,
+                          cu_seqlens_k: torch.Tensor | None = None,
+                          key: torch.Tensor | None = None, value: torch.Tensor | None = None,
+                          slot_mapping: torch.Tensor | None = None,
+                          out: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """pa_varlen_prefill over 4-bit caches (as pa_decode_fp4): q [Tq, H, D] -> out [Tq, H, D].
+    New tokens, when given, are quantised into the caches first."""
+    lib = load()
+    dev = q.device
+    nb, hkv, bs, d = _fp4_cache(k_cache, v_cache, dev, "pa_varlen_prefill_fp4")
+    _need(q, torch.bfloat16, "q", dev)
+    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q", dev)
+    _need(block_table, torch.int32, "block_table", dev)
+    total_q, num_heads, head_dim = q.shape
+    num_seqs = cu_seqlens_q.shape[0] - 1
+    if d != head_dim or block_table.dim() != 2 or block_table.shape[0] != num_seqs:
+        raise ValueError("pa_varlen_prefill_fp4: inconsistent shapes")
+    for t, n, rows in ((seq_lens, "seq_lens", num_seqs), (cu_seqlens_k, "cu_seqlens_k", num_seqs + 1)):
+        if t is not None:
+            _need(t, torch.int32, n, dev)
+            if t.shape != (rows,):
+                raise ValueError(f"pa_varlen_prefill_fp4: {n} must have {rows} entries")
+    _new_tokens(key, value, slot_mapping, total_q, hkv, head_dim, dev, "pa_varlen_prefill_fp4")
+    out = _out(out, q.shape, torch.bfloat16, dev)
+    need = 0 if seq_lens is None else pa_varlen_prefill_fp4_workspace_size(
+        num_seqs, num_heads, hkv, head_dim, max_seqlen_k, sliding_window)
+    ws, ws_bytes, workspace = _workspace(workspace, need, dev)
+    with _on(dev):
+        st = lib.pa_varlen_prefill_fp4(
+            _ptr(out), _ptr(q), _ptr(key), _ptr(value), _ptr(slot_mapping), _ptr(k_cache),
+            _ptr(v_cache), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(seq_lens),
+            _ptr(block_table), block_table.shape[1], num_seqs, total_q, max_seqlen_q,
+            max_seqlen_k, nb, bs, num_heads, hkv, head_dim, sliding_window, scale, kv_scale, ws,
+            ws_bytes, _stream(dev))
+    _check(st, "pa_varlen_prefill_fp4")
     return out
 
 

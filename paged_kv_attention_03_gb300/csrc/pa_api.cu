@@ -32,6 +32,9 @@ constexpr int kMaxDevices = 64;
 std::atomic<unsigned *> g_err_ptr[kMaxDevices];
 std::mutex g_err_mutex;
 
+}  // namespace
+
+namespace pa {
 // Device address of this device's error word (looked up once per device).
 unsigned *device_error_word() {
     int dev = 0;
@@ -48,6 +51,11 @@ unsigned *device_error_word() {
     }
     return p;
 }
+}  // namespace pa
+
+namespace {
+
+using pa::device_error_word;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
@@ -537,7 +545,7 @@ pa_status varlen_prefill(void *out, const void *q, const void *key, const void *
     a.head_dim = head_dim;
     a.sliding_window = sliding_window;
     a.scale = scale;
-    a.fp8 = fp8 ? 1 : 0;
+    a.cache = fp8 ? pa::kCacheE4m3 : pa::kCacheBf16;
     a.kv_scale = kv_scale;
     a.err = device_error_word();
     return from_cuda(pa::launch_prefill(a, s));

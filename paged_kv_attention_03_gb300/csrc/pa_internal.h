@@ -29,6 +29,52 @@ cudaError_t launch_store_kvcache(const StoreArgs &a, cudaStream_t stream);
 // FP8 E4M3 cache: k_cache / v_cache are [num_slots, row_elems] bytes (row_elems % 16 == 0).
 cudaError_t launch_store_kvcache_fp8(const StoreArgs &a, float kv_scale, cudaStream_t stream);
 
+// 4-bit cache (fp4.cuh): k_cache / v_cache are [num_blocks, kv_heads, block_size] rows.
+cudaError_t launch_store_kvcache_fp4(const StoreArgs &a, int kv_heads, int head_dim, int log2_bs,
+                                     float kv_scale, cudaStream_t stream);
+struct GatherArgs {
+    void *key;  // [num_tokens, num_kv_heads, head_dim] bf16, written
+    void *value;
+    const void *k_cache;
+    const void *v_cache;
+    const int32_t *slot_mapping;
+    int64_t num_tokens;
+    int64_t num_slots;
+    int num_kv_heads;
+    int head_dim;
+    int log2_bs;
+    float kv_scale;
+    unsigned *err;
+};
+cudaError_t launch_gather_kvcache_fp4(const GatherArgs &a, cudaStream_t stream);
+
+// ------------------------------------------------- block tables and slots ---
+struct StepArgs {
+    int32_t *block_table;      // [num_seqs, max_num_blocks]
+    int max_num_blocks;
+    int num_seqs;
+    int log2_bs;
+    int32_t *free_blocks;      // [num_blocks]; the free ones are [0, *num_free)
+    const int32_t *num_free;
+    int32_t *num_free_out;
+    int64_t num_blocks;
+    // prepare
+    const int32_t *context_lens;
+    const int32_t *query_lens;
+    int32_t *cu_seqlens_q;     // [num_seqs + 1]
+    int32_t *slot_mapping;     // [max_tokens]
+    int32_t *positions;        // [max_tokens] or null
+    int64_t max_tokens;
+    // release
+    const int32_t *finished;
+    const int32_t *seq_lens;
+    int32_t *seq_lens_out;     // [num_seqs] (prepare: the new lengths)
+    unsigned *err;
+};
+constexpr int kMaxStepSeqs = 16384;  // two words of shared memory a sequence
+cudaError_t launch_prepare_step(const StepArgs &a, cudaStream_t stream);
+cudaError_t launch_release_blocks(const StepArgs &a, cudaStream_t stream);
+
 // ----------------------------------------------------------------- decode ---
 // SM count the decode split plan is made for.  The plan does not query the device, so
 // pa_decode_workspace_size stays a pure function of its arguments (callers size the
@@ -106,7 +152,25 @@ struct DecodeArgs {
 };
 cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStream_t stream);
 
+// Decode over the 4-bit cache (decode_fp4.cu): `blocks` blocks of four warps share the units
+// of all sequences evenly; whole: each warp takes one whole (sequence, head tile).
+struct DecodeFp4Plan {
+    int group;
+    int head_tiles;
+    int tile_heads;  // min(group, 16)
+    bool whole;
+    int blocks;
+    int workers;
+    size_t pieces_bytes;
+    size_t workspace_bytes;
+};
+bool plan_decode_fp4(int batch, int num_heads, int num_kv_heads, int head_dim, int max_seq_len,
+                     int sliding_window, DecodeFp4Plan *plan);
+cudaError_t launch_decode_fp4(const DecodeArgs &a, const DecodeFp4Plan &plan, cudaStream_t stream);
+
 // ---------------------------------------------------------------- prefill ---
+// What the cache holds: bf16, E4M3 codes, or 4-bit rows (fp4.cuh).
+enum : int { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheFp4 = 2 };
 struct PrefillArgs {
     void *out;
     const void *q;
@@ -128,9 +192,12 @@ struct PrefillArgs {
     int head_dim;
     int sliding_window;
     float scale;
-    // FP8 E4M3 cache (head_dim 128): k_cache / v_cache hold codes of x / kv_scale.
-    int fp8;
+    // E4M3 cache (head_dim 128): k_cache / v_cache hold codes of x / kv_scale; 4-bit cache:
+    // rows of fp4.cuh.
+    int cache;  // kCacheBf16 ..
     float kv_scale;
+    // 4-bit cache: scratch of the decode rows (decode_fp4 plan of the batch).
+    void *workspace;
     unsigned *err;
 };
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);
@@ -177,6 +244,9 @@ struct MergeArgs {
     int head_dim;
 };
 cudaError_t launch_merge_states(const MergeArgs &a, cudaStream_t stream);
+
+// The current device's error word (kernels OR PA_DEVERR_* bits into it).
+unsigned *device_error_word();
 
 // Map a CUDA error to a pa_status, remembering it for pa_last_cuda_error_string().
 pa_status cuda_status(cudaError_t e);

@@ -47,13 +47,12 @@
 #include <mutex>
 #include <type_traits>
 
+#include "fp4.cuh"
 #include "pa_common.cuh"
 #include "pa_internal.h"
 #include "sm100_ptx.cuh"
 
 namespace pa {
-
-constexpr unsigned kErrTimeout = 0x20u;
 
 namespace {
 
@@ -118,7 +117,9 @@ struct PrefillKernelParams {
     int chunk_tiles;
     // Sequences with one query row are left to the decode kernel of the same call.
     int skip_decode_rows;
-    float kv_scale;    // FP8 cache: attention reads code * kv_scale (folded into scale_log2 for K)
+    float kv_scale;    // E4M3 / 4-bit cache: elements are times kv_scale (folded into scale_log2 for K)
+    const uint8_t *k4;  // 4-bit cache rows (fp4.cuh): K and V
+    const uint8_t *v4;
     uint64_t wait_ns;  // limit of every wait (kTimeoutNs unless a test lowers it)
     int stall;         // testing aid: publish no work item, so every wait runs out
     unsigned *err;
@@ -137,7 +138,7 @@ enum : int {
     B_ODONE = B_PFULL + 2,     // [2]
     B_IFULL = B_ODONE + 2,       // [kRing]: item-info ring slot written
     B_IEMPTY = B_IFULL + kRing,  // [kRing]: slot read by every consumer
-    // FP8 cache: the codes of a K / V tile landed (before their conversion to f16), and
+    // E4M3 / 4-bit cache: the codes of a K / V tile landed (before their conversion to f16), and
     // both query tiles converted to f16 by the softmax warps.
     B_LK = B_IEMPTY + kRing,     // [NSK]
     B_LV = B_LK + NSK,           // [NSV]
@@ -500,14 +501,59 @@ __device__ __forceinline__ void convert_tile_e4m3(uint32_t stage, int lane) {
     }
 }
 
-// FP8: the cache holds E4M3 codes (head_dim 128).  The producers TMA-load a tile's codes into
-// the upper half of its shared-memory stage and expand them in place to f16 in the MMA
-// operand layout (every E4M3 value is an f16); the softmax warps convert each query tile
+// One 128-key tile of 4-bit rows (fp4.cuh), landed as [128][9 HD / 16 bytes] at the end of a
+// stage, expanded in place like convert_tile_e4m3.  A row's f16 lines cover codes of other
+// rows: those of the first 32 (i + 1) rows are written only after all lanes have read
+// rows 32 i .. 32 i + 31, and reach no further than those rows (HD 128: line r ends at byte
+// 16384 + 128 r + 127 of the stage, row q starts at 23552 + 72 q; HD 64: 128 r + 127 and
+// 11776 + 36 q).  Row pitches of 72 and 36 bytes put the lanes' reads on different banks.
+template <int HD>
+__device__ __forceinline__ void convert_tile_fp4(uint32_t stage, int lane) {
+    constexpr int RB = fp4::row_bytes(HD);
+    constexpr uint32_t kRows = (HD / 64) * HALF - 128u * RB;
+    constexpr int W = HD / 64;  // words a read
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t r = static_cast<uint32_t>(lane + 32 * i);
+        uint32_t c[9 * W];  // codes, then scales
+#pragma unroll
+        for (int j = 0; j < 9; ++j) {
+            const uint32_t a = stage + kRows + r * RB + 4 * W * j;
+            if constexpr (W == 2)
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(c[2 * j]), "=r"(c[2 * j + 1]) : "r"(a) : "memory");
+            else
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(c[j]) : "r"(a) : "memory");
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < HD / 16; ++j) {
+            // group j: scale byte j, 64-dim half j / 4, chunks 2 (j % 4) and + 1 of row r
+            const uint32_t sc = fp4::e4m3x2_to_f16x2(c[8 * W + (j >> 2)] >> (16 * ((j >> 1) & 1)));
+            const uint32_t s2 = __byte_perm(sc, 0u, (j & 1) ? 0x3232 : 0x1010);
+            const uint32_t line = stage + (j >> 2) * HALF + r * 128u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t f[4];
+                fp4::e2m1x8_to_f16x2x4(c[2 * j + h], f);
+                st_shared_v4(line + (((2u * (j & 3) + h) ^ (r & 7u)) << 4), fp4::mul_f16x2(f[0], s2),
+                             fp4::mul_f16x2(f[1], s2), fp4::mul_f16x2(f[2], s2), fp4::mul_f16x2(f[3], s2));
+            }
+        }
+    }
+}
+
+// CACHE kCacheE4m3: the cache holds E4M3 codes (head_dim 128).  The producers TMA-load a tile's
+// codes into the upper half of its shared-memory stage and expand them in place to f16 in the
+// MMA operand layout (every E4M3 value is an f16); the softmax warps convert each query tile
 // to f16 in place; the products are f16 MMAs with P in f16.
-template <int HD, bool PREFIX, bool FP8>
+// CACHE kCacheFp4: likewise with 4-bit rows, each 16-key piece of a page one bulk copy.
+template <int HD, bool PREFIX, int CACHE>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillKernelParams p) {
-    static_assert(!FP8 || (HD == 128 && !PREFIX), "the FP8 cache path is built for head_dim 128");
+    constexpr bool FP4 = CACHE == kCacheFp4;
+    constexpr bool CODES = CACHE != kCacheBf16;  // codes in the cache, f16 products
+    static_assert(CACHE != kCacheE4m3 || HD == 128, "the E4M3 cache path is built for head_dim 128");
+    static_assert(!CODES || !PREFIX, "the shared-prefix mode is built for bf16 caches");
     using L = Layout<HD>;
     constexpr int NHALF = L::NHALF;
     constexpr int KSTEPS_S = HD / 16;  // MMAs per S tile
@@ -603,6 +649,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     };
 
+    // One tile of 4-bit rows at dst: a bulk copy for each 16-key piece, a lane each; a piece past
+    // the sequence, or of an invalid block, is zeros.
+    auto load_fp4 = [&](const uint8_t *cache, const Item &it, int key0, uint32_t dst, uint32_t full) {
+        constexpr uint32_t kPiece = 16 * fp4::row_bytes(HD);
+        const int slot = lane < BN / 16 ? kv_row(it, key0 + 16 * lane) : -16;
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, slot >= 0));
+        if (lane == 0) {
+            if (n > 0)
+                mbar_arrive_expect_tx(full, n * kPiece);
+            else
+                mbar_arrive(full);
+        }
+        __syncwarp();
+        if (slot >= 0) {
+            const int64_t row = ((static_cast<int64_t>(slot >> p.log2_bs) * p.num_kv_heads + it.kvh) << p.log2_bs) +
+                                (slot & bs_mask);
+            bulk_load(dst + lane * kPiece, cache + row * fp4::row_bytes(HD), kPiece, full);
+        } else if (lane < BN / 16) {
+            for (uint32_t i = 0; i < kPiece; i += 16) st_shared_v4(dst + lane * kPiece + i, 0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+    };
+
     if (warp >= 8) {
         // The register limit must be set inside each role's branch: code after a
         // merge of the two paths would get the smaller of the two limits.
@@ -658,11 +727,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t sbase = is_k ? sK : sV;
             constexpr uint32_t NS = is_k ? NSK : NSV;
             constexpr int b_full = is_k ? B_KFULL : B_VFULL, b_empty = is_k ? B_KEMPTY : B_VEMPTY;
-            if (lane == 0) prefetch_tmap(map);
+            if constexpr (!FP4)
+                if (lane == 0) prefetch_tmap(map);
             uint32_t t = 0;  // tiles issued
             bool ok = true;
             Item it;
-            if constexpr (!FP8) {
+            if constexpr (!CODES) {
                 for (uint32_t ic = 0; ok && take_item(ic, it); ++ic) {
                     for (int j = 0; j < it.n_tiles; ++j, ++t) {
                         const uint32_t st = t % NS;
@@ -706,12 +776,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t st = t % NS;
                         if (t < NS ||
                             __all_sync(0xffffffffu, mbar_test_wait(bar(b_empty + st), ((t / NS) - 1) & 1))) {
+                            if constexpr (FP4) {
+                                load_fp4(is_k ? p.k4 : p.v4, it, (it.kt0 + j) * BN,
+                                         sbase + (st + 1) * L::TILE - BN * fp4::row_bytes(HD), bar(b_land + st));
+                            } else {
                             if (lane == 0) mbar_arrive_expect_tx(bar(b_land + st), L::TILE / 2);
                             __syncwarp();
                             if (lane < BN / 16) {  // one 16-key piece of codes per lane
                                 const int row = kv_row(it, (it.kt0 + j) * BN + 16 * lane);
                                 tma_load_3d(sbase + st * L::TILE + L::TILE / 2 + lane * 2048, map, 0,
                                             it.kvh, row, bar(b_land + st));
+                            }
                             }
                             ++t;
                             if (++j == it.n_tiles) have = false;
@@ -722,7 +797,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (tc < t) {
                         const uint32_t sc = tc % NS;
                         if (__all_sync(0xffffffffu, mbar_test_wait(bar(b_land + sc), (tc / NS) & 1))) {
-                            convert_tile_e4m3(sbase + sc * L::TILE, lane);
+                            if constexpr (FP4)
+                                convert_tile_fp4<HD>(sbase + sc * L::TILE, lane);
+                            else
+                                convert_tile_e4m3(sbase + sc * L::TILE, lane);
                             fence_proxy_async_smem();
                             __syncwarp();
                             if (lane == 0) mbar_arrive(bar(b_full + sc));
@@ -756,13 +834,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---------------- MMA issuer ----------------
             // Order on the tensor pipe, across items: P0 V(g-1), S0(g), P1 V(g-1), S1(g).
             if (lane == 0) {
-                constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, false, FP8);
+                constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, false, CODES);
                 // Half tile: the item's last K/V tile when no row sees its upper 64 keys
                 // (diagonal of a query block that ends in the tile's lower half): S over
                 // 64 keys, P V over 64 keys.  The softmax needs no change: the causal mask
                 // already sets columns 64..127 to -inf.
-                constexpr uint32_t idesc_s_half = idesc_bf16_f32(BM, BN / 2, false, FP8);
-                constexpr uint32_t idesc_o = idesc_bf16_f32(BM, HD, true, FP8);
+                constexpr uint32_t idesc_s_half = idesc_bf16_f32(BM, BN / 2, false, CODES);
+                constexpr uint32_t idesc_o = idesc_bf16_f32(BM, HD, true, CODES);
                 uint32_t g = 0;                  // global KV tile counter
                 uint32_t cnt[2] = {0, 0};        // tiles issued per query tile (S / P V)
                 uint32_t ic = 0;                 // items
@@ -818,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (end) break;
                     // Finish the previous item before waiting for this item's Q, so its
                     // epilogue never waits on a Q load.
-                    if (!flush() || !wait1(bar(FP8 ? B_QCONV : B_QFULL), ic & 1, abort_flag, p.err, p.wait_ns)) {
+                    if (!flush() || !wait1(bar(CODES ? B_QCONV : B_QFULL), ic & 1, abort_flag, p.err, p.wait_ns)) {
                         ok = false;
                         break;
                     }
@@ -881,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_IEMPTY + ic % kRing));
             if (end) break;
-            if constexpr (FP8) {
+            if constexpr (CODES) {
                 // The item's query tiles to f16, in place (a thread converts its row; the
                 // 16-byte chunks of a row share its 128-byte line whatever the swizzle, and
                 // taking them in swizzled order puts the 8 rows of a lane octet on 8 bank
@@ -1011,7 +1089,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                   sl2x2, negm2);
                         float x0, x1;
                         f2_unpack(x, x0, x1);
-                        if constexpr (FP8) {
+                        if constexpr (CODES) {
                             pk[i] = pack_f16x2(ex2_approx(x0), ex2_approx(x1));
                             add_f16x2_f32(acc[2 * (i & 1)], acc[2 * (i & 1) + 1], pk[i]);
                         } else {
@@ -1054,8 +1132,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
-            // (FP8: V elements are code * kv_scale.)
-            const float inv = l_sum > 0.f ? (FP8 ? p.kv_scale : 1.f) / l_sum : 0.f;
+            // (Codes: V elements are times kv_scale.)
+            const float inv = l_sum > 0.f ? (CODES ? p.kv_scale : 1.f) / l_sum : 0.f;
             if constexpr (PREFIX) {
                 // Partial state of this key split: fp32 row and ln of its denominator.
                 const int64_t rows = static_cast<int64_t>(p.num_req) * p.num_heads;
@@ -1237,7 +1315,7 @@ int sm_count() {
     return n;
 }
 
-template <int HD, bool PREFIX, bool FP8 = false>
+template <int HD, bool PREFIX, int CACHE = kCacheBf16>
 cudaError_t launch_prefill_d(PrefillKernelParams &kp, const PrefillArgs &a, cudaStream_t stream) {
     using L = Layout<HD>;
     const int64_t slots = a.num_blocks * a.block_size;
@@ -1246,14 +1324,16 @@ cudaError_t launch_prefill_d(PrefillKernelParams &kp, const PrefillArgs &a, cuda
         return cudaErrorInvalidValue;
     // K / V boxes: one 16-row piece of a page and a 64-dim half (bf16), or the piece's whole
     // rows of codes (FP8).
+    // (4-bit caches are copied without a tensor map.)
+    constexpr bool FP8 = CACHE == kCacheE4m3;
     const uint64_t eb = FP8 ? 1ull : 2ull;  // bytes per cache element
-    for (int kv = 0; kv < 2; ++kv) {
+    for (int kv = 0; kv < 2 && CACHE != kCacheFp4; ++kv) {
         if (!encode_3d(kv ? &kp.tmap_v : &kp.tmap_k, kv ? a.v_cache : a.k_cache, HD,
                        a.num_kv_heads, static_cast<uint64_t>(slots), HD * eb,
                        static_cast<uint64_t>(a.num_kv_heads) * HD * eb, FP8 ? HD : 64, 1, 16, FP8))
             return cudaErrorInvalidValue;
     }
-    auto kern = prefill_kernel<HD, PREFIX, FP8>;
+    auto kern = prefill_kernel<HD, PREFIX, CACHE>;
     static std::atomic<uint64_t> smem_set;
     cudaError_t e = smem_limit_once(kern, static_cast<int>(L::SMEM), smem_set);
     if (e != cudaSuccess) return e;
@@ -1301,21 +1381,29 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
     if (n_items > 0x7fffffffLL) return cudaErrorInvalidValue;
     kp.n_items = static_cast<int>(n_items);
     kp.window = a.sliding_window;
-    kp.kv_scale = a.fp8 ? a.kv_scale : 1.f;
-    kp.scale_log2 = a.scale * kp.kv_scale * kLog2e;  // FP8: K elements are code * kv_scale
+    kp.kv_scale = a.cache != kCacheBf16 ? a.kv_scale : 1.f;
+    kp.scale_log2 = a.scale * kp.kv_scale * kLog2e;  // codes: K elements are times kv_scale
+    kp.k4 = static_cast<const uint8_t *>(a.k_cache);
+    kp.v4 = static_cast<const uint8_t *>(a.v_cache);
     kp.err = a.err;
     set_launch_limits(kp);
     // Sequences with a single query row (decode rows of a mixed batch) would fill one
     // token of a 128-row tile: with seq_lens given, a single-split decode launch takes
-    // them (it needs no workspace) and the prefill kernel skips them.
+    // them (it needs no workspace but over a 4-bit cache) and the prefill kernel skips them.
     const bool route = a.seq_lens != nullptr;
     kp.skip_decode_rows = route ? 1 : 0;
     const bool prefill_launched = !route || a.max_seqlen_q > 1;
     if (prefill_launched) {
         cudaError_t e;
-        if (a.fp8) {
+        if (a.cache == kCacheE4m3) {
             if (a.head_dim != 128) return cudaErrorInvalidValue;
-            e = launch_prefill_d<128, false, true>(kp, a, stream);
+            e = launch_prefill_d<128, false, kCacheE4m3>(kp, a, stream);
+        } else if (a.cache == kCacheFp4) {
+            switch (a.head_dim) {
+                case 64: e = launch_prefill_d<64, false, kCacheFp4>(kp, a, stream); break;
+                case 128: e = launch_prefill_d<128, false, kCacheFp4>(kp, a, stream); break;
+                default: return cudaErrorInvalidValue;
+            }
         } else {
             switch (a.head_dim) {
                 case 64: e = launch_prefill_d<64, false>(kp, a, stream); break;
@@ -1325,10 +1413,6 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
         }
         if (e != cudaSuccess || !route) return e;
     }
-    DecodePlan plan;
-    if (!plan_decode(a.num_seqs, a.num_heads, a.num_kv_heads, a.head_dim, a.max_seqlen_k,
-                     a.sliding_window, 1, &plan))
-        return cudaErrorInvalidValue;
     DecodeArgs d{};
     d.out = a.out;
     d.q = a.q;
@@ -1351,10 +1435,22 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
     d.check_rows = !prefill_launched;
     d.max_seqlen_q = a.max_seqlen_q;
     d.cu_seqlens_k = a.cu_seqlens_k;
-    d.fp8 = a.fp8;
+    d.fp8 = a.cache == kCacheE4m3;
     d.kv_scale = a.kv_scale;
     d.after_prefill = prefill_launched;
     d.err = a.err;
+    if (a.cache == kCacheFp4) {
+        DecodeFp4Plan plan;
+        if (!plan_decode_fp4(a.num_seqs, a.num_heads, a.num_kv_heads, a.head_dim, a.max_seqlen_k,
+                             a.sliding_window, &plan))
+            return cudaErrorInvalidValue;
+        d.workspace = a.workspace;
+        return launch_decode_fp4(d, plan, stream);
+    }
+    DecodePlan plan;
+    if (!plan_decode(a.num_seqs, a.num_heads, a.num_kv_heads, a.head_dim, a.max_seqlen_k,
+                     a.sliding_window, 1, &plan))
+        return cudaErrorInvalidValue;
     return launch_decode(d, plan, stream);
 }
 

@@ -1,0 +1,357 @@
+// step_tables.cu - the metadata of a serving step built on the GPU from the requests' lengths:
+// block tables, slots, positions, lengths and offsets, with the pool's free blocks kept as a
+// stack in device memory; and the release of finished requests' blocks.
+//
+// prepare: with c_i cached and q_i new tokens of request i and blocks of B tokens,
+//     have_i = ceil(c_i / B),  need_i = ceil((c_i + q_i) / B) - have_i,
+//     cu = exclusive prefix sum of q,  off = exclusive prefix sum of need,
+//     block_table[i][have_i + k] = free[n_free - 1 - off_i - k],  0 <= k < need_i,
+//     token t of request i: position p = c_i + t - cu_i, slot block_table[i][p / B] * B + p % B.
+// release: the entries [0, ceil(len_i / B)) of finished rows follow free[n_free) in row order.
+//
+// The data is a few bytes a token, so the time is launches and dependent loads.  Every block
+// scans all requests by itself (at most kMaxStepSeqs, two words of shared memory each) and
+// takes its share of the tokens, so no block waits for another.  A thread takes four
+// consecutive tokens: one binary search in shared memory and 16-byte stores; a token's block
+// comes straight from the free list, and the first token of each new block writes the table
+// entry.  What a caller may update in place (lengths, the free count) is written when no
+// block reads it any more: by the same block when there is one, else by a second launch, a
+// programmatic dependent that repeats the scan while the first runs.
+#include <algorithm>
+
+#include "pa_common.cuh"
+#include "pa_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace pa {
+
+namespace {
+
+constexpr int kThreads = 512;
+// Items (tokens or table entries) up to which one block does all of a call.
+constexpr int64_t kAloneItems = 8192;
+
+// Sums saturate at 2^31 - 1: they are offsets into arrays of fewer items, and a saturated sum
+// of non-negative numbers does not depend on the order.
+constexpr uint32_t kTop = 0x7fffffffu;
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) { return min(a + b, kTop); }
+
+// One request: tokens (prepare) or entries (release), and new blocks.
+struct Need {
+    uint32_t items;
+    uint32_t blocks;
+};
+
+__device__ __forceinline__ uint32_t table_cap(const StepArgs &a) {
+    const uint64_t cap = static_cast<uint64_t>(a.max_num_blocks) << a.log2_bs;
+    return static_cast<uint32_t>(min(cap, static_cast<uint64_t>(kTop)));
+}
+
+// Cached tokens of request i, inside [0, capacity of its row].
+__device__ __forceinline__ uint32_t cached(const StepArgs &a, int i) {
+    return min(static_cast<uint32_t>(max(a.context_lens[i], 0)), table_cap(a));
+}
+
+template <bool PREPARE>
+__device__ __forceinline__ Need need_of(const StepArgs &a, int i, bool report) {
+    Need n;
+    const uint32_t cap = table_cap(a);
+    const uint32_t up = (1u << a.log2_bs) - 1u;
+    if constexpr (PREPARE) {
+        const int c_raw = a.context_lens[i], q_raw = a.query_lens[i];
+        const uint32_t c = cached(a, i);
+        n.items = static_cast<uint32_t>(max(q_raw, 0));
+        const uint32_t len = min(c + n.items, cap);  // below 2^32
+        n.blocks = ((len + up) >> a.log2_bs) - ((c + up) >> a.log2_bs);
+        if (report) {
+            if (c_raw < 0 || static_cast<uint32_t>(c_raw) > cap || c + n.items > cap)
+                flag_error(a.err, kErrSeqRange);
+            if (q_raw < 0) flag_error(a.err, kErrQueryLen);
+        }
+    } else {
+        const int raw = a.seq_lens[i];
+        const bool done = a.finished[i] != 0;
+        const uint32_t len = min(static_cast<uint32_t>(max(raw, 0)), cap);
+        n.items = done ? (len + up) >> a.log2_bs : 0u;
+        n.blocks = 0;
+        if (report && done && (raw < 0 || static_cast<uint32_t>(raw) > cap)) flag_error(a.err, kErrSeqRange);
+    }
+    return n;
+}
+
+// Exclusive prefix sums of all requests' needs into shared memory (n + 1 words each).
+template <bool PREPARE>
+__device__ __forceinline__ void scan(const StepArgs &a, uint32_t *items, uint32_t *blocks, bool report) {
+    __shared__ uint32_t wsum[2][kThreads / 32];
+    const int n = a.num_seqs;
+    const int per = (n + kThreads - 1) / kThreads;
+    const int i0 = min(n, static_cast<int>(threadIdx.x) * per), i1 = min(n, i0 + per);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t si = 0, sb = 0;
+    for (int i = i0; i < i1; ++i) {
+        const Need x = need_of<PREPARE>(a, i, report);
+        items[i] = si;
+        if (PREPARE) blocks[i] = sb;
+        si = add_sat(si, x.items);
+        sb = add_sat(sb, x.blocks);
+    }
+    uint32_t pi = si, pb = sb;  // inclusive over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, pi, o), y = __shfl_up_sync(0xffffffffu, pb, o);
+        if (lane >= o) {
+            pi = add_sat(pi, x);
+            pb = add_sat(pb, y);
+        }
+    }
+    if (lane == 31) {
+        wsum[0][warp] = pi;
+        wsum[1][warp] = pb;
+    }
+    uint32_t ei = __shfl_up_sync(0xffffffffu, pi, 1), eb = __shfl_up_sync(0xffffffffu, pb, 1);
+    if (lane == 0) ei = eb = 0;
+    __syncthreads();
+    for (int k = 0; k < warp; ++k) {
+        ei = add_sat(ei, wsum[0][k]);
+        eb = add_sat(eb, wsum[1][k]);
+    }
+    for (int i = i0; i < i1; ++i) {
+        items[i] = add_sat(items[i], ei);
+        if (PREPARE) blocks[i] = add_sat(blocks[i], eb);
+    }
+    if (threadIdx.x == kThreads - 1) {
+        items[n] = add_sat(ei, si);
+        if (PREPARE) blocks[n] = add_sat(eb, sb);
+    }
+    __syncthreads();
+}
+
+// The last request whose first item is at or before k (k below the total): the one that holds k.
+__device__ __forceinline__ int holder(const uint32_t *items, int n, uint32_t k) {
+    int lo = 0, hi = n;  // items[lo] <= k < items[hi]
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (items[m] <= k)
+            lo = m;
+        else
+            hi = m;
+    }
+    return lo;
+}
+
+// The free count, inside [0, num_blocks].
+__device__ __forceinline__ uint32_t free_count(const StepArgs &a, bool report) {
+    const int raw = *a.num_free;
+    if (report && (raw < 0 || raw > a.num_blocks)) flag_error(a.err, kErrBlockRange);
+    return static_cast<uint32_t>(min(static_cast<int64_t>(max(raw, 0)), a.num_blocks));
+}
+
+__device__ __forceinline__ void store4(int32_t *dst, int64_t k, int64_t end, const int (&v)[4]) {
+    if (k + 4 <= end && (reinterpret_cast<uintptr_t>(dst + k) & 15u) == 0) {
+        *reinterpret_cast<int4 *>(dst + k) = make_int4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (k + j < end) dst[k + j] = v[j];
+    }
+}
+
+// Slots, positions and new table entries of this block's tokens.
+__device__ __forceinline__ void tokens(const StepArgs &a, const uint32_t *cu, const uint32_t *off) {
+    const int n = a.num_seqs;
+    const uint32_t total = n > 0 ? cu[n] : 0u;
+    const uint32_t nfree = free_count(a, false);
+    const uint32_t cap = table_cap(a);
+    const uint32_t up = (1u << a.log2_bs) - 1u;
+    const int64_t stride = 4ll * kThreads * gridDim.x;
+    for (int64_t t0 = 4ll * (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x);
+         t0 < a.max_tokens; t0 += stride) {
+        int slot[4], posv[4];
+        int seq = -1;
+        uint32_t begin = 0, end = 0, c = 0, have = 0, cur_blk = 0xffffffffu;
+        int entry = -1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            slot[j] = -1;  // past the last token: padding
+            posv[j] = 0;
+            const int64_t tt = t0 + j;
+            if (tt >= total || tt >= a.max_tokens) continue;
+            const uint32_t t = static_cast<uint32_t>(tt);
+            if (seq < 0 || t >= end) {
+                // Often the next request; else (empty ones between) search again.
+                if (seq >= 0 && t < cu[seq + 2 <= n ? seq + 2 : n])
+                    ++seq;
+                else
+                    seq = holder(cu, n, t);
+                begin = cu[seq];
+                end = cu[seq + 1];
+                c = cached(a, seq);
+                have = (c + up) >> a.log2_bs;
+                cur_blk = 0xffffffffu;
+            }
+            const uint32_t pos = c + (t - begin);  // below 2^32
+            posv[j] = static_cast<int>(min(pos, kTop));
+            if (pos >= cap) continue;  // no room in the row (flagged by the scan)
+            const uint32_t blk = pos >> a.log2_bs;
+            int32_t *at = a.block_table + static_cast<int64_t>(seq) * a.max_num_blocks + blk;
+            if (blk != cur_blk) {
+                cur_blk = blk;
+                const bool fresh = blk >= have;
+                if (fresh) {
+                    const uint32_t rank = add_sat(off[seq], blk - have);
+                    entry = rank < nfree ? a.free_blocks[nfree - 1 - rank] : -1;
+                } else {
+                    entry = *at;
+                }
+                if (entry < 0 || entry >= a.num_blocks) {
+                    // Out of blocks is flagged where the count is; other entries are bad ones.
+                    if (!fresh || add_sat(off[seq], blk - have) < nfree) flag_error(a.err, kErrBlockRange);
+                    entry = -1;
+                }
+            }
+            if ((pos & up) == 0) *at = entry;  // the first token of a block: the block is new
+            if (entry >= 0) slot[j] = (entry << a.log2_bs) | static_cast<int>(pos & up);
+        }
+        store4(a.slot_mapping, t0, a.max_tokens, slot);
+        if (a.positions != nullptr) store4(a.positions, t0, a.max_tokens, posv);
+    }
+}
+
+// Lengths, offsets and the free count.
+__device__ __forceinline__ void publish_prepare(const StepArgs &a, const uint32_t *cu,
+                                                const uint32_t *off) {
+    const int n = a.num_seqs;
+    const uint32_t nfree = free_count(a, true);
+    const uint32_t up = (1u << a.log2_bs) - 1u;
+    const uint32_t cap = table_cap(a);
+    const uint32_t most = static_cast<uint32_t>(min(a.max_tokens, static_cast<int64_t>(kTop)));
+    const uint32_t used = min(n > 0 ? off[n] : 0u, nfree);
+    if (threadIdx.x == 0) {
+        if (n > 0 && off[n] > nfree) flag_error(a.err, kErrNoBlocks);
+        if (n > 0 && cu[n] > most) flag_error(a.err, kErrQueryLen);
+        a.cu_seqlens_q[n] = n > 0 ? static_cast<int>(min(cu[n], most)) : 0;
+    }
+    __syncthreads();  // the count has been read by all (num_free_out may be num_free)
+    if (threadIdx.x == 0) *a.num_free_out = static_cast<int>(nfree - used);
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint32_t c = cached(a, i);
+        uint32_t len = min(c + static_cast<uint32_t>(max(a.query_lens[i], 0)), cap);
+        // Out of blocks: the sequence ends where its last block does.
+        const uint32_t have = (c + up) >> a.log2_bs;
+        const uint32_t got = off[i] < nfree ? nfree - off[i] : 0u;
+        const uint64_t room = static_cast<uint64_t>(have + static_cast<uint64_t>(got)) << a.log2_bs;
+        if (room < len) len = static_cast<uint32_t>(room);
+        a.seq_lens_out[i] = static_cast<int>(len);
+        a.cu_seqlens_q[i] = static_cast<int>(min(cu[i], most));
+    }
+}
+
+// This block's released entries to the end of the free list.
+__device__ __forceinline__ void push_blocks(const StepArgs &a, const uint32_t *first) {
+    const int n = a.num_seqs;
+    const uint32_t total = n > 0 ? first[n] : 0u;
+    const uint32_t nfree = free_count(a, false);
+    const int64_t stride = 4ll * kThreads * gridDim.x;
+    for (int64_t k0 = 4ll * (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x); k0 < total;
+         k0 += stride) {
+        int seq = -1;
+        uint32_t begin = 0, end = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t k = static_cast<uint32_t>(k0) + j;
+            if (k >= total) continue;
+            if (seq < 0 || k >= end) {
+                seq = holder(first, n, k);
+                begin = first[seq];
+                end = first[seq + 1];
+            }
+            const int entry = a.block_table[static_cast<int64_t>(seq) * a.max_num_blocks + (k - begin)];
+            const int64_t dst = static_cast<int64_t>(nfree) + k;
+            if (entry < 0 || entry >= a.num_blocks || dst >= a.num_blocks) flag_error(a.err, kErrBlockRange);
+            if (dst < a.num_blocks) a.free_blocks[dst] = entry;
+        }
+    }
+}
+
+__device__ __forceinline__ void publish_release(const StepArgs &a, const uint32_t *first) {
+    const int n = a.num_seqs;
+    const uint32_t nfree = free_count(a, true);
+    const uint32_t total = n > 0 ? first[n] : 0u;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        *a.num_free_out = static_cast<int>(min(static_cast<int64_t>(nfree) + total, a.num_blocks));
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const int len = a.seq_lens[i];
+        a.seq_lens_out[i] = a.finished[i] != 0 ? 0 : len;
+    }
+}
+
+enum : int { kAll = 0, kItems = 1, kPublish = 2 };
+
+// PART kItems: the first launch of two; kPublish: the second; kAll: one block does both.
+template <bool PREPARE, int PART>
+__global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
+    extern __shared__ uint32_t sums[];
+    uint32_t *items = sums, *blocks = sums + a.num_seqs + 1;
+    if constexpr (PART == kItems) sm100::griddep_launch_dependents();
+    scan<PREPARE>(a, items, blocks, PART != kItems);
+    if constexpr (PART != kPublish) {
+        if constexpr (PREPARE)
+            tokens(a, items, blocks);
+        else
+            push_blocks(a, items);
+    }
+    if constexpr (PART == kAll) __syncthreads();
+    if constexpr (PART == kPublish) sm100::griddep_wait();
+    if constexpr (PART != kItems) {
+        if constexpr (PREPARE)
+            publish_prepare(a, items, blocks);
+        else
+            publish_release(a, items);
+    }
+}
+
+template <bool PREPARE, int PART>
+cudaError_t launch_part(const StepArgs &a, int blocks, cudaStream_t stream) {
+    const int smem = (a.num_seqs + 1) * (PREPARE ? 2 : 1) * 4;
+    auto kern = step_kernel<PREPARE, PART>;
+    if (smem > 48 * 1024) {
+        static std::atomic<uint64_t> smem_set;
+        const cudaError_t e = smem_limit_once(kern, (kMaxStepSeqs + 1) * (PREPARE ? 2 : 1) * 4, smem_set);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PART == kPublish ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <bool PREPARE>
+cudaError_t launch_step(const StepArgs &a, int64_t items, cudaStream_t stream) {
+    if (items <= kAloneItems) return launch_part<PREPARE, kAll>(a, 1, stream);
+    const int64_t want = (items + 4 * kThreads - 1) / (4 * kThreads);
+    const cudaError_t e =
+        launch_part<PREPARE, kItems>(a, static_cast<int>(std::min<int64_t>(want, kPlanSms)), stream);
+    return e != cudaSuccess ? e : launch_part<PREPARE, kPublish>(a, 1, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_prepare_step(const StepArgs &a, cudaStream_t stream) {
+    return launch_step<true>(a, a.max_tokens, stream);
+}
+
+cudaError_t launch_release_blocks(const StepArgs &a, cudaStream_t stream) {
+    // The released entries are at most the whole table and at most the pool.
+    return launch_step<false>(a, std::min<int64_t>(static_cast<int64_t>(a.num_seqs) * a.max_num_blocks, a.num_blocks), stream);
+}
+
+}  // namespace pa

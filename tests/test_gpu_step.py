@@ -1,0 +1,172 @@
+"""Block tables, slots and the free list built on the GPU against the oracle's
+request-by-request walk: whole numbers, equal bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_attention_03_gb300 as pa
+from oracle import fp4
+
+pytestmark = pytest.mark.gpu
+
+
+def _t(a, dev):
+    return torch.as_tensor(np.ascontiguousarray(a), dtype=torch.int32, device=dev)
+
+
+def _state(ctx, bs, mb, extra, seed):
+    """Tables holding the cached tokens' blocks and a shuffled free list of `extra` blocks."""
+    rng = np.random.default_rng(seed)
+    have = [-(-int(c) // bs) for c in ctx]
+    nb = sum(have) + extra
+    perm = rng.permutation(nb)
+    table = np.full((len(ctx), mb), -7, np.int32)  # entries that nobody may touch
+    at = 0
+    for i, n in enumerate(have):
+        table[i, :n] = perm[at:at + n]
+        at += n
+    free = np.full(nb, -9, np.int32)
+    free[:extra] = perm[at:]
+    return table, free, extra
+
+
+def _check(dev, ctx, q, bs, mb, extra, max_tokens, seed=0, flags=0):
+    table, free, nf = _state(ctx, bs, mb, extra, seed)
+    want = fp4.prepare_step(ctx, q, table, free, nf, bs, max_tokens)
+    bt = _t(table, dev)
+    got = pa.pa_prepare_step(_t(ctx, dev), _t(q, dev), bt, _t(free, dev), _t([nf], dev), bs, max_tokens)
+    assert pa.pa_read_device_error(device=dev) == flags
+    for name, g, w in zip(("seq_lens", "cu_seqlens_q", "slot_mapping", "positions"), got, want[1:]):
+        np.testing.assert_array_equal(g.cpu().numpy(), w, err_msg=name)
+    assert int(got[4]) == want[5]
+    np.testing.assert_array_equal(bt.cpu().numpy(), want[0])
+
+
+@pytest.mark.parametrize("bs", [1, 16, 64, 1024])
+@pytest.mark.parametrize("ctx,q", [([0], [1]), ([5], [0]), ([0, 0, 0], [0, 0, 0]), ([15, 16, 17], [1, 1, 1]),
+                                   ([0, 31, 100, 7, 64], [130, 1, 0, 33, 64]), ([0] * 9, [0, 0, 3, 0, 0, 0, 2, 0, 0])])
+def test_prepare_small(cuda, bs, ctx, q):
+    mb = max(-(-(c + n) // bs) for c, n in zip(ctx, q)) + 2
+    need = sum(-(-(c + n) // bs) + (-c // bs) for c, n in zip(ctx, q))
+    for pad in (0, 5):
+        _check(cuda, ctx, q, bs, mb, need + 3, sum(q) + pad)
+
+
+@pytest.mark.parametrize("n,high,bs", [(1, 20000, 16), (33, 700, 16), (700, 40, 32), (5000, 3, 16),
+                                       (16384, 2, 64), (64, 1, 16), (600, 90, 1)])
+def test_prepare_many(cuda, n, high, bs):
+    # One block or two launches, one request or the most there may be.
+    rng = np.random.default_rng(n)
+    ctx = rng.integers(0, 200, n)
+    q = rng.integers(0, high + 1, n)
+    q[rng.random(n) < 0.2] = 0
+    mb = -(-(200 + high) // bs) + 1
+    need = int(sum(-(-(ctx + q) // bs) - -(-ctx // bs)))
+    _check(cuda, ctx, q, bs, mb, need, int(q.sum()) + 13, seed=n)
+
+
+def test_prepare_no_requests(cuda):
+    z = torch.zeros(0, dtype=torch.int32, device=cuda)
+    got = pa.pa_prepare_step(z, z, torch.zeros(0, 4, dtype=torch.int32, device=cuda), _t([3, 1], cuda),
+                             _t([2], cuda), 16, 5)
+    assert got[1].tolist() == [0] and got[2].tolist() == [-1] * 5 and got[3].tolist() == [0] * 5
+    assert got[4].tolist() == [2] and pa.pa_read_device_error(device=cuda) == 0
+
+
+@pytest.mark.parametrize("max_tokens", [200, 20000])
+@pytest.mark.parametrize("extra", [0, 1, 4, 7])
+def test_prepare_out_of_blocks(cuda, extra, max_tokens):
+    # The blocks that are left go to the first requests; the others end with what they hold.
+    _check(cuda, [10, 0, 40, 3], [40, 50, 20, 9], 16, 8, extra, max_tokens, flags=pa.DEVERR_NO_BLOCKS)
+
+
+def test_prepare_clamps_bad_lengths(cuda):
+    # Negative lengths count as none; a row's end cuts a request; more tokens than the capacity.
+    bt = torch.full((3, 2), -1, dtype=torch.int32, device=cuda)
+    free = torch.arange(50, dtype=torch.int32, device=cuda)
+    args = (bt, free, _t([50], cuda), 16)
+    lens, cu, slots, pos, nf = pa.pa_prepare_step(_t([-3, 0, 0], cuda), _t([2, -1, 40], cuda), *args, 42)
+    assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_SEQ_RANGE | pa.DEVERR_QUERY_LEN
+    assert lens.tolist() == [2, 0, 32] and cu.tolist() == [0, 2, 2, 42] and nf.tolist() == [47]
+    assert slots.tolist() == [49 * 16, 49 * 16 + 1] + [48 * 16 + i for i in range(16)] + \
+        [47 * 16 + i for i in range(16)] + [-1] * 8
+    assert bt.tolist() == [[49, -1], [-1, -1], [48, 47]]
+    lens, cu, slots, pos, nf = pa.pa_prepare_step(_t([0, 0, 0], cuda), _t([6, 6, 6], cuda), *args, 10)
+    assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_QUERY_LEN
+    assert cu.tolist() == [0, 6, 10, 10] and len(slots) == 10
+
+
+def test_prepare_flags_bad_block_ids(cuda):
+    # A bad id in the free list or in the table gives no slot, and no access.
+    bt = torch.tensor([[99, -1], [-1, -1]], dtype=torch.int32, device=cuda)
+    free = torch.tensor([1, -5, 1000], dtype=torch.int32, device=cuda)
+    _, _, slots, _, nf = pa.pa_prepare_step(_t([3, 0], cuda), _t([1, 17], cuda), bt, free, _t([2], cuda), 16, 18)
+    assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_BLOCK_RANGE
+    assert slots.tolist() == [-1] + [-1] * 16 + [16] and nf.tolist() == [0]
+    pa.pa_prepare_step(_t([3, 0], cuda), _t([0, 0], cuda), bt, free, _t([9], cuda), 16, 1)
+    assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_BLOCK_RANGE  # a count above the pool
+
+
+@pytest.mark.parametrize("n,high,share,bs", [(1, 50, 1.0, 16), (64, 4096, 0.2, 16), (700, 3000, 0.5, 16),
+                                             (3, 20, 0.0, 32), (300, 5, 1.0, 1), (16384, 40, 0.7, 16)])
+def test_release(cuda, n, high, share, bs):
+    rng = np.random.default_rng(n)
+    lens = rng.integers(0, high + 1, n)
+    table, free, nf = _state(lens, bs, -(-high // bs) + 1, 11, n)
+    fin = (rng.random(n) < share).astype(np.int32) * 5
+    want = fp4.release_blocks(fin, lens, table, free, nf, bs)
+    f, bt = _t(free, cuda), _t(table, cuda)
+    out, count = pa.pa_release_blocks(_t(fin, cuda), _t(lens, cuda), bt, f, _t([nf], cuda), bs)
+    assert pa.pa_read_device_error(device=cuda) == 0
+    np.testing.assert_array_equal(f.cpu().numpy(), want[0])
+    np.testing.assert_array_equal(out.cpu().numpy(), want[1])
+    assert int(count) == want[2]
+    np.testing.assert_array_equal(bt.cpu().numpy(), table)
+
+
+@pytest.mark.parametrize("n", [3, 2000])
+def test_release_flags_bad_entries(cuda, n):
+    # More blocks than the pool has ids, and an id out of range: flagged, nothing written behind.
+    lens = torch.full((n,), 32 * 16, dtype=torch.int32, device=cuda)
+    bt = torch.zeros(n, 32, dtype=torch.int32, device=cuda)
+    buf = torch.full((40,), -3, dtype=torch.int32, device=cuda)
+    free = buf[:20]
+    _, count = pa.pa_release_blocks(torch.ones_like(lens), lens, bt, free, _t([4], cuda), 16)
+    assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_BLOCK_RANGE
+    assert count.tolist() == [20] and (buf[20:] == -3).all() and (buf[:4] == -3).all()
+
+
+@pytest.mark.parametrize("n,chunk", [(5, 3), (300, 90)])
+def test_steps_in_place_as_a_graph(cuda, n, chunk):
+    # Prefill, then decode steps from one captured graph that updates lengths and the free count
+    # in place, then releases; the oracle walks along.
+    bs, mb = 16, 12
+    rng = np.random.default_rng(n)
+    table, free, nf = _state([0] * n, bs, mb, n * mb, 1)
+    q = rng.integers(1, chunk + 1, n)
+    lens, bt, f, count = _t([0] * n, cuda), _t(table, cuda), _t(free, cuda), _t([nf], cuda)
+    pa.pa_prepare_step(lens, _t(q, cuda), bt, f, count, bs, n * chunk, seq_lens=lens, num_free_out=count)
+    table, want_lens, *_, nf = fp4.prepare_step([0] * n, q, table, free, nf, bs, n * chunk)
+    one = torch.ones_like(lens)
+    bufs = dict(cu_seqlens_q=torch.empty(n + 1, dtype=torch.int32, device=cuda),
+                slot_mapping=torch.empty(n, dtype=torch.int32, device=cuda),
+                positions=torch.empty(n, dtype=torch.int32, device=cuda))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.pa_prepare_step(lens, one, bt, f, count, bs, n, seq_lens=lens, num_free_out=count, **bufs)
+    for _ in range(40):
+        graph.replay()
+        table, want_lens, cu, slots, pos, nf = fp4.prepare_step(want_lens, [1] * n, table, free, nf, bs, n)
+        for k, w in (("cu_seqlens_q", cu), ("slot_mapping", slots), ("positions", pos)):
+            np.testing.assert_array_equal(bufs[k].cpu().numpy(), w)
+    np.testing.assert_array_equal(lens.cpu().numpy(), want_lens)
+    np.testing.assert_array_equal(bt.cpu().numpy(), table)
+    fin = (rng.random(n) < 0.5).astype(np.int32)
+    free_np = f.cpu().numpy()
+    pa.pa_release_blocks(_t(fin, cuda), lens, bt, f, count, bs, seq_lens_out=lens, num_free_out=count)
+    free_np, want_lens, nf = fp4.release_blocks(fin, want_lens, table, free_np, nf, bs)
+    np.testing.assert_array_equal(f.cpu().numpy(), free_np)
+    np.testing.assert_array_equal(lens.cpu().numpy(), want_lens)
+    assert int(count) == nf and pa.pa_read_device_error(device=cuda) == 0
+    held = np.concatenate([table[i, : -(-int(c) // bs)] for i, c in enumerate(want_lens)])
+    assert sorted([*held, *free_np[:nf]]) == list(range(n * mb))  # every block is somewhere, once
