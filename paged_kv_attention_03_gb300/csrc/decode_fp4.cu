@@ -5,21 +5,22 @@
 //
 // A byte of cache holds 1.8 elements, so the kernel has to spend few instructions on each
 // byte and keep the stream going without a pause:
-//  * The keys of all (sequence, kv head, 16-head tile) segments are one flat list of 16-key
+//  * The keys of all (sequence, kv head, 16-head tile) segments are one flat list of 32-key
 //    units, cut into equal ranges, one for each resident warp.  A warp streams its range
 //    through its own ring of shared-memory stages without stopping at segment ends, so there
 //    are no waves of blocks, no ragged tail and one pipeline fill a warp.
-//  * One 16-key unit is 9 D contiguous bytes of K and of V (rows of codes and scales), each
-//    moved by one bulk copy that a single lane issues.
-//  * The products are f16 warp MMAs (m16n8k16, fp32 accumulate) with the unit's keys as the
-//    M rows of S^T = K Q^T and the head dims as those of O^T += V^T P^T, the query heads the
-//    8 columns of an n-tile (two n-tiles above 8 heads a kv head).  Codes become f16 by one
-//    conversion for two and are scaled by one f16x2 product, exactly (fp4.cuh).
-//  * The MMA's key and dim indices are permuted so that a lane needs whole groups of 16 dims:
-//    K lane t of a quad takes groups t and t + 4 of its key rows; V lane group g owns dims
-//    16 g .. 16 g + 15 (one scale a key) and keys 4 t .. 4 t + 3.  Loads are 8 bytes wide and,
-//    with 72-byte rows, free of bank conflicts for V; and a lane ends up with 16 consecutive
-//    dims of O for its heads, which it writes as whole vectors.
+//  * 16 tokens of one kv head are 9 D contiguous bytes (rows of codes and scales): a unit is
+//    two bulk copies of K and two of V, which two lanes issue.
+//  * The products are f16 warp MMAs (m16n8k16, fp32 accumulate) with 16 keys as the M rows of
+//    S^T = K Q^T and the head dims as those of O^T += V^T P^T, the query heads the 8 columns
+//    of an n-tile (two n-tiles above 8 heads a kv head).  Codes become f16 by one conversion
+//    for two and are scaled by one f16x2 product, exactly (fp4.cuh).  The softmax denominator
+//    is one more MMA, with a matrix of ones in V's place.
+//  * The MMA's key and dim indices are permuted so that a lane needs whole runs of a row: K
+//    lane t of a quad takes dims D / 4 t .. of its key rows; V lane group g owns D / 8
+//    consecutive dims (one scale a key) of keys 4 t .. 4 t + 3.  Loads are 8 bytes wide and, with
+//    72-byte rows, free of bank conflicts for V; and a lane ends up with consecutive dims of
+//    O for its heads, which it writes as whole vectors.
 //  * A segment inside one warp's range is finished there.  A cut one leaves (m, l, O) of each
 //    piece in the workspace and decode_fp4_combine_kernel (a programmatic dependent) merges
 //    them.  When no sequence can be longer than kWholeUnits units, ranges are whole segments
@@ -42,9 +43,12 @@ using namespace sm100;
 
 constexpr int kWarps = 4;          // independent warps of a block
 constexpr int kCtasPerSm = 4;      // resident blocks: 16 warps an SM
-constexpr int kStages = 6;         // ring stages of a warp, one 16-key unit of K and V each
-constexpr int kMinUnits = 8;       // smallest range of a warp (128 keys)
-constexpr int kWholeUnits = 9;     // spans up to this many units are never cut
+constexpr int kUnit = 32;          // keys of a unit: two 16-key halves
+constexpr int kStages = 3;         // ring stages of a warp, one unit of K and V each
+constexpr int kMinUnits = 4;       // smallest range of a warp (128 keys)
+constexpr int kWholeUnits = 5;     // spans up to this many units are never cut
+constexpr int kMergeWarps = 8;     // warps of a combine block
+constexpr int kMaxWorkers = (kPlanSms * kCtasPerSm * kWarps + 255) / 256 * 256;  // cut ranges of a call
 constexpr uint64_t kWaitNs = 2000000000ull;  // limit of a wait for a bulk copy
 
 struct Params {
@@ -104,21 +108,55 @@ __device__ __forceinline__ int seq_units(const Params &p, int b, SeqRange &r, bo
         }
     }
     r = decode_range(p.seq_lens[b], p.seq_cap, p.window, 0, p.err, report);
-    return (r.L - r.base + 15) >> 4;
+    return (r.L - r.base + kUnit - 1) / kUnit;
 }
 
-template <int N>
-__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N]) {
-    if constexpr (N == 2)
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-    else
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+// Shared-memory loads at a constant offset from a register address.
+template <int OFF>
+__device__ __forceinline__ void lds_64(uint32_t addr, uint32_t &a, uint32_t &b) {
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2 + %3];" : "=r"(a), "=r"(b) : "r"(addr), "n"(OFF));
 }
-
+template <int OFF>
+__device__ __forceinline__ uint32_t lds_32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1 + %2];" : "=r"(v) : "r"(addr), "n"(OFF));
+    return v;
+}
+template <int OFF>
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=h"(v) : "r"(addr), "n"(OFF));
+    return v;
+}
+template <int OFF>
 __device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
     uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    asm volatile("ld.shared.u8 %0, [%1 + %2];" : "=r"(v) : "r"(addr), "n"(OFF));
     return v;
+}
+
+// The codes and scales of a lane's part of K row key_a (+ 2 rows: ROW 1) of a 16-key half: D / 32
+// words of codes (two k-steps each), scales as f16x2.
+template <int D, int OFF>
+__device__ __forceinline__ uint32_t k_row(uint32_t codes, uint32_t scales, uint32_t (&w)[D / 32]) {
+    if constexpr (D == 128) {  // 72-byte rows: 8-byte aligned
+        lds_64<OFF>(codes, w[0], w[1]);
+        lds_64<OFF + 8>(codes, w[2], w[3]);
+        return fp4::e4m3x2_to_f16x2(lds_u16<OFF>(scales));
+    } else {  // 36-byte rows: 4-byte aligned
+        w[0] = lds_32<OFF>(codes);
+        w[1] = lds_32<OFF + 4>(codes);
+        return fp4::e4m3x2_to_f16x2(lds_u8<OFF>(scales));
+    }
+}
+
+// V codes of one key row: the lane's D / 8 dims.
+template <int D, int OFF>
+__device__ __forceinline__ void v_row(uint32_t codes, uint32_t (&w)[D / 64]) {
+    if constexpr (D == 128)
+        lds_64<OFF>(codes, w[0], w[1]);
+    else
+        w[0] = lds_32<OFF>(codes);
 }
 
 __device__ __forceinline__ void sts_u32(uint32_t addr, uint32_t v) {
@@ -137,9 +175,9 @@ struct Segment {
 template <int D, int NT>
 __device__ __forceinline__ void split_body(const Params &p) {
     constexpr int RB = fp4::row_bytes(D);
-    constexpr int UB = 16 * RB;         // bytes of a unit of K (or V)
-    constexpr int SB = 2 * UB;          // bytes of a stage
-    constexpr int KC = D / 64;          // 16-dim groups of K a lane takes: t and t + 4
+    constexpr int HB = 16 * RB;         // bytes of a 16-key half of K (or V)
+    constexpr int UB = 2 * HB;          // bytes of a unit of K (or V)
+    constexpr int SB = 2 * UB;          // bytes of a stage: K halves, then V halves
     constexpr int KSTEPS = D / 16;
     constexpr int VW = D / 64;          // words of V codes a lane takes of a key row
     constexpr int VD = 8 * VW;          // dims of V a lane owns
@@ -251,7 +289,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
             f_end = f + seg.units;
         }
     }
-    long long todo = f < f_end ? f_end - f : 0;  // units this warp has to read
+    int todo = f < f_end ? static_cast<int>(f_end - f) : 0;  // units this warp has to read
     if (p.cuts != nullptr && lane == 0) {
         // The first cut of a segment lies at the start of this range: its last worker.
         int2 cut = make_int2(-1, 0);
@@ -301,20 +339,20 @@ __device__ __forceinline__ void split_body(const Params &p) {
     // ---- the issue side: units ahead of the consumer, across segments ----
     Segment is = seg;
     int iu = unit;                 // next unit to issue
-    long long ileft = todo;
-    int blk_lane = -1;             // lane i: block of unit (iu_base + i) of segment is
+    int ileft = todo;
+    int blk_lane = -1;             // lane i: block of 16-key half 2 iu_base + i of segment is
     int iu_base = iu;
     auto load_blocks = [&]() {
         iu_base = iu;
-        const int u = iu + lane;
-        blk_lane = u < is.units
-                       ? __ldg(p.block_table + static_cast<int64_t>(is.b) * p.max_num_blocks +
-                               ((is.r.base + 16 * u) >> p.log2_bs))
+        const int key = is.r.base + kUnit * iu + 16 * lane;
+        blk_lane = key < is.r.L
+                       ? __ldg(p.block_table + static_cast<int64_t>(is.b) * p.max_num_blocks + (key >> p.log2_bs))
                        : -1;
     };
     load_blocks();
     const int bs_mask = (1 << p.log2_bs) - 1;
-    // Issue the next unit into stage st (all lanes call; lane 0 copies).
+    const int64_t block_bytes = (static_cast<int64_t>(p.num_kv_heads) << p.log2_bs) * RB;
+    // Issue the next unit into stage st (all lanes call; lane h copies half h of K and of V).
     auto issue = [&](int st) {
         if (iu == is.units) {  // next segment
             if (++is.ht == p.head_tiles) {
@@ -329,27 +367,40 @@ __device__ __forceinline__ void split_body(const Params &p) {
             }
             iu = 0;
             load_blocks();
-        } else if (iu - iu_base == 32) {
+        } else if (iu - iu_base == 16) {
             load_blocks();
         }
-        const int blk = __shfl_sync(0xffffffffu, blk_lane, iu - iu_base);
+        const int half = lane & 1;
+        const int blk = __shfl_sync(0xffffffffu, blk_lane, 2 * (iu - iu_base) + half);
+        const int key = is.r.base + kUnit * iu + 16 * half;
         const uint32_t bar = bar0 + 8 * st;
-        const uint32_t dst = ring + st * SB;
-        if (blk >= 0 && blk < p.num_blocks) {
-            if (lane == 0) {
-                const int64_t row = ((static_cast<int64_t>(blk) * p.num_kv_heads + is.kvh) << p.log2_bs) +
-                                    ((is.r.base + 16 * iu) & bs_mask);
-                mbar_arrive_expect_tx(bar, SB);
-                bulk_load_policy(dst, p.k_cache + row * RB, UB, bar, policy);
-                bulk_load_policy(dst + UB, p.v_cache + row * RB, UB, bar, policy);
-            }
-        } else {
+        const uint32_t dst = ring + st * SB + half * HB;
+        const bool there = key < is.r.L;
+        const bool good = there && blk >= 0 && blk < p.num_blocks;
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, good) & 3u);
+        const bool bad = __any_sync(0xffffffffu, there && !good);
+        if (bad) {
             // A bad table entry reads as zeros.
-            if (lane == 0) flag_error(p.err, kErrBlockRange);
-            for (int i = lane; i < SB / 4; i += 32) sts_u32(dst + 4 * i, 0u);
+            if (there && !good) {
+                if (lane < 2) flag_error(p.err, kErrBlockRange);
+                for (int i = lane >> 1; i < HB / 4; i += 16) {
+                    sts_u32(dst + 4 * i, 0u);
+                    sts_u32(dst + UB + 4 * i, 0u);
+                }
+            }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
+        }
+        if (lane == 0) {
+            if (n > 0)
+                mbar_arrive_expect_tx(bar, n * 2 * HB);
+            else
+                mbar_arrive(bar);
+        }
+        if (lane < 2 && good) {
+            const int64_t off = blk * block_bytes + ((is.kvh << p.log2_bs) + (key & bs_mask)) * RB;
+            bulk_load_policy(dst, p.k_cache + off, HB, bar, policy);
+            bulk_load_policy(dst + UB, p.v_cache + off, HB, bar, policy);
         }
         ++iu;
         --ileft;
@@ -358,8 +409,8 @@ __device__ __forceinline__ void split_body(const Params &p) {
     for (int s = 0; s < kStages && ileft > 0; ++s) issue(s);
 
     // ---- the consumer side ----
-    // Q^T fragments of a segment: the B operand of S^T.  k-step ks is dims 4 (ks & 3) .. + 3 of
-    // group t (ks < 4) or t + 4; head 8 j + g.  Heads past the group are zero.
+    // Q^T fragments of a segment: the B operand of S^T.  k-step ks is dims D / 4 t + 4 ks .. + 3;
+    // head 8 j + g.  Heads past the group are zero.
     uint32_t qf[NT][KSTEPS][2];
     auto load_q = [&]() {
         const int rows_valid = min(16, p.group - seg.ht * 16);
@@ -368,36 +419,30 @@ __device__ __forceinline__ void split_body(const Params &p) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-                if (8 * j + g < rows_valid) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(
-                        qb + (8 * j + g) * D + 16 * (t + 4 * c));
-                    x[0] = __ldg(src);
-                    x[1] = __ldg(src + 1);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    qf[j][4 * c + 2 * h][0] = bf16x2_to_f16x2(x[h].x);
-                    qf[j][4 * c + 2 * h][1] = bf16x2_to_f16x2(x[h].y);
-                    qf[j][4 * c + 2 * h + 1][0] = bf16x2_to_f16x2(x[h].z);
-                    qf[j][4 * c + 2 * h + 1][1] = bf16x2_to_f16x2(x[h].w);
-                }
+            for (int c = 0; c < KSTEPS / 2; ++c) {
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (8 * j + g < rows_valid)
+                    x = __ldg(reinterpret_cast<const uint4 *>(qb + (8 * j + g) * D + D / 4 * t) + c);
+                qf[j][2 * c][0] = bf16x2_to_f16x2(x.x);
+                qf[j][2 * c][1] = bf16x2_to_f16x2(x.y);
+                qf[j][2 * c + 1][0] = bf16x2_to_f16x2(x.z);
+                qf[j][2 * c + 1][1] = bf16x2_to_f16x2(x.w);
             }
     };
     // O^T accumulators: tile i of 16 rows: row g is dim VD g + 2 i, row g + 8 dim VD g + 2 i + 1;
     // columns (heads) 8 j + 2 t and + 1.
     float o[NT][MT][4];
     // Per head: m_run is the reference maximum the weights are taken against (base 2); it moves
-    // only when a score exceeds it by more than 8.  l_run sums this lane's keys.
-    float m_run[NT][2], l_run[NT][2];
+    // only when a score exceeds it by more than 8.  lsum is the tile of the ones' product: every
+    // row of it is the denominator.
+    float m_run[NT][2], lsum[NT][4];
     auto reset = [&]() {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
 #pragma unroll
             for (int i = 0; i < MT; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
+            lsum[j][0] = lsum[j][1] = lsum[j][2] = lsum[j][3] = 0.f;
             m_run[j][0] = m_run[j][1] = -INFINITY;
-            l_run[j][0] = l_run[j][1] = 0.f;
         }
     };
     load_q();
@@ -407,7 +452,9 @@ __device__ __forceinline__ void split_body(const Params &p) {
     // MMA row r of a unit is key 4 (r % 8 / 2) + r % 2 + 2 (r / 8): rows 2 t, 2 t + 1, 2 t + 8 and
     // 2 t + 9 are keys 4 t .. 4 t + 3.
     const int key_a = 4 * (g >> 1) + (g & 1);  // of row g; row g + 8 is key_a + 2
-    const uint32_t k_off = key_a * RB, v_off = 4 * t * RB;
+    const uint32_t k_off = key_a * RB + D / 8 * t, ks_off = key_a * RB + D / 2 + (D == 128 ? 2 * t : t);
+    const uint32_t v_off = 4 * t * RB + 4 * VW * g, vs_off = 4 * t * RB + D / 2 + (D == 128 ? g : g >> 1);
+    constexpr uint32_t kOnes[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
 
     int st = 0;
     uint32_t phase = 0;
@@ -432,7 +479,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
         }
         const uint32_t kb = ring + st * SB;
         const uint32_t vb = kb + UB;
-        const int key0 = seg.r.base + 16 * unit;
+        const int key0 = seg.r.base + kUnit * unit;
         const bool last_unit = unit == seg.units - 1;
 
         // The new token's rows replace the unit's last key in shared memory, and are written
@@ -464,7 +511,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
                     reinterpret_cast<uint32_t *>(dst)[2 * gr + 1] = c.y;
                     dst[D / 2 + gr] = static_cast<uint8_t>(sc);
                     if (match) {
-                        const uint32_t row = (which ? vb : kb) + (pos & 15) * RB;
+                        const uint32_t row = (which ? vb : kb) + (pos - key0) * RB;
                         sts_u32(row + 8 * gr, c.x);
                         sts_u32(row + 8 * gr + 4, c.y);
                         asm volatile("st.shared.u8 [%0], %1;" ::"r"(row + D / 2 + gr), "r"(sc) : "memory");
@@ -475,36 +522,24 @@ __device__ __forceinline__ void split_body(const Params &p) {
             }
         }
 
-        // S^T = K Q^T: even and odd k-steps in separate accumulators.
-        float s[NT][4], s2[NT][4];
+        // S^T = K Q^T of the two halves.
+        float s[2][NT][4];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[j][e] = s2[j][e] = 0.f;
+            for (int j = 0; j < NT; ++j) s[h][j][0] = s[h][j][1] = s[h][j][2] = s[h][j][3] = 0.f;
 #pragma unroll
-        for (int c = 0; c < KC; ++c) {
-            uint32_t wa[2], wb[2];  // 16 codes of rows g and g + 8
-            if constexpr (D == 128) {
-                lds_words<2>(kb + k_off + 8 * (t + 4 * c), wa);
-                lds_words<2>(kb + k_off + 2 * RB + 8 * (t + 4 * c), wb);
-            } else {  // 36-byte rows: 4-byte aligned
+        for (int h = 0; h < 2; ++h) {
+            uint32_t wa[D / 32], wb[D / 32];  // codes of rows g and g + 8
+            const uint32_t ca = kb + h * HB + k_off, cs = kb + h * HB + ks_off;
+            const uint32_t sca = k_row<D, 0>(ca, cs, wa), scb = k_row<D, 2 * RB>(ca, cs, wb);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t x[1];
-                    lds_words<1>(kb + k_off + 8 * t + 4 * h, x);
-                    wa[h] = x[0];
-                    lds_words<1>(kb + k_off + 2 * RB + 8 * t + 4 * h, x);
-                    wb[h] = x[0];
-                }
-            }
-            const uint32_t sc = fp4::e4m3x2_to_f16x2(lds_u8(kb + k_off + D / 2 + t + 4 * c) |
-                                                     (lds_u8(kb + k_off + 2 * RB + D / 2 + t + 4 * c) << 8));
-            const uint32_t sa = __byte_perm(sc, 0u, 0x1010), sb = __byte_perm(sc, 0u, 0x3232);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int x = 0; x < D / 32; ++x) {
+                const uint32_t pick = (x >> 1) ? 0x3232 : 0x1010;  // a scale for two words
+                const uint32_t sa = __byte_perm(sca, 0u, pick), sb = __byte_perm(scb, 0u, pick);
                 uint32_t fa[4], fb[4];
-                fp4::e2m1x8_to_f16x2x4(wa[h], fa);
-                fp4::e2m1x8_to_f16x2x4(wb[h], fb);
+                fp4::e2m1x8_to_f16x2x4(wa[x], fa);
+                fp4::e2m1x8_to_f16x2x4(wb[x], fb);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const uint32_t a[4] = {fp4::mul_f16x2(fa[2 * k], sa), fp4::mul_f16x2(fb[2 * k], sb),
@@ -512,59 +547,68 @@ __device__ __forceinline__ void split_body(const Params &p) {
                                            fp4::mul_f16x2(fb[2 * k + 1], sb)};
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
-                        mma_f16_16816(k ? s2[j] : s[j], a, qf[j][4 * c + 2 * h + k][0],
-                                      qf[j][4 * c + 2 * h + k][1]);
+                        mma_f16_16816(s[h][j], a, qf[j][2 * x + k][0], qf[j][2 * x + k][1]);
                 }
             }
         }
 
-        // V codes and scales of keys 4 t .. 4 t + 3.
-        uint32_t vw[4][VW], vs[4];
+        // V codes and scales of keys 4 t .. 4 t + 3 of each half.
+        uint32_t vw[2][4][VW], vs[2][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            lds_words<VW>(vb + v_off + k * RB + 4 * VW * g, vw[k]);
-            vs[k] = lds_u8(vb + v_off + k * RB + D / 2 + (D == 128 ? g : g >> 1));
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t c = vb + h * HB + v_off, x = vb + h * HB + vs_off;
+            v_row<D, 0>(c, vw[h][0]);
+            v_row<D, RB>(c, vw[h][1]);
+            v_row<D, 2 * RB>(c, vw[h][2]);
+            v_row<D, 3 * RB>(c, vw[h][3]);
+            vs[h][0] = lds_u8<0>(x);
+            vs[h][1] = lds_u8<RB>(x);
+            vs[h][2] = lds_u8<2 * RB>(x);
+            vs[h][3] = lds_u8<3 * RB>(x);
         }
 
-        // Scale, mask (edge units only), online softmax per head column: elements 0, 1 are
-        // key key_a, elements 2, 3 key key_a + 2; elements 0, 2 head 2t, 1, 3 head 2t+1.
-        const bool edge = key0 < seg.r.start || key0 + 16 > seg.r.L;
+        // Mask (edge units only): element e of half h is key 16 h + key_a + (e & 2) and head
+        // 2 t + (e & 1).  Rows outside the range may hold anything: a zero scale makes V zeros.
+        if (key0 < seg.r.start || key0 + kUnit > seg.r.L) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = key0 + 16 * h + key_a + (e & 2);
+                    if (key < seg.r.start || key >= seg.r.L)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) s[h][j][e] = -INFINITY;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int key = key0 + 16 * h + 4 * t + k;
+                    if (key < seg.r.start || key >= seg.r.L) vs[h][k] = 0u;
+                }
+            }
+        }
+        // Online softmax per head column, the scale (> 0) folded into the exponent.
+        float mx[NT][2];
         bool over = false;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float v = (s[j][e] + s2[j][e]) * p.scale_log2;
-                if (edge) {
-                    const int key = key0 + key_a + (e & 2);
-                    if (key < seg.r.start || key >= seg.r.L) v = -INFINITY;
-                }
-                s[j][e] = v;
-                over |= v > m_run[j][e & 1] + 8.f;
+            for (int e = 0; e < 2; ++e) {
+                mx[j][e] = fmaxf(max3f(s[0][j][e], s[0][j][e + 2], s[1][j][e]), s[1][j][e + 2]) * p.scale_log2;
+                over |= mx[j][e] > m_run[j][e] + 8.f;
             }
-        if (edge) {
-            // Rows outside the range may hold anything: a zero scale makes them zeros.
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int key = key0 + 4 * t + k;
-                if (key < seg.r.start || key >= seg.r.L) vs[k] = 0u;
-            }
-        }
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 float fr[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float m = fmaxf(s[j][e], s[j][e + 2]);
+                    float m = mx[j][e];
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
                     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                    const float m_new = fmaxf(m_run[j][e], m);
-                    const bool nd = m_new > m_run[j][e] + 8.f;
-                    fr[e] = nd ? ex2_approx(m_run[j][e] - m_new) : 1.f;
-                    l_run[j][e] *= fr[e];
-                    if (nd) m_run[j][e] = m_new;
+                    const bool nd = m > m_run[j][e] + 8.f;
+                    fr[e] = nd ? ex2_approx(m_run[j][e] - m) : 1.f;
+                    if (nd) m_run[j][e] = m;
                 }
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
@@ -573,39 +617,48 @@ __device__ __forceinline__ void split_body(const Params &p) {
                     o[j][i][2] *= fr[0];
                     o[j][i][3] *= fr[1];
                 }
+                lsum[j][0] *= fr[0];
+                lsum[j][1] *= fr[1];
             }
         }
-        // P^T (B operand): f16 weights packed per key row and transposed; the denominator sums
-        // the rounded weights that the MMA uses.
-        uint32_t pb[NT][2];
+        // P^T (B operand): f16 weights packed per key row and transposed; the ones' product sums
+        // the rounded weights that V's product uses.
+        uint32_t pb[2][NT][2];
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const float m0 = m_run[j][0] == -INFINITY ? 0.f : m_run[j][0];
             const float m1 = m_run[j][1] == -INFINITY ? 0.f : m_run[j][1];
-            const uint32_t w0 = pack_f16x2(ex2_approx(s[j][0] - m0), ex2_approx(s[j][1] - m1));
-            const uint32_t w1 = pack_f16x2(ex2_approx(s[j][2] - m0), ex2_approx(s[j][3] - m1));
-            add_f16x2_f32(l_run[j][0], l_run[j][1], w0);
-            add_f16x2_f32(l_run[j][0], l_run[j][1], w1);
-            pb[j][0] = movmatrix_trans(w0);  // keys 4 t, 4 t + 1
-            pb[j][1] = movmatrix_trans(w1);  // keys 4 t + 2, 4 t + 3
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float *x = s[h][j];
+                pb[h][j][0] = movmatrix_trans(pack_f16x2(ex2_approx(fmaf(x[0], p.scale_log2, -m0)),
+                                                         ex2_approx(fmaf(x[1], p.scale_log2, -m1))));
+                pb[h][j][1] = movmatrix_trans(pack_f16x2(ex2_approx(fmaf(x[2], p.scale_log2, -m0)),
+                                                         ex2_approx(fmaf(x[3], p.scale_log2, -m1))));
+                mma_f16_16816(lsum[j], kOnes, pb[h][j][0], pb[h][j][1]);
+            }
         }
         // O^T += V^T P^T: the codes of two keys and one dim meet in a byte, low code first.
-        const uint32_t s01 = fp4::e4m3x2_to_f16x2(vs[0] | (vs[1] << 8));
-        const uint32_t s23 = fp4::e4m3x2_to_f16x2(vs[2] | (vs[3] << 8));
 #pragma unroll
-        for (int x = 0; x < VW; ++x) {
-            constexpr uint32_t LO = 0x0f0f0f0fu;
-            uint32_t f0[4], f1[4], f2[4], f3[4];
-            fp4::e2m1x8_to_f16x2x4((vw[0][x] & LO) | ((vw[1][x] << 4) & ~LO), f0);  // even dims
-            fp4::e2m1x8_to_f16x2x4(((vw[0][x] >> 4) & LO) | (vw[1][x] & ~LO), f1);  // odd dims
-            fp4::e2m1x8_to_f16x2x4((vw[2][x] & LO) | ((vw[3][x] << 4) & ~LO), f2);
-            fp4::e2m1x8_to_f16x2x4(((vw[2][x] >> 4) & LO) | (vw[3][x] & ~LO), f3);
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t s01 = fp4::e4m3x2_to_f16x2(vs[h][0] | (vs[h][1] << 8));
+            const uint32_t s23 = fp4::e4m3x2_to_f16x2(vs[h][2] | (vs[h][3] << 8));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t a[4] = {fp4::mul_f16x2(f0[k], s01), fp4::mul_f16x2(f1[k], s01),
-                                       fp4::mul_f16x2(f2[k], s23), fp4::mul_f16x2(f3[k], s23)};
+            for (int x = 0; x < VW; ++x) {
+                constexpr uint32_t LO = 0x0f0f0f0fu;
+                const uint32_t k0 = vw[h][0][x], k1 = vw[h][1][x], k2 = vw[h][2][x], k3 = vw[h][3][x];
+                uint32_t f0[4], f1[4], f2[4], f3[4];
+                fp4::e2m1x8_to_f16x2x4((k0 & LO) | ((k1 << 4) & ~LO), f0);  // even dims
+                fp4::e2m1x8_to_f16x2x4(((k0 >> 4) & LO) | (k1 & ~LO), f1);  // odd dims
+                fp4::e2m1x8_to_f16x2x4((k2 & LO) | ((k3 << 4) & ~LO), f2);
+                fp4::e2m1x8_to_f16x2x4(((k2 >> 4) & LO) | (k3 & ~LO), f3);
 #pragma unroll
-                for (int j = 0; j < NT; ++j) mma_f16_16816(o[j][4 * x + k], a, pb[j][0], pb[j][1]);
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t a[4] = {fp4::mul_f16x2(f0[k], s01), fp4::mul_f16x2(f1[k], s01),
+                                           fp4::mul_f16x2(f2[k], s23), fp4::mul_f16x2(f3[k], s23)};
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) mma_f16_16816(o[j][4 * x + k], a, pb[h][j][0], pb[h][j][1]);
+                }
             }
         }
         __syncwarp();
@@ -619,14 +672,6 @@ __device__ __forceinline__ void split_body(const Params &p) {
         if (!last_unit && todo > 0) continue;
 
         // ---- end of the segment's piece: lanes t hold heads 2 t, 2 t + 1 of each n-tile ----
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                l_run[j][e] += __shfl_xor_sync(0xffffffffu, l_run[j][e], 4);
-                l_run[j][e] += __shfl_xor_sync(0xffffffffu, l_run[j][e], 8);
-                l_run[j][e] += __shfl_xor_sync(0xffffffffu, l_run[j][e], 16);
-            }
         const int rows_valid = min(16, p.group - seg.ht * 16);
         const bool whole = first_unit == 0 && last_unit;
         const int64_t row = p.q_rows != nullptr ? p.q_rows[seg.b] : seg.b;
@@ -641,7 +686,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
                 const int h = 8 * j + 2 * t + e;
                 if (h >= rows_valid) continue;
                 if (whole) {
-                    const float inv = p.kv_scale / l_run[j][e];
+                    const float inv = p.kv_scale / lsum[j][e];
                     uint32_t x[MT];
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
@@ -656,7 +701,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
                     for (int i = 0; i < MT; ++i)
                         *reinterpret_cast<float2 *>(ph + VD * g + 2 * i) =
                             make_float2(o[j][i][e], o[j][i][e + 2]);
-                    if (g == 0) *reinterpret_cast<float2 *>(ph + D) = make_float2(m_run[j][e], l_run[j][e]);
+                    if (g == 0) *reinterpret_cast<float2 *>(ph + D) = make_float2(m_run[j][e], lsum[j][e]);
                 }
             }
         if (todo == 0) break;
@@ -694,31 +739,72 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : 3)
     if (p.after_prefill && blockIdx.x == gridDim.x - 1) griddep_wait();
 }
 
-// Merge of the pieces of one cut segment, a block for each worker; the worker whose range
-// starts at the segment's first cut does it.  With piece i holding (m_i, l_i, O_i):
+// Merge of the pieces of the cut segments: one item for each (cut segment, head).  With piece i
+// holding (m_i, l_i, O_i):
 //     M = max m_i,  out = kv_scale * sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+// Every block finds the first cuts among all workers' entries by itself; as many warps as there
+// are for an item share its pieces (one long sequence may be cut into a hundred).
 template <int D>
-__global__ void __launch_bounds__(128) decode_fp4_combine_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kMergeWarps * 32) decode_fp4_combine_kernel(const __grid_constant__ Params p) {
     constexpr int PER = D / 32;
+    constexpr int kPer = kMaxWorkers / (kMergeWarps * 32);  // entries a thread looks at
+    static_assert(kMaxWorkers % (kMergeWarps * 32) == 0, "whole rounds of entries");
+    __shared__ int list[kMaxWorkers];
+    __shared__ int counts[kMergeWarps];
+    __shared__ float part[kMergeWarps][D + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     griddep_wait();
-    const int w = blockIdx.x;
-    const int2 cut = p.cuts[w];
-    if (cut.x < 0) return;
+    bool mine[kPer];
+    int n_mine = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int w = threadIdx.x + k * kMergeWarps * 32;
+        mine[k] = w < p.workers && p.cuts[w].x >= 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) n_mine += __popc(__ballot_sync(0xffffffffu, mine[k]));
+    if (lane == 0) counts[warp] = n_mine;
+    __syncthreads();
+    int at = 0, n_cuts = 0;
+#pragma unroll
+    for (int v = 0; v < kMergeWarps; ++v) {
+        if (v < warp) at += counts[v];
+        n_cuts += counts[v];
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const unsigned m = __ballot_sync(0xffffffffu, mine[k]);
+        if (mine[k]) list[at + __popc(m & ((1u << lane) - 1u))] = threadIdx.x + k * kMergeWarps * 32;
+        at += __popc(m);
+    }
+    __syncthreads();
     const int HT = p.num_kv_heads * p.head_tiles;
-    const int b = cut.x / HT;
-    const int hs = cut.x - b * HT;
-    const int kvh = hs / p.head_tiles, ht = hs - kvh * p.head_tiles;
-    const int rows_valid = min(16, p.group - ht * 16);
-    const int lane = threadIdx.x & 31;
-    const int64_t row = p.q_rows != nullptr ? p.q_rows[b] : b;
     const int64_t stride = static_cast<int64_t>(p.tile_heads) * (D + 2);
-    for (int h = threadIdx.x >> 5; h < rows_valid; h += 4) {
+    const int items = n_cuts * p.tile_heads;
+    int share = kMergeWarps;  // warps an item
+    while (share > 1 && items * share > static_cast<int>(gridDim.x) * kMergeWarps) share >>= 1;
+    const int per_block = kMergeWarps / share;
+    const int sub = warp & (share - 1);
+    for (int i0 = blockIdx.x * per_block; i0 < items; i0 += gridDim.x * per_block) {
+        const int item = i0 + warp / share;
+        bool valid = item < items;
+        int h = 0, row_h = 0, b = 0, n = 0, w = 0;
+        if (valid) {
+            w = list[item / p.tile_heads];
+            h = item % p.tile_heads;
+            const int2 cut = p.cuts[w];
+            b = cut.x / HT;
+            const int hs = cut.x - b * HT;
+            const int kvh = hs / p.head_tiles, ht = hs - kvh * p.head_tiles;
+            valid = h < p.group - ht * 16;
+            row_h = kvh * p.group + ht * 16 + h;
+            n = valid ? cut.y - w + 2 : 0;
+        }
         // Piece 0 is the second one of worker w - 1; piece i the first one of worker w - 1 + i.
         auto piece = [&](int i) {
             return p.pieces + ((static_cast<int64_t>(w - 1 + i)) * 2 + (i == 0 ? 1 : 0)) * stride +
                    h * (D + 2);
         };
-        const int n = cut.y - w + 2;
         float M = -INFINITY;
         for (int i = lane; i < n; i += 32) M = fmaxf(M, piece(i)[D]);
         M = warp_max(M);
@@ -726,18 +812,20 @@ __global__ void __launch_bounds__(128) decode_fp4_combine_kernel(const __grid_co
         float acc[PER], den = 0.f;
 #pragma unroll
         for (int k = 0; k < PER; ++k) acc[k] = 0.f;
-        for (int i0 = 0; i0 < n; i0 += 32) {
+        // This warp's pieces are sub, sub + share, ...: lane l holds the weight of the l-th.
+        for (int i0p = sub; i0p < n; i0p += 32 * share) {
+            const int mine_i = i0p + lane * share;
             float wt = 0.f;
-            if (i0 + lane < n) {
-                const float *ml = piece(i0 + lane) + D;
-                wt = ex2_approx(ml[0] - M);
-                den += wt * ml[1];
+            if (mine_i < n) {
+                const float2 ml = *reinterpret_cast<const float2 *>(piece(mine_i) + D);
+                wt = ex2_approx(ml.x - M);
+                den += wt * ml.y;
             }
-            const int m = min(32, n - i0);
-#pragma unroll 4
+            const int m = min(32, (n - i0p + share - 1) / share);
+#pragma unroll 8
             for (int k = 0; k < m; ++k) {
                 const float x = __shfl_sync(0xffffffffu, wt, k);
-                const float2 *src = reinterpret_cast<const float2 *>(piece(i0 + k)) + lane * (PER / 2);
+                const float2 *src = reinterpret_cast<const float2 *>(piece(i0p + k * share)) + lane * (PER / 2);
 #pragma unroll
                 for (int c = 0; c < PER / 2; ++c) {
                     const float2 v = src[c];
@@ -747,9 +835,23 @@ __global__ void __launch_bounds__(128) decode_fp4_combine_kernel(const __grid_co
             }
         }
         den = warp_sum(den);
+        if (share > 1) {
+            __syncthreads();  // the previous item's sums have been read
+#pragma unroll
+            for (int k = 0; k < PER; ++k) part[warp][lane * PER + k] = acc[k];
+            if (lane == 0) part[warp][D] = den;
+            __syncthreads();
+            if (sub != 0) continue;
+            for (int v = 1; v < share; ++v) {
+#pragma unroll
+                for (int k = 0; k < PER; ++k) acc[k] += part[warp + v][lane * PER + k];
+                den += part[warp + v][D];
+            }
+        }
+        if (!valid) continue;
         const float inv = p.kv_scale / den;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(
-            p.out + (row * p.num_heads + kvh * p.group + ht * 16 + h) * D + lane * PER);
+        const int64_t row = p.q_rows != nullptr ? p.q_rows[b] : b;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + (row * p.num_heads + row_h) * D + lane * PER);
 #pragma unroll
         for (int c = 0; c < PER / 2; ++c) dst[c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
     }
@@ -757,7 +859,7 @@ __global__ void __launch_bounds__(128) decode_fp4_combine_kernel(const __grid_co
 
 template <int D, int NT>
 cudaError_t launch_d(const Params &p, int blocks, bool combine, cudaStream_t stream) {
-    constexpr int smem = kWarps * kStages * 2 * 16 * fp4::row_bytes(D);
+    constexpr int smem = kWarps * kStages * 2 * kUnit * fp4::row_bytes(D);
     static std::atomic<uint64_t> smem_set;
     auto kern = decode_fp4_split_kernel<D, NT>;
     cudaError_t e = smem_limit_once(kern, smem, smem_set);
@@ -774,8 +876,8 @@ cudaError_t launch_d(const Params &p, int blocks, bool combine, cudaStream_t str
     cfg.numAttrs = p.after_prefill ? 1 : 0;
     e = cudaLaunchKernelEx(&cfg, kern, p);
     if (e != cudaSuccess || !combine) return e;
-    cfg.gridDim = dim3(p.workers);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(2 * kPlanSms);
+    cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, decode_fp4_combine_kernel<D>, p);
@@ -797,7 +899,7 @@ bool plan_decode_fp4(int batch, int num_heads, int num_kv_heads, int head_dim, i
     int64_t span = max_seq_len;
     if (sliding_window > 0 && static_cast<int64_t>(sliding_window) + 15 < span)
         span = static_cast<int64_t>(sliding_window) + 15;
-    const int64_t units = (span + 15) / 16;
+    const int64_t units = (span + kUnit - 1) / kUnit;
     const int64_t segments = static_cast<int64_t>(batch) * num_kv_heads * p.head_tiles;
     // Whole segments when they are short: one launch and no merge.
     p.whole = units <= kWholeUnits;
@@ -807,6 +909,7 @@ bool plan_decode_fp4(int batch, int num_heads, int num_kv_heads, int head_dim, i
     if (!p.whole && blocks > resident) blocks = resident;
     if (blocks < 1) blocks = 1;
     if (blocks > 0x7fffffffLL / kWarps) return false;
+    if (segments * units / blocks > 0x3fffffff) return false;  // a warp counts its units in 32 bits
     p.blocks = static_cast<int>(blocks);
     p.workers = p.blocks * kWarps;
     if (!p.whole) {
