@@ -9,8 +9,10 @@
 //    units, cut into equal ranges, one for each resident warp.  A warp streams its range
 //    through its own ring of shared-memory stages without stopping at segment ends, so there
 //    are no waves of blocks, no ragged tail and one pipeline fill a warp.
-//  * 16 tokens of one kv head are 9 D contiguous bytes (rows of codes and scales): a unit is
-//    two bulk copies of K and two of V, which two lanes issue.
+//  * 16 tokens of one kv head are 9 D contiguous bytes (rows of codes and scales), so a unit is
+//    four runs (K and V of two 16-key halves) that the lanes copy 16 bytes at a time
+//    (cp.async), a lane's chunks at constant distances.  (Bulk copies, which one lane issues,
+//    took more issue slots: their operands go through uniform registers one copy at a time.)
 //  * The products are f16 warp MMAs (m16n8k16, fp32 accumulate) with 16 keys as the M rows of
 //    S^T = K Q^T and the head dims as those of O^T += V^T P^T, the query heads the 8 columns
 //    of an n-tile (two n-tiles above 8 heads a kv head).  Codes become f16 by one conversion
@@ -49,7 +51,6 @@ constexpr int kMinUnits = 4;       // smallest range of a warp (128 keys)
 constexpr int kWholeUnits = 5;     // spans up to this many units are never cut
 constexpr int kMergeWarps = 8;     // warps of a combine block
 constexpr int kMaxWorkers = (kPlanSms * kCtasPerSm * kWarps + 255) / 256 * 256;  // cut ranges of a call
-constexpr uint64_t kWaitNs = 2000000000ull;  // limit of a wait for a bulk copy
 
 struct Params {
     __nv_bfloat16 *out;
@@ -135,6 +136,16 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
     return v;
 }
 
+// D(16x8 f32) = A(16x16 f16, row) * B(16x8 f16, col)
+__device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                   uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // The codes and scales of a lane's part of K row key_a (+ 2 rows: ROW 1) of a 16-key half: D / 32
 // words of codes (two k-steps each), scales as f16x2.
 template <int D, int OFF>
@@ -172,19 +183,37 @@ struct Segment {
     int units;
 };
 
+// The next segment of the list (the caller knows that there is one).
+__device__ __forceinline__ void advance(const Params &p, Segment &s) {
+    if (++s.ht < p.head_tiles) return;
+    s.ht = 0;
+    if (++s.kvh < p.num_kv_heads) return;
+    s.kvh = 0;
+    do {
+        ++s.b;
+        s.units = max(seq_units(p, s.b, s.r, false), 0);
+    } while (s.units == 0);
+}
+
+// Where a warp's copies are: ahead of its products.
+struct Ahead {
+    Segment seg;
+    int unit;  // next unit of the segment
+    int left;  // units of the warp's range not listed yet
+};
+
 template <int D, int NT>
 __device__ __forceinline__ void split_body(const Params &p) {
     constexpr int RB = fp4::row_bytes(D);
     constexpr int HB = 16 * RB;         // bytes of a 16-key half of K (or V)
-    constexpr int UB = 2 * HB;          // bytes of a unit of K (or V)
-    constexpr int SB = 2 * UB;          // bytes of a stage: K halves, then V halves
+    constexpr int SB = 4 * HB;          // bytes of a stage: K and V of half 0, then of half 1
     constexpr int KSTEPS = D / 16;
     constexpr int VW = D / 64;          // words of V codes a lane takes of a key row
     constexpr int VD = 8 * VW;          // dims of V a lane owns
     constexpr int MT = D / 16;          // m-tiles of O^T
 
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t bars[kWarps * kStages];
+    __shared__ Ahead s_ahead[kWarps];
     __shared__ long long part_sum[kWarps * 32];
     __shared__ long long s_total;
 
@@ -193,14 +222,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
     const int g = lane >> 2, t = lane & 3;
     const int HT = p.num_kv_heads * p.head_tiles;  // segments of a sequence
     const uint32_t ring = smem_u32(smem) + warp * kStages * SB;
-    const uint32_t bar0 = smem_u32(&bars[warp * kStages]);
     const uint64_t policy = l2_policy_evict_first();
-
-    if (lane == 0) {
-        for (int s = 0; s < kStages; ++s) mbar_init(bar0 + 8 * s, 1);
-        fence_barrier_init();
-    }
-    __syncwarp();
 
     // ---- this warp's range [f, f_end) of the flat unit list ----
     // Worker w of warp v of block c is v * blocks + c: few workers spread over many SMs.
@@ -337,76 +359,76 @@ __device__ __forceinline__ void split_body(const Params &p) {
     if (todo == 0) return;
 
     // ---- the issue side: units ahead of the consumer, across segments ----
-    Segment is = seg;
-    int iu = unit;                 // next unit to issue
-    int ileft = todo;
-    int blk_lane = -1;             // lane i: block of 16-key half 2 iu_base + i of segment is
-    int iu_base = iu;
-    auto load_blocks = [&]() {
-        iu_base = iu;
-        const int key = is.r.base + kUnit * iu + 16 * lane;
-        blk_lane = key < is.r.L
-                       ? __ldg(p.block_table + static_cast<int64_t>(is.b) * p.max_num_blocks + (key >> p.log2_bs))
-                       : -1;
-    };
-    load_blocks();
-    const int bs_mask = (1 << p.log2_bs) - 1;
+    // Its place is kept in shared memory: it is needed once for 16 units.  In registers are the
+    // byte offsets of the next units' halves, lane i that of half i (less the place of its runs
+    // in a stage; odd: past the sequence or a bad table entry, read as zeros), and how many units they cover.
+    s_ahead[warp].seg = seg;
+    s_ahead[warp].unit = unit;
+    s_ahead[warp].left = todo;
+    __syncwarp();
     const int64_t block_bytes = (static_cast<int64_t>(p.num_kv_heads) << p.log2_bs) * RB;
-    // Issue the next unit into stage st (all lanes call; lane h copies half h of K and of V).
-    auto issue = [&](int st) {
-        if (iu == is.units) {  // next segment
-            if (++is.ht == p.head_tiles) {
-                is.ht = 0;
-                if (++is.kvh == p.num_kv_heads) {
-                    is.kvh = 0;
-                    do {
-                        ++is.b;
-                        is.units = max(seq_units(p, is.b, is.r, false), 0);
-                    } while (is.units == 0);
-                }
+    const int bs_mask = (1 << p.log2_bs) - 1;
+    long long half_off = 0;
+    int listed = 0, next = 0;  // units of the list, units issued of it
+    auto list_units = [&]() {
+        Ahead a = s_ahead[warp];
+        next = listed = 0;
+        if (a.left == 0) return;
+        if (a.unit == a.seg.units) {
+            advance(p, a.seg);
+            a.unit = 0;
+        }
+        listed = min(16, min(a.left, a.seg.units - a.unit));
+        const int key = a.seg.r.base + kUnit * a.unit + 16 * lane;
+        half_off = -(lane & 1) * 2 * HB + 1;
+        if (lane < 2 * listed && key < a.seg.r.L) {
+            const int blk = __ldg(p.block_table + static_cast<int64_t>(a.seg.b) * p.max_num_blocks + (key >> p.log2_bs));
+            if (blk >= 0 && blk < p.num_blocks) {
+                half_off += blk * block_bytes + ((a.seg.kvh << p.log2_bs) + (key & bs_mask)) * RB - 1;
+            } else {
+                flag_error(p.err, kErrBlockRange);
             }
-            iu = 0;
-            load_blocks();
-        } else if (iu - iu_base == 16) {
-            load_blocks();
         }
-        const int half = lane & 1;
-        const int blk = __shfl_sync(0xffffffffu, blk_lane, 2 * (iu - iu_base) + half);
-        const int key = is.r.base + kUnit * iu + 16 * half;
-        const uint32_t bar = bar0 + 8 * st;
-        const uint32_t dst = ring + st * SB + half * HB;
-        const bool there = key < is.r.L;
-        const bool good = there && blk >= 0 && blk < p.num_blocks;
-        const uint32_t n = __popc(__ballot_sync(0xffffffffu, good) & 3u);
-        const bool bad = __any_sync(0xffffffffu, there && !good);
-        if (bad) {
-            // A bad table entry reads as zeros.
-            if (there && !good) {
-                if (lane < 2) flag_error(p.err, kErrBlockRange);
-                for (int i = lane >> 1; i < HB / 4; i += 16) {
-                    sts_u32(dst + 4 * i, 0u);
-                    sts_u32(dst + UB + 4 * i, 0u);
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-        }
-        if (lane == 0) {
-            if (n > 0)
-                mbar_arrive_expect_tx(bar, n * 2 * HB);
-            else
-                mbar_arrive(bar);
-        }
-        if (lane < 2 && good) {
-            const int64_t off = blk * block_bytes + ((is.kvh << p.log2_bs) + (key & bs_mask)) * RB;
-            bulk_load_policy(dst, p.k_cache + off, HB, bar, policy);
-            bulk_load_policy(dst + UB, p.v_cache + off, HB, bar, policy);
-        }
-        ++iu;
-        --ileft;
+        a.unit += listed;
+        a.left -= listed;
+        __syncwarp();
+        if (lane == 0) s_ahead[warp] = a;
+        __syncwarp();
     };
+    // Issue the next unit (if there is one) into stage st.  Chunk c of the unit's SB / 16 belongs
+    // to run c / CH (K and V of half 0, K and V of half 1); lane l copies chunks l, l + 32, ...
+    const uint8_t *k_lane = p.k_cache + 16 * lane, *v_lane = p.v_cache + (16 * lane - HB);
+    auto issue = [&](int st) {
+        constexpr int CH = HB / 16, NC = SB / 16, last = NC - 1;
+        if (next == listed) list_units();
+        if (next < listed) {
+            const uint8_t *run[4];
+            uint32_t size[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                long long off = __shfl_sync(0xffffffffu, half_off, 2 * next + h);
+                size[h] = (off & 1) ? 0u : 16u;
+                off &= ~1ll;
+                run[2 * h] = k_lane + off;
+                run[2 * h + 1] = v_lane + off;
+            }
+            const uint32_t dst = ring + st * SB + 16 * lane;
+#pragma unroll
+            for (int i = 0; i < (NC + 31) / 32; ++i) {
+                const int r0 = 32 * i / CH, r1 = (32 * i + 31 < last ? 32 * i + 31 : last) / CH;
+                const bool second = r1 != r0 && 32 * i + lane >= r1 * CH;
+                const uint8_t *src = (second ? run[r1] : run[r0]) + 512 * i;
+                const uint32_t n = second ? size[r1 >> 1] : size[r0 >> 1];
+                if (32 * i + 31 <= last || 32 * i + lane <= last) cp_async_16_policy(dst + 512 * i, src, n, policy);
+            }
+            ++next;
+        }
+        cp_async_commit();
+    };
+    // kStages - 1 units in flight before the first one is waited for; every step commits one
+    // group, so that counting groups counts units.
 #pragma unroll 1
-    for (int s = 0; s < kStages && ileft > 0; ++s) issue(s);
+    for (int s = 0; s < kStages - 1; ++s) issue(s);
 
     // ---- the consumer side ----
     // Q^T fragments of a segment: the B operand of S^T.  k-step ks is dims D / 4 t + 4 ks .. + 3;
@@ -457,28 +479,14 @@ __device__ __forceinline__ void split_body(const Params &p) {
     constexpr uint32_t kOnes[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
 
     int st = 0;
-    uint32_t phase = 0;
-    bool ok = true;
 #pragma unroll 1
     for (;;) {
-        {
-            uint64_t t0 = 0;
-            for (uint32_t it = 0;; ++it) {
-                const bool done = mbar_try_wait(bar0 + 8 * st, phase);
-                if (__all_sync(0xffffffffu, done)) break;
-                if ((it & 31u) == 31u) {
-                    const uint64_t now = globaltimer_ns();
-                    if (t0 == 0) t0 = now;
-                    if (__any_sync(0xffffffffu, now - t0 > kWaitNs)) {
-                        ok = false;
-                        break;
-                    }
-                }
-            }
-            if (!ok) break;
-        }
+        // The stage that the previous unit left takes the next one.
+        issue(st == 0 ? kStages - 1 : st - 1);
+        cp_async_wait<kStages - 1>();
+        __syncwarp();
         const uint32_t kb = ring + st * SB;
-        const uint32_t vb = kb + UB;
+        const uint32_t vb = kb + HB;  // of half 0; half 1 is 2 HB further
         const int key0 = seg.r.base + kUnit * unit;
         const bool last_unit = unit == seg.units - 1;
 
@@ -511,13 +519,13 @@ __device__ __forceinline__ void split_body(const Params &p) {
                     reinterpret_cast<uint32_t *>(dst)[2 * gr + 1] = c.y;
                     dst[D / 2 + gr] = static_cast<uint8_t>(sc);
                     if (match) {
-                        const uint32_t row = (which ? vb : kb) + (pos - key0) * RB;
+                        const int j = pos - key0;
+                        const uint32_t row = (which ? vb : kb) + (j >> 4) * 2 * HB + (j & 15) * RB;
                         sts_u32(row + 8 * gr, c.x);
                         sts_u32(row + 8 * gr + 4, c.y);
                         asm volatile("st.shared.u8 [%0], %1;" ::"r"(row + D / 2 + gr), "r"(sc) : "memory");
                     }
                 }
-                fence_proxy_async_smem();  // before the next copy into this stage
                 __syncwarp();
             }
         }
@@ -525,13 +533,9 @@ __device__ __forceinline__ void split_body(const Params &p) {
         // S^T = K Q^T of the two halves.
         float s[2][NT][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) s[h][j][0] = s[h][j][1] = s[h][j][2] = s[h][j][3] = 0.f;
-#pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t wa[D / 32], wb[D / 32];  // codes of rows g and g + 8
-            const uint32_t ca = kb + h * HB + k_off, cs = kb + h * HB + ks_off;
+            const uint32_t ca = kb + 2 * h * HB + k_off, cs = kb + 2 * h * HB + ks_off;
             const uint32_t sca = k_row<D, 0>(ca, cs, wa), scb = k_row<D, 2 * RB>(ca, cs, wb);
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) {
@@ -546,8 +550,12 @@ __device__ __forceinline__ void split_body(const Params &p) {
                                            fp4::mul_f16x2(fa[2 * k + 1], sa),
                                            fp4::mul_f16x2(fb[2 * k + 1], sb)};
 #pragma unroll
-                    for (int j = 0; j < NT; ++j)
-                        mma_f16_16816(s[h][j], a, qf[j][2 * x + k][0], qf[j][2 * x + k][1]);
+                    for (int j = 0; j < NT; ++j) {
+                        if (x == 0 && k == 0)
+                            mma_f16_16816_zero(s[h][j], a, qf[j][0][0], qf[j][0][1]);
+                        else
+                            mma_f16_16816(s[h][j], a, qf[j][2 * x + k][0], qf[j][2 * x + k][1]);
+                    }
                 }
             }
         }
@@ -556,7 +564,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
         uint32_t vw[2][4][VW], vs[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t c = vb + h * HB + v_off, x = vb + h * HB + vs_off;
+            const uint32_t c = vb + 2 * h * HB + v_off, x = vb + 2 * h * HB + vs_off;
             v_row<D, 0>(c, vw[h][0]);
             v_row<D, RB>(c, vw[h][1]);
             v_row<D, 2 * RB>(c, vw[h][2]);
@@ -662,11 +670,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
             }
         }
         __syncwarp();
-        if (ileft > 0) issue(st);
-        if (++st == kStages) {
-            st = 0;
-            phase ^= 1u;
-        }
+        if (++st == kStages) st = 0;
         --todo;
         ++unit;
         if (!last_unit && todo > 0) continue;
@@ -706,27 +710,12 @@ __device__ __forceinline__ void split_body(const Params &p) {
             }
         if (todo == 0) break;
         // Next segment.
-        if (++seg.ht == p.head_tiles) {
-            seg.ht = 0;
-            if (++seg.kvh == p.num_kv_heads) {
-                seg.kvh = 0;
-                do {
-                    ++seg.b;
-                    seg.units = max(seq_units(p, seg.b, seg.r, false), 0);
-                } while (seg.units == 0);
-            }
-        }
+        advance(p, seg);
         unit = first_unit = 0;
         load_q();
         reset();
     }
-    if (!ok) {
-        // A copy never landed: flagged; give the copies in flight time to land, then leave.
-        if (lane == 0) flag_error(p.err, kErrTimeout);
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 2000000ull) {
-        }
-    }
+    cp_async_wait<0>();
 }
 
 template <int D, int NT>
