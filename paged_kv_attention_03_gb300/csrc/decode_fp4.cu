@@ -44,13 +44,12 @@ namespace {
 using namespace sm100;
 
 constexpr int kWarps = 4;          // independent warps of a block
-constexpr int kCtasPerSm = 4;      // resident blocks: 16 warps an SM
+constexpr int kCtas1 = 3, kCtas2 = 2;  // resident blocks an SM with one and two n-tiles of heads
 constexpr int kUnit = 32;          // keys of a unit: two 16-key halves
 constexpr int kStages = 3;         // ring stages of a warp, one unit of K and V each
 constexpr int kMinUnits = 4;       // smallest range of a warp (128 keys)
 constexpr int kWholeUnits = 5;     // spans up to this many units are never cut
 constexpr int kMergeWarps = 8;     // warps of a combine block
-constexpr int kMaxWorkers = (kPlanSms * kCtasPerSm * kWarps + 255) / 256 * 256;  // cut ranges of a call
 
 struct Params {
     __nv_bfloat16 *out;
@@ -75,7 +74,6 @@ struct Params {
     int whole_units;   // > 0: ranges are whole segments of at most this many units
     float *pieces;     // [workers][2][tile heads][D + 2]: O, m, l of a cut segment's piece
     int tile_heads;    // min(group, 16)
-    int2 *cuts;        // [workers]: (segment, its last worker) if the first cut of it is here
     // Fused store of each sequence's new token (null when not fused).
     const __nv_bfloat16 *key;
     const __nv_bfloat16 *value;
@@ -110,6 +108,12 @@ __device__ __forceinline__ int seq_units(const Params &p, int b, SeqRange &r, bo
     }
     r = decode_range(p.seq_lens[b], p.seq_cap, p.window, 0, p.err, report);
     return (r.L - r.base + kUnit - 1) / kUnit;
+}
+
+// Units of a worker's range when the whole list has `total`.
+__device__ __forceinline__ long long range_of(const Params &p, long long total) {
+    const long long r = (total + p.workers - 1) / p.workers;
+    return r < kMinUnits ? kMinUnits : r;
 }
 
 // Shared-memory loads at a constant offset from a register address.
@@ -272,8 +276,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
         seg.b = w / HT;
     } else {
         const long long total = s_total * HT;
-        range = (total + p.workers - 1) / p.workers;
-        if (range < kMinUnits) range = kMinUnits;
+        range = range_of(p, total);
         f = min(total, range * w);
         f_end = min(total, f + range);
     }
@@ -312,16 +315,6 @@ __device__ __forceinline__ void split_body(const Params &p) {
         }
     }
     int todo = f < f_end ? static_cast<int>(f_end - f) : 0;  // units this warp has to read
-    if (p.cuts != nullptr && lane == 0) {
-        // The first cut of a segment lies at the start of this range: its last worker.
-        int2 cut = make_int2(-1, 0);
-        if (todo > 0 && unit > 0 && unit <= range) {
-            cut.x = seg.b * HT + seg.kvh * p.head_tiles + seg.ht;
-            cut.y = static_cast<int>((f - unit + seg.units - 1) / range);
-        }
-        p.cuts[w] = cut;
-    }
-
     // ---- rows without keys (zeros), and their new tokens ----
     for (int b = blockIdx.x; b < p.batch; b += gridDim.x) {
         SeqRange r;
@@ -719,7 +712,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : 3)
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtas1 : kCtas2)
     decode_fp4_split_kernel(const __grid_constant__ Params p) {
     griddep_launch_dependents();
     split_body<D, NT>(p);
@@ -728,121 +721,144 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtasPerSm : 3)
     if (p.after_prefill && blockIdx.x == gridDim.x - 1) griddep_wait();
 }
 
-// Merge of the pieces of the cut segments: one item for each (cut segment, head).  With piece i
-// holding (m_i, l_i, O_i):
+// Merge of the pieces of the cut segments, a block taking consecutive (segment, head) items and
+// as many warps as there are for an item sharing its pieces (one long sequence may be cut into a
+// hundred).  With piece i holding (m_i, l_i, O_i):
 //     M = max m_i,  out = kv_scale * sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
-// Every block finds the first cuts among all workers' entries by itself; as many warps as there
-// are for an item share its pieces (one long sequence may be cut into a hundred).
+// Where a segment is cut follows from the lengths alone, so that is worked out before the wait
+// for the split grid; after it there is one round trip for eight pieces.
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) decode_fp4_combine_kernel(const __grid_constant__ Params p) {
     constexpr int PER = D / 32;
-    constexpr int kPer = kMaxWorkers / (kMergeWarps * 32);  // entries a thread looks at
-    static_assert(kMaxWorkers % (kMergeWarps * 32) == 0, "whole rounds of entries");
-    __shared__ int list[kMaxWorkers];
-    __shared__ int counts[kMergeWarps];
-    __shared__ float part[kMergeWarps][D + 1];
+    constexpr int BATCH = 8;  // pieces in flight
+    __shared__ long long sums[2][kMergeWarps];
+    __shared__ float part[kMergeWarps][D + 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    griddep_wait();
-    bool mine[kPer];
-    int n_mine = 0;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const int w = threadIdx.x + k * kMergeWarps * 32;
-        mine[k] = w < p.workers && p.cuts[w].x >= 0;
+    const int HT = p.num_kv_heads * p.head_tiles;
+    const int64_t items = static_cast<int64_t>(p.batch) * HT * p.tile_heads;
+    const int64_t per_block = (items + gridDim.x - 1) / gridDim.x;
+    const int64_t i0 = blockIdx.x * per_block, i1 = min(items, i0 + per_block);
+    int b = static_cast<int>(min(i0 / (HT * p.tile_heads), static_cast<int64_t>(p.batch)));
+    SeqRange r;
+    long long before = 0, total = 0;  // units of sequences before b, and of all
+    for (int k = threadIdx.x; k < p.batch; k += kMergeWarps * 32) {
+        const int u = max(seq_units(p, k, r, false), 0);
+        total += u;
+        if (k < b) before += u;
     }
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) n_mine += __popc(__ballot_sync(0xffffffffu, mine[k]));
-    if (lane == 0) counts[warp] = n_mine;
+    for (int o = 16; o > 0; o >>= 1) {
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+    }
+    if (lane == 0) {
+        sums[0][warp] = before;
+        sums[1][warp] = total;
+    }
     __syncthreads();
-    int at = 0, n_cuts = 0;
+    before = total = 0;
 #pragma unroll
     for (int v = 0; v < kMergeWarps; ++v) {
-        if (v < warp) at += counts[v];
-        n_cuts += counts[v];
+        before += sums[0][v];
+        total += sums[1][v];
     }
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const unsigned m = __ballot_sync(0xffffffffu, mine[k]);
-        if (mine[k]) list[at + __popc(m & ((1u << lane) - 1u))] = threadIdx.x + k * kMergeWarps * 32;
-        at += __popc(m);
-    }
-    __syncthreads();
-    const int HT = p.num_kv_heads * p.head_tiles;
-    const int64_t stride = static_cast<int64_t>(p.tile_heads) * (D + 2);
-    const int items = n_cuts * p.tile_heads;
+    const long long range = range_of(p, total * HT);
+    int units = b < p.batch ? max(seq_units(p, b, r, false), 0) : 0;
     int share = kMergeWarps;  // warps an item
-    while (share > 1 && items * share > static_cast<int>(gridDim.x) * kMergeWarps) share >>= 1;
-    const int per_block = kMergeWarps / share;
+    while (share > 1 && share * per_block > kMergeWarps) share >>= 1;
+    const int per_round = kMergeWarps / share;
     const int sub = warp & (share - 1);
-    for (int i0 = blockIdx.x * per_block; i0 < items; i0 += gridDim.x * per_block) {
-        const int item = i0 + warp / share;
-        bool valid = item < items;
-        int h = 0, row_h = 0, b = 0, n = 0, w = 0;
-        if (valid) {
-            w = list[item / p.tile_heads];
-            h = item % p.tile_heads;
-            const int2 cut = p.cuts[w];
-            b = cut.x / HT;
-            const int hs = cut.x - b * HT;
-            const int kvh = hs / p.head_tiles, ht = hs - kvh * p.head_tiles;
-            valid = h < p.group - ht * 16;
-            row_h = kvh * p.group + ht * 16 + h;
-            n = valid ? cut.y - w + 2 : 0;
+    griddep_wait();
+    for (int64_t it = i0; it < i1; it += per_round) {
+        const int64_t item = it + warp / share;
+        const int64_t s = item / p.tile_heads;
+        const int h = static_cast<int>(item - s * p.tile_heads);
+        const int bi = item < i1 ? static_cast<int>(s / HT) : b;
+        while (b < bi) {
+            before += units;
+            units = max(seq_units(p, ++b, r, false), 0);
         }
-        // Piece 0 is the second one of worker w - 1; piece i the first one of worker w - 1 + i.
-        auto piece = [&](int i) {
-            return p.pieces + ((static_cast<int64_t>(w - 1 + i)) * 2 + (i == 0 ? 1 : 0)) * stride +
-                   h * (D + 2);
-        };
-        float M = -INFINITY;
-        for (int i = lane; i < n; i += 32) M = fmaxf(M, piece(i)[D]);
-        M = warp_max(M);
-        if (M == -INFINITY) M = 0.f;
-        float acc[PER], den = 0.f;
+        const int hs = static_cast<int>(s - static_cast<int64_t>(b) * HT);
+        const int kvh = hs / p.head_tiles, ht = hs - kvh * p.head_tiles;
+        const long long f0 = before * HT + static_cast<long long>(hs) * units;
+        const bool valid = item < i1 && units > 0 && h < p.group - ht * 16;
+        const int w0 = valid ? static_cast<int>(f0 / range) : 0;
+        const int n = valid ? static_cast<int>((f0 + units - 1) / range) - w0 + 1 : 0;  // pieces
+        float M = -INFINITY, den = 0.f, acc[PER];
 #pragma unroll
         for (int k = 0; k < PER; ++k) acc[k] = 0.f;
-        // This warp's pieces are sub, sub + share, ...: lane l holds the weight of the l-th.
-        for (int i0p = sub; i0p < n; i0p += 32 * share) {
-            const int mine_i = i0p + lane * share;
-            float wt = 0.f;
-            if (mine_i < n) {
-                const float2 ml = *reinterpret_cast<const float2 *>(piece(mine_i) + D);
-                wt = ex2_approx(ml.x - M);
-                den += wt * ml.y;
-            }
-            const int m = min(32, (n - i0p + share - 1) / share);
-#pragma unroll 8
-            for (int k = 0; k < m; ++k) {
-                const float x = __shfl_sync(0xffffffffu, wt, k);
-                const float2 *src = reinterpret_cast<const float2 *>(piece(i0p + k * share)) + lane * (PER / 2);
+        if (n > 1) {
+            // Piece 0 is the second one of its worker, which started the segment; the others are
+            // the first ones of theirs.
+            auto piece = [&](int i) {
+                return p.pieces + (static_cast<int64_t>(w0 + i) * 2 + (i == 0 ? 1 : 0)) * p.tile_heads * (D + 2) +
+                       h * (D + 2);
+            };
+            for (int k0 = sub; k0 < n; k0 += BATCH * share) {
+                float2 v[BATCH][PER / 2], ml[BATCH];
 #pragma unroll
-                for (int c = 0; c < PER / 2; ++c) {
-                    const float2 v = src[c];
-                    acc[2 * c] += x * v.x;
-                    acc[2 * c + 1] += x * v.y;
+                for (int k = 0; k < BATCH; ++k) {
+                    const int i = k0 + k * share;
+                    ml[k] = make_float2(-INFINITY, 0.f);
+                    if (i < n) {
+                        const float2 *src = reinterpret_cast<const float2 *>(piece(i));
+                        ml[k] = src[D / 2];
+#pragma unroll
+                        for (int c = 0; c < PER / 2; ++c) v[k][c] = src[lane + 32 * c];
+                    }
                 }
+                float m_new = M;
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) m_new = fmaxf(m_new, ml[k].x);
+                const float m_use = m_new == -INFINITY ? 0.f : m_new;
+                const float f = ex2_approx(M - m_use);
+                den *= f;
+#pragma unroll
+                for (int c = 0; c < PER; ++c) acc[c] *= f;
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    if (k0 + k * share >= n) break;
+                    const float wt = ex2_approx(ml[k].x - m_use);
+                    den += wt * ml[k].y;
+#pragma unroll
+                    for (int c = 0; c < PER / 2; ++c) {
+                        acc[2 * c] += wt * v[k][c].x;
+                        acc[2 * c + 1] += wt * v[k][c].y;
+                    }
+                }
+                M = m_new;
             }
         }
-        den = warp_sum(den);
         if (share > 1) {
-            __syncthreads();  // the previous item's sums have been read
+            __syncthreads();  // the previous round's sums have been read
 #pragma unroll
-            for (int k = 0; k < PER; ++k) part[warp][lane * PER + k] = acc[k];
-            if (lane == 0) part[warp][D] = den;
+            for (int c = 0; c < PER; ++c) part[warp][32 * c + lane] = acc[c];
+            if (lane == 0) {
+                part[warp][D] = M;
+                part[warp][D + 1] = den;
+            }
             __syncthreads();
-            if (sub != 0) continue;
-            for (int v = 1; v < share; ++v) {
+            if (sub != 0 || n <= 1) continue;
+            float m_all = M;
+            for (int v = 1; v < share; ++v) m_all = fmaxf(m_all, part[warp + v][D]);
+            const float m_use = m_all == -INFINITY ? 0.f : m_all;
+            const float f0w = ex2_approx(M - m_use);
+            den *= f0w;
 #pragma unroll
-                for (int k = 0; k < PER; ++k) acc[k] += part[warp + v][lane * PER + k];
-                den += part[warp + v][D];
+            for (int c = 0; c < PER; ++c) acc[c] *= f0w;
+            for (int v = 1; v < share; ++v) {
+                const float f = ex2_approx(part[warp + v][D] - m_use);
+                den += f * part[warp + v][D + 1];
+#pragma unroll
+                for (int c = 0; c < PER; ++c) acc[c] += f * part[warp + v][32 * c + lane];
             }
         }
-        if (!valid) continue;
+        if (n <= 1) continue;
         const float inv = p.kv_scale / den;
         const int64_t row = p.q_rows != nullptr ? p.q_rows[b] : b;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + (row * p.num_heads + row_h) * D + lane * PER);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(p.out + (row * p.num_heads + kvh * p.group + ht * 16 + h) * D);
 #pragma unroll
-        for (int c = 0; c < PER / 2; ++c) dst[c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+        for (int c = 0; c < PER / 2; ++c) dst[lane + 32 * c] = pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
     }
 }
 
@@ -894,7 +910,7 @@ bool plan_decode_fp4(int batch, int num_heads, int num_kv_heads, int head_dim, i
     p.whole = units <= kWholeUnits;
     const int64_t want = p.whole ? segments : (segments * units + kMinUnits - 1) / kMinUnits;
     int64_t blocks = (want + kWarps - 1) / kWarps;
-    const int64_t resident = static_cast<int64_t>(kPlanSms) * (p.group > 8 ? 3 : kCtasPerSm);
+    const int64_t resident = static_cast<int64_t>(kPlanSms) * (p.group > 8 ? kCtas2 : kCtas1);
     if (!p.whole && blocks > resident) blocks = resident;
     if (blocks < 1) blocks = 1;
     if (blocks > 0x7fffffffLL / kWarps) return false;
@@ -902,8 +918,7 @@ bool plan_decode_fp4(int batch, int num_heads, int num_kv_heads, int head_dim, i
     p.blocks = static_cast<int>(blocks);
     p.workers = p.blocks * kWarps;
     if (!p.whole) {
-        p.pieces_bytes = (static_cast<size_t>(p.workers) * 2 * p.tile_heads * (head_dim + 2) * sizeof(float) + 255) / 256 * 256;
-        p.workspace_bytes = p.pieces_bytes + static_cast<size_t>(p.workers) * sizeof(int2);
+        p.workspace_bytes = static_cast<size_t>(p.workers) * 2 * p.tile_heads * (head_dim + 2) * sizeof(float);
     }
     *plan = p;
     return true;
@@ -938,7 +953,6 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, const DecodeFp4Plan &plan, cu
     p.tile_heads = plan.tile_heads;
     if (!plan.whole) {
         p.pieces = static_cast<float *>(a.workspace);
-        p.cuts = reinterpret_cast<int2 *>(static_cast<uint8_t *>(a.workspace) + plan.pieces_bytes);
     }
     p.key = static_cast<const __nv_bfloat16 *>(a.key);
     p.value = static_cast<const __nv_bfloat16 *>(a.value);

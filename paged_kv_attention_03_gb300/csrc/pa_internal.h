@@ -161,7 +161,6 @@ struct DecodeFp4Plan {
     bool whole;
     int blocks;
     int workers;
-    size_t pieces_bytes;
     size_t workspace_bytes;
 };
 bool plan_decode_fp4(int batch, int num_heads, int num_kv_heads, int head_dim, int max_seq_len,
