@@ -502,40 +502,43 @@ __device__ __forceinline__ void convert_tile_e4m3(uint32_t stage, int lane) {
 }
 
 // One 128-key tile of 4-bit rows (fp4.cuh), landed as [128][9 HD / 16 bytes] at the end of a
-// stage, expanded in place like convert_tile_e4m3.  A row's f16 lines cover codes of other
-// rows: those of the first 32 (i + 1) rows are written only after all lanes have read
-// rows 32 i .. 32 i + 31, and reach no further than those rows (HD 128: line r ends at byte
-// 16384 + 128 r + 127 of the stage, row q starts at 23552 + 72 q; HD 64: 128 r + 127 and
-// 11776 + 36 q).  Row pitches of 72 and 36 bytes put the lanes' reads on different banks.
+// stage, expanded in place like convert_tile_e4m3, a 64-dim half of 32 rows at a time.  The f16
+// lines of the last half cover codes of other rows: those of rows 32 i .. 32 i + 31 are written
+// only after all lanes have read that half's codes, and reach no further than those rows
+// (HD 128: line r ends at byte 16384 + 128 r + 127 of the stage, row q starts at 23552 + 72 q;
+// HD 64: 128 r + 127 and 11776 + 36 q).  Row pitches of 72 and 36 bytes put the lanes' reads on
+// different banks.  The loops stay rolled: the softmax warps need the instruction cache.
 template <int HD>
 __device__ __forceinline__ void convert_tile_fp4(uint32_t stage, int lane) {
     constexpr int RB = fp4::row_bytes(HD);
     constexpr uint32_t kRows = (HD / 64) * HALF - 128u * RB;
-    constexpr int W = HD / 64;  // words a read
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t r = static_cast<uint32_t>(lane + 32 * i);
-        uint32_t c[9 * W];  // codes, then scales
+    for (int ih = 0; ih < 4 * (HD / 64); ++ih) {
+        const uint32_t half = ih & (HD / 64 - 1);
+        const uint32_t r = static_cast<uint32_t>(lane + 32 * (ih / (HD / 64)));
+        const uint32_t row = stage + kRows + r * RB;
+        uint32_t c[8], s;
 #pragma unroll
-        for (int j = 0; j < 9; ++j) {
-            const uint32_t a = stage + kRows + r * RB + 4 * W * j;
-            if constexpr (W == 2)
-                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(c[2 * j]), "=r"(c[2 * j + 1]) : "r"(a) : "memory");
-            else
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(c[j]) : "r"(a) : "memory");
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (HD == 128) {
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(c[2 * j]), "=r"(c[2 * j + 1]) : "r"(row + 32 * half + 8 * j) : "memory");
+            } else {
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(c[2 * j]) : "r"(row + 8 * j) : "memory");
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(c[2 * j + 1]) : "r"(row + 8 * j + 4) : "memory");
+            }
         }
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(s) : "r"(row + HD / 2 + 4 * half) : "memory");
         __syncwarp();
+        const uint32_t line = stage + half * HALF + r * 128u;
 #pragma unroll
-        for (int j = 0; j < HD / 16; ++j) {
-            // group j: scale byte j, 64-dim half j / 4, chunks 2 (j % 4) and + 1 of row r
-            const uint32_t sc = fp4::e4m3x2_to_f16x2(c[8 * W + (j >> 2)] >> (16 * ((j >> 1) & 1)));
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t sc = fp4::e4m3x2_to_f16x2(s >> (16 * (j >> 1)));
             const uint32_t s2 = __byte_perm(sc, 0u, (j & 1) ? 0x3232 : 0x1010);
-            const uint32_t line = stage + (j >> 2) * HALF + r * 128u;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t f[4];
                 fp4::e2m1x8_to_f16x2x4(c[2 * j + h], f);
-                st_shared_v4(line + (((2u * (j & 3) + h) ^ (r & 7u)) << 4), fp4::mul_f16x2(f[0], s2),
+                st_shared_v4(line + (((2u * j + h) ^ (r & 7u)) << 4), fp4::mul_f16x2(f[0], s2),
                              fp4::mul_f16x2(f[1], s2), fp4::mul_f16x2(f[2], s2), fp4::mul_f16x2(f[3], s2));
             }
         }
