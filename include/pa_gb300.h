@@ -454,7 +454,11 @@ pa_status pa_release_blocks(int32_t *free_blocks, int32_t *num_free_out, int32_t
  *     code * scale is an f16, q is rounded to f16 once (exactly for |q| in [2^-14, 65504],
  *     clamped beyond) and so are the softmax weights; sums are fp32.
  * pa_varlen_prefill_fp4: as pa_varlen_prefill; single-row sequences run on the decode kernel
- *     when seq_lens is given, in the workspace.
+ *     when seq_lens is given, in the workspace.  The advertised workspace also has room for
+ *     the keys of num_seqs sequences of max_seqlen_k keys in 16 bits (up to 4 GiB each for K
+ *     and V; none beyond): with it, long queries expand their sequences' keys once instead of
+ *     in every query block.  pa_decode_fp4_workspace_size(num_seqs, ...) bytes are enough to
+ *     run without.
  *
  *   workspace  at least pa_decode_fp4_workspace_size(...) /
  *              pa_varlen_prefill_fp4_workspace_size(...) bytes, 256-byte aligned (may be NULL

@@ -520,7 +520,7 @@ def pa_varlen_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
                 raise ValueError(f"pa_varlen_prefill_fp4: {n} must have {rows} entries")
     _new_tokens(key, value, slot_mapping, total_q, hkv, head_dim, dev, "pa_varlen_prefill_fp4")
     out = _out(out, q.shape, torch.bfloat16, dev)
-    need = 0 if seq_lens is None else pa_varlen_prefill_fp4_workspace_size(
+    need = pa_varlen_prefill_fp4_workspace_size(
         num_seqs, num_heads, hkv, head_dim, max_seqlen_k, sliding_window)
     ws, ws_bytes, workspace = _workspace(workspace, need, dev)
     with _on(dev):

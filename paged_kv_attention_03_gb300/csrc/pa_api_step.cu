@@ -10,6 +10,7 @@
 namespace {
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
 int log2_of(int x) {
@@ -234,7 +235,11 @@ pa_status pa_decode_fp4(void *out, const void *q, const void *key, const void *v
 
 size_t pa_varlen_prefill_fp4_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
                                             int head_dim, int max_seqlen_k, int sliding_window) {
-    return pa_decode_fp4_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen_k, sliding_window);
+    pa::DecodeFp4Plan plan;
+    if (!pa::plan_decode_fp4(num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen_k, sliding_window, &plan))
+        return 0;
+    return up256(plan.workspace_bytes) +
+           2 * pa::prefill_fp4_scratch_bytes(num_seqs, num_kv_heads, head_dim, max_seqlen_k);
 }
 
 pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const void *value,
@@ -273,14 +278,16 @@ pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
         return PA_ERR_INVALID_ARG;
     if (max_seqlen_k > 0 && max_num_blocks == 0) return PA_ERR_INVALID_ARG;
-    if (seq_lens) {  // its single-row sequences run on the decode kernel
-        pa::DecodeFp4Plan plan;
-        if (!pa::plan_decode_fp4(num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen_k, sliding_window, &plan))
-            return PA_ERR_INVALID_ARG;
-        if (plan.workspace_bytes > 0 &&
-            (!workspace || workspace_bytes < plan.workspace_bytes || !aligned(workspace, 256)))
-            return PA_ERR_INVALID_ARG;
-    }
+    // The workspace: what the decode kernel needs for the single-row sequences (with seq_lens),
+    // then the scratch cache, if it is large enough for that too.
+    pa::DecodeFp4Plan plan;
+    if (!pa::plan_decode_fp4(num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen_k, sliding_window, &plan))
+        return PA_ERR_INVALID_ARG;
+    if (seq_lens && plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes))
+        return PA_ERR_INVALID_ARG;
+    if (workspace && !aligned(workspace, 256)) return PA_ERR_INVALID_ARG;
+    const size_t scratch = 2 * pa::prefill_fp4_scratch_bytes(num_seqs, num_kv_heads, head_dim, max_seqlen_k);
+    const bool has_scratch = workspace && scratch > 0 && workspace_bytes >= up256(plan.workspace_bytes) + scratch;
     if (has_new) {
         st = store();
         if (st != PA_OK) return st;
@@ -309,6 +316,7 @@ pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const
     a.cache = pa::kCacheFp4;
     a.kv_scale = kv_scale;
     a.workspace = workspace;
+    a.scratch = has_scratch ? static_cast<uint8_t *>(workspace) + up256(plan.workspace_bytes) : nullptr;
     a.err = pa::device_error_word();
     return pa::cuda_status(pa::launch_prefill(a, s));
 }

@@ -169,7 +169,8 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, const DecodeFp4Plan &plan, cu
 
 // ---------------------------------------------------------------- prefill ---
 // What the cache holds: bf16, E4M3 codes, or 4-bit rows (fp4.cuh).
-enum : int { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheFp4 = 2 };
+// (kCacheExpanded: 4-bit rows that the call itself expanded to 16 bits.)
+enum : int { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheFp4 = 2, kCacheExpanded = 3 };
 struct PrefillArgs {
     void *out;
     const void *q;
@@ -195,10 +196,13 @@ struct PrefillArgs {
     // rows of fp4.cuh.
     int cache;  // kCacheBf16 ..
     float kv_scale;
-    // 4-bit cache: scratch of the decode rows (decode_fp4 plan of the batch).
+    // 4-bit cache: workspace of the decode rows (decode_fp4 plan of the batch), and the scratch
+    // cache (two halves of prefill_fp4_scratch_bytes) or null.
     void *workspace;
+    void *scratch;
     unsigned *err;
 };
+size_t prefill_fp4_scratch_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_seqlen_k);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);
 // Testing aid behind pa_debug_prefill_stall (process-wide; read at each prefill launch).
 void debug_prefill_stall(int stall, uint64_t wait_ns);

@@ -120,6 +120,7 @@ struct PrefillKernelParams {
     float kv_scale;    // E4M3 / 4-bit cache: elements are times kv_scale (folded into scale_log2 for K)
     const uint8_t *k4;  // 4-bit cache rows (fp4.cuh): K and V
     const uint8_t *v4;
+    int expanded_blocks;  // expanded 4-bit cache: blocks of a sequence in the scratch cache
     uint64_t wait_ns;  // limit of every wait (kTimeoutNs unless a test lowers it)
     int stall;         // testing aid: publish no work item, so every wait runs out
     unsigned *err;
@@ -550,11 +551,15 @@ __device__ __forceinline__ void convert_tile_fp4(uint32_t stage, int lane) {
 // MMA operand layout (every E4M3 value is an f16); the softmax warps convert each query tile
 // to f16 in place; the products are f16 MMAs with P in f16.
 // CACHE kCacheFp4: likewise with 4-bit rows, each 16-key piece of a page one bulk copy.
+// CACHE kCacheExpanded: the sequences' 4-bit rows were expanded into a scratch cache, K as bf16
+// (as the queries are) and V as f16 (as the weights are); the producers are the bf16 ones, and
+// sequence i has the scratch blocks i * expanded_blocks ...
 template <int HD, bool PREFIX, int CACHE>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillKernelParams p) {
     constexpr bool FP4 = CACHE == kCacheFp4;
-    constexpr bool CODES = CACHE != kCacheBf16;  // codes in the cache, f16 products
+    constexpr bool CODES = CACHE == kCacheE4m3 || FP4;  // codes in the cache, S in f16
+    constexpr bool PV16 = CACHE != kCacheBf16;          // P and V in f16
     static_assert(CACHE != kCacheE4m3 || HD == 128, "the E4M3 cache path is built for head_dim 128");
     static_assert(!CODES || !PREFIX, "the shared-prefix mode is built for bf16 caches");
     using L = Layout<HD>;
@@ -630,6 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // out-of-range row (zero fill) past the sequence or for an invalid block index.
     auto kv_row = [&](const Item &it, int k0) -> int {
         if (k0 >= it.sk) return -16;
+        if constexpr (CACHE == kCacheExpanded) return ((it.seq * p.expanded_blocks) << p.log2_bs) + k0;
         const int blk = __ldg(p.block_table + static_cast<int64_t>(it.seq) * p.max_num_blocks +
                               (k0 >> p.log2_bs));
         if (blk < 0 || blk >= p.num_blocks) {
@@ -843,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // 64 keys, P V over 64 keys.  The softmax needs no change: the causal mask
                 // already sets columns 64..127 to -inf.
                 constexpr uint32_t idesc_s_half = idesc_bf16_f32(BM, BN / 2, false, CODES);
-                constexpr uint32_t idesc_o = idesc_bf16_f32(BM, HD, true, CODES);
+                constexpr uint32_t idesc_o = idesc_bf16_f32(BM, HD, true, PV16);
                 uint32_t g = 0;                  // global KV tile counter
                 uint32_t cnt[2] = {0, 0};        // tiles issued per query tile (S / P V)
                 uint32_t ic = 0;                 // items
@@ -1092,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                   sl2x2, negm2);
                         float x0, x1;
                         f2_unpack(x, x0, x1);
-                        if constexpr (CODES) {
+                        if constexpr (PV16) {
                             pk[i] = pack_f16x2(ex2_approx(x0), ex2_approx(x1));
                             add_f16x2_f32(acc[2 * (i & 1)], acc[2 * (i & 1) + 1], pk[i]);
                         } else {
@@ -1135,8 +1141,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
-            // (Codes: V elements are times kv_scale.)
-            const float inv = l_sum > 0.f ? (CODES ? p.kv_scale : 1.f) / l_sum : 0.f;
+            // (E4M3 / 4-bit: V elements are times kv_scale.)
+            const float inv = l_sum > 0.f ? (PV16 ? p.kv_scale : 1.f) / l_sum : 0.f;
             if constexpr (PREFIX) {
                 // Partial state of this key split: fp32 row and ln of its denominator.
                 const int64_t rows = static_cast<int64_t>(p.num_req) * p.num_heads;
@@ -1262,6 +1268,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// --------------------------------------------------- expansion of a 4-bit cache ---
+// The keys that the prefill of a sequence reads (from the 128-key tile of the first visible one)
+// as 16-bit rows [slots, Hkv, HD] of a scratch cache: K bf16, V f16, code * scale in both, which
+// is exact.  A thread takes 16 dims of one key, for every kv head in turn: the lanes of a key
+// write a row, the table is read once, and the loads of four heads are in flight together.
+constexpr int kExpandThreads = 256;
+template <int HD>
+constexpr int expand_keys() {  // keys of a block
+    return kExpandThreads / (HD / 16);
+}
+// Query-tile pairs of the longest sequence from which the keys are expanded beforehand: every pair
+// expands each tile again otherwise.
+constexpr int kExpandItems = 3;
+
+template <int HD>
+__global__ void __launch_bounds__(kExpandThreads)
+    expand_fp4_kernel(const PrefillKernelParams p, uint4 *__restrict__ k_out, uint4 *__restrict__ v_out) {
+    constexpr int GROUPS = HD / 16;
+    constexpr int RB = fp4::row_bytes(HD);
+    const int seq = blockIdx.y;
+    const int q_start = p.cu_q[seq], sq = p.cu_q[seq + 1] - q_start;
+    int sk = p.seq_lens != nullptr ? p.seq_lens[seq] : p.cu_k[seq + 1] - p.cu_k[seq];
+    // (Lengths are clamped as get_item does, which reports what is wrong with them.)
+    sk = sk < 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(sk), p.seq_cap));
+    if (sq <= 0 || sq > sk || (p.skip_decode_rows && sq == 1)) return;
+    const int first = p.window > 0 ? max(0, sk - sq - p.window + 1) / BN * BN : 0;
+    const int g = threadIdx.x % GROUPS;
+    const int key = blockIdx.x * expand_keys<HD>() + threadIdx.x / GROUPS;
+    if (key >= sk || key < first) return;
+    const int blk = __ldg(p.block_table + static_cast<int64_t>(seq) * p.max_num_blocks + (key >> p.log2_bs));
+    const bool good = blk >= 0 && blk < p.num_blocks;
+    if (!good && g == 0) flag_error(p.err, kErrBlockRange);
+    const int64_t row = ((static_cast<int64_t>(good ? blk : 0) * p.num_kv_heads) << p.log2_bs) +
+                        (key & ((1 << p.log2_bs) - 1));
+    const int64_t step = static_cast<int64_t>(RB) << p.log2_bs;  // to the next head
+    const uint8_t *src[2] = {p.k4 + row * RB, p.v4 + row * RB};
+    const int64_t dst = (((static_cast<int64_t>(seq) * p.expanded_blocks) << p.log2_bs) + key) * p.num_kv_heads * GROUPS + g;
+#pragma unroll 4
+    for (int h = 0; h < p.num_kv_heads; ++h) {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            uint32_t c[2] = {0u, 0u}, s = 0u;  // zeros for a bad block
+            if (good) {
+                const uint8_t *at = src[kv] + h * step;
+                if constexpr (HD == 128) {
+                    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(at) + g);
+                    c[0] = x.x;
+                    c[1] = x.y;
+                } else {  // 36-byte rows: 4-byte aligned
+                    c[0] = __ldg(reinterpret_cast<const uint32_t *>(at) + 2 * g);
+                    c[1] = __ldg(reinterpret_cast<const uint32_t *>(at) + 2 * g + 1);
+                }
+                s = __ldg(at + HD / 2 + g);
+            }
+            const uint32_t s2 = __byte_perm(fp4::e4m3x2_to_f16x2(s), 0u, 0x1010);
+            uint32_t w[8];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uint32_t f[4];
+                fp4::e2m1x8_to_f16x2x4(c[x], f);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t v = fp4::mul_f16x2(f[k], s2);
+                    w[4 * x + k] = kv ? v : pack_bf16x2(fp4::f16_lo(v), fp4::f16_hi(v));
+                }
+            }
+            uint4 *out = (kv ? v_out : k_out) + 2 * (dst + h * GROUPS);
+            out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    }
+}
+
 // ------------------------------------------------------------------ host side ---
 
 // Testing aid (pa_debug_prefill_stall): later launches publish no item / use this limit.
@@ -1353,6 +1432,36 @@ void debug_prefill_stall(int stall, uint64_t wait_ns) {
     g_debug_stall.store(stall != 0 ? 1 : 0, std::memory_order_relaxed);
 }
 
+// Bytes of one half (K or V) of the scratch cache of a 4-bit prefill: whole blocks for the longest
+// sequence, for each sequence.  0: not worth a scratch this large.
+size_t prefill_fp4_scratch_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_seqlen_k) {
+    constexpr int64_t kMost = 1ll << 32;  // of each half
+    const int64_t keys = (static_cast<int64_t>(max_seqlen_k) + 255) / 256 * 256;  // whole blocks of any size
+    const int64_t bytes = keys * num_kv_heads * head_dim * 2;
+    return num_seqs > 0 && bytes > 0 && bytes <= kMost / num_seqs ? static_cast<size_t>(bytes * num_seqs) : 0;
+}
+
+namespace {
+
+// The 4-bit prefill with its keys expanded beforehand, where a.workspace holds the scratch cache.
+template <int HD>
+cudaError_t launch_expanded(PrefillKernelParams &kp, const PrefillArgs &a, cudaStream_t stream) {
+    const size_t half = prefill_fp4_scratch_bytes(a.num_seqs, a.num_kv_heads, HD, a.max_seqlen_k);
+    uint8_t *k16 = static_cast<uint8_t *>(a.scratch), *v16 = k16 + half;
+    kp.expanded_blocks = (a.max_seqlen_k + a.block_size - 1) / a.block_size;
+    const dim3 grid((a.max_seqlen_k + expand_keys<HD>() - 1) / expand_keys<HD>(), a.num_seqs);
+    expand_fp4_kernel<HD><<<grid, kExpandThreads, 0, stream>>>(kp, reinterpret_cast<uint4 *>(k16), reinterpret_cast<uint4 *>(v16));
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    PrefillArgs x = a;
+    x.k_cache = k16;
+    x.v_cache = v16;
+    x.num_blocks = static_cast<int64_t>(a.num_seqs) * kp.expanded_blocks;
+    return launch_prefill_d<HD, false, kCacheExpanded>(kp, x, stream);
+}
+
+}  // namespace
+
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
     if (a.num_seqs == 0 || a.total_q == 0 || a.max_seqlen_q == 0) return cudaSuccess;
     const int64_t slots = a.num_blocks * a.block_size;
@@ -1401,6 +1510,12 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
         if (a.cache == kCacheE4m3) {
             if (a.head_dim != 128) return cudaErrorInvalidValue;
             e = launch_prefill_d<128, false, kCacheE4m3>(kp, a, stream);
+        } else if (a.cache == kCacheFp4 && a.scratch != nullptr && kp.q_items >= kExpandItems) {
+            switch (a.head_dim) {
+                case 64: e = launch_expanded<64>(kp, a, stream); break;
+                case 128: e = launch_expanded<128>(kp, a, stream); break;
+                default: return cudaErrorInvalidValue;
+            }
         } else if (a.cache == kCacheFp4) {
             switch (a.head_dim) {
                 case 64: e = launch_prefill_d<64, false, kCacheFp4>(kp, a, stream); break;

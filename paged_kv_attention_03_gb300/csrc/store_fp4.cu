@@ -23,6 +23,24 @@ __device__ __forceinline__ int64_t cache_row(int64_t slot, int head, int kv_head
     return (((slot >> log2_bs) * kv_heads + head) << log2_bs) + (slot & ((1 << log2_bs) - 1));
 }
 
+// The place of group i: token, head, group of 16 dims (32-bit divisions where they do).
+struct Place {
+    int64_t token;
+    int head;
+    int group;
+};
+template <int GROUPS>
+__device__ __forceinline__ Place place_of(int64_t i, int64_t total, int kv_heads) {
+    if (total <= 0xffffffffll) {
+        const unsigned th = static_cast<unsigned>(i) / GROUPS;
+        const unsigned t = th / static_cast<unsigned>(kv_heads);
+        return {t, static_cast<int>(th - t * kv_heads), static_cast<int>(i % GROUPS)};
+    }
+    const int64_t th = i / GROUPS;
+    const int64_t t = th / kv_heads;
+    return {t, static_cast<int>(th - t * kv_heads), static_cast<int>(i % GROUPS)};
+}
+
 __device__ __forceinline__ void load_words(const uint4 *src, uint32_t (&w)[8]) {
     const uint4 a = __ldcs(src), b = __ldcs(src + 1);
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
@@ -64,33 +82,29 @@ store_kvcache_fp4_kernel(const uint4 *__restrict__ key, const uint4 *__restrict_
                          float kv_scale6, unsigned *err) {
     constexpr int GROUPS = D / 16;
     constexpr int RB = fp4::row_bytes(D);
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
     const int lane = threadIdx.x & 31;
     // The lanes of one row: they take every branch together.
     const unsigned mask = ((1u << GROUPS) - 1u) << (lane & ~(GROUPS - 1));
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += stride) {
-        const int64_t th = i / GROUPS;  // (token, head)
-        const int g = static_cast<int>(i % GROUPS);
-        const int64_t t = th / kv_heads;
-        const int h = static_cast<int>(th - t * kv_heads);
-        const int64_t slot = __ldg(slot_mapping + t);
-        if (slot < 0) continue;  // padding token
-        if (slot >= num_slots) {
-            if (g == 0 && h == 0) flag_error(err, kErrSlotRange);
-            continue;
-        }
-        uint32_t kw[8], vw[8];
-        load_words(key + 2 * i, kw);
-        load_words(value + 2 * i, vw);
-        uint32_t ks, vs;
-        const uint2 kc = fp4::quant_group(kw, kv_scale, kv_scale6, ks);
-        const uint2 vc = fp4::quant_group(vw, kv_scale, kv_scale6, vs);
-        const uint2 kss = row_scales<GROUPS>(ks, g, mask), vss = row_scales<GROUPS>(vs, g, mask);
-        const int64_t row = cache_row(slot, h, kv_heads, log2_bs);
-        write_row<D>(k_cache + row * RB, g, kc, kss);
-        write_row<D>(v_cache + row * RB, g, vc, vss);
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= total) return;
+    const Place at = place_of<GROUPS>(i, total, kv_heads);
+    const int g = at.group, h = at.head;
+    const int64_t slot = __ldg(slot_mapping + at.token);
+    if (slot < 0) return;  // padding token
+    if (slot >= num_slots) {
+        if (g == 0 && h == 0) flag_error(err, kErrSlotRange);
+        return;
     }
+    uint32_t kw[8], vw[8];
+    load_words(key + 2 * i, kw);
+    load_words(value + 2 * i, vw);
+    uint32_t ks, vs;
+    const uint2 kc = fp4::quant_group(kw, kv_scale, kv_scale6, ks);
+    const uint2 vc = fp4::quant_group(vw, kv_scale, kv_scale6, vs);
+    const uint2 kss = row_scales<GROUPS>(ks, g, mask), vss = row_scales<GROUPS>(vs, g, mask);
+    const int64_t row = cache_row(slot, h, kv_heads, log2_bs);
+    write_row<D>(k_cache + row * RB, g, kc, kss);
+    write_row<D>(v_cache + row * RB, g, vc, vss);
 }
 
 namespace {
@@ -134,34 +148,31 @@ gather_kvcache_fp4_kernel(uint4 *__restrict__ key, uint4 *__restrict__ value,
                           unsigned *err) {
     constexpr int GROUPS = D / 16;
     constexpr int RB = fp4::row_bytes(D);
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += stride) {
-        const int64_t th = i / GROUPS;
-        const int g = static_cast<int>(i % GROUPS);
-        const int64_t t = th / kv_heads;
-        const int h = static_cast<int>(th - t * kv_heads);
-        const int64_t slot = __ldg(slot_mapping + t);
-        if (slot < 0 || slot >= num_slots) {
-            if (slot >= 0 && g == 0 && h == 0) flag_error(err, kErrSlotRange);
-            const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-            key[2 * i] = z;
-            key[2 * i + 1] = z;
-            value[2 * i] = z;
-            value[2 * i + 1] = z;
-            continue;
-        }
-        const int64_t row = cache_row(slot, h, kv_heads, log2_bs);
-        expand_group<D>(k_cache + row * RB, g, kv_scale, key + 2 * i);
-        expand_group<D>(v_cache + row * RB, g, kv_scale, value + 2 * i);
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= total) return;
+    const Place at = place_of<GROUPS>(i, total, kv_heads);
+    const int g = at.group, h = at.head;
+    const int64_t slot = __ldg(slot_mapping + at.token);
+    if (slot < 0 || slot >= num_slots) {
+        if (slot >= 0 && g == 0 && h == 0) flag_error(err, kErrSlotRange);
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        key[2 * i] = z;
+        key[2 * i + 1] = z;
+        value[2 * i] = z;
+        value[2 * i + 1] = z;
+        return;
     }
+    const int64_t row = cache_row(slot, h, kv_heads, log2_bs);
+    expand_group<D>(k_cache + row * RB, g, kv_scale, key + 2 * i);
+    expand_group<D>(v_cache + row * RB, g, kv_scale, value + 2 * i);
 }
 
 namespace {
 
+constexpr int64_t kMostGroups = 0x7fffffffll * 256;  // one block for 256 groups
+
 unsigned fp4_blocks(int64_t total) {
-    const int64_t blocks = (total + 255) / 256;
-    return static_cast<unsigned>(blocks < 152LL * 64 ? blocks : 152LL * 64);
+    return static_cast<unsigned>((total + 255) / 256);  // (checked against the grid's limit)
 }
 
 template <int D>
@@ -190,6 +201,7 @@ cudaError_t launch_gather_d(const GatherArgs &a, cudaStream_t stream) {
 cudaError_t launch_store_kvcache_fp4(const StoreArgs &a, int kv_heads, int head_dim, int log2_bs,
                                      float kv_scale, cudaStream_t stream) {
     if (a.num_tokens == 0) return cudaSuccess;
+    if (a.num_tokens > kMostGroups / (static_cast<int64_t>(kv_heads) * (head_dim / 16))) return cudaErrorInvalidValue;
     switch (head_dim) {
         case 64: return launch_store_d<64>(a, kv_heads, log2_bs, kv_scale, stream);
         case 128: return launch_store_d<128>(a, kv_heads, log2_bs, kv_scale, stream);
@@ -199,6 +211,7 @@ cudaError_t launch_store_kvcache_fp4(const StoreArgs &a, int kv_heads, int head_
 
 cudaError_t launch_gather_kvcache_fp4(const GatherArgs &a, cudaStream_t stream) {
     if (a.num_tokens == 0) return cudaSuccess;
+    if (a.num_tokens > kMostGroups / (static_cast<int64_t>(a.num_kv_heads) * (a.head_dim / 16))) return cudaErrorInvalidValue;
     switch (a.head_dim) {
         case 64: return launch_gather_d<64>(a, stream);
         case 128: return launch_gather_d<128>(a, stream);

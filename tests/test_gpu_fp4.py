@@ -80,9 +80,15 @@ class Case:
         return pa.pa_decode_fp4(kw.pop("q"), kw.pop("k_cache"), kw.pop("v_cache"), kw.pop("block_table"),
                                 kw.pop("seq_lens"), max(int(self.lens.max()), 0), self.scale, self.kv_scale, window, **kw)
 
-    def prefill(self, window=0, lens=True, cu_k=False, **kw):
+    def prefill(self, window=0, lens=True, cu_k=False, expand=True, **kw):
+        """expand False: a workspace without room for the expanded keys, so that every query block
+        expands its tiles itself."""
         x = dict(kw) if "q" in kw else {**self.device(), **kw}
         sl = x.pop("seq_lens")
+        if not expand:
+            need = pa.pa_decode_fp4_workspace_size(len(self.lens), self.heads, self.kc.shape[1], self.dim, int(self.lens.max()),
+                                                   window)
+            x["workspace"] = torch.empty(max(need, 256), dtype=torch.uint8, device=self.dev)
         if cu_k:
             x["cu_seqlens_k"] = _t(np.concatenate([[0], np.cumsum(self.lens)]), self.dev)
         return pa.pa_varlen_prefill_fp4(x.pop("q"), x.pop("k_cache"), x.pop("v_cache"), _t(self.cu, self.dev),
@@ -320,61 +326,84 @@ def test_decode_ignores_what_its_workspace_holds(cuda):
 
 
 # ----------------------------------------------------------------- prefill ---
+both = pytest.mark.parametrize("expand", [True, False])
+
+
+@both
 @pytest.mark.parametrize("dim", [128, 64])
 @pytest.mark.parametrize("heads,kv_heads", HEADS)
-def test_prefill_head_layouts(cuda, heads, kv_heads, dim):
-    c = Case(cuda, [0, 15, 100], [40, 130, 2], heads, kv_heads, dim, seed=heads)
-    c.check(c.prefill())
+def test_prefill_head_layouts(cuda, heads, kv_heads, dim, expand):
+    c = Case(cuda, [0, 15, 100], [40, 430, 2], heads, kv_heads, dim, seed=heads)
+    c.check(c.prefill(expand=expand))
 
 
+@both
 @pytest.mark.parametrize("window", [0, 1, 60, 128, 400])
 @pytest.mark.parametrize("bs", [16, 64, 256])
-def test_prefill_chunks_and_windows(cuda, window, bs):
+def test_prefill_chunks_and_windows(cuda, window, bs, expand):
     c = Case(cuda, [0, 0, 37, 130, 500, 3], [1, 160, 64, 129, 31, 1], 8, 2, 128, bs=bs, seed=20)
-    c.check(c.prefill(window), window)
+    c.check(c.prefill(window, expand=expand), window)
 
 
+@both
 @pytest.mark.parametrize("dim", [128, 64])
 @pytest.mark.parametrize("n", [2, 16, 63, 64, 65, 127, 128, 129, 255, 257, 700])
-def test_prefill_tile_edges(cuda, n, dim):
+def test_prefill_tile_edges(cuda, n, dim, expand):
     c = Case(cuda, [0, 5], [n, n // 2 + 1], 8, 2, dim, seed=n)
-    c.check(c.prefill())
+    c.check(c.prefill(expand=expand))
 
 
-def test_prefill_without_seq_lens(cuda):
-    c = Case(cuda, [0, 20, 9], [33, 1, 60], 8, 2, 128, seed=21)
-    c.check(c.prefill(lens=False, cu_k=True))
-    c.check(c.prefill(cu_k=True))
+@both
+@pytest.mark.parametrize("n", [33, 200])
+def test_prefill_without_seq_lens(cuda, n, expand):
+    c = Case(cuda, [0, 20, 9], [n, 1, 60], 8, 2, 128, seed=21)
+    c.check(c.prefill(lens=False, cu_k=True, expand=expand))
+    c.check(c.prefill(cu_k=True, expand=expand))
 
 
+@both
 @pytest.mark.parametrize("new", [[1] * 5, [300, 1, 1, 200, 1], [0, 1, 0, 17, 0]])
 @pytest.mark.parametrize("dim", [128, 64])
-def test_prefill_mixed_batches_store_their_tokens(cuda, new, dim):
+def test_prefill_mixed_batches_store_their_tokens(cuda, new, dim, expand):
     c = Case(cuda, [1000, 0, 37, 90, 600], new, 32, 8, dim, seed=22)
     x = c.device()
-    out = c.prefill(**x, **c.new_tokens())
+    out = c.prefill(expand=expand, **x, **c.new_tokens())
     c.store()
     np.testing.assert_array_equal(x["k_cache"].cpu().numpy(), c.kc)
     np.testing.assert_array_equal(x["v_cache"].cpu().numpy(), c.vc)
     c.check(out)
 
 
-def test_prefill_ignores_rows_behind_the_last_key(cuda):
-    c = Case(cuda, [0, 7], [37, 130], 8, 2, 128, seed=23)
+@both
+@pytest.mark.parametrize("dim", [128, 64])
+def test_prefill_ignores_rows_behind_the_last_key(cuda, dim, expand):
+    c = Case(cuda, [0, 7], [37, 235], 8, 2, dim, seed=23)
     dirty = [torch.from_numpy(x.copy()).to(cuda) for x in (c.kc, c.vc)]
     for d in dirty:
         for i, n in enumerate(c.lens):
             if n % 16:
                 d[int(c.table[i, n // 16]), :, int(n % 16):] = 0xff  # NaN scales
-    c.check(c.prefill(k_cache=dirty[0], v_cache=dirty[1]))
+    c.check(c.prefill(k_cache=dirty[0], v_cache=dirty[1], expand=expand))
 
 
-def test_prefill_flags_bad_blocks(cuda):
+def test_prefill_ignores_what_its_workspace_holds(cuda):
+    # The scratch cache starts as NaN: keys before a window's first tile and behind the last key
+    # stay that.
+    c = Case(cuda, [700, 7, 30], [300, 130, 1], 8, 2, 128, seed=26)
+    for window in (0, 100):
+        need = pa.pa_varlen_prefill_fp4_workspace_size(3, 8, 2, 128, 1000, window)
+        ws = torch.full((need + 64,), 0xff, dtype=torch.uint8, device=cuda)
+        c.check(c.prefill(window, workspace=ws[:need]), window)
+        assert (ws[need:] == 0xff).all()
+
+
+@both
+def test_prefill_flags_bad_blocks(cuda, expand):
     c = Case(cuda, [0, 7], [300, 130], 8, 2, 128, seed=24)
     x = c.device()
     x["block_table"][0, 2] = -1
     x["block_table"][1] = c.kc.shape[0]
-    out = c.prefill(**x)
+    out = c.prefill(expand=expand, **x)
     assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_BLOCK_RANGE
     zero = np.zeros((1,) + c.kc.shape[1:], np.uint8)
     c.kc, c.vc = np.concatenate([c.kc, zero]), np.concatenate([c.vc, zero])
