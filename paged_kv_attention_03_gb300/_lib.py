@@ -298,14 +298,37 @@ def pa_decode_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     return out
 
 
-def _need_i32(dev: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        _need(t, torch.int32, name, dev)
+def _arg(t: torch.Tensor, dtype: torch.dtype, name: str, dev: int, shape: tuple) -> int:
+    """The address of a contiguous tensor of this type, device and shape, or an exception that
+    says what is wrong with it (one pass over a tensor: a step's small calls are host bound)."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _one(num_free: torch.Tensor, name: str) -> None:
-    if num_free.numel() != 1:
-        raise ValueError(f"{name} must have one entry")
+def _device_of(t: torch.Tensor, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _run(what: str, fn, dev: int, *args) -> None:
+    """Call the library on device `dev` and its current stream."""
+    stream = _raw_stream(dev) if _raw_stream is not None else _stream(torch.device("cuda", dev))
+    if dev == torch.cuda.current_device():
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st != PA_OK:
+        raise PAError(st, what)
 
 
 def pa_prepare_step(context_lens: torch.Tensor, query_lens: torch.Tensor,
@@ -320,28 +343,34 @@ def pa_prepare_step(context_lens: torch.Tensor, query_lens: torch.Tensor,
     blocks from the end of free_blocks[:num_free] into block_table (in place) and returns
     (seq_lens [S], cu_seqlens_q [S + 1], slot_mapping [max_tokens], positions [max_tokens],
     num_free_out [1]).  num_free_out may be num_free and seq_lens may be context_lens."""
-    lib = load()
-    dev = block_table.device
-    _need_i32(dev, context_lens=context_lens, query_lens=query_lens, block_table=block_table,
-              free_blocks=free_blocks, num_free=num_free)
-    n = context_lens.shape[0]
-    if block_table.dim() != 2 or block_table.shape[0] != n or query_lens.shape != (n,) \
-            or context_lens.dim() != 1 or free_blocks.dim() != 1:
-        raise ValueError("pa_prepare_step: inconsistent shapes")
-    _one(num_free, "num_free")
-    max_tokens = int(max_tokens)
-    seq_lens = _out(seq_lens, (n,), torch.int32, dev, "seq_lens")
-    cu_seqlens_q = _out(cu_seqlens_q, (n + 1,), torch.int32, dev, "cu_seqlens_q")
-    slot_mapping = _out(slot_mapping, (max(max_tokens, 0),), torch.int32, dev, "slot_mapping")
-    positions = _out(positions, (max(max_tokens, 0),), torch.int32, dev, "positions")
-    num_free_out = _out(num_free_out, (1,), torch.int32, dev, "num_free_out")
-    with _on(dev):
-        st = lib.pa_prepare_step(_ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens_q),
-                                 _ptr(slot_mapping), _ptr(positions), _ptr(num_free_out),
-                                 _ptr(context_lens), _ptr(query_lens), _ptr(free_blocks),
-                                 _ptr(num_free), n, block_table.shape[1], max_tokens,
-                                 free_blocks.shape[0], block_size, _stream(dev))
-    _check(st, "pa_prepare_step")
+    lib = _lib or load()
+    dev = _device_of(block_table, "block_table")
+    n, width = block_table.shape
+    pool, = free_blocks.shape
+    tokens = max(int(max_tokens), 0)
+    i32 = torch.int32
+    if seq_lens is None:
+        seq_lens = torch.empty(n, dtype=i32, device=block_table.device)
+    if cu_seqlens_q is None:
+        cu_seqlens_q = torch.empty(n + 1, dtype=i32, device=block_table.device)
+    if slot_mapping is None:
+        slot_mapping = torch.empty(tokens, dtype=i32, device=block_table.device)
+    if positions is None:
+        positions = torch.empty(tokens, dtype=i32, device=block_table.device)
+    if num_free_out is None:
+        num_free_out = torch.empty(1, dtype=i32, device=block_table.device)
+    _run("pa_prepare_step", lib.pa_prepare_step, dev,
+         _arg(block_table, i32, "block_table", dev, (n, width)),
+         _arg(seq_lens, i32, "seq_lens", dev, (n,)),
+         _arg(cu_seqlens_q, i32, "cu_seqlens_q", dev, (n + 1,)),
+         _arg(slot_mapping, i32, "slot_mapping", dev, (tokens,)),
+         _arg(positions, i32, "positions", dev, (tokens,)),
+         _arg(num_free_out, i32, "num_free_out", dev, (1,)),
+         _arg(context_lens, i32, "context_lens", dev, (n,)),
+         _arg(query_lens, i32, "query_lens", dev, (n,)),
+         _arg(free_blocks, i32, "free_blocks", dev, (pool,)),
+         _arg(num_free, i32, "num_free", dev, (1,)),
+         n, width, max_tokens, pool, block_size)
     return seq_lens, cu_seqlens_q, slot_mapping, positions, num_free_out
 
 
@@ -353,33 +382,31 @@ def pa_release_blocks(finished: torch.Tensor, seq_lens: torch.Tensor, block_tabl
     """Append the blocks of the rows with finished != 0 (int32) to free_blocks[:num_free] (in
     place) and return (seq_lens_out [S], 0 for those rows, num_free_out [1]).  The outputs may
     be seq_lens and num_free."""
-    lib = load()
-    dev = block_table.device
-    _need_i32(dev, finished=finished, seq_lens=seq_lens, block_table=block_table,
-              free_blocks=free_blocks, num_free=num_free)
-    n = seq_lens.shape[0]
-    if block_table.dim() != 2 or block_table.shape[0] != n or finished.shape != (n,) \
-            or seq_lens.dim() != 1 or free_blocks.dim() != 1:
-        raise ValueError("pa_release_blocks: inconsistent shapes")
-    _one(num_free, "num_free")
-    seq_lens_out = _out(seq_lens_out, (n,), torch.int32, dev, "seq_lens_out")
-    num_free_out = _out(num_free_out, (1,), torch.int32, dev, "num_free_out")
-    with _on(dev):
-        st = lib.pa_release_blocks(_ptr(free_blocks), _ptr(num_free_out), _ptr(seq_lens_out),
-                                   _ptr(finished), _ptr(seq_lens), _ptr(block_table),
-                                   _ptr(num_free), n, block_table.shape[1],
-                                   free_blocks.shape[0], block_size, _stream(dev))
-    _check(st, "pa_release_blocks")
+    lib = _lib or load()
+    dev = _device_of(block_table, "block_table")
+    n, width = block_table.shape
+    pool, = free_blocks.shape
+    i32 = torch.int32
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty(n, dtype=i32, device=block_table.device)
+    if num_free_out is None:
+        num_free_out = torch.empty(1, dtype=i32, device=block_table.device)
+    _run("pa_release_blocks", lib.pa_release_blocks, dev,
+         _arg(free_blocks, i32, "free_blocks", dev, (pool,)),
+         _arg(num_free_out, i32, "num_free_out", dev, (1,)),
+         _arg(seq_lens_out, i32, "seq_lens_out", dev, (n,)),
+         _arg(finished, i32, "finished", dev, (n,)),
+         _arg(seq_lens, i32, "seq_lens", dev, (n,)),
+         _arg(block_table, i32, "block_table", dev, (n, width)),
+         _arg(num_free, i32, "num_free", dev, (1,)),
+         n, width, pool, block_size)
     return seq_lens_out, num_free_out
 
 
-def _fp4_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, dev: torch.device,
-               what: str) -> tuple[int, int, int, int]:
-    """(num_blocks, num_kv_heads, block_size, head_dim) of 4-bit caches, uint8
+def _fp4_shape(k_cache: torch.Tensor, what: str) -> tuple[int, int, int, int]:
+    """(num_blocks, num_kv_heads, block_size, head_dim) of a 4-bit cache, uint8
     [num_blocks, num_kv_heads, block_size, head_dim / 2 + head_dim / 16]."""
-    _need(k_cache, torch.uint8, "k_cache", dev)
-    _need(v_cache, torch.uint8, "v_cache", dev)
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or k_cache.shape[3] % 9:
+    if k_cache.dim() != 4 or k_cache.shape[3] % 9:
         raise ValueError(f"{what}: 4-bit caches are [num_blocks, num_kv_heads, block_size, "
                          "head_dim / 2 + head_dim / 16] bytes")
     nb, hkv, bs, row = k_cache.shape
@@ -391,20 +418,17 @@ def pa_store_kvcache_fp4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.
                          kv_scale: float) -> None:
     """Quantise key/value [T, Hkv, D] bf16 into 4-bit caches (uint8 [NB, Hkv, bs, D/2 + D/16]:
     E2M1 codes, then an E4M3 scale for each 16 dims) at slot_mapping [T] (< 0: skipped)."""
-    lib = load()
-    dev = k_cache.device
-    nb, hkv, bs, d = _fp4_cache(k_cache, v_cache, dev, "pa_store_kvcache_fp4")
-    _need(key, torch.bfloat16, "key", dev)
-    _need(value, torch.bfloat16, "value", dev)
-    _need(slot_mapping, torch.int32, "slot_mapping", dev)
-    if key.dim() != 3 or key.shape != value.shape or key.shape[1:] != (hkv, d) \
-            or slot_mapping.shape != key.shape[:1]:
-        raise ValueError("pa_store_kvcache_fp4: inconsistent shapes")
-    with _on(dev):
-        st = lib.pa_store_kvcache_fp4(_ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache),
-                                      _ptr(slot_mapping), key.shape[0], nb, bs, hkv, d,
-                                      kv_scale, _stream(dev))
-    _check(st, "pa_store_kvcache_fp4")
+    lib = _lib or load()
+    dev = _device_of(k_cache, "k_cache")
+    nb, hkv, bs, d = _fp4_shape(k_cache, "pa_store_kvcache_fp4")
+    n, = slot_mapping.shape
+    _run("pa_store_kvcache_fp4", lib.pa_store_kvcache_fp4, dev,
+         _arg(key, torch.bfloat16, "key", dev, (n, hkv, d)),
+         _arg(value, torch.bfloat16, "value", dev, (n, hkv, d)),
+         _arg(k_cache, torch.uint8, "k_cache", dev, k_cache.shape),
+         _arg(v_cache, torch.uint8, "v_cache", dev, k_cache.shape),
+         _arg(slot_mapping, torch.int32, "slot_mapping", dev, (n,)),
+         n, nb, bs, hkv, d, kv_scale)
 
 
 def pa_gather_kvcache_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -413,20 +437,21 @@ def pa_gather_kvcache_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor,
                           ) -> tuple[torch.Tensor, torch.Tensor]:
     """Read rows of 4-bit caches back: (key, value) [T, Hkv, D] bf16 of slot_mapping [T], zeros
     for a negative slot."""
-    lib = load()
-    dev = k_cache.device
-    nb, hkv, bs, d = _fp4_cache(k_cache, v_cache, dev, "pa_gather_kvcache_fp4")
-    _need(slot_mapping, torch.int32, "slot_mapping", dev)
-    if slot_mapping.dim() != 1:
-        raise ValueError("pa_gather_kvcache_fp4: slot_mapping must be one-dimensional")
-    n = slot_mapping.shape[0]
-    key = _out(key, (n, hkv, d), torch.bfloat16, dev, "key")
-    value = _out(value, (n, hkv, d), torch.bfloat16, dev, "value")
-    with _on(dev):
-        st = lib.pa_gather_kvcache_fp4(_ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache),
-                                       _ptr(slot_mapping), n, nb, bs, hkv, d, kv_scale,
-                                       _stream(dev))
-    _check(st, "pa_gather_kvcache_fp4")
+    lib = _lib or load()
+    dev = _device_of(k_cache, "k_cache")
+    nb, hkv, bs, d = _fp4_shape(k_cache, "pa_gather_kvcache_fp4")
+    n, = slot_mapping.shape
+    if key is None:
+        key = torch.empty(n, hkv, d, dtype=torch.bfloat16, device=k_cache.device)
+    if value is None:
+        value = torch.empty(n, hkv, d, dtype=torch.bfloat16, device=k_cache.device)
+    _run("pa_gather_kvcache_fp4", lib.pa_gather_kvcache_fp4, dev,
+         _arg(key, torch.bfloat16, "key", dev, (n, hkv, d)),
+         _arg(value, torch.bfloat16, "value", dev, (n, hkv, d)),
+         _arg(k_cache, torch.uint8, "k_cache", dev, k_cache.shape),
+         _arg(v_cache, torch.uint8, "v_cache", dev, k_cache.shape),
+         _arg(slot_mapping, torch.int32, "slot_mapping", dev, (n,)),
+         n, nb, bs, hkv, d, kv_scale)
     return key, value
 
 
@@ -446,16 +471,27 @@ def pa_varlen_prefill_fp4_workspace_size(num_seqs: int, num_heads: int, num_kv_h
                                                            sliding_window))
 
 
-def _workspace(workspace: torch.Tensor | None, need: int, dev: torch.device):
-    """(pointer, bytes) of a caller's scratch that is large enough, or of a new one; the tensor
-    is returned too, so that it lives until the call is queued."""
-    if need == 0:
-        return None, 0, None
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev:
-        raise ValueError(f"workspace is on {workspace.device}, expected {dev}")
-    return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
+def _workspace(workspace: torch.Tensor | None, need: int, dev: int):
+    """A caller's scratch, or a new one of `need` bytes: (address, bytes, tensor).  The tensor is
+    kept until the call is queued; the allocator orders its reuse on the same stream."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=f"cuda:{dev}")
+    elif workspace.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.device}, expected cuda:{dev}")
+    return _ptr(workspace), workspace.nbytes, workspace
+
+
+def _fp4_new_tokens(key, value, slot_mapping, rows: int, hkv: int, d: int, dev: int, what: str):
+    """Addresses of the optional new tokens (all three or none)."""
+    if key is None and value is None and slot_mapping is None:
+        return None, None, None
+    if key is None or value is None or slot_mapping is None:
+        raise ValueError(f"{what}: key, value and slot_mapping are given together")
+    return (_arg(key, torch.bfloat16, "key", dev, (rows, hkv, d)),
+            _arg(value, torch.bfloat16, "value", dev, (rows, hkv, d)),
+            _arg(slot_mapping, torch.int32, "slot_mapping", dev, (rows,)))
 
 
 def pa_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -466,29 +502,27 @@ def pa_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Paged decode over 4-bit caches (uint8 [NB, Hkv, bs, D/2 + D/16], elements
     code * scale * kv_scale): q [B, H, D] -> out [B, H, D].  New tokens, when given, are
-    quantised into the caches in the same launch."""
-    lib = load()
-    dev = q.device
-    nb, hkv, bs, d = _fp4_cache(k_cache, v_cache, dev, "pa_decode_fp4")
-    _need(q, torch.bfloat16, "q", dev)
-    _need(block_table, torch.int32, "block_table", dev)
-    _need(seq_lens, torch.int32, "seq_lens", dev)
-    batch, num_heads, head_dim = q.shape
-    if d != head_dim or block_table.dim() != 2 or block_table.shape[0] != batch \
-            or seq_lens.shape != (batch,):
-        raise ValueError("pa_decode_fp4: inconsistent shapes")
-    _new_tokens(key, value, slot_mapping, batch, hkv, head_dim, dev, "pa_decode_fp4")
-    out = _out(out, q.shape, torch.bfloat16, dev)
+    quantised into the caches in the same launch.  A workspace of fewer than
+    pa_decode_fp4_workspace_size(...) bytes is refused; without one it is allocated."""
+    lib = _lib or load()
+    dev = _device_of(q, "q")
+    nb, hkv, bs, d = _fp4_shape(k_cache, "pa_decode_fp4")
+    batch, heads, _ = q.shape
+    width = block_table.shape[-1]
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    new = _fp4_new_tokens(key, value, slot_mapping, batch, hkv, d, dev, "pa_decode_fp4")
     ws, ws_bytes, workspace = _workspace(
-        workspace, pa_decode_fp4_workspace_size(batch, num_heads, hkv, head_dim, max_seq_len,
-                                                sliding_window), dev)
-    with _on(dev):
-        st = lib.pa_decode_fp4(_ptr(out), _ptr(q), _ptr(key), _ptr(value), _ptr(slot_mapping),
-                               _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
-                               block_table.shape[1], _ptr(seq_lens), batch, max_seq_len, nb, bs,
-                               num_heads, hkv, head_dim, sliding_window, scale, kv_scale, ws,
-                               ws_bytes, _stream(dev))
-    _check(st, "pa_decode_fp4")
+        workspace, 0 if workspace is not None else pa_decode_fp4_workspace_size(
+            batch, heads, hkv, d, max_seq_len, sliding_window), dev)
+    _run("pa_decode_fp4", lib.pa_decode_fp4, dev,
+         _arg(out, torch.bfloat16, "out", dev, (batch, heads, d)),
+         _arg(q, torch.bfloat16, "q", dev, (batch, heads, d)), *new,
+         _arg(k_cache, torch.uint8, "k_cache", dev, k_cache.shape),
+         _arg(v_cache, torch.uint8, "v_cache", dev, k_cache.shape),
+         _arg(block_table, torch.int32, "block_table", dev, (batch, width)), width,
+         _arg(seq_lens, torch.int32, "seq_lens", dev, (batch,)), batch, max_seq_len, nb, bs, heads,
+         hkv, d, sliding_window, scale, kv_scale, ws, ws_bytes)
     return out
 
 
@@ -502,35 +536,32 @@ def pa_varlen_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
                           out: torch.Tensor | None = None,
                           workspace: torch.Tensor | None = None) -> torch.Tensor:
     """pa_varlen_prefill over 4-bit caches (as pa_decode_fp4): q [Tq, H, D] -> out [Tq, H, D].
-    New tokens, when given, are quantised into the caches first."""
-    lib = load()
-    dev = q.device
-    nb, hkv, bs, d = _fp4_cache(k_cache, v_cache, dev, "pa_varlen_prefill_fp4")
-    _need(q, torch.bfloat16, "q", dev)
-    _need(cu_seqlens_q, torch.int32, "cu_seqlens_q", dev)
-    _need(block_table, torch.int32, "block_table", dev)
-    total_q, num_heads, head_dim = q.shape
-    num_seqs = cu_seqlens_q.shape[0] - 1
-    if d != head_dim or block_table.dim() != 2 or block_table.shape[0] != num_seqs:
-        raise ValueError("pa_varlen_prefill_fp4: inconsistent shapes")
-    for t, n, rows in ((seq_lens, "seq_lens", num_seqs), (cu_seqlens_k, "cu_seqlens_k", num_seqs + 1)):
-        if t is not None:
-            _need(t, torch.int32, n, dev)
-            if t.shape != (rows,):
-                raise ValueError(f"pa_varlen_prefill_fp4: {n} must have {rows} entries")
-    _new_tokens(key, value, slot_mapping, total_q, hkv, head_dim, dev, "pa_varlen_prefill_fp4")
-    out = _out(out, q.shape, torch.bfloat16, dev)
-    need = pa_varlen_prefill_fp4_workspace_size(
-        num_seqs, num_heads, hkv, head_dim, max_seqlen_k, sliding_window)
-    ws, ws_bytes, workspace = _workspace(workspace, need, dev)
-    with _on(dev):
-        st = lib.pa_varlen_prefill_fp4(
-            _ptr(out), _ptr(q), _ptr(key), _ptr(value), _ptr(slot_mapping), _ptr(k_cache),
-            _ptr(v_cache), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(seq_lens),
-            _ptr(block_table), block_table.shape[1], num_seqs, total_q, max_seqlen_q,
-            max_seqlen_k, nb, bs, num_heads, hkv, head_dim, sliding_window, scale, kv_scale, ws,
-            ws_bytes, _stream(dev))
-    _check(st, "pa_varlen_prefill_fp4")
+    New tokens, when given, are quantised into the caches first.  Without a workspace one of
+    pa_varlen_prefill_fp4_workspace_size(...) bytes is allocated."""
+    lib = _lib or load()
+    dev = _device_of(q, "q")
+    nb, hkv, bs, d = _fp4_shape(k_cache, "pa_varlen_prefill_fp4")
+    total_q, heads, _ = q.shape
+    n = cu_seqlens_q.shape[0] - 1
+    width = block_table.shape[-1]
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    new = _fp4_new_tokens(key, value, slot_mapping, total_q, hkv, d, dev, "pa_varlen_prefill_fp4")
+    ws, ws_bytes, workspace = _workspace(
+        workspace, 0 if workspace is not None else pa_varlen_prefill_fp4_workspace_size(
+            n, heads, hkv, d, max_seqlen_k, sliding_window), dev)
+    _run("pa_varlen_prefill_fp4", lib.pa_varlen_prefill_fp4, dev,
+         _arg(out, torch.bfloat16, "out", dev, (total_q, heads, d)),
+         _arg(q, torch.bfloat16, "q", dev, (total_q, heads, d)), *new,
+         _arg(k_cache, torch.uint8, "k_cache", dev, k_cache.shape),
+         _arg(v_cache, torch.uint8, "v_cache", dev, k_cache.shape),
+         _arg(cu_seqlens_q, torch.int32, "cu_seqlens_q", dev, (n + 1,)),
+         None if cu_seqlens_k is None else
+         _arg(cu_seqlens_k, torch.int32, "cu_seqlens_k", dev, (n + 1,)),
+         None if seq_lens is None else _arg(seq_lens, torch.int32, "seq_lens", dev, (n,)),
+         _arg(block_table, torch.int32, "block_table", dev, (n, width)), width, n, total_q,
+         max_seqlen_q, max_seqlen_k, nb, bs, heads, hkv, d, sliding_window, scale, kv_scale, ws,
+         ws_bytes)
     return out
 
 
