@@ -1278,9 +1278,13 @@ template <int HD>
 constexpr int expand_keys() {  // keys of a block
     return kExpandThreads / (HD / 16);
 }
-// Query-tile pairs of the longest sequence from which the keys are expanded beforehand: every pair
-// expands each tile again otherwise.
-constexpr int kExpandItems = 3;
+// Keys are expanded beforehand when the longest sequence has this many query-tile pairs (each pair
+// expands its tiles again otherwise) and the call a few items for every SM (the extra launch and
+// its writes cost more than they save in a call of one round).  32/8 heads, expanded / in the
+// kernel: 16 x 2048 tokens 501 / 695 us; 8 x 512 after 8192 529 / 697; 16 x 256 after 2048
+// 185 / 201; 8 x 256 after 1024 67.1 / 67.5; three prompts of 37-301 tokens 32 / 27.
+constexpr int kExpandPairs = 3;
+constexpr int kExpandRounds = 2;
 
 template <int HD>
 __global__ void __launch_bounds__(kExpandThreads)
@@ -1510,7 +1514,8 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
         if (a.cache == kCacheE4m3) {
             if (a.head_dim != 128) return cudaErrorInvalidValue;
             e = launch_prefill_d<128, false, kCacheE4m3>(kp, a, stream);
-        } else if (a.cache == kCacheFp4 && a.scratch != nullptr && kp.q_items >= kExpandItems) {
+        } else if (a.cache == kCacheFp4 && a.scratch != nullptr && kp.q_items >= kExpandPairs &&
+                   kp.n_items >= kExpandRounds * kPlanSms) {
             switch (a.head_dim) {
                 case 64: e = launch_expanded<64>(kp, a, stream); break;
                 case 128: e = launch_expanded<128>(kp, a, stream); break;
