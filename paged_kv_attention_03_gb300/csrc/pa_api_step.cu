@@ -23,6 +23,9 @@ int log2_of(int x) {
 // inside the normal fp32 range.
 bool fp4_scale_ok(float s) { return s >= 1e-30f && s <= 1e30f; }
 
+// Longest sequence: positions past its end, up to a list of units, stay inside 32 bits.
+constexpr int kMostKeys = 0x7ffff000;
+
 // Sizes of a 4-bit cache: PA_OK, or why it is refused.
 pa_status check_fp4_cache(int64_t num_blocks, int block_size, int num_kv_heads, int head_dim,
                           float kv_scale) {
@@ -187,6 +190,7 @@ pa_status pa_decode_fp4(void *out, const void *q, const void *key, const void *v
                         float scale, float kv_scale, void *workspace, size_t workspace_bytes,
                         void *stream) {
     if (batch < 0 || max_seq_len < 0 || max_num_blocks < 0) return PA_ERR_INVALID_ARG;
+    if (max_seq_len > kMostKeys) return PA_ERR_UNSUPPORTED;
     pa_status st = check_fp4_cache(num_blocks, block_size, num_kv_heads, head_dim, kv_scale);
     if (st == PA_OK) st = check_fp4_heads(num_heads, num_kv_heads, scale);
     if (st != PA_OK) return st;
@@ -253,6 +257,7 @@ pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const
                                 size_t workspace_bytes, void *stream) {
     if (num_seqs < 0 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || max_num_blocks < 0)
         return PA_ERR_INVALID_ARG;
+    if (max_seqlen_k > kMostKeys) return PA_ERR_UNSUPPORTED;
     pa_status st = check_fp4_cache(num_blocks, block_size, num_kv_heads, head_dim, kv_scale);
     if (st == PA_OK) st = check_fp4_heads(num_heads, num_kv_heads, scale);
     if (st != PA_OK) return st;

@@ -116,6 +116,7 @@ def test_attention_empty_calls_and_workspace(lib):
     assert _decode(lib, batch=65536) == UNSUPPORTED
     assert _prefill(lib, total=0) == OK and _prefill(lib, n=0) == OK
     assert _prefill(lib, mq=200) == INVALID  # more queries than keys
+    assert _decode(lib, most=2 ** 31 - 1) == UNSUPPORTED and _prefill(lib, mk=2 ** 31 - 1) == UNSUPPORTED
     assert _prefill(lib, lens=None) == INVALID
     # Short sequences need no workspace; long ones one of the advertised size and alignment.
     assert pa.pa_decode_fp4_workspace_size(4, 8, 2, 64, 100) == 0

@@ -319,6 +319,23 @@ def test_decode_is_deterministic_and_leaves_other_rows(cuda):
     assert torch.equal(buf[1:5], first) and (buf[0] == 7).all() and (buf[5] == 7).all()
 
 
+def test_calls_refuse_wrong_tensors(cuda):
+    c = Case(cuda, [300, 40], [1, 1], 8, 2, 128, seed=19)
+    x = c.device()
+    for name, bad, error in (("q", x["q"].half(), TypeError), ("k_cache", x["k_cache"][..., :36], ValueError),
+                             ("v_cache", x["v_cache"][:2], ValueError), ("seq_lens", x["seq_lens"][:1], ValueError),
+                             ("block_table", x["block_table"].cpu(), ValueError)):
+        with pytest.raises(error):
+            c.decode(**{**x, name: bad})
+        with pytest.raises(error):
+            c.prefill(**{**x, name: bad})
+    with pytest.raises(ValueError, match="together"):
+        c.decode(**x, key=c.key.to(cuda))
+    with pytest.raises(pa.PAError) as e:  # a workspace that is too small
+        c.decode(**x, workspace=torch.empty(256, dtype=torch.uint8, device=cuda))
+    assert e.value.status == pa.PA_ERR_INVALID_ARG
+
+
 def test_decode_ignores_what_its_workspace_holds(cuda):
     c = Case(cuda, [300, 4000, 50, 9], [1] * 4, 32, 8, 128, seed=18)
     good = c.decode()

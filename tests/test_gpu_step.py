@@ -73,6 +73,34 @@ def test_prepare_no_requests(cuda):
     assert got[4].tolist() == [2] and pa.pa_read_device_error(device=cuda) == 0
 
 
+@pytest.mark.parametrize("tokens", [6, 9000])
+def test_prepare_without_positions(cuda, tokens):
+    # The C entry point takes NULL for them.
+    ctx, q, bt, free, nf = _t([3, 0], cuda), _t([1, 5], cuda), _t([[7, -1], [-1, -1]], cuda), _t([5, 6], cuda), _t([2], cuda)
+    lens, cu, slots = _t([0, 0], cuda), _t([0, 0, 0], cuda), torch.zeros(tokens, dtype=torch.int32, device=cuda)
+    p = lambda t: t.data_ptr()  # noqa: E731
+    st = pa.load().pa_prepare_step(p(bt), p(lens), p(cu), p(slots), None, p(nf), p(ctx), p(q), p(free), p(nf), 2, 2, tokens, 8,
+                                   16, torch.cuda.current_stream().cuda_stream)
+    assert st == pa.PA_OK
+    assert slots[:6].tolist() == [7 * 16 + 3] + [6 * 16 + i for i in range(5)] and (slots[6:] == -1).all()
+    assert lens.tolist() == [4, 5] and nf.tolist() == [1] and pa.pa_read_device_error(device=cuda) == 0
+
+
+def test_binding_names_what_is_wrong(cuda):
+    i = _t([1, 2], cuda)
+    table = _t([[0], [0]], cuda)
+    with pytest.raises(TypeError, match="query_lens"):
+        pa.pa_prepare_step(i, i.long(), table, i, i[:1], 16, 4)
+    with pytest.raises(ValueError, match="num_free"):
+        pa.pa_prepare_step(i, i, table, i, i, 16, 4)
+    with pytest.raises(ValueError, match="slot_mapping"):
+        pa.pa_prepare_step(i, i, table, i, i[:1], 16, 4, slot_mapping=i)
+    with pytest.raises(ValueError, match="finished"):
+        pa.pa_release_blocks(i.cpu(), i, table, i, i[:1], 16)
+    with pytest.raises(ValueError, match="contiguous"):
+        pa.pa_release_blocks(i, i, _t([[0, 0], [0, 0]], cuda)[:, :1], i, i[:1], 16)
+
+
 @pytest.mark.parametrize("max_tokens", [200, 20000])
 @pytest.mark.parametrize("extra", [0, 1, 4, 7])
 def test_prepare_out_of_blocks(cuda, extra, max_tokens):
