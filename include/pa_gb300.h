@@ -438,7 +438,7 @@ pa_status pa_release_blocks(int32_t *free_blocks, int32_t *num_free_out, int32_t
  * four), then head_dim / 16 scales.  An element reads
  *     code * scale * kv_scale,
  * code in {0, .5, 1, 1.5, 2, 3, 4, 6} with a sign (bit 3).  kv_scale is one number a cache,
- * in [1e-30, 1e30].  The store of 16 values x with the largest magnitude a:
+ * in [1e-25, 1e25].  The store of 16 values x with the largest magnitude a:
  *     scale = max(E4M3(a / (6 kv_scale)), 2^-9),   code = E2M1(x / (scale * kv_scale)),
  * each division and product one fp32 operation, each conversion to the nearest (ties to
  * even), saturating at 448 and 6.  A NaN makes its group's scale NaN; an infinity saturates.

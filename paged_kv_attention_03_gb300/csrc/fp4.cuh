@@ -8,6 +8,7 @@
 // kv head are contiguous, so 16 tokens are 9 D bytes that one bulk copy moves.
 #pragma once
 
+#include <math.h>
 #include <stdint.h>
 
 #include "pa_common.cuh"
@@ -66,6 +67,13 @@ constexpr uint32_t kMinScale = 1;
 // each division and product one fp32 operation, each conversion to the nearest with ties to
 // even, saturating (448, 6).  A NaN in the group makes its scale NaN, so the group reads NaN;
 // an infinity saturates.
+//
+// The 16 quotients share their divisor d: with r the rounded reciprocal, q = x r and one
+// correction q + (x - q d) r by two fused operations give the rounded quotient (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990, asks for
+// a q within one unit; here every 8-bit x against every 24-bit d was tried, and all 2^30
+// quotients are the rounded ones).  That scales by powers of two as long as x - q d keeps its
+// bits, which kv_scale >= 1e-25 sees to.  17403 tokens: 20.3 us against 23.5 with divisions.
 __device__ __forceinline__ uint2 quant_group(const uint32_t (&w)[8], float kv_scale,
                                              float kv_scale6, uint32_t &scale_code) {
     // Magnitudes of bf16 order like their bit patterns, and a NaN's is above infinity's.
@@ -79,11 +87,19 @@ __device__ __forceinline__ uint2 quant_group(const uint32_t (&w)[8], float kv_sc
         : "f"(0.f), "f"(__fdiv_rn(amax, kv_scale6)));
     scale_code = max(static_cast<uint32_t>(s8) & 0xffu, kMinScale);
     const float den = __fmul_rn(f16_lo(e4m3x2_to_f16x2(scale_code)), kv_scale);
+    const float r = __frcp_rn(den);
+    // Only a saturated scale leaves quotients beyond 6.5 (to infinity): those saturate too.
+    const float top_x = scale_code >= 126u ? 8.f * den : INFINITY;
+    auto quotient = [&](float x) {
+        x = fminf(fmaxf(x, -top_x), top_x);
+        const float q = __fmul_rn(x, r);
+        return __fmaf_rn(__fmaf_rn(-q, den, x), r, q);
+    };
     uint32_t c[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float lo = __fdiv_rn(__uint_as_float(w[i] << 16), den);
-        const float hi = __fdiv_rn(__uint_as_float(w[i] & 0xffff0000u), den);
+        const float lo = quotient(__uint_as_float(w[i] << 16));
+        const float hi = quotient(__uint_as_float(w[i] & 0xffff0000u));
         uint32_t b;
         asm("{\n.reg .b8 t;\ncvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\ncvt.u32.u8 %0, t;\n}\n"
             : "=r"(b)

@@ -19,9 +19,9 @@ int log2_of(int x) {
     return l;
 }
 
-// kv_scale of a 4-bit cache: 6 kv_scale and the smallest scale (2^-9) times kv_scale stay
-// inside the normal fp32 range.
-bool fp4_scale_ok(float s) { return s >= 1e-30f && s <= 1e30f; }
+// kv_scale of a 4-bit cache: the scales times it stay far enough inside the normal fp32 range
+// that quotients by them and their remainders keep all bits.
+bool fp4_scale_ok(float s) { return s >= 1e-25f && s <= 1e25f; }
 
 // Longest sequence: positions past its end, up to a list of units, stay inside 32 bits.
 constexpr int kMostKeys = 0x7ffff000;

@@ -160,6 +160,24 @@ def test_store_ties_and_special_values(cuda):
     assert want[2, 0, 5] == -6 * 448 and want[2, 0, 40] == 1.03125
 
 
+@pytest.mark.parametrize("kv_scale", [1.0, 1 / 3, 1e-25, 3.7e-24, 1e25, 7.3e24, 0.0117, 271.828])
+def test_store_rounds_every_quotient(cuda, kv_scale):
+    # Every bf16 significand at every distance from its group's largest value, for scales with few
+    # and with all bits: codes and scales equal the oracle's, whose divisions are fp32 ones.
+    g = torch.Generator().manual_seed(1)
+    kvs = float(np.float32(kv_scale))
+    x = torch.randint(128, 256, (4000, 2, 64), generator=g).double() * 2.0 ** torch.randint(-12, 1, (4000, 2, 64), generator=g).double()
+    x = (x * torch.where(torch.rand(x.shape, generator=g) < 0.5, -1.0, 1.0) * kvs *
+         2.0 ** torch.randint(-12, 7, (4000, 2, 1), generator=g).double()).float().bfloat16()
+    host = np.zeros((250, 2, 16, 36), np.uint8)
+    k = torch.from_numpy(host.copy()).to(cuda)
+    v = torch.zeros_like(k)
+    pa.pa_store_kvcache_fp4(x.to(cuda), x.to(cuda), k, v, torch.arange(4000, dtype=torch.int32, device=cuda), kv_scale)
+    fp4.store(x.double().numpy(), host, np.arange(4000), kv_scale)
+    np.testing.assert_array_equal(k.cpu().numpy(), host)
+    assert torch.equal(k, v)
+
+
 def test_store_and_gather_flag_slots_past_the_pool(cuda):
     x = _bf((3, 2, 64), 1).to(cuda)
     buf = torch.zeros(3, 2, 16, 36, dtype=torch.uint8, device=cuda)  # a block behind the caches
