@@ -353,8 +353,8 @@ __device__ __forceinline__ void split_body(const Params &p) {
 
     // ---- the issue side: units ahead of the consumer, across segments ----
     // Its place is kept in shared memory: it is needed once for 16 units.  In registers are the
-    // byte offsets of the next units' halves, lane i that of half i (less the place of its runs
-    // in a stage; odd: past the sequence or a bad table entry, read as zeros), and how many units they cover.
+    // byte offsets of the next units' halves, lane i that of half i (odd: past the sequence or
+    // a bad table entry, read as zeros), and how many units they cover.
     s_ahead[warp].seg = seg;
     s_ahead[warp].unit = unit;
     s_ahead[warp].left = todo;
@@ -373,7 +373,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
         }
         listed = min(16, min(a.left, a.seg.units - a.unit));
         const int key = a.seg.r.base + kUnit * a.unit + 16 * lane;
-        half_off = -(lane & 1) * 2 * HB + 1;
+        half_off = 1;
         if (lane < 2 * listed && key < a.seg.r.L) {
             const int blk = __ldg(p.block_table + static_cast<int64_t>(a.seg.b) * p.max_num_blocks + (key >> p.log2_bs));
             if (blk >= 0 && blk < p.num_blocks) {
@@ -388,32 +388,35 @@ __device__ __forceinline__ void split_body(const Params &p) {
         if (lane == 0) s_ahead[warp] = a;
         __syncwarp();
     };
-    // Issue the next unit (if there is one) into stage st.  Chunk c of the unit's SB / 16 belongs
-    // to run c / CH (K and V of half 0, K and V of half 1); lane l copies chunks l, l + 32, ...
-    const uint8_t *k_lane = p.k_cache + 16 * lane, *v_lane = p.v_cache + (16 * lane - HB);
+    // Issue the next unit (if there is one) into stage st.  Of each run's CH 16-byte chunks (K and V
+    // of half 0, K and V of half 1), whole sets of 32 are a copy of the warp each; the rests of
+    // the four runs share one, CT lanes for a run.
+    constexpr int CH = HB / 16, CT = CH % 32;
+    static_assert(4 * CT <= 32, "the rests of the four runs fit one copy");
+    const int t_run = lane / CT;  // (4 and above: no part in the last copy)
+    const uint32_t t_at = (CH - CT + lane % CT) * 16;
+    const uint8_t *k_lane = p.k_cache + 16 * lane, *v_lane = p.v_cache + 16 * lane;
+    const uint8_t *t_lane = ((t_run & 1) ? p.v_cache : p.k_cache) + t_at;
+    const uint32_t t_dst = ring + t_run * HB + t_at;
     auto issue = [&](int st) {
-        constexpr int CH = HB / 16, NC = SB / 16, last = NC - 1;
         if (next == listed) list_units();
         if (next < listed) {
-            const uint8_t *run[4];
+            const uint32_t dst = ring + st * SB + 16 * lane;
+            long long off[2];
             uint32_t size[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                long long off = __shfl_sync(0xffffffffu, half_off, 2 * next + h);
-                size[h] = (off & 1) ? 0u : 16u;
-                off &= ~1ll;
-                run[2 * h] = k_lane + off;
-                run[2 * h + 1] = v_lane + off;
-            }
-            const uint32_t dst = ring + st * SB + 16 * lane;
+                off[h] = __shfl_sync(0xffffffffu, half_off, 2 * next + h);
+                size[h] = (off[h] & 1) ? 0u : 16u;
+                off[h] &= ~1ll;
 #pragma unroll
-            for (int i = 0; i < (NC + 31) / 32; ++i) {
-                const int r0 = 32 * i / CH, r1 = (32 * i + 31 < last ? 32 * i + 31 : last) / CH;
-                const bool second = r1 != r0 && 32 * i + lane >= r1 * CH;
-                const uint8_t *src = (second ? run[r1] : run[r0]) + 512 * i;
-                const uint32_t n = second ? size[r1 >> 1] : size[r0 >> 1];
-                if (32 * i + 31 <= last || 32 * i + lane <= last) cp_async_16_policy(dst + 512 * i, src, n, policy);
+                for (int i = 0; i < CH / 32; ++i) {
+                    cp_async_16_policy(dst + 2 * h * HB + 512 * i, k_lane + off[h] + 512 * i, size[h], policy);
+                    cp_async_16_policy(dst + (2 * h + 1) * HB + 512 * i, v_lane + off[h] + 512 * i, size[h], policy);
+                }
             }
+            if (t_run < 4)
+                cp_async_16_policy(t_dst + st * SB, t_lane + (t_run < 2 ? off[0] : off[1]), t_run < 2 ? size[0] : size[1], policy);
             ++next;
         }
         cp_async_commit();
@@ -523,25 +526,35 @@ __device__ __forceinline__ void split_body(const Params &p) {
             }
         }
 
-        // S^T = K Q^T of the two halves.
+        // S^T = K Q^T of the two halves, in turn: a step of one covers the latency of the other's.
         float s[2][NT][4];
+        uint32_t wa[2][D / 32], wb[2][D / 32], sca[2], scb[2];  // codes and scales of rows g and g + 8
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint32_t wa[D / 32], wb[D / 32];  // codes of rows g and g + 8
             const uint32_t ca = kb + 2 * h * HB + k_off, cs = kb + 2 * h * HB + ks_off;
-            const uint32_t sca = k_row<D, 0>(ca, cs, wa), scb = k_row<D, 2 * RB>(ca, cs, wb);
+            sca[h] = k_row<D, 0>(ca, cs, wa[h]);
+            scb[h] = k_row<D, 2 * RB>(ca, cs, wb[h]);
+        }
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
-                const uint32_t pick = (x >> 1) ? 0x3232 : 0x1010;  // a scale for two words
-                const uint32_t sa = __byte_perm(sca, 0u, pick), sb = __byte_perm(scb, 0u, pick);
-                uint32_t fa[4], fb[4];
-                fp4::e2m1x8_to_f16x2x4(wa[x], fa);
-                fp4::e2m1x8_to_f16x2x4(wb[x], fb);
+        for (int x = 0; x < D / 32; ++x) {
+            const uint32_t pick = (x >> 1) ? 0x3232 : 0x1010;  // a scale for two words
+            uint32_t fa[2][4], fb[2][4];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t a[4] = {fp4::mul_f16x2(fa[2 * k], sa), fp4::mul_f16x2(fb[2 * k], sb),
-                                           fp4::mul_f16x2(fa[2 * k + 1], sa),
-                                           fp4::mul_f16x2(fb[2 * k + 1], sb)};
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t sa = __byte_perm(sca[h], 0u, pick), sb = __byte_perm(scb[h], 0u, pick);
+                fp4::e2m1x8_to_f16x2x4(wa[h][x], fa[h]);
+                fp4::e2m1x8_to_f16x2x4(wb[h][x], fb[h]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    fa[h][k] = fp4::mul_f16x2(fa[h][k], sa);
+                    fb[h][k] = fp4::mul_f16x2(fb[h][k], sb);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t a[4] = {fa[h][2 * k], fb[h][2 * k], fa[h][2 * k + 1], fb[h][2 * k + 1]};
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
                         if (x == 0 && k == 0)
@@ -550,7 +563,6 @@ __device__ __forceinline__ void split_body(const Params &p) {
                             mma_f16_16816(s[h][j], a, qf[j][2 * x + k][0], qf[j][2 * x + k][1]);
                     }
                 }
-            }
         }
 
         // V codes and scales of keys 4 t .. 4 t + 3 of each half.
