@@ -447,13 +447,6 @@ __device__ __forceinline__ void schedule_items(const PrefillKernelParams &p, Ite
     }
 }
 
-// 32-byte global store (the address must be 32-byte aligned).
-__device__ __forceinline__ void st_global_v8(void *ptr, const uint32_t *w) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(w[0]),
-                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-}
-
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -1273,7 +1266,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // as 16-bit rows [slots, Hkv, HD] of a scratch cache: K bf16, V f16, code * scale in both, which
 // is exact.  A thread takes 16 dims of one key, for every kv head in turn: the lanes of a key
 // write a row, the table is read once, and the loads of four heads are in flight together.
-constexpr int kExpandThreads = 256;
+constexpr int kExpandThreads = 128;
+constexpr int kExpandHeads = 4;
 template <int HD>
 constexpr int expand_keys() {  // keys of a block
     return kExpandThreads / (HD / 16);
@@ -1309,38 +1303,45 @@ __global__ void __launch_bounds__(kExpandThreads)
     const int64_t step = static_cast<int64_t>(RB) << p.log2_bs;  // to the next head
     const uint8_t *src[2] = {p.k4 + row * RB, p.v4 + row * RB};
     const int64_t dst = (((static_cast<int64_t>(seq) * p.expanded_blocks) << p.log2_bs) + key) * p.num_kv_heads * GROUPS + g;
-#pragma unroll 4
-    for (int h = 0; h < p.num_kv_heads; ++h) {
+    for (int h0 = 0; h0 < p.num_kv_heads; h0 += kExpandHeads) {
+        uint32_t c[kExpandHeads][2][2], s[kExpandHeads][2];
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            uint32_t c[2] = {0u, 0u}, s = 0u;  // zeros for a bad block
-            if (good) {
-                const uint8_t *at = src[kv] + h * step;
+        for (int i = 0; i < kExpandHeads; ++i)
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                c[i][kv][0] = c[i][kv][1] = s[i][kv] = 0u;  // zeros for a bad block
+                if (!good || h0 + i >= p.num_kv_heads) continue;
+                const uint8_t *at = src[kv] + (h0 + i) * step;
                 if constexpr (HD == 128) {
                     const uint2 x = __ldg(reinterpret_cast<const uint2 *>(at) + g);
-                    c[0] = x.x;
-                    c[1] = x.y;
+                    c[i][kv][0] = x.x;
+                    c[i][kv][1] = x.y;
                 } else {  // 36-byte rows: 4-byte aligned
-                    c[0] = __ldg(reinterpret_cast<const uint32_t *>(at) + 2 * g);
-                    c[1] = __ldg(reinterpret_cast<const uint32_t *>(at) + 2 * g + 1);
+                    c[i][kv][0] = __ldg(reinterpret_cast<const uint32_t *>(at) + 2 * g);
+                    c[i][kv][1] = __ldg(reinterpret_cast<const uint32_t *>(at) + 2 * g + 1);
                 }
-                s = __ldg(at + HD / 2 + g);
+                s[i][kv] = __ldg(at + HD / 2 + g);
             }
-            const uint32_t s2 = __byte_perm(fp4::e4m3x2_to_f16x2(s), 0u, 0x1010);
-            uint32_t w[8];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                uint32_t f[4];
-                fp4::e2m1x8_to_f16x2x4(c[x], f);
+        for (int i = 0; i < kExpandHeads; ++i) {
+            if (h0 + i >= p.num_kv_heads) break;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t v = fp4::mul_f16x2(f[k], s2);
-                    w[4 * x + k] = kv ? v : pack_bf16x2(fp4::f16_lo(v), fp4::f16_hi(v));
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint32_t s2 = __byte_perm(fp4::e4m3x2_to_f16x2(s[i][kv]), 0u, 0x1010);
+                uint32_t w[8];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t f[4];
+                    fp4::e2m1x8_to_f16x2x4(c[i][kv][x], f);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t v = fp4::mul_f16x2(f[k], s2);
+                        w[4 * x + k] = kv ? v : pack_bf16x2(fp4::f16_lo(v), fp4::f16_hi(v));
+                    }
                 }
+                // (The scratch is 256-byte aligned: whole sectors.)
+                st_global_v8((kv ? v_out : k_out) + 2 * (dst + (h0 + i) * GROUPS), w);
             }
-            uint4 *out = (kv ? v_out : k_out) + 2 * (dst + h * GROUPS);
-            out[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            out[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
     }
 }

@@ -12,6 +12,7 @@
 // run, its scales gathered by shuffles and written by the row's first lane.
 #include "fp4.cuh"
 #include "pa_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace pa {
 
@@ -109,8 +110,9 @@ store_kvcache_fp4_kernel(const uint4 *__restrict__ key, const uint4 *__restrict_
 
 namespace {
 
-// One group of a row as 16 bf16.
-template <int D>
+// One group of a row as 16 bf16 (32 bytes: one store where dst is aligned to that, so that the L2
+// gets whole sectors).
+template <int D, bool ALIGNED>
 __device__ __forceinline__ void expand_group(const uint8_t *row, int g, float kv_scale, uint4 *dst) {
     uint32_t c[2];
     if constexpr (D == 128) {
@@ -133,13 +135,17 @@ __device__ __forceinline__ void expand_group(const uint8_t *row, int g, float kv
             o[4 * h + k] = pack_bf16x2(fp4::f16_lo(f[k]) * s * kv_scale,
                                        fp4::f16_hi(f[k]) * s * kv_scale);
     }
-    __stcs(dst, make_uint4(o[0], o[1], o[2], o[3]));
-    __stcs(dst + 1, make_uint4(o[4], o[5], o[6], o[7]));
+    if constexpr (ALIGNED) {
+        sm100::st_global_v8(dst, o);
+    } else {
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
 }
 
 }  // namespace
 
-template <int D>
+template <int D, bool ALIGNED>
 __global__ void __launch_bounds__(256)
 gather_kvcache_fp4_kernel(uint4 *__restrict__ key, uint4 *__restrict__ value,
                           const uint8_t *__restrict__ k_cache, const uint8_t *__restrict__ v_cache,
@@ -163,8 +169,8 @@ gather_kvcache_fp4_kernel(uint4 *__restrict__ key, uint4 *__restrict__ value,
         return;
     }
     const int64_t row = cache_row(slot, h, kv_heads, log2_bs);
-    expand_group<D>(k_cache + row * RB, g, kv_scale, key + 2 * i);
-    expand_group<D>(v_cache + row * RB, g, kv_scale, value + 2 * i);
+    expand_group<D, ALIGNED>(k_cache + row * RB, g, kv_scale, key + 2 * i);
+    expand_group<D, ALIGNED>(v_cache + row * RB, g, kv_scale, value + 2 * i);
 }
 
 namespace {
@@ -189,7 +195,9 @@ cudaError_t launch_store_d(const StoreArgs &a, int kv_heads, int log2_bs, float 
 template <int D>
 cudaError_t launch_gather_d(const GatherArgs &a, cudaStream_t stream) {
     const int64_t total = a.num_tokens * a.num_kv_heads * (D / 16);
-    gather_kvcache_fp4_kernel<D><<<fp4_blocks(total), 256, 0, stream>>>(
+    const bool aligned = ((reinterpret_cast<uintptr_t>(a.key) | reinterpret_cast<uintptr_t>(a.value)) & 31u) == 0;
+    auto kern = aligned ? gather_kvcache_fp4_kernel<D, true> : gather_kvcache_fp4_kernel<D, false>;
+    kern<<<fp4_blocks(total), 256, 0, stream>>>(
         static_cast<uint4 *>(a.key), static_cast<uint4 *>(a.value),
         static_cast<const uint8_t *>(a.k_cache), static_cast<const uint8_t *>(a.v_cache),
         a.slot_mapping, total, a.num_slots, a.num_kv_heads, a.log2_bs, a.kv_scale, a.err);

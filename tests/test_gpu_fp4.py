@@ -137,6 +137,12 @@ def test_store_is_bit_exact_and_gather_reads_it_back(cuda, dim, hkv, bs, tokens)
         # code * scale is exact; times kv_scale is one fp32 rounding, then one to bf16
         want = torch.from_numpy(rows.astype(np.float32)).bfloat16()
         assert torch.equal(back.cpu(), want)
+    # Outputs that are aligned to 16 bytes only.
+    n = key.numel()
+    buf = torch.zeros(2, n + 16, dtype=torch.bfloat16, device=cuda)
+    odd = [b[8:8 + n].view(key.shape) for b in buf]
+    pa.pa_gather_kvcache_fp4(*dev, _t(slots, cuda), KVS, key=odd[0], value=odd[1])
+    assert torch.equal(odd[0], key) and torch.equal(odd[1], value) and (buf[:, :8] == 0).all() and (buf[:, 8 + n:] == 0).all()
 
 
 def test_store_ties_and_special_values(cuda):
