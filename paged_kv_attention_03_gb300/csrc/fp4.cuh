@@ -73,9 +73,9 @@ constexpr uint32_t kMinScale = 1;
 // "Computation of elementary functions on the IBM RISC System/6000 processor", 1990, asks for
 // a q within one unit; here every 8-bit x against every 24-bit d was tried, and all 2^30
 // quotients are the rounded ones).  That scales by powers of two as long as x - q d keeps its
-// bits, which kv_scale >= 1e-25 sees to.  17403 tokens: 20.3 us against 23.5 with divisions.
-__device__ __forceinline__ uint2 quant_group(const uint32_t (&w)[8], float kv_scale,
-                                             float kv_scale6, uint32_t &scale_code) {
+// bits, which kv_scale >= 1e-25 sees to.  17403 tokens: 18.3 us against 23.5 with divisions.
+__device__ __forceinline__ uint2 quant_group(uint32_t (&w)[8], float kv_scale, float kv_scale6,
+                                             uint32_t &scale_code) {
     // Magnitudes of bf16 order like their bit patterns, and a NaN's is above infinity's.
     uint32_t top = w[0] & 0x7fff7fffu;
 #pragma unroll
@@ -88,10 +88,16 @@ __device__ __forceinline__ uint2 quant_group(const uint32_t (&w)[8], float kv_sc
     scale_code = max(static_cast<uint32_t>(s8) & 0xffu, kMinScale);
     const float den = __fmul_rn(f16_lo(e4m3x2_to_f16x2(scale_code)), kv_scale);
     const float r = __frcp_rn(den);
-    // Only a saturated scale leaves quotients beyond 6.5 (to infinity): those saturate too.
-    const float top_x = scale_code >= 126u ? 8.f * den : INFINITY;
+    if (scale_code >= 126u) {
+        // Only a saturated scale leaves quotients beyond 6.5, up to infinity: those saturate too.
+        const __nv_bfloat162 most = __float2bfloat162_rn(8.f * den);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 x = __hmax2(__hmin2(*reinterpret_cast<__nv_bfloat162 *>(&w[i]), most), __hneg2(most));
+            w[i] = *reinterpret_cast<const uint32_t *>(&x);
+        }
+    }
     auto quotient = [&](float x) {
-        x = fminf(fmaxf(x, -top_x), top_x);
         const float q = __fmul_rn(x, r);
         return __fmaf_rn(__fmaf_rn(-q, den, x), r, q);
     };
