@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---------------- K / V producer (whole warp) ----------------
             auto produce = [&](auto is_k_tag) {
             constexpr bool is_k = decltype(is_k_tag)::value;
-            const CUtensorMap *map = is_k ? &p.tmap_k : &p.tmap_v;
+            [[maybe_unused]] const CUtensorMap *map = is_k ? &p.tmap_k : &p.tmap_v;
             const uint32_t sbase = is_k ? sK : sV;
             constexpr uint32_t NS = is_k ? NSK : NSV;
             constexpr int b_full = is_k ? B_KFULL : B_VFULL, b_empty = is_k ? B_KEMPTY : B_VEMPTY;
