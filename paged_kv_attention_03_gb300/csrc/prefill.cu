@@ -1272,13 +1272,12 @@ template <int HD>
 constexpr int expand_keys() {  // keys of a block
     return kExpandThreads / (HD / 16);
 }
-// Keys are expanded beforehand when the longest sequence has this many query-tile pairs (each pair
-// expands its tiles again otherwise) and the call a few items for every SM (the extra launch and
-// its writes cost more than they save in a call of one round).  32/8 heads, expanded / in the
-// kernel: 16 x 2048 tokens 501 / 695 us; 8 x 512 after 8192 529 / 697; 16 x 256 after 2048
-// 185 / 201; 8 x 256 after 1024 67.1 / 67.5; three prompts of 37-301 tokens 32 / 27.
+// Keys are expanded beforehand when the longest sequence has this many query-tile pairs: each
+// pair expands its tiles again otherwise.  32/8 heads (64 tokens a pair), expanded / in the
+// kernel: 64 x 64 tokens after 2048 252 / 201 us, 64 x 128 after 2048 349 / 341, 16 x 128 after
+// 4096 182 / 188, 8 x 192 after 1024 54.5 / 59.3, four of 300 after 300 27.7 / 29.5, 8 x 512 after
+// 8192 505 / 692, 16 x 2048 490 / 697.
 constexpr int kExpandPairs = 3;
-constexpr int kExpandRounds = 2;
 
 template <int HD>
 __global__ void __launch_bounds__(kExpandThreads)
@@ -1515,8 +1514,7 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
         if (a.cache == kCacheE4m3) {
             if (a.head_dim != 128) return cudaErrorInvalidValue;
             e = launch_prefill_d<128, false, kCacheE4m3>(kp, a, stream);
-        } else if (a.cache == kCacheFp4 && a.scratch != nullptr && kp.q_items >= kExpandPairs &&
-                   kp.n_items >= kExpandRounds * kPlanSms) {
+        } else if (a.cache == kCacheFp4 && a.scratch != nullptr && kp.q_items >= kExpandPairs) {
             switch (a.head_dim) {
                 case 64: e = launch_expanded<64>(kp, a, stream); break;
                 case 128: e = launch_expanded<128>(kp, a, stream); break;

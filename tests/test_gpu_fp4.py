@@ -83,10 +83,10 @@ class Case:
     def prefill(self, window=0, lens=True, cu_k=False, expand=True, **kw):
         """expand False: a workspace without room for the expanded keys, so that every query block
         expands its tiles itself; True: the declared maximum of the query lengths is so large that
-        the keys are expanded beforehand whatever the batch."""
+        the keys are expanded beforehand whatever the lengths."""
         x = dict(kw) if "q" in kw else {**self.device(), **kw}
         sl = x.pop("seq_lens")
-        most = 128 * 304 if expand else int(self.new.max())
+        most = 128 * 6 if expand else int(self.new.max())
         if not expand:
             need = pa.pa_decode_fp4_workspace_size(len(self.lens), self.heads, self.kc.shape[1], self.dim, int(self.lens.max()),
                                                    window)
@@ -434,7 +434,7 @@ def test_prefill_ignores_what_its_workspace_holds(cuda):
     # stay that.
     c = Case(cuda, [700, 7, 30], [300, 130, 1], 8, 2, 128, seed=26)
     for window in (0, 100):
-        need = pa.pa_varlen_prefill_fp4_workspace_size(3, 8, 2, 128, 128 * 304, window)
+        need = pa.pa_varlen_prefill_fp4_workspace_size(3, 8, 2, 128, 1000, window)
         ws = torch.full((need + 64,), 0xff, dtype=torch.uint8, device=cuda)
         c.check(c.prefill(window, workspace=ws[:need]), window)
         assert (ws[need:] == 0xff).all()
