@@ -458,7 +458,9 @@ pa_status pa_release_blocks(int32_t *free_blocks, int32_t *num_free_out, int32_t
  *     the keys of num_seqs sequences of max_seqlen_k keys in 16 bits (up to 4 GiB each for K
  *     and V; none beyond): with it, long queries expand their sequences' keys once instead of
  *     in every query block.  pa_decode_fp4_workspace_size(num_seqs, ...) bytes are enough to
- *     run without.
+ *     run without.  As in the other prefills a key that a row does not see has weight 0, so a
+ *     NaN value reaches the rows whose 128-key tiles hold it (rows behind a sequence's last
+ *     key are never read as values; the decode reads no value outside a row's range).
  *
  *   workspace  at least pa_decode_fp4_workspace_size(...) /
  *              pa_varlen_prefill_fp4_workspace_size(...) bytes, 256-byte aligned (may be NULL

@@ -347,7 +347,8 @@ def pa_prepare_step(context_lens: torch.Tensor, query_lens: torch.Tensor,
     dev = _device_of(block_table, "block_table")
     n, width = block_table.shape
     pool, = free_blocks.shape
-    tokens = max(int(max_tokens), 0)
+    max_tokens = int(max_tokens)
+    tokens = max(max_tokens, 0)
     i32 = torch.int32
     if seq_lens is None:
         seq_lens = torch.empty(n, dtype=i32, device=block_table.device)
@@ -370,7 +371,7 @@ def pa_prepare_step(context_lens: torch.Tensor, query_lens: torch.Tensor,
          _arg(query_lens, i32, "query_lens", dev, (n,)),
          _arg(free_blocks, i32, "free_blocks", dev, (pool,)),
          _arg(num_free, i32, "num_free", dev, (1,)),
-         n, width, max_tokens, pool, block_size)
+         n, width, max_tokens, pool, int(block_size))
     return seq_lens, cu_seqlens_q, slot_mapping, positions, num_free_out
 
 
@@ -399,7 +400,7 @@ def pa_release_blocks(finished: torch.Tensor, seq_lens: torch.Tensor, block_tabl
          _arg(seq_lens, i32, "seq_lens", dev, (n,)),
          _arg(block_table, i32, "block_table", dev, (n, width)),
          _arg(num_free, i32, "num_free", dev, (1,)),
-         n, width, pool, block_size)
+         n, width, pool, int(block_size))
     return seq_lens_out, num_free_out
 
 
@@ -428,7 +429,7 @@ def pa_store_kvcache_fp4(key: torch.Tensor, value: torch.Tensor, k_cache: torch.
          _arg(k_cache, torch.uint8, "k_cache", dev, k_cache.shape),
          _arg(v_cache, torch.uint8, "v_cache", dev, k_cache.shape),
          _arg(slot_mapping, torch.int32, "slot_mapping", dev, (n,)),
-         n, nb, bs, hkv, d, kv_scale)
+         n, nb, bs, hkv, d, float(kv_scale))
 
 
 def pa_gather_kvcache_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -451,7 +452,7 @@ def pa_gather_kvcache_fp4(k_cache: torch.Tensor, v_cache: torch.Tensor,
          _arg(k_cache, torch.uint8, "k_cache", dev, k_cache.shape),
          _arg(v_cache, torch.uint8, "v_cache", dev, k_cache.shape),
          _arg(slot_mapping, torch.int32, "slot_mapping", dev, (n,)),
-         n, nb, bs, hkv, d, kv_scale)
+         n, nb, bs, hkv, d, float(kv_scale))
     return key, value
 
 
@@ -509,6 +510,7 @@ def pa_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     nb, hkv, bs, d = _fp4_shape(k_cache, "pa_decode_fp4")
     batch, heads, _ = q.shape
     width = block_table.shape[-1]
+    max_seq_len, sliding_window = int(max_seq_len), int(sliding_window)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     new = _fp4_new_tokens(key, value, slot_mapping, batch, hkv, d, dev, "pa_decode_fp4")
@@ -522,7 +524,7 @@ def pa_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
          _arg(v_cache, torch.uint8, "v_cache", dev, k_cache.shape),
          _arg(block_table, torch.int32, "block_table", dev, (batch, width)), width,
          _arg(seq_lens, torch.int32, "seq_lens", dev, (batch,)), batch, max_seq_len, nb, bs, heads,
-         hkv, d, sliding_window, scale, kv_scale, ws, ws_bytes)
+         hkv, d, sliding_window, float(scale), float(kv_scale), ws, ws_bytes)
     return out
 
 
@@ -544,6 +546,8 @@ def pa_varlen_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     total_q, heads, _ = q.shape
     n = cu_seqlens_q.shape[0] - 1
     width = block_table.shape[-1]
+    max_seqlen_q, max_seqlen_k = int(max_seqlen_q), int(max_seqlen_k)
+    sliding_window = int(sliding_window)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     new = _fp4_new_tokens(key, value, slot_mapping, total_q, hkv, d, dev, "pa_varlen_prefill_fp4")
@@ -560,8 +564,8 @@ def pa_varlen_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
          _arg(cu_seqlens_k, torch.int32, "cu_seqlens_k", dev, (n + 1,)),
          None if seq_lens is None else _arg(seq_lens, torch.int32, "seq_lens", dev, (n,)),
          _arg(block_table, torch.int32, "block_table", dev, (n, width)), width, n, total_q,
-         max_seqlen_q, max_seqlen_k, nb, bs, heads, hkv, d, sliding_window, scale, kv_scale, ws,
-         ws_bytes)
+         max_seqlen_q, max_seqlen_k, nb, bs, heads, hkv, d, sliding_window, float(scale),
+         float(kv_scale), ws, ws_bytes)
     return out
 
 

@@ -78,7 +78,7 @@ class Case:
     def decode(self, window=0, **kw):
         kw = dict(kw) if "q" in kw else {**self.device(), **kw}
         return pa.pa_decode_fp4(kw.pop("q"), kw.pop("k_cache"), kw.pop("v_cache"), kw.pop("block_table"),
-                                kw.pop("seq_lens"), max(int(self.lens.max()), 0), self.scale, self.kv_scale, window, **kw)
+                                kw.pop("seq_lens"), max(self.lens.max(), np.int64(0)), self.scale, self.kv_scale, window, **kw)
 
     def prefill(self, window=0, lens=True, cu_k=False, expand=True, **kw):
         """expand False: a workspace without room for the expanded keys, so that every query block
@@ -465,6 +465,38 @@ def test_prefill_wait_limit_runs_out_then_device_is_usable(cuda):
         pa.pa_debug_prefill_stall(False, 0)
     assert flags & pa.DEVERR_TIMEOUT
     c.check(c.prefill())
+
+
+def test_caches_beyond_four_gigabytes(cuda):
+    # Every block of the step lies past byte 2^32 of both caches.
+    c = Case(cuda, [300, 20, 0], [1, 200, 1], 8, 8, 128, seed=27)
+    nb, row = c.kc.shape[0], 8 * 16 * 72
+    first = (2 ** 32 + row) // row + 1
+    big = [torch.empty(first + nb, 8, 16, 72, dtype=torch.uint8, device=cuda) for _ in range(2)]
+    for b, h in zip(big, (c.kc, c.vc)):
+        b[first:] = torch.from_numpy(h).to(cuda)
+    x = c.device()
+    x |= {"k_cache": big[0], "v_cache": big[1], "block_table": torch.where(x["block_table"] >= 0, x["block_table"] + first, -1)}
+    new = c.new_tokens()
+    new["slot_mapping"] = new["slot_mapping"] + first * 16
+    for expand in (True, False):
+        out = c.prefill(expand=expand, **x, **new)
+    c.store()
+    for b, h in zip(big, (c.kc, c.vc)):
+        np.testing.assert_array_equal(b[first:].cpu().numpy(), h)
+    c.check(out)
+    key, value = pa.pa_gather_kvcache_fp4(*big, new["slot_mapping"], KVS)
+    want = pa.pa_gather_kvcache_fp4(big[0][first:], big[1][first:], _t(c.slots, cuda), KVS)
+    assert torch.equal(key, want[0]) and torch.equal(value, want[1])
+    # The decode of the first and last sequence.
+    rows = [0, 2]
+    d = Case.__new__(Case)
+    d.__dict__ = dict(c.__dict__)
+    d.q, d.key, d.value = (t[[int(c.cu[i]) for i in rows]] for t in (c.q, c.key, c.value))
+    d.lens, d.new, d.table, d.cu = c.lens[rows], c.new[rows], c.table[rows], np.array([0, 1, 2], np.int32)
+    y = d.device() | {"k_cache": big[0], "v_cache": big[1]}
+    y["block_table"] = torch.where(y["block_table"] >= 0, y["block_table"] + first, -1)
+    d.check(d.decode(**y))
 
 
 # ------------------------------------------------------ streams and graphs ---
