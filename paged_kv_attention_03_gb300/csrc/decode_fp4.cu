@@ -43,14 +43,18 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kWarps = 4;          // independent warps of a block
-constexpr int kCtas1 = 3, kCtas2 = 2;  // resident blocks an SM with one and two n-tiles of heads
+// Independent warps of a block, one block an SM: 168 registers a thread with one n-tile of heads
+// (12 warps), 255 with two (8 warps).  (As three blocks of four warps an SM the same kernel took 133
+// us for 128.5, 8 x 81920 keys, 40/8 heads: the schedulers prefer an older block's warps, so of
+// equal ranges the last block's ended at 121 us where the first one's did at 93, and ran alone
+// at the end; the warps of one block end together.)
+__host__ __device__ constexpr int warps_of(int nt) { return nt == 1 ? 12 : 8; }
+constexpr int kScan = 128;         // threads that add up the sequences' units
 constexpr int kUnit = 32;          // keys of a unit: two 16-key halves
 constexpr int kStages = 3;         // ring stages of a warp, one unit of K and V each
 constexpr int kMinUnits = 4;       // smallest range of a warp (128 keys)
 constexpr int kWholeUnits = 5;     // spans up to this many units are never cut
 constexpr int kMergeWarps = 8;     // warps of a combine block
-
 struct Params {
     __nv_bfloat16 *out;
     const __nv_bfloat16 *q;
@@ -217,23 +221,24 @@ __device__ __forceinline__ void split_body(const Params &p) {
     constexpr int MT = D / 16;          // m-tiles of O^T
 
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ Ahead s_ahead[kWarps];
-    __shared__ long long part_sum[kWarps * 32];
+    __shared__ Ahead s_ahead[warps_of(NT)];
+    __shared__ long long part_sum[kScan];
     __shared__ long long s_total;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
     const int HT = p.num_kv_heads * p.head_tiles;  // segments of a sequence
+    constexpr int kWarps = warps_of(NT);
     const uint32_t ring = smem_u32(smem) + warp * kStages * SB;
     const uint64_t policy = l2_policy_evict_first();
 
     // ---- this warp's range [f, f_end) of the flat unit list ----
-    // Worker w of warp v of block c is v * blocks + c: few workers spread over many SMs.
+    // Worker v * blocks + c is warp v of block c: few workers spread over many SMs.
     const int w = warp * gridDim.x + blockIdx.x;
-    const int chunk = (p.batch + kWarps * 32 - 1) / (kWarps * 32);
+    const int chunk = (p.batch + kScan - 1) / kScan;
     const bool report = blockIdx.x == 0;
-    {
+    if (threadIdx.x < kScan) {
         long long sum = 0;
         const int b0 = threadIdx.x * chunk, b1 = min(p.batch, b0 + chunk);
         if (p.whole_units == 0 || report)
@@ -265,7 +270,6 @@ __device__ __forceinline__ void split_body(const Params &p) {
     __syncthreads();
 
     long long f, f_end;       // flat range
-    long long range = 0;      // R: units a worker
     Segment seg;              // segment at f
     int unit = 0;             // f's unit in it
     const int n_seg = p.batch * HT;
@@ -276,7 +280,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
         seg.b = w / HT;
     } else {
         const long long total = s_total * HT;
-        range = range_of(p, total);
+        const long long range = range_of(p, total);
         f = min(total, range * w);
         f_end = min(total, f + range);
     }
@@ -350,6 +354,28 @@ __device__ __forceinline__ void split_body(const Params &p) {
         }
     }
     if (todo == 0) return;
+
+    // Q^T fragments of a segment: the B operand of S^T.  k-step ks is dims D / 4 t + 4 ks .. + 3;
+    // head 8 j + g.  Heads past the group are zero.
+    uint32_t qf[NT][KSTEPS][2];
+    auto load_q = [&]() {
+        const int rows_valid = min(16, p.group - seg.ht * 16);
+        const int64_t row = p.q_rows != nullptr ? p.q_rows[seg.b] : seg.b;
+        const __nv_bfloat16 *qb = p.q + (row * p.num_heads + seg.kvh * p.group + seg.ht * 16) * D;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < KSTEPS / 2; ++c) {
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (8 * j + g < rows_valid)
+                    x = __ldg(reinterpret_cast<const uint4 *>(qb + (8 * j + g) * D + D / 4 * t) + c);
+                qf[j][2 * c][0] = bf16x2_to_f16x2(x.x);
+                qf[j][2 * c][1] = bf16x2_to_f16x2(x.y);
+                qf[j][2 * c + 1][0] = bf16x2_to_f16x2(x.z);
+                qf[j][2 * c + 1][1] = bf16x2_to_f16x2(x.w);
+            }
+    };
+    load_q();  // in flight beside the block table
 
     // ---- the issue side: units ahead of the consumer, across segments ----
     // Its place is kept in shared memory: it is needed once for 16 units.  In registers are the
@@ -427,26 +453,6 @@ __device__ __forceinline__ void split_body(const Params &p) {
     for (int s = 0; s < kStages - 1; ++s) issue(s);
 
     // ---- the consumer side ----
-    // Q^T fragments of a segment: the B operand of S^T.  k-step ks is dims D / 4 t + 4 ks .. + 3;
-    // head 8 j + g.  Heads past the group are zero.
-    uint32_t qf[NT][KSTEPS][2];
-    auto load_q = [&]() {
-        const int rows_valid = min(16, p.group - seg.ht * 16);
-        const int64_t row = p.q_rows != nullptr ? p.q_rows[seg.b] : seg.b;
-        const __nv_bfloat16 *qb = p.q + (row * p.num_heads + seg.kvh * p.group + seg.ht * 16) * D;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int c = 0; c < KSTEPS / 2; ++c) {
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (8 * j + g < rows_valid)
-                    x = __ldg(reinterpret_cast<const uint4 *>(qb + (8 * j + g) * D + D / 4 * t) + c);
-                qf[j][2 * c][0] = bf16x2_to_f16x2(x.x);
-                qf[j][2 * c][1] = bf16x2_to_f16x2(x.y);
-                qf[j][2 * c + 1][0] = bf16x2_to_f16x2(x.z);
-                qf[j][2 * c + 1][1] = bf16x2_to_f16x2(x.w);
-            }
-    };
     // O^T accumulators: tile i of 16 rows: row g is dim VD g + 2 i, row g + 8 dim VD g + 2 i + 1;
     // columns (heads) 8 j + 2 t and + 1.
     float o[NT][MT][4];
@@ -463,7 +469,6 @@ __device__ __forceinline__ void split_body(const Params &p) {
             m_run[j][0] = m_run[j][1] = -INFINITY;
         }
     };
-    load_q();
     reset();
     int first_unit = unit;  // first unit of the segment's piece in this range
 
@@ -724,7 +729,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? kCtas1 : kCtas2)
+__global__ void __launch_bounds__(warps_of(NT) * 32, 1)
     decode_fp4_split_kernel(const __grid_constant__ Params p) {
     griddep_launch_dependents();
     split_body<D, NT>(p);
@@ -876,6 +881,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_fp4_combine_kernel(co
 
 template <int D, int NT>
 cudaError_t launch_d(const Params &p, int blocks, bool combine, cudaStream_t stream) {
+    constexpr int kWarps = warps_of(NT);
     constexpr int smem = kWarps * kStages * 2 * kUnit * fp4::row_bytes(D);
     static std::atomic<uint64_t> smem_set;
     auto kern = decode_fp4_split_kernel<D, NT>;
@@ -921,14 +927,15 @@ bool plan_decode_fp4(int batch, int num_heads, int num_kv_heads, int head_dim, i
     // Whole segments when they are short: one launch and no merge.
     p.whole = units <= kWholeUnits;
     const int64_t want = p.whole ? segments : (segments * units + kMinUnits - 1) / kMinUnits;
-    int64_t blocks = (want + kWarps - 1) / kWarps;
-    const int64_t resident = static_cast<int64_t>(kPlanSms) * (p.group > 8 ? kCtas2 : kCtas1);
-    if (!p.whole && blocks > resident) blocks = resident;
+    const int warps = warps_of(p.group > 8 ? 2 : 1);
+    // One block an SM, on as many SMs as there is work for; beyond that only whole segments.
+    int64_t blocks = want < kPlanSms ? want : kPlanSms;
+    if (p.whole && want > static_cast<int64_t>(kPlanSms) * warps) blocks = (want + warps - 1) / warps;
     if (blocks < 1) blocks = 1;
-    if (blocks > 0x7fffffffLL / kWarps) return false;
+    if (blocks > 0x7fffffffLL / warps) return false;
     if (segments * units / blocks > 0x3fffffff) return false;  // a warp counts its units in 32 bits
     p.blocks = static_cast<int>(blocks);
-    p.workers = p.blocks * kWarps;
+    p.workers = p.blocks * warps;
     if (!p.whole) {
         p.workspace_bytes = static_cast<size_t>(p.workers) * 2 * p.tile_heads * (head_dim + 2) * sizeof(float);
     }

@@ -152,7 +152,7 @@ struct DecodeArgs {
 };
 cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStream_t stream);
 
-// Decode over the 4-bit cache (decode_fp4.cu): `blocks` blocks of four warps share the units
+// Decode over the 4-bit cache (decode_fp4.cu): `blocks` blocks share the units
 // of all sequences evenly; whole: each warp takes one whole (sequence, head tile).
 struct DecodeFp4Plan {
     int group;
