@@ -55,6 +55,7 @@ constexpr int kStages = 3;         // ring stages of a warp, one unit of K and V
 constexpr int kMinUnits = 4;       // smallest range of a warp (128 keys)
 constexpr int kWholeUnits = 5;     // spans up to this many units are never cut
 constexpr int kMergeWarps = 8;     // warps of a combine block
+
 struct Params {
     __nv_bfloat16 *out;
     const __nv_bfloat16 *q;
@@ -732,6 +733,9 @@ template <int D, int NT>
 __global__ void __launch_bounds__(warps_of(NT) * 32, 1)
     decode_fp4_split_kernel(const __grid_constant__ Params p) {
     griddep_launch_dependents();
+    // Always launched as a programmatic dependent, so that its launch overlaps the end of whatever
+    // precedes it on the stream; beside a prefill it starts at once, else it waits here.
+    if (!p.after_prefill) griddep_wait();
     split_body<D, NT>(p);
     // As a programmatic dependent of the prefill kernel of the same call, this grid (and what
     // waits for it) completes after the prefill: its last block waits for the prefill grid.
@@ -781,6 +785,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_fp4_combine_kernel(co
     }
     const long long range = range_of(p, total * HT);
     int units = b < p.batch ? max(seq_units(p, b, r, false), 0) : 0;
+    griddep_launch_dependents();
     int share = kMergeWarps;  // warps an item
     while (share > 1 && share * per_block > kMergeWarps) share >>= 1;
     const int per_round = kMergeWarps / share;
@@ -896,7 +901,7 @@ cudaError_t launch_d(const Params &p, int blocks, bool combine, cudaStream_t str
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = p.after_prefill ? 1 : 0;
+    cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kern, p);
     if (e != cudaSuccess || !combine) return e;
     cfg.gridDim = dim3(2 * kPlanSms);

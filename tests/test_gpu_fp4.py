@@ -537,6 +537,54 @@ def test_decode_in_a_graph_follows_its_lengths(cuda):
         c.check(out)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_decode_waits_for_what_precedes_it(cuda, captured):
+    # Its inputs come from a copy, a kernel and another stream's kernels right before it; two calls
+    # in a row share a workspace.
+    c = Case(cuda, [300, 1000, 50, 9], [1] * 4, 32, 8, 128, seed=33)
+    d = Case(cuda, [900, 10, 500, 70], [1] * 4, 32, 8, 128, seed=34)
+    x, y = c.device(), d.device()
+    want = [c.decode(**x), d.decode(**y)]
+    ws = torch.empty(pa.pa_decode_fp4_workspace_size(4, 32, 8, 128, 1001), dtype=torch.uint8, device=cuda)
+    q, lens, table = torch.empty_like(x["q"]), torch.empty_like(x["seq_lens"]), torch.empty_like(x["block_table"])
+    out = [torch.empty_like(q), torch.empty_like(q)]
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    main.wait_stream(torch.cuda.current_stream())
+
+    def step():
+        if not captured:
+            torch.cuda._sleep(2_000_000)
+        q.zero_()
+        lens.copy_(x["seq_lens"])
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.mul(x["q"], 1, out=q)
+            table.copy_(x["block_table"])
+        torch.cuda.current_stream().wait_stream(side)
+        c.decode(**{**x, "q": q, "seq_lens": lens, "block_table": table}, out=out[0], workspace=ws)
+        d.decode(**y, out=out[1], workspace=ws)
+        lens.zero_()
+        table.fill_(-1)
+        q.fill_(float("nan"))
+
+    with torch.cuda.stream(main):
+        step()
+        if captured:
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=main):
+                step()
+    for _ in range(5):
+        with torch.cuda.stream(main):
+            for o in out:
+                o.fill_(0)
+            graph.replay() if captured else step()
+            got = [o.clone() for o in out]
+        torch.cuda.synchronize()
+        assert pa.pa_read_device_error(device=cuda) == 0
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_a_serving_loop(cuda):
     """Lengths -> tables and slots -> prefill with its store -> decode steps -> release, one run
     of them together; every step's outputs against the oracle on the oracle's own cache."""
