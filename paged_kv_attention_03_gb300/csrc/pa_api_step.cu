@@ -38,9 +38,10 @@ pa_status check_fp4_cache(int64_t num_blocks, int block_size, int num_kv_heads, 
 }
 
 // Sizes shared by decode and prefill.
-pa_status check_fp4_heads(int num_heads, int num_kv_heads, float scale) {
+pa_status check_fp4_heads(int num_heads, int num_kv_heads, float scale, float kv_scale) {
     if (num_heads <= 0 || num_heads % num_kv_heads != 0) return PA_ERR_INVALID_ARG;
-    if (!(scale > 0.f) || !(scale < 3.0e38f)) return PA_ERR_INVALID_ARG;
+    // (scale * kv_scale * log2 e is one factor in the kernels.)
+    if (!(scale > 0.f) || !(scale * kv_scale < 1.0e38f)) return PA_ERR_INVALID_ARG;
     if (num_heads / num_kv_heads > 64) return PA_ERR_UNSUPPORTED;
     return PA_OK;
 }
@@ -192,7 +193,7 @@ pa_status pa_decode_fp4(void *out, const void *q, const void *key, const void *v
     if (batch < 0 || max_seq_len < 0 || max_num_blocks < 0) return PA_ERR_INVALID_ARG;
     if (max_seq_len > kMostKeys) return PA_ERR_UNSUPPORTED;
     pa_status st = check_fp4_cache(num_blocks, block_size, num_kv_heads, head_dim, kv_scale);
-    if (st == PA_OK) st = check_fp4_heads(num_heads, num_kv_heads, scale);
+    if (st == PA_OK) st = check_fp4_heads(num_heads, num_kv_heads, scale, kv_scale);
     if (st != PA_OK) return st;
     if (batch > 65535) return PA_ERR_UNSUPPORTED;
     const bool has_new = key || value || slot_mapping;
@@ -259,7 +260,7 @@ pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const
         return PA_ERR_INVALID_ARG;
     if (max_seqlen_k > kMostKeys) return PA_ERR_UNSUPPORTED;
     pa_status st = check_fp4_cache(num_blocks, block_size, num_kv_heads, head_dim, kv_scale);
-    if (st == PA_OK) st = check_fp4_heads(num_heads, num_kv_heads, scale);
+    if (st == PA_OK) st = check_fp4_heads(num_heads, num_kv_heads, scale, kv_scale);
     if (st != PA_OK) return st;
     if (max_seqlen_q > max_seqlen_k) return PA_ERR_INVALID_ARG;
     if (num_seqs > 65535 || total_q > 0x7fffff00) return PA_ERR_UNSUPPORTED;

@@ -17,6 +17,9 @@
 // entry.  What a caller may update in place (lengths, the free count) is written when no
 // block reads it any more: by the same block when there is one, else by a second launch, a
 // programmatic dependent that repeats the scan while the first runs.
+//
+// Measured (serialised): 64 decodes 7.5 us in one launch; 2033 requests with 526k slots 10 + 5 us
+// (a call from Python takes the host 9-11); the release of half of 1024 requests 6.5 + 4.5 us.
 #include <algorithm>
 
 #include "pa_common.cuh"

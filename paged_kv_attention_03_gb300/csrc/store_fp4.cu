@@ -10,6 +10,9 @@
 // One thread takes one group of 16 dims of K and of V (32 bytes each of bf16, 8 bytes of
 // codes): the groups of a row sit in consecutive lanes, so a row is written as one contiguous
 // run, its scales gathered by shuffles and written by the row's first lane.
+//
+// Measured on 17403 tokens of 8 heads of 128 (91 MB each way): store 18.3 us (5.0 TB/s; issue
+// slots 68 % busy, the quantisation), gather 14.3 us (6.4 TB/s, the rate of a copy).
 #include "fp4.cuh"
 #include "pa_internal.h"
 #include "sm100_ptx.cuh"

@@ -104,6 +104,8 @@ def test_attention_refusals(lib, call):
     assert call(lib, bs=8) == UNSUPPORTED
     assert call(lib, scale=0.0) == INVALID
     assert call(lib, scale=float("nan")) == INVALID
+    assert call(lib, scale=float("inf")) == INVALID
+    assert call(lib, scale=1e20, kvs=1e20) == INVALID
     assert call(lib, kvs=0.0) == INVALID
     assert call(lib, key=FAKE) == INVALID
     assert call(lib, q=None) == INVALID
