@@ -1285,6 +1285,7 @@ __global__ void __launch_bounds__(kExpandThreads)
     expand_fp4_kernel(const PrefillKernelParams p, uint4 *__restrict__ k_out, uint4 *__restrict__ v_out) {
     constexpr int GROUPS = HD / 16;
     constexpr int RB = fp4::row_bytes(HD);
+    griddep_wait();  // a programmatic dependent of whatever precedes it: its launch overlaps that
     const int seq = blockIdx.y;
     const int q_start = p.cu_q[seq], sq = p.cu_q[seq + 1] - q_start;
     int sk = p.seq_lens != nullptr ? p.seq_lens[seq] : p.cu_k[seq + 1] - p.cu_k[seq];
@@ -1455,8 +1456,17 @@ cudaError_t launch_expanded(PrefillKernelParams &kp, const PrefillArgs &a, cudaS
     uint8_t *k16 = static_cast<uint8_t *>(a.scratch), *v16 = k16 + half;
     kp.expanded_blocks = (a.max_seqlen_k + a.block_size - 1) / a.block_size;
     const dim3 grid((a.max_seqlen_k + expand_keys<HD>() - 1) / expand_keys<HD>(), a.num_seqs);
-    expand_fp4_kernel<HD><<<grid, kExpandThreads, 0, stream>>>(kp, reinterpret_cast<uint4 *>(k16), reinterpret_cast<uint4 *>(v16));
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kExpandThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, expand_fp4_kernel<HD>, kp, reinterpret_cast<uint4 *>(k16),
+                                             reinterpret_cast<uint4 *>(v16));
     if (e != cudaSuccess) return e;
     PrefillArgs x = a;
     x.k_cache = k16;

@@ -585,6 +585,50 @@ def test_decode_waits_for_what_precedes_it(cuda, captured):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@both
+@pytest.mark.parametrize("captured", [False, True])
+def test_prefill_waits_for_what_precedes_it(cuda, captured, expand):
+    # The cache and the tables arrive by copies right before the call and are wiped right after it;
+    # calls in a row share the workspace and its scratch cache.
+    c = Case(cuda, [300, 0, 50, 9], [200, 300, 1, 33], 8, 2, 128, seed=35)
+    x = c.device()
+    most = 768 if expand else 300
+    cu = _t(c.cu, cuda)
+    need = pa.pa_varlen_prefill_fp4_workspace_size(4, 8, 2, 128, 768) if expand else \
+        pa.pa_decode_fp4_workspace_size(4, 8, 2, 128, 768)
+    ws = torch.empty(need, dtype=torch.uint8, device=cuda)
+    y = {k: torch.empty_like(v) for k, v in x.items()}
+    out = torch.empty_like(x["q"])
+
+    def step():
+        if not captured:
+            torch.cuda._sleep(1_000_000)
+        for k in x:
+            y[k].copy_(x[k])
+        for _ in range(2):
+            pa.pa_varlen_prefill_fp4(y["q"], y["k_cache"], y["v_cache"], cu, y["seq_lens"], y["block_table"], most, 768,
+                                     c.scale, c.kv_scale, out=out, workspace=ws)
+        for k in ("k_cache", "v_cache", "q"):
+            y[k].zero_()
+        y["block_table"].fill_(-1)
+
+    main = torch.cuda.Stream()
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main):
+        step()
+        torch.cuda.synchronize()
+        c.check(out)
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=main):
+                step()
+        for _ in range(3):
+            out.fill_(float("nan"))
+            graph.replay() if captured else step()
+        torch.cuda.synchronize()
+    c.check(out)
+
+
 def test_a_serving_loop(cuda):
     """Lengths -> tables and slots -> prefill with its store -> decode steps -> release, one run
     of them together; every step's outputs against the oracle on the oracle's own cache."""
