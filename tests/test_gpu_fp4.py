@@ -86,7 +86,7 @@ class Case:
         the keys are expanded beforehand whatever the lengths."""
         x = dict(kw) if "q" in kw else {**self.device(), **kw}
         sl = x.pop("seq_lens")
-        most = 128 * 6 if expand else int(self.new.max())
+        most = max(128 * 6 if expand else 0, int(self.new.max()))
         if not expand:
             need = pa.pa_decode_fp4_workspace_size(len(self.lens), self.heads, self.kc.shape[1], self.dim, int(self.lens.max()),
                                                    window)
