@@ -405,9 +405,9 @@ pa_status pa_varlen_prefill_fp8(void *out, const void *q, const void *key, const
  * tokens without a block get slot -1, and seq_lens[i] ends with the last block the request
  * holds (less than c_i + q_i: the caller's sign to preempt it; the attention of such a
  * request in this step is not meaningful).  Negative or too long lengths are clamped to the
- * row and flagged PA_DEVERR_SEQ_RANGE / PA_DEVERR_QUERY_LEN (more than max_tokens tokens
- * too; cu_seqlens_q then ends at max_tokens); bad block ids give -1 and
- * PA_DEVERR_BLOCK_RANGE.
+ * row and flagged PA_DEVERR_SEQ_RANGE / PA_DEVERR_QUERY_LEN.  More than max_tokens tokens are
+ * cut there, under the latter flag: every output is that of requests whose new tokens end at
+ * max_tokens.  Bad block ids give -1 and PA_DEVERR_BLOCK_RANGE.
  * Supported: block_size a power of two in [1, 1024]; num_seqs <= 16384; num_blocks *
  * block_size and max_tokens below 2^31.  No workspace.
  *

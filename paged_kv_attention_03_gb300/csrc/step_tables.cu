@@ -18,8 +18,9 @@
 // block reads it any more: by the same block when there is one, else by a second launch, a
 // programmatic dependent that repeats the scan while the first runs.
 //
-// Measured (serialised): 64 decodes 7.5 us in one launch; 2033 requests with 526k slots 10 + 5 us
-// (a call from Python takes the host 9-11); the release of half of 1024 requests 6.5 + 4.5 us.
+// Measured (replayed from a graph): 64 decodes 4.7 us in one launch; 2033 requests with 526k
+// slots 8.9 us in two; the release of a seventh of 64 requests 4.4 us, of half of 1024 6.2 (a call
+// from Python takes the host 9-11 us).
 #include <algorithm>
 
 #include "pa_common.cuh"
@@ -56,17 +57,22 @@ __device__ __forceinline__ uint32_t cached(const StepArgs &a, int i) {
     return min(static_cast<uint32_t>(max(a.context_lens[i], 0)), table_cap(a));
 }
 
+// New blocks of a request with c cached and q new tokens.
+__device__ __forceinline__ uint32_t new_blocks(const StepArgs &a, uint32_t c, uint32_t q) {
+    const uint32_t up = (1u << a.log2_bs) - 1u;
+    const uint32_t len = min(c + q, table_cap(a));  // below 2^32
+    return ((len + up) >> a.log2_bs) - ((c + up) >> a.log2_bs);
+}
+
 template <bool PREPARE>
 __device__ __forceinline__ Need need_of(const StepArgs &a, int i, bool report) {
     Need n;
     const uint32_t cap = table_cap(a);
-    const uint32_t up = (1u << a.log2_bs) - 1u;
     if constexpr (PREPARE) {
         const int c_raw = a.context_lens[i], q_raw = a.query_lens[i];
         const uint32_t c = cached(a, i);
         n.items = static_cast<uint32_t>(max(q_raw, 0));
-        const uint32_t len = min(c + n.items, cap);  // below 2^32
-        n.blocks = ((len + up) >> a.log2_bs) - ((c + up) >> a.log2_bs);
+        n.blocks = new_blocks(a, c, n.items);
         if (report) {
             if (c_raw < 0 || static_cast<uint32_t>(c_raw) > cap || c + n.items > cap)
                 flag_error(a.err, kErrSeqRange);
@@ -76,7 +82,7 @@ __device__ __forceinline__ Need need_of(const StepArgs &a, int i, bool report) {
         const int raw = a.seq_lens[i];
         const bool done = a.finished[i] != 0;
         const uint32_t len = min(static_cast<uint32_t>(max(raw, 0)), cap);
-        n.items = done ? (len + up) >> a.log2_bs : 0u;
+        n.items = done ? (len + (1u << a.log2_bs) - 1u) >> a.log2_bs : 0u;
         n.blocks = 0;
         if (report && done && (raw < 0 || static_cast<uint32_t>(raw) > cap)) flag_error(a.err, kErrSeqRange);
     }
@@ -140,6 +146,26 @@ __device__ __forceinline__ void scan(const StepArgs &a, uint32_t *items, uint32_
         if (PREPARE) blocks[n] = eb;
     }
     __syncthreads();
+    // More tokens than max_tokens: what is beyond is no token of any request, so that no block is
+    // taken for it (a flagged call, its second sum is left to one thread).
+    const uint32_t most = static_cast<uint32_t>(a.max_tokens);
+    if (PREPARE && items[n] > most) {
+        for (int i = threadIdx.x; i < n; i += kThreads)
+            blocks[i] = new_blocks(a, cached(a, i), min(items[i + 1], most) - min(items[i], most));
+        __syncthreads();
+        for (int i = threadIdx.x; i <= n; i += kThreads) items[i] = min(items[i], most);
+        if (threadIdx.x == 0) {
+            uint32_t sum = 0;
+            for (int i = 0; i < n; ++i) {
+                const uint32_t x = blocks[i];
+                blocks[i] = sum;
+                sum = add_sat(sum, x);
+            }
+            blocks[n] = sum;
+            if (report) flag_error(a.err, kErrQueryLen);
+        }
+        __syncthreads();
+    }
 }
 
 // The last request whose first item is at or before k (k below the total): the one that holds k.
@@ -191,7 +217,7 @@ __device__ __forceinline__ void tokens(const StepArgs &a, const uint32_t *cu, co
             slot[j] = -1;  // past the last token: padding
             posv[j] = 0;
             const int64_t tt = t0 + j;
-            if (tt >= total || tt >= a.max_tokens) continue;
+            if (tt >= total) continue;
             const uint32_t t = static_cast<uint32_t>(tt);
             if (seq < 0 || t >= end) {
                 // Often the next request; else (empty ones between) search again.
@@ -240,25 +266,23 @@ __device__ __forceinline__ void publish_prepare(const StepArgs &a, const uint32_
     const uint32_t nfree = free_count(a, true);
     const uint32_t up = (1u << a.log2_bs) - 1u;
     const uint32_t cap = table_cap(a);
-    const uint32_t most = static_cast<uint32_t>(min(a.max_tokens, static_cast<int64_t>(kTop)));
     const uint32_t used = min(n > 0 ? off[n] : 0u, nfree);
     if (threadIdx.x == 0) {
         if (n > 0 && off[n] > nfree) flag_error(a.err, kErrNoBlocks);
-        if (n > 0 && cu[n] > most) flag_error(a.err, kErrQueryLen);
-        a.cu_seqlens_q[n] = n > 0 ? static_cast<int>(min(cu[n], most)) : 0;
+        a.cu_seqlens_q[n] = n > 0 ? static_cast<int>(cu[n]) : 0;
     }
     __syncthreads();  // the count has been read by all (num_free_out may be num_free)
     if (threadIdx.x == 0) *a.num_free_out = static_cast<int>(nfree - used);
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const uint32_t c = cached(a, i);
-        uint32_t len = min(c + static_cast<uint32_t>(max(a.query_lens[i], 0)), cap);
+        uint32_t len = min(c + (cu[i + 1] - cu[i]), cap);
         // Out of blocks: the sequence ends where its last block does.
         const uint32_t have = (c + up) >> a.log2_bs;
         const uint32_t got = off[i] < nfree ? nfree - off[i] : 0u;
         const uint64_t room = static_cast<uint64_t>(have + static_cast<uint64_t>(got)) << a.log2_bs;
         if (room < len) len = static_cast<uint32_t>(room);
         a.seq_lens_out[i] = static_cast<int>(len);
-        a.cu_seqlens_q[i] = static_cast<int>(min(cu[i], most));
+        a.cu_seqlens_q[i] = static_cast<int>(cu[i]);
     }
 }
 

@@ -124,6 +124,39 @@ def test_prepare_clamps_bad_lengths(cuda):
     assert cu.tolist() == [0, 6, 10, 10] and len(slots) == 10
 
 
+@pytest.mark.parametrize("n,high,max_tokens", [(3, 9, 0), (3, 40, 10), (40, 60, 5), (40, 200, 3000), (5000, 3, 100),
+                                               (16384, 3, 6000), (200, 300, 2048)])
+def test_prepare_cuts_at_max_tokens(cuda, n, high, max_tokens):
+    # Tokens beyond the capacity are nobody's: no length, table entry or free block counts them.
+    rng = np.random.default_rng(n + max_tokens)
+    ctx, q = rng.integers(0, 100, n), rng.integers(1, high + 1, n)
+    end = np.minimum(np.cumsum(q), max_tokens)
+    cut = np.diff(end, prepend=0)
+    assert cut.sum() == max_tokens < q.sum()
+    table, free, nf = _state(ctx, 16, 30, 6000, 1)
+    want = fp4.prepare_step(ctx, cut, table, free, nf, 16, max_tokens)
+    bt = _t(table, cuda)
+    got = pa.pa_prepare_step(_t(ctx, cuda), _t(q, cuda), bt, _t(free, cuda), _t([nf], cuda), 16, max_tokens)
+    assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_QUERY_LEN
+    for name, g, w in zip(("seq_lens", "cu_seqlens_q", "slot_mapping", "positions"), got, want[1:]):
+        np.testing.assert_array_equal(g.cpu().numpy(), w, err_msg=name)
+    assert int(got[4]) == want[5]
+    np.testing.assert_array_equal(bt.cpu().numpy(), want[0])
+
+
+def test_prepare_sums_beyond_32_bits(cuda):
+    # Lengths whose sum passes 2^32, cut at the capacity; each is cut at its row as well.
+    bt = _t([[-1, -1], [60, 61], [-1, -1], [62, -1]], cuda)
+    free = torch.arange(70, dtype=torch.int32, device=cuda)
+    big = 2**31 - 1
+    lens, cu, slots, pos, nf = pa.pa_prepare_step(
+        _t([0, 20, 0, 5], cuda), _t([3, big, big, big], cuda), bt, free, _t([50], cuda), 16, 40)
+    assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_SEQ_RANGE | pa.DEVERR_QUERY_LEN
+    assert lens.tolist() == [3, 32, 0, 5] and cu.tolist() == [0, 3, 40, 40, 40] and nf.tolist() == [49]
+    assert slots.tolist() == [49 * 16 + i for i in range(3)] + [61 * 16 + i for i in range(4, 16)] + [-1] * 25
+    assert pos.tolist() == [0, 1, 2] + list(range(20, 57))
+
+
 def test_prepare_flags_bad_block_ids(cuda):
     # A bad id in the free list or in the table gives no slot, and no access.
     bt = torch.tensor([[99, -1], [-1, -1]], dtype=torch.int32, device=cuda)
