@@ -24,8 +24,8 @@
 //    72-byte rows, free of bank conflicts for V; and a lane ends up with consecutive dims of
 //    O for its heads, which it writes as whole vectors.
 //  * A segment inside one warp's range is finished there.  A cut one leaves (m, l, O) of each
-//    piece in the workspace and decode_fp4_combine_kernel (a programmatic dependent) merges
-//    them.  When no sequence can be longer than kWholeUnits units, ranges are whole segments
+//    piece in the workspace and decode_fp4_combine_kernel (a programmatic dependent, which may
+//    start as soon as the split kernel's inputs are complete) merges them.  When no sequence can be longer than kWholeUnits units, ranges are whole segments
 //    and no combine is launched.
 //
 // Measured: 8 sequences of 81920 keys, 40/8 heads, 128.5 us a call (755 MB, 5.9 TB/s); 64 of
@@ -101,12 +101,16 @@ struct Params {
 };
 
 // Units of sequence b and its key range: 0 without keys, -1 for a sequence that is not decoded here.
+// EARLY: read by a kernel that has not waited for what precedes it (the merge), from the L2, where
+// the writes that the split kernel waited for are.
+template <bool EARLY = false>
 __device__ __forceinline__ int seq_units(const Params &p, int b, SeqRange &r, bool report) {
+    auto load = [](const int32_t *at) { return EARLY ? __ldcg(at) : *at; };
     if (p.q_rows != nullptr) {
-        const int r0 = p.q_rows[b];
-        const int sq = p.q_rows[b + 1] - r0;
+        const int r0 = load(p.q_rows + b);
+        const int sq = load(p.q_rows + b + 1) - r0;
         if (report && p.check_rows) {
-            const int sk = p.seq_lens[b];
+            const int sk = load(p.seq_lens + b);
             if (sq < 0 || sq > p.max_seqlen_q || sq > sk) flag_error(p.err, kErrQueryLen);
             if (p.cu_k != nullptr && p.cu_k[b + 1] - p.cu_k[b] != sk) flag_error(p.err, kErrSeqlensK);
         }
@@ -116,7 +120,7 @@ __device__ __forceinline__ int seq_units(const Params &p, int b, SeqRange &r, bo
             return -1;
         }
     }
-    r = decode_range(p.seq_lens[b], p.seq_cap, p.window, 0, p.err, report);
+    r = decode_range(load(p.seq_lens + b), p.seq_cap, p.window, 0, p.err, report);
     return (r.L - r.base + kUnit - 1) / kUnit;
 }
 
@@ -738,10 +742,12 @@ __device__ __forceinline__ void split_body(const Params &p) {
 template <int D, int NT>
 __global__ void __launch_bounds__(warps_of(NT) * 32, 1)
     decode_fp4_split_kernel(const __grid_constant__ Params p) {
-    griddep_launch_dependents();
     // Always launched as a programmatic dependent, so that its launch overlaps the end of whatever
-    // precedes it on the stream; beside a prefill it starts at once, else it waits here.
+    // precedes it on the stream; beside a prefill (which itself began when all before it was
+    // complete) it starts at once, else it waits here.  The merge reads the lengths before it waits
+    // for this grid, so it is let in only behind this wait: what precedes the call may write them.
     if (!p.after_prefill) griddep_wait();
+    griddep_launch_dependents();
     split_body<D, NT>(p);
     // As a programmatic dependent of the prefill kernel of the same call, this grid (and what
     // waits for it) completes after the prefill: its last block waits for the prefill grid.
@@ -753,7 +759,8 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1)
 // hundred).  With piece i holding (m_i, l_i, O_i):
 //     M = max m_i,  out = kv_scale * sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 // Where a segment is cut follows from the lengths alone, so that is worked out before the wait
-// for the split grid; after it there is one round trip for eight pieces.
+// for the split grid (whose blocks have all passed theirs, so the lengths are the call's); after it
+// there is one round trip for eight pieces.
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) decode_fp4_combine_kernel(const __grid_constant__ Params p) {
     constexpr int PER = D / 32;
@@ -769,7 +776,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_fp4_combine_kernel(co
     SeqRange r;
     long long before = 0, total = 0;  // units of sequences before b, and of all
     for (int k = threadIdx.x; k < p.batch; k += kMergeWarps * 32) {
-        const int u = max(seq_units(p, k, r, false), 0);
+        const int u = max(seq_units<true>(p, k, r, false), 0);
         total += u;
         if (k < b) before += u;
     }
@@ -790,7 +797,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_fp4_combine_kernel(co
         total += sums[1][v];
     }
     const long long range = range_of(p, total * HT);
-    int units = b < p.batch ? max(seq_units(p, b, r, false), 0) : 0;
+    int units = b < p.batch ? max(seq_units<true>(p, b, r, false), 0) : 0;
     griddep_launch_dependents();
     int share = kMergeWarps;  // warps an item
     while (share > 1 && share * per_block > kMergeWarps) share >>= 1;
@@ -804,7 +811,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_fp4_combine_kernel(co
         const int bi = item < i1 ? static_cast<int>(s / HT) : b;
         while (b < bi) {
             before += units;
-            units = max(seq_units(p, ++b, r, false), 0);
+            units = max(seq_units<true>(p, ++b, r, false), 0);
         }
         const int hs = static_cast<int>(s - static_cast<int64_t>(b) * HT);
         const int kvh = hs / p.head_tiles, ht = hs - kvh * p.head_tiles;
