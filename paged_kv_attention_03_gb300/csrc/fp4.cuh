@@ -69,11 +69,12 @@ constexpr uint32_t kMinScale = 1;
 // an infinity saturates.
 //
 // The 16 quotients share their divisor d: with r the rounded reciprocal, q = x r and one
-// correction q + (x - q d) r by two fused operations give the rounded quotient (Markstein,
+// correction q - (q d - x) r by two fused operations give the rounded quotient (Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor", 1990, asks for
 // a q within one unit; here every 8-bit x against every 24-bit d was tried, and all 2^30
-// quotients are the rounded ones).  That scales by powers of two as long as x - q d keeps its
-// bits, which kv_scale >= 1e-25 sees to.  17403 tokens: 18.3 us against 23.5 with divisions.
+// quotients are the rounded ones).  That scales by powers of two as long as q d - x keeps its
+// bits, which kv_scale >= 1e-25 sees to.  Written this way round a zero keeps its sign: for
+// x = -0 the remainder is (-0) - (-0) = +0 and the sum (-0) + (-0); x - q d would add +0.  17403 tokens: 18.3 us against 23.5 with divisions.
 __device__ __forceinline__ uint2 quant_group(uint32_t (&w)[8], float kv_scale, float kv_scale6,
                                              uint32_t &scale_code) {
     // Magnitudes of bf16 order like their bit patterns, and a NaN's is above infinity's.
@@ -89,7 +90,8 @@ __device__ __forceinline__ uint2 quant_group(uint32_t (&w)[8], float kv_scale, f
     const float den = __fmul_rn(f16_lo(e4m3x2_to_f16x2(scale_code)), kv_scale);
     const float r = __frcp_rn(den);
     if (scale_code >= 126u) {
-        // Only a saturated scale leaves quotients beyond 6.5, up to infinity: those saturate too.
+        // Only a saturated scale leaves quotients beyond 9 (the smallest scales are coarse: 2^-9
+        // stands for up to 1.5 times itself), up to infinity: those saturate too.
         const __nv_bfloat162 most = __float2bfloat162_rn(8.f * den);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -99,7 +101,7 @@ __device__ __forceinline__ uint2 quant_group(uint32_t (&w)[8], float kv_scale, f
     }
     auto quotient = [&](float x) {
         const float q = __fmul_rn(x, r);
-        return __fmaf_rn(__fmaf_rn(-q, den, x), r, q);
+        return __fmaf_rn(-__fmaf_rn(q, den, -x), r, q);
     };
     uint32_t c[2] = {0u, 0u};
 #pragma unroll

@@ -666,3 +666,43 @@ def test_a_serving_loop(cuda):
         assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
     np.testing.assert_array_equal(d_lens.cpu().numpy(), lens)
     assert int(d_nf) == nf
+
+
+def test_store_keeps_the_sign_of_zero(cuda):
+    # -0.0 has code 8 wherever it stands: beside numbers, in a group of zeros, under a saturated
+    # scale; numbers that underflow keep their sign too.
+    x = torch.zeros(5, 2, 64)
+    x[:, 0] = -0.0
+    x[:, 1, ::2] = -0.0
+    x[0, :, 3], x[0, :, 20] = 6.0, -1.5
+    x[1, :, 7] = float("-inf")
+    x[2, :, 9], x[2, :, 41] = 3e38, -3e38
+    x[3, :, 1], x[3, :, 2] = -1e-38, 1e-38
+    x[4, 1, 16:32] = 5000.0
+    x = x.bfloat16()
+    for kv_scale in (1.0, KVS, 1e-25, 1e25):
+        host = np.zeros((1, 2, 16, 36), np.uint8)
+        fp4.store(x.double().numpy(), host, np.arange(5), kv_scale)
+        k = torch.zeros(1, 2, 16, 36, dtype=torch.uint8, device=cuda)
+        v = torch.zeros_like(k)
+        slots = torch.arange(5, dtype=torch.int32, device=cuda)
+        pa.pa_store_kvcache_fp4(x.to(cuda), x.to(cuda), k, v, slots, kv_scale)
+        np.testing.assert_array_equal(k.cpu().numpy(), host)
+        assert torch.equal(k, v) and host[0, 0, 4, 0] == 0x88
+        key, _ = pa.pa_gather_kvcache_fp4(k, v, slots, kv_scale)
+        rows = np.moveaxis(host[0, :, :5], 0, 1)
+        want = torch.from_numpy(fp4.expand(rows, kv_scale).astype(np.float32)).bfloat16()
+        assert torch.equal(key.cpu().view(torch.int16), want.view(torch.int16))
+
+
+def test_decode_stores_the_sign_of_zero(cuda):
+    # The stores inside the decode: a sequence's last key, and a row that no position owns.
+    c = Case(cuda, [40, 0], [1, 1], 8, 2, 128, seed=36)
+    c.key[:, :, ::3], c.value[:, :, 1::3] = -0.0, -0.0
+    x, new = c.device(), c.new_tokens()
+    x["seq_lens"][1] = 0
+    c.decode(**x, **new)
+    assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_SLOT_MISMATCH
+    c.store()
+    np.testing.assert_array_equal(x["k_cache"].cpu().numpy(), c.kc)
+    np.testing.assert_array_equal(x["v_cache"].cpu().numpy(), c.vc)
