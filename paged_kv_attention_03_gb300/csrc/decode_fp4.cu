@@ -379,7 +379,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
             for (int c = 0; c < KSTEPS / 2; ++c) {
                 uint4 x = make_uint4(0u, 0u, 0u, 0u);
                 if (8 * j + g < rows_valid)
-                    x = __ldg(reinterpret_cast<const uint4 *>(qb + (8 * j + g) * D + D / 4 * t) + c);
+                    x = reinterpret_cast<const uint4 *>(qb + (8 * j + g) * D + D / 4 * t)[c];
                 qf[j][2 * c][0] = bf16x2_to_f16x2(x.x);
                 qf[j][2 * c][1] = bf16x2_to_f16x2(x.y);
                 qf[j][2 * c + 1][0] = bf16x2_to_f16x2(x.z);
@@ -412,7 +412,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
         const int key = a.seg.r.base + kUnit * a.unit + 16 * lane;
         half_off = 1;
         if (lane < 2 * listed && key < a.seg.r.L) {
-            const int blk = __ldg(p.block_table + static_cast<int64_t>(a.seg.b) * p.max_num_blocks + (key >> p.log2_bs));
+            const int blk = p.block_table[static_cast<int64_t>(a.seg.b) * p.max_num_blocks + (key >> p.log2_bs)];
             if (blk >= 0 && blk < p.num_blocks) {
                 half_off += blk * block_bytes + ((a.seg.kvh << p.log2_bs) + (key & bs_mask)) * RB - 1;
             } else {
@@ -511,8 +511,7 @@ __device__ __forceinline__ void split_body(const Params &p) {
             if (slot >= num_slots) {
                 if (lane == 0) flag_error(p.err, kErrSlotRange);
             } else if (slot >= 0) {
-                const int blk = __ldg(p.block_table + static_cast<int64_t>(seg.b) * p.max_num_blocks +
-                                      (pos >> p.log2_bs));
+                const int blk = p.block_table[static_cast<int64_t>(seg.b) * p.max_num_blocks + (pos >> p.log2_bs)];
                 const bool match = ((static_cast<int64_t>(blk) << p.log2_bs) | (pos & bs_mask)) == slot;
                 if (!match && lane == 0) flag_error(p.err, kErrSlotMismatch);
                 if (lane < 2 * (D / 16)) {
@@ -746,6 +745,8 @@ __global__ void __launch_bounds__(warps_of(NT) * 32, 1)
     // precedes it on the stream; beside a prefill (which itself began when all before it was
     // complete) it starts at once, else it waits here.  The merge reads the lengths before it waits
     // for this grid, so it is let in only behind this wait: what precedes the call may write them.
+    // (For the same reason the inputs are read by ordinary loads: they may have been written while
+    // this grid was there already, which read-only loads do not allow.)
     if (!p.after_prefill) griddep_wait();
     griddep_launch_dependents();
     split_body<D, NT>(p);

@@ -1285,7 +1285,10 @@ __global__ void __launch_bounds__(kExpandThreads)
     expand_fp4_kernel(const PrefillKernelParams p, uint4 *__restrict__ k_out, uint4 *__restrict__ v_out) {
     constexpr int GROUPS = HD / 16;
     constexpr int RB = fp4::row_bytes(HD);
-    griddep_wait();  // a programmatic dependent of whatever precedes it: its launch overlaps that
+    // A programmatic dependent of whatever precedes it: its launch overlaps that.  So the cache and
+    // the table may have been written while this grid was there (a decode that stores its new tokens
+    // lets its dependents in before it writes them): ordinary loads, no read-only ones.
+    griddep_wait();
     const int seq = blockIdx.y;
     const int q_start = p.cu_q[seq], sq = p.cu_q[seq + 1] - q_start;
     int sk = p.seq_lens != nullptr ? p.seq_lens[seq] : p.cu_k[seq + 1] - p.cu_k[seq];
@@ -1296,7 +1299,7 @@ __global__ void __launch_bounds__(kExpandThreads)
     const int g = threadIdx.x % GROUPS;
     const int key = blockIdx.x * expand_keys<HD>() + threadIdx.x / GROUPS;
     if (key >= sk || key < first) return;
-    const int blk = __ldg(p.block_table + static_cast<int64_t>(seq) * p.max_num_blocks + (key >> p.log2_bs));
+    const int blk = p.block_table[static_cast<int64_t>(seq) * p.max_num_blocks + (key >> p.log2_bs)];
     const bool good = blk >= 0 && blk < p.num_blocks;
     if (!good && g == 0) flag_error(p.err, kErrBlockRange);
     const int64_t row = ((static_cast<int64_t>(good ? blk : 0) * p.num_kv_heads) << p.log2_bs) +
@@ -1314,14 +1317,14 @@ __global__ void __launch_bounds__(kExpandThreads)
                 if (!good || h0 + i >= p.num_kv_heads) continue;
                 const uint8_t *at = src[kv] + (h0 + i) * step;
                 if constexpr (HD == 128) {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(at) + g);
+                    const uint2 x = reinterpret_cast<const uint2 *>(at)[g];
                     c[i][kv][0] = x.x;
                     c[i][kv][1] = x.y;
                 } else {  // 36-byte rows: 4-byte aligned
-                    c[i][kv][0] = __ldg(reinterpret_cast<const uint32_t *>(at) + 2 * g);
-                    c[i][kv][1] = __ldg(reinterpret_cast<const uint32_t *>(at) + 2 * g + 1);
+                    c[i][kv][0] = reinterpret_cast<const uint32_t *>(at)[2 * g];
+                    c[i][kv][1] = reinterpret_cast<const uint32_t *>(at)[2 * g + 1];
                 }
-                s[i][kv] = __ldg(at + HD / 2 + g);
+                s[i][kv] = at[HD / 2 + g];
             }
 #pragma unroll
         for (int i = 0; i < kExpandHeads; ++i) {

@@ -116,3 +116,93 @@ def test_lengths_of_a_prepared_step_reach_the_merge(cuda):
                            seq_lens=lens)
         assert torch.equal(c.decode(**{**x, "seq_lens": lens}), want)
     assert pa.pa_read_device_error(device=cuda) == 0
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_decode_reads_inputs_that_an_early_trigger_precedes(cuda, early_write, captured):
+    # Queries, tables and both caches are written while the decode's blocks may be there already.
+    c = Case(cuda, [3999, 2000, 40], [1] * 3, 8, 2, 128, seed=53)
+    x = c.device()
+    want = c.decode(**x)
+    c.check(want)
+    late = {k: torch.empty_like(v) for k, v in x.items()}
+    out = torch.empty_like(x["q"])
+    ws = torch.empty(pa.pa_decode_fp4_workspace_size(3, 8, 2, 128, 4000), dtype=torch.uint8, device=cuda)
+    for name in ("q", "block_table", "k_cache", "v_cache"):
+        def step():
+            for k, v in x.items():
+                late[k].copy_(v)
+            late[name].view(torch.uint8).fill_(0xff)  # NaN queries and scales, entries of -1
+            c.decode(**late, out=out, workspace=ws)  # (its loads of the old values)
+            early_write(late[name].view(torch.int32).flatten(), x[name].view(torch.int32).flatten())
+            c.decode(**late, out=out, workspace=ws)
+
+        for got in _run(step, out, captured):
+            assert torch.equal(got, want), name
+        assert pa.pa_read_device_error(device=cuda) == (pa.DEVERR_BLOCK_RANGE if name == "block_table" else 0)
+
+
+@pytest.mark.parametrize("dim", [128, 64])
+@pytest.mark.parametrize("captured", [False, True])
+def test_expansion_reads_what_an_early_trigger_precedes(cuda, early_write, captured, dim):
+    # The expansion of a long prefill's keys: caches, table, lengths and offsets written late.
+    c = Case(cuda, [300, 0, 50], [200, 300, 33], 8, 2, dim, seed=54)
+    x = c.device() | {"cu": _t(c.cu, cuda)}
+    late = {k: torch.empty_like(v) for k, v in x.items()}
+    out = torch.empty_like(x["q"])
+    ws = torch.empty(pa.pa_varlen_prefill_fp4_workspace_size(3, 8, 2, dim, 800), dtype=torch.uint8, device=cuda)
+
+    def call(y):
+        pa.pa_varlen_prefill_fp4(y["q"], y["k_cache"], y["v_cache"], y["cu"], y["seq_lens"], y["block_table"], 768, 800, c.scale,
+                                 c.kv_scale, out=out, workspace=ws)
+
+    call(x)
+    c.check(out)
+    want = out.clone()
+    for name in ("block_table", "k_cache", "v_cache", "seq_lens", "cu"):
+        def step():
+            for k, v in x.items():
+                late[k].copy_(v)
+            late[name].zero_()
+            call(late)
+            early_write(late[name].view(torch.int32).flatten(), x[name].view(torch.int32).flatten())
+            call(late)
+
+        for got in _run(step, out, captured):
+            assert torch.equal(got, want), name
+        pa.pa_read_device_error(device=cuda)  # (the call with zeros in the place of lengths is flagged)
+
+
+@pytest.mark.parametrize("dim", [128, 64])
+@pytest.mark.parametrize("captured", [False, True])
+def test_prefill_reads_the_rows_of_the_decode_before_it(cuda, captured, dim):
+    # A decode stores its new tokens and lets the next call in before it writes them; the next call
+    # expands a cache with those rows.
+    c = Case(cuda, [700, 2047, 15, 64], [1] * 4, 8, 2, dim, seed=55)
+    x, new = c.device(), c.new_tokens()
+    start = {k: x[k].clone() for k in ("k_cache", "v_cache")}
+    first = c.decode(**x, **new)
+    c.store()
+    # The prefill: the last rows of every sequence, the new token's the last.
+    p = Case.__new__(Case)
+    p.__dict__ = dict(c.__dict__)
+    p.new = np.array([300, 1, 16, 65])
+    p.cu = np.concatenate([[0], np.cumsum(p.new)]).astype(np.int32)
+    p.q = torch.randn(int(p.cu[-1]), 8, dim, generator=torch.Generator().manual_seed(56)).bfloat16()
+    q, cu = p.q.to(cuda), _t(p.cu, cuda)
+    out = torch.empty_like(q)
+    ws = torch.empty(pa.pa_varlen_prefill_fp4_workspace_size(4, 8, 2, dim, 2048), dtype=torch.uint8, device=cuda)
+
+    def step():
+        for k, v in start.items():
+            x[k].copy_(v)
+        c.decode(**x, **new)
+        pa.pa_varlen_prefill_fp4(q, x["k_cache"], x["v_cache"], cu, x["seq_lens"], x["block_table"], 768, 2048, p.scale,
+                                 p.kv_scale, out=out, workspace=ws)
+
+    step()
+    p.check(out)
+    want = out.clone()
+    for got in _run(step, out, captured):
+        assert torch.equal(got, want)
+    assert torch.equal(c.decode(**x), first)
