@@ -416,8 +416,9 @@ pa_status pa_varlen_prefill_fp8(void *out, const void *q, const void *key, const
  * appended to free_blocks, seq_lens_out[i] = 0 (other rows: seq_lens[i]), and *num_free_out =
  * *num_free plus their number.  The table is left as it is.  Blocks that several rows share
  * (a common prefix) are the caller's to release once.  num_free_out may be num_free and
- * seq_lens_out may be seq_lens.  Entries out of range, or beyond the pool's num_blocks ids,
- * are flagged PA_DEVERR_BLOCK_RANGE.  Limits as pa_prepare_step.
+ * seq_lens_out may be seq_lens.  Entries out of range (as of a request that got no block)
+ * are flagged PA_DEVERR_BLOCK_RANGE and left out, the others follow one another; so are those
+ * beyond the pool's num_blocks ids.  Limits as pa_prepare_step.
  */
 pa_status pa_prepare_step(int32_t *block_table, int32_t *seq_lens, int32_t *cu_seqlens_q,
                           int32_t *slot_mapping, int32_t *positions, int32_t *num_free_out,

@@ -7,7 +7,8 @@
 //     cu = exclusive prefix sum of q,  off = exclusive prefix sum of need,
 //     block_table[i][have_i + k] = free[n_free - 1 - off_i - k],  0 <= k < need_i,
 //     token t of request i: position p = c_i + t - cu_i, slot block_table[i][p / B] * B + p % B.
-// release: the entries [0, ceil(len_i / B)) of finished rows follow free[n_free) in row order.
+// release: the entries [0, ceil(len_i / B)) of finished rows follow free[n_free) in row order;
+//     entries that are no block ids are left out (a flagged call).
 //
 // The data is a few bytes a token, so the time is launches and dependent loads.  Every block
 // scans all requests by itself (at most kMaxStepSeqs, two words of shared memory each) and
@@ -286,37 +287,103 @@ __device__ __forceinline__ void publish_prepare(const StepArgs &a, const uint32_
     }
 }
 
-// This block's released entries to the end of the free list.
-__device__ __forceinline__ void push_blocks(const StepArgs &a, const uint32_t *first) {
+// Set for good once a release in two launches has met an entry that is no block id: from then on
+// the second launch of every one (this call's among them) appends the entries anew, without such
+// ones.  (Never cleared, so no clearing can come between the launches of another stream's call.)
+__device__ unsigned bad_entries_seen;
+
+// The table entries of four consecutive released items k0 .. k0 + 3; -1 past the total.
+__device__ __forceinline__ void released(const StepArgs &a, const uint32_t *first, uint32_t total,
+                                         uint32_t k0, int (&entry)[4]) {
+    int seq = -1;
+    uint32_t begin = 0, end = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        entry[j] = -1;
+        const uint32_t k = k0 + j;
+        if (k >= total) continue;
+        if (seq < 0 || k >= end) {
+            seq = holder(first, a.num_seqs, k);
+            begin = first[seq];
+            end = first[seq + 1];
+        }
+        entry[j] = a.block_table[static_cast<int64_t>(seq) * a.max_num_blocks + (k - begin)];
+    }
+}
+
+__device__ __forceinline__ bool is_block(const StepArgs &a, int entry) {
+    return entry >= 0 && entry < a.num_blocks;
+}
+
+// This block's released entries to the end of the free list, each at its place among all of them:
+// whether that holds for this thread's, or one of them is no block id.
+__device__ __forceinline__ bool push_blocks(const StepArgs &a, const uint32_t *first) {
     const int n = a.num_seqs;
     const uint32_t total = n > 0 ? first[n] : 0u;
     const uint32_t nfree = free_count(a, false);
     const int64_t stride = 4ll * kThreads * gridDim.x;
+    bool good = true;
     for (int64_t k0 = 4ll * (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x); k0 < total;
          k0 += stride) {
-        int seq = -1;
-        uint32_t begin = 0, end = 0;
+        int entry[4];
+        released(a, first, total, static_cast<uint32_t>(k0), entry);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t k = static_cast<uint32_t>(k0) + j;
-            if (k >= total) continue;
-            if (seq < 0 || k >= end) {
-                seq = holder(first, n, k);
-                begin = first[seq];
-                end = first[seq + 1];
-            }
-            const int entry = a.block_table[static_cast<int64_t>(seq) * a.max_num_blocks + (k - begin)];
-            const int64_t dst = static_cast<int64_t>(nfree) + k;
-            if (entry < 0 || entry >= a.num_blocks || dst >= a.num_blocks) flag_error(a.err, kErrBlockRange);
-            if (dst < a.num_blocks) a.free_blocks[dst] = entry;
+            if (k0 + j >= total) continue;
+            const int64_t dst = static_cast<int64_t>(nfree) + k0 + j;
+            const bool id = is_block(a, entry[j]);
+            if (!id || dst >= a.num_blocks) flag_error(a.err, kErrBlockRange);
+            good = good && id;
+            if (id && dst < a.num_blocks) a.free_blocks[dst] = entry[j];
         }
     }
+    return good;
 }
 
-__device__ __forceinline__ void publish_release(const StepArgs &a, const uint32_t *first) {
+// One block appends all released entries that are block ids, one behind the other; how many.
+__device__ __forceinline__ uint32_t push_blocks_only(const StepArgs &a, const uint32_t *first,
+                                                     uint32_t nfree) {
+    __shared__ uint32_t wcount[kThreads / 32];
+    const uint32_t total = a.num_seqs > 0 ? first[a.num_seqs] : 0u;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t kept = 0;
+    for (uint32_t k0 = 0; k0 < total; k0 += 4 * kThreads) {  // (below 2^32: total is below 2^31)
+        int entry[4];
+        released(a, first, total, k0 + 4 * threadIdx.x, entry);
+        uint32_t mine = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mine += is_block(a, entry[j]) ? 1u : 0u;
+        uint32_t inc = mine;  // inclusive over the warp
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += x;
+        }
+        __syncthreads();  // the previous round's counts have been read
+        if (lane == 31) wcount[warp] = inc;
+        __syncthreads();
+        int64_t dst = static_cast<int64_t>(nfree) + kept + (inc - mine);
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) dst += wcount[w];
+            kept += wcount[w];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (!is_block(a, entry[j])) continue;
+            if (dst < a.num_blocks) a.free_blocks[dst] = entry[j];
+            ++dst;
+        }
+    }
+    return kept;
+}
+
+// again: not every entry was at its place.
+__device__ __forceinline__ void publish_release(const StepArgs &a, const uint32_t *first, bool again) {
     const int n = a.num_seqs;
     const uint32_t nfree = free_count(a, true);
-    const uint32_t total = n > 0 ? first[n] : 0u;
+    uint32_t total = n > 0 ? first[n] : 0u;
+    if (again) total = push_blocks_only(a, first, nfree);
     __syncthreads();
     if (threadIdx.x == 0)
         *a.num_free_out = static_cast<int>(min(static_cast<int64_t>(nfree) + total, a.num_blocks));
@@ -335,19 +402,25 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
     uint32_t *items = sums, *blocks = sums + a.num_seqs + 1;
     if constexpr (PART == kItems) sm100::griddep_launch_dependents();
     scan<PREPARE>(a, items, blocks, PART != kItems);
+    bool again = false;
     if constexpr (PART != kPublish) {
         if constexpr (PREPARE)
             tokens(a, items, blocks);
         else
-            push_blocks(a, items);
+            again = !push_blocks(a, items);
     }
-    if constexpr (PART == kAll) __syncthreads();
-    if constexpr (PART == kPublish) sm100::griddep_wait();
+    if constexpr (!PREPARE && PART == kItems)
+        if (again) atomicExch(&bad_entries_seen, 1u);
+    if constexpr (PART == kAll) again = __syncthreads_or(again);
+    if constexpr (PART == kPublish) {
+        sm100::griddep_wait();
+        if constexpr (!PREPARE) again = __ldcg(&bad_entries_seen) != 0u;
+    }
     if constexpr (PART != kItems) {
         if constexpr (PREPARE)
             publish_prepare(a, items, blocks);
         else
-            publish_release(a, items);
+            publish_release(a, items, again);
     }
 }
 

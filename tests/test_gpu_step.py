@@ -231,3 +231,71 @@ def test_steps_in_place_as_a_graph(cuda, n, chunk):
     assert int(count) == nf and pa.pa_read_device_error(device=cuda) == 0
     held = np.concatenate([table[i, : -(-int(c) // bs)] for i, c in enumerate(want_lens)])
     assert sorted([*held, *free_np[:nf]]) == list(range(n * mb))  # every block is somewhere, once
+
+
+@pytest.mark.parametrize("n,width,extra", [(3, 8, 0), (40, 50, 700), (700, 40, 2), (2000, 64, 0)])
+def test_release_keeps_bad_entries_off_the_free_list(cuda, n, width, extra):
+    # Rows with -1 and ids past the pool among their blocks, in one launch and in two: flagged, and
+    # the list and the count hold the others, in order.  What is left over is sound for a later step.
+    rng = np.random.default_rng(n)
+    nb = n * width + extra
+    table = rng.permutation(nb)[: n * width].reshape(n, width)
+    bad = rng.random(table.shape) < 0.1
+    bad[0, 0] = bad[n - 1, width - 1] = True
+    table = np.where(bad, rng.choice([-1, -2**31, nb, 2**31 - 1], table.shape), table)
+    lens = rng.integers(0, width * 16 + 1, n)
+    lens[0] = lens[n - 1] = width * 16
+    fin = rng.random(n) < 0.7
+    fin[0] = fin[n - 1] = True
+    held = np.concatenate([table[i, : -(-lens[i] // 16)] for i in range(n) if fin[i]])
+    held = held[(held >= 0) & (held < nb)]
+    for _ in range(2):  # (the second time with the fault on record)
+        free = torch.full((nb,), -9, dtype=torch.int32, device=cuda)
+        first = rng.integers(0, nb - len(held) + 1)
+        ids = rng.integers(0, nb, first)
+        free[:first] = _t(ids, cuda)
+        out, count = pa.pa_release_blocks(_t(fin, cuda), _t(lens, cuda), _t(table, cuda), free, _t([first], cuda), 16)
+        assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_BLOCK_RANGE
+        assert int(count) == first + len(held)
+        np.testing.assert_array_equal(free[: int(count)].cpu().numpy(), np.concatenate([ids, held]))
+        np.testing.assert_array_equal(out.cpu().numpy(), np.where(fin, 0, lens))
+    # A release without a fault, behind one with it.
+    good = _t(np.arange(n * width).reshape(n, width), cuda)
+    free = torch.full((nb,), -9, dtype=torch.int32, device=cuda)
+    _, count = pa.pa_release_blocks(_t([1] * n, cuda), _t([width * 16] * n, cuda), good, free, _t([0], cuda), 16)
+    assert pa.pa_read_device_error(device=cuda) == 0
+    assert int(count) == n * width and torch.equal(free[: n * width], good.flatten())
+
+
+@pytest.mark.parametrize("n", [4, 500])
+def test_release_of_bad_entries_into_a_nearly_full_pool(cuda, n):
+    # Valid ids take the places that bad entries before them leave; those beyond the pool are dropped.
+    width, nb = 16, n * 16
+    table = np.arange(nb).reshape(n, width)
+    table[:, ::2] = -1
+    lens = np.full(n, width * 16)
+    valid = table[table >= 0]
+    for room in (len(valid) + 3, len(valid), len(valid) - 5):
+        buf = torch.full((nb + 9,), -3, dtype=torch.int32, device=cuda)
+        free = buf[:nb]
+        start = nb - room
+        _, count = pa.pa_release_blocks(_t([1] * n, cuda), _t(lens, cuda), _t(table, cuda), free, _t([start], cuda), 16)
+        assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_BLOCK_RANGE
+        want = valid[:room]
+        assert int(count) == start + len(want) and (buf[nb:] == -3).all() and (buf[:start] == -3).all()
+        np.testing.assert_array_equal(free[start: int(count)].cpu().numpy(), want)
+
+
+def test_release_of_a_preempted_row(cuda):
+    # A request that got no block has -1 in its table; released by its uncut length, later steps
+    # still take sound blocks only.
+    bt, free, nf = _t([[-1, -1], [-1, -1]], cuda), _t([5, 4, 3, 2, 1, 0], cuda), _t([2], cuda)
+    lens, _, slots, _, nf = pa.pa_prepare_step(_t([0, 0], cuda), _t([17, 20], cuda), bt, free, nf, 16, 37)
+    assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_NO_BLOCKS
+    assert bt.tolist() == [[4, 5], [-1, -1]] and nf.tolist() == [0]
+    _, nf = pa.pa_release_blocks(_t([1, 1], cuda), _t([17, 20], cuda), bt, free, nf, 16)
+    assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_BLOCK_RANGE
+    assert nf.tolist() == [2] and free[:2].tolist() == [4, 5]
+    lens, _, slots, _, nf = pa.pa_prepare_step(_t([0, 0], cuda), _t([17, 20], cuda), bt, free, nf, 16, 37)
+    assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_NO_BLOCKS
+    assert lens.tolist() == [17, 0] and bt.tolist() == [[5, 4], [-1, -1]] and (slots[:17] >= 0).all()
