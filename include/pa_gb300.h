@@ -457,11 +457,14 @@ pa_status pa_release_blocks(int32_t *free_blocks, int32_t *num_free_out, int32_t
  * pa_varlen_prefill_fp4: as pa_varlen_prefill; single-row sequences run on the decode kernel
  *     when seq_lens is given, in the workspace.  The advertised workspace also has room for
  *     the keys of num_seqs sequences of max_seqlen_k keys in 16 bits (up to 4 GiB each for K
- *     and V; none beyond): with it, long queries expand their sequences' keys once instead of
- *     in every query block.  pa_decode_fp4_workspace_size(num_seqs, ...) bytes are enough to
- *     run without.  As in the other prefills a key that a row does not see has weight 0, so a
- *     NaN value reaches the rows whose 128-key tiles hold it (rows behind a sequence's last
- *     key are never read as values; the decode reads no value outside a row's range).
+ *     and V; none beyond): with it, calls whose max_seqlen_q is above 4 floor(128 / G) tokens, G
+ *     query heads a kv head, expand their sequences' keys once instead of in every query block.
+ *     pa_decode_fp4_workspace_size(num_seqs, ...) bytes are enough to run without;
+ *     pa_varlen_prefill_fp4_workspace_size_q is what a call with this max_seqlen_q makes use of
+ *     (the one or the other).  As in the other prefills a key that a row does not see has
+ *     weight 0, so a NaN value reaches the rows whose 128-key tiles hold it (rows behind a
+ *     sequence's last key are never read as values; the decode reads no value outside a row's
+ *     range).
  *
  *   workspace  at least pa_decode_fp4_workspace_size(...) /
  *              pa_varlen_prefill_fp4_workspace_size(...) bytes, 256-byte aligned (may be NULL
@@ -490,6 +493,9 @@ pa_status pa_decode_fp4(void *out, const void *q, const void *key, const void *v
                         void *stream);
 size_t pa_varlen_prefill_fp4_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
                                             int head_dim, int max_seqlen_k, int sliding_window);
+size_t pa_varlen_prefill_fp4_workspace_size_q(int num_seqs, int num_heads, int num_kv_heads,
+                                              int head_dim, int max_seqlen_q, int max_seqlen_k,
+                                              int sliding_window);
 pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const void *value,
                                 const int32_t *slot_mapping, void *k_cache, void *v_cache,
                                 const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,

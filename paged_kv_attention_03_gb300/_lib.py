@@ -38,7 +38,8 @@ EXPORTED = ("pa_status_string", "pa_version", "pa_store_kvcache", "pa_decode_num
             "pa_store_kvcache_fp8", "pa_decode_fp8", "pa_debug_prefill_stall",
             "pa_varlen_prefill_fp8", "pa_prepare_step", "pa_release_blocks",
             "pa_store_kvcache_fp4", "pa_gather_kvcache_fp4", "pa_decode_fp4_workspace_size",
-            "pa_decode_fp4", "pa_varlen_prefill_fp4_workspace_size", "pa_varlen_prefill_fp4")
+            "pa_decode_fp4", "pa_varlen_prefill_fp4_workspace_size",
+            "pa_varlen_prefill_fp4_workspace_size_q", "pa_varlen_prefill_fp4")
 
 
 class PAError(RuntimeError):
@@ -116,6 +117,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         for fn in (lib.pa_decode_fp4_workspace_size, lib.pa_varlen_prefill_fp4_workspace_size):
             fn.argtypes = [i32] * 6
             fn.restype = sz
+        lib.pa_varlen_prefill_fp4_workspace_size_q.argtypes = [i32] * 7
+        lib.pa_varlen_prefill_fp4_workspace_size_q.restype = sz
         lib.pa_decode_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i64, i32,
                                       i32, i32, i32, i32, f32, f32, vp, sz, vp]
         lib.pa_decode_fp4.restype = ctypes.c_int
@@ -466,7 +469,14 @@ def pa_decode_fp4_workspace_size(batch: int, num_heads: int, num_kv_heads: int, 
 @functools.lru_cache(maxsize=1024)
 def pa_varlen_prefill_fp4_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int,
                                          head_dim: int, max_seqlen_k: int,
-                                         sliding_window: int = 0) -> int:
+                                         sliding_window: int = 0,
+                                         max_seqlen_q: int | None = None) -> int:
+    """Bytes for calls of any query lengths, or what one with this max_seqlen_q makes use of (short
+    queries none of the scratch for expanded keys)."""
+    if max_seqlen_q is not None:
+        return int(load().pa_varlen_prefill_fp4_workspace_size_q(
+            num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen_q, max_seqlen_k,
+            sliding_window))
     return int(load().pa_varlen_prefill_fp4_workspace_size(num_seqs, num_heads, num_kv_heads,
                                                            head_dim, max_seqlen_k,
                                                            sliding_window))
@@ -539,7 +549,7 @@ def pa_varlen_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
                           workspace: torch.Tensor | None = None) -> torch.Tensor:
     """pa_varlen_prefill over 4-bit caches (as pa_decode_fp4): q [Tq, H, D] -> out [Tq, H, D].
     New tokens, when given, are quantised into the caches first.  Without a workspace one of
-    pa_varlen_prefill_fp4_workspace_size(...) bytes is allocated."""
+    pa_varlen_prefill_fp4_workspace_size(..., max_seqlen_q=max_seqlen_q) bytes is allocated."""
     lib = _lib or load()
     dev = _device_of(q, "q")
     nb, hkv, bs, d = _fp4_shape(k_cache, "pa_varlen_prefill_fp4")
@@ -553,7 +563,7 @@ def pa_varlen_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     new = _fp4_new_tokens(key, value, slot_mapping, total_q, hkv, d, dev, "pa_varlen_prefill_fp4")
     ws, ws_bytes, workspace = _workspace(
         workspace, 0 if workspace is not None else pa_varlen_prefill_fp4_workspace_size(
-            n, heads, hkv, d, max_seqlen_k, sliding_window), dev)
+            n, heads, hkv, d, max_seqlen_k, sliding_window, max_seqlen_q), dev)
     _run("pa_varlen_prefill_fp4", lib.pa_varlen_prefill_fp4, dev,
          _arg(out, torch.bfloat16, "out", dev, (total_q, heads, d)),
          _arg(q, torch.bfloat16, "q", dev, (total_q, heads, d)), *new,

@@ -247,6 +247,17 @@ size_t pa_varlen_prefill_fp4_workspace_size(int num_seqs, int num_heads, int num
            2 * pa::prefill_fp4_scratch_bytes(num_seqs, num_kv_heads, head_dim, max_seqlen_k);
 }
 
+size_t pa_varlen_prefill_fp4_workspace_size_q(int num_seqs, int num_heads, int num_kv_heads,
+                                              int head_dim, int max_seqlen_q, int max_seqlen_k,
+                                              int sliding_window) {
+    if (max_seqlen_q < 0 || num_kv_heads <= 0) return 0;
+    const int group = num_heads / num_kv_heads;
+    if (group >= 1 && group <= 64 && pa::prefill_fp4_expands(group, max_seqlen_q))
+        return pa_varlen_prefill_fp4_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen_k,
+                                                    sliding_window);
+    return pa_decode_fp4_workspace_size(num_seqs, num_heads, num_kv_heads, head_dim, max_seqlen_k, sliding_window);
+}
+
 pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const void *value,
                                 const int32_t *slot_mapping, void *k_cache, void *v_cache,
                                 const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,

@@ -203,6 +203,8 @@ struct PrefillArgs {
     unsigned *err;
 };
 size_t prefill_fp4_scratch_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_seqlen_k);
+// Whether a 4-bit prefill expands its keys beforehand, given a scratch cache.
+bool prefill_fp4_expands(int group, int max_seqlen_q);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);
 // Testing aid behind pa_debug_prefill_stall (process-wide; read at each prefill launch).
 void debug_prefill_stall(int stall, uint64_t wait_ns);

@@ -1279,6 +1279,8 @@ constexpr int expand_keys() {  // keys of a block
 // 4096 182 / 188, 8 x 192 after 1024 54.5 / 59.3, four of 300 after 300 27.7 / 29.5, 8 x 512 after
 // 8192 505 / 692, 16 x 2048 490 / 697.
 constexpr int kExpandPairs = 3;
+// Tokens of a query-tile pair.
+constexpr int item_tokens_of(int group) { return 2 * (BM / group); }
 
 template <int HD>
 __global__ void __launch_bounds__(kExpandThreads)
@@ -1450,6 +1452,10 @@ size_t prefill_fp4_scratch_bytes(int num_seqs, int num_kv_heads, int head_dim, i
     return num_seqs > 0 && bytes > 0 && bytes <= kMost / num_seqs ? static_cast<size_t>(bytes * num_seqs) : 0;
 }
 
+bool prefill_fp4_expands(int group, int max_seqlen_q) {
+    return max_seqlen_q > (kExpandPairs - 1) * item_tokens_of(group);
+}
+
 namespace {
 
 // The 4-bit prefill with its keys expanded beforehand, where a.workspace holds the scratch cache.
@@ -1505,7 +1511,7 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
     kp.num_kv_heads = a.num_kv_heads;
     kp.group = a.num_heads / a.num_kv_heads;
     kp.tok_per_tile = BM / kp.group;
-    const int item_tokens = 2 * kp.tok_per_tile;
+    const int item_tokens = item_tokens_of(kp.group);
     kp.q_items = (a.max_seqlen_q + item_tokens - 1) / item_tokens;
     const int64_t n_items = static_cast<int64_t>(kp.q_items) * a.num_kv_heads * a.num_seqs;
     if (n_items > 0x7fffffffLL) return cudaErrorInvalidValue;
@@ -1528,7 +1534,7 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
         if (a.cache == kCacheE4m3) {
             if (a.head_dim != 128) return cudaErrorInvalidValue;
             e = launch_prefill_d<128, false, kCacheE4m3>(kp, a, stream);
-        } else if (a.cache == kCacheFp4 && a.scratch != nullptr && kp.q_items >= kExpandPairs) {
+        } else if (a.cache == kCacheFp4 && a.scratch != nullptr && prefill_fp4_expands(kp.group, a.max_seqlen_q)) {
             switch (a.head_dim) {
                 case 64: e = launch_expanded<64>(kp, a, stream); break;
                 case 128: e = launch_expanded<128>(kp, a, stream); break;

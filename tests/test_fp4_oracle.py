@@ -165,3 +165,17 @@ def test_binding_refuses_wrong_tensors():
     c = torch.zeros(4, 2, 16, 72, dtype=torch.uint8)
     with pytest.raises(ValueError):
         pa.pa_gather_kvcache_fp4(c, c, i, 1.0)
+
+
+@pytest.mark.parametrize("heads,hkv", [(8, 8), (32, 8), (40, 8), (14, 2), (64, 1)])
+def test_prefill_workspace_for_a_query_length(lib, heads, hkv):
+    # Up to two blocks of queries (of 2 floor(128 / group) tokens) a sequence: what the decode rows
+    # need; longer ones: with the room for expanded keys.
+    small = pa.pa_decode_fp4_workspace_size(4, heads, hkv, 128, 4096)
+    full = pa.pa_varlen_prefill_fp4_workspace_size(4, heads, hkv, 128, 4096)
+    assert 0 < small and full >= small + 2 * 2 * 4 * 4096 * hkv * 128
+    edge = 4 * (128 // (heads // hkv))
+    for most, want in ((0, small), (1, small), (edge, small), (edge + 1, full), (4096, full)):
+        assert pa.pa_varlen_prefill_fp4_workspace_size(4, heads, hkv, 128, 4096, 0, most) == want
+    assert pa.pa_varlen_prefill_fp4_workspace_size(4, heads, hkv, 128, 4096, 0, -1) == 0
+    assert pa.pa_varlen_prefill_fp4_workspace_size(4, 9, 2, 128, 4096, 0, 4096) == 0

@@ -706,3 +706,20 @@ def test_decode_stores_the_sign_of_zero(cuda):
     c.store()
     np.testing.assert_array_equal(x["k_cache"].cpu().numpy(), c.kc)
     np.testing.assert_array_equal(x["v_cache"].cpu().numpy(), c.vc)
+
+
+@pytest.mark.parametrize("new", [[1] * 64, [8] * 60 + [1] * 4])
+def test_prefill_allocates_no_scratch_that_it_does_not_use(cuda, new):
+    # One or two blocks of queries a sequence never expand their keys beforehand, so a call without a
+    # workspace takes no room for them (64 sequences of up to 32768 keys: 8 GiB).
+    c = Case(cuda, [300] * 64, new, 8, 8, 128, seed=37)
+    x = c.device()
+    cu = _t(c.cu, cuda)
+    call = lambda **kw: pa.pa_varlen_prefill_fp4(  # noqa: E731
+        x["q"], x["k_cache"], x["v_cache"], cu, x["seq_lens"], x["block_table"], max(new), 32768, c.scale, c.kv_scale, **kw)
+    c.check(call())
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    out = call()
+    assert torch.cuda.max_memory_allocated() - before <= out.nbytes + 2 * pa.pa_decode_fp4_workspace_size(64, 8, 8, 128, 32768)
