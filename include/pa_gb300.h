@@ -472,7 +472,9 @@ pa_status pa_release_blocks(int32_t *free_blocks, int32_t *num_free_out, int32_t
  *              overlap on the GPU need one each
  * Supported: head_dim in {64, 128}; block_size a power of two in [16, 256]; num_blocks *
  * block_size below 2^31; max_seq_len <= 2^31 - 4096; num_heads / num_kv_heads <= 64; batch,
- * num_seqs <= 65535; scale positive, scale * kv_scale below 1e38.
+ * num_seqs <= 65535; scale positive, scale * kv_scale below 1e38.  Prefill: the query-tile pairs
+ * of max_seqlen_q (of 2 floor(128 / G) tokens) times num_seqs * num_kv_heads below 2^31, and
+ * num_blocks * block_size and total_q below 2^31 - 256.
  */
 pa_status pa_store_kvcache_fp4(const void *key, const void *value, void *k_cache, void *v_cache,
                                const int32_t *slot_mapping, int64_t num_tokens,

@@ -290,6 +290,8 @@ pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const
                              num_kv_heads, head_dim, kv_scale, s);
     };
     if (num_seqs == 0) return has_new ? store() : PA_OK;
+    if (!pa::prefill_fits(num_seqs, num_kv_heads, num_heads / num_kv_heads, total_q, max_seqlen_q, num_blocks * block_size))
+        return PA_ERR_UNSUPPORTED;
     if (!out || !q || !k_cache || !v_cache || !block_table || !cu_seqlens_q) return PA_ERR_INVALID_ARG;
     if (!seq_lens && !cu_seqlens_k) return PA_ERR_INVALID_ARG;
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))

@@ -205,6 +205,10 @@ struct PrefillArgs {
 size_t prefill_fp4_scratch_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_seqlen_k);
 // Whether a 4-bit prefill expands its keys beforehand, given a scratch cache.
 bool prefill_fp4_expands(int group, int max_seqlen_q);
+// Whether the prefill's places and work items fit its 32-bit counters (launch_prefill refuses the
+// rest, but a call that stores new tokens first has to know before that).
+bool prefill_fits(int num_seqs, int num_kv_heads, int group, int64_t total_q, int max_seqlen_q,
+                  int64_t slots);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);
 // Testing aid behind pa_debug_prefill_stall (process-wide; read at each prefill launch).
 void debug_prefill_stall(int stall, uint64_t wait_ns);

@@ -1281,6 +1281,10 @@ constexpr int expand_keys() {  // keys of a block
 constexpr int kExpandPairs = 3;
 // Tokens of a query-tile pair.
 constexpr int item_tokens_of(int group) { return 2 * (BM / group); }
+// Query-tile pairs of the longest sequence.
+constexpr int64_t query_items(int group, int max_seqlen_q) {
+    return (static_cast<int64_t>(max_seqlen_q) + item_tokens_of(group) - 1) / item_tokens_of(group);
+}
 
 template <int HD>
 __global__ void __launch_bounds__(kExpandThreads)
@@ -1486,10 +1490,17 @@ cudaError_t launch_expanded(PrefillKernelParams &kp, const PrefillArgs &a, cudaS
 
 }  // namespace
 
+bool prefill_fits(int num_seqs, int num_kv_heads, int group, int64_t total_q, int max_seqlen_q,
+                  int64_t slots) {
+    return slots <= 0x7fffffffLL - 256 && total_q <= 0x7fffffffLL - 256 &&
+           query_items(group, max_seqlen_q) * num_kv_heads <= 0x7fffffffLL / num_seqs;
+}
+
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
     if (a.num_seqs == 0 || a.total_q == 0 || a.max_seqlen_q == 0) return cudaSuccess;
-    const int64_t slots = a.num_blocks * a.block_size;
-    if (slots > 0x7fffffffLL - 256 || a.total_q > 0x7fffffff - 256) return cudaErrorInvalidValue;
+    if (!prefill_fits(a.num_seqs, a.num_kv_heads, a.num_heads / a.num_kv_heads, a.total_q, a.max_seqlen_q,
+                      a.num_blocks * a.block_size))
+        return cudaErrorInvalidValue;
     PrefillKernelParams kp;
     memset(&kp, 0, sizeof kp);
     kp.out = static_cast<__nv_bfloat16 *>(a.out);
@@ -1511,11 +1522,8 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
     kp.num_kv_heads = a.num_kv_heads;
     kp.group = a.num_heads / a.num_kv_heads;
     kp.tok_per_tile = BM / kp.group;
-    const int item_tokens = item_tokens_of(kp.group);
-    kp.q_items = (a.max_seqlen_q + item_tokens - 1) / item_tokens;
-    const int64_t n_items = static_cast<int64_t>(kp.q_items) * a.num_kv_heads * a.num_seqs;
-    if (n_items > 0x7fffffffLL) return cudaErrorInvalidValue;
-    kp.n_items = static_cast<int>(n_items);
+    kp.q_items = static_cast<int>(query_items(kp.group, a.max_seqlen_q));
+    kp.n_items = kp.q_items * a.num_kv_heads * a.num_seqs;
     kp.window = a.sliding_window;
     kp.kv_scale = a.cache != kCacheBf16 ? a.kv_scale : 1.f;
     kp.scale_log2 = a.scale * kp.kv_scale * kLog2e;  // codes: K elements are times kv_scale

@@ -179,3 +179,13 @@ def test_prefill_workspace_for_a_query_length(lib, heads, hkv):
         assert pa.pa_varlen_prefill_fp4_workspace_size(4, heads, hkv, 128, 4096, 0, most) == want
     assert pa.pa_varlen_prefill_fp4_workspace_size(4, heads, hkv, 128, 4096, 0, -1) == 0
     assert pa.pa_varlen_prefill_fp4_workspace_size(4, 9, 2, 128, 4096, 0, 4096) == 0
+
+
+@pytest.mark.parametrize("new", [{}, dict(key=FAKE, value=FAKE, slot=FAKE)])
+def test_prefill_refuses_sizes_before_it_stores(lib, new):
+    # Sizes past the prefill's own counters are refused while nothing has been stored.
+    need = 1 << 40
+    big = dict(ws=FAKE, wsb=need, mb=1 << 20, **new)
+    assert _prefill(lib, n=65535, mq=1 << 20, mk=1 << 20, H=64, Hkv=8, **big) == UNSUPPORTED  # 2^36 items
+    assert _prefill(lib, nb=(1 << 27) - 16, bs=16, **big) == UNSUPPORTED  # 2^31 - 256 slots
+    assert _prefill(lib, total=2 ** 31 - 256, **big) == UNSUPPORTED
