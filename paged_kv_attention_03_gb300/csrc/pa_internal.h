@@ -69,6 +69,7 @@ struct StepArgs {
     const int32_t *finished;
     const int32_t *seq_lens;
     int32_t *seq_lens_out;     // [num_seqs] (prepare: the new lengths)
+    int mark;                  // set by the launcher
     unsigned *err;
 };
 constexpr int kMaxStepSeqs = 16384;  // two words of shared memory a sequence

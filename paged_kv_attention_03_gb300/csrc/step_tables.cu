@@ -287,10 +287,13 @@ __device__ __forceinline__ void publish_prepare(const StepArgs &a, const uint32_
     }
 }
 
-// Set for good once a release in two launches has met an entry that is no block id: from then on
-// the second launch of every one (this call's among them) appends the entries anew, without such
-// ones.  (Never cleared, so no clearing can come between the launches of another stream's call.)
-__device__ unsigned bad_entries_seen;
+// A release in two launches that meets an entry that is no block id sets its mark, which tells the
+// second launch to append the entries anew, without such ones.  Calls take the marks in turn, and a
+// mark stays set: clearing it could come between the launches of another stream's call.  So after
+// a bad call one in kMarks takes the slow way too (262k entries: 262 us against 7), as do replays
+// of a captured one.
+constexpr int kMarks = 4096;
+__device__ unsigned bad_entries[kMarks];
 
 // The table entries of four consecutive released items k0 .. k0 + 3; -1 past the total.
 __device__ __forceinline__ void released(const StepArgs &a, const uint32_t *first, uint32_t total,
@@ -410,11 +413,11 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepArgs a) {
             again = !push_blocks(a, items);
     }
     if constexpr (!PREPARE && PART == kItems)
-        if (again) atomicExch(&bad_entries_seen, 1u);
+        if (again) atomicExch(&bad_entries[a.mark], 1u);
     if constexpr (PART == kAll) again = __syncthreads_or(again);
     if constexpr (PART == kPublish) {
         sm100::griddep_wait();
-        if constexpr (!PREPARE) again = __ldcg(&bad_entries_seen) != 0u;
+        if constexpr (!PREPARE) again = __ldcg(&bad_entries[a.mark]) != 0u;
     }
     if constexpr (PART != kItems) {
         if constexpr (PREPARE)
@@ -462,7 +465,10 @@ cudaError_t launch_prepare_step(const StepArgs &a, cudaStream_t stream) {
     return launch_step<true>(a, a.max_tokens, stream);
 }
 
-cudaError_t launch_release_blocks(const StepArgs &a, cudaStream_t stream) {
+cudaError_t launch_release_blocks(const StepArgs &args, cudaStream_t stream) {
+    static std::atomic<unsigned> calls{0};
+    StepArgs a = args;
+    a.mark = static_cast<int>(calls.fetch_add(1, std::memory_order_relaxed) % kMarks);
     // The released entries are at most the whole table and at most the pool.
     return launch_step<false>(a, std::min<int64_t>(static_cast<int64_t>(a.num_seqs) * a.max_num_blocks, a.num_blocks), stream);
 }

@@ -299,3 +299,41 @@ def test_release_of_a_preempted_row(cuda):
     lens, _, slots, _, nf = pa.pa_prepare_step(_t([0, 0], cuda), _t([17, 20], cuda), bt, free, nf, 16, 37)
     assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_NO_BLOCKS
     assert lens.tolist() == [17, 0] and bt.tolist() == [[5, 4], [-1, -1]] and (slots[:17] >= 0).all()
+
+
+def test_release_replayed_with_and_without_bad_entries(cuda):
+    # A captured release in two launches, replayed over sound rows, rows with bad entries and sound
+    # ones again, while another stream releases rows with bad entries all the time.
+    n, width = 300, 40
+    nb = n * width
+    sound = np.arange(nb).reshape(n, width)
+    broken = np.where(np.random.default_rng(3).random(sound.shape) < 0.2, -1, sound)
+    table, lens, one = _t(sound, cuda), _t([width * 16] * n, cuda), _t([1] * n, cuda)
+    free, count, out = (torch.empty(k, dtype=torch.int32, device=cuda) for k in (nb, 1, n))
+    zero = _t([0], cuda)
+    other = [_t(broken, cuda), torch.empty(nb, dtype=torch.int32, device=cuda), torch.empty(n, dtype=torch.int32, device=cuda),
+             torch.empty(1, dtype=torch.int32, device=cuda)]
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(main):
+        pa.pa_release_blocks(one, lens, table, free, zero, 16, seq_lens_out=out, num_free_out=count)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=main):
+            pa.pa_release_blocks(one, lens, table, free, zero, 16, seq_lens_out=out, num_free_out=count)
+    for rows in (sound, broken, sound, broken):
+        want = rows[rows >= 0]
+        with torch.cuda.stream(main):
+            table.copy_(_t(rows, cuda))
+            free.fill_(-9)
+        torch.cuda.synchronize()
+        for _ in range(5):
+            with torch.cuda.stream(side):
+                pa.pa_release_blocks(one, lens, other[0], other[1], zero, 16, seq_lens_out=other[2], num_free_out=other[3])
+            with torch.cuda.stream(main):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert int(count) == len(want) and int(other[3]) == (broken >= 0).sum()
+        np.testing.assert_array_equal(free[: len(want)].cpu().numpy(), want)
+        np.testing.assert_array_equal(other[1][: int(other[3])].cpu().numpy(), broken[broken >= 0])
+    assert pa.pa_read_device_error(device=cuda) == pa.DEVERR_BLOCK_RANGE
