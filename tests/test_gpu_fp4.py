@@ -723,3 +723,76 @@ def test_prefill_allocates_no_scratch_that_it_does_not_use(cuda, new):
     before = torch.cuda.memory_allocated()
     out = call()
     assert torch.cuda.max_memory_allocated() - before <= out.nbytes + 2 * pa.pa_decode_fp4_workspace_size(64, 8, 8, 128, 32768)
+
+
+# ------------------------------------------------------- limits of the variants ---
+@pytest.mark.parametrize("lens,heads,kv_heads,dim", [([90] * 1000, 8, 2, 64), ([17, 90] * 320, 18, 2, 128), ([160] * 3, 8, 2, 128),
+                                                     ([159, 160, 1], 32, 2, 64), ([161, 7], 8, 2, 128), ([161] * 3, 32, 2, 64)])
+def test_decode_at_the_whole_segment_limit(cuda, lens, heads, kv_heads, dim):
+    # Up to 160 keys (five units of 32): whole segments, however many (2000 on 1824 warps, 1280 of
+    # two n-tiles on 1216); from 161 on pieces and a merge.
+    c = Case(cuda, np.array(lens) - 1, [1] * len(lens), heads, kv_heads, dim, seed=len(lens))
+    need = pa.pa_decode_fp4_workspace_size(len(lens), heads, kv_heads, dim, max(lens))
+    assert (need == 0) == (max(lens) <= 160)
+    c.check(c.decode())
+
+
+@pytest.mark.parametrize("window", [144, 145, 146, 160])
+def test_decode_at_the_windows_whole_segment_limit(cuda, window):
+    # A window's keys begin inside a 16-key half: with up to 145 of them five units hold them always.
+    c = Case(cuda, [300, 304, 319, 1000, 1001, 15], [1] * 6, 8, 2, 128, seed=window)
+    need = pa.pa_decode_fp4_workspace_size(6, 8, 2, 128, int(c.lens.max()), window)
+    assert (need == 0) == (window <= 145)
+    c.check(c.decode(window), window)
+
+
+@pytest.mark.parametrize("dim", [128, 64])
+@pytest.mark.parametrize("heads,kv_heads", [(8, 8), (32, 8), (40, 8)])
+def test_prefill_at_the_expansion_limit(cuda, heads, kv_heads, dim):
+    # The last query length whose keys are expanded in the kernel, and the first expanded beforehand.
+    edge = 4 * (128 // (heads // kv_heads))
+    for n in (edge, edge + 1):
+        c = Case(cuda, [20, 3], [n, 5], heads, kv_heads, dim, seed=n)
+        x = c.device()
+        most = int(c.lens.max())
+        ws = torch.full((pa.pa_varlen_prefill_fp4_workspace_size(2, heads, kv_heads, dim, most, 0, n),), 0xff, dtype=torch.uint8,
+                        device=cuda)
+        c.check(pa.pa_varlen_prefill_fp4(x["q"], x["k_cache"], x["v_cache"], _t(c.cu, cuda), x["seq_lens"], x["block_table"], n,
+                                         most, c.scale, c.kv_scale, workspace=ws))
+
+
+def test_a_decode_step_with_empty_rows_at_its_end(cuda):
+    # A padded batch: rows without a request have no tokens, stand last and give zeros.
+    c = Case(cuda, [40, 15, 700, -1, -1], [1] * 5, 8, 2, 128, seed=38)
+    table = c.table.copy()
+    nb = c.kc.shape[0]
+    free = np.setdiff1d(np.arange(nb), table[table >= 0])
+    pool = np.zeros(nb, np.int32)
+    pool[: len(free)] = free
+    bt, lens = _t(table, cuda), _t([40, 15, 700, 0, 0], cuda)
+    lens, _, slots, _, _ = pa.pa_prepare_step(lens, _t([1, 1, 1, 0, 0], cuda), bt, _t(pool, cuda), _t([len(free)], cuda), 16, 5,
+                                              seq_lens=lens)
+    assert slots[3:].tolist() == [-1, -1] and lens.tolist() == [41, 16, 701, 0, 0]
+    x = c.device() | {"block_table": bt, "seq_lens": lens}
+    key, value = _bf((5, 2, 128), 80), _bf((5, 2, 128), 81)
+    out = c.decode(**x, key=key.to(cuda), value=value.to(cuda), slot_mapping=slots)
+    c.key, c.value, c.slots, c.table = key, value, slots.cpu().numpy(), bt.cpu().numpy()
+    c.store()
+    np.testing.assert_array_equal(x["k_cache"].cpu().numpy(), c.kc)
+    c.check(out)
+    assert (out[3:] == 0).all()
+
+
+@pytest.mark.parametrize("what", ["decode", "in the kernel", "beforehand"])
+def test_queries_beyond_the_f16_range(cuda, what):
+    # Where the products are f16 ones a query beyond 65504 is clamped; with keys expanded beforehand
+    # (K bf16, as the queries) it is not.  The small scale keeps the scores below 100.
+    new = [1, 1] if what == "decode" else [100, 5]
+    c = Case(cuda, [300, 40], new, 8, 2, 128, seed=39)
+    c.q = (c.q.float() * 5e4).bfloat16()
+    assert int((c.q.abs() > 65504).sum()) > 100
+    c.scale = 1e-5
+    out = c.decode() if what == "decode" else c.prefill(expand=what == "beforehand")
+    if what != "beforehand":
+        c.q = c.q.double().clamp(-65504, 65504)
+    c.check(out)
