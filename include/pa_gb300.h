@@ -392,7 +392,8 @@ pa_status pa_varlen_prefill_fp8(void *out, const void *q, const void *key, const
  *     slot_mapping[t] = its slot; entries from the last token to max_tokens get position 0
  *     and slot -1 (padding, which every store skips).
  *     *num_free_out = *num_free minus the blocks taken.
- * A request may have no new tokens (q_i = 0) or nothing cached.  No other table entry is
+ * A request may have no new tokens (q_i = 0) or nothing cached.  (Tokens are packed: where the
+ * decode takes slot_mapping[b] for row b, rows without a token stand behind the others.)  No other table entry is
  * read (but the block that holds position c_i - 1 when that block is not full) or written.
  *
  *   block_table   [num_seqs, max_num_blocks] int32, device, updated in place
@@ -445,7 +446,9 @@ pa_status pa_release_blocks(int32_t *free_blocks, int32_t *num_free_out, int32_t
  * even), saturating at 448 and 6.  A NaN makes its group's scale NaN; an infinity saturates.
  *
  * pa_store_kvcache_fp4: as pa_store_kvcache.  Distinct slots are written by disjoint stores;
- *     no other byte of the cache changes.
+ *     no other byte of the cache changes.  Two tokens of one slot in one call may leave codes
+ *     of the one beside scales of the other (here and in the stores of the attention calls).  A
+ *     zero keeps its sign.
  * pa_gather_kvcache_fp4: the rows of slot_mapping read back: key[t] / value[t] [num_kv_heads,
  *     head_dim] bf16 (rounded to nearest); a negative slot gives zeros (one past the pool too,
  *     flagged PA_DEVERR_SLOT_RANGE).
@@ -461,7 +464,9 @@ pa_status pa_release_blocks(int32_t *free_blocks, int32_t *num_free_out, int32_t
  *     query heads a kv head, expand their sequences' keys once instead of in every query block.
  *     pa_decode_fp4_workspace_size(num_seqs, ...) bytes are enough to run without;
  *     pa_varlen_prefill_fp4_workspace_size_q is what a call with this max_seqlen_q makes use of
- *     (the one or the other).  As in the other prefills a key that a row does not see has
+ *     (the one or the other).  Keys expanded beforehand are bf16, and so q stays: no rounding of
+ *     it and no clamp, so that the scratch can change a result's last bits and, with |q| beyond
+ *     65504, the result.  As in the other prefills a key that a row does not see has
  *     weight 0, so a NaN value reaches the rows whose 128-key tiles hold it (rows behind a
  *     sequence's last key are never read as values; the decode reads no value outside a row's
  *     range).
