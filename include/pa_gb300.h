@@ -393,8 +393,9 @@ pa_status pa_varlen_prefill_fp8(void *out, const void *q, const void *key, const
  *     and slot -1 (padding, which every store skips).
  *     *num_free_out = *num_free minus the blocks taken.
  * A request may have no new tokens (q_i = 0) or nothing cached.  (Tokens are packed: where the
- * decode takes slot_mapping[b] for row b, rows without a token stand behind the others.)  No other table entry is
- * read (but the block that holds position c_i - 1 when that block is not full) or written.
+ * decode takes slot_mapping[b] for row b, rows without a token stand behind the others.)  No
+ * other table entry is read (but the block that holds position c_i - 1 when that block is not
+ * full) or written.
  *
  *   block_table   [num_seqs, max_num_blocks] int32, device, updated in place
  *   seq_lens      [num_seqs], cu_seqlens_q [num_seqs + 1], slot_mapping [max_tokens],

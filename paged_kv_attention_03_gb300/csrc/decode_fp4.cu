@@ -28,9 +28,10 @@
 //    start as soon as the split kernel's inputs are complete) merges them.  When no sequence can be longer than kWholeUnits units, ranges are whole segments
 //    and no combine is launched.
 //
-// Measured: 8 sequences of 81920 keys, 40/8 heads, 128.5 us a call (755 MB, 5.9 TB/s); 64 of
-// 2304, 32/8 heads, 37.6 us (170 MB; 5 us to the first data, 3 of ragged ends, 3 of merge); 4 of
-// 96, 8/2 heads of 64, 5.2 us.  Without its arithmetic the long call takes 117 us: the loads and
+// Measured: 8 sequences of 81920 keys, 40/8 heads, 129 us a call (755 MB, 5.8 TB/s); 64 of
+// 2304, 32/8 heads, 38 us (170 MB; 5 us to the first data, 3 of ragged ends, 3 of merge); 4 of
+// 17-100, 8/2 heads of 64, 4.2 us (replayed from a graph).  Storing the new tokens as well takes 1 to 2 us
+// more with short sequences (40.7 us against 38.8, 64 of 512-4096), nothing with long ones.  Without its arithmetic the long call takes 117 us: the loads and
 // the issue of 594 instructions a unit (128 conversions at half rate among them) bound it
 // together.
 

@@ -19,9 +19,9 @@
 // block reads it any more: by the same block when there is one, else by a second launch, a
 // programmatic dependent that repeats the scan while the first runs.
 //
-// Measured (replayed from a graph): 64 decodes 4.7 us in one launch; 2033 requests with 526k
-// slots 8.9 us in two; the release of a seventh of 64 requests 4.4 us, of half of 1024 6.2 (a call
-// from Python takes the host 9-11 us).
+// Measured (replayed from a graph): 64 decodes 4.6 us in one launch; 2033 requests with 526k
+// slots 8.6 us in two; the release of a seventh of 64 requests 4.0 us, of half of 1024 5.9 (a call
+// from Python takes the host 9-12 us).
 #include <algorithm>
 
 #include "pa_common.cuh"

@@ -11,8 +11,9 @@
 // codes): the groups of a row sit in consecutive lanes, so a row is written as one contiguous
 // run, its scales gathered by shuffles and written by the row's first lane.
 //
-// Measured on 17403 tokens of 8 heads of 128 (91 MB each way): store 18.3 us (5.0 TB/s; issue
-// slots 68 % busy, the quantisation), gather 14.3 us (6.4 TB/s, the rate of a copy).
+// Measured on 17403 tokens of 8 heads of 128 (91 MB each), three sets of tensors in turn: store
+// 17.5 us (5.2 TB/s; issue slots 68 % busy, DRAM 46 %: neither at its limit, a thread loads,
+// quantises and stores one group of K and V in that order), gather 16.4 us (5.6 TB/s).
 #include "fp4.cuh"
 #include "pa_internal.h"
 #include "sm100_ptx.cuh"
