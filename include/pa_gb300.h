@@ -515,6 +515,96 @@ pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const
                                 size_t workspace_bytes, void *stream);
 
 /*
+ * Attention of packed sequences on plain K / V rows, its gradient, and a learned relative
+ * position bias for it and for the paged cache's decode and prefill.  This library's own: the
+ * pages have no gradient, and as a bias only the linear one.
+ *
+ * Sequence i owns query rows cu_seqlens_q[i] .. cu_seqlens_q[i + 1] - 1 (sq of them) and key rows
+ * cu_seqlens_k[i] .. (sk).  Its queries are its last sq positions; the query at position p = sk - sq + r
+ * sees the keys j <= p, with sliding_window = w > 0 those with p - j < w.  With
+ *     s_j = scale * q . K_j + bias[bucket(p - j)][h],
+ * out = sum_j e^{s_j} V_j / sum_j e^{s_j}, lse = ln sum_j e^{s_j}.  There may be more queries than
+ * keys: a row at a position below 0 sees no key and gets zeros and lse = -inf, as does any row
+ * whose keys all have a bias of -inf.
+ *
+ * The bias: a table [num_buckets, num_heads] fp32 (NULL, 0 buckets: none).  With m = num_buckets / 2,
+ * distances n < m have bucket n and longer ones min(num_buckets - 1, m + floor(ln(n / m) /
+ * ln(max_distance / m) (num_buckets - m))): the floor of the real number, so a distance on a border
+ * belongs to the bucket beyond it.
+ *
+ * pa_varlen_attn: out [total_q, num_heads, head_dim] and lse [total_q, num_heads] (natural log).
+ *     q [total_q, num_heads, head_dim], k / v [total_k, num_kv_heads, head_dim] bf16: a token's heads
+ *     are contiguous, tokens q_stride / k_stride / v_stride elements apart (multiples of 8, so
+ *     that the three may lie in the rows of one projection).
+ * pa_varlen_attn_backward: from dout (the gradient of out, contiguous) and what the forward call
+ *     took and gave, dq, dk, dv (bf16, rows apart by strides of their own) and dbias
+ *     [num_buckets, num_heads] fp32 (NULL exactly when bias is); lse has no gradient of its own:
+ *         P = e^{s - lse},  dP = dout V^T,  dS = P (dP - sum_j P_j dP_j),
+ *         dq = scale dS K,  dk = scale dS^T q,  dv = P^T dout,  dbias[b] = sum of dS over bucket b,
+ *     dk and dv summed over the query heads of a kv head.  Keys and rows that nothing pairs get
+ *     zeros, and so do buckets that no pair reaches.  No atomics: equal calls
+ *     give equal bits.  P and dS are rounded to bf16 for the products, all sums are fp32; dbias
+ *     is summed from unrounded terms.
+ * pa_decode_bias, pa_varlen_prefill_bias: pa_decode and pa_varlen_prefill (optional store of new
+ *     tokens included) with the bias, which is required.
+ *
+ * In all of them rows behind the last sequence are left as they were, and a key that a row does
+ * not see has weight 0: an infinite or NaN key or value of its sequence may reach the rows whose
+ * 128-key tiles hold it (another sequence's never does).  Sequences with offsets outside the
+ * arrays, or longer than max_seqlen_q / max_seqlen_k, are flagged (PA_DEVERR_QUERY_LEN,
+ * PA_DEVERR_SEQ_RANGE) and left out.
+ *
+ *   workspace  256-byte aligned, contents on entry do not matter; calls that may overlap on the
+ *              GPU need one each.
+ *              pa_varlen_attn and pa_varlen_prefill_bias: pa_relative_bias_workspace_size(...)
+ *              bytes (none without a bias); pa_varlen_attn_backward:
+ *              pa_varlen_attn_backward_workspace_size(...); pa_decode_bias: pa_decode_workspace_size(...)
+ * Supported: head_dim in {64, 128}; num_heads / num_kv_heads <= 64; 2 to 128 buckets,
+ * max_distance above num_buckets / 2 and up to 32768; scale positive, below 1e38; total_q and
+ * total_k below 2^30; num_seqs <= 65535; the 128-row tiles of max_seqlen_q (max_seqlen_k) times
+ * num_seqs times num_heads (num_kv_heads) below 2^31; in the backward call also (total_q / 128 +
+ * num_seqs + 1) num_heads.  Sizes of the paged calls as pa_decode and pa_varlen_prefill, but at
+ * most 64 query heads a kv head.  Size functions return 0 for what is not supported.
+ */
+size_t pa_relative_bias_workspace_size(int num_heads, int num_buckets, int max_distance);
+size_t pa_varlen_attn_backward_workspace_size(int total_q, int num_seqs, int num_heads,
+                                              int num_buckets, int max_distance);
+pa_status pa_varlen_attn(void *out, float *lse, const void *q, const void *k, const void *v,
+                         int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                         const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int num_seqs,
+                         int total_q, int total_k, int max_seqlen_q, int max_seqlen_k,
+                         int num_heads, int num_kv_heads, int head_dim, int sliding_window,
+                         float scale, const float *bias, int num_buckets, int max_distance,
+                         void *workspace, size_t workspace_bytes, void *stream);
+pa_status pa_varlen_attn_backward(void *dq, void *dk, void *dv, float *dbias, int64_t dq_stride,
+                                  int64_t dk_stride, int64_t dv_stride, const void *dout,
+                                  const void *q, const void *k, const void *v, const void *out,
+                                  const float *lse, int64_t q_stride, int64_t k_stride,
+                                  int64_t v_stride, const int32_t *cu_seqlens_q,
+                                  const int32_t *cu_seqlens_k, int num_seqs, int total_q,
+                                  int total_k, int max_seqlen_q, int max_seqlen_k, int num_heads,
+                                  int num_kv_heads, int head_dim, int sliding_window, float scale,
+                                  const float *bias, int num_buckets, int max_distance,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+pa_status pa_decode_bias(void *out, const void *q, const void *key, const void *value,
+                         const int32_t *slot_mapping, void *k_cache, void *v_cache,
+                         const int32_t *block_table, int max_num_blocks, const int32_t *seq_lens,
+                         int batch, int max_seq_len, int64_t num_blocks, int block_size,
+                         int num_heads, int num_kv_heads, int head_dim, int sliding_window,
+                         float scale, const float *bias, int num_buckets, int max_distance,
+                         int num_splits, void *workspace, size_t workspace_bytes, void *stream);
+pa_status pa_varlen_prefill_bias(void *out, const void *q, const void *key, const void *value,
+                                 const int32_t *slot_mapping, void *k_cache, void *v_cache,
+                                 const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                 const int32_t *seq_lens, const int32_t *block_table,
+                                 int max_num_blocks, int num_seqs, int total_q, int max_seqlen_q,
+                                 int max_seqlen_k, int64_t num_blocks, int block_size,
+                                 int num_heads, int num_kv_heads, int head_dim,
+                                 int sliding_window, float scale, const float *bias,
+                                 int num_buckets, int max_distance, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
  * pa_read_device_error - synchronise `stream`, then return in *flags the device
  * error word of the current device (PA_DEVERR_* bits OR-ed by every launch since it
  * was last cleared) and clear it when `clear` is non-zero.  Returns PA_OK when no

@@ -39,7 +39,10 @@ EXPORTED = ("pa_status_string", "pa_version", "pa_store_kvcache", "pa_decode_num
             "pa_varlen_prefill_fp8", "pa_prepare_step", "pa_release_blocks",
             "pa_store_kvcache_fp4", "pa_gather_kvcache_fp4", "pa_decode_fp4_workspace_size",
             "pa_decode_fp4", "pa_varlen_prefill_fp4_workspace_size",
-            "pa_varlen_prefill_fp4_workspace_size_q", "pa_varlen_prefill_fp4")
+            "pa_varlen_prefill_fp4_workspace_size_q", "pa_varlen_prefill_fp4",
+            "pa_relative_bias_workspace_size", "pa_varlen_attn_backward_workspace_size",
+            "pa_varlen_attn", "pa_varlen_attn_backward", "pa_decode_bias",
+            "pa_varlen_prefill_bias")
 
 
 class PAError(RuntimeError):
@@ -125,6 +128,20 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.pa_varlen_prefill_fp4.argtypes = [vp] * 11 + [i32, i32, i32, i32, i32, i64, i32, i32,
                                                           i32, i32, i32, f32, f32, vp, sz, vp]
         lib.pa_varlen_prefill_fp4.restype = ctypes.c_int
+        lib.pa_relative_bias_workspace_size.argtypes = [i32] * 3
+        lib.pa_relative_bias_workspace_size.restype = sz
+        lib.pa_varlen_attn_backward_workspace_size.argtypes = [i32] * 5
+        lib.pa_varlen_attn_backward_workspace_size.restype = sz
+        lib.pa_varlen_attn.argtypes = [vp] * 5 + [i64] * 3 + [vp] * 2 + [i32] * 9 + [f32, vp, i32, i32, vp, sz, vp]
+        lib.pa_varlen_attn.restype = ctypes.c_int
+        lib.pa_varlen_attn_backward.argtypes = ([vp] * 4 + [i64] * 3 + [vp] * 6 + [i64] * 3 + [vp] * 2 + [i32] * 9 +
+                                                [f32, vp, i32, i32, vp, sz, vp])
+        lib.pa_varlen_attn_backward.restype = ctypes.c_int
+        lib.pa_decode_bias.argtypes = [vp] * 8 + [i32, vp, i32, i32, i64, i32, i32, i32, i32, i32, f32, vp, i32, i32, i32,
+                                                  vp, sz, vp]
+        lib.pa_decode_bias.restype = ctypes.c_int
+        lib.pa_varlen_prefill_bias.argtypes = [vp] * 11 + [i32] * 5 + [i64] + [i32] * 5 + [f32, vp, i32, i32, vp, sz, vp]
+        lib.pa_varlen_prefill_bias.restype = ctypes.c_int
         lib.pa_read_device_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
         lib.pa_read_device_error.restype = ctypes.c_int
         _lib = lib
@@ -494,7 +511,7 @@ def _workspace(workspace: torch.Tensor | None, need: int, dev: int):
     return _ptr(workspace), workspace.nbytes, workspace
 
 
-def _fp4_new_tokens(key, value, slot_mapping, rows: int, hkv: int, d: int, dev: int, what: str):
+def _step_tokens(key, value, slot_mapping, rows: int, hkv: int, d: int, dev: int, what: str):
     """Addresses of the optional new tokens (all three or none)."""
     if key is None and value is None and slot_mapping is None:
         return None, None, None
@@ -523,7 +540,7 @@ def pa_decode_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     max_seq_len, sliding_window = int(max_seq_len), int(sliding_window)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    new = _fp4_new_tokens(key, value, slot_mapping, batch, hkv, d, dev, "pa_decode_fp4")
+    new = _step_tokens(key, value, slot_mapping, batch, hkv, d, dev, "pa_decode_fp4")
     ws, ws_bytes, workspace = _workspace(
         workspace, 0 if workspace is not None else pa_decode_fp4_workspace_size(
             batch, heads, hkv, d, max_seq_len, sliding_window), dev)
@@ -560,7 +577,7 @@ def pa_varlen_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     sliding_window = int(sliding_window)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    new = _fp4_new_tokens(key, value, slot_mapping, total_q, hkv, d, dev, "pa_varlen_prefill_fp4")
+    new = _step_tokens(key, value, slot_mapping, total_q, hkv, d, dev, "pa_varlen_prefill_fp4")
     ws, ws_bytes, workspace = _workspace(
         workspace, 0 if workspace is not None else pa_varlen_prefill_fp4_workspace_size(
             n, heads, hkv, d, max_seqlen_k, sliding_window, max_seqlen_q), dev)
@@ -576,6 +593,197 @@ def pa_varlen_prefill_fp4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
          _arg(block_table, torch.int32, "block_table", dev, (n, width)), width, n, total_q,
          max_seqlen_q, max_seqlen_k, nb, bs, heads, hkv, d, sliding_window, float(scale),
          float(kv_scale), ws, ws_bytes)
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def pa_relative_bias_workspace_size(num_heads: int, num_buckets: int, max_distance: int) -> int:
+    return int(load().pa_relative_bias_workspace_size(num_heads, num_buckets, max_distance))
+
+
+@functools.lru_cache(maxsize=1024)
+def pa_varlen_attn_backward_workspace_size(total_q: int, num_seqs: int, num_heads: int,
+                                           num_buckets: int = 0, max_distance: int = 0) -> int:
+    return int(load().pa_varlen_attn_backward_workspace_size(total_q, num_seqs, num_heads,
+                                                             num_buckets, max_distance))
+
+
+def _rows(t: torch.Tensor, name: str, dev: int, shape: tuple) -> tuple[int, int]:
+    """Address and row stride (elements) of a bf16 tensor [rows, heads, head_dim] whose rows may lie
+    apart, as slices of a projection's do, but are contiguous in themselves."""
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    rows, heads, d = shape
+    row = heads * d
+    step, head, last = t.stride()
+    if rows < 2 or t.is_contiguous():
+        step = row
+    if last != 1 or (heads > 1 and head != d) or step < row or step % 8:
+        raise ValueError(f"{name}: the heads of a row must be contiguous, and rows a multiple of 8 elements apart")
+    return t.data_ptr(), step
+
+
+def _bias(bias: torch.Tensor | None, max_distance: int, heads: int, dev: int) -> tuple:
+    """(address, num_buckets, max_distance) of a bias [num_buckets, num_heads] fp32, or none."""
+    if bias is None:
+        return None, 0, 0
+    if bias.dim() != 2:
+        raise ValueError("bias must have shape (num_buckets, num_heads)")
+    n = bias.shape[0]
+    return _arg(bias, torch.float32, "bias", dev, (n, heads)), n, int(max_distance)
+
+
+def pa_varlen_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                   cu_seqlens_k: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int, scale: float,
+                   sliding_window: int = 0, bias: torch.Tensor | None = None,
+                   max_distance: int = 0, out: torch.Tensor | None = None,
+                   lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None
+                   ) -> tuple[torch.Tensor, torch.Tensor]:
+    """Causal attention of packed sequences on plain rows: q [Tq, H, D], k / v [Tk, Hkv, D] ->
+    (out [Tq, H, D] bf16, lse [Tq, H] fp32).  q, k and v may be slices of a wider row.  bias
+    [num_buckets, H] fp32: a learned bias by relative position, in buckets up to max_distance."""
+    lib = _lib or load()
+    dev = _device_of(q, "q")
+    total_q, heads, d = q.shape
+    total_k, hkv, _ = k.shape
+    n = cu_seqlens_q.shape[0] - 1
+    if out is None:
+        out = torch.empty((total_q, heads, d), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((total_q, heads), dtype=torch.float32, device=q.device)
+    qp, qs = _rows(q, "q", dev, (total_q, heads, d))
+    kp, ks = _rows(k, "k", dev, (total_k, hkv, d))
+    vp, vs = _rows(v, "v", dev, (total_k, hkv, d))
+    b = _bias(bias, max_distance, heads, dev)
+    ws, ws_bytes, workspace = _workspace(
+        workspace, 0 if workspace is not None or bias is None else
+        pa_relative_bias_workspace_size(heads, b[1], b[2]), dev)
+    _run("pa_varlen_attn", lib.pa_varlen_attn, dev,
+         _arg(out, torch.bfloat16, "out", dev, (total_q, heads, d)),
+         _arg(lse, torch.float32, "lse", dev, (total_q, heads)), qp, kp, vp, qs, ks, vs,
+         _arg(cu_seqlens_q, torch.int32, "cu_seqlens_q", dev, (n + 1,)),
+         _arg(cu_seqlens_k, torch.int32, "cu_seqlens_k", dev, (n + 1,)), n, total_q, total_k,
+         int(max_seqlen_q), int(max_seqlen_k), heads, hkv, d, int(sliding_window), float(scale), *b,
+         ws, ws_bytes)
+    return out, lse
+
+
+def pa_varlen_attn_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                            out: torch.Tensor, lse: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                            cu_seqlens_k: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int,
+                            scale: float, sliding_window: int = 0,
+                            bias: torch.Tensor | None = None, max_distance: int = 0,
+                            dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                            dv: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None
+                            ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor,
+                                       torch.Tensor | None]:
+    """Gradient of pa_varlen_attn: (dq, dk, dv, dbias) from dout and what the forward call took and
+    returned; dbias [num_buckets, H] fp32 is None without a bias.  dq, dk and dv may be slices
+    of a wider row, as q, k and v."""
+    lib = _lib or load()
+    dev = _device_of(q, "q")
+    total_q, heads, d = q.shape
+    total_k, hkv, _ = k.shape
+    n = cu_seqlens_q.shape[0] - 1
+    new = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device=q.device)  # noqa: E731
+    dq = new(total_q, heads, d) if dq is None else dq
+    dk = new(total_k, hkv, d) if dk is None else dk
+    dv = new(total_k, hkv, d) if dv is None else dv
+    if bias is not None and dbias is None:
+        dbias = torch.empty(bias.shape, dtype=torch.float32, device=q.device)
+    grads = [_rows(dq, "dq", dev, (total_q, heads, d)), _rows(dk, "dk", dev, (total_k, hkv, d)),
+             _rows(dv, "dv", dev, (total_k, hkv, d))]
+    ins = [_rows(q, "q", dev, (total_q, heads, d)), _rows(k, "k", dev, (total_k, hkv, d)),
+           _rows(v, "v", dev, (total_k, hkv, d))]
+    b = _bias(bias, max_distance, heads, dev)
+    db = None if dbias is None else _arg(dbias, torch.float32, "dbias", dev, (b[1], heads))
+    ws, ws_bytes, workspace = _workspace(
+        workspace, 0 if workspace is not None else
+        pa_varlen_attn_backward_workspace_size(total_q, n, heads, b[1], b[2]), dev)
+    _run("pa_varlen_attn_backward", lib.pa_varlen_attn_backward, dev,
+         *(g[0] for g in grads), db, *(g[1] for g in grads),
+         _arg(dout, torch.bfloat16, "dout", dev, (total_q, heads, d)), *(x[0] for x in ins),
+         _arg(out, torch.bfloat16, "out", dev, (total_q, heads, d)),
+         _arg(lse, torch.float32, "lse", dev, (total_q, heads)), *(x[1] for x in ins),
+         _arg(cu_seqlens_q, torch.int32, "cu_seqlens_q", dev, (n + 1,)),
+         _arg(cu_seqlens_k, torch.int32, "cu_seqlens_k", dev, (n + 1,)), n, total_q, total_k,
+         int(max_seqlen_q), int(max_seqlen_k), heads, hkv, d, int(sliding_window), float(scale), *b,
+         ws, ws_bytes)
+    return dq, dk, dv, dbias
+
+
+def pa_decode_bias(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   block_table: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int,
+                   scale: float, bias: torch.Tensor, max_distance: int, sliding_window: int = 0,
+                   num_splits: int = 0, key: torch.Tensor | None = None,
+                   value: torch.Tensor | None = None, slot_mapping: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None, workspace: torch.Tensor | None = None
+                   ) -> torch.Tensor:
+    """pa_decode with a learned relative position bias [num_buckets, H] fp32."""
+    lib = _lib or load()
+    dev = _device_of(q, "q")
+    nb, bs, hkv, d = k_cache.shape
+    batch, heads, _ = q.shape
+    width = block_table.shape[-1]
+    max_seq_len, sliding_window, num_splits = int(max_seq_len), int(sliding_window), int(num_splits)
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    new = _step_tokens(key, value, slot_mapping, batch, hkv, d, dev, "pa_decode_bias")
+    b = _bias(bias, max_distance, heads, dev)
+    ws, ws_bytes, workspace = _workspace(
+        workspace, 0 if workspace is not None else pa_decode_workspace_size(
+            batch, heads, hkv, d, max_seq_len, sliding_window, num_splits), dev)
+    _run("pa_decode_bias", lib.pa_decode_bias, dev,
+         _arg(out, torch.bfloat16, "out", dev, (batch, heads, d)),
+         _arg(q, torch.bfloat16, "q", dev, (batch, heads, d)), *new,
+         _arg(k_cache, torch.bfloat16, "k_cache", dev, k_cache.shape),
+         _arg(v_cache, torch.bfloat16, "v_cache", dev, k_cache.shape),
+         _arg(block_table, torch.int32, "block_table", dev, (batch, width)), width,
+         _arg(seq_lens, torch.int32, "seq_lens", dev, (batch,)), batch, max_seq_len, nb, bs, heads,
+         hkv, d, sliding_window, float(scale), *b, num_splits, ws, ws_bytes)
+    return out
+
+
+def pa_varlen_prefill_bias(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           cu_seqlens_q: torch.Tensor, seq_lens: torch.Tensor | None,
+                           block_table: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int,
+                           scale: float, bias: torch.Tensor, max_distance: int,
+                           sliding_window: int = 0, cu_seqlens_k: torch.Tensor | None = None,
+                           key: torch.Tensor | None = None, value: torch.Tensor | None = None,
+                           slot_mapping: torch.Tensor | None = None,
+                           out: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """pa_varlen_prefill with a learned relative position bias [num_buckets, H] fp32."""
+    lib = _lib or load()
+    dev = _device_of(q, "q")
+    nb, bs, hkv, d = k_cache.shape
+    total_q, heads, _ = q.shape
+    n = cu_seqlens_q.shape[0] - 1
+    width = block_table.shape[-1]
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    new = _step_tokens(key, value, slot_mapping, total_q, hkv, d, dev, "pa_varlen_prefill_bias")
+    b = _bias(bias, max_distance, heads, dev)
+    ws, ws_bytes, workspace = _workspace(
+        workspace, 0 if workspace is not None else
+        pa_relative_bias_workspace_size(heads, b[1], b[2]), dev)
+    _run("pa_varlen_prefill_bias", lib.pa_varlen_prefill_bias, dev,
+         _arg(out, torch.bfloat16, "out", dev, (total_q, heads, d)),
+         _arg(q, torch.bfloat16, "q", dev, (total_q, heads, d)), *new,
+         _arg(k_cache, torch.bfloat16, "k_cache", dev, k_cache.shape),
+         _arg(v_cache, torch.bfloat16, "v_cache", dev, k_cache.shape),
+         _arg(cu_seqlens_q, torch.int32, "cu_seqlens_q", dev, (n + 1,)),
+         None if cu_seqlens_k is None else
+         _arg(cu_seqlens_k, torch.int32, "cu_seqlens_k", dev, (n + 1,)),
+         None if seq_lens is None else _arg(seq_lens, torch.int32, "seq_lens", dev, (n,)),
+         _arg(block_table, torch.int32, "block_table", dev, (n, width)), width, n, total_q,
+         int(max_seqlen_q), int(max_seqlen_k), nb, bs, heads, hkv, d, int(sliding_window),
+         float(scale), *b, ws, ws_bytes)
     return out
 
 

@@ -38,6 +38,7 @@
 #include "decode_common.cuh"
 #include "pa_common.cuh"
 #include "pa_internal.h"
+#include "relative_bias.cuh"
 #include "sm100_ptx.cuh"
 
 namespace pa {
@@ -117,6 +118,14 @@ struct DecodeKernelParams {
     unsigned *err;
 };
 
+// The kernels' argument for a learned relative position bias: nothing without one.
+template <bool BIAS>
+struct BiasArg {};
+template <>
+struct BiasArg<true> {
+    RelativeBias b;
+};
+
 __device__ __forceinline__ uint32_t ld_u32(const __nv_bfloat16 *p) {
     return *reinterpret_cast<const uint32_t *>(p);
 }
@@ -142,8 +151,12 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
 // fp8 rows with the head-dim index permuted alike in Q, V fragments from a transposing
 // ldmatrix on byte pairs plus one byte permute (even and odd head dims in separate
 // MMAs).  kv_scale is applied to the scores (K) and the results (V); Q and P are f16.
-template <int D, int NWARPS, int NSTAGES, bool FP8, int NT>
-__device__ __forceinline__ void decode_split_body(const DecodeKernelParams &p) {
+//
+// BIAS: the key at distance n = L - 1 - key has the bias of n's bucket added to its logit.  Keys far
+// enough have the last bucket's (a register per head); the units of the nearest ones, a few at the
+// end of the sequence, look their two keys' buckets up.
+template <int D, int NWARPS, int NSTAGES, bool FP8, int NT, bool BIAS>
+__device__ __forceinline__ void decode_split_body(const DecodeKernelParams &p, const BiasArg<BIAS> &rb) {
     constexpr int ROWB = D * 2;               // bytes of one key row of one kv head
     constexpr int TILE_BYTES = 16 * ROWB;     // 16 keys
     constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K tile then V tile
@@ -438,6 +451,18 @@ __device__ __forceinline__ void decode_split_body(const DecodeKernelParams &p) {
     const int rv = (lane >> 4) * 8 + (lane & 7);
     const int cv = (lane >> 3) & 1;
 
+    // Bias of the last bucket for this lane's heads, in base-2 units.
+    [[maybe_unused]] float far_bias[NT][2];
+    if constexpr (BIAS) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int h = 8 * j + 2 * (lane & 3) + e;
+                far_bias[j][e] = h < rows_valid ? rb.b.bias[(rb.b.num_buckets - 1) * p.num_heads + h0 + h] * kLog2e : 0.f;
+            }
+    }
+
     int it = 0;
     for (int u = my_first; u <= u_last; u += NWARPS, ++it) {
         {
@@ -491,6 +516,27 @@ __device__ __forceinline__ void decode_split_body(const DecodeKernelParams &p) {
         // Scale, mask (edge units only), online softmax per head column: elements 0, 1 are
         // key u*16 + lane/4, elements 2, 3 key + 8; elements 0, 2 head 2t, 1, 3 head 2t+1.
         const bool edge = u * 16 < lo || u * 16 + 16 > hi;
+        [[maybe_unused]] float near_bias[NT][4];
+        if constexpr (BIAS) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) near_bias[j][e] = far_bias[j][e & 1];
+            if (sr.L - 16 - u * 16 < rb.b.last()) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int n = max(sr.L - 1 - (u * 16 + g + 8 * k), 0);
+                    const float *row = rb.b.bias + bucket_of(rb.b, n) * p.num_heads + h0;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int h = 8 * j + 2 * (lane & 3) + e;
+                            if (h < rows_valid) near_bias[j][2 * k + e] = row[h] * kLog2e;
+                        }
+                }
+            }
+        }
         // The reference maximum only moves when a score exceeds it by more than 8, so the
         // column maxima (three dependent shuffles per head) are formed only when some
         // score of the warp does; otherwise nothing changes.
@@ -500,6 +546,7 @@ __device__ __forceinline__ void decode_split_body(const DecodeKernelParams &p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float v = (s[j][e] + s2[j][e]) * p.scale_log2;
+                if constexpr (BIAS) v += near_bias[j][e];
                 if (edge) {
                     const int key = u * 16 + g + (e >> 1) * 8;
                     if (key < lo || key >= hi) v = -INFINITY;
@@ -655,6 +702,7 @@ __device__ __forceinline__ void decode_split_body(const DecodeKernelParams &p) {
             acc += f * o_s[(w * 16 + row) * OSTRIDE + d];
         }
         float res = acc / L;
+        if constexpr (BIAS) res = L > 0.f ? res : 0.f;  // (a bias of -inf can hide every key)
         if constexpr (FP8) res *= p.kv_scale;  // V elements read code * kv_scale
         const int64_t bh = static_cast<int64_t>(b) * p.num_heads + h0 + row;
         if (p.ws_o == nullptr) {
@@ -670,9 +718,10 @@ __device__ __forceinline__ void decode_split_body(const DecodeKernelParams &p) {
     }
 }
 
-template <int D, int NWARPS, int NSTAGES, bool FP8, int NT>
-__global__ void __launch_bounds__(NWARPS * 32, (decode_ctas_per_sm<FP8, NT>())) decode_split_kernel(const DecodeKernelParams p) {
-    decode_split_body<D, NWARPS, NSTAGES, FP8, NT>(p);
+template <int D, int NWARPS, int NSTAGES, bool FP8, int NT, bool BIAS>
+__global__ void __launch_bounds__(NWARPS * 32, (decode_ctas_per_sm<FP8, NT>()))
+    decode_split_kernel(const DecodeKernelParams p, const __grid_constant__ BiasArg<BIAS> rb) {
+    decode_split_body<D, NWARPS, NSTAGES, FP8, NT, BIAS>(p, rb);
     // As a programmatic dependent of the prefill kernel of the same call (single-row
     // sequences of a varlen batch, or a cascade's suffix) the CTAs run beside the prefill
     // on the SMs it leaves free.  The grid's last CTA waits for the prefill grid, so this
@@ -801,17 +850,17 @@ constexpr int decode_smem_bytes() {
     return FP8 ? kDecodeWarps * kFp8Stages * 2 * 16 * D : kDecodeWarps * kDecodeStages * 2 * 16 * D * 2;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool BIAS = false>
 cudaError_t launch_decode_d(const DecodeKernelParams &kp, const DecodePlan &plan, int batch,
-                            cudaStream_t stream) {
+                            cudaStream_t stream, const BiasArg<BIAS> &rb = {}) {
     constexpr int smem = decode_smem_bytes<D, FP8>();
     static_assert(smem >= (kDecodeWarps * 16 * 2 + kDecodeWarps * 16 * (D + 4)) * 4,
                   "merge area must fit in the stage ring");
     // 8 heads per n-tile: a group of at most 8 query heads takes one, larger ones two.
     static std::atomic<uint64_t> smem_set[2];
     const int nt = kp.group <= 8 ? 0 : 1;
-    auto kern = nt == 0 ? decode_split_kernel<D, kDecodeWarps, kDecodeStages, FP8, 1>
-                        : decode_split_kernel<D, kDecodeWarps, kDecodeStages, FP8, 2>;
+    auto kern = nt == 0 ? decode_split_kernel<D, kDecodeWarps, kDecodeStages, FP8, 1, BIAS>
+                        : decode_split_kernel<D, kDecodeWarps, kDecodeStages, FP8, 2, BIAS>;
     cudaError_t e = smem_limit_once(kern, smem, smem_set[nt]);
     if (e != cudaSuccess) return e;
     dim3 grid(plan.num_splits, kp.num_kv_heads * plan.head_tiles, batch);
@@ -829,10 +878,10 @@ cudaError_t launch_decode_d(const DecodeKernelParams &kp, const DecodePlan &plan
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        e = cudaLaunchKernelEx(&cfg, kern, kp);
+        e = cudaLaunchKernelEx(&cfg, kern, kp, rb);
         if (e != cudaSuccess) return e;
     } else {
-        kern<<<grid, kDecodeWarps * 32, smem, stream>>>(kp);
+        kern<<<grid, kDecodeWarps * 32, smem, stream>>>(kp, rb);
     }
     e = cudaGetLastError();
     if (e != cudaSuccess || (plan.num_splits == 1 && kp.st_o == nullptr && kp.pre_parts == 0))
@@ -974,6 +1023,14 @@ cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStrea
         switch (a.head_dim) {
             case 64: return launch_decode_d<64, true>(kp, plan, a.batch, stream);
             case 128: return launch_decode_d<128, true>(kp, plan, a.batch, stream);
+            default: return cudaErrorInvalidValue;
+        }
+    }
+    if (a.bias.bias != nullptr) {
+        const BiasArg<true> rb{a.bias};
+        switch (a.head_dim) {
+            case 64: return launch_decode_d<64, false, true>(kp, plan, a.batch, stream, rb);
+            case 128: return launch_decode_d<128, false, true>(kp, plan, a.batch, stream, rb);
             default: return cudaErrorInvalidValue;
         }
     }

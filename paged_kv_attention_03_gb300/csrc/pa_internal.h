@@ -2,6 +2,7 @@
 // Arguments reaching these launchers have already been validated on the host.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -12,6 +13,23 @@
 #include "pa_gb300.h"
 
 namespace pa {
+
+// ---------------------------------------------------- relative position bias ---
+constexpr int kMaxBuckets = 128;
+constexpr int kMaxBiasDistance = 32768;
+// bias[bucket(n)][head] is added to the logit of a key at distance n; bucket b begins at distance
+// first[b], first[num_buckets] is beyond every distance.
+struct RelativeBias {
+    const float *bias;  // [num_buckets, num_heads]; null: no bias
+    int num_buckets;
+    int first[kMaxBuckets + 1];
+    __host__ __device__ int last() const { return num_buckets > 0 ? first[num_buckets - 1] : 0; }
+};
+// Fills num_buckets and first; false when the sizes are not supported.
+bool plan_relative_bias(int num_buckets, int max_distance, RelativeBias *b);
+// The bias by distance in base-2 units, for every head: relative_bias.cuh.
+size_t bias_table_bytes(int num_heads, const RelativeBias &b);
+cudaError_t launch_bias_table(float *table, int num_heads, const RelativeBias &b, cudaStream_t stream);
 
 // ------------------------------------------------------------------ store ---
 struct StoreArgs {
@@ -149,6 +167,8 @@ struct DecodeArgs {
     // once all its CTAs are resident).  The split CTAs run beside the prefill; the grid's
     // last CTA waits for the prefill grid before it exits.
     bool after_prefill;
+    // Learned relative position bias (bias.bias null: none), bf16 caches.
+    RelativeBias bias;
     unsigned *err;
 };
 cudaError_t launch_decode(const DecodeArgs &a, const DecodePlan &plan, cudaStream_t stream);
@@ -170,8 +190,9 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, const DecodeFp4Plan &plan, cu
 
 // ---------------------------------------------------------------- prefill ---
 // What the cache holds: bf16, E4M3 codes, or 4-bit rows (fp4.cuh).
-// (kCacheExpanded: 4-bit rows that the call itself expanded to 16 bits.)
-enum : int { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheFp4 = 2, kCacheExpanded = 3 };
+// (kCacheExpanded: 4-bit rows that the call itself expanded to 16 bits; kCachePacked: no cache,
+// plain rows of packed sequences.)
+enum : int { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheFp4 = 2, kCacheExpanded = 3, kCachePacked = 4 };
 struct PrefillArgs {
     void *out;
     const void *q;
@@ -201,6 +222,13 @@ struct PrefillArgs {
     // cache (two halves of prefill_fp4_scratch_bytes) or null.
     void *workspace;
     void *scratch;
+    // Relative position bias (null: none): the table of launch_bias_table for the prefill kernel,
+    // the bias itself for the decode rows.
+    const float *bias_table;
+    int bias_last;
+    RelativeBias bias;
+    // Elements from one row of q / packed k / v to the next (q: 0 for contiguous rows).
+    int64_t q_stride, k_stride, v_stride;
     unsigned *err;
 };
 size_t prefill_fp4_scratch_bytes(int num_seqs, int num_kv_heads, int head_dim, int max_seqlen_k);
@@ -211,6 +239,52 @@ bool prefill_fp4_expands(int group, int max_seqlen_q);
 bool prefill_fits(int num_seqs, int num_kv_heads, int group, int64_t total_q, int max_seqlen_q,
                   int64_t slots);
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);
+
+// ------------------------------------------------------- packed attention ---
+// Packed sequences on plain rows: q [total_q, num_heads, head_dim], k / v [total_k, num_kv_heads,
+// head_dim], a token's heads contiguous, tokens a stride apart.
+struct PackedArgs {
+    const void *q;
+    const void *k;
+    const void *v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *cu_seqlens_q;
+    const int32_t *cu_seqlens_k;
+    int num_seqs;
+    int total_q, total_k;
+    int max_seqlen_q, max_seqlen_k;
+    int num_heads;
+    int num_kv_heads;
+    int head_dim;
+    int sliding_window;
+    float scale;
+    RelativeBias bias;        // bias.bias null: none
+    const float *bias_table;  // its table (launch_bias_table), null without a bias
+    unsigned *err;
+};
+cudaError_t launch_packed_attn(const PackedArgs &a, void *out, float *lse, cudaStream_t stream);
+
+struct PackedGradArgs {
+    PackedArgs fwd;
+    const void *out;   // [total_q, num_heads, head_dim]
+    const void *dout;
+    const float *lse;  // [total_q, num_heads]
+    void *dq;
+    void *dk;
+    void *dv;
+    int64_t dq_stride, dk_stride, dv_stride;
+    float *dbias;      // [num_buckets, num_heads]
+    void *workspace;   // packed_grad_workspace
+};
+// Bytes of the backward pass's workspace behind the bias table; false: too large for the kernels' counters.
+bool packed_grad_workspace(int total_q, int num_seqs, int num_heads, int num_buckets, size_t *bytes);
+cudaError_t launch_packed_attn_backward(const PackedGradArgs &a, cudaStream_t stream);
+
+// Tensor map of [d2][d1][d0] 16-bit elements (codes: bytes), boxes [b2][b1][b0], 128-byte swizzle.
+bool encode_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,
+               uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t b0, uint32_t b1,
+               uint32_t b2, bool codes = false);
+
 // Testing aid behind pa_debug_prefill_stall (process-wide; read at each prefill launch).
 void debug_prefill_stall(int stall, uint64_t wait_ns);
 

@@ -50,6 +50,7 @@
 #include "fp4.cuh"
 #include "pa_common.cuh"
 #include "pa_internal.h"
+#include "relative_bias.cuh"
 #include "sm100_ptx.cuh"
 
 namespace pa {
@@ -123,6 +124,13 @@ struct PrefillKernelParams {
     int expanded_blocks;  // expanded 4-bit cache: blocks of a sequence in the scratch cache
     uint64_t wait_ns;  // limit of every wait (kTimeoutNs unless a test lowers it)
     int stall;         // testing aid: publish no work item, so every wait runs out
+    // Packed K / V (kCachePacked): rows of k / v, and where the rows' log-sum-exp goes.
+    int total_k;
+    float *lse;  // [total_q, num_heads]
+    // Relative position bias (BIAS): relative_bias.cuh's table; distances from bias_last on share
+    // one value.
+    const float *bias_table;
+    int bias_last;
     unsigned *err;
 };
 
@@ -183,7 +191,10 @@ constexpr int kConsumersPerItem = 11;  // K and V producers, MMA issuer, 8 softm
 
 // PREFIX: the shared-prefix (cascade) mode; item idx = (split, query-tile pair, kv head),
 // the requests play the tokens of one sequence whose keys are the prefix.
-template <bool PREFIX>
+// PACKED: keys cu_k[i] .. cu_k[i + 1] - 1 of plain K / V; the item keeps the first one's row in
+// `split`.  More queries than keys are allowed there: the first rows see nothing, and an item of
+// such rows alone has no tiles.
+template <bool PREFIX, bool PACKED>
 __device__ __forceinline__ Item get_item(const PrefillKernelParams &p, int idx, bool report) {
     Item it;
     it.split = 0;
@@ -229,21 +240,28 @@ __device__ __forceinline__ Item get_item(const PrefillKernelParams &p, int idx, 
         return it;
     }
     int sk;
-    if (p.seq_lens != nullptr) {
+    if constexpr (PACKED) {
+        it.split = p.cu_k[it.seq];
+        sk = p.cu_k[it.seq + 1] - it.split;
+        if (it.split < 0 || sk < 0 || static_cast<int64_t>(it.split) + sk > p.total_k || sk > p.seq_cap) {
+            if (report) flag_error(p.err, kErrSeqRange);
+            return it;
+        }
+    } else if (p.seq_lens != nullptr) {
         sk = p.seq_lens[it.seq];
         if (report && p.cu_k != nullptr && p.cu_k[it.seq + 1] - p.cu_k[it.seq] != sk)
             flag_error(p.err, kErrSeqlensK);
     } else {
         sk = p.cu_k[it.seq + 1] - p.cu_k[it.seq];
     }
-    if (sk < 0 || static_cast<int64_t>(sk) > p.seq_cap) {
+    if (!PACKED && (sk < 0 || static_cast<int64_t>(sk) > p.seq_cap)) {
         if (report) flag_error(p.err, kErrSeqRange);
         sk = sk < 0 ? 0 : static_cast<int>(p.seq_cap);
     }
     it.sk = sk;
-    if (it.sq < 0 || it.sq > sk || it.sq > p.max_seqlen_q) {
+    if (it.sq < 0 || (!PACKED && it.sq > sk) || it.sq > p.max_seqlen_q) {
         if (report) flag_error(p.err, kErrQueryLen);
-        if (it.sq < 0 || it.sq > sk) return it;
+        if (it.sq < 0 || PACKED || it.sq > sk) return it;
     }
     if (p.skip_decode_rows && it.sq == 1) return it;  // the decode launch's row
     const int T = p.tok_per_tile;
@@ -256,53 +274,10 @@ __device__ __forceinline__ Item get_item(const PrefillKernelParams &p, int idx, 
     const int p_hi = p_lo + it.rows0 + it.rows1 - 1;
     const int kmin = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;
     it.kt0 = kmin / BN;
-    it.n_tiles = p_hi / BN - it.kt0 + 1;
+    it.n_tiles = PACKED && p_hi < 0 ? 0 : p_hi / BN - it.kt0 + 1;
     it.half_last = p_hi < (it.kt0 + it.n_tiles - 1) * BN + BN / 2;
     it.valid = true;
     return it;
-}
-
-// Bounded wait by one thread.
-__device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                      unsigned *err, uint64_t limit_ns) {
-    uint64_t t0 = 0;
-    for (uint32_t it = 0;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 31u) == 31u) {
-            if (*abort_flag) return false;
-            const uint64_t now = globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > limit_ns) {
-                *abort_flag = 1;
-                flag_error(err, kErrTimeout);
-                return false;
-            }
-        }
-    }
-}
-
-// Bounded wait by a whole warp; every lane returns the same answer.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity,
-                                          volatile int *abort_flag, unsigned *err,
-                                          uint64_t limit_ns) {
-    uint64_t t0 = 0;
-    for (uint32_t it = 0;; ++it) {
-        const bool ok = mbar_try_wait(bar, parity);
-        if (__all_sync(0xffffffffu, ok)) return true;
-        if ((it & 31u) == 31u) {
-            bool stop = *abort_flag != 0;
-            const uint64_t now = globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            stop = stop || (now - t0 > limit_ns);
-            if (__any_sync(0xffffffffu, stop)) {
-                if ((threadIdx.x & 31) == 0) {
-                    *abort_flag = 1;
-                    flag_error(err, kErrTimeout);
-                }
-                return false;
-            }
-        }
-    }
 }
 
 // ------------------------------------------------------------------ scheduler ---
@@ -315,7 +290,7 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity,
 // and V producers can run ahead across short items.  Q loads go through the callbacks:
 // q_free(l) (non-blocking) / q_wait(l) (bounded) tell whether the buffer of load l is free,
 // q_load(l, item, next item or null) issues it.
-template <bool PREFIX, class QFree, class QWait, class QLoad>
+template <bool PREFIX, bool PACKED, class QFree, class QWait, class QLoad>
 __device__ __forceinline__ void schedule_items(const PrefillKernelParams &p, ItemSlot *info,
                                                uint32_t bar_ifull, uint32_t bar_iempty,
                                                volatile int *abort_flag, uint32_t P,
@@ -383,7 +358,7 @@ __device__ __forceinline__ void schedule_items(const PrefillKernelParams &p, Ite
                 // Scan 32 pairs: the kv heads of a pair are all valid or none.
                 const int pp = scan + lane;
                 const bool v = pp < n_pairs &&
-                               get_item<PREFIX>(p, pp * Hkv,
+                               get_item<PREFIX, PACKED>(p, pp * Hkv,
                                                 reporter && static_cast<uint32_t>(pp) % P == cta)
                                    .valid;
                 const uint32_t vm = __ballot_sync(0xffffffffu, v);
@@ -416,7 +391,7 @@ __device__ __forceinline__ void schedule_items(const PrefillKernelParams &p, Ite
             }
             const int idx = (win + cur) * Hkv + static_cast<int>(tv - cur_r0);
             if (lane == 0) {
-                const Item it = get_item<PREFIX>(p, idx, false);
+                const Item it = get_item<PREFIX, PACKED>(p, idx, false);
                 if (pub >= kRing && !wait1(iempty(pub % kRing), ((pub / kRing) - 1) & 1,
                                            abort_flag, p.err, p.wait_ns)) {
                     ok = false;
@@ -445,22 +420,6 @@ __device__ __forceinline__ void schedule_items(const PrefillKernelParams &p, Ite
         info[pub % kRing].end = 1;
         mbar_arrive(ifull(pub % kRing));
     }
-}
-
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                             uint32_t d) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-                 "r"(d)
-                 : "memory");
 }
 
 // One 128-key tile of E4M3 codes, [128 rows][128 codes] in the upper half of a stage with
@@ -547,12 +506,16 @@ __device__ __forceinline__ void convert_tile_fp4(uint32_t stage, int lane) {
 // CACHE kCacheExpanded: the sequences' 4-bit rows were expanded into a scratch cache, K as bf16
 // (as the queries are) and V as f16 (as the weights are); the producers are the bf16 ones, and
 // sequence i has the scratch blocks i * expanded_blocks ...
-template <int HD, bool PREFIX, int CACHE>
+// CACHE kCachePacked: K and V are plain [total_k, Hkv, HD] rows; the log-sum-exp of each row is
+// written too.
+// BIAS: a learned bias by the distance pos - key is added to the logits.
+template <int HD, bool PREFIX, int CACHE, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillKernelParams p) {
     constexpr bool FP4 = CACHE == kCacheFp4;
     constexpr bool CODES = CACHE == kCacheE4m3 || FP4;  // codes in the cache, S in f16
-    constexpr bool PV16 = CACHE != kCacheBf16;          // P and V in f16
+    constexpr bool PACKED = CACHE == kCachePacked;
+    constexpr bool PV16 = CACHE != kCacheBf16 && !PACKED;  // P and V in f16
     static_assert(CACHE != kCacheE4m3 || HD == 128, "the E4M3 cache path is built for head_dim 128");
     static_assert(!CODES || !PREFIX, "the shared-prefix mode is built for bf16 caches");
     using L = Layout<HD>;
@@ -628,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // out-of-range row (zero fill) past the sequence or for an invalid block index.
     auto kv_row = [&](const Item &it, int k0) -> int {
         if (k0 >= it.sk) return -16;
+        if constexpr (PACKED) return it.split + k0;
         if constexpr (CACHE == kCacheExpanded) return ((it.seq * p.expanded_blocks) << p.log2_bs) + k0;
         const int blk = __ldg(p.block_table + static_cast<int64_t>(it.seq) * p.max_num_blocks +
                               (k0 >> p.log2_bs));
@@ -719,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             };
-            schedule_items<PREFIX>(p, info, bar(B_IFULL), bar(B_IEMPTY), abort_flag, gridDim.x,
+            schedule_items<PREFIX, PACKED>(p, info, bar(B_IFULL), bar(B_IEMPTY), abort_flag, gridDim.x,
                                    blockIdx.x, true, q_free, q_wait, q_load);
         } else if (warp == kWarpK || warp == kWarpV) {
             // ---------------- K / V producer (whole warp) ----------------
@@ -933,6 +897,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         prev_half = half;
                     }
                     if (!ok) break;
+                    // (An item without tiles read no Q.)
+                    if (PACKED && it.n_tiles == 0) mma_commit(bar(B_QEMPTY));
                 }
                 if (ok) flush();
             }
@@ -1003,6 +969,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pos = it.sk - it.sq + it.q0 + tok;
                 lo = w > 0 ? pos - w + 1 : INT_MIN;
             }
+            [[maybe_unused]] const float *bias_row = nullptr;  // entry of distance 0
+            [[maybe_unused]] float far_bias = 0.f;
+            if constexpr (BIAS) {
+                bias_row = bias_row_of(p.bias_table, min(it.kvh * G + g, p.num_heads - 1), p.bias_last);
+                far_bias = __ldg(bias_row + p.bias_last);
+            }
             float m_ref = -INFINITY;  // reference max (base-2 units) the weights use
             float l_sum = 0.f;
             for (int j = 0; j < it.n_tiles; ++j, ++gt, ++c) {
@@ -1020,6 +992,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float *s = &sc[0][0];
 
                 const int key0 = (it.kt0 + j) * BN;
+                // x = mul * s + add is the logit in base 2.  With a bias, chunks of 32 keys nearer than
+                // bias_last take it from the table (future keys' entries are whatever stands
+                // before the distance 0 and are masked below); a tile without any such chunk
+                // has one bias, which is added to the row's maximum instead of its logits.
+                float mul = sl2, add = 0.f;
+                if constexpr (BIAS) {
+                    add = far_bias;
+                    const int d0 = pos - key0;  // distance to the tile's first key
+                    if (__shfl_sync(0xffffffffu, d0, 0) - (BN - 1) < p.bias_last) {
+                        mul = 1.f;
+                        add = 0.f;
+#pragma unroll
+                        for (int cc = 0; cc < BN / 32; ++cc) {
+                            const int dc = d0 - cc * 32;
+                            const bool future = __shfl_sync(0xffffffffu, dc, 31) < 0;
+                            if (future || __shfl_sync(0xffffffffu, dc, 0) - 31 >= p.bias_last) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) sc[cc][i] = fmaf(sc[cc][i], sl2, far_bias);
+                            } else {
+                                const float *bt = bias_row + dc;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) sc[cc][i] = fmaf(sc[cc][i], sl2, __ldg(bt - i));
+                            }
+                        }
+                    }
+                }
                 // Row maximum as 8 independent 3-input max chains, then a tree (a single
                 // dependent chain of 128 maxima would cost ~4 cycles per element).
                 // Edge tiles: the causal bound and the window's lower bound are masked
@@ -1050,7 +1048,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int a = 0; a < 8; ++a) mx8[a] = fmaxf(mx8[a], s[a + 120]);
                 const float mx = fmaxf(fmaxf(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5])),
                                        fmaxf(mx8[6], mx8[7]));
-                const float m_new = fmaxf(m_ref, mx * sl2);
+                const float m_new = fmaxf(m_ref, BIAS ? fmaf(mx, mul, add) : mx * sl2);
                 if (j == 0) {
                     m_ref = m_new;  // O holds nothing of this item yet
                 } else {
@@ -1079,8 +1077,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // Pairs of columns go through packed f32x2 arithmetic; 2^x on the MUFU unit
                 // (moving part of it to a polynomial on the FMA pipe measured slower: the
                 // softmax is bound by instruction issue).
-                const uint64_t sl2x2 = f2_pack(sl2, sl2);
-                const uint64_t negm2 = f2_pack(-m_use, -m_use);
+                const float neg = BIAS ? add - m_use : -m_use;
+                const uint64_t sl2x2 = f2_pack(mul, mul);
+                const uint64_t negm2 = f2_pack(neg, neg);
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};  // partial sums of the bf16 weights
 #pragma unroll
                 for (int cc = 0; cc < 2; ++cc) {
@@ -1094,6 +1093,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if constexpr (PV16) {
                             pk[i] = pack_f16x2(ex2_approx(x0), ex2_approx(x1));
                             add_f16x2_f32(acc[2 * (i & 1)], acc[2 * (i & 1) + 1], pk[i]);
+                        } else if constexpr (PACKED) {
+                            // (The sum behind lse takes the weights as they are: rounded ones
+                            // would leave it a bf16's error off in rows of few keys.)
+                            const float w0 = ex2_approx(x0), w1 = ex2_approx(x1);
+                            pk[i] = pack_bf16x2(w0, w1);
+                            acc[2 * (i & 1)] += w0;
+                            acc[2 * (i & 1) + 1] += w1;
                         } else {
                             pk[i] = pack_bf16x2(ex2_approx(x0), ex2_approx(x1));
                             add_bf16x2_f32(acc[2 * (i & 1)], acc[2 * (i & 1) + 1], pk[i]);
@@ -1128,6 +1134,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(bar(B_PFULL + wg));
             }
             if (!ok) break;
+            if constexpr (PACKED) {
+                const int64_t r = static_cast<int64_t>(it.q_start + it.q0 + tok) * p.num_heads + it.kvh * G + g;
+                if (it.n_tiles == 0) {  // no row of the item sees a key
+                    if (valid) {
+                        uint4 *d4 = reinterpret_cast<uint4 *>(p.out + r * HD);
+                        for (int i = 0; i < HD / 8; ++i) d4[i] = make_uint4(0u, 0u, 0u, 0u);
+                        p.lse[r] = -INFINITY;
+                    }
+                    continue;
+                }
+                if (valid) p.lse[r] = l_sum > 0.f ? (m_ref + log2f(l_sum)) * kLn2 : -INFINITY;
+            }
             // ---- epilogue: O / l -> bf16 rows (P V of the item's last tile is number c-1) ----
             if (!wait_warp(bar(B_ODONE + wg), (c - 1) & 1, abort_flag, p.err, p.wait_ns)) {
                 ok = false;
@@ -1382,9 +1400,11 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
     return fn;
 }
 
+}  // namespace
+
 bool encode_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,
                uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t b0, uint32_t b1,
-               uint32_t b2, bool codes = false) {
+               uint32_t b2, bool codes) {
     auto fn = get_encode_fn();
     if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {d0, d1, d2};
@@ -1399,6 +1419,8 @@ bool encode_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uin
     return r == CUDA_SUCCESS;
 }
 
+namespace {
+
 int sm_count() {
     static std::atomic<int> counts[64];
     int dev = 0;
@@ -1412,12 +1434,14 @@ int sm_count() {
     return n;
 }
 
-template <int HD, bool PREFIX, int CACHE = kCacheBf16>
+template <int HD, bool PREFIX, int CACHE = kCacheBf16, bool BIAS = false>
 cudaError_t launch_prefill_d(PrefillKernelParams &kp, const PrefillArgs &a, cudaStream_t stream) {
     using L = Layout<HD>;
     const int64_t slots = a.num_blocks * a.block_size;
-    if (!encode_3d(&kp.tmap_q, a.q, HD, a.num_heads, a.total_q, HD * 2ull,
-                   static_cast<uint64_t>(a.num_heads) * HD * 2ull, 64, kp.group, kp.tok_per_tile))
+    const int64_t q_stride = a.q_stride > 0 ? a.q_stride : static_cast<int64_t>(a.num_heads) * HD;
+    const int64_t kv_stride = static_cast<int64_t>(a.num_kv_heads) * HD;
+    if (!encode_3d(&kp.tmap_q, a.q, HD, a.num_heads, a.total_q, HD * 2ull, q_stride * 2ull, 64, kp.group,
+                   kp.tok_per_tile))
         return cudaErrorInvalidValue;
     // K / V boxes: one 16-row piece of a page and a 64-dim half (bf16), or the piece's whole
     // rows of codes (FP8).
@@ -1427,10 +1451,10 @@ cudaError_t launch_prefill_d(PrefillKernelParams &kp, const PrefillArgs &a, cuda
     for (int kv = 0; kv < 2 && CACHE != kCacheFp4; ++kv) {
         if (!encode_3d(kv ? &kp.tmap_v : &kp.tmap_k, kv ? a.v_cache : a.k_cache, HD,
                        a.num_kv_heads, static_cast<uint64_t>(slots), HD * eb,
-                       static_cast<uint64_t>(a.num_kv_heads) * HD * eb, FP8 ? HD : 64, 1, 16, FP8))
+                       (CACHE != kCachePacked ? kv_stride : kv ? a.v_stride : a.k_stride) * eb, FP8 ? HD : 64, 1, 16, FP8))
             return cudaErrorInvalidValue;
     }
-    auto kern = prefill_kernel<HD, PREFIX, CACHE>;
+    auto kern = prefill_kernel<HD, PREFIX, CACHE, BIAS>;
     static std::atomic<uint64_t> smem_set;
     cudaError_t e = smem_limit_once(kern, static_cast<int>(L::SMEM), smem_set);
     if (e != cudaSuccess) return e;
@@ -1529,6 +1553,8 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
     kp.scale_log2 = a.scale * kp.kv_scale * kLog2e;  // codes: K elements are times kv_scale
     kp.k4 = static_cast<const uint8_t *>(a.k_cache);
     kp.v4 = static_cast<const uint8_t *>(a.v_cache);
+    kp.bias_table = a.bias_table;
+    kp.bias_last = a.bias_last;
     kp.err = a.err;
     set_launch_limits(kp);
     // Sequences with a single query row (decode rows of a mixed batch) would fill one
@@ -1552,6 +1578,12 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
             switch (a.head_dim) {
                 case 64: e = launch_prefill_d<64, false, kCacheFp4>(kp, a, stream); break;
                 case 128: e = launch_prefill_d<128, false, kCacheFp4>(kp, a, stream); break;
+                default: return cudaErrorInvalidValue;
+            }
+        } else if (a.bias_table != nullptr) {
+            switch (a.head_dim) {
+                case 64: e = launch_prefill_d<64, false, kCacheBf16, true>(kp, a, stream); break;
+                case 128: e = launch_prefill_d<128, false, kCacheBf16, true>(kp, a, stream); break;
                 default: return cudaErrorInvalidValue;
             }
         } else {
@@ -1588,6 +1620,7 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
     d.fp8 = a.cache == kCacheE4m3;
     d.kv_scale = a.kv_scale;
     d.after_prefill = prefill_launched;
+    d.bias = a.bias;
     d.err = a.err;
     if (a.cache == kCacheFp4) {
         DecodeFp4Plan plan;
@@ -1602,6 +1635,59 @@ cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream) {
                      a.sliding_window, 1, &plan))
         return cudaErrorInvalidValue;
     return launch_decode(d, plan, stream);
+}
+
+cudaError_t launch_packed_attn(const PackedArgs &a, void *out, float *lse, cudaStream_t stream) {
+    PrefillKernelParams kp;
+    memset(&kp, 0, sizeof kp);
+    kp.out = static_cast<__nv_bfloat16 *>(out);
+    kp.lse = lse;
+    kp.cu_q = a.cu_seqlens_q;
+    kp.cu_k = a.cu_seqlens_k;
+    kp.num_seqs = a.num_seqs;
+    kp.total_q = a.total_q;
+    kp.total_k = a.total_k;
+    kp.max_seqlen_q = a.max_seqlen_q;
+    kp.seq_cap = a.max_seqlen_k;
+    kp.num_heads = a.num_heads;
+    kp.num_kv_heads = a.num_kv_heads;
+    kp.group = a.num_heads / a.num_kv_heads;
+    kp.tok_per_tile = BM / kp.group;
+    kp.q_items = static_cast<int>(query_items(kp.group, a.max_seqlen_q));
+    kp.n_items = kp.q_items * a.num_kv_heads * a.num_seqs;
+    kp.window = a.sliding_window;
+    kp.kv_scale = 1.f;
+    kp.scale_log2 = a.scale * kLog2e;
+    kp.bias_table = a.bias_table;
+    kp.bias_last = a.bias.last();
+    kp.err = a.err;
+    set_launch_limits(kp);
+    // The launcher's view of the call: a cache of one-row blocks.
+    PrefillArgs x{};
+    x.q = a.q;
+    // (With no key at all nothing is loaded, but a tensor map has a row and an address.)
+    const bool keys = a.total_k > 0;
+    x.k_cache = keys ? a.k : a.q;
+    x.v_cache = keys ? a.v : a.q;
+    x.q_stride = a.q_stride;
+    x.k_stride = keys ? a.k_stride : static_cast<int64_t>(a.num_kv_heads) * a.head_dim;
+    x.v_stride = keys ? a.v_stride : x.k_stride;
+    x.total_q = a.total_q;
+    x.num_blocks = keys ? a.total_k : 1;
+    x.block_size = 1;
+    x.num_heads = a.num_heads;
+    x.num_kv_heads = a.num_kv_heads;
+    x.head_dim = a.head_dim;
+    const bool bias = a.bias_table != nullptr;
+    switch (a.head_dim) {
+        case 64:
+            return bias ? launch_prefill_d<64, false, kCachePacked, true>(kp, x, stream)
+                        : launch_prefill_d<64, false, kCachePacked>(kp, x, stream);
+        case 128:
+            return bias ? launch_prefill_d<128, false, kCachePacked, true>(kp, x, stream)
+                        : launch_prefill_d<128, false, kCachePacked>(kp, x, stream);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 void plan_prefix_splits(int num_req, int num_heads, int num_kv_heads, int prefix_len,

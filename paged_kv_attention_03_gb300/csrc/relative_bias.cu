@@ -1,0 +1,87 @@
+// relative_bias.cu - buckets of a learned relative position bias, and its table by distance.
+//
+// A distance n = query position - key position >= 0 has bucket n below m = num_buckets / 2, and
+// beyond it min(num_buckets - 1, m + floor(ln(n / m) / ln(max_distance / m) (num_buckets - m))).
+// The floor is that of the real number: bucket m + j begins at the smallest n with
+//     n^r >= m^(r - j) max_distance^j,   r = num_buckets - m,
+// which is found in double precision and, where the border is next to a whole number, decided
+// in whole numbers.
+#include <math.h>
+
+#include <vector>
+
+#include "pa_common.cuh"
+#include "relative_bias.cuh"
+
+namespace pa {
+
+namespace {
+
+// x *= f, least significant word first.
+void multiply(std::vector<uint32_t> &x, uint32_t f) {
+    uint64_t carry = 0;
+    for (uint32_t &w : x) {
+        carry += static_cast<uint64_t>(w) * f;
+        w = static_cast<uint32_t>(carry);
+        carry >>= 32;
+    }
+    if (carry != 0) x.push_back(static_cast<uint32_t>(carry));
+}
+
+// n^r >= m^(r - j) d^j
+bool reaches(int n, int m, int d, int r, int j) {
+    std::vector<uint32_t> a{1}, b{1};
+    for (int i = 0; i < r; ++i) multiply(a, n);
+    for (int i = 0; i < r; ++i) multiply(b, i < j ? d : m);
+    if (a.size() != b.size()) return a.size() > b.size();
+    for (size_t i = a.size(); i-- > 0;)
+        if (a[i] != b[i]) return a[i] > b[i];
+    return true;
+}
+
+// One thread an entry; a bucket's first distances are read through the kernel's parameters.
+__global__ void __launch_bounds__(128)
+    bias_table_kernel(float *__restrict__ table, const __grid_constant__ RelativeBias b, int num_heads) {
+    const int stride = bias_stride(b.last());
+    const int i = blockIdx.x * 128 + threadIdx.x;
+    if (i >= stride) return;
+    const int k = bucket_of(b, max(i - kBiasPad, 0));
+    // (A block's heads in turn: the search is shared.)
+    for (int h = blockIdx.y; h < num_heads; h += gridDim.y)
+        table[static_cast<int64_t>(h) * stride + i] = b.bias[static_cast<int64_t>(k) * num_heads + h] * kLog2e;
+}
+
+}  // namespace
+
+bool plan_relative_bias(int num_buckets, int max_distance, RelativeBias *b) {
+    if (num_buckets < 2 || num_buckets > kMaxBuckets) return false;
+    const int m = num_buckets / 2, r = num_buckets - m;
+    if (max_distance <= m || max_distance > kMaxBiasDistance) return false;
+    b->num_buckets = num_buckets;
+    for (int i = 0; i <= m; ++i) b->first[i] = i;
+    for (int j = 1; j < r; ++j) {
+        const double x = m * pow(static_cast<double>(max_distance) / m, static_cast<double>(j) / r);
+        const double whole = nearbyint(x);
+        int n = static_cast<int>(ceil(x));
+        // pow is within a few units of its last place; distances are below 2^15.
+        if (fabs(x - whole) < 1e-9 * x) {
+            n = static_cast<int>(whole);
+            if (!reaches(n, m, max_distance, r, j)) ++n;
+        }
+        b->first[m + j] = n;
+    }
+    b->first[num_buckets] = 1 << 30;
+    return true;
+}
+
+size_t bias_table_bytes(int num_heads, const RelativeBias &b) {
+    return (static_cast<size_t>(num_heads) * bias_stride(b.last()) * sizeof(float) + 255) / 256 * 256;
+}
+
+cudaError_t launch_bias_table(float *table, int num_heads, const RelativeBias &b, cudaStream_t stream) {
+    const dim3 grid((bias_stride(b.last()) + 127) / 128, num_heads < 64 ? num_heads : 64);
+    bias_table_kernel<<<grid, 128, 0, stream>>>(table, b, num_heads);
+    return cudaGetLastError();
+}
+
+}  // namespace pa

@@ -341,5 +341,65 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
 }
 
 
+// ------------------------------------------------------------ bounded waits ---
+// Bounded wait by one thread.
+__device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity, volatile int *abort_flag,
+                                      unsigned *err, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 31u) == 31u) {
+            if (*abort_flag) return false;
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > limit_ns) {
+                *abort_flag = 1;
+                flag_error(err, kErrTimeout);
+                return false;
+            }
+        }
+    }
+}
+
+// Bounded wait by a whole warp; every lane returns the same answer.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity,
+                                          volatile int *abort_flag, unsigned *err,
+                                          uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        const bool ok = mbar_try_wait(bar, parity);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if ((it & 31u) == 31u) {
+            bool stop = *abort_flag != 0;
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            stop = stop || (now - t0 > limit_ns);
+            if (__any_sync(0xffffffffu, stop)) {
+                if ((threadIdx.x & 31) == 0) {
+                    *abort_flag = 1;
+                    flag_error(err, kErrTimeout);
+                }
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+
 }  // namespace sm100
 }  // namespace pa
