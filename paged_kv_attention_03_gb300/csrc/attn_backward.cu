@@ -6,8 +6,9 @@
 //     dP = dout V^T,   D_i = sum_j P_ij dP_ij,   dS = P (dP - D),
 //     dV = P^T dout,   dQ = scale dS K,   dK = scale dS^T Q,   dbias_b = sum of dS over bucket b.
 // D_i also equals dout_i out_i, but out is bf16 there: good enough inside dQ, whose terms are rounded
-// to bf16 anyway, and not for sums of dS, in which large terms cancel.  So the dQ kernel starts from
-// dout_i out_i and leaves the sum over j, in fp32, for the others.
+// to bf16 anyway, unless a row's dS nearly cancel, as they do in rows of few keys; and not for sums
+// of dS.  So the dQ kernel starts from dout_i out_i (a tile with rows of fewer than kFewKeys keys
+// goes over its keys once before, for D alone) and leaves the sum over j, in fp32, for the others.
 //
 // Three kernels share the work, each with its accumulators in tensor memory and no atomics, so equal
 // calls give equal bits:
@@ -47,6 +48,10 @@ constexpr uint32_t HALF = 128u * 128u;  // [128 rows][64 bf16]: one swizzle span
 constexpr int kWarpLoad = 8, kWarpMma = 9;
 constexpr int kThreads = 320;
 constexpr uint32_t kTmemCols = 512;
+// Rows of fewer keys get their D from the sum over the keys also for dQ.  dout . out is off by about
+// 2^-9 |dout . out|, and |dout . out| shrinks against dP as the root of the number of keys that share
+// the weight: from 128 on the error is below a tenth of that of dS in bf16.
+constexpr int kFewKeys = 128;
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
 
 struct GradParams {
@@ -121,7 +126,8 @@ enum : int {
     B_PFULL = 9,   // P in tensor memory (8 warps)
     B_DSFULL = 10, // dS in tensor memory (8 warps)
     B_DONE = 11,   // all products done
-    NBARS = 12
+    B_SUMS = 12,   // both halves of the rows' D written (8 warps)
+    NBARS = 13
 };
 
 // The 16-row pieces of two [128][HD] tiles from row0 of a sequence that ends at row `end`: a box a
@@ -234,6 +240,7 @@ __device__ __forceinline__ Cta setup() {
         mbar_init(bar(B_PFULL), 8);
         mbar_init(bar(B_DSFULL), 8);
         mbar_init(bar(B_DONE), 1);
+        mbar_init(bar(B_SUMS), 8);
         *c.abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -333,6 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
     const int kt0 = kmin / BN;
     const int n = p_hi < 0 ? 0 : p_hi / BN - kt0 + 1;
     const int n_far = BIAS && !BAND ? max(kmin, p_lo - last + 1) / BN - kt0 : 0;  // tiles that the band leaves out
+    // Tiles in all: the first n_sum only for D.
+    const int n_sum = !BAND && (p_lo + 1 < kFewKeys || (p.window > 0 && p.window < kFewKeys)) ? n : 0;
+    const int n_all = n + n_sum;
     const int64_t stat_row = static_cast<int64_t>(h) * p.total_q + s.q_start + r0;
     __nv_bfloat16 *dq = p.dq + (static_cast<int64_t>(s.q_start) + r0) * p.dq_stride + h * HD;
     if (n == 0) {
@@ -370,10 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             __syncwarp();
             if (ok && lane == 0) mbar_arrive(bar(B_RES));
         }
-        for (int j = 0; ok && j < n; ++j) {
+        for (int j = 0; ok && j < n_all; ++j) {
             const int st = j & 1;
             if (j >= 2 && !wait_warp(bar(B_EMPTY + st), ((j >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-            const int k0 = (kt0 + j) * BN;
+            const int k0 = (kt0 + (j < n_sum ? j : j - n_sum)) * BN;
             const bool cut = ragged(s.sk - k0);
             const uint32_t full = bar(B_FULL + st), land = cut ? bar(B_LAND) : full;
             if (lane == 0) mbar_arrive_expect_tx(land, 2 * L::TILE);
@@ -397,11 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 issue_abt<HD>(c.tmem, sQ, sK(0));
                 mma_commit(bar(B_SFULL));
             }
-            for (int j = 0; ok && j < n; ++j) {
+            for (int j = 0; ok && j < n_all; ++j) {
                 const int st = j & 1;
                 issue_abt<HD>(c.tmem + kDp, sDo, sK(st) + L::TILE);
                 mma_commit(bar(B_DPFULL));
-                if (j + 1 < n) {
+                if (j + 1 < n_all) {
                     const int sn = (j + 1) & 1;
                     ok = wait(B_FULL + sn, ((j + 1) >> 1) & 1);
                     if (!ok) break;
@@ -412,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 ok = wait(B_DSFULL, j & 1);
                 if (!ok) break;
                 tc_fence_after();
-                if constexpr (!BAND) issue_ab<HD>(c.tmem + kDq, c.tmem + kDp, sK(st), j == 0);
+                if (!BAND && j >= n_sum) issue_ab<HD>(c.tmem + kDq, c.tmem + kDp, sK(st), j == n_sum);
                 mma_commit(bar(B_EMPTY + st));
             }
             if (ok) mma_commit(bar(B_DONE));
@@ -423,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
         const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
         const bool valid = row < rows;
         const float lse2 = valid ? p.lse2[stat_row + row] : INFINITY;
-        const float delta = valid ? p.delta[stat_row + row] : 0.f;
+        float delta = valid ? p.delta[stat_row + row] : 0.f;
         const float sl2 = p.scale_log2;
         const int pos = p_lo + row;
         [[maybe_unused]] const float *bias_row = nullptr;
@@ -433,8 +443,10 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             far = __ldg(bias_row + last) - lse2;
         }
         const uint32_t dp = c.tmem + t_lane + kDp + 64u * wg;
-        for (int j = 0; j < n; ++j) {
-            const int key0 = (kt0 + j) * BN + 64 * wg;  // this warpgroup's first key
+        for (int j = 0; j < n_all; ++j) {
+            const bool sum_only = j < n_sum;
+            const int tile = sum_only ? j : j - n_sum;
+            const int key0 = (kt0 + tile) * BN + 64 * wg;  // this warpgroup's first key
             if (!wait_warp(bar(B_SFULL + (j & 1)), (j >> 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
             tc_fence_after();
             float w[2][32];  // logits, then weights P
@@ -466,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             }
 #pragma unroll
             for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = ex2_approx(w[i >> 5][i & 31]);
-            if (BIAS && !BAND && j < n_far) {
+            if (BIAS && !BAND && !sum_only && tile < n_far) {
                 float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < 64; ++i) a[i & 3] += w[i >> 5][i & 31];
@@ -493,13 +505,24 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             }
             if constexpr (!BAND) {
                 d_sum += acc[0] + acc[1];
-                if (BIAS && j + 1 == n_far) d_far = d_sum;
-                tmem_st_32x32b_x32_u(dp, pk);
-                tmem_wait_st();
+                if (BIAS && !sum_only && tile + 1 == n_far) d_far = d_sum;
+                if (!sum_only) {
+                    tmem_st_32x32b_x32_u(dp, pk);
+                    tmem_wait_st();
+                }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_DSFULL));
+            if (!BAND && j + 1 == n_sum) {
+                // D of the row: this warpgroup's half and the other's.
+                small[512 + 128 * wg + row] = d_sum;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_SUMS));
+                if (!wait_warp(bar(B_SUMS), 0, c.abort_flag, p.err, kTimeoutNs)) break;
+                delta = small[512 + row] + small[640 + row];
+                d_sum = 0.f;
+            }
             if constexpr (BAND) {
                 // Sums along the diagonals row - column = lane, lane - 32, lane - 64 of the warp's 32 x
                 // 64 block: at column i the lane fetches the element of row (lane + i) % 32.
