@@ -55,11 +55,11 @@ constexpr int kFewKeys = 128;
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
 
 struct GradParams {
-    // Boxes of 16 rows x 64 dims of one head.
-    CUtensorMap tmap_q;
-    CUtensorMap tmap_do;
-    CUtensorMap tmap_k;
-    CUtensorMap tmap_v;
+    // Boxes of 64 dims of one head: [0] of 128 rows, [1] of 16 rows.
+    CUtensorMap tmap_q[2];
+    CUtensorMap tmap_do[2];
+    CUtensorMap tmap_k[2];
+    CUtensorMap tmap_v[2];
     const int32_t *cu_q;
     const int32_t *cu_k;
     __nv_bfloat16 *dq;
@@ -100,65 +100,102 @@ __device__ __forceinline__ Seq load_seq(const GradParams &p, int seq, bool repor
     return s;
 }
 
-// Shared memory: two resident tiles, two stages of two tiles, then barriers and small arrays.
-template <int HD>
+// Shared memory: two resident tiles (Q and dout, or K and V), rings of the tiles that pass by (K
+// and V, or Q and dout), small arrays, barriers.  K outlives V by the time from dP to dQ, so it has
+// three stages there.
+template <int HD, int STAGES_A, uint32_t SMALL_BYTES>
 struct Layout {
     static constexpr int NHALF = HD / 64;
     static constexpr uint32_t TILE = NHALF * HALF;
-    static constexpr uint32_t OFF_A = 0;             // K, V (dK, dV) or Q, dout (dQ)
-    static constexpr uint32_t OFF_B = 2 * TILE;      // stages of (Q, dout) or (K, V)
-    static constexpr uint32_t OFF_STAT = 6 * TILE;   // 8 KB of small arrays
-    static constexpr uint32_t OFF_BAR = OFF_STAT + 8192;
-    static constexpr uint32_t OFF_MISC = OFF_BAR + 256;
+    static constexpr int NA = STAGES_A, NB = 2;
+    static constexpr uint32_t OFF_RES = 0;
+    static constexpr uint32_t OFF_A = 2 * TILE;          // Q (dK, dV) or K (dQ)
+    static constexpr uint32_t OFF_B = OFF_A + NA * TILE;  // dout (dK, dV) or V (dQ)
+    static constexpr uint32_t OFF_SMALL = OFF_B + NB * TILE;
+    static constexpr uint32_t OFF_BAR = OFF_SMALL + SMALL_BYTES;
+    static constexpr uint32_t OFF_MISC = OFF_BAR + 160;
     static constexpr uint32_t BYTES = OFF_MISC + 16;
     // At least 116 KB so a single CTA owns an SM (and all of its TMEM).
     static constexpr uint32_t SMEM = (BYTES + 1024 > 118784u ? BYTES + 1024 : 118784u);
     static_assert(SMEM <= 232448u, "at most 227 KB of shared memory per CTA");
 };
 
+template <int HD, bool BAND>
+using LayoutQ = Layout<HD, BAND ? 2 : 3, BAND ? 8u * (96 + 128) * 4 : 3u * 512>;
+template <int HD>
+using LayoutKv = Layout<HD, 2, 2u * 3 * 512>;
+
 enum : int {
-    B_RES = 0,     // resident tiles loaded
-    B_FULL = 1,    // [2] stage ready (two arrivals: the copies, and the loading warp)
-    B_EMPTY = 3,   // [2] stage read
-    B_LAND = 5,    // copies of a tile that the loading warp edits
-    B_SFULL = 6,   // [2] logits of a tile ready
-    B_DPFULL = 8,  // dP ready
-    B_PFULL = 9,   // P in tensor memory (8 warps)
-    B_DSFULL = 10, // dS in tensor memory (8 warps)
-    B_DONE = 11,   // all products done
-    B_SUMS = 12,   // both halves of the rows' D written (8 warps)
-    NBARS = 13
+    B_RES = 0,      // resident tiles loaded
+    B_AFULL = 1,    // [3] tile of ring A ready (two arrivals: the copies, and the loading warp)
+    B_AEMPTY = 4,   // [3] read
+    B_BFULL = 7,    // [2] ring B, likewise
+    B_BEMPTY = 9,   // [2]
+    B_LAND = 11,    // copies of a tile that the loading warp edits
+    B_SFULL = 12,   // logits of a tile ready
+    B_PFULL = 13,   // logits read (dQ), or P in tensor memory (dK, dV) (8 warps)
+    B_DPFULL = 14,  // [2] dP ready
+    B_DSFULL = 16,  // [2] dS in tensor memory (8 warps)
+    B_DONE = 18,    // all products done
+    B_SUMS = 19,    // both halves of the rows' D written (8 warps)
+    NBARS = 20
 };
 
-// The 16-row pieces of two [128][HD] tiles from row0 of a sequence that ends at row `end`: a box a
-// lane.  Pieces past the end come from an out-of-range row, which reads as zeros.
+// A [128][HD] tile from row0 of a sequence that ends at row `end`: a box a lane.  A tile that the
+// sequence fills comes in boxes of 128 rows (a pair of tiles in 16-row pieces took 2900 cycles to land,
+// 1400 this way), another one in 16-row pieces, those past the end from an out-of-range row, which
+// reads as zeros.
 template <int HD>
-__device__ __forceinline__ void load_pair(const CUtensorMap *m0, const CUtensorMap *m1, uint32_t dst, int head0,
-                                          int head1, int start, int row0, int end, uint32_t bar) {
-    constexpr int NHALF = HD / 64, N = 8 * NHALF;
+__device__ __forceinline__ void load_tile(const CUtensorMap *map, uint32_t dst, int head, int start, int row0, int end,
+                                          uint32_t bar) {
+    constexpr int NHALF = HD / 64;
     const int lane = threadIdx.x & 31;
-    if (lane < 2 * N) {
-        const int which = lane / N, l = lane - which * N;
-        const int u = l / NHALF, h = l - u * NHALF;
+    if (end - row0 >= BM) {
+        if (lane < NHALF) tma_load_3d(dst + lane * HALF, map, lane * 64, head, start + row0, bar);
+    } else if (lane < 8 * NHALF) {
+        const int u = lane / NHALF, h = lane - u * NHALF;
         const int row = row0 + 16 * u < end ? start + row0 + 16 * u : -16;
-        tma_load_3d(dst + which * (NHALF * HALF) + h * HALF + u * 2048, which ? m1 : m0, h * 64, which ? head1 : head0,
-                    row, bar);
+        tma_load_3d(dst + h * HALF + u * 2048, map + 1, h * 64, head, row, bar);
     }
 }
 
-// Rows `from` .. of the last 16-row piece belong to the next sequence: zeros in both tiles, so that
-// a product over rows gets nothing from them whatever they hold.
+// Rows `from` .. of the last 16-row piece belong to the next sequence: zeros, so that a product over
+// rows gets nothing from them whatever they hold.
 template <int HD>
-__device__ __forceinline__ void clear_rows(uint32_t tiles, int from) {
+__device__ __forceinline__ void clear_rows(uint32_t tile, int from) {
     constexpr int NHALF = HD / 64;
     const int rows = 16 - (from & 15);
-    for (int i = threadIdx.x & 31; i < rows * 16 * NHALF; i += 32) {
-        const int r = from + i / (16 * NHALF), c = i % (16 * NHALF);
-        st_shared_v4(tiles + (c >> 3) * HALF + r * 128 + (c & 7) * 16, 0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x & 31; i < rows * 8 * NHALF; i += 32) {
+        const int r = from + i / (8 * NHALF), c = i % (8 * NHALF);
+        st_shared_v4(tile + (c >> 3) * HALF + r * 128 + (c & 7) * 16, 0u, 0u, 0u, 0u);
     }
     fence_proxy_async_smem();
 }
 __device__ __forceinline__ bool ragged(int left) { return left < BM && (left & 15) != 0; }
+
+// Tile -> stage, by the loading warp; `full` expects two arrivals.  `lands` counts the edited tiles,
+// `extra` runs before the second arrival.  False: a wait ran out.
+template <int HD, class Extra>
+__device__ __forceinline__ bool load_stage(const CUtensorMap *map, uint32_t dst, int head, int start, int row0, int end,
+                                           uint32_t full, uint32_t land, uint32_t &lands, volatile int *abort_flag,
+                                           unsigned *err, Extra extra) {
+    const int lane = threadIdx.x & 31;
+    const bool cut = ragged(end - row0);
+    if (lane == 0) mbar_arrive_expect_tx(cut ? land : full, (HD / 64) * HALF);
+    __syncwarp();
+    load_tile<HD>(map, dst, head, start, row0, end, cut ? land : full);
+    extra();
+    if (cut) {
+        if (!wait_warp(land, lands++ & 1, abort_flag, err, kTimeoutNs)) return false;
+        clear_rows<HD>(dst, end - row0);
+    }
+    __syncwarp();
+    if (lane == 0) {
+        if (cut) mbar_arrive(full);
+        mbar_arrive(full);
+    }
+    return true;
+}
 
 // D[128 x 128] = A B^T over HD dims, both tiles [128][HD].
 template <int HD>
@@ -218,9 +255,8 @@ struct Cta {
     uint32_t tmem;
     volatile int *abort_flag;
 };
-template <int HD>
+template <class L>
 __device__ __forceinline__ Cta setup() {
-    using L = Layout<HD>;
     extern __shared__ uint8_t smem_raw[];
     Cta c;
     const uint32_t raw = smem_u32(smem_raw);
@@ -230,15 +266,19 @@ __device__ __forceinline__ Cta setup() {
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     if (threadIdx.x == 0) {
         mbar_init(bar(B_RES), 1);
+        for (int s = 0; s < 3; ++s) {
+            mbar_init(bar(B_AFULL + s), 2);
+            mbar_init(bar(B_AEMPTY + s), 1);
+        }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(bar(B_FULL + s), 2);
-            mbar_init(bar(B_EMPTY + s), 1);
-            mbar_init(bar(B_SFULL + s), 1);
+            mbar_init(bar(B_BFULL + s), 2);
+            mbar_init(bar(B_BEMPTY + s), 1);
+            mbar_init(bar(B_DPFULL + s), 1);
+            mbar_init(bar(B_DSFULL + s), 8);
         }
         mbar_init(bar(B_LAND), 1);
-        mbar_init(bar(B_DPFULL), 1);
+        mbar_init(bar(B_SFULL), 1);
         mbar_init(bar(B_PFULL), 8);
-        mbar_init(bar(B_DSFULL), 8);
         mbar_init(bar(B_DONE), 1);
         mbar_init(bar(B_SUMS), 8);
         *c.abort_flag = 0;
@@ -319,12 +359,15 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------------------- dQ ---
-// Tensor memory: S of two tiles in turn at 0 and 128, dP (then dS) at 256, dQ at 384.
+// Tensor memory: S at 0, dP (then dS) of two tiles in turn at 128 and 256, dQ at 384.  S is free once
+// its rows are in registers, so the products of the next tile run while this one's dS is formed:
+//     S(j + 1), dP(j + 1), then dQ(j).
 template <int HD, bool BIAS, bool BAND>
 __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_constant__ GradParams p) {
     static_assert(BIAS || !BAND, "the band is the bias's");
-    using L = Layout<HD>;
-    constexpr uint32_t kDp = 256, kDq = 384;
+    using L = LayoutQ<HD, BAND>;
+    constexpr int NA = L::NA;
+    constexpr uint32_t kDp = 128, kDq = 384;
     const int h = blockIdx.x % p.num_heads;
     const int rest = blockIdx.x / p.num_heads;
     const int seq = rest % p.num_seqs;
@@ -352,12 +395,14 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
         }
         return;
     }
-    const Cta c = setup<HD>();
+    const Cta c = setup<L>();
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t sQ = c.base + L::OFF_A, sDo = sQ + L::TILE;
-    auto sK = [&](int st) -> uint32_t { return c.base + L::OFF_B + st * 2 * L::TILE; };
-    float *small = reinterpret_cast<float *>(c.sb + L::OFF_STAT);
+    const uint32_t sQ = c.base + L::OFF_RES, sDo = sQ + L::TILE;
+    auto sK = [&](int st) -> uint32_t { return c.base + L::OFF_A + st * L::TILE; };
+    auto sV = [&](int st) -> uint32_t { return c.base + L::OFF_B + st * L::TILE; };
+    // [384], or the band's windows [8][96] and sums [8][128].
+    float *small = reinterpret_cast<float *>(c.sb + L::OFF_SMALL);
     const int kvh = h / p.group;
     // What the element-wise warps have at the end.
     float d_sum = 0.f;
@@ -365,67 +410,62 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
     [[maybe_unused]] float by_bucket[4] = {0.f, 0.f, 0.f, 0.f};
 
     if (warp == kWarpLoad) {
-        if (lane < 4) prefetch_tmap(lane == 0 ? &p.tmap_q : lane == 1 ? &p.tmap_do : lane == 2 ? &p.tmap_k : &p.tmap_v);
+        if (lane < 4) prefetch_tmap(lane == 0 ? p.tmap_q : lane == 1 ? p.tmap_do : lane == 2 ? p.tmap_k : p.tmap_v);
         uint32_t lands = 0;
         // (Rows behind the sequence stay in their own rows of every product here, but the band's sums
         // run across rows.)
         const bool edit = BAND && ragged(rows);
         if (lane == 0) mbar_arrive_expect_tx(bar(edit ? B_LAND : B_RES), 2 * L::TILE);
         __syncwarp();
-        load_pair<HD>(&p.tmap_q, &p.tmap_do, sQ, h, h, s.q_start, r0, s.sq, bar(edit ? B_LAND : B_RES));
+        load_tile<HD>(p.tmap_q, sQ, h, s.q_start, r0, s.sq, bar(edit ? B_LAND : B_RES));
+        load_tile<HD>(p.tmap_do, sDo, h, s.q_start, r0, s.sq, bar(edit ? B_LAND : B_RES));
         bool ok = true;
         if (edit) {
             ok = wait_warp(bar(B_LAND), lands++ & 1, c.abort_flag, p.err, kTimeoutNs);
-            if (ok) clear_rows<HD>(sQ, rows);
+            if (ok) {
+                clear_rows<HD>(sQ, rows);
+                clear_rows<HD>(sDo, rows);
+            }
             __syncwarp();
             if (ok && lane == 0) mbar_arrive(bar(B_RES));
         }
+        auto load = [&](const CUtensorMap *map, uint32_t dst, int j, uint32_t full) -> bool {
+            return load_stage<HD>(map, dst, kvh, s.k_start, (kt0 + (j < n_sum ? j : j - n_sum)) * BN, s.sk, full, bar(B_LAND), lands,
+                                  c.abort_flag, p.err, [] {});
+        };
         for (int j = 0; ok && j < n_all; ++j) {
-            const int st = j & 1;
-            if (j >= 2 && !wait_warp(bar(B_EMPTY + st), ((j >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-            const int k0 = (kt0 + (j < n_sum ? j : j - n_sum)) * BN;
-            const bool cut = ragged(s.sk - k0);
-            const uint32_t full = bar(B_FULL + st), land = cut ? bar(B_LAND) : full;
-            if (lane == 0) mbar_arrive_expect_tx(land, 2 * L::TILE);
-            __syncwarp();
-            load_pair<HD>(&p.tmap_k, &p.tmap_v, sK(st), kvh, kvh, s.k_start, k0, s.sk, land);
-            if (cut) {
-                ok = wait_warp(land, lands++ & 1, c.abort_flag, p.err, kTimeoutNs);
-                if (!ok) break;
-                clear_rows<HD>(sK(st), s.sk - k0);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full);
-            }
-            if (lane == 0) mbar_arrive(full);
+            const int sa = j % NA, sb = j & 1;
+            if (j >= NA && !wait_warp(bar(B_AEMPTY + sa), (j / NA - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+            if (!load(p.tmap_k, sK(sa), j, bar(B_AFULL + sa))) break;
+            if (j >= 2 && !wait_warp(bar(B_BEMPTY + sb), ((j >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+            ok = load(p.tmap_v, sV(sb), j, bar(B_BFULL + sb));
         }
     } else if (warp == kWarpMma) {
         if (lane == 0) {
             auto wait = [&](int b, uint32_t parity) { return wait1(bar(b), parity, c.abort_flag, p.err, kTimeoutNs); };
-            bool ok = wait(B_RES, 0) && wait(B_FULL, 0);
-            if (ok) {
+            auto products = [&](int j) -> bool {  // S(j) and dP(j)
+                if (!wait(B_AFULL + j % NA, (j / NA) & 1)) return false;
                 tc_fence_after();
-                issue_abt<HD>(c.tmem, sQ, sK(0));
+                issue_abt<HD>(c.tmem, sQ, sK(j % NA));
                 mma_commit(bar(B_SFULL));
-            }
+                if (!wait(B_BFULL + (j & 1), (j >> 1) & 1)) return false;
+                tc_fence_after();
+                issue_abt<HD>(c.tmem + kDp + 128u * (j & 1), sDo, sV(j & 1));
+                mma_commit(bar(B_DPFULL + (j & 1)));
+                mma_commit(bar(B_BEMPTY + (j & 1)));
+                return true;
+            };
+            bool ok = wait(B_RES, 0) && products(0);
             for (int j = 0; ok && j < n_all; ++j) {
-                const int st = j & 1;
-                issue_abt<HD>(c.tmem + kDp, sDo, sK(st) + L::TILE);
-                mma_commit(bar(B_DPFULL));
-                if (j + 1 < n_all) {
-                    const int sn = (j + 1) & 1;
-                    ok = wait(B_FULL + sn, ((j + 1) >> 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_abt<HD>(c.tmem + 128u * sn, sQ, sK(sn));
-                    mma_commit(bar(B_SFULL + sn));
-                }
-                ok = wait(B_DSFULL, j & 1);
+                // (dP(j + 1) goes where dS(j - 1) was: dQ(j - 1) is before it in the queue.)
+                if (j + 1 < n_all && !(wait(B_PFULL, j & 1) && products(j + 1))) break;
+                ok = wait(B_DSFULL + (j & 1), (j >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                if (!BAND && j >= n_sum) issue_ab<HD>(c.tmem + kDq, c.tmem + kDp, sK(st), j == n_sum);
-                mma_commit(bar(B_EMPTY + st));
+                if (!BAND && j >= n_sum) issue_ab<HD>(c.tmem + kDq, c.tmem + kDp + 128u * (j & 1), sK(j % NA), j == n_sum);
+                mma_commit(bar(B_AEMPTY + j % NA));
+                if (j + 1 == n_all) mma_commit(bar(B_DONE));
             }
-            if (ok) mma_commit(bar(B_DONE));
         }
     } else {
         const int wg = warp >> 2, quarter = warp & 3;
@@ -442,18 +482,22 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             bias_row = bias_row_of(p.bias_table, h, last);
             far = __ldg(bias_row + last) - lse2;
         }
-        const uint32_t dp = c.tmem + t_lane + kDp + 64u * wg;
+        const uint64_t sl2x2 = f2_pack(sl2, sl2), far2 = f2_pack(far, far);
         for (int j = 0; j < n_all; ++j) {
+            const uint32_t dp = c.tmem + t_lane + kDp + 128u * (j & 1) + 64u * wg;
             const bool sum_only = j < n_sum;
             const int tile = sum_only ? j : j - n_sum;
             const int key0 = (kt0 + tile) * BN + 64 * wg;  // this warpgroup's first key
-            if (!wait_warp(bar(B_SFULL + (j & 1)), (j >> 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+            if (!wait_warp(bar(B_SFULL), j & 1, c.abort_flag, p.err, kTimeoutNs)) break;
             tc_fence_after();
             float w[2][32];  // logits, then weights P
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc) tmem_ld_32x32b_x32(c.tmem + t_lane + 128u * (j & 1) + 64u * wg + 32u * cc, w[cc]);
+            for (int cc = 0; cc < 2; ++cc) tmem_ld_32x32b_x32(c.tmem + t_lane + 64u * wg + 32u * cc, w[cc]);
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) tmem_wait_ld_regs(w[cc]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_PFULL));
             const int d0 = pos - key0;  // distance to the first key
             bool near = false;
             if constexpr (BIAS) near = __shfl_sync(0xffffffffu, d0, 0) - 63 < last && __shfl_sync(0xffffffffu, d0, 31) >= 0;
@@ -463,7 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = fmaf(w[i >> 5][i & 31], sl2, __ldg(bt - i)) - lse2;
             } else {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = fmaf(w[i >> 5][i & 31], sl2, far);
+                for (int i = 0; i < 32; ++i) {
+                    float &a = w[i >> 4][2 * (i & 15)], &b = w[i >> 4][2 * (i & 15) + 1];
+                    f2_unpack(f2_fma(f2_pack(a, b), sl2x2, far2), a, b);
+                }
             }
             if (d0 < 63) {
 #pragma unroll
@@ -484,27 +531,28 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 for (int i = 0; i < 64; ++i) a[i & 3] += w[i >> 5][i & 31];
                 w_far += (a[0] + a[1]) + (a[2] + a[3]);
             }
-            if (!wait_warp(bar(B_DPFULL), j & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+            if (!wait_warp(bar(B_DPFULL + (j & 1)), (j >> 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
             tc_fence_after();
             uint32_t pk[32];
-            float acc[2] = {0.f, 0.f};
+            uint64_t acc[2] = {0ull, 0ull};
+            const uint64_t delta2 = f2_pack(-delta, -delta);
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
                 float d[32];
                 tmem_ld_32x32b_x32(dp + 32u * cc, d);
                 tmem_wait_ld_regs(d);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if constexpr (!BAND) acc[i & 1] = fmaf(w[cc][i], d[i], acc[i & 1]);
-                    w[cc][i] *= d[i] - delta;
-                }
-                if constexpr (!BAND) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) pk[16 * cc + i] = pack_bf16x2(w[cc][2 * i], w[cc][2 * i + 1]);
+                for (int i = 0; i < 16; ++i) {
+                    const uint64_t w2 = f2_pack(w[cc][2 * i], w[cc][2 * i + 1]), d2 = f2_pack(d[2 * i], d[2 * i + 1]);
+                    if constexpr (!BAND) acc[i & 1] = f2_fma(w2, d2, acc[i & 1]);
+                    f2_unpack(f2_mul(w2, f2_add(d2, delta2)), w[cc][2 * i], w[cc][2 * i + 1]);
+                    if constexpr (!BAND) pk[16 * cc + i] = pack_bf16x2(w[cc][2 * i], w[cc][2 * i + 1]);
                 }
             }
             if constexpr (!BAND) {
-                d_sum += acc[0] + acc[1];
+                float a0, a1;
+                f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
+                d_sum += a0 + a1;
                 if (BIAS && !sum_only && tile + 1 == n_far) d_far = d_sum;
                 if (!sum_only) {
                     tmem_st_32x32b_x32_u(dp, pk);
@@ -513,14 +561,14 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_DSFULL));
+            if (lane == 0) mbar_arrive(bar(B_DSFULL + (j & 1)));
             if (!BAND && j + 1 == n_sum) {
                 // D of the row: this warpgroup's half and the other's.
-                small[512 + 128 * wg + row] = d_sum;
+                small[128 * wg + row] = d_sum;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_SUMS));
                 if (!wait_warp(bar(B_SUMS), 0, c.abort_flag, p.err, kTimeoutNs)) break;
-                delta = small[512 + row] + small[640 + row];
+                delta = small[row] + small[128 + row];
                 d_sum = 0.f;
             }
             if constexpr (BAND) {
@@ -574,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
         } else {
             // (Nothing may arrive at a barrier after the CTA's end.)
             wait_warp(bar(B_DONE), 0, c.abort_flag, p.err, kTimeoutNs);
-            float *mine = small + 1024 + 128 * warp;
+            float *mine = small + 768 + 128 * warp;
 #pragma unroll
             for (int k = 0; k < 4; ++k) mine[lane + 32 * k] = by_bucket[k];
         }
@@ -591,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
         if (b < p.bias.num_buckets) {
             float t = b == p.bias.num_buckets - 1 ? partial[b] : 0.f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) t += small[1024 + 128 * w + b];
+            for (int w = 0; w < 8; ++w) t += small[768 + 128 * w + b];
             partial[b] = t;
         }
     } else {
@@ -602,21 +650,25 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             if constexpr (BIAS) t = d_far + small[128 + threadIdx.x] - d * (w_far + small[256 + threadIdx.x]);
         }
         if constexpr (BIAS) {
+            __syncthreads();  // (the rows' sums are read)
             if (warp < 4) {
                 t = warp_sum(t);
-                if (lane == 0) small[384 + warp] = t;
+                if (lane == 0) small[warp] = t;
             }
             __syncthreads();
-            if (threadIdx.x == 0) partial[p.bias.num_buckets - 1] = (small[384] + small[385]) + (small[386] + small[387]);
+            if (threadIdx.x == 0) partial[p.bias.num_buckets - 1] = (small[0] + small[1]) + (small[2] + small[3]);
         }
     }
 }
 
 // --------------------------------------------------------------------- dK, dV ---
-// Tensor memory: S^T (then P^T) at 0, dP^T (then dS^T) at 128, dV at 256, dK at 384.
+// Tensor memory: S^T (then P^T) at 0, dP^T (then dS^T) at 128, dV at 256, dK at 384.  While the
+// element-wise warps form P^T, the tensor cores run dK of the tile before and dP^T; while they form
+// dS^T, dV and the next tile's S^T:
+//     dP(i), dV(i), S(i + 1), dK(i).
 template <int HD, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_constant__ GradParams p) {
-    using L = Layout<HD>;
+    using L = LayoutKv<HD>;
     constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 384;
     const int kvh = blockIdx.x % p.num_kv_heads;
     const int rest = blockIdx.x / p.num_kv_heads;
@@ -639,51 +691,46 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
         zero_rows<HD>(dv, p.dv_stride, rows);
         return;
     }
-    const Cta c = setup<HD>();
+    const Cta c = setup<L>();
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t sK = c.base + L::OFF_A, sV = sK + L::TILE;
-    auto sQ = [&](int st) -> uint32_t { return c.base + L::OFF_B + st * 2 * L::TILE; };
-    // Per stage: -lse2, D and (BIAS) the last bucket's bias - lse2 of the tile's queries.
-    auto stat = [&](int st) -> float * { return reinterpret_cast<float *>(c.sb + L::OFF_STAT) + st * 384; };
+    const uint32_t sK = c.base + L::OFF_RES, sV = sK + L::TILE;
+    auto sQ = [&](int st) -> uint32_t { return c.base + L::OFF_A + st * L::TILE; };
+    auto sDo = [&](int st) -> uint32_t { return c.base + L::OFF_B + st * L::TILE; };
+    // Per stage: -lse2, -D and (BIAS) the last bucket's bias - lse2 of the tile's queries.
+    auto stat = [&](int st) -> float * { return reinterpret_cast<float *>(c.sb + L::OFF_SMALL) + st * 384; };
     const int last = p.bias.last();
 
     if (warp == kWarpLoad) {
-        if (lane < 4) prefetch_tmap(lane == 0 ? &p.tmap_q : lane == 1 ? &p.tmap_do : lane == 2 ? &p.tmap_k : &p.tmap_v);
+        if (lane < 4) prefetch_tmap(lane == 0 ? p.tmap_q : lane == 1 ? p.tmap_do : lane == 2 ? p.tmap_k : p.tmap_v);
         if (lane == 0) mbar_arrive_expect_tx(bar(B_RES), 2 * L::TILE);
         __syncwarp();
-        load_pair<HD>(&p.tmap_k, &p.tmap_v, sK, kvh, kvh, s.k_start, k_lo, s.sk, bar(B_RES));
+        load_tile<HD>(p.tmap_k, sK, kvh, s.k_start, k_lo, s.sk, bar(B_RES));
+        load_tile<HD>(p.tmap_v, sV, kvh, s.k_start, k_lo, s.sk, bar(B_RES));
         uint32_t lands = 0;
         int g = 0, t = 0;
         for (int i = 0; i < n; ++i) {
             const int st = i & 1;
-            if (i >= 2 && !wait_warp(bar(B_EMPTY + st), ((i >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
             const int r = r_first + t * BN, head = kvh * p.group + g;
-            const bool cut = ragged(s.sq - r);
-            const uint32_t full = bar(B_FULL + st), land = cut ? bar(B_LAND) : full;
-            if (lane == 0) mbar_arrive_expect_tx(land, 2 * L::TILE);
-            __syncwarp();
-            load_pair<HD>(&p.tmap_q, &p.tmap_do, sQ(st), head, head, s.q_start, r, s.sq, land);
-            float far = 0.f;
-            if constexpr (BIAS) far = __ldg(bias_row_of(p.bias_table, head, last) + last);
-            const int64_t at = static_cast<int64_t>(head) * p.total_q + s.q_start + r;
+            // (dout's stage is free first: dV comes before dK.)
+            if (i >= 2 && !wait_warp(bar(B_BEMPTY + st), ((i >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+            if (!load_stage<HD>(p.tmap_do, sDo(st), head, s.q_start, r, s.sq, bar(B_BFULL + st), bar(B_LAND), lands, c.abort_flag, p.err, [] {})) break;
+            if (i >= 2 && !wait_warp(bar(B_AEMPTY + st), ((i >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+            auto stats = [&] {
+                float far = 0.f;
+                if constexpr (BIAS) far = __ldg(bias_row_of(p.bias_table, head, last) + last);
+                const int64_t at = static_cast<int64_t>(head) * p.total_q + s.q_start + r;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int x = lane + 32 * e;
-                const bool in = r + x < s.sq;
-                const float l2 = in ? p.lse2[at + x] : INFINITY;
-                stat(st)[x] = -l2;
-                stat(st)[128 + x] = in ? p.delta[at + x] : 0.f;
-                if constexpr (BIAS) stat(st)[256 + x] = far - l2;
-            }
-            if (cut) {
-                if (!wait_warp(land, lands++ & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-                clear_rows<HD>(sQ(st), s.sq - r);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(full);
+                for (int e = 0; e < 4; ++e) {
+                    const int x = lane + 32 * e;
+                    const bool in = r + x < s.sq;
+                    const float l2 = in ? p.lse2[at + x] : INFINITY;
+                    stat(st)[x] = -l2;
+                    stat(st)[128 + x] = in ? -p.delta[at + x] : 0.f;
+                    if constexpr (BIAS) stat(st)[256 + x] = far - l2;
+                }
+            };
+            if (!load_stage<HD>(p.tmap_q, sQ(st), head, s.q_start, r, s.sq, bar(B_AFULL + st), bar(B_LAND), lands, c.abort_flag, p.err, stats)) break;
             if (++t == nq) {
                 t = 0;
                 ++g;
@@ -692,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
     } else if (warp == kWarpMma) {
         if (lane == 0) {
             auto wait = [&](int b, uint32_t parity) { return wait1(bar(b), parity, c.abort_flag, p.err, kTimeoutNs); };
-            bool ok = wait(B_RES, 0) && wait(B_FULL, 0);
+            bool ok = wait(B_RES, 0) && wait(B_AFULL, 0);
             if (ok) {
                 tc_fence_after();
                 issue_abt<HD>(c.tmem + kS, sK, sQ(0));
@@ -700,15 +747,19 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             }
             for (int i = 0; ok && i < n; ++i) {
                 const int st = i & 1;
-                issue_abt<HD>(c.tmem + kDp, sV, sQ(st) + L::TILE);
+                ok = wait(B_BFULL + st, (i >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                issue_abt<HD>(c.tmem + kDp, sV, sDo(st));
                 mma_commit(bar(B_DPFULL));
                 ok = wait(B_PFULL, i & 1);
                 if (!ok) break;
                 tc_fence_after();
-                issue_ab<HD>(c.tmem + kDv, c.tmem + kS, sQ(st) + L::TILE, i == 0);
+                issue_ab<HD>(c.tmem + kDv, c.tmem + kS, sDo(st), i == 0);
+                mma_commit(bar(B_BEMPTY + st));
                 if (i + 1 < n) {
                     const int sn = (i + 1) & 1;
-                    ok = wait(B_FULL + sn, ((i + 1) >> 1) & 1);
+                    ok = wait(B_AFULL + sn, ((i + 1) >> 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
                     issue_abt<HD>(c.tmem + kS, sK, sQ(sn));
@@ -718,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
                 if (!ok) break;
                 tc_fence_after();
                 issue_ab<HD>(c.tmem + kDk, c.tmem + kDp, sQ(st), i == 0);
-                mma_commit(bar(B_EMPTY + st));
+                mma_commit(bar(B_AEMPTY + st));
             }
             if (ok) mma_commit(bar(B_DONE));
         }
@@ -734,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
         for (int i = 0; i < n; ++i) {
             const int st = i & 1;
             const int pos0 = off + r_first + t * BN + 64 * wg;  // position of this warpgroup's first query
-            if (!wait_warp(bar(B_FULL + st), (i >> 1) & 1, c.abort_flag, p.err, kTimeoutNs) ||
+            if (!wait_warp(bar(B_AFULL + st), (i >> 1) & 1, c.abort_flag, p.err, kTimeoutNs) ||
                 !wait_warp(bar(B_SFULL), i & 1, c.abort_flag, p.err, kTimeoutNs)) {
                 ok = false;
                 break;
@@ -762,15 +813,14 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
                     v[3] = fmaf(v[3], sl2, __ldg(bt + 4 * x + 3)) + l.w;
                 }
             } else {
-                const float4 *nl = reinterpret_cast<const float4 *>(stat(st) + (BIAS ? 256 : 0) + 64 * wg);
+                const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(stat(st) + (BIAS ? 256 : 0) + 64 * wg);
+                const uint64_t sl2x2 = f2_pack(sl2, sl2);
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
-                    const float4 l = nl[x];
+                    const ulonglong2 l = nl[x];
                     float *v = &w[x >> 3][4 * (x & 7)];
-                    v[0] = fmaf(v[0], sl2, l.x);
-                    v[1] = fmaf(v[1], sl2, l.y);
-                    v[2] = fmaf(v[2], sl2, l.z);
-                    v[3] = fmaf(v[3], sl2, l.w);
+                    f2_unpack(f2_fma(f2_pack(v[0], v[1]), sl2x2, l.x), v[0], v[1]);
+                    f2_unpack(f2_fma(f2_pack(v[2], v[3]), sl2x2, l.y), v[2], v[3]);
                 }
             }
             if (d0 < 0) {
@@ -802,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
                 break;
             }
             tc_fence_after();
-            const float4 *dl = reinterpret_cast<const float4 *>(stat(st) + 128 + 64 * wg);
+            const ulonglong2 *dl = reinterpret_cast<const ulonglong2 *>(stat(st) + 128 + 64 * wg);
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
                 float d[32];
@@ -810,10 +860,13 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
                 tmem_wait_ld_regs(d);
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    const float4 l = dl[8 * cc + x];
-                    pk[16 * cc + 2 * x] = pack_bf16x2(w[cc][4 * x] * (d[4 * x] - l.x), w[cc][4 * x + 1] * (d[4 * x + 1] - l.y));
-                    pk[16 * cc + 2 * x + 1] =
-                        pack_bf16x2(w[cc][4 * x + 2] * (d[4 * x + 2] - l.z), w[cc][4 * x + 3] * (d[4 * x + 3] - l.w));
+                    const ulonglong2 l = dl[8 * cc + x];
+                    float *v = &d[4 * x];
+                    const float *pw = &w[cc][4 * x];
+                    f2_unpack(f2_mul(f2_pack(pw[0], pw[1]), f2_add(f2_pack(v[0], v[1]), l.x)), v[0], v[1]);
+                    f2_unpack(f2_mul(f2_pack(pw[2], pw[3]), f2_add(f2_pack(v[2], v[3]), l.y)), v[2], v[3]);
+                    pk[16 * cc + 2 * x] = pack_bf16x2(v[0], v[1]);
+                    pk[16 * cc + 2 * x + 1] = pack_bf16x2(v[2], v[3]);
                 }
             }
             tmem_st_32x32b_x32_u(dp, pk);
@@ -876,17 +929,19 @@ cudaError_t launch_tiles(Kernel kern, uint32_t smem, std::atomic<uint64_t> &set,
 
 template <int HD, bool BIAS>
 cudaError_t launch_backward_d(GradParams &p, const PackedGradArgs &g, cudaStream_t stream) {
-    using L = Layout<HD>;
     const PackedArgs &a = g.fwd;
     const int64_t rows = static_cast<int64_t>(a.num_heads) * HD;
     // (Without queries, or keys, nothing is loaded, but a tensor map has a row and an address.)
     auto rows_map = [](CUtensorMap *map, const void *base, const void *spare, int heads, int total, int64_t stride) {
-        return encode_3d(map, total > 0 ? base : spare, HD, heads, total > 0 ? total : 1, HD * 2, stride * 2, 64, 1, 16);
+        for (int i = 0; i < 2; ++i)
+            if (!encode_3d(map + i, total > 0 ? base : spare, HD, heads, total > 0 ? total : 1, HD * 2, stride * 2, 64, 1, i ? 16 : 128))
+                return false;
+        return true;
     };
-    if (!rows_map(&p.tmap_q, a.q, a.k, a.num_heads, a.total_q, a.q_stride) ||
-        !rows_map(&p.tmap_do, g.dout, a.k, a.num_heads, a.total_q, rows) ||
-        !rows_map(&p.tmap_k, a.k, a.q, a.num_kv_heads, a.total_k, a.k_stride) ||
-        !rows_map(&p.tmap_v, a.v, a.q, a.num_kv_heads, a.total_k, a.v_stride))
+    if (!rows_map(p.tmap_q, a.q, a.k, a.num_heads, a.total_q, a.q_stride) ||
+        !rows_map(p.tmap_do, g.dout, a.k, a.num_heads, a.total_q, rows) ||
+        !rows_map(p.tmap_k, a.k, a.q, a.num_kv_heads, a.total_k, a.k_stride) ||
+        !rows_map(p.tmap_v, a.v, a.q, a.num_kv_heads, a.total_k, a.v_stride))
         return cudaErrorInvalidValue;
     cudaError_t e = cudaSuccess;
     if (a.total_q > 0) {
@@ -901,10 +956,10 @@ cudaError_t launch_backward_d(GradParams &p, const PackedGradArgs &g, cudaStream
     const int slots = static_cast<int>(tile_slots(a.total_q, a.num_seqs));
     if (BIAS && e == cudaSuccess)  // (places without a tile)
         e = cudaMemsetAsync(p.partial, 0, static_cast<size_t>(slots) * a.num_heads * a.bias.num_buckets * sizeof(float), stream);
-    if (e == cudaSuccess) e = launch_tiles(grad_q_kernel<HD, BIAS, false>, L::SMEM, set[0], q_blocks, p, stream);
-    if (e == cudaSuccess) e = launch_tiles(grad_kv_kernel<HD, BIAS>, L::SMEM, set[1], k_blocks, p, stream);
+    if (e == cudaSuccess) e = launch_tiles(grad_q_kernel<HD, BIAS, false>, LayoutQ<HD, false>::SMEM, set[0], q_blocks, p, stream);
+    if (e == cudaSuccess) e = launch_tiles(grad_kv_kernel<HD, BIAS>, LayoutKv<HD>::SMEM, set[1], k_blocks, p, stream);
     if constexpr (BIAS) {
-        if (e == cudaSuccess) e = launch_tiles(grad_q_kernel<HD, true, true>, L::SMEM, set[2], q_blocks, p, stream);
+        if (e == cudaSuccess) e = launch_tiles(grad_q_kernel<HD, true, true>, LayoutQ<HD, true>::SMEM, set[2], q_blocks, p, stream);
         if (e != cudaSuccess) return e;
         grad_bias_kernel<<<a.num_heads, 1024, 0, stream>>>(g.dbias, p.partial, slots, a.num_heads, a.bias.num_buckets);
         e = cudaGetLastError();
