@@ -7,17 +7,17 @@
 //     dV = P^T dout,   dQ = scale dS K,   dK = scale dS^T Q,   dbias_b = sum of dS over bucket b.
 // D_i also equals dout_i out_i, but out is bf16 there: good enough inside dQ, whose terms are rounded
 // to bf16 anyway, unless a row's dS nearly cancel, as they do in rows of few keys; and not for sums
-// of dS.  So the dQ kernel starts from dout_i out_i (a tile with rows of fewer than kFewKeys keys
-// goes over its keys once before, for D alone) and leaves the sum over j, in fp32, for the others.
+// of dS.  So the dQ kernel starts from dout_i out_i, goes twice over the tiles that need the sum
+// itself, first for D alone, and leaves D in fp32 for dK.
 //
-// Three kernels share the work, each with its accumulators in tensor memory and no atomics, so equal
+// Two kernels share the work, each with its accumulators in tensor memory and no atomics, so equal
 // calls give equal bits:
-//  * grad_q_kernel: 128 queries of one head against their keys in turn (3 products a tile);
+//  * grad_q_kernel: 128 queries of one head against their keys in turn (3 products a tile).  dbias: the
+//    tiles whose distances all belong to the last bucket add sum_j P dP - D sum_j P to it; the others,
+//    the nearest ones, come last, once for D and once more with it, and their dS are summed along
+//    diagonals into buckets;
 //  * grad_kv_kernel: 128 keys of one kv head against the queries of every head that shares it
 //    (4 products a tile), so the sum over the heads happens in the accumulator;
-//  * grad_q_kernel with BAND: the tiles that hold distances below the last bucket's first one once
-//    more (2 products), summed along their diagonals into buckets; the others, which all belong to the
-//    last bucket, are summed by the dQ kernel as sum_j P dP - D sum_j P.
 // The products count 7 for the 5 of the formula (S and dP are formed twice); dQ added up across
 // the CTAs of one pass over the keys would need atomics, whose order changes the result.
 //
@@ -116,12 +116,12 @@ struct Layout {
     static constexpr uint32_t OFF_MISC = OFF_BAR + 160;
     static constexpr uint32_t BYTES = OFF_MISC + 16;
     // At least 116 KB so a single CTA owns an SM (and all of its TMEM).
-    static constexpr uint32_t SMEM = (BYTES + 1024 > 118784u ? BYTES + 1024 : 118784u);
+    static constexpr uint32_t SMEM = (BYTES > 118784u ? BYTES : 118784u);
     static_assert(SMEM <= 232448u, "at most 227 KB of shared memory per CTA");
 };
 
-template <int HD, bool BAND>
-using LayoutQ = Layout<HD, BAND ? 2 : 3, BAND ? 8u * (96 + 128) * 4 : 3u * 512>;
+template <int HD>
+using LayoutQ = Layout<HD, 3, 2048>;
 template <int HD>
 using LayoutKv = Layout<HD, 2, 2u * 3 * 512>;
 
@@ -257,11 +257,10 @@ struct Cta {
 };
 template <class L>
 __device__ __forceinline__ Cta setup() {
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];  // (swizzled tiles start on 1024 bytes)
     Cta c;
-    const uint32_t raw = smem_u32(smem_raw);
-    c.base = (raw + 1023u) & ~1023u;
-    c.sb = smem_raw + (c.base - raw);
+    c.base = smem_u32(smem_raw);
+    c.sb = smem_raw;
     c.abort_flag = reinterpret_cast<volatile int *>(c.sb + L::OFF_MISC + 4);
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     if (threadIdx.x == 0) {
@@ -362,37 +361,36 @@ __global__ void __launch_bounds__(256)
 // Tensor memory: S at 0, dP (then dS) of two tiles in turn at 128 and 256, dQ at 384.  S is free once
 // its rows are in registers, so the products of the next tile run while this one's dS is formed:
 //     S(j + 1), dP(j + 1), then dQ(j).
-template <int HD, bool BIAS, bool BAND>
+template <int HD, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_constant__ GradParams p) {
-    static_assert(BIAS || !BAND, "the band is the bias's");
-    using L = LayoutQ<HD, BAND>;
+    using L = LayoutQ<HD>;
     constexpr int NA = L::NA;
     constexpr uint32_t kDp = 128, kDq = 384;
     const int h = blockIdx.x % p.num_heads;
     const int rest = blockIdx.x / p.num_heads;
     const int seq = rest % p.num_seqs;
     const int qt = p.q_tiles - 1 - rest / p.num_seqs;  // rows with more keys first
-    const Seq s = load_seq(p, seq, !BAND && h == 0 && qt == 0 && threadIdx.x == 0);
+    const Seq s = load_seq(p, seq, h == 0 && qt == 0 && threadIdx.x == 0);
     const int r0 = qt * BM;
     if (!s.ok || r0 >= s.sq) return;
     const int rows = min(BM, s.sq - r0);
     const int p_lo = s.sk - s.sq + r0, p_hi = p_lo + rows - 1;  // positions
-    int kmin = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;
+    const int kmin = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;
     const int last = p.bias.last();
-    if constexpr (BAND) kmin = max(kmin, p_lo - last + 1);
     const int kt0 = kmin / BN;
     const int n = p_hi < 0 ? 0 : p_hi / BN - kt0 + 1;
-    const int n_far = BIAS && !BAND ? max(kmin, p_lo - last + 1) / BN - kt0 : 0;  // tiles that the band leaves out
-    // Tiles in all: the first n_sum only for D.
-    const int n_sum = !BAND && (p_lo + 1 < kFewKeys || (p.window > 0 && p.window < kFewKeys)) ? n : 0;
-    const int n_all = n + n_sum;
+    // Steps: the tiles 0 .. n_pre - 1 with D from dout . out; tiles n_pre .. n - 1 for D alone; then the
+    // same with D.
+    const bool few = p_lo + 1 < kFewKeys || (p.window > 0 && p.window < kFewKeys);
+    const int n_far = BIAS ? min(max(kmin, p_lo - last + 1) / BN - kt0, n) : n;  // tiles of the last bucket alone
+    const int n_pre = few ? 0 : n_far;
+    const int n_all = 2 * n - n_pre;
+    auto tile_of = [&](int j) -> int { return j < n ? j : j - (n - n_pre); };
     const int64_t stat_row = static_cast<int64_t>(h) * p.total_q + s.q_start + r0;
     __nv_bfloat16 *dq = p.dq + (static_cast<int64_t>(s.q_start) + r0) * p.dq_stride + h * HD;
     if (n == 0) {
-        if constexpr (!BAND) {
-            zero_rows<HD>(dq, p.dq_stride, rows);
-            for (int i = threadIdx.x; i < rows; i += kThreads) p.delta[stat_row + i] = 0.f;
-        }
+        zero_rows<HD>(dq, p.dq_stride, rows);
+        for (int i = threadIdx.x; i < rows; i += kThreads) p.delta[stat_row + i] = 0.f;
         return;
     }
     const Cta c = setup<L>();
@@ -401,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
     const uint32_t sQ = c.base + L::OFF_RES, sDo = sQ + L::TILE;
     auto sK = [&](int st) -> uint32_t { return c.base + L::OFF_A + st * L::TILE; };
     auto sV = [&](int st) -> uint32_t { return c.base + L::OFF_B + st * L::TILE; };
-    // [384], or the band's windows [8][96] and sums [8][128].
+    // The rows' half sums [2][128], the warps' runs of diagonals [8][32].
     float *small = reinterpret_cast<float *>(c.sb + L::OFF_SMALL);
     const int kvh = h / p.group;
     // What the element-wise warps have at the end.
@@ -412,9 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
     if (warp == kWarpLoad) {
         if (lane < 4) prefetch_tmap(lane == 0 ? p.tmap_q : lane == 1 ? p.tmap_do : lane == 2 ? p.tmap_k : p.tmap_v);
         uint32_t lands = 0;
-        // (Rows behind the sequence stay in their own rows of every product here, but the band's sums
-        // run across rows.)
-        const bool edit = BAND && ragged(rows);
+        // (Sums along diagonals run across rows; in all else a row behind the sequence stays on its own.)
+        const bool edit = BIAS && ragged(rows);
         if (lane == 0) mbar_arrive_expect_tx(bar(edit ? B_LAND : B_RES), 2 * L::TILE);
         __syncwarp();
         load_tile<HD>(p.tmap_q, sQ, h, s.q_start, r0, s.sq, bar(edit ? B_LAND : B_RES));
@@ -430,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             if (ok && lane == 0) mbar_arrive(bar(B_RES));
         }
         auto load = [&](const CUtensorMap *map, uint32_t dst, int j, uint32_t full) -> bool {
-            return load_stage<HD>(map, dst, kvh, s.k_start, (kt0 + (j < n_sum ? j : j - n_sum)) * BN, s.sk, full, bar(B_LAND), lands,
+            return load_stage<HD>(map, dst, kvh, s.k_start, (kt0 + tile_of(j)) * BN, s.sk, full, bar(B_LAND), lands,
                                   c.abort_flag, p.err, [] {});
         };
         for (int j = 0; ok && j < n_all; ++j) {
@@ -462,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 ok = wait(B_DSFULL + (j & 1), (j >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                if (!BAND && j >= n_sum) issue_ab<HD>(c.tmem + kDq, c.tmem + kDp + 128u * (j & 1), sK(j % NA), j == n_sum);
+                if (j < n_pre || j >= n)
+                    issue_ab<HD>(c.tmem + kDq, c.tmem + kDp + 128u * (j & 1), sK(j % NA), j == (n_pre > 0 ? 0 : n));
                 mma_commit(bar(B_AEMPTY + j % NA));
                 if (j + 1 == n_all) mma_commit(bar(B_DONE));
             }
@@ -485,8 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
         const uint64_t sl2x2 = f2_pack(sl2, sl2), far2 = f2_pack(far, far);
         for (int j = 0; j < n_all; ++j) {
             const uint32_t dp = c.tmem + t_lane + kDp + 128u * (j & 1) + 64u * wg;
-            const bool sum_only = j < n_sum;
-            const int tile = sum_only ? j : j - n_sum;
+            const bool sum_only = j >= n_pre && j < n;
+            const int tile = tile_of(j);
             const int key0 = (kt0 + tile) * BN + 64 * wg;  // this warpgroup's first key
             if (!wait_warp(bar(B_SFULL), j & 1, c.abort_flag, p.err, kTimeoutNs)) break;
             tc_fence_after();
@@ -525,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             }
 #pragma unroll
             for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = ex2_approx(w[i >> 5][i & 31]);
-            if (BIAS && !BAND && !sum_only && tile < n_far) {
+            if (BIAS && !sum_only && tile < n_far) {
                 float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < 64; ++i) a[i & 3] += w[i >> 5][i & 31];
@@ -544,119 +542,104 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const uint64_t w2 = f2_pack(w[cc][2 * i], w[cc][2 * i + 1]), d2 = f2_pack(d[2 * i], d[2 * i + 1]);
-                    if constexpr (!BAND) acc[i & 1] = f2_fma(w2, d2, acc[i & 1]);
+                    acc[i & 1] = f2_fma(w2, d2, acc[i & 1]);
                     f2_unpack(f2_mul(w2, f2_add(d2, delta2)), w[cc][2 * i], w[cc][2 * i + 1]);
-                    if constexpr (!BAND) pk[16 * cc + i] = pack_bf16x2(w[cc][2 * i], w[cc][2 * i + 1]);
+                    pk[16 * cc + i] = pack_bf16x2(w[cc][2 * i], w[cc][2 * i + 1]);
                 }
             }
-            if constexpr (!BAND) {
-                float a0, a1;
-                f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
-                d_sum += a0 + a1;
-                if (BIAS && !sum_only && tile + 1 == n_far) d_far = d_sum;
-                if (!sum_only) {
-                    tmem_st_32x32b_x32_u(dp, pk);
-                    tmem_wait_st();
-                }
+            float a0, a1;
+            f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
+            d_sum += a0 + a1;
+            if (!sum_only) {
+                if (BIAS && tile + 1 == n_far) d_far = d_sum;
+                tmem_st_32x32b_x32_u(dp, pk);
+                tmem_wait_st();
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_DSFULL + (j & 1)));
-            if (!BAND && j + 1 == n_sum) {
+            if (j + 1 == n && n_pre < n) {
                 // D of the row: this warpgroup's half and the other's.
                 small[128 * wg + row] = d_sum;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_SUMS));
                 if (!wait_warp(bar(B_SUMS), 0, c.abort_flag, p.err, kTimeoutNs)) break;
                 delta = small[row] + small[128 + row];
-                d_sum = 0.f;
+                if (few) d_sum = 0.f;  // (the sums of the last bucket's tiles are formed in the second round)
             }
-            if constexpr (BAND) {
+            if (BIAS && j >= n && tile >= n_far) {
                 // Sums along the diagonals row - column = lane, lane - 32, lane - 64 of the warp's 32 x
                 // 64 block: at column i the lane fetches the element of row (lane + i) % 32.
-                float a0 = 0.f, a1 = 0.f, a2 = 0.f;
+                float a[3] = {0.f, 0.f, 0.f};
 #pragma unroll
                 for (int i = 0; i < 64; ++i) {
                     const float v = __shfl_sync(0xffffffffu, w[i >> 5][i & 31], lane + i);
                     const bool wrap = lane + (i & 31) >= 32;
-                    if (i < 32) {
-                        if (wrap) a1 += v; else a0 += v;
-                    } else {
-                        if (wrap) a2 += v; else a1 += v;
-                    }
+                    if (wrap)
+                        a[(i >> 5) + 1] += v;
+                    else
+                        a[i >> 5] += v;
                 }
-                // window[x]: the sum at distance base + x
-                float *window = small + warp * 96;
-                const int base = p_lo + quarter * 32 - key0 - 64;
-                __syncwarp();
-                window[lane] = a2;
-                window[lane + 32] = a1;
-                window[lane + 64] = a0;
-                __syncwarp();
+                // 32 distances at a time, from the nearest on; a lane adds up a bucket's.
+                float *run = small + 256 + 32 * warp;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int b = lane + 32 * k;
-                    if (b < p.bias.num_buckets) {
-                        const int lo = max(p.bias.first[b] - base, 0), hi = min(p.bias.first[b + 1] - base, 96);
-                        for (int x = lo; x < hi; ++x) by_bucket[k] += window[x];
+                for (int r = 2; r >= 0; --r) {
+                    const int base = p_lo + quarter * 32 - key0 - 32 * r;
+                    __syncwarp();
+                    run[lane] = a[r];
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int b = lane + 32 * k;
+                        if (b < p.bias.num_buckets) {
+                            const int lo = max(p.bias.first[b] - base, 0), hi = min(p.bias.first[b + 1] - base, 32);
+                            for (int x = lo; x < hi; ++x) by_bucket[k] += run[x];
+                        }
                     }
                 }
             }
         }
-        if constexpr (!BAND) {
-            if (wait_warp(bar(B_DONE), 0, c.abort_flag, p.err, kTimeoutNs)) {
-                tc_fence_after();
-                const bool v8 = aligned32(p.dq, p.dq_stride);
-                __nv_bfloat16 *dst = dq + static_cast<int64_t>(row) * p.dq_stride + wg * (HD / 2);
+        if (wait_warp(bar(B_DONE), 0, c.abort_flag, p.err, kTimeoutNs)) {
+            tc_fence_after();
+            const bool v8 = aligned32(p.dq, p.dq_stride);
+            __nv_bfloat16 *dst = dq + static_cast<int64_t>(row) * p.dq_stride + wg * (HD / 2);
 #pragma unroll 1
-                for (int cc = 0; cc < HD / 64; ++cc)
-                    store_chunk(c.tmem + t_lane + kDq + wg * (HD / 2) + cc * 32, p.scale, dst + cc * 32, valid, v8);
-            }
-            if (wg == 1) {
-                small[row] = d_sum;
-                if constexpr (BIAS) {
-                    small[128 + row] = d_far;
-                    small[256 + row] = w_far;
-                }
-            }
-        } else {
-            // (Nothing may arrive at a barrier after the CTA's end.)
-            wait_warp(bar(B_DONE), 0, c.abort_flag, p.err, kTimeoutNs);
-            float *mine = small + 768 + 128 * warp;
+            for (int cc = 0; cc < HD / 64; ++cc)
+                store_chunk(c.tmem + t_lane + kDq + wg * (HD / 2) + cc * 32, p.scale, dst + cc * 32, valid, v8);
+            // What is left to add up goes to K's first stage, which no copy or product uses any more:
+            // the last bucket's half sums of the rows, the warps' buckets.
+            if constexpr (BIAS) {
+                float *sums = reinterpret_cast<float *>(c.sb + L::OFF_A);
+                sums[256 * wg + row] = d_far;
+                sums[256 * wg + 128 + row] = w_far;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mine[lane + 32 * k] = by_bucket[k];
+                for (int k = 0; k < 4; ++k) sums[512 + 128 * warp + lane + 32 * k] = by_bucket[k];
+            }
+            if (n_pre == n) small[128 * wg + row] = d_sum;
         }
     }
     teardown(c);
     if (*c.abort_flag) return;
-    // Partial sums of the buckets of this tile: the last one's far tiles first, the band's are added.
-    [[maybe_unused]] float *partial = nullptr;
-    if constexpr (BIAS)
-        partial = p.partial + ((static_cast<int64_t>(s.q_start / BM) + seq + qt) * p.num_heads + h) * p.bias.num_buckets;
-    if constexpr (BAND) {
-        // Warp by warp: [8][128] behind the windows.
+    // (The half sums of D are in `small` either way.)
+    float far_sum = 0.f;
+    const float *sums = reinterpret_cast<const float *>(c.sb + L::OFF_A);
+    if (threadIdx.x < rows) {
+        const float d = small[threadIdx.x] + small[128 + threadIdx.x];
+        p.delta[stat_row + threadIdx.x] = d;
+        if constexpr (BIAS)
+            far_sum = sums[threadIdx.x] + sums[256 + threadIdx.x] - d * (sums[128 + threadIdx.x] + sums[384 + threadIdx.x]);
+    }
+    if constexpr (BIAS) {
+        __syncthreads();
+        far_sum = warp_sum(far_sum);
+        if (lane == 0) small[warp] = far_sum;  // (warps 4 on: 0)
+        __syncthreads();
         const int b = threadIdx.x;
         if (b < p.bias.num_buckets) {
-            float t = b == p.bias.num_buckets - 1 ? partial[b] : 0.f;
+            float t = b == p.bias.num_buckets - 1 ? (small[0] + small[1]) + (small[2] + small[3]) : 0.f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) t += small[768 + 128 * w + b];
-            partial[b] = t;
-        }
-    } else {
-        float t = 0.f;
-        if (threadIdx.x < rows) {
-            const float d = d_sum + small[threadIdx.x];
-            p.delta[stat_row + threadIdx.x] = d;
-            if constexpr (BIAS) t = d_far + small[128 + threadIdx.x] - d * (w_far + small[256 + threadIdx.x]);
-        }
-        if constexpr (BIAS) {
-            __syncthreads();  // (the rows' sums are read)
-            if (warp < 4) {
-                t = warp_sum(t);
-                if (lane == 0) small[warp] = t;
-            }
-            __syncthreads();
-            if (threadIdx.x == 0) partial[p.bias.num_buckets - 1] = (small[0] + small[1]) + (small[2] + small[3]);
+            for (int w = 0; w < 8; ++w) t += sums[512 + 128 * w + b];
+            p.partial[((static_cast<int64_t>(s.q_start / BM) + seq + qt) * p.num_heads + h) * p.bias.num_buckets + b] = t;
         }
     }
 }
@@ -950,16 +933,15 @@ cudaError_t launch_backward_d(GradParams &p, const PackedGradArgs &g, cudaStream
                                                        const_cast<float *>(p.lse2), p.delta, a.total_q, a.num_heads);
         e = cudaGetLastError();
     }
-    static std::atomic<uint64_t> set[3];
+    static std::atomic<uint64_t> set[2];
     const int64_t q_blocks = static_cast<int64_t>(p.q_tiles) * a.num_seqs * a.num_heads;
     const int64_t k_blocks = (static_cast<int64_t>(a.max_seqlen_k) + BM - 1) / BM * a.num_seqs * a.num_kv_heads;
     const int slots = static_cast<int>(tile_slots(a.total_q, a.num_seqs));
     if (BIAS && e == cudaSuccess)  // (places without a tile)
         e = cudaMemsetAsync(p.partial, 0, static_cast<size_t>(slots) * a.num_heads * a.bias.num_buckets * sizeof(float), stream);
-    if (e == cudaSuccess) e = launch_tiles(grad_q_kernel<HD, BIAS, false>, LayoutQ<HD, false>::SMEM, set[0], q_blocks, p, stream);
+    if (e == cudaSuccess) e = launch_tiles(grad_q_kernel<HD, BIAS>, LayoutQ<HD>::SMEM, set[0], q_blocks, p, stream);
     if (e == cudaSuccess) e = launch_tiles(grad_kv_kernel<HD, BIAS>, LayoutKv<HD>::SMEM, set[1], k_blocks, p, stream);
     if constexpr (BIAS) {
-        if (e == cudaSuccess) e = launch_tiles(grad_q_kernel<HD, true, true>, LayoutQ<HD, true>::SMEM, set[2], q_blocks, p, stream);
         if (e != cudaSuccess) return e;
         grad_bias_kernel<<<a.num_heads, 1024, 0, stream>>>(g.dbias, p.partial, slots, a.num_heads, a.bias.num_buckets);
         e = cudaGetLastError();
