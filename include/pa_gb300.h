@@ -563,12 +563,12 @@ pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const
  * max_distance above num_buckets / 2 and up to 32768; scale positive, below 1e38; total_q and
  * total_k below 2^30; num_seqs <= 65535; the 128-row tiles of max_seqlen_q (max_seqlen_k) times
  * num_seqs times num_heads (num_kv_heads) below 2^31; in the backward call also (total_q / 128 +
- * num_seqs + 1) num_heads.  Sizes of the paged calls as pa_decode and pa_varlen_prefill, but at
+ * num_seqs) num_heads and (total_k / 128 + num_seqs) num_heads.  Sizes of the paged calls as pa_decode and pa_varlen_prefill, but at
  * most 64 query heads a kv head.  Size functions return 0 for what is not supported.
  */
 size_t pa_relative_bias_workspace_size(int num_heads, int num_buckets, int max_distance);
-size_t pa_varlen_attn_backward_workspace_size(int total_q, int num_seqs, int num_heads,
-                                              int num_buckets, int max_distance);
+size_t pa_varlen_attn_backward_workspace_size(int total_q, int total_k, int num_seqs,
+                                              int num_heads, int num_buckets, int max_distance);
 pa_status pa_varlen_attn(void *out, float *lse, const void *q, const void *k, const void *v,
                          int64_t q_stride, int64_t k_stride, int64_t v_stride,
                          const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int num_seqs,

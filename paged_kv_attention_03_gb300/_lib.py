@@ -130,7 +130,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.pa_varlen_prefill_fp4.restype = ctypes.c_int
         lib.pa_relative_bias_workspace_size.argtypes = [i32] * 3
         lib.pa_relative_bias_workspace_size.restype = sz
-        lib.pa_varlen_attn_backward_workspace_size.argtypes = [i32] * 5
+        lib.pa_varlen_attn_backward_workspace_size.argtypes = [i32] * 6
         lib.pa_varlen_attn_backward_workspace_size.restype = sz
         lib.pa_varlen_attn.argtypes = [vp] * 5 + [i64] * 3 + [vp] * 2 + [i32] * 9 + [f32, vp, i32, i32, vp, sz, vp]
         lib.pa_varlen_attn.restype = ctypes.c_int
@@ -602,9 +602,9 @@ def pa_relative_bias_workspace_size(num_heads: int, num_buckets: int, max_distan
 
 
 @functools.lru_cache(maxsize=1024)
-def pa_varlen_attn_backward_workspace_size(total_q: int, num_seqs: int, num_heads: int,
+def pa_varlen_attn_backward_workspace_size(total_q: int, total_k: int, num_seqs: int, num_heads: int,
                                            num_buckets: int = 0, max_distance: int = 0) -> int:
-    return int(load().pa_varlen_attn_backward_workspace_size(total_q, num_seqs, num_heads,
+    return int(load().pa_varlen_attn_backward_workspace_size(total_q, total_k, num_seqs, num_heads,
                                                              num_buckets, max_distance))
 
 
@@ -704,7 +704,7 @@ def pa_varlen_attn_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor
     db = None if dbias is None else _arg(dbias, torch.float32, "dbias", dev, (b[1], heads))
     ws, ws_bytes, workspace = _workspace(
         workspace, 0 if workspace is not None else
-        pa_varlen_attn_backward_workspace_size(total_q, n, heads, b[1], b[2]), dev)
+        pa_varlen_attn_backward_workspace_size(total_q, total_k, n, heads, b[1], b[2]), dev)
     _run("pa_varlen_attn_backward", lib.pa_varlen_attn_backward, dev,
          *(g[0] for g in grads), db, *(g[1] for g in grads),
          _arg(dout, torch.bfloat16, "dout", dev, (total_q, heads, d)), *(x[0] for x in ins),

@@ -21,6 +21,10 @@
 // The products count 7 for the 5 of the formula (S and dP are formed twice); dQ added up across
 // the CTAs of one pass over the keys would need atomics, whose order changes the result.
 //
+// Persistent CTAs, one an SM, take (tile, head) items from a list sorted by the number of steps,
+// dealt in snake order: a CTA's start, about 6600 cycles to its first product, is paid once, and an
+// item's loads run during the end of the one before.
+//
 // Roles in a CTA: warps 0-7 are two warpgroups of element-wise work, each on 64 of a tile's 128
 // columns (a thread owns a TMEM lane, i.e. an accumulator row); warp 8 loads tiles by TMA, warp 9
 // issues the products.  P and dS go back to tensor memory as bf16, over the fp32 tile they came
@@ -54,14 +58,35 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kFewKeys = 128;
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
 
+// 128 queries of a sequence.
+struct alignas(16) QTile {
+    int row;      // first row of q
+    int left;     // rows from there to the sequence's end (1 ..)
+    int pos;      // position of the first row (negative: it sees no key)
+    int k_start;  // first row of k
+    int sk;       // keys
+    int n;        // tiles of 128 keys that some row sees
+    int id;       // place among all query tiles in the sequences' order
+    int pad;
+};
+// 128 keys of a sequence.
+struct alignas(16) KTile {
+    int row;      // first row of k
+    int left;     // rows from there to the sequence's end (1 ..)
+    int key;      // position of the first key
+    int off;      // position of the first query
+    int q_start;  // first row of q
+    int sq;       // queries
+    int n;        // tiles of 128 queries that see some of the keys
+    int pad;
+};
+
 struct GradParams {
     // Boxes of 64 dims of one head: [0] of 128 rows, [1] of 16 rows.
     CUtensorMap tmap_q[2];
     CUtensorMap tmap_do[2];
     CUtensorMap tmap_k[2];
     CUtensorMap tmap_v[2];
-    const int32_t *cu_q;
-    const int32_t *cu_k;
     __nv_bfloat16 *dq;
     __nv_bfloat16 *dk;
     __nv_bfloat16 *dv;
@@ -69,11 +94,11 @@ struct GradParams {
     const float *lse2;  // [num_heads, total_q]: lse in base 2, +inf for a row without keys
     float *delta;       // [num_heads, total_q]: D
     const float *bias_table;
-    float *partial;     // [slots, num_heads, num_buckets]
-    int num_seqs;
+    float *partial;     // [query tiles, num_heads, 8 warps, num_buckets]
+    const int *counts;  // [2]: query tiles, key tiles
+    const QTile *q_list;
+    const KTile *k_list;
     int total_q, total_k;
-    int max_q, max_k;
-    int q_tiles;
     int num_heads, num_kv_heads, group;
     int window;
     float scale, scale_log2;
@@ -81,23 +106,26 @@ struct GradParams {
     RelativeBias bias;
 };
 
-struct Seq {
-    int q_start, sq, k_start, sk;
-    bool ok;
-};
+// First key tile of a query tile, and first query of a key tile.
+__device__ __forceinline__ int first_key(int pos, int window) { return window > 0 ? max(0, pos - window + 1) : 0; }
+__device__ __forceinline__ int first_query(const KTile &t) { return max(0, t.key - t.off); }
 
-__device__ __forceinline__ Seq load_seq(const GradParams &p, int seq, bool report) {
-    Seq s;
-    s.q_start = p.cu_q[seq];
-    s.sq = p.cu_q[seq + 1] - s.q_start;
-    s.k_start = p.cu_k[seq];
-    s.sk = p.cu_k[seq + 1] - s.k_start;
-    const bool q_ok = s.q_start >= 0 && s.sq >= 0 && static_cast<int64_t>(s.q_start) + s.sq <= p.total_q && s.sq <= p.max_q;
-    const bool k_ok = s.k_start >= 0 && s.sk >= 0 && static_cast<int64_t>(s.k_start) + s.sk <= p.total_k && s.sk <= p.max_k;
-    if (report && !q_ok) flag_error(p.err, kErrQueryLen);
-    if (report && !k_ok) flag_error(p.err, kErrSeqRange);
-    s.ok = q_ok && k_ok;
-    return s;
+// Item k of a CTA: (list entry, head), in snake order over the CTAs.  False: no more.
+__device__ __forceinline__ bool item_of(int k, int count, int heads, int &entry, int &head) {
+    const int64_t g = gridDim.x;
+    const int64_t v = k * g + ((k & 1) ? g - 1 - blockIdx.x : blockIdx.x);
+    if (v >= static_cast<int64_t>(count) * heads) return false;
+    entry = static_cast<int>(v / heads);
+    head = static_cast<int>(v - static_cast<int64_t>(entry) * heads);
+    return true;
+}
+template <class Tile>
+__device__ __forceinline__ Tile load_entry(const Tile *list, int i) {
+    Tile t;
+    const int4 a = __ldg(reinterpret_cast<const int4 *>(list + i)), b = __ldg(reinterpret_cast<const int4 *>(list + i) + 1);
+    int *d = reinterpret_cast<int *>(&t);
+    d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
+    return t;
 }
 
 // Shared memory: two resident tiles (Q and dout, or K and V), rings of the tiles that pass by (K
@@ -113,7 +141,7 @@ struct Layout {
     static constexpr uint32_t OFF_B = OFF_A + NA * TILE;  // dout (dK, dV) or V (dQ)
     static constexpr uint32_t OFF_SMALL = OFF_B + NB * TILE;
     static constexpr uint32_t OFF_BAR = OFF_SMALL + SMALL_BYTES;
-    static constexpr uint32_t OFF_MISC = OFF_BAR + 160;
+    static constexpr uint32_t OFF_MISC = OFF_BAR + 176;
     static constexpr uint32_t BYTES = OFF_MISC + 16;
     // At least 116 KB so a single CTA owns an SM (and all of its TMEM).
     static constexpr uint32_t SMEM = (BYTES > 118784u ? BYTES : 118784u);
@@ -121,12 +149,14 @@ struct Layout {
 };
 
 template <int HD>
-using LayoutQ = Layout<HD, 3, 2048>;
+using LayoutQ = Layout<HD, 3, 1024 + 528>;
 template <int HD>
 using LayoutKv = Layout<HD, 2, 2u * 3 * 512>;
 
 enum : int {
     B_RES = 0,      // resident tiles loaded
+    B_RESEMPTY = 20,  // resident tiles read
+    B_ACCFREE = 21,   // accumulators stored (8 warps)
     B_AFULL = 1,    // [3] tile of ring A ready (two arrivals: the copies, and the loading warp)
     B_AEMPTY = 4,   // [3] read
     B_BFULL = 7,    // [2] ring B, likewise
@@ -138,7 +168,7 @@ enum : int {
     B_DSFULL = 16,  // [2] dS in tensor memory (8 warps)
     B_DONE = 18,    // all products done
     B_SUMS = 19,    // both halves of the rows' D written (8 warps)
-    NBARS = 20
+    NBARS = 22
 };
 
 // A [128][HD] tile from row0 of a sequence that ends at row `end`: a box a lane.  A tile that the
@@ -241,9 +271,10 @@ __device__ __forceinline__ void store_chunk(uint32_t taddr, float f, __nv_bfloat
 __device__ __forceinline__ bool aligned32(const void *ptr, int64_t stride) {
     return ((reinterpret_cast<uintptr_t>(ptr) | static_cast<uintptr_t>(stride * 2)) & 31u) == 0;
 }
+// By the element-wise warps.
 template <int HD>
 __device__ __forceinline__ void zero_rows(__nv_bfloat16 *dst, int64_t stride, int rows) {
-    for (int i = threadIdx.x; i < rows * (HD / 8); i += kThreads)
+    for (int i = threadIdx.x; i < rows * (HD / 8); i += 256)
         *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(i / (HD / 8)) * stride + i % (HD / 8) * 8) =
             make_uint4(0u, 0u, 0u, 0u);
 }
@@ -265,6 +296,8 @@ __device__ __forceinline__ Cta setup() {
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     if (threadIdx.x == 0) {
         mbar_init(bar(B_RES), 1);
+        mbar_init(bar(B_RESEMPTY), 1);
+        mbar_init(bar(B_ACCFREE), 8);
         for (int s = 0; s < 3; ++s) {
             mbar_init(bar(B_AFULL + s), 2);
             mbar_init(bar(B_AEMPTY + s), 1);
@@ -311,16 +344,160 @@ __device__ __forceinline__ void teardown(const Cta &c) {
     }
 }
 
-// ------------------------------------------------------------- rows' statistics ---
-// lse in base 2 and dout_i out_i, both as [num_heads, total_q].  A block takes 8 tokens of 8 heads:
-// half a warp (128 dims) or a quarter (64) a row.
+// ------------------------------------------------- lists and rows' statistics ---
+// The tiles of all sequences, sorted by their number of steps (the longest first), by one block.  A
+// warp takes 32 sequences at a time, a lane a tile; the order of equal tiles is left to chance (no
+// result depends on it).  Bad sequences are flagged and have no tiles.
+struct PlanParams {
+    const int32_t *cu_q;
+    const int32_t *cu_k;
+    int num_seqs, total_q, total_k, max_q, max_k, window;
+    int *counts;
+    QTile *q_list;
+    KTile *k_list;
+    unsigned *err;
+};
+constexpr int kPlanBins = 1024;  // longer tiles share the last bin
+
+// emit(chunk of sequences, tile of the chunk, tile of the sequence, the sequence)
+template <class Emit, class Chunk>
+__device__ __forceinline__ void plan_tiles(const PlanParams &p, bool keys, bool report, Emit emit, Chunk chunk) {
+    const int lane = threadIdx.x & 31;
+    for (int s0 = (threadIdx.x >> 5) * 32; s0 < p.num_seqs; s0 += blockDim.x) {
+        int q_start = 0, sq = 0, k_start = 0, sk = 0;
+        const int seq = s0 + lane;
+        bool ok = false;
+        if (seq < p.num_seqs) {
+            q_start = p.cu_q[seq], sq = p.cu_q[seq + 1] - q_start;
+            k_start = p.cu_k[seq], sk = p.cu_k[seq + 1] - k_start;
+            const bool q_ok = q_start >= 0 && sq >= 0 && static_cast<int64_t>(q_start) + sq <= p.total_q && sq <= p.max_q;
+            const bool k_ok = k_start >= 0 && sk >= 0 && static_cast<int64_t>(k_start) + sk <= p.total_k && sk <= p.max_k;
+            if (report && !q_ok) flag_error(p.err, kErrQueryLen);
+            if (report && !k_ok) flag_error(p.err, kErrSeqRange);
+            ok = q_ok && k_ok;
+        }
+        const int tiles = ok ? ((keys ? sk : sq) + BM - 1) / BM : 0;
+        int end = tiles;  // inclusive sum over the lanes
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += x;
+        }
+        const int total = __shfl_sync(0xffffffffu, end, 31);
+        if (lane == 0) chunk(s0 / 32, total);
+        for (int i0 = 0; i0 < total; i0 += 32) {
+            const int i = i0 + lane;
+            int src = 0;  // the first lane whose tiles end behind i
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                if (__shfl_sync(0xffffffffu, end, src + o - 1) <= i) src += o;
+            src = min(src, 31);
+            const int first = __shfl_sync(0xffffffffu, end - tiles, src);
+            const int a = __shfl_sync(0xffffffffu, q_start, src), b = __shfl_sync(0xffffffffu, sq, src);
+            const int c = __shfl_sync(0xffffffffu, k_start, src), d = __shfl_sync(0xffffffffu, sk, src);
+            if (i < total) emit(s0 / 32, i, i - first, a, b, c, d);
+        }
+    }
+}
+
+__device__ __forceinline__ QTile q_tile(const PlanParams &p, int id, int t, int q_start, int sq, int k_start, int sk) {
+    QTile r;
+    r.row = q_start + t * BM;
+    r.left = sq - t * BM;
+    r.pos = sk - sq + t * BM;
+    r.k_start = k_start;
+    r.sk = sk;
+    const int hi = r.pos + min(r.left, BM) - 1;
+    r.n = hi < 0 ? 0 : hi / BN - first_key(r.pos, p.window) / BN + 1;
+    r.id = id;
+    r.pad = 0;
+    return r;
+}
+__device__ __forceinline__ KTile k_tile(const PlanParams &p, int t, int q_start, int sq, int k_start, int sk) {
+    KTile r;
+    r.row = k_start + t * BM;
+    r.left = sk - t * BM;
+    r.key = t * BM;
+    r.off = sk - sq;
+    r.q_start = q_start;
+    r.sq = sq;
+    const int from = first_query(r);
+    int64_t to = sq;
+    if (p.window > 0) to = min(to, static_cast<int64_t>(r.key) + min(r.left, BM) - 1 + p.window - r.off);
+    r.n = to > from ? static_cast<int>((to - from + BN - 1) / BN) : 0;
+    r.pad = 0;
+    return r;
+}
+
+// Exclusive sums of n numbers in shared memory, by one warp; returns their sum.
+__device__ __forceinline__ int exclusive_sums(int *x, int n) {
+    const int lane = threadIdx.x & 31;
+    int sum = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane, v = i < n ? x[i] : 0;
+        int end = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += y;
+        }
+        if (i < n) x[i] = sum + end - v;
+        sum += __shfl_sync(0xffffffffu, end, 31);
+    }
+    return sum;
+}
+
+__device__ __forceinline__ void plan_lists(const PlanParams &p) {
+    __shared__ int bins[kPlanBins];
+    __shared__ int before[65536 / 32];  // tiles of the chunks of 32 sequences before
+    const int chunks = (p.num_seqs + 31) / 32;
+    for (int keys = 0; keys < 2; ++keys) {
+        auto bin = [](int n) { return kPlanBins - 1 - min(n, kPlanBins - 1); };
+        for (int i = threadIdx.x; i < kPlanBins; i += blockDim.x) bins[i] = 0;
+        __syncthreads();
+        plan_tiles(
+            p, keys, keys == 0,
+            [&](int, int, int t, int a, int b, int c, int d) {
+                atomicAdd(&bins[bin(keys ? k_tile(p, t, a, b, c, d).n : q_tile(p, 0, t, a, b, c, d).n)], 1);
+            },
+            [&](int chunk, int tiles) { before[chunk] = tiles; });
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            const int count = exclusive_sums(bins, kPlanBins);
+            exclusive_sums(before, chunks);
+            if (threadIdx.x == 0) p.counts[keys] = count;
+        }
+        __syncthreads();
+        plan_tiles(
+            p, keys, false,
+            [&](int chunk, int i, int t, int a, int b, int c, int d) {
+                if (keys) {
+                    const KTile x = k_tile(p, t, a, b, c, d);
+                    p.k_list[atomicAdd(&bins[bin(x.n)], 1)] = x;
+                } else {
+                    const QTile x = q_tile(p, before[chunk] + i, t, a, b, c, d);
+                    p.q_list[atomicAdd(&bins[bin(x.n)], 1)] = x;
+                }
+            },
+            [](int, int) {});
+        __syncthreads();
+    }
+}
+
+// lse in base 2 and dout_i out_i, both as [num_heads, total_q]: a block takes 8 tokens of 8 heads, half
+// a warp (128 dims) or a quarter (64) a row.  The first block makes the lists.
 template <int HD>
 __global__ void __launch_bounds__(256)
     grad_stat_kernel(const uint4 *__restrict__ out, const uint4 *__restrict__ dout, const float *__restrict__ lse,
-                     float *__restrict__ lse2, float *__restrict__ delta, int total_q, int num_heads) {
+                     float *__restrict__ lse2, float *__restrict__ delta, int total_q, int num_heads,
+                     const __grid_constant__ PlanParams plan) {
     constexpr int LANES = HD / 8, ROWS = 256 / LANES;
     __shared__ float s_l[8][9], s_d[8][9];  // [head][token]
-    const int t0 = blockIdx.x * 8, h0 = blockIdx.y * 8;
+    if (blockIdx.x == 0) {
+        if (blockIdx.y == 0) plan_lists(plan);
+        return;
+    }
+    const int t0 = (blockIdx.x - 1) * 8, h0 = blockIdx.y * 8;
     const int l = threadIdx.x % LANES;
 #pragma unroll
     for (int r = threadIdx.x / LANES; r < 64; r += ROWS) {
@@ -366,81 +543,81 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
     using L = LayoutQ<HD>;
     constexpr int NA = L::NA;
     constexpr uint32_t kDp = 128, kDq = 384;
-    const int h = blockIdx.x % p.num_heads;
-    const int rest = blockIdx.x / p.num_heads;
-    const int seq = rest % p.num_seqs;
-    const int qt = p.q_tiles - 1 - rest / p.num_seqs;  // rows with more keys first
-    const Seq s = load_seq(p, seq, h == 0 && qt == 0 && threadIdx.x == 0);
-    const int r0 = qt * BM;
-    if (!s.ok || r0 >= s.sq) return;
-    const int rows = min(BM, s.sq - r0);
-    const int p_lo = s.sk - s.sq + r0, p_hi = p_lo + rows - 1;  // positions
-    const int kmin = p.window > 0 ? max(0, p_lo - p.window + 1) : 0;
-    const int last = p.bias.last();
-    const int kt0 = kmin / BN;
-    const int n = p_hi < 0 ? 0 : p_hi / BN - kt0 + 1;
-    // Steps: the tiles 0 .. n_pre - 1 with D from dout . out; tiles n_pre .. n - 1 for D alone; then the
-    // same with D.
-    const bool few = p_lo + 1 < kFewKeys || (p.window > 0 && p.window < kFewKeys);
-    const int n_far = BIAS ? min(max(kmin, p_lo - last + 1) / BN - kt0, n) : n;  // tiles of the last bucket alone
-    const int n_pre = few ? 0 : n_far;
-    const int n_all = 2 * n - n_pre;
-    auto tile_of = [&](int j) -> int { return j < n ? j : j - (n - n_pre); };
-    const int64_t stat_row = static_cast<int64_t>(h) * p.total_q + s.q_start + r0;
-    __nv_bfloat16 *dq = p.dq + (static_cast<int64_t>(s.q_start) + r0) * p.dq_stride + h * HD;
-    if (n == 0) {
-        zero_rows<HD>(dq, p.dq_stride, rows);
-        for (int i = threadIdx.x; i < rows; i += kThreads) p.delta[stat_row + i] = 0.f;
-        return;
+    if constexpr (BIAS) {  // the buckets' first distances, behind the rows' sums
+        extern __shared__ __align__(1024) uint8_t smem_raw[];
+        int *first = reinterpret_cast<int *>(smem_raw + L::OFF_SMALL + 1024);
+        for (int i = threadIdx.x; i <= p.bias.num_buckets; i += kThreads) first[i] = p.bias.first[i];
     }
     const Cta c = setup<L>();
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sQ = c.base + L::OFF_RES, sDo = sQ + L::TILE;
-    auto sK = [&](int st) -> uint32_t { return c.base + L::OFF_A + st * L::TILE; };
-    auto sV = [&](int st) -> uint32_t { return c.base + L::OFF_B + st * L::TILE; };
-    // The rows' half sums [2][128], the warps' runs of diagonals [8][32].
-    float *small = reinterpret_cast<float *>(c.sb + L::OFF_SMALL);
-    const int kvh = h / p.group;
-    // What the element-wise warps have at the end.
-    float d_sum = 0.f;
-    [[maybe_unused]] float d_far = 0.f, w_far = 0.f;  // sums of P dP and of P over the first n_far tiles
-    [[maybe_unused]] float by_bucket[4] = {0.f, 0.f, 0.f, 0.f};
+    auto sK = [&](uint32_t st) -> uint32_t { return c.base + L::OFF_A + st * L::TILE; };
+    auto sV = [&](uint32_t st) -> uint32_t { return c.base + L::OFF_B + st * L::TILE; };
+    const int last = p.bias.last();
+    const int count = *p.counts;
+    // An item's steps: the tiles 0 .. n_pre - 1 with D from dout . out; tiles n_pre .. n - 1 for D alone;
+    // then the same with D.
+    struct Steps {
+        int n, n_far, n_pre, n_all, kt0;
+        __device__ int tile(int j) const { return j < n ? j : j - (n - n_pre); }
+    };
+    auto steps_of = [&](const QTile &t) -> Steps {
+        Steps s;
+        const int kmin = first_key(t.pos, p.window);
+        s.n = t.n;
+        s.kt0 = kmin / BN;
+        // (tiles of the last bucket alone)
+        s.n_far = BIAS ? min(max(kmin, t.pos - last + 1) / BN - s.kt0, t.n) : t.n;
+        const bool few = t.pos + 1 < kFewKeys || (p.window > 0 && p.window < kFewKeys);
+        s.n_pre = few ? 0 : s.n_far;
+        s.n_all = 2 * s.n - s.n_pre;
+        return s;
+    };
 
     if (warp == kWarpLoad) {
         if (lane < 4) prefetch_tmap(lane == 0 ? p.tmap_q : lane == 1 ? p.tmap_do : lane == 2 ? p.tmap_k : p.tmap_v);
-        uint32_t lands = 0;
-        // (Sums along diagonals run across rows; in all else a row behind the sequence stays on its own.)
-        const bool edit = BIAS && ragged(rows);
-        if (lane == 0) mbar_arrive_expect_tx(bar(edit ? B_LAND : B_RES), 2 * L::TILE);
-        __syncwarp();
-        load_tile<HD>(p.tmap_q, sQ, h, s.q_start, r0, s.sq, bar(edit ? B_LAND : B_RES));
-        load_tile<HD>(p.tmap_do, sDo, h, s.q_start, r0, s.sq, bar(edit ? B_LAND : B_RES));
+        uint32_t lands = 0, items = 0, J = 0;
         bool ok = true;
-        if (edit) {
-            ok = wait_warp(bar(B_LAND), lands++ & 1, c.abort_flag, p.err, kTimeoutNs);
-            if (ok) {
-                clear_rows<HD>(sQ, rows);
-                clear_rows<HD>(sDo, rows);
-            }
+        int e, h;
+        for (int k = 0; ok && item_of(k, count, p.num_heads, e, h); ++k) {
+            const QTile t = load_entry(p.q_list, e);
+            if (t.n == 0) continue;
+            const Steps s = steps_of(t);
+            if (items > 0 && !wait_warp(bar(B_RESEMPTY), (items - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+            // (Sums along diagonals run across rows; in all else a row behind the sequence stays on its own.)
+            const bool edit = BIAS && ragged(t.left);
+            const uint32_t land = bar(edit ? B_LAND : B_RES);
+            if (lane == 0) mbar_arrive_expect_tx(land, 2 * L::TILE);
             __syncwarp();
-            if (ok && lane == 0) mbar_arrive(bar(B_RES));
-        }
-        auto load = [&](const CUtensorMap *map, uint32_t dst, int j, uint32_t full) -> bool {
-            return load_stage<HD>(map, dst, kvh, s.k_start, (kt0 + tile_of(j)) * BN, s.sk, full, bar(B_LAND), lands,
-                                  c.abort_flag, p.err, [] {});
-        };
-        for (int j = 0; ok && j < n_all; ++j) {
-            const int sa = j % NA, sb = j & 1;
-            if (j >= NA && !wait_warp(bar(B_AEMPTY + sa), (j / NA - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-            if (!load(p.tmap_k, sK(sa), j, bar(B_AFULL + sa))) break;
-            if (j >= 2 && !wait_warp(bar(B_BEMPTY + sb), ((j >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-            ok = load(p.tmap_v, sV(sb), j, bar(B_BFULL + sb));
+            load_tile<HD>(p.tmap_q, sQ, h, t.row, 0, t.left, land);
+            load_tile<HD>(p.tmap_do, sDo, h, t.row, 0, t.left, land);
+            if (edit) {
+                if (!wait_warp(land, lands++ & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+                clear_rows<HD>(sQ, t.left);
+                clear_rows<HD>(sDo, t.left);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_RES));
+            }
+            ++items;
+            const int kvh = h / p.group;
+            auto load = [&](const CUtensorMap *map, uint32_t dst, int j, uint32_t full) -> bool {
+                return load_stage<HD>(map, dst, kvh, t.k_start, (s.kt0 + s.tile(j)) * BN, t.sk, full, bar(B_LAND), lands,
+                                      c.abort_flag, p.err, [] {});
+            };
+            for (int j = 0; ok && j < s.n_all; ++j, ++J) {
+                const uint32_t sa = J % NA, sb = J & 1;
+                ok = (J < NA || wait_warp(bar(B_AEMPTY + sa), (J / NA - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) &&
+                     load(p.tmap_k, sK(sa), j, bar(B_AFULL + sa)) &&
+                     (J < 2 || wait_warp(bar(B_BEMPTY + sb), ((J >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) &&
+                     load(p.tmap_v, sV(sb), j, bar(B_BFULL + sb));
+            }
         }
     } else if (warp == kWarpMma) {
         if (lane == 0) {
             auto wait = [&](int b, uint32_t parity) { return wait1(bar(b), parity, c.abort_flag, p.err, kTimeoutNs); };
-            auto products = [&](int j) -> bool {  // S(j) and dP(j)
+            uint32_t items = 0, J = 0;
+            auto products = [&](uint32_t j, bool end) -> bool {  // S(j) and dP(j)
                 if (!wait(B_AFULL + j % NA, (j / NA) & 1)) return false;
                 tc_fence_after();
                 issue_abt<HD>(c.tmem, sQ, sK(j % NA));
@@ -450,198 +627,266 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 issue_abt<HD>(c.tmem + kDp + 128u * (j & 1), sDo, sV(j & 1));
                 mma_commit(bar(B_DPFULL + (j & 1)));
                 mma_commit(bar(B_BEMPTY + (j & 1)));
+                if (end) mma_commit(bar(B_RESEMPTY));
                 return true;
             };
-            bool ok = wait(B_RES, 0) && products(0);
-            for (int j = 0; ok && j < n_all; ++j) {
-                // (dP(j + 1) goes where dS(j - 1) was: dQ(j - 1) is before it in the queue.)
-                if (j + 1 < n_all && !(wait(B_PFULL, j & 1) && products(j + 1))) break;
-                ok = wait(B_DSFULL + (j & 1), (j >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                if (j < n_pre || j >= n)
-                    issue_ab<HD>(c.tmem + kDq, c.tmem + kDp + 128u * (j & 1), sK(j % NA), j == (n_pre > 0 ? 0 : n));
-                mma_commit(bar(B_AEMPTY + j % NA));
-                if (j + 1 == n_all) mma_commit(bar(B_DONE));
+            bool ok = true;
+            int e, h;
+            for (int k = 0; ok && item_of(k, count, p.num_heads, e, h); ++k) {
+                const QTile t = load_entry(p.q_list, e);
+                if (t.n == 0) continue;
+                const Steps s = steps_of(t);
+                // (The item before has read S: its dS is waited for.)
+                ok = wait(B_RES, items & 1) && products(J, s.n_all == 1);
+                for (int j = 0; ok && j < s.n_all; ++j, ++J) {
+                    // (dP(J + 1) goes where dS(J - 1) was: dQ(J - 1) is before it in the queue.)
+                    if (j + 1 < s.n_all) ok = wait(B_PFULL, J & 1) && products(J + 1, j + 2 == s.n_all);
+                    ok = ok && wait(B_DSFULL + (J & 1), (J >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (j < s.n_pre || j >= s.n) {
+                        const bool first = j == (s.n_pre > 0 ? 0 : s.n);
+                        if (first && items > 0) {
+                            ok = wait(B_ACCFREE, (items - 1) & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        issue_ab<HD>(c.tmem + kDq, c.tmem + kDp + 128u * (J & 1), sK(J % NA), first);
+                    }
+                    mma_commit(bar(B_AEMPTY + J % NA));
+                    if (j + 1 == s.n_all) mma_commit(bar(B_DONE));
+                }
+                ++items;
             }
         }
     } else {
         const int wg = warp >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
-        const bool valid = row < rows;
-        const float lse2 = valid ? p.lse2[stat_row + row] : INFINITY;
-        float delta = valid ? p.delta[stat_row + row] : 0.f;
         const float sl2 = p.scale_log2;
-        const int pos = p_lo + row;
-        [[maybe_unused]] const float *bias_row = nullptr;
-        float far = -lse2;  // x = sl2 s + far, where the bias is that of the last bucket
-        if constexpr (BIAS) {
-            bias_row = bias_row_of(p.bias_table, h, last);
-            far = __ldg(bias_row + last) - lse2;
-        }
-        const uint64_t sl2x2 = f2_pack(sl2, sl2), far2 = f2_pack(far, far);
-        for (int j = 0; j < n_all; ++j) {
-            const uint32_t dp = c.tmem + t_lane + kDp + 128u * (j & 1) + 64u * wg;
-            const bool sum_only = j >= n_pre && j < n;
-            const int tile = tile_of(j);
-            const int key0 = (kt0 + tile) * BN + 64 * wg;  // this warpgroup's first key
-            if (!wait_warp(bar(B_SFULL), j & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-            tc_fence_after();
-            float w[2][32];  // logits, then weights P
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc) tmem_ld_32x32b_x32(c.tmem + t_lane + 64u * wg + 32u * cc, w[cc]);
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc) tmem_wait_ld_regs(w[cc]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_PFULL));
-            const int d0 = pos - key0;  // distance to the first key
-            bool near = false;
-            if constexpr (BIAS) near = __shfl_sync(0xffffffffu, d0, 0) - 63 < last && __shfl_sync(0xffffffffu, d0, 31) >= 0;
-            if (near) {
-                const float *bt = bias_row + d0;
-#pragma unroll
-                for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = fmaf(w[i >> 5][i & 31], sl2, __ldg(bt - i)) - lse2;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float &a = w[i >> 4][2 * (i & 15)], &b = w[i >> 4][2 * (i & 15) + 1];
-                    f2_unpack(f2_fma(f2_pack(a, b), sl2x2, far2), a, b);
-                }
+        const uint64_t sl2x2 = f2_pack(sl2, sl2);
+        // The rows' half sums, and the buckets' first distances.
+        float *small = reinterpret_cast<float *>(c.sb + L::OFF_SMALL);
+        [[maybe_unused]] const int *first = reinterpret_cast<const int *>(small + 256);
+        const bool v8 = aligned32(p.dq, p.dq_stride);
+        uint32_t items = 0, J = 0;
+        bool ok = true;
+        int e, h;
+        bool more = item_of(0, count, p.num_heads, e, h);
+        QTile next{};
+        float next_lse = 0.f, next_delta = 0.f;
+        auto prefetch = [&] {  // what the next item needs of the rows
+            next = load_entry(p.q_list, e);
+            const int64_t at = static_cast<int64_t>(h) * p.total_q + next.row + row;
+            next_lse = row < next.left ? p.lse2[at] : INFINITY;
+            next_delta = row < next.left ? p.delta[at] : 0.f;
+        };
+        if (more) prefetch();
+        for (int k = 0; ok && more; ++k) {
+            const QTile t = next;
+            const int head = h;
+            const float lse2 = next_lse;
+            float delta = next_delta;
+            const int rows = min(t.left, BM);
+            const int64_t stat_row = static_cast<int64_t>(head) * p.total_q + t.row;
+            __nv_bfloat16 *dq = p.dq + static_cast<int64_t>(t.row) * p.dq_stride + head * HD;
+            more = item_of(k + 1, count, p.num_heads, e, h);
+            [[maybe_unused]] float by_bucket[4] = {0.f, 0.f, 0.f, 0.f};
+            float *partial = nullptr;
+            if constexpr (BIAS)
+                partial = p.partial + ((static_cast<int64_t>(t.id) * p.num_heads + head) * 8 + warp) * p.bias.num_buckets;
+            if (t.n == 0) {
+                zero_rows<HD>(dq, p.dq_stride, rows);
+                if (wg == 0 && row < rows) p.delta[stat_row + row] = 0.f;
+                if constexpr (BIAS)
+                    for (int b = lane; b < p.bias.num_buckets; b += 32) partial[b] = 0.f;
+                if (more) prefetch();
+                continue;
             }
-            if (d0 < 63) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    if (i > d0) w[i >> 5][i & 31] = -INFINITY;
+            const Steps s = steps_of(t);
+            const int pos = t.pos + row;
+            float d_sum = 0.f;
+            [[maybe_unused]] float d_far = 0.f, w_far = 0.f;  // sums of P dP and of P over the first n_far tiles
+            [[maybe_unused]] const float *bias_row = nullptr;
+            float far = -lse2;  // x = sl2 s + far, where the bias is that of the last bucket
+            if constexpr (BIAS) {
+                bias_row = bias_row_of(p.bias_table, head, last);
+                far = __ldg(bias_row + last) - lse2;
             }
-            if (p.window > 0 && d0 >= p.window) {
-                const int first = d0 - p.window + 1;
+            const uint64_t far2 = f2_pack(far, far);
+            for (int j = 0; j < s.n_all; ++j, ++J) {
+                const uint32_t dp = c.tmem + t_lane + kDp + 128u * (J & 1) + 64u * wg;
+                const bool sum_only = j >= s.n_pre && j < s.n;
+                const int tile = s.tile(j);
+                const int key0 = (s.kt0 + tile) * BN + 64 * wg;  // this warpgroup's first key
+                ok = wait_warp(bar(B_SFULL), J & 1, c.abort_flag, p.err, kTimeoutNs);
+                if (!ok) break;
+                tc_fence_after();
+                float w[2][32];  // logits, then weights P
 #pragma unroll
-                for (int i = 0; i < 64; ++i)
-                    if (i < first) w[i >> 5][i & 31] = -INFINITY;
-            }
+                for (int cc = 0; cc < 2; ++cc) tmem_ld_32x32b_x32(c.tmem + t_lane + 64u * wg + 32u * cc, w[cc]);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = ex2_approx(w[i >> 5][i & 31]);
-            if (BIAS && !sum_only && tile < n_far) {
-                float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < 64; ++i) a[i & 3] += w[i >> 5][i & 31];
-                w_far += (a[0] + a[1]) + (a[2] + a[3]);
-            }
-            if (!wait_warp(bar(B_DPFULL + (j & 1)), (j >> 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-            tc_fence_after();
-            uint32_t pk[32];
-            uint64_t acc[2] = {0ull, 0ull};
-            const uint64_t delta2 = f2_pack(-delta, -delta);
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-                float d[32];
-                tmem_ld_32x32b_x32(dp + 32u * cc, d);
-                tmem_wait_ld_regs(d);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const uint64_t w2 = f2_pack(w[cc][2 * i], w[cc][2 * i + 1]), d2 = f2_pack(d[2 * i], d[2 * i + 1]);
-                    acc[i & 1] = f2_fma(w2, d2, acc[i & 1]);
-                    f2_unpack(f2_mul(w2, f2_add(d2, delta2)), w[cc][2 * i], w[cc][2 * i + 1]);
-                    pk[16 * cc + i] = pack_bf16x2(w[cc][2 * i], w[cc][2 * i + 1]);
-                }
-            }
-            float a0, a1;
-            f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
-            d_sum += a0 + a1;
-            if (!sum_only) {
-                if (BIAS && tile + 1 == n_far) d_far = d_sum;
-                tmem_st_32x32b_x32_u(dp, pk);
-                tmem_wait_st();
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_DSFULL + (j & 1)));
-            if (j + 1 == n && n_pre < n) {
-                // D of the row: this warpgroup's half and the other's.
-                small[128 * wg + row] = d_sum;
+                for (int cc = 0; cc < 2; ++cc) tmem_wait_ld_regs(w[cc]);
+                tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_SUMS));
-                if (!wait_warp(bar(B_SUMS), 0, c.abort_flag, p.err, kTimeoutNs)) break;
-                delta = small[row] + small[128 + row];
-                if (few) d_sum = 0.f;  // (the sums of the last bucket's tiles are formed in the second round)
-            }
-            if (BIAS && j >= n && tile >= n_far) {
-                // Sums along the diagonals row - column = lane, lane - 32, lane - 64 of the warp's 32 x
-                // 64 block: at column i the lane fetches the element of row (lane + i) % 32.
-                float a[3] = {0.f, 0.f, 0.f};
+                if (lane == 0) mbar_arrive(bar(B_PFULL));
+                const int d0 = pos - key0;  // distance to the first key
+                bool near = false;
+                const int d00 = __shfl_sync(0xffffffffu, d0, 0);  // the warp's first row's
+                if constexpr (BIAS) near = d00 - 63 < last && d00 + 31 >= 0;
+                if (near) {
+                    // The warp's rows and columns span 95 distances: three registers a lane, from which
+                    // element (row, i) fetches distance d00 + row - i.
+                    float r[3];
 #pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    const float v = __shfl_sync(0xffffffffu, w[i >> 5][i & 31], lane + i);
-                    const bool wrap = lane + (i & 31) >= 32;
-                    if (wrap)
-                        a[(i >> 5) + 1] += v;
-                    else
-                        a[i >> 5] += v;
+                    for (int x = 0; x < 3; ++x) r[x] = __ldg(bias_row + d00 - 64 + 32 * x + lane);
+#pragma unroll
+                    for (int b = 0; b < 32; ++b) {
+                        const bool low = lane + b >= 32;
+#pragma unroll
+                        for (int a = 0; a < 2; ++a) {
+                            const float v = __shfl_sync(0xffffffffu, low ? r[1 - a] : r[2 - a], lane - b);
+                            w[a][b] = fmaf(w[a][b], sl2, v) - lse2;
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float &a = w[i >> 4][2 * (i & 15)], &b = w[i >> 4][2 * (i & 15) + 1];
+                        f2_unpack(f2_fma(f2_pack(a, b), sl2x2, far2), a, b);
+                    }
                 }
-                // 32 distances at a time, from the nearest on; a lane adds up a bucket's.
-                float *run = small + 256 + 32 * warp;
+                if (d0 < 63) {
 #pragma unroll
-                for (int r = 2; r >= 0; --r) {
-                    const int base = p_lo + quarter * 32 - key0 - 32 * r;
-                    __syncwarp();
-                    run[lane] = a[r];
-                    __syncwarp();
+                    for (int i = 0; i < 64; ++i)
+                        if (i > d0) w[i >> 5][i & 31] = -INFINITY;
+                }
+                if (p.window > 0 && d0 >= p.window) {
+                    const int hidden = d0 - p.window + 1;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int b = lane + 32 * k;
-                        if (b < p.bias.num_buckets) {
-                            const int lo = max(p.bias.first[b] - base, 0), hi = min(p.bias.first[b + 1] - base, 32);
-                            for (int x = lo; x < hi; ++x) by_bucket[k] += run[x];
+                    for (int i = 0; i < 64; ++i)
+                        if (i < hidden) w[i >> 5][i & 31] = -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = ex2_approx(w[i >> 5][i & 31]);
+                if (BIAS && !sum_only && tile < s.n_far) {
+                    float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) a[i & 3] += w[i >> 5][i & 31];
+                    w_far += (a[0] + a[1]) + (a[2] + a[3]);
+                }
+                ok = wait_warp(bar(B_DPFULL + (J & 1)), (J >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t pk[32];
+                uint64_t acc[2] = {0ull, 0ull};
+                const uint64_t delta2 = f2_pack(-delta, -delta);
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) {
+                    float d[32];
+                    tmem_ld_32x32b_x32(dp + 32u * cc, d);
+                    tmem_wait_ld_regs(d);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t w2 = f2_pack(w[cc][2 * i], w[cc][2 * i + 1]), d2 = f2_pack(d[2 * i], d[2 * i + 1]);
+                        acc[i & 1] = f2_fma(w2, d2, acc[i & 1]);
+                        f2_unpack(f2_mul(w2, f2_add(d2, delta2)), w[cc][2 * i], w[cc][2 * i + 1]);
+                        pk[16 * cc + i] = pack_bf16x2(w[cc][2 * i], w[cc][2 * i + 1]);
+                    }
+                }
+                float a0, a1;
+                f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
+                d_sum += a0 + a1;
+                if (!sum_only) {
+                    if (BIAS && tile + 1 == s.n_far) d_far = d_sum;
+                    tmem_st_32x32b_x32_u(dp, pk);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_DSFULL + (J & 1)));
+                if (j + 1 == s.n) {
+                    // D of the row: this warpgroup's half and the other's.
+                    small[128 * wg + row] = d_sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_SUMS));
+                    ok = wait_warp(bar(B_SUMS), items & 1, c.abort_flag, p.err, kTimeoutNs);
+                    if (!ok) break;
+                    delta = small[row] + small[128 + row];
+                    if (s.n_pre == 0) d_sum = 0.f;  // (the last bucket's tiles are added up in the second round)
+                    if (wg == 0 && row < rows) p.delta[stat_row + row] = delta;
+                }
+                if (BIAS && j >= s.n && tile >= s.n_far) {
+                    // Sums along the diagonals row - column = lane, lane - 32, lane - 64 of the warp's 32 x
+                    // 64 block: at column i the lane fetches the element of row (lane + i) % 32.
+                    float a[3] = {0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int b = 0; b < 32; ++b) {
+                        const bool wrap = lane + b >= 32;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float v = __shfl_sync(0xffffffffu, w[x][b], lane + b);
+                            if (wrap)
+                                a[x + 1] += v;
+                            else
+                                a[x] += v;
+                        }
+                    }
+                    // 32 distances at a time: runs of a bucket's are added up from its first one on (`heads`
+                    // marks those), and the lane that has the bucket fetches the sum at its end.
+#pragma unroll
+                    for (int r = 0; r < 3; ++r) {
+                        const int base = d00 - 32 * r;
+                        uint32_t heads = 0u;
+                        for (int b = lane; b < p.bias.num_buckets; b += 32) {
+                            const int x = first[b] - base;
+                            if (x >= 0 && x < 32) heads |= 1u << x;
+                        }
+                        heads = __reduce_or_sync(0xffffffffu, heads);
+                        const uint32_t mine = heads & (0xffffffffu >> (31 - lane));
+                        const int from = mine != 0u ? 31 - __clz(mine) : 0;
+                        float v = a[r];
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const float x = __shfl_up_sync(0xffffffffu, v, o);
+                            if (lane - o >= from) v += x;
+                        }
+#pragma unroll
+                        for (int k4 = 0; k4 < 4; ++k4) {
+                            if (32 * k4 >= p.bias.num_buckets) break;
+                            const int b = lane + 32 * k4;
+                            const bool in = b < p.bias.num_buckets;
+                            const int lo = in ? first[b] - base : 32, hi = in ? min(first[b + 1] - base, 32) : 0;
+                            const float x = __shfl_sync(0xffffffffu, v, hi - 1);
+                            if (lo < 32 && hi > max(lo, 0)) by_bucket[k4] += x;
                         }
                     }
                 }
             }
-        }
-        if (wait_warp(bar(B_DONE), 0, c.abort_flag, p.err, kTimeoutNs)) {
+            if (!ok) break;
+            if constexpr (BIAS) {
+                const float t_far = warp_sum(d_far - delta * w_far);
+#pragma unroll
+                for (int k4 = 0; k4 < 4; ++k4) {
+                    const int b = lane + 32 * k4;
+                    if (b < p.bias.num_buckets) partial[b] = by_bucket[k4] + (b == p.bias.num_buckets - 1 ? t_far : 0.f);
+                }
+            }
+            if (more) prefetch();
+            ok = wait_warp(bar(B_DONE), items & 1, c.abort_flag, p.err, kTimeoutNs);
+            if (!ok) break;
             tc_fence_after();
-            const bool v8 = aligned32(p.dq, p.dq_stride);
             __nv_bfloat16 *dst = dq + static_cast<int64_t>(row) * p.dq_stride + wg * (HD / 2);
 #pragma unroll 1
             for (int cc = 0; cc < HD / 64; ++cc)
-                store_chunk(c.tmem + t_lane + kDq + wg * (HD / 2) + cc * 32, p.scale, dst + cc * 32, valid, v8);
-            // What is left to add up goes to K's first stage, which no copy or product uses any more:
-            // the last bucket's half sums of the rows, the warps' buckets.
-            if constexpr (BIAS) {
-                float *sums = reinterpret_cast<float *>(c.sb + L::OFF_A);
-                sums[256 * wg + row] = d_far;
-                sums[256 * wg + 128 + row] = w_far;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sums[512 + 128 * warp + lane + 32 * k] = by_bucket[k];
-            }
-            if (n_pre == n) small[128 * wg + row] = d_sum;
+                store_chunk(c.tmem + t_lane + kDq + wg * (HD / 2) + cc * 32, p.scale, dst + cc * 32, row < rows, v8);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_ACCFREE));
+            ++items;
         }
     }
     teardown(c);
-    if (*c.abort_flag) return;
-    // (The half sums of D are in `small` either way.)
-    float far_sum = 0.f;
-    const float *sums = reinterpret_cast<const float *>(c.sb + L::OFF_A);
-    if (threadIdx.x < rows) {
-        const float d = small[threadIdx.x] + small[128 + threadIdx.x];
-        p.delta[stat_row + threadIdx.x] = d;
-        if constexpr (BIAS)
-            far_sum = sums[threadIdx.x] + sums[256 + threadIdx.x] - d * (sums[128 + threadIdx.x] + sums[384 + threadIdx.x]);
-    }
-    if constexpr (BIAS) {
-        __syncthreads();
-        far_sum = warp_sum(far_sum);
-        if (lane == 0) small[warp] = far_sum;  // (warps 4 on: 0)
-        __syncthreads();
-        const int b = threadIdx.x;
-        if (b < p.bias.num_buckets) {
-            float t = b == p.bias.num_buckets - 1 ? (small[0] + small[1]) + (small[2] + small[3]) : 0.f;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) t += sums[512 + 128 * w + b];
-            p.partial[((static_cast<int64_t>(s.q_start / BM) + seq + qt) * p.num_heads + h) * p.bias.num_buckets + b] = t;
-        }
-    }
 }
 
 // --------------------------------------------------------------------- dK, dV ---
@@ -653,27 +898,6 @@ template <int HD, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_constant__ GradParams p) {
     using L = LayoutKv<HD>;
     constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 384;
-    const int kvh = blockIdx.x % p.num_kv_heads;
-    const int rest = blockIdx.x / p.num_kv_heads;
-    const int seq = rest % p.num_seqs;
-    const int kt = rest / p.num_seqs;  // the first keys are seen by the most rows
-    const Seq s = load_seq(p, seq, false);
-    const int k_lo = kt * BM;
-    if (!s.ok || k_lo >= s.sk) return;
-    const int rows = min(BM, s.sk - k_lo);
-    const int off = s.sk - s.sq;  // position of the first query
-    const int r_first = max(0, k_lo - off);
-    int r_end = s.sq;
-    if (p.window > 0) r_end = static_cast<int>(min(static_cast<int64_t>(r_end), static_cast<int64_t>(k_lo) + rows - 1 + p.window - off));
-    const int nq = r_end > r_first ? (r_end - r_first + BN - 1) / BN : 0;
-    const int n = nq * p.group;
-    __nv_bfloat16 *dk = p.dk + (static_cast<int64_t>(s.k_start) + k_lo) * p.dk_stride + kvh * HD;
-    __nv_bfloat16 *dv = p.dv + (static_cast<int64_t>(s.k_start) + k_lo) * p.dv_stride + kvh * HD;
-    if (n == 0) {  // no row sees these keys
-        zero_rows<HD>(dk, p.dk_stride, rows);
-        zero_rows<HD>(dv, p.dv_stride, rows);
-        return;
-    }
     const Cta c = setup<L>();
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -684,92 +908,125 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
     auto stat = [&](int st) -> float * { return reinterpret_cast<float *>(c.sb + L::OFF_SMALL) + st * 384; };
     const int last = p.bias.last();
 
+    const int count = p.counts[1];
+
     if (warp == kWarpLoad) {
         if (lane < 4) prefetch_tmap(lane == 0 ? p.tmap_q : lane == 1 ? p.tmap_do : lane == 2 ? p.tmap_k : p.tmap_v);
-        if (lane == 0) mbar_arrive_expect_tx(bar(B_RES), 2 * L::TILE);
-        __syncwarp();
-        load_tile<HD>(p.tmap_k, sK, kvh, s.k_start, k_lo, s.sk, bar(B_RES));
-        load_tile<HD>(p.tmap_v, sV, kvh, s.k_start, k_lo, s.sk, bar(B_RES));
-        uint32_t lands = 0;
-        int g = 0, t = 0;
-        for (int i = 0; i < n; ++i) {
-            const int st = i & 1;
-            const int r = r_first + t * BN, head = kvh * p.group + g;
-            // (dout's stage is free first: dV comes before dK.)
-            if (i >= 2 && !wait_warp(bar(B_BEMPTY + st), ((i >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-            if (!load_stage<HD>(p.tmap_do, sDo(st), head, s.q_start, r, s.sq, bar(B_BFULL + st), bar(B_LAND), lands, c.abort_flag, p.err, [] {})) break;
-            if (i >= 2 && !wait_warp(bar(B_AEMPTY + st), ((i >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-            auto stats = [&] {
-                float far = 0.f;
-                if constexpr (BIAS) far = __ldg(bias_row_of(p.bias_table, head, last) + last);
-                const int64_t at = static_cast<int64_t>(head) * p.total_q + s.q_start + r;
+        uint32_t lands = 0, items = 0, J = 0;
+        bool ok = true;
+        int e, kvh;
+        for (int k = 0; ok && item_of(k, count, p.num_kv_heads, e, kvh); ++k) {
+            const KTile t = load_entry(p.k_list, e);
+            if (t.n == 0) continue;
+            if (items > 0 && !wait_warp(bar(B_RESEMPTY), (items - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+            if (lane == 0) mbar_arrive_expect_tx(bar(B_RES), 2 * L::TILE);
+            __syncwarp();
+            load_tile<HD>(p.tmap_k, sK, kvh, t.row, 0, t.left, bar(B_RES));
+            load_tile<HD>(p.tmap_v, sV, kvh, t.row, 0, t.left, bar(B_RES));
+            ++items;
+            const int r_first = first_query(t);
+            for (int i = 0; ok && i < t.n * p.group; ++i, ++J) {
+                const uint32_t st = J & 1;
+                const int r = r_first + i % t.n * BN, head = kvh * p.group + i / t.n;
+                auto stats = [&] {
+                    float far = 0.f;
+                    if constexpr (BIAS) far = __ldg(bias_row_of(p.bias_table, head, last) + last);
+                    const int64_t at = static_cast<int64_t>(head) * p.total_q + t.q_start + r;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int x = lane + 32 * e;
-                    const bool in = r + x < s.sq;
-                    const float l2 = in ? p.lse2[at + x] : INFINITY;
-                    stat(st)[x] = -l2;
-                    stat(st)[128 + x] = in ? -p.delta[at + x] : 0.f;
-                    if constexpr (BIAS) stat(st)[256 + x] = far - l2;
-                }
-            };
-            if (!load_stage<HD>(p.tmap_q, sQ(st), head, s.q_start, r, s.sq, bar(B_AFULL + st), bar(B_LAND), lands, c.abort_flag, p.err, stats)) break;
-            if (++t == nq) {
-                t = 0;
-                ++g;
+                    for (int x4 = 0; x4 < 4; ++x4) {
+                        const int x = lane + 32 * x4;
+                        const bool in = r + x < t.sq;
+                        const float l2 = in ? p.lse2[at + x] : INFINITY;
+                        stat(st)[x] = -l2;
+                        stat(st)[128 + x] = in ? -p.delta[at + x] : 0.f;
+                        if constexpr (BIAS) stat(st)[256 + x] = far - l2;
+                    }
+                };
+                // (dout's stage is free first: dV comes before dK.)
+                ok = (J < 2 || wait_warp(bar(B_BEMPTY + st), ((J >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) &&
+                     load_stage<HD>(p.tmap_do, sDo(st), head, t.q_start, r, t.sq, bar(B_BFULL + st), bar(B_LAND), lands, c.abort_flag,
+                                    p.err, [] {}) &&
+                     (J < 2 || wait_warp(bar(B_AEMPTY + st), ((J >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) &&
+                     load_stage<HD>(p.tmap_q, sQ(st), head, t.q_start, r, t.sq, bar(B_AFULL + st), bar(B_LAND), lands, c.abort_flag,
+                                    p.err, stats);
             }
         }
     } else if (warp == kWarpMma) {
         if (lane == 0) {
-            auto wait = [&](int b, uint32_t parity) { return wait1(bar(b), parity, c.abort_flag, p.err, kTimeoutNs); };
-            bool ok = wait(B_RES, 0) && wait(B_AFULL, 0);
-            if (ok) {
+            auto wait = [&](int b, uint32_t parity) {
+                const bool ok = wait1(bar(b), parity, c.abort_flag, p.err, kTimeoutNs);
                 tc_fence_after();
-                issue_abt<HD>(c.tmem + kS, sK, sQ(0));
+                return ok;
+            };
+            uint32_t items = 0, J = 0;
+            bool ok = true;
+            int e, kvh;
+            for (int k = 0; ok && item_of(k, count, p.num_kv_heads, e, kvh); ++k) {
+                const int n = load_entry(p.k_list, e).n * p.group;
+                if (n == 0) continue;
+                ok = wait(B_RES, items & 1) && wait(B_AFULL + (J & 1), (J >> 1) & 1);
+                if (!ok) break;
+                issue_abt<HD>(c.tmem + kS, sK, sQ(J & 1));
                 mma_commit(bar(B_SFULL));
-            }
-            for (int i = 0; ok && i < n; ++i) {
-                const int st = i & 1;
-                ok = wait(B_BFULL + st, (i >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                issue_abt<HD>(c.tmem + kDp, sV, sDo(st));
-                mma_commit(bar(B_DPFULL));
-                ok = wait(B_PFULL, i & 1);
-                if (!ok) break;
-                tc_fence_after();
-                issue_ab<HD>(c.tmem + kDv, c.tmem + kS, sDo(st), i == 0);
-                mma_commit(bar(B_BEMPTY + st));
-                if (i + 1 < n) {
-                    const int sn = (i + 1) & 1;
-                    ok = wait(B_AFULL + sn, ((i + 1) >> 1) & 1);
+                for (int i = 0; i < n; ++i, ++J) {
+                    const uint32_t st = J & 1, sn = st ^ 1u;
+                    ok = wait(B_BFULL + st, (J >> 1) & 1);
                     if (!ok) break;
-                    tc_fence_after();
-                    issue_abt<HD>(c.tmem + kS, sK, sQ(sn));
-                    mma_commit(bar(B_SFULL));
+                    issue_abt<HD>(c.tmem + kDp, sV, sDo(st));
+                    mma_commit(bar(B_DPFULL));
+                    if (i + 1 == n) mma_commit(bar(B_RESEMPTY));
+                    // (The item before's accumulators are stored before they are overwritten.)
+                    ok = wait(B_PFULL, J & 1) && (i > 0 || items == 0 || wait(B_ACCFREE, (items - 1) & 1));
+                    if (!ok) break;
+                    issue_ab<HD>(c.tmem + kDv, c.tmem + kS, sDo(st), i == 0);
+                    mma_commit(bar(B_BEMPTY + st));
+                    if (i + 1 < n) {
+                        ok = wait(B_AFULL + sn, ((J + 1) >> 1) & 1);
+                        if (!ok) break;
+                        issue_abt<HD>(c.tmem + kS, sK, sQ(sn));
+                        mma_commit(bar(B_SFULL));
+                    }
+                    ok = wait(B_DSFULL, J & 1);
+                    if (!ok) break;
+                    issue_ab<HD>(c.tmem + kDk, c.tmem + kDp, sQ(st), i == 0);
+                    mma_commit(bar(B_AEMPTY + st));
                 }
-                ok = wait(B_DSFULL, i & 1);
-                if (!ok) break;
-                tc_fence_after();
-                issue_ab<HD>(c.tmem + kDk, c.tmem + kDp, sQ(st), i == 0);
-                mma_commit(bar(B_AEMPTY + st));
+                if (ok) mma_commit(bar(B_DONE));
+                ++items;
             }
-            if (ok) mma_commit(bar(B_DONE));
         }
     } else {
         const int wg = warp >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
         const float sl2 = p.scale_log2;
-        const int key = k_lo + row;
         const uint32_t sc = c.tmem + t_lane + kS + 64u * wg, dp = c.tmem + t_lane + kDp + 64u * wg;
-        int g = 0, t = 0;
+        uint32_t items = 0, J = 0;
         bool ok = true;
-        for (int i = 0; i < n; ++i) {
-            const int st = i & 1;
-            const int pos0 = off + r_first + t * BN + 64 * wg;  // position of this warpgroup's first query
-            if (!wait_warp(bar(B_AFULL + st), (i >> 1) & 1, c.abort_flag, p.err, kTimeoutNs) ||
-                !wait_warp(bar(B_SFULL), i & 1, c.abort_flag, p.err, kTimeoutNs)) {
+        int e, kvh;
+        bool more = item_of(0, count, p.num_kv_heads, e, kvh);
+        KTile next{};
+        if (more) next = load_entry(p.k_list, e);
+        for (int k = 0; ok && more; ++k) {
+        const KTile t = next;
+        const int head0 = kvh * p.group;
+        const int rows = min(t.left, BM), key = t.key + row;
+        __nv_bfloat16 *dk = p.dk + static_cast<int64_t>(t.row) * p.dk_stride + kvh * HD;
+        __nv_bfloat16 *dv = p.dv + static_cast<int64_t>(t.row) * p.dv_stride + kvh * HD;
+        more = item_of(k + 1, count, p.num_kv_heads, e, kvh);
+        if (more) next = load_entry(p.k_list, e);
+        if (t.n == 0) {  // no row sees these keys
+            zero_rows<HD>(dk, p.dk_stride, rows);
+            zero_rows<HD>(dv, p.dv_stride, rows);
+            continue;
+        }
+        const int pos_first = t.off + first_query(t) + 64 * wg;  // of this warpgroup's first query
+        for (int g = 0; ok && g < p.group; ++g)
+        for (int q = 0; q < t.n; ++q, ++J) {
+            const uint32_t st = J & 1;
+            const int pos0 = pos_first + q * BN;
+            if (!wait_warp(bar(B_AFULL + st), (J >> 1) & 1, c.abort_flag, p.err, kTimeoutNs) ||
+                !wait_warp(bar(B_SFULL), J & 1, c.abort_flag, p.err, kTimeoutNs)) {
                 ok = false;
                 break;
             }
@@ -784,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             // (lane 31 has the nearest key)
             if constexpr (BIAS) near = __shfl_sync(0xffffffffu, d0, 31) < last && __shfl_sync(0xffffffffu, d0, 0) + 63 >= 0;
             if (near) {
-                const float *bt = bias_row_of(p.bias_table, kvh * p.group + g, last) + d0;
+                const float *bt = bias_row_of(p.bias_table, head0 + g, last) + d0;
                 const float4 *nl = reinterpret_cast<const float4 *>(stat(st) + 64 * wg);
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
@@ -830,7 +1087,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_PFULL));
-            if (!wait_warp(bar(B_DPFULL), i & 1, c.abort_flag, p.err, kTimeoutNs)) {
+            if (!wait_warp(bar(B_DPFULL), J & 1, c.abort_flag, p.err, kTimeoutNs)) {
                 ok = false;
                 break;
             }
@@ -857,39 +1114,44 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_DSFULL));
-            if (++t == nq) {
-                t = 0;
-                ++g;
-            }
         }
-        if (ok && wait_warp(bar(B_DONE), 0, c.abort_flag, p.err, kTimeoutNs)) {
-            tc_fence_after();
-            const int64_t stride = wg ? p.dk_stride : p.dv_stride;
-            __nv_bfloat16 *dst = (wg ? dk : dv) + static_cast<int64_t>(row) * stride;
-            const bool v8 = aligned32(wg ? p.dk : p.dv, stride);
+        ok = ok && wait_warp(bar(B_DONE), items & 1, c.abort_flag, p.err, kTimeoutNs);
+        if (!ok) break;
+        tc_fence_after();
+        const int64_t stride = wg ? p.dk_stride : p.dv_stride;
+        __nv_bfloat16 *dst = (wg ? dk : dv) + static_cast<int64_t>(row) * stride;
+        const bool v8 = aligned32(wg ? p.dk : p.dv, stride);
 #pragma unroll 1
-            for (int cc = 0; cc < HD / 32; ++cc)
-                store_chunk(c.tmem + t_lane + (wg ? kDk : kDv) + cc * 32, wg ? p.scale : 1.f, dst + cc * 32, row < rows, v8);
+        for (int cc = 0; cc < HD / 32; ++cc)
+            store_chunk(c.tmem + t_lane + (wg ? kDk : kDv) + cc * 32, wg ? p.scale : 1.f, dst + cc * 32, row < rows, v8);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_ACCFREE));
+        ++items;
         }
     }
     teardown(c);
 }
 
 // ---------------------------------------------------------------------- dbias ---
-// Sums the query tiles' partial sums in their order, a block a head.
+// Sums the query tiles' partial sums, eight warps' for each, a block a head: always in the same order.
 __global__ void __launch_bounds__(1024)
-    grad_bias_kernel(float *__restrict__ dbias, const float *__restrict__ partial, int slots, int num_heads, int num_buckets) {
-    __shared__ float s[8][128];
-    const int h = blockIdx.x, b = threadIdx.x & 127, part = threadIdx.x >> 7;
+    grad_bias_kernel(float *__restrict__ dbias, const float *__restrict__ partial, const int *__restrict__ counts, int num_heads,
+                     int num_buckets, int log2_width) {  // 2^log2_width threads a row of buckets
+    __shared__ float s[1024];
+    const int h = blockIdx.x, b = threadIdx.x & ((1 << log2_width) - 1), part = threadIdx.x >> log2_width;
+    const int parts = 1024 >> log2_width, rows = *counts * 8;
     float t = 0.f;
-    if (b < num_buckets)
-        for (int i = part; i < slots; i += 8) t += partial[(static_cast<int64_t>(i) * num_heads + h) * num_buckets + b];
-    s[part][b] = t;
+    if (b < num_buckets) {
+#pragma unroll 4
+        for (int r = part; r < rows; r += parts)
+            t += partial[((static_cast<int64_t>(r >> 3) * num_heads + h) * 8 + (r & 7)) * num_buckets + b];
+    }
+    s[threadIdx.x] = t;
     __syncthreads();
     if (part == 0 && b < num_buckets) {
         t = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t += s[i][b];
+        for (int i = 0; i < parts; ++i) t += s[(i << log2_width) + b];
         dbias[b * num_heads + h] = t;
     }
 }
@@ -897,21 +1159,33 @@ __global__ void __launch_bounds__(1024)
 // ------------------------------------------------------------------ host side ---
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Query tiles of all sequences: tile t of sequence i has place cu_seqlens_q[i] / 128 + i + t.
-int64_t tile_slots(int total_q, int num_seqs) { return static_cast<int64_t>(total_q) / BM + num_seqs + 1; }
+// Most tiles that sequences of `total` rows in all can have.
+int64_t most_tiles(int total, int num_seqs) { return static_cast<int64_t>(total) / BM + num_seqs; }
+
+// The workspace: lse2, delta, counts, lists, partial sums.
+struct Workspace {
+    size_t stat, q_list, k_list, partial;
+    size_t bytes() const { return 2 * stat + 256 + q_list + k_list + partial; }
+    Workspace(int total_q, int total_k, int num_seqs, int num_heads, int num_buckets)
+        : stat(up256(static_cast<size_t>(total_q) * num_heads * sizeof(float))),
+          q_list(up256(most_tiles(total_q, num_seqs) * sizeof(QTile))),
+          k_list(up256(most_tiles(total_k, num_seqs) * sizeof(KTile))),
+          partial(up256(static_cast<size_t>(most_tiles(total_q, num_seqs)) * num_heads * 8 * num_buckets * sizeof(float))) {}
+};
 
 template <class Kernel>
-cudaError_t launch_tiles(Kernel kern, uint32_t smem, std::atomic<uint64_t> &set, int64_t blocks, const GradParams &p,
+cudaError_t launch_tiles(Kernel kern, uint32_t smem, std::atomic<uint64_t> &set, int64_t items, const GradParams &p,
                          cudaStream_t stream) {
-    if (blocks <= 0) return cudaSuccess;
+    if (items <= 0) return cudaSuccess;
     const cudaError_t e = smem_limit_once(kern, static_cast<int>(smem), set);
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p);
+    const int sms = sm_count();
+    kern<<<static_cast<unsigned>(items < sms ? items : sms), kThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <int HD, bool BIAS>
-cudaError_t launch_backward_d(GradParams &p, const PackedGradArgs &g, cudaStream_t stream) {
+cudaError_t launch_backward_d(GradParams &p, const PlanParams &plan, const PackedGradArgs &g, cudaStream_t stream) {
     const PackedArgs &a = g.fwd;
     const int64_t rows = static_cast<int64_t>(a.num_heads) * HD;
     // (Without queries, or keys, nothing is loaded, but a tensor map has a row and an address.)
@@ -926,24 +1200,19 @@ cudaError_t launch_backward_d(GradParams &p, const PackedGradArgs &g, cudaStream
         !rows_map(p.tmap_k, a.k, a.q, a.num_kv_heads, a.total_k, a.k_stride) ||
         !rows_map(p.tmap_v, a.v, a.q, a.num_kv_heads, a.total_k, a.v_stride))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaSuccess;
-    if (a.total_q > 0) {
-        const dim3 grid((a.total_q + 7) / 8, (a.num_heads + 7) / 8);
-        grad_stat_kernel<HD><<<grid, 256, 0, stream>>>(static_cast<const uint4 *>(g.out), static_cast<const uint4 *>(g.dout), g.lse,
-                                                       const_cast<float *>(p.lse2), p.delta, a.total_q, a.num_heads);
-        e = cudaGetLastError();
-    }
+    const dim3 grid((a.total_q + 7) / 8 + 1, (a.num_heads + 7) / 8);
+    grad_stat_kernel<HD><<<grid, 256, 0, stream>>>(static_cast<const uint4 *>(g.out), static_cast<const uint4 *>(g.dout), g.lse,
+                                                   const_cast<float *>(p.lse2), p.delta, a.total_q, a.num_heads, plan);
+    cudaError_t e = cudaGetLastError();
     static std::atomic<uint64_t> set[2];
-    const int64_t q_blocks = static_cast<int64_t>(p.q_tiles) * a.num_seqs * a.num_heads;
-    const int64_t k_blocks = (static_cast<int64_t>(a.max_seqlen_k) + BM - 1) / BM * a.num_seqs * a.num_kv_heads;
-    const int slots = static_cast<int>(tile_slots(a.total_q, a.num_seqs));
-    if (BIAS && e == cudaSuccess)  // (places without a tile)
-        e = cudaMemsetAsync(p.partial, 0, static_cast<size_t>(slots) * a.num_heads * a.bias.num_buckets * sizeof(float), stream);
-    if (e == cudaSuccess) e = launch_tiles(grad_q_kernel<HD, BIAS>, LayoutQ<HD>::SMEM, set[0], q_blocks, p, stream);
-    if (e == cudaSuccess) e = launch_tiles(grad_kv_kernel<HD, BIAS>, LayoutKv<HD>::SMEM, set[1], k_blocks, p, stream);
-    if constexpr (BIAS) {
-        if (e != cudaSuccess) return e;
-        grad_bias_kernel<<<a.num_heads, 1024, 0, stream>>>(g.dbias, p.partial, slots, a.num_heads, a.bias.num_buckets);
+    const int64_t q_items = a.total_q > 0 ? most_tiles(a.total_q, a.num_seqs) * a.num_heads : 0;
+    const int64_t k_items = a.total_k > 0 ? most_tiles(a.total_k, a.num_seqs) * a.num_kv_heads : 0;
+    if (e == cudaSuccess) e = launch_tiles(grad_q_kernel<HD, BIAS>, LayoutQ<HD>::SMEM, set[0], q_items, p, stream);
+    if (e == cudaSuccess) e = launch_tiles(grad_kv_kernel<HD, BIAS>, LayoutKv<HD>::SMEM, set[1], k_items, p, stream);
+    if (BIAS && e == cudaSuccess) {
+        int width = 0;
+        while ((1 << width) < a.bias.num_buckets) ++width;
+        grad_bias_kernel<<<a.num_heads, 1024, 0, stream>>>(g.dbias, p.partial, p.counts, a.num_heads, a.bias.num_buckets, width);
         e = cudaGetLastError();
     }
     return e;
@@ -951,11 +1220,9 @@ cudaError_t launch_backward_d(GradParams &p, const PackedGradArgs &g, cudaStream
 
 }  // namespace
 
-bool packed_grad_workspace(int total_q, int num_seqs, int num_heads, int num_buckets, size_t *bytes) {
-    const int64_t slots = tile_slots(total_q, num_seqs);
-    if (slots * num_heads > INT_MAX) return false;
-    *bytes = 2 * up256(static_cast<size_t>(total_q) * num_heads * sizeof(float)) +
-             up256(static_cast<size_t>(slots) * num_heads * num_buckets * sizeof(float));
+bool packed_grad_workspace(int total_q, int total_k, int num_seqs, int num_heads, int num_buckets, size_t *bytes) {
+    if (most_tiles(total_q, num_seqs) * num_heads > INT_MAX || most_tiles(total_k, num_seqs) * num_heads > INT_MAX) return false;
+    *bytes = Workspace(total_q, total_k, num_seqs, num_heads, num_buckets).bytes();
     return true;
 }
 
@@ -963,26 +1230,41 @@ cudaError_t launch_packed_attn_backward(const PackedGradArgs &g, cudaStream_t st
     const PackedArgs &a = g.fwd;
     GradParams p;
     memset(&p, 0, sizeof p);
-    p.cu_q = a.cu_seqlens_q;
-    p.cu_k = a.cu_seqlens_k;
     p.dq = static_cast<__nv_bfloat16 *>(g.dq);
     p.dk = static_cast<__nv_bfloat16 *>(g.dk);
     p.dv = static_cast<__nv_bfloat16 *>(g.dv);
     p.dq_stride = g.dq_stride;
     p.dk_stride = g.dk_stride;
     p.dv_stride = g.dv_stride;
-    uint8_t *ws = static_cast<uint8_t *>(g.workspace);
-    const size_t stat = up256(static_cast<size_t>(a.total_q) * a.num_heads * sizeof(float));
-    p.lse2 = reinterpret_cast<const float *>(ws);
-    p.delta = reinterpret_cast<float *>(ws + stat);
-    p.partial = reinterpret_cast<float *>(ws + 2 * stat);
+    const Workspace w(a.total_q, a.total_k, a.num_seqs, a.num_heads, a.bias.num_buckets);
+    uint8_t *at = static_cast<uint8_t *>(g.workspace);
+    auto take = [&](size_t bytes) {
+        uint8_t *const here = at;
+        at += bytes;
+        return here;
+    };
+    p.lse2 = reinterpret_cast<const float *>(take(w.stat));
+    p.delta = reinterpret_cast<float *>(take(w.stat));
+    PlanParams plan;
+    plan.cu_q = a.cu_seqlens_q;
+    plan.cu_k = a.cu_seqlens_k;
+    plan.num_seqs = a.num_seqs;
+    plan.total_q = a.total_q;
+    plan.total_k = a.total_k;
+    plan.max_q = a.max_seqlen_q;
+    plan.max_k = a.max_seqlen_k;
+    plan.window = a.sliding_window;
+    plan.counts = reinterpret_cast<int *>(take(256));
+    plan.q_list = reinterpret_cast<QTile *>(take(w.q_list));
+    plan.k_list = reinterpret_cast<KTile *>(take(w.k_list));
+    plan.err = a.err;
+    p.counts = plan.counts;
+    p.q_list = plan.q_list;
+    p.k_list = plan.k_list;
+    p.partial = reinterpret_cast<float *>(take(w.partial));
     p.bias_table = a.bias_table;
-    p.num_seqs = a.num_seqs;
     p.total_q = a.total_q;
     p.total_k = a.total_k;
-    p.max_q = a.max_seqlen_q;
-    p.max_k = a.max_seqlen_k;
-    p.q_tiles = static_cast<int>((static_cast<int64_t>(a.max_seqlen_q) + BM - 1) / BM);
     p.num_heads = a.num_heads;
     p.num_kv_heads = a.num_kv_heads;
     p.group = a.num_heads / a.num_kv_heads;
@@ -993,8 +1275,8 @@ cudaError_t launch_packed_attn_backward(const PackedGradArgs &g, cudaStream_t st
     p.bias = a.bias;
     const bool bias = a.bias_table != nullptr;
     switch (a.head_dim) {
-        case 64: return bias ? launch_backward_d<64, true>(p, g, stream) : launch_backward_d<64, false>(p, g, stream);
-        case 128: return bias ? launch_backward_d<128, true>(p, g, stream) : launch_backward_d<128, false>(p, g, stream);
+        case 64: return bias ? launch_backward_d<64, true>(p, plan, g, stream) : launch_backward_d<64, false>(p, plan, g, stream);
+        case 128: return bias ? launch_backward_d<128, true>(p, plan, g, stream) : launch_backward_d<128, false>(p, plan, g, stream);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -66,10 +66,11 @@ size_t pa_relative_bias_workspace_size(int num_heads, int num_buckets, int max_d
     return pa::bias_table_bytes(num_heads, b);
 }
 
-size_t pa_varlen_attn_backward_workspace_size(int total_q, int num_seqs, int num_heads, int num_buckets, int max_distance) {
-    if (total_q < 0 || num_seqs < 0 || num_heads <= 0) return 0;
+size_t pa_varlen_attn_backward_workspace_size(int total_q, int total_k, int num_seqs, int num_heads, int num_buckets,
+                                              int max_distance) {
+    if (total_q < 0 || total_k < 0 || num_seqs < 0 || num_heads <= 0 || num_buckets < 0 || num_buckets > pa::kMaxBuckets) return 0;
     size_t bytes = 0;
-    if (!pa::packed_grad_workspace(total_q, num_seqs, num_heads, num_buckets, &bytes)) return 0;
+    if (!pa::packed_grad_workspace(total_q, total_k, num_seqs, num_heads, num_buckets, &bytes)) return 0;
     return bytes + (num_buckets > 0 ? pa_relative_bias_workspace_size(num_heads, num_buckets, max_distance) : 0);
 }
 
@@ -157,7 +158,7 @@ pa_status pa_varlen_attn_backward(void *dq, void *dk, void *dv, float *dbias, in
         return PA_ERR_INVALID_ARG;
     if (total_k > 0 && (!dk || !dv || !aligned(dk, 16) || !aligned(dv, 16))) return PA_ERR_INVALID_ARG;
     size_t need = 0;
-    if (!pa::packed_grad_workspace(total_q, num_seqs, num_heads, num_buckets, &need)) return PA_ERR_UNSUPPORTED;
+    if (!pa::packed_grad_workspace(total_q, total_k, num_seqs, num_heads, num_buckets, &need)) return PA_ERR_UNSUPPORTED;
     const size_t table = bias ? pa::bias_table_bytes(num_heads, a.bias) : 0;
     if (need + table > 0 && (!workspace || workspace_bytes < need + table || !aligned(workspace, 256))) return PA_ERR_INVALID_ARG;
     a.err = pa::device_error_word();

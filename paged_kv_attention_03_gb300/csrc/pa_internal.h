@@ -277,13 +277,16 @@ struct PackedGradArgs {
     void *workspace;   // packed_grad_workspace
 };
 // Bytes of the backward pass's workspace behind the bias table; false: too large for the kernels' counters.
-bool packed_grad_workspace(int total_q, int num_seqs, int num_heads, int num_buckets, size_t *bytes);
+bool packed_grad_workspace(int total_q, int total_k, int num_seqs, int num_heads, int num_buckets, size_t *bytes);
 cudaError_t launch_packed_attn_backward(const PackedGradArgs &a, cudaStream_t stream);
 
 // Tensor map of [d2][d1][d0] 16-bit elements (codes: bytes), boxes [b2][b1][b0], 128-byte swizzle.
 bool encode_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,
                uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t b0, uint32_t b1,
                uint32_t b2, bool codes = false);
+
+// SMs of the current device.
+int sm_count();
 
 // Testing aid behind pa_debug_prefill_stall (process-wide; read at each prefill launch).
 void debug_prefill_stall(int stall, uint64_t wait_ns);

@@ -1419,8 +1419,6 @@ bool encode_3d(CUtensorMap *map, const void *base, uint64_t d0, uint64_t d1, uin
     return r == CUDA_SUCCESS;
 }
 
-namespace {
-
 int sm_count() {
     static std::atomic<int> counts[64];
     int dev = 0;
@@ -1433,6 +1431,8 @@ int sm_count() {
     }
     return n;
 }
+
+namespace {
 
 template <int HD, bool PREFIX, int CACHE = kCacheBf16, bool BIAS = false>
 cudaError_t launch_prefill_d(PrefillKernelParams &kp, const PrefillArgs &a, cudaStream_t stream) {

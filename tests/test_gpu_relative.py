@@ -279,7 +279,7 @@ def test_graph_streams_and_repeats():
             assert torch.equal(a, b)
     cu_q, cu_k = dev(c.cu_q), dev(c.cu_k)
     outs = [torch.empty_like(t) for t in want]
-    ws = torch.empty(pa.pa_varlen_attn_backward_workspace_size(len(c.q), 3, 8, 32, 128), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(pa.pa_varlen_attn_backward_workspace_size(len(c.q), len(c.k), 3, 8, 32, 128), dtype=torch.uint8, device="cuda")
 
     def step():
         pa.pa_varlen_attn(c.q, c.k, c.v, cu_q, cu_k, 300, 300, c.scale, bias=c.bias, max_distance=128, out=outs[0], lse=outs[1], workspace=ws)

@@ -79,7 +79,7 @@ def test_packed_refusals(call):
     lib = pa.load()
     assert call(lib) == INVALID  # no workspace
     table = pa.pa_relative_bias_workspace_size(8, 32, 128)
-    need = table if call is _packed else pa.pa_varlen_attn_backward_workspace_size(10, 2, 8, 32, 128)
+    need = table if call is _packed else pa.pa_varlen_attn_backward_workspace_size(10, 12, 2, 8, 32, 128)
     assert need >= table > 0
     assert call(lib, ws=FAKE, ws_bytes=need - 1) == INVALID
     assert call(lib, ws=FAKE + 16, ws_bytes=need) == INVALID
@@ -132,5 +132,5 @@ def test_size_functions_of_unsupported_sizes():
     assert pa.pa_relative_bias_workspace_size(8, 1, 10) == 0
     assert pa.pa_relative_bias_workspace_size(8, 32, 16) == 0
     assert pa.pa_relative_bias_workspace_size(0, 32, 128) == 0
-    assert pa.pa_varlen_attn_backward_workspace_size(-1, 1, 8) == 0
-    assert pa.pa_varlen_attn_backward_workspace_size(100, 3, 8) > 0
+    assert pa.pa_varlen_attn_backward_workspace_size(-1, 10, 1, 8) == 0
+    assert pa.pa_varlen_attn_backward_workspace_size(100, 90, 3, 8) > 0
