@@ -614,50 +614,53 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             }
         }
     } else if (warp == kWarpMma) {
-        if (lane == 0) {
-            auto wait = [&](int b, uint32_t parity) { return wait1(bar(b), parity, c.abort_flag, p.err, kTimeoutNs); };
-            uint32_t items = 0, J = 0;
-            auto products = [&](uint32_t j, bool end) -> bool {  // S(j) and dP(j)
-                if (!wait(B_AFULL + j % NA, (j / NA) & 1)) return false;
-                tc_fence_after();
+        // The whole warp waits, one lane issues (always the same: a commit covers what its thread issued).
+        auto wait = [&](int b, uint32_t parity) {
+            const bool ok = wait_warp(bar(b), parity, c.abort_flag, p.err, kTimeoutNs);
+            tc_fence_after();
+            return ok;
+        };
+        uint32_t items = 0, J = 0;
+        auto products = [&](uint32_t j, bool end) -> bool {  // S(j) and dP(j)
+            if (!wait(B_AFULL + j % NA, (j / NA) & 1)) return false;
+            if (elect_one()) {
                 issue_abt<HD>(c.tmem, sQ, sK(j % NA));
                 mma_commit(bar(B_SFULL));
-                if (!wait(B_BFULL + (j & 1), (j >> 1) & 1)) return false;
-                tc_fence_after();
+            }
+            __syncwarp();
+            if (!wait(B_BFULL + (j & 1), (j >> 1) & 1)) return false;
+            if (elect_one()) {
                 issue_abt<HD>(c.tmem + kDp + 128u * (j & 1), sDo, sV(j & 1));
                 mma_commit(bar(B_DPFULL + (j & 1)));
                 mma_commit(bar(B_BEMPTY + (j & 1)));
                 if (end) mma_commit(bar(B_RESEMPTY));
-                return true;
-            };
-            bool ok = true;
-            int e, h;
-            for (int k = 0; ok && item_of(k, count, p.num_heads, e, h); ++k) {
-                const QTile t = load_entry(p.q_list, e);
-                if (t.n == 0) continue;
-                const Steps s = steps_of(t);
-                // (The item before has read S: its dS is waited for.)
-                ok = wait(B_RES, items & 1) && products(J, s.n_all == 1);
-                for (int j = 0; ok && j < s.n_all; ++j, ++J) {
-                    // (dP(J + 1) goes where dS(J - 1) was: dQ(J - 1) is before it in the queue.)
-                    if (j + 1 < s.n_all) ok = wait(B_PFULL, J & 1) && products(J + 1, j + 2 == s.n_all);
-                    ok = ok && wait(B_DSFULL + (J & 1), (J >> 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (j < s.n_pre || j >= s.n) {
-                        const bool first = j == (s.n_pre > 0 ? 0 : s.n);
-                        if (first && items > 0) {
-                            ok = wait(B_ACCFREE, (items - 1) & 1);
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = true;
+        int e, h;
+        for (int k = 0; ok && item_of(k, count, p.num_heads, e, h); ++k) {
+            const QTile t = load_entry(p.q_list, e);
+            if (t.n == 0) continue;
+            const Steps s = steps_of(t);
+            // (The item before has read S: its dS is waited for.)
+            ok = wait(B_RES, items & 1) && products(J, s.n_all == 1);
+            for (int j = 0; ok && j < s.n_all; ++j, ++J) {
+                // (dP(J + 1) goes where dS(J - 1) was: dQ(J - 1) is before it in the queue.)
+                if (j + 1 < s.n_all) ok = wait(B_PFULL, J & 1) && products(J + 1, j + 2 == s.n_all);
+                const bool first = j == (s.n_pre > 0 ? 0 : s.n);
+                ok = ok && wait(B_DSFULL + (J & 1), (J >> 1) & 1) && (!first || items == 0 || wait(B_ACCFREE, (items - 1) & 1));
+                if (!ok) break;
+                if (elect_one()) {
+                    if (j < s.n_pre || j >= s.n)
                         issue_ab<HD>(c.tmem + kDq, c.tmem + kDp + 128u * (J & 1), sK(J % NA), first);
-                    }
                     mma_commit(bar(B_AEMPTY + J % NA));
                     if (j + 1 == s.n_all) mma_commit(bar(B_DONE));
                 }
-                ++items;
+                __syncwarp();
             }
+            ++items;
         }
     } else {
         const int wg = warp >> 2, quarter = warp & 3;
@@ -952,48 +955,61 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             }
         }
     } else if (warp == kWarpMma) {
-        if (lane == 0) {
-            auto wait = [&](int b, uint32_t parity) {
-                const bool ok = wait1(bar(b), parity, c.abort_flag, p.err, kTimeoutNs);
-                tc_fence_after();
-                return ok;
-            };
-            uint32_t items = 0, J = 0;
-            bool ok = true;
-            int e, kvh;
-            for (int k = 0; ok && item_of(k, count, p.num_kv_heads, e, kvh); ++k) {
-                const int n = load_entry(p.k_list, e).n * p.group;
-                if (n == 0) continue;
-                ok = wait(B_RES, items & 1) && wait(B_AFULL + (J & 1), (J >> 1) & 1);
-                if (!ok) break;
+        auto wait = [&](int b, uint32_t parity) {
+            const bool ok = wait_warp(bar(b), parity, c.abort_flag, p.err, kTimeoutNs);
+            tc_fence_after();
+            return ok;
+        };
+        uint32_t items = 0, J = 0;
+        bool ok = true;
+        int e, kvh;
+        for (int k = 0; ok && item_of(k, count, p.num_kv_heads, e, kvh); ++k) {
+            const int n = load_entry(p.k_list, e).n * p.group;
+            if (n == 0) continue;
+            ok = wait(B_RES, items & 1) && wait(B_AFULL + (J & 1), (J >> 1) & 1);
+            if (!ok) break;
+            if (elect_one()) {
                 issue_abt<HD>(c.tmem + kS, sK, sQ(J & 1));
                 mma_commit(bar(B_SFULL));
-                for (int i = 0; i < n; ++i, ++J) {
-                    const uint32_t st = J & 1, sn = st ^ 1u;
-                    ok = wait(B_BFULL + st, (J >> 1) & 1);
-                    if (!ok) break;
+            }
+            __syncwarp();
+            for (int i = 0; i < n; ++i, ++J) {
+                const uint32_t st = J & 1, sn = st ^ 1u;
+                ok = wait(B_BFULL + st, (J >> 1) & 1);
+                if (!ok) break;
+                if (elect_one()) {
                     issue_abt<HD>(c.tmem + kDp, sV, sDo(st));
                     mma_commit(bar(B_DPFULL));
                     if (i + 1 == n) mma_commit(bar(B_RESEMPTY));
-                    // (The item before's accumulators are stored before they are overwritten.)
-                    ok = wait(B_PFULL, J & 1) && (i > 0 || items == 0 || wait(B_ACCFREE, (items - 1) & 1));
-                    if (!ok) break;
+                }
+                __syncwarp();
+                // (The item before's accumulators are stored before they are overwritten.)
+                ok = wait(B_PFULL, J & 1) && (i > 0 || items == 0 || wait(B_ACCFREE, (items - 1) & 1));
+                if (!ok) break;
+                if (elect_one()) {
                     issue_ab<HD>(c.tmem + kDv, c.tmem + kS, sDo(st), i == 0);
                     mma_commit(bar(B_BEMPTY + st));
-                    if (i + 1 < n) {
-                        ok = wait(B_AFULL + sn, ((J + 1) >> 1) & 1);
-                        if (!ok) break;
+                }
+                __syncwarp();
+                if (i + 1 < n) {
+                    ok = wait(B_AFULL + sn, ((J + 1) >> 1) & 1);
+                    if (!ok) break;
+                    if (elect_one()) {
                         issue_abt<HD>(c.tmem + kS, sK, sQ(sn));
                         mma_commit(bar(B_SFULL));
                     }
-                    ok = wait(B_DSFULL, J & 1);
-                    if (!ok) break;
+                    __syncwarp();
+                }
+                ok = wait(B_DSFULL, J & 1);
+                if (!ok) break;
+                if (elect_one()) {
                     issue_ab<HD>(c.tmem + kDk, c.tmem + kDp, sQ(st), i == 0);
                     mma_commit(bar(B_AEMPTY + st));
+                    if (i + 1 == n) mma_commit(bar(B_DONE));
                 }
-                if (ok) mma_commit(bar(B_DONE));
-                ++items;
+                __syncwarp();
             }
+            ++items;
         }
     } else {
         const int wg = warp >> 2, quarter = warp & 3;

@@ -171,6 +171,20 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
 }
 
 
+// One lane of a converged warp.  In a branch on it, and not in one on a lane number, the compiler
+// knows that a single thread runs, and a tcgen05.mma takes about 20 cycles to issue instead of 55.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "elect.sync _|p, 0xffffffff;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
