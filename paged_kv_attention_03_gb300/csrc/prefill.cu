@@ -798,110 +798,115 @@ __global__ void __launch_bounds__(kThreads, 1)
                 produce(std::false_type{});
         } else if (warp == kWarpMma) {
             // ---------------- MMA issuer ----------------
-            // Order on the tensor pipe, across items: P0 V(g-1), S0(g), P1 V(g-1), S1(g).
-            if (lane == 0) {
-                constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, false, CODES);
-                // Half tile: the item's last K/V tile when no row sees its upper 64 keys
-                // (diagonal of a query block that ends in the tile's lower half): S over
-                // 64 keys, P V over 64 keys.  The softmax needs no change: the causal mask
-                // already sets columns 64..127 to -inf.
-                constexpr uint32_t idesc_s_half = idesc_bf16_f32(BM, BN / 2, false, CODES);
-                constexpr uint32_t idesc_o = idesc_bf16_f32(BM, HD, true, PV16);
-                uint32_t g = 0;                  // global KV tile counter
-                uint32_t cnt[2] = {0, 0};        // tiles issued per query tile (S / P V)
-                uint32_t ic = 0;                 // items
-                bool ok = true;
-                // Pending P V of the previous KV tile: its V stage, whether it is the first tile
-                // of its item (overwrite O), and whether query tile 1 takes part.
-                bool have_prev = false, prev_first = false, prev_has1 = false, prev_half = false;
-                uint32_t prev_g = 0;
-                auto issue_pv = [&](int i, uint32_t gv, bool first, bool half) -> bool {
-                    const uint32_t c = cnt[i]++;
-                    if (!wait1(bar(B_PFULL + i), c & 1, abort_flag, p.err, p.wait_ns)) return false;
-                    if (i == 0 && !wait1(bar(B_VFULL + gv % NSV), (gv / NSV) & 1, abort_flag, p.err, p.wait_ns))
-                        return false;
-                    tc_fence_after();
+            // Order on the tensor pipe, across items: P0 V(g-1), S0(g), P1 V(g-1), S1(g).  The whole
+            // warp waits, one elected lane issues (the same one always: a commit covers what its
+            // thread issued).
+            constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, false, CODES);
+            // Half tile: the item's last K/V tile when no row sees its upper 64 keys
+            // (diagonal of a query block that ends in the tile's lower half): S over
+            // 64 keys, P V over 64 keys.  The softmax needs no change: the causal mask
+            // already sets columns 64..127 to -inf.
+            constexpr uint32_t idesc_s_half = idesc_bf16_f32(BM, BN / 2, false, CODES);
+            constexpr uint32_t idesc_o = idesc_bf16_f32(BM, HD, true, PV16);
+            uint32_t g = 0;                  // global KV tile counter
+            uint32_t cnt[2] = {0, 0};        // tiles issued per query tile (S / P V)
+            uint32_t ic = 0;                 // items
+            bool ok = true;
+            // Pending P V of the previous KV tile: its V stage, whether it is the first tile
+            // of its item (overwrite O), and whether query tile 1 takes part.
+            bool have_prev = false, prev_first = false, prev_has1 = false, prev_half = false;
+            uint32_t prev_g = 0;
+            auto wait = [&](int b, uint32_t parity) -> bool {
+                return wait_warp(bar(b), parity, abort_flag, p.err, p.wait_ns);
+            };
+            auto commit = [&](int b) {
+                if (elect_one()) mma_commit(bar(b));
+                __syncwarp();
+            };
+            auto issue_pv = [&](int i, uint32_t gv, bool first, bool half) -> bool {
+                const uint32_t c = cnt[i]++;
+                if (!wait(B_PFULL + i, c & 1)) return false;
+                if (i == 0 && !wait(B_VFULL + gv % NSV, (gv / NSV) & 1)) return false;
+                tc_fence_after();
+                if (elect_one()) {
                     const uint64_t b0 = smem_desc_sw128(sV + (gv % NSV) * L::TILE, HALF, 1024);
-    #pragma unroll
+#pragma unroll
                     for (int k = 0; k < KSTEPS_O; ++k) {
                         if (half && k >= KSTEPS_O / 2) break;
                         mma_bf16_ts(tmem + col_o(i), tmem + col_s(i) + k * 8, desc_advance(b0, k * 2048),
                                     idesc_o, (!first || k > 0) ? 1u : 0u);
                     }
                     mma_commit(bar(B_ODONE + i));
-                    return true;
-                };
-                auto issue_s = [&](int i, uint32_t gk, bool half) {
+                }
+                __syncwarp();
+                return true;
+            };
+            auto issue_s = [&](int i, uint32_t gk, bool half) {
+                if (elect_one()) {
                     const uint64_t a0 = smem_desc_sw128(sQ + i * L::TILE, 16, 1024);
                     const uint64_t b0 = smem_desc_sw128(sK + (gk % NSK) * L::TILE, 16, 1024);
                     const uint32_t id = half ? idesc_s_half : idesc_s;
-    #pragma unroll
+#pragma unroll
                     for (int k = 0; k < KSTEPS_S; ++k) {
                         const uint32_t off = (k >> 2) * HALF + (k & 3) * 32;
                         mma_bf16_ss(tmem + col_s(i), desc_advance(a0, off), desc_advance(b0, off), id, k > 0);
                     }
                     mma_commit(bar(B_SFULL + i));
-                };
-                // Issue the P V products still pending from the previous KV tile.
-                auto flush = [&]() -> bool {
-                    if (!have_prev) return true;
-                    have_prev = false;
-                    if (!issue_pv(0, prev_g, prev_first, prev_half)) return false;
-                    if (prev_has1 && !issue_pv(1, prev_g, prev_first, prev_half)) return false;
-                    mma_commit(bar(B_VEMPTY + prev_g % NSV));
-                    return true;
-                };
-                for (;; ++ic) {
-                    if (!wait1(bar(B_IFULL + ic % kRing), (ic / kRing) & 1, abort_flag, p.err, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    const Item it = info[ic % kRing].it;
-                    const bool end = info[ic % kRing].end != 0;
-                    mbar_arrive(bar(B_IEMPTY + ic % kRing));
-                    if (end) break;
-                    // Finish the previous item before waiting for this item's Q, so its
-                    // epilogue never waits on a Q load.
-                    if (!flush() || !wait1(bar(CODES ? B_QCONV : B_QFULL), ic & 1, abort_flag, p.err, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    for (int j = 0; j < it.n_tiles; ++j, ++g) {
-                        const int st = g % NSK;
-                        // query tile 0: P0 V of the previous tile needs no K, so it goes to
-                        // the tensor core before the wait for K(g)
-                        const bool half = it.half_last && j == it.n_tiles - 1;
-                        if (have_prev && !issue_pv(0, prev_g, prev_first, prev_half)) {
-                            ok = false;
-                            break;
-                        }
-                        if (!wait1(bar(B_KFULL + st), (g / NSK) & 1, abort_flag, p.err, p.wait_ns)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        issue_s(0, g, half);
-                        // query tile 1
-                        if (have_prev && prev_has1 && !issue_pv(1, prev_g, prev_first, prev_half)) {
-                            ok = false;
-                            break;
-                        }
-                        if (have_prev) mma_commit(bar(B_VEMPTY + prev_g % NSV));
-                        if (it.has1) issue_s(1, g, half);
-                        mma_commit(bar(B_KEMPTY + st));
-                        if (j == it.n_tiles - 1) mma_commit(bar(B_QEMPTY));
-                        have_prev = true;
-                        prev_g = g;
-                        prev_first = j == 0;
-                        prev_has1 = it.has1;
-                        prev_half = half;
-                    }
-                    if (!ok) break;
-                    // (An item without tiles read no Q.)
-                    if (PACKED && it.n_tiles == 0) mma_commit(bar(B_QEMPTY));
                 }
-                if (ok) flush();
+                __syncwarp();
+            };
+            // Issue the P V products still pending from the previous KV tile.
+            auto flush = [&]() -> bool {
+                if (!have_prev) return true;
+                have_prev = false;
+                if (!issue_pv(0, prev_g, prev_first, prev_half)) return false;
+                if (prev_has1 && !issue_pv(1, prev_g, prev_first, prev_half)) return false;
+                commit(B_VEMPTY + prev_g % NSV);
+                return true;
+            };
+            Item it;
+            for (; take_item(ic, it); ++ic) {
+                // Finish the previous item before waiting for this item's Q, so its
+                // epilogue never waits on a Q load.
+                if (!flush() || !wait(CODES ? B_QCONV : B_QFULL, ic & 1)) {
+                    ok = false;
+                    break;
+                }
+                for (int j = 0; j < it.n_tiles; ++j, ++g) {
+                    const int st = g % NSK;
+                    // query tile 0: P0 V of the previous tile needs no K, so it goes to
+                    // the tensor core before the wait for K(g)
+                    const bool half = it.half_last && j == it.n_tiles - 1;
+                    if (have_prev && !issue_pv(0, prev_g, prev_first, prev_half)) {
+                        ok = false;
+                        break;
+                    }
+                    if (!wait(B_KFULL + st, (g / NSK) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    issue_s(0, g, half);
+                    // query tile 1
+                    if (have_prev && prev_has1 && !issue_pv(1, prev_g, prev_first, prev_half)) {
+                        ok = false;
+                        break;
+                    }
+                    if (have_prev) commit(B_VEMPTY + prev_g % NSV);
+                    if (it.has1) issue_s(1, g, half);
+                    commit(B_KEMPTY + st);
+                    if (j == it.n_tiles - 1) commit(B_QEMPTY);
+                    have_prev = true;
+                    prev_g = g;
+                    prev_first = j == 0;
+                    prev_has1 = it.has1;
+                    prev_half = half;
+                }
+                if (!ok) break;
+                // (An item without tiles read no Q.)
+                if (PACKED && it.n_tiles == 0) commit(B_QEMPTY);
             }
+            if (ok && !*abort_flag) flush();
         }
     } else {
         setmaxnreg_inc<kRegsSoftmax>();
