@@ -734,12 +734,11 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_PFULL));
                 const int d0 = pos - key0;  // distance to the first key
-                bool near = false;
-                const int d00 = __shfl_sync(0xffffffffu, d0, 0);  // the warp's first row's
-                if constexpr (BIAS) near = d00 - 63 < last && d00 + 31 >= 0;
+                const int d00 = __shfl_sync(0xffffffffu, d0, 0);  // the warp's first row's: its block has d00 - 63 .. d00 + 31
+                const bool near = BIAS && d00 - 63 < last;
                 if (near) {
-                    // The warp's rows and columns span 95 distances: three registers a lane, from which
-                    // element (row, i) fetches distance d00 + row - i.
+                    // The block spans 95 distances: three registers a lane, from which element (row, i)
+                    // fetches distance d00 + row - i (-inf before 0).
                     float r[3];
 #pragma unroll
                     for (int x = 0; x < 3; ++x) r[x] = __ldg(bias_row + d00 - 64 + 32 * x + lane);
@@ -759,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                         f2_unpack(f2_fma(f2_pack(a, b), sl2x2, far2), a, b);
                     }
                 }
-                if (d0 < 63) {
+                if (!BIAS && d0 < 63) {
 #pragma unroll
                     for (int i = 0; i < 64; ++i)
                         if (i > d0) w[i >> 5][i & 31] = -INFINITY;
@@ -773,10 +772,12 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
 #pragma unroll
                 for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = ex2_approx(w[i >> 5][i & 31]);
                 if (BIAS && !sum_only && tile < s.n_far) {
-                    float a[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint64_t a[2] = {0ull, 0ull};
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) a[i & 3] += w[i >> 5][i & 31];
-                    w_far += (a[0] + a[1]) + (a[2] + a[3]);
+                    for (int i = 0; i < 32; ++i) a[i & 1] = f2_add(a[i & 1], f2_pack(w[i >> 4][2 * (i & 15)], w[i >> 4][2 * (i & 15) + 1]));
+                    float a0, a1;
+                    f2_unpack(f2_add(a[0], a[1]), a0, a1);
+                    w_far += a0 + a1;
                 }
                 ok = wait_warp(bar(B_DPFULL + (J & 1)), (J >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
                 if (!ok) break;
@@ -1053,9 +1054,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) tmem_wait_ld_regs(w[cc]);
             const int d0 = pos0 - key;  // distance from the first query
-            bool near = false;
-            // (lane 31 has the nearest key)
-            if constexpr (BIAS) near = __shfl_sync(0xffffffffu, d0, 31) < last && __shfl_sync(0xffffffffu, d0, 0) + 63 >= 0;
+            // (Lane 31 has the nearest key.)
+            const bool near = BIAS && __shfl_sync(0xffffffffu, d0, 31) < last;
             if (near) {
                 const float *bt = bias_row_of(p.bias_table, head0 + g, last) + d0;
                 const float4 *nl = reinterpret_cast<const float4 *>(stat(st) + 64 * wg);
@@ -1079,7 +1079,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
                     f2_unpack(f2_fma(f2_pack(v[2], v[3]), sl2x2, l.y), v[2], v[3]);
                 }
             }
-            if (d0 < 0) {
+            if (!BIAS && d0 < 0) {  // (the table hides future keys)
 #pragma unroll
                 for (int x = 0; x < 64; ++x)
                     if (x < -d0) w[x >> 5][x & 31] = -INFINITY;

@@ -48,7 +48,8 @@ __global__ void __launch_bounds__(128)
     const int k = bucket_of(b, max(i - kBiasPad, 0));
     // (A block's heads in turn: the search is shared.)
     for (int h = blockIdx.y; h < num_heads; h += gridDim.y)
-        table[static_cast<int64_t>(h) * stride + i] = b.bias[static_cast<int64_t>(k) * num_heads + h] * kLog2e;
+        table[static_cast<int64_t>(h) * stride + i] =
+            i < kBiasPad ? -INFINITY : b.bias[static_cast<int64_t>(k) * num_heads + h] * kLog2e;
 }
 
 }  // namespace

@@ -1,18 +1,18 @@
 // relative_bias.cuh - the table of a learned relative position bias by distance.
 //
-// Row h holds head h's bias times log2(e) for the distances -kBiasPad .. last + kBiasPad - 1 (last:
-// the first distance of the last bucket).  Entries below 0 repeat distance 0 and those from last on
-// are all the last bucket's, so that a kernel may read whole runs around a tile's distances without
-// clamping each one: what lies below 0 is masked by the kernel, what lies beyond last is right.
+// Row h holds head h's bias times log2(e) for the distances -kBiasPad .. last + kBiasTail - 1 (last:
+// the first distance of the last bucket).  Entries below 0 are -inf, which hides future keys, and those
+// from last on are all the last bucket's, so that a kernel may read whole runs around a tile's
+// distances without clamping each one.
 #pragma once
 
 #include "pa_internal.h"
 
 namespace pa {
 
-constexpr int kBiasPad = 192;
+constexpr int kBiasPad = 256, kBiasTail = 128;
 
-__host__ __device__ inline int bias_stride(int last) { return (last + 2 * kBiasPad + 3) & ~3; }
+__host__ __device__ inline int bias_stride(int last) { return (last + kBiasPad + kBiasTail + 3) & ~3; }
 
 // Entry of distance 0 of a head's row.
 __device__ __forceinline__ const float *bias_row_of(const float *table, int head, int last) {
