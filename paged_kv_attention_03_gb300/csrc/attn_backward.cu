@@ -49,8 +49,8 @@ using namespace sm100;
 constexpr int BM = 128;                 // rows (TMEM lanes) of a tile
 constexpr int BN = 128;                 // columns of a tile
 constexpr uint32_t HALF = 128u * 128u;  // [128 rows][64 bf16]: one swizzle span
-constexpr int kWarpLoad = 8, kWarpMma = 9;
-constexpr int kThreads = 320;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpMma2 = 10;
+constexpr int kThreads = 352;
 constexpr uint32_t kTmemCols = 512;
 // Rows of fewer keys get their D from the sum over the keys also for dQ.  dout . out is off by about
 // 2^-9 |dout . out|, and |dout . out| shrinks against dP as the root of the number of keys that share
@@ -141,7 +141,7 @@ struct Layout {
     static constexpr uint32_t OFF_B = OFF_A + NA * TILE;  // dout (dK, dV) or V (dQ)
     static constexpr uint32_t OFF_SMALL = OFF_B + NB * TILE;
     static constexpr uint32_t OFF_BAR = OFF_SMALL + SMALL_BYTES;
-    static constexpr uint32_t OFF_MISC = OFF_BAR + 176;
+    static constexpr uint32_t OFF_MISC = OFF_BAR + 192;
     static constexpr uint32_t BYTES = OFF_MISC + 16;
     // At least 116 KB so a single CTA owns an SM (and all of its TMEM).
     static constexpr uint32_t SMEM = (BYTES > 118784u ? BYTES : 118784u);
@@ -157,7 +157,7 @@ enum : int {
     B_RES = 0,      // resident tiles loaded
     B_RESEMPTY = 20,  // resident tiles read
     B_ACCFREE = 21,   // accumulators stored (8 warps)
-    B_AFULL = 1,    // [3] tile of ring A ready (two arrivals: the copies, and the loading warp)
+    B_AFULL = 1,    // [3] tile of ring A ready (two arrivals: the copies, and the loading warp; dK, dV: of both rings)
     B_AEMPTY = 4,   // [3] read
     B_BFULL = 7,    // [2] ring B, likewise
     B_BEMPTY = 9,   // [2]
@@ -168,7 +168,8 @@ enum : int {
     B_DSFULL = 16,  // [2] dS in tensor memory (8 warps)
     B_DONE = 18,    // all products done
     B_SUMS = 19,    // both halves of the rows' D written (8 warps)
-    NBARS = 22
+    B_DQDONE = 22,    // [2] dQ's product of a step done
+    NBARS = 24
 };
 
 // A [128][HD] tile from row0 of a sequence that ends at row `end`: a box a lane.  A tile that the
@@ -286,7 +287,7 @@ struct Cta {
     uint32_t tmem;
     volatile int *abort_flag;
 };
-template <class L>
+template <class L, int A_ARRIVALS>
 __device__ __forceinline__ Cta setup() {
     extern __shared__ __align__(1024) uint8_t smem_raw[];  // (swizzled tiles start on 1024 bytes)
     Cta c;
@@ -299,7 +300,7 @@ __device__ __forceinline__ Cta setup() {
         mbar_init(bar(B_RESEMPTY), 1);
         mbar_init(bar(B_ACCFREE), 8);
         for (int s = 0; s < 3; ++s) {
-            mbar_init(bar(B_AFULL + s), 2);
+            mbar_init(bar(B_AFULL + s), A_ARRIVALS);
             mbar_init(bar(B_AEMPTY + s), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -307,6 +308,7 @@ __device__ __forceinline__ Cta setup() {
             mbar_init(bar(B_BEMPTY + s), 1);
             mbar_init(bar(B_DPFULL + s), 1);
             mbar_init(bar(B_DSFULL + s), 8);
+            mbar_init(bar(B_DQDONE + s), 1);
         }
         mbar_init(bar(B_LAND), 1);
         mbar_init(bar(B_SFULL), 1);
@@ -548,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
         int *first = reinterpret_cast<int *>(smem_raw + L::OFF_SMALL + 1024);
         for (int i = threadIdx.x; i <= p.bias.num_buckets; i += kThreads) first[i] = p.bias.first[i];
     }
-    const Cta c = setup<L>();
+    const Cta c = setup<L, 2>();
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sQ = c.base + L::OFF_RES, sDo = sQ + L::TILE;
@@ -577,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
 
     if (warp == kWarpLoad) {
         if (lane < 4) prefetch_tmap(lane == 0 ? p.tmap_q : lane == 1 ? p.tmap_do : lane == 2 ? p.tmap_k : p.tmap_v);
-        uint32_t lands = 0, items = 0, J = 0;
+        uint32_t lands = 0, items = 0, J = 0, sa = 0, pa = 1;  // ring A: stage, phase of its emptying
         bool ok = true;
         int e, h;
         for (int k = 0; ok && item_of(k, count, p.num_heads, e, h); ++k) {
@@ -606,63 +608,70 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                                       c.abort_flag, p.err, [] {});
             };
             for (int j = 0; ok && j < s.n_all; ++j, ++J) {
-                const uint32_t sa = J % NA, sb = J & 1;
-                ok = (J < NA || wait_warp(bar(B_AEMPTY + sa), (J / NA - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) &&
+                const uint32_t sb = J & 1;
+                ok = (J < NA || wait_warp(bar(B_AEMPTY + sa), pa, c.abort_flag, p.err, kTimeoutNs)) &&
                      load(p.tmap_k, sK(sa), j, bar(B_AFULL + sa)) &&
                      (J < 2 || wait_warp(bar(B_BEMPTY + sb), ((J >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) &&
                      load(p.tmap_v, sV(sb), j, bar(B_BFULL + sb));
+                if (++sa == NA) sa = 0, pa ^= 1u;
             }
         }
-    } else if (warp == kWarpMma) {
+    } else if (warp == kWarpMma || warp == kWarpMma2) {
+        // One warp issues S and dP, the other dQ, so that neither's waits hold up the other's products.
         // The whole warp waits, one lane issues (always the same: a commit covers what its thread issued).
         auto wait = [&](int b, uint32_t parity) {
             const bool ok = wait_warp(bar(b), parity, c.abort_flag, p.err, kTimeoutNs);
             tc_fence_after();
             return ok;
         };
-        uint32_t items = 0, J = 0;
-        auto products = [&](uint32_t j, bool end) -> bool {  // S(j) and dP(j)
-            if (!wait(B_AFULL + j % NA, (j / NA) & 1)) return false;
-            if (elect_one()) {
-                issue_abt<HD>(c.tmem, sQ, sK(j % NA));
-                mma_commit(bar(B_SFULL));
-            }
-            __syncwarp();
-            if (!wait(B_BFULL + (j & 1), (j >> 1) & 1)) return false;
-            if (elect_one()) {
-                issue_abt<HD>(c.tmem + kDp + 128u * (j & 1), sDo, sV(j & 1));
-                mma_commit(bar(B_DPFULL + (j & 1)));
-                mma_commit(bar(B_BEMPTY + (j & 1)));
-                if (end) mma_commit(bar(B_RESEMPTY));
-            }
-            __syncwarp();
-            return true;
-        };
+        uint32_t items = 0, J = 0, sa = 0, pa = 0;  // stage of ring A and its phase
         bool ok = true;
         int e, h;
         for (int k = 0; ok && item_of(k, count, p.num_heads, e, h); ++k) {
             const QTile t = load_entry(p.q_list, e);
             if (t.n == 0) continue;
             const Steps s = steps_of(t);
-            // (The item before has read S: its dS is waited for.)
-            ok = wait(B_RES, items & 1) && products(J, s.n_all == 1);
-            for (int j = 0; ok && j < s.n_all; ++j, ++J) {
-                // (dP(J + 1) goes where dS(J - 1) was: dQ(J - 1) is before it in the queue.)
-                if (j + 1 < s.n_all) ok = wait(B_PFULL, J & 1) && products(J + 1, j + 2 == s.n_all);
-                const bool first = j == (s.n_pre > 0 ? 0 : s.n);
-                ok = ok && wait(B_DSFULL + (J & 1), (J >> 1) & 1) && (!first || items == 0 || wait(B_ACCFREE, (items - 1) & 1));
-                if (!ok) break;
-                if (elect_one()) {
-                    if (j < s.n_pre || j >= s.n)
-                        issue_ab<HD>(c.tmem + kDq, c.tmem + kDp + 128u * (J & 1), sK(J % NA), first);
-                    mma_commit(bar(B_AEMPTY + J % NA));
-                    if (j + 1 == s.n_all) mma_commit(bar(B_DONE));
+            if (warp == kWarpMma) {
+                ok = wait(B_RES, items & 1);
+                for (int j = 0; ok && j < s.n_all; ++j, ++J) {
+                    const uint32_t sb = J & 1;
+                    ok = wait(B_AFULL + sa, pa) && (J == 0 || wait(B_PFULL, (J - 1) & 1));
+                    if (!ok) break;
+                    if (elect_one()) {
+                        issue_abt<HD>(c.tmem, sQ, sK(sa));
+                        mma_commit(bar(B_SFULL));
+                    }
+                    __syncwarp();
+                    // (dP goes where dS of the step before the last one was: its dQ has to be done.)
+                    ok = wait(B_BFULL + sb, (J >> 1) & 1) && (J < 2 || wait(B_DQDONE + sb, ((J >> 1) - 1) & 1));
+                    if (!ok) break;
+                    if (elect_one()) {
+                        issue_abt<HD>(c.tmem + kDp + 128u * sb, sDo, sV(sb));
+                        mma_commit(bar(B_DPFULL + sb));
+                        mma_commit(bar(B_BEMPTY + sb));
+                        if (j + 1 == s.n_all) mma_commit(bar(B_RESEMPTY));
+                    }
+                    __syncwarp();
+                    if (++sa == NA) sa = 0, pa ^= 1u;
                 }
-                __syncwarp();
+            } else {
+                for (int j = 0; j < s.n_all; ++j, ++J) {
+                    const bool first = j == (s.n_pre > 0 ? 0 : s.n);
+                    ok = wait(B_DSFULL + (J & 1), (J >> 1) & 1) && (!first || items == 0 || wait(B_ACCFREE, (items - 1) & 1));
+                    if (!ok) break;
+                    if (elect_one()) {
+                        if (j < s.n_pre || j >= s.n) issue_ab<HD>(c.tmem + kDq, c.tmem + kDp + 128u * (J & 1), sK(sa), first);
+                        mma_commit(bar(B_DQDONE + (J & 1)));
+                        mma_commit(bar(B_AEMPTY + sa));
+                        if (j + 1 == s.n_all) mma_commit(bar(B_DONE));
+                    }
+                    __syncwarp();
+                    if (++sa == NA) sa = 0;
+                }
             }
             ++items;
         }
-    } else {
+    } else if (warp < 8) {
         const int wg = warp >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
@@ -902,7 +911,7 @@ template <int HD, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_constant__ GradParams p) {
     using L = LayoutKv<HD>;
     constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 384;
-    const Cta c = setup<L>();
+    const Cta c = setup<L, 4>();  // (Q and dout of a step share a barrier: one wait less)
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sK = c.base + L::OFF_RES, sV = sK + L::TILE;
@@ -948,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
                 };
                 // (dout's stage is free first: dV comes before dK.)
                 ok = (J < 2 || wait_warp(bar(B_BEMPTY + st), ((J >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) &&
-                     load_stage<HD>(p.tmap_do, sDo(st), head, t.q_start, r, t.sq, bar(B_BFULL + st), bar(B_LAND), lands, c.abort_flag,
+                     load_stage<HD>(p.tmap_do, sDo(st), head, t.q_start, r, t.sq, bar(B_AFULL + st), bar(B_LAND), lands, c.abort_flag,
                                     p.err, [] {}) &&
                      (J < 2 || wait_warp(bar(B_AEMPTY + st), ((J >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) &&
                      load_stage<HD>(p.tmap_q, sQ(st), head, t.q_start, r, t.sq, bar(B_AFULL + st), bar(B_LAND), lands, c.abort_flag,
@@ -976,8 +985,6 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             __syncwarp();
             for (int i = 0; i < n; ++i, ++J) {
                 const uint32_t st = J & 1, sn = st ^ 1u;
-                ok = wait(B_BFULL + st, (J >> 1) & 1);
-                if (!ok) break;
                 if (elect_one()) {
                     issue_abt<HD>(c.tmem + kDp, sV, sDo(st));
                     mma_commit(bar(B_DPFULL));
@@ -1012,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             }
             ++items;
         }
-    } else {
+    } else if (warp < 8) {
         const int wg = warp >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
@@ -1150,24 +1157,29 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
 }
 
 // ---------------------------------------------------------------------- dbias ---
-// Sums the query tiles' partial sums, eight warps' for each, a block a head: always in the same order.
+// Sums the query tiles' partial sums, eight warps' for each, always in the same order: a block takes
+// eight buckets of a head (a sector of a row), 128 threads a bucket.
+constexpr int kBiasBuckets = 8;
 __global__ void __launch_bounds__(1024)
     grad_bias_kernel(float *__restrict__ dbias, const float *__restrict__ partial, const int *__restrict__ counts, int num_heads,
-                     int num_buckets, int log2_width) {  // 2^log2_width threads a row of buckets
-    __shared__ float s[1024];
-    const int h = blockIdx.x, b = threadIdx.x & ((1 << log2_width) - 1), part = threadIdx.x >> log2_width;
-    const int parts = 1024 >> log2_width, rows = *counts * 8;
+                     int num_buckets) {
+    __shared__ float s[32][kBiasBuckets];
+    const int h = blockIdx.x, b = blockIdx.y * kBiasBuckets + threadIdx.x % kBiasBuckets;
+    const int rows = *counts * 8;
     float t = 0.f;
     if (b < num_buckets) {
 #pragma unroll 4
-        for (int r = part; r < rows; r += parts)
+        for (int r = threadIdx.x / kBiasBuckets; r < rows; r += 1024 / kBiasBuckets)
             t += partial[((static_cast<int64_t>(r >> 3) * num_heads + h) * 8 + (r & 7)) * num_buckets + b];
     }
-    s[threadIdx.x] = t;
+    t += __shfl_xor_sync(0xffffffffu, t, 8);
+    t += __shfl_xor_sync(0xffffffffu, t, 16);
+    if ((threadIdx.x & 31) < kBiasBuckets) s[threadIdx.x >> 5][threadIdx.x & 31] = t;
     __syncthreads();
-    if (part == 0 && b < num_buckets) {
+    if (threadIdx.x < kBiasBuckets && b < num_buckets) {
         t = 0.f;
-        for (int i = 0; i < parts; ++i) t += s[(i << log2_width) + b];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) t += s[i][threadIdx.x];
         dbias[b * num_heads + h] = t;
     }
 }
@@ -1226,9 +1238,8 @@ cudaError_t launch_backward_d(GradParams &p, const PlanParams &plan, const Packe
     if (e == cudaSuccess) e = launch_tiles(grad_q_kernel<HD, BIAS>, LayoutQ<HD>::SMEM, set[0], q_items, p, stream);
     if (e == cudaSuccess) e = launch_tiles(grad_kv_kernel<HD, BIAS>, LayoutKv<HD>::SMEM, set[1], k_items, p, stream);
     if (BIAS && e == cudaSuccess) {
-        int width = 0;
-        while ((1 << width) < a.bias.num_buckets) ++width;
-        grad_bias_kernel<<<a.num_heads, 1024, 0, stream>>>(g.dbias, p.partial, p.counts, a.num_heads, a.bias.num_buckets, width);
+        const dim3 blocks(a.num_heads, (a.bias.num_buckets + kBiasBuckets - 1) / kBiasBuckets);
+        grad_bias_kernel<<<blocks, 1024, 0, stream>>>(g.dbias, p.partial, p.counts, a.num_heads, a.bias.num_buckets);
         e = cudaGetLastError();
     }
     return e;
