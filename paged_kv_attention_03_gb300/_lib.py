@@ -619,8 +619,10 @@ def _rows(t: torch.Tensor, name: str, dev: int, shape: tuple) -> tuple[int, int]
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     rows, heads, d = shape
     row = heads * d
+    if t.is_contiguous():
+        return t.data_ptr(), row
     step, head, last = t.stride()
-    if rows < 2 or t.is_contiguous():
+    if rows < 2:
         step = row
     if last != 1 or (heads > 1 and head != d) or step < row or step % 8:
         raise ValueError(f"{name}: the heads of a row must be contiguous, and rows a multiple of 8 elements apart")
@@ -651,10 +653,18 @@ def pa_varlen_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens
     total_q, heads, d = q.shape
     total_k, hkv, _ = k.shape
     n = cu_seqlens_q.shape[0] - 1
+    where = q.device
+    # (New tensors are right as they are.)
     if out is None:
-        out = torch.empty((total_q, heads, d), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty((total_q, heads, d), dtype=torch.bfloat16, device=where)
+        outp = out.data_ptr()
+    else:
+        outp = _arg(out, torch.bfloat16, "out", dev, (total_q, heads, d))
     if lse is None:
-        lse = torch.empty((total_q, heads), dtype=torch.float32, device=q.device)
+        lse = torch.empty((total_q, heads), dtype=torch.float32, device=where)
+        lsep = lse.data_ptr()
+    else:
+        lsep = _arg(lse, torch.float32, "lse", dev, (total_q, heads))
     qp, qs = _rows(q, "q", dev, (total_q, heads, d))
     kp, ks = _rows(k, "k", dev, (total_k, hkv, d))
     vp, vs = _rows(v, "v", dev, (total_k, hkv, d))
@@ -662,9 +672,7 @@ def pa_varlen_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens
     ws, ws_bytes, workspace = _workspace(
         workspace, 0 if workspace is not None or bias is None else
         pa_relative_bias_workspace_size(heads, b[1], b[2]), dev)
-    _run("pa_varlen_attn", lib.pa_varlen_attn, dev,
-         _arg(out, torch.bfloat16, "out", dev, (total_q, heads, d)),
-         _arg(lse, torch.float32, "lse", dev, (total_q, heads)), qp, kp, vp, qs, ks, vs,
+    _run("pa_varlen_attn", lib.pa_varlen_attn, dev, outp, lsep, qp, kp, vp, qs, ks, vs,
          _arg(cu_seqlens_q, torch.int32, "cu_seqlens_q", dev, (n + 1,)),
          _arg(cu_seqlens_k, torch.int32, "cu_seqlens_k", dev, (n + 1,)), n, total_q, total_k,
          int(max_seqlen_q), int(max_seqlen_k), heads, hkv, d, int(sliding_window), float(scale), *b,
@@ -690,26 +698,36 @@ def pa_varlen_attn_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor
     total_q, heads, d = q.shape
     total_k, hkv, _ = k.shape
     n = cu_seqlens_q.shape[0] - 1
-    new = lambda *shape: torch.empty(shape, dtype=torch.bfloat16, device=q.device)  # noqa: E731
-    dq = new(total_q, heads, d) if dq is None else dq
-    dk = new(total_k, hkv, d) if dk is None else dk
-    dv = new(total_k, hkv, d) if dv is None else dv
-    if bias is not None and dbias is None:
-        dbias = torch.empty(bias.shape, dtype=torch.float32, device=q.device)
-    grads = [_rows(dq, "dq", dev, (total_q, heads, d)), _rows(dk, "dk", dev, (total_k, hkv, d)),
-             _rows(dv, "dv", dev, (total_k, hkv, d))]
-    ins = [_rows(q, "q", dev, (total_q, heads, d)), _rows(k, "k", dev, (total_k, hkv, d)),
-           _rows(v, "v", dev, (total_k, hkv, d))]
+    where = q.device
+    q_shape, k_shape = (total_q, heads, d), (total_k, hkv, d)
+
+    def grad(g, name, shape):  # (new tensors are right as they are)
+        if g is not None:
+            return g, *_rows(g, name, dev, shape)
+        g = torch.empty(shape, dtype=torch.bfloat16, device=where)
+        return g, g.data_ptr(), shape[1] * d
+
+    dq, dqp, dqs = grad(dq, "dq", q_shape)
+    dk, dkp, dks = grad(dk, "dk", k_shape)
+    dv, dvp, dvs = grad(dv, "dv", k_shape)
+    qp, qs = _rows(q, "q", dev, q_shape)
+    kp, ks = _rows(k, "k", dev, k_shape)
+    vp, vs = _rows(v, "v", dev, k_shape)
     b = _bias(bias, max_distance, heads, dev)
-    db = None if dbias is None else _arg(dbias, torch.float32, "dbias", dev, (b[1], heads))
+    if dbias is not None:
+        dbp = _arg(dbias, torch.float32, "dbias", dev, (b[1], heads))
+    elif bias is not None:
+        dbias = torch.empty((b[1], heads), dtype=torch.float32, device=where)
+        dbp = dbias.data_ptr()
+    else:
+        dbp = None
     ws, ws_bytes, workspace = _workspace(
         workspace, 0 if workspace is not None else
         pa_varlen_attn_backward_workspace_size(total_q, total_k, n, heads, b[1], b[2]), dev)
-    _run("pa_varlen_attn_backward", lib.pa_varlen_attn_backward, dev,
-         *(g[0] for g in grads), db, *(g[1] for g in grads),
-         _arg(dout, torch.bfloat16, "dout", dev, (total_q, heads, d)), *(x[0] for x in ins),
-         _arg(out, torch.bfloat16, "out", dev, (total_q, heads, d)),
-         _arg(lse, torch.float32, "lse", dev, (total_q, heads)), *(x[1] for x in ins),
+    _run("pa_varlen_attn_backward", lib.pa_varlen_attn_backward, dev, dqp, dkp, dvp, dbp, dqs, dks, dvs,
+         _arg(dout, torch.bfloat16, "dout", dev, q_shape), qp, kp, vp,
+         _arg(out, torch.bfloat16, "out", dev, q_shape),
+         _arg(lse, torch.float32, "lse", dev, (total_q, heads)), qs, ks, vs,
          _arg(cu_seqlens_q, torch.int32, "cu_seqlens_q", dev, (n + 1,)),
          _arg(cu_seqlens_k, torch.int32, "cu_seqlens_k", dev, (n + 1,)), n, total_q, total_k,
          int(max_seqlen_q), int(max_seqlen_k), heads, hkv, d, int(sliding_window), float(scale), *b,
