@@ -130,12 +130,13 @@ __device__ __forceinline__ Tile load_entry(const Tile *list, int i) {
 
 // Shared memory: two resident tiles (Q and dout, or K and V), rings of the tiles that pass by (K
 // and V, or Q and dout), small arrays, barriers.  K outlives V by the time from dP to dQ, so it has
-// three stages there.
-template <int HD, int STAGES_A, uint32_t SMALL_BYTES>
+// three stages there.  With a bias the element-wise work is what bounds dQ, V's second stage gives
+// nothing (train varlen 414 us with and without it), and its place holds the bias of two items' heads.
+template <int HD, int STAGES_A, int STAGES_B, uint32_t SMALL_BYTES>
 struct Layout {
     static constexpr int NHALF = HD / 64;
     static constexpr uint32_t TILE = NHALF * HALF;
-    static constexpr int NA = STAGES_A, NB = 2;
+    static constexpr int NA = STAGES_A, NB = STAGES_B;
     static constexpr uint32_t OFF_RES = 0;
     static constexpr uint32_t OFF_A = 2 * TILE;          // Q (dK, dV) or K (dQ)
     static constexpr uint32_t OFF_B = OFF_A + NA * TILE;  // dout (dK, dV) or V (dQ)
@@ -148,10 +149,12 @@ struct Layout {
     static_assert(SMEM <= 232448u, "at most 227 KB of shared memory per CTA");
 };
 
+constexpr uint32_t kTableBytes = 16384;  // a head's bias in shared memory; longer ones are read from global memory
+constexpr uint32_t kSmallQ = 1024 + 528;
+template <int HD, bool BIAS>
+using LayoutQ = Layout<HD, 3, BIAS ? 1 : 2, kSmallQ + (BIAS ? 2 * kTableBytes : 0u)>;
 template <int HD>
-using LayoutQ = Layout<HD, 3, 1024 + 528>;
-template <int HD>
-using LayoutKv = Layout<HD, 2, 2u * 3 * 512>;
+using LayoutKv = Layout<HD, 2, 2, 2u * 3 * 512>;
 
 enum : int {
     B_RES = 0,      // resident tiles loaded
@@ -542,8 +545,8 @@ __global__ void __launch_bounds__(256)
 //     S(j + 1), dP(j + 1), then dQ(j).
 template <int HD, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_constant__ GradParams p) {
-    using L = LayoutQ<HD>;
-    constexpr int NA = L::NA;
+    using L = LayoutQ<HD, BIAS>;
+    constexpr int NA = L::NA, NB = L::NB;
     constexpr uint32_t kDp = 128, kDq = 384;
     if constexpr (BIAS) {  // the buckets' first distances, behind the rows' sums
         extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -557,6 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
     auto sK = [&](uint32_t st) -> uint32_t { return c.base + L::OFF_A + st * L::TILE; };
     auto sV = [&](uint32_t st) -> uint32_t { return c.base + L::OFF_B + st * L::TILE; };
     const int last = p.bias.last();
+    const uint32_t table_bytes = BIAS ? bias_stride(last) * 4u : 0u;
+    const bool table_here = BIAS && table_bytes <= kTableBytes;
     const int count = *p.counts;
     // An item's steps: the tiles 0 .. n_pre - 1 with D from dout . out; tiles n_pre .. n - 1 for D alone;
     // then the same with D.
@@ -590,7 +595,14 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             // (Sums along diagonals run across rows; in all else a row behind the sequence stays on its own.)
             const bool edit = BIAS && ragged(t.left);
             const uint32_t land = bar(edit ? B_LAND : B_RES);
-            if (lane == 0) mbar_arrive_expect_tx(land, 2 * L::TILE);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(land, 2 * L::TILE + (table_here ? table_bytes : 0u));
+                // (The item before the last one, whose table this overwrites, is done: the last one's first
+                // logits were read after it.)
+                if (table_here)
+                    bulk_load(c.base + L::OFF_SMALL + kSmallQ + (items & 1) * kTableBytes, bias_row_of(p.bias_table, h, last) - kBiasPad,
+                              table_bytes, land);
+            }
             __syncwarp();
             load_tile<HD>(p.tmap_q, sQ, h, t.row, 0, t.left, land);
             load_tile<HD>(p.tmap_do, sDo, h, t.row, 0, t.left, land);
@@ -608,10 +620,10 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                                       c.abort_flag, p.err, [] {});
             };
             for (int j = 0; ok && j < s.n_all; ++j, ++J) {
-                const uint32_t sb = J & 1;
+                const uint32_t sb = J % NB;
                 ok = (J < NA || wait_warp(bar(B_AEMPTY + sa), pa, c.abort_flag, p.err, kTimeoutNs)) &&
                      load(p.tmap_k, sK(sa), j, bar(B_AFULL + sa)) &&
-                     (J < 2 || wait_warp(bar(B_BEMPTY + sb), ((J >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) &&
+                     (J < NB || wait_warp(bar(B_BEMPTY + sb), (J / NB - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) &&
                      load(p.tmap_v, sV(sb), j, bar(B_BFULL + sb));
                 if (++sa == NA) sa = 0, pa ^= 1u;
             }
@@ -634,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             if (warp == kWarpMma) {
                 ok = wait(B_RES, items & 1);
                 for (int j = 0; ok && j < s.n_all; ++j, ++J) {
-                    const uint32_t sb = J & 1;
+                    const uint32_t sb = J % NB, sd = J & 1;  // stage of V, place of dP
                     ok = wait(B_AFULL + sa, pa) && (J == 0 || wait(B_PFULL, (J - 1) & 1));
                     if (!ok) break;
                     if (elect_one()) {
@@ -643,11 +655,11 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                     }
                     __syncwarp();
                     // (dP goes where dS of the step before the last one was: its dQ has to be done.)
-                    ok = wait(B_BFULL + sb, (J >> 1) & 1) && (J < 2 || wait(B_DQDONE + sb, ((J >> 1) - 1) & 1));
+                    ok = wait(B_BFULL + sb, (J / NB) & 1) && (J < 2 || wait(B_DQDONE + sd, ((J >> 1) - 1) & 1));
                     if (!ok) break;
                     if (elect_one()) {
-                        issue_abt<HD>(c.tmem + kDp + 128u * sb, sDo, sV(sb));
-                        mma_commit(bar(B_DPFULL + sb));
+                        issue_abt<HD>(c.tmem + kDp + 128u * sd, sDo, sV(sb));
+                        mma_commit(bar(B_DPFULL + sd));
                         mma_commit(bar(B_BEMPTY + sb));
                         if (j + 1 == s.n_all) mma_commit(bar(B_RESEMPTY));
                     }
@@ -719,11 +731,16 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             const int pos = t.pos + row;
             float d_sum = 0.f;
             [[maybe_unused]] float d_far = 0.f, w_far = 0.f;  // sums of P dP and of P over the first n_far tiles
-            [[maybe_unused]] const float *bias_row = nullptr;
+            [[maybe_unused]] const float *bias_row = nullptr;  // entry of distance 0
             float far = -lse2;  // x = sl2 s + far, where the bias is that of the last bucket
             if constexpr (BIAS) {
                 bias_row = bias_row_of(p.bias_table, head, last);
-                far = __ldg(bias_row + last) - lse2;
+                if (table_here) {
+                    ok = wait_warp(bar(B_RES), items & 1, c.abort_flag, p.err, kTimeoutNs);
+                    if (!ok) break;
+                    bias_row = small + kSmallQ / 4 + (items & 1) * (kTableBytes / 4) + kBiasPad;
+                }
+                far = bias_row[last] - lse2;
             }
             const uint64_t far2 = f2_pack(far, far);
             for (int j = 0; j < s.n_all; ++j, ++J) {
@@ -746,20 +763,9 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 const int d00 = __shfl_sync(0xffffffffu, d0, 0);  // the warp's first row's: its block has d00 - 63 .. d00 + 31
                 const bool near = BIAS && d00 - 63 < last;
                 if (near) {
-                    // The block spans 95 distances: three registers a lane, from which element (row, i)
-                    // fetches distance d00 + row - i (-inf before 0).
-                    float r[3];
+                    const float *bt = bias_row + d0;  // (-inf before distance 0)
 #pragma unroll
-                    for (int x = 0; x < 3; ++x) r[x] = __ldg(bias_row + d00 - 64 + 32 * x + lane);
-#pragma unroll
-                    for (int b = 0; b < 32; ++b) {
-                        const bool low = lane + b >= 32;
-#pragma unroll
-                        for (int a = 0; a < 2; ++a) {
-                            const float v = __shfl_sync(0xffffffffu, low ? r[1 - a] : r[2 - a], lane - b);
-                            w[a][b] = fmaf(w[a][b], sl2, v) - lse2;
-                        }
-                    }
+                    for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = fmaf(w[i >> 5][i & 31], sl2, bt[-i]) - lse2;
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
@@ -1235,7 +1241,7 @@ cudaError_t launch_backward_d(GradParams &p, const PlanParams &plan, const Packe
     static std::atomic<uint64_t> set[2];
     const int64_t q_items = a.total_q > 0 ? most_tiles(a.total_q, a.num_seqs) * a.num_heads : 0;
     const int64_t k_items = a.total_k > 0 ? most_tiles(a.total_k, a.num_seqs) * a.num_kv_heads : 0;
-    if (e == cudaSuccess) e = launch_tiles(grad_q_kernel<HD, BIAS>, LayoutQ<HD>::SMEM, set[0], q_items, p, stream);
+    if (e == cudaSuccess) e = launch_tiles(grad_q_kernel<HD, BIAS>, LayoutQ<HD, BIAS>::SMEM, set[0], q_items, p, stream);
     if (e == cudaSuccess) e = launch_tiles(grad_kv_kernel<HD, BIAS>, LayoutKv<HD>::SMEM, set[1], k_items, p, stream);
     if (BIAS && e == cudaSuccess) {
         const dim3 blocks(a.num_heads, (a.bias.num_buckets + kBiasBuckets - 1) / kBiasBuckets);
