@@ -142,7 +142,7 @@ struct Layout {
     static constexpr uint32_t OFF_B = OFF_A + NA * TILE;  // dout (dK, dV) or V (dQ)
     static constexpr uint32_t OFF_SMALL = OFF_B + NB * TILE;
     static constexpr uint32_t OFF_BAR = OFF_SMALL + SMALL_BYTES;
-    static constexpr uint32_t OFF_MISC = OFF_BAR + 192;
+    static constexpr uint32_t OFF_MISC = OFF_BAR + 224;
     static constexpr uint32_t BYTES = OFF_MISC + 16;
     // At least 116 KB so a single CTA owns an SM (and all of its TMEM).
     static constexpr uint32_t SMEM = (BYTES > 118784u ? BYTES : 118784u);
@@ -172,7 +172,9 @@ enum : int {
     B_DONE = 18,    // all products done
     B_SUMS = 19,    // both halves of the rows' D written (8 warps)
     B_DQDONE = 22,    // [2] dQ's product of a step done
-    NBARS = 24
+    B_TABFULL = 24,   // [2] an item's bias in shared memory
+    B_TABFREE = 26,   // [2] read (8 warps)
+    NBARS = 28
 };
 
 // A [128][HD] tile from row0 of a sequence that ends at row `end`: a box a lane.  A tile that the
@@ -312,6 +314,8 @@ __device__ __forceinline__ Cta setup() {
             mbar_init(bar(B_DPFULL + s), 1);
             mbar_init(bar(B_DSFULL + s), 8);
             mbar_init(bar(B_DQDONE + s), 1);
+            mbar_init(bar(B_TABFULL + s), 1);
+            mbar_init(bar(B_TABFREE + s), 8);
         }
         mbar_init(bar(B_LAND), 1);
         mbar_init(bar(B_SFULL), 1);
@@ -563,11 +567,13 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
     const uint32_t table_bytes = BIAS ? bias_stride(last) * 4u : 0u;
     const bool table_here = BIAS && table_bytes <= kTableBytes;
     const int count = *p.counts;
-    // An item's steps: the tiles 0 .. n_pre - 1 with D from dout . out; tiles n_pre .. n - 1 for D alone;
-    // then the same with D.
+    // An item's steps: the tiles 0 .. n_pre - 1 with D from dout . out; tiles n_pre .. n - 2 for D alone;
+    // the last tile, where D is complete before its dS is formed; then tiles n_pre .. n - 2 with D.
     struct Steps {
         int n, n_far, n_pre, n_all, kt0;
         __device__ int tile(int j) const { return j < n ? j : j - (n - n_pre); }
+        __device__ bool sum_only(int j) const { return j >= n_pre && j + 1 < n; }
+        __device__ bool first_dq(int j) const { return j == (n_pre > 0 ? 0 : n - 1); }
     };
     auto steps_of = [&](const QTile &t) -> Steps {
         Steps s;
@@ -578,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
         s.n_far = BIAS ? min(max(kmin, t.pos - last + 1) / BN - s.kt0, t.n) : t.n;
         const bool few = t.pos + 1 < kFewKeys || (p.window > 0 && p.window < kFewKeys);
         s.n_pre = few ? 0 : s.n_far;
-        s.n_all = 2 * s.n - s.n_pre;
+        s.n_all = s.n + max(s.n - 1 - s.n_pre, 0);
         return s;
     };
 
@@ -595,14 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             // (Sums along diagonals run across rows; in all else a row behind the sequence stays on its own.)
             const bool edit = BIAS && ragged(t.left);
             const uint32_t land = bar(edit ? B_LAND : B_RES);
-            if (lane == 0) {
-                mbar_arrive_expect_tx(land, 2 * L::TILE + (table_here ? table_bytes : 0u));
-                // (The item before the last one, whose table this overwrites, is done: the last one's first
-                // logits were read after it.)
-                if (table_here)
-                    bulk_load(c.base + L::OFF_SMALL + kSmallQ + (items & 1) * kTableBytes, bias_row_of(p.bias_table, h, last) - kBiasPad,
-                              table_bytes, land);
-            }
+            if (lane == 0) mbar_arrive_expect_tx(land, 2 * L::TILE);
             __syncwarp();
             load_tile<HD>(p.tmap_q, sQ, h, t.row, 0, t.left, land);
             load_tile<HD>(p.tmap_do, sDo, h, t.row, 0, t.left, land);
@@ -612,6 +611,16 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 clear_rows<HD>(sDo, t.left);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_RES));
+            }
+            if (table_here) {
+                const uint32_t slot = items & 1;
+                if (items >= 2 && !wait_warp(bar(B_TABFREE + slot), ((items >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(B_TABFULL + slot), table_bytes);
+                    bulk_load(c.base + L::OFF_SMALL + kSmallQ + slot * kTableBytes, bias_row_of(p.bias_table, h, last) - kBiasPad,
+                              table_bytes, bar(B_TABFULL + slot));
+                }
+                __syncwarp();
             }
             ++items;
             const int kvh = h / p.group;
@@ -668,11 +677,11 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 }
             } else {
                 for (int j = 0; j < s.n_all; ++j, ++J) {
-                    const bool first = j == (s.n_pre > 0 ? 0 : s.n);
+                    const bool first = s.first_dq(j);
                     ok = wait(B_DSFULL + (J & 1), (J >> 1) & 1) && (!first || items == 0 || wait(B_ACCFREE, (items - 1) & 1));
                     if (!ok) break;
                     if (elect_one()) {
-                        if (j < s.n_pre || j >= s.n) issue_ab<HD>(c.tmem + kDq, c.tmem + kDp + 128u * (J & 1), sK(sa), first);
+                        if (!s.sum_only(j)) issue_ab<HD>(c.tmem + kDq, c.tmem + kDp + 128u * (J & 1), sK(sa), first);
                         mma_commit(bar(B_DQDONE + (J & 1)));
                         mma_commit(bar(B_AEMPTY + sa));
                         if (j + 1 == s.n_all) mma_commit(bar(B_DONE));
@@ -736,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             if constexpr (BIAS) {
                 bias_row = bias_row_of(p.bias_table, head, last);
                 if (table_here) {
-                    ok = wait_warp(bar(B_RES), items & 1, c.abort_flag, p.err, kTimeoutNs);
+                    ok = wait_warp(bar(B_TABFULL + (items & 1)), (items >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
                     if (!ok) break;
                     bias_row = small + kSmallQ / 4 + (items & 1) * (kTableBytes / 4) + kBiasPad;
                 }
@@ -745,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             const uint64_t far2 = f2_pack(far, far);
             for (int j = 0; j < s.n_all; ++j, ++J) {
                 const uint32_t dp = c.tmem + t_lane + kDp + 128u * (J & 1) + 64u * wg;
-                const bool sum_only = j >= s.n_pre && j < s.n;
+                const bool sum_only = s.sum_only(j);
                 const int tile = s.tile(j);
                 const int key0 = (s.kt0 + tile) * BN + 64 * wg;  // this warpgroup's first key
                 ok = wait_warp(bar(B_SFULL), J & 1, c.abort_flag, p.err, kTimeoutNs);
@@ -797,6 +806,32 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 ok = wait_warp(bar(B_DPFULL + (J & 1)), (J >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
                 if (!ok) break;
                 tc_fence_after();
+                // D of the row: this warpgroup's half and the other's.
+                auto exchange = [&]() -> bool {
+                    small[128 * wg + row] = d_sum;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_SUMS));
+                    if (!wait_warp(bar(B_SUMS), items & 1, c.abort_flag, p.err, kTimeoutNs)) return false;
+                    delta = small[row] + small[128 + row];
+                    if (wg == 0 && row < rows) p.delta[stat_row + row] = delta;
+                    return true;
+                };
+                const bool pivot = j + 1 == s.n && s.n_pre < s.n;
+                if (pivot) {
+                    float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int cc = 0; cc < 2; ++cc) {
+                        float d[32];
+                        tmem_ld_32x32b_x32(dp + 32u * cc, d);
+                        tmem_wait_ld_regs(d);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) a[i & 3] = fmaf(w[cc][i], d[i], a[i & 3]);
+                    }
+                    d_sum += (a[0] + a[1]) + (a[2] + a[3]);
+                    ok = exchange();
+                    if (!ok) break;
+                    d_sum = s.n_pre == 0 ? 0.f : d_sum;  // (the last bucket's tiles may still be to come)
+                }
                 uint32_t pk[32];
                 uint64_t acc[2] = {0ull, 0ull};
                 const uint64_t delta2 = f2_pack(-delta, -delta);
@@ -815,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 }
                 float a0, a1;
                 f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
-                d_sum += a0 + a1;
+                if (!pivot) d_sum += a0 + a1;
                 if (!sum_only) {
                     if (BIAS && tile + 1 == s.n_far) d_far = d_sum;
                     tmem_st_32x32b_x32_u(dp, pk);
@@ -824,18 +859,11 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_DSFULL + (J & 1)));
-                if (j + 1 == s.n) {
-                    // D of the row: this warpgroup's half and the other's.
-                    small[128 * wg + row] = d_sum;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_SUMS));
-                    ok = wait_warp(bar(B_SUMS), items & 1, c.abort_flag, p.err, kTimeoutNs);
+                if (j + 1 == s.n && s.n_pre == s.n) {
+                    ok = exchange();
                     if (!ok) break;
-                    delta = small[row] + small[128 + row];
-                    if (s.n_pre == 0) d_sum = 0.f;  // (the last bucket's tiles are added up in the second round)
-                    if (wg == 0 && row < rows) p.delta[stat_row + row] = delta;
                 }
-                if (BIAS && j >= s.n && tile >= s.n_far) {
+                if (BIAS && j + 1 >= s.n && tile >= s.n_far) {
                     // Sums along the diagonals row - column = lane, lane - 32, lane - 64 of the warp's 32 x
                     // 64 block: at column i the lane fetches the element of row (lane + i) % 32.
                     float a[3] = {0.f, 0.f, 0.f};
@@ -884,6 +912,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             }
             if (!ok) break;
             if constexpr (BIAS) {
+                __syncwarp();
+                if (table_here && lane == 0) mbar_arrive(bar(B_TABFREE + (items & 1)));
                 const float t_far = warp_sum(d_far - delta * w_far);
 #pragma unroll
                 for (int k4 = 0; k4 < 4; ++k4) {

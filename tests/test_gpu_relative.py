@@ -120,6 +120,20 @@ def test_packed_and_gradient(lengths, heads, hkv, dim, window, buckets, distance
     check(c, out, lse, grads)
 
 
+@pytest.mark.parametrize("heads,hkv,dim", [(12, 12, 64), (16, 4, 128)])
+@pytest.mark.parametrize("window,buckets,distance", [(0, 32, 128), (0, 0, 0), (0, 16, 30000), (40, 8, 20), (200, 32, 128)])
+def test_many_tiles_a_block(heads, hkv, dim, window, buckets, distance):
+    """Several items for each of the GPU's persistent blocks, of one tile and of several, empty ones among them."""
+    g = np.random.default_rng(4)
+    sq = g.integers(0, 200, 90).tolist() + [400, 129]
+    sk = [n + int(m) for n, m in zip(sq, g.integers(-30, 90, 92))]
+    c = Case(sq, [max(n, 0) for n in sk], heads, hkv, dim, window, buckets, distance, seed=6)
+    out, lse, grads = both(c)
+    check(c, out, lse, grads)
+    for a, b in zip((out, lse, *grads), (lambda r: (r[0], r[1], *r[2]))(both(c))):
+        assert (a is None and b is None) or torch.equal(a, b)
+
+
 @pytest.mark.parametrize("heads,hkv", [(64, 1), (32, 2), (33, 1), (3, 3), (128, 2)])
 def test_head_layouts(heads, hkv):
     c = Case([70, 9], [70, 30], heads, hkv, 128, 0, 32, 128)
