@@ -149,12 +149,14 @@ struct Layout {
     static_assert(SMEM <= 232448u, "at most 227 KB of shared memory per CTA");
 };
 
-constexpr uint32_t kTableBytes = 16384;  // a head's bias in shared memory; longer ones are read from global memory
+// An item's bias (dK, dV: of its kv head's heads) in shared memory; a longer one is read from global memory.
+constexpr uint32_t kTableBytes = 15360;
 constexpr uint32_t kSmallQ = 1024 + 528;
 template <int HD, bool BIAS>
 using LayoutQ = Layout<HD, 3, BIAS ? 1 : 2, kSmallQ + (BIAS ? 2 * kTableBytes : 0u)>;
-template <int HD>
-using LayoutKv = Layout<HD, 2, 2, 2u * 3 * 512>;
+constexpr uint32_t kSmallKv = 2u * 3 * 512;
+template <int HD, bool BIAS>
+using LayoutKv = Layout<HD, 2, 2, kSmallKv + (BIAS ? 2 * kTableBytes : 0u)>;
 
 enum : int {
     B_RES = 0,      // resident tiles loaded
@@ -945,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
 //     dP(i), dV(i), S(i + 1), dK(i).
 template <int HD, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_constant__ GradParams p) {
-    using L = LayoutKv<HD>;
+    using L = LayoutKv<HD, BIAS>;
     constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 384;
     const Cta c = setup<L, 4>();  // (Q and dout of a step share a barrier: one wait less)
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
@@ -957,6 +959,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
     auto stat = [&](int st) -> float * { return reinterpret_cast<float *>(c.sb + L::OFF_SMALL) + st * 384; };
     const int last = p.bias.last();
 
+    const uint32_t table_bytes = BIAS ? bias_stride(last) * 4u * p.group : 0u;
+    const bool table_here = BIAS && table_bytes <= kTableBytes;
     const int count = p.counts[1];
 
     if (warp == kWarpLoad) {
@@ -972,6 +976,16 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             __syncwarp();
             load_tile<HD>(p.tmap_k, sK, kvh, t.row, 0, t.left, bar(B_RES));
             load_tile<HD>(p.tmap_v, sV, kvh, t.row, 0, t.left, bar(B_RES));
+            if (table_here) {
+                const uint32_t slot = items & 1;
+                if (items >= 2 && !wait_warp(bar(B_TABFREE + slot), ((items >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar(B_TABFULL + slot), table_bytes);
+                    bulk_load(c.base + L::OFF_SMALL + kSmallKv + slot * kTableBytes,
+                              bias_row_of(p.bias_table, kvh * p.group, last) - kBiasPad, table_bytes, bar(B_TABFULL + slot));
+                }
+                __syncwarp();
+            }
             ++items;
             const int r_first = first_query(t);
             for (int i = 0; ok && i < t.n * p.group; ++i, ++J) {
@@ -1081,6 +1095,15 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             continue;
         }
         const int pos_first = t.off + first_query(t) + 64 * wg;  // of this warpgroup's first query
+        [[maybe_unused]] const float *bias_row = nullptr;  // entry of distance 0 of the item's first head
+        if constexpr (BIAS) {
+            bias_row = bias_row_of(p.bias_table, head0, last);
+            if (table_here) {
+                ok = wait_warp(bar(B_TABFULL + (items & 1)), (items >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
+                if (!ok) break;
+                bias_row = reinterpret_cast<const float *>(c.sb + L::OFF_SMALL + kSmallKv + (items & 1) * kTableBytes) + kBiasPad;
+            }
+        }
         for (int g = 0; ok && g < p.group; ++g)
         for (int q = 0; q < t.n; ++q, ++J) {
             const uint32_t st = J & 1;
@@ -1100,16 +1123,16 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             // (Lane 31 has the nearest key.)
             const bool near = BIAS && __shfl_sync(0xffffffffu, d0, 31) < last;
             if (near) {
-                const float *bt = bias_row_of(p.bias_table, head0 + g, last) + d0;
+                const float *bt = bias_row + g * bias_stride(last) + d0;  // (-inf before distance 0)
                 const float4 *nl = reinterpret_cast<const float4 *>(stat(st) + 64 * wg);
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
                     const float4 l = nl[x];
                     float *v = &w[x >> 3][4 * (x & 7)];
-                    v[0] = fmaf(v[0], sl2, __ldg(bt + 4 * x)) + l.x;
-                    v[1] = fmaf(v[1], sl2, __ldg(bt + 4 * x + 1)) + l.y;
-                    v[2] = fmaf(v[2], sl2, __ldg(bt + 4 * x + 2)) + l.z;
-                    v[3] = fmaf(v[3], sl2, __ldg(bt + 4 * x + 3)) + l.w;
+                    v[0] = fmaf(v[0], sl2, bt[4 * x]) + l.x;
+                    v[1] = fmaf(v[1], sl2, bt[4 * x + 1]) + l.y;
+                    v[2] = fmaf(v[2], sl2, bt[4 * x + 2]) + l.z;
+                    v[3] = fmaf(v[3], sl2, bt[4 * x + 3]) + l.w;
                 }
             } else {
                 const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(stat(st) + (BIAS ? 256 : 0) + 64 * wg);
@@ -1173,6 +1196,10 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_DSFULL));
+        }
+        if (BIAS && ok) {
+            __syncwarp();
+            if (table_here && lane == 0) mbar_arrive(bar(B_TABFREE + (items & 1)));
         }
         ok = ok && wait_warp(bar(B_DONE), items & 1, c.abort_flag, p.err, kTimeoutNs);
         if (!ok) break;
@@ -1272,7 +1299,7 @@ cudaError_t launch_backward_d(GradParams &p, const PlanParams &plan, const Packe
     const int64_t q_items = a.total_q > 0 ? most_tiles(a.total_q, a.num_seqs) * a.num_heads : 0;
     const int64_t k_items = a.total_k > 0 ? most_tiles(a.total_k, a.num_seqs) * a.num_kv_heads : 0;
     if (e == cudaSuccess) e = launch_tiles(grad_q_kernel<HD, BIAS>, LayoutQ<HD, BIAS>::SMEM, set[0], q_items, p, stream);
-    if (e == cudaSuccess) e = launch_tiles(grad_kv_kernel<HD, BIAS>, LayoutKv<HD>::SMEM, set[1], k_items, p, stream);
+    if (e == cudaSuccess) e = launch_tiles(grad_kv_kernel<HD, BIAS>, LayoutKv<HD, BIAS>::SMEM, set[1], k_items, p, stream);
     if (BIAS && e == cudaSuccess) {
         const dim3 blocks(a.num_heads, (a.bias.num_buckets + kBiasBuckets - 1) / kBiasBuckets);
         grad_bias_kernel<<<blocks, 1024, 0, stream>>>(g.dbias, p.partial, p.counts, a.num_heads, a.bias.num_buckets);
