@@ -162,7 +162,7 @@ enum : int {
     B_RES = 0,      // resident tiles loaded
     B_RESEMPTY = 20,  // resident tiles read
     B_ACCFREE = 21,   // accumulators stored (8 warps)
-    B_AFULL = 1,    // [3] tile of ring A ready (two arrivals: the copies, and the loading warp; dK, dV: of both rings)
+    B_AFULL = 1,    // [3] tile of ring A ready (two arrivals: the copies, and the loading warp; dK, dV: for both rings)
     B_AEMPTY = 4,   // [3] read
     B_BFULL = 7,    // [2] ring B, likewise
     B_BEMPTY = 9,   // [2]
@@ -211,18 +211,17 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int from) {
 }
 __device__ __forceinline__ bool ragged(int left) { return left < BM && (left & 15) != 0; }
 
-// Tile -> stage, by the loading warp; `full` expects two arrivals.  `lands` counts the edited tiles,
-// `extra` runs before the second arrival.  False: a wait ran out.
-template <int HD, class Extra>
+// Tile -> stage, by the loading warp; `full` expects two arrivals.  `lands` counts the edited tiles.
+// False: a wait ran out.
+template <int HD>
 __device__ __forceinline__ bool load_stage(const CUtensorMap *map, uint32_t dst, int head, int start, int row0, int end,
                                            uint32_t full, uint32_t land, uint32_t &lands, volatile int *abort_flag,
-                                           unsigned *err, Extra extra) {
+                                           unsigned *err) {
     const int lane = threadIdx.x & 31;
     const bool cut = ragged(end - row0);
     if (lane == 0) mbar_arrive_expect_tx(cut ? land : full, (HD / 64) * HALF);
     __syncwarp();
     load_tile<HD>(map, dst, head, start, row0, end, cut ? land : full);
-    extra();
     if (cut) {
         if (!wait_warp(land, lands++ & 1, abort_flag, err, kTimeoutNs)) return false;
         clear_rows<HD>(dst, end - row0);
@@ -294,7 +293,7 @@ struct Cta {
     uint32_t tmem;
     volatile int *abort_flag;
 };
-template <class L, int A_ARRIVALS>
+template <class L>
 __device__ __forceinline__ Cta setup() {
     extern __shared__ __align__(1024) uint8_t smem_raw[];  // (swizzled tiles start on 1024 bytes)
     Cta c;
@@ -307,7 +306,7 @@ __device__ __forceinline__ Cta setup() {
         mbar_init(bar(B_RESEMPTY), 1);
         mbar_init(bar(B_ACCFREE), 8);
         for (int s = 0; s < 3; ++s) {
-            mbar_init(bar(B_AFULL + s), A_ARRIVALS);
+            mbar_init(bar(B_AFULL + s), 2);
             mbar_init(bar(B_AEMPTY + s), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -559,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
         int *first = reinterpret_cast<int *>(smem_raw + L::OFF_SMALL + 1024);
         for (int i = threadIdx.x; i <= p.bias.num_buckets; i += kThreads) first[i] = p.bias.first[i];
     }
-    const Cta c = setup<L, 2>();
+    const Cta c = setup<L>();
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sQ = c.base + L::OFF_RES, sDo = sQ + L::TILE;
@@ -628,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             const int kvh = h / p.group;
             auto load = [&](const CUtensorMap *map, uint32_t dst, int j, uint32_t full) -> bool {
                 return load_stage<HD>(map, dst, kvh, t.k_start, (s.kt0 + s.tile(j)) * BN, t.sk, full, bar(B_LAND), lands,
-                                      c.abort_flag, p.err, [] {});
+                                      c.abort_flag, p.err);
             };
             for (int j = 0; ok && j < s.n_all; ++j, ++J) {
                 const uint32_t sb = J % NB;
@@ -949,7 +948,7 @@ template <int HD, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_constant__ GradParams p) {
     using L = LayoutKv<HD, BIAS>;
     constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 384;
-    const Cta c = setup<L, 4>();  // (Q and dout of a step share a barrier: one wait less)
+    const Cta c = setup<L>();
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t sK = c.base + L::OFF_RES, sV = sK + L::TILE;
@@ -991,27 +990,41 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             for (int i = 0; ok && i < t.n * p.group; ++i, ++J) {
                 const uint32_t st = J & 1;
                 const int r = r_first + i % t.n * BN, head = kvh * p.group + i / t.n;
-                auto stats = [&] {
-                    float far = 0.f;
-                    if constexpr (BIAS) far = __ldg(bias_row_of(p.bias_table, head, last) + last);
-                    const int64_t at = static_cast<int64_t>(head) * p.total_q + t.q_start + r;
+                // (dout's stage is free first: dV comes before dK.  The copies of a tile that is edited
+                // are under way together.)
+                const bool cut = ragged(t.sq - r);
+                const uint32_t full = bar(B_AFULL + st), land = cut ? bar(B_LAND) : full;
+                ok = J < 2 || wait_warp(bar(B_BEMPTY + st), ((J >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(land, 2 * L::TILE);
+                __syncwarp();
+                load_tile<HD>(p.tmap_do, sDo(st), head, t.q_start, r, t.sq, land);
+                ok = J < 2 || wait_warp(bar(B_AEMPTY + st), ((J >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs);
+                if (!ok) break;
+                load_tile<HD>(p.tmap_q, sQ(st), head, t.q_start, r, t.sq, land);
+                float far = 0.f;
+                if constexpr (BIAS) far = __ldg(bias_row_of(p.bias_table, head, last) + last);
+                const int64_t at = static_cast<int64_t>(head) * p.total_q + t.q_start + r;
 #pragma unroll
-                    for (int x4 = 0; x4 < 4; ++x4) {
-                        const int x = lane + 32 * x4;
-                        const bool in = r + x < t.sq;
-                        const float l2 = in ? p.lse2[at + x] : INFINITY;
-                        stat(st)[x] = -l2;
-                        stat(st)[128 + x] = in ? -p.delta[at + x] : 0.f;
-                        if constexpr (BIAS) stat(st)[256 + x] = far - l2;
-                    }
-                };
-                // (dout's stage is free first: dV comes before dK.)
-                ok = (J < 2 || wait_warp(bar(B_BEMPTY + st), ((J >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) &&
-                     load_stage<HD>(p.tmap_do, sDo(st), head, t.q_start, r, t.sq, bar(B_AFULL + st), bar(B_LAND), lands, c.abort_flag,
-                                    p.err, [] {}) &&
-                     (J < 2 || wait_warp(bar(B_AEMPTY + st), ((J >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) &&
-                     load_stage<HD>(p.tmap_q, sQ(st), head, t.q_start, r, t.sq, bar(B_AFULL + st), bar(B_LAND), lands, c.abort_flag,
-                                    p.err, stats);
+                for (int x4 = 0; x4 < 4; ++x4) {
+                    const int x = lane + 32 * x4;
+                    const bool in = r + x < t.sq;
+                    const float l2 = in ? p.lse2[at + x] : INFINITY;
+                    stat(st)[x] = -l2;
+                    stat(st)[128 + x] = in ? -p.delta[at + x] : 0.f;
+                    if constexpr (BIAS) stat(st)[256 + x] = far - l2;
+                }
+                if (cut) {
+                    ok = wait_warp(land, lands++ & 1, c.abort_flag, p.err, kTimeoutNs);
+                    if (!ok) break;
+                    clear_rows<HD>(sDo(st), t.sq - r);
+                    clear_rows<HD>(sQ(st), t.sq - r);
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (cut) mbar_arrive(full);
+                    mbar_arrive(full);
+                }
             }
         }
     } else if (warp == kWarpMma) {
