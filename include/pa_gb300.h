@@ -530,7 +530,7 @@ pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const
  * The bias: a table [num_buckets, num_heads] fp32 (NULL, 0 buckets: none).  With m = num_buckets / 2,
  * distances n < m have bucket n and longer ones min(num_buckets - 1, m + floor(ln(n / m) /
  * ln(max_distance / m) (num_buckets - m))): the floor of the real number, so a distance on a border
- * belongs to the bucket beyond it.
+ * belongs to the bucket beyond it.  A bias below -1e30 hides its keys, as -inf does.
  *
  * pa_varlen_attn: out [total_q, num_heads, head_dim] and lse [total_q, num_heads] (natural log).
  *     q [total_q, num_heads, head_dim], k / v [total_k, num_kv_heads, head_dim] bf16: a token's heads
@@ -560,7 +560,8 @@ pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const
  *              bytes (none without a bias); pa_varlen_attn_backward:
  *              pa_varlen_attn_backward_workspace_size(...); pa_decode_bias: pa_decode_workspace_size(...)
  * Supported: head_dim in {64, 128}; num_heads / num_kv_heads <= 64; 2 to 128 buckets,
- * max_distance above num_buckets / 2 and up to 32768; scale positive, below 1e38; total_q and
+ * max_distance above num_buckets / 2 and up to 32768; scale positive, below 1e38
+ * (with a bias also at least 1e-20, and bias / scale inside the fp32 range); total_q and
  * total_k below 2^30; num_seqs <= 65535; the 128-row tiles of max_seqlen_q (max_seqlen_k) times
  * num_seqs times num_heads (num_kv_heads) below 2^31; in the backward call also (total_q / 128 +
  * num_seqs) num_heads and (total_k / 128 + num_seqs) num_heads.  Sizes of the paged calls as pa_decode and pa_varlen_prefill, but at

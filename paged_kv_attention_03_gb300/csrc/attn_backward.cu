@@ -151,6 +151,9 @@ struct Layout {
 
 // An item's bias (dK, dV: of its kv head's heads) in shared memory; a longer one is read from global memory.
 constexpr uint32_t kTableBytes = 15360;
+// What is kept of a head's row: distances -kNearPad .. last + 127.
+constexpr int kNearPad = 256;
+__host__ __device__ constexpr int near_entries(int last) { return (last + kNearPad + 128 + 3) & ~3; }
 constexpr uint32_t kSmallQ = 1024 + 528;
 template <int HD, bool BIAS>
 using LayoutQ = Layout<HD, 3, BIAS ? 1 : 2, kSmallQ + (BIAS ? 2 * kTableBytes : 0u)>;
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
     auto sK = [&](uint32_t st) -> uint32_t { return c.base + L::OFF_A + st * L::TILE; };
     auto sV = [&](uint32_t st) -> uint32_t { return c.base + L::OFF_B + st * L::TILE; };
     const int last = p.bias.last();
-    const uint32_t table_bytes = BIAS ? bias_stride(last) * 4u : 0u;
+    const uint32_t table_bytes = BIAS ? near_entries(last) * 4u : 0u;
     const bool table_here = BIAS && table_bytes <= kTableBytes;
     const int count = *p.counts;
     // An item's steps: the tiles 0 .. n_pre - 1 with D from dout . out; tiles n_pre .. n - 2 for D alone;
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 if (items >= 2 && !wait_warp(bar(B_TABFREE + slot), ((items >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar(B_TABFULL + slot), table_bytes);
-                    bulk_load(c.base + L::OFF_SMALL + kSmallQ + slot * kTableBytes, bias_row_of(p.bias_table, h, last) - kBiasPad,
+                    bulk_load(c.base + L::OFF_SMALL + kSmallQ + slot * kTableBytes, bias_row_of(p.bias_table, h, last) - kNearPad,
                               table_bytes, bar(B_TABFULL + slot));
                 }
                 __syncwarp();
@@ -748,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 if (table_here) {
                     ok = wait_warp(bar(B_TABFULL + (items & 1)), (items >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
                     if (!ok) break;
-                    bias_row = small + kSmallQ / 4 + (items & 1) * (kTableBytes / 4) + kBiasPad;
+                    bias_row = small + kSmallQ / 4 + (items & 1) * (kTableBytes / 4) + kNearPad;
                 }
                 far = bias_row[last] - lse2;
             }
@@ -958,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
     auto stat = [&](int st) -> float * { return reinterpret_cast<float *>(c.sb + L::OFF_SMALL) + st * 384; };
     const int last = p.bias.last();
 
-    const uint32_t table_bytes = BIAS ? bias_stride(last) * 4u * p.group : 0u;
+    const uint32_t head_bytes = BIAS ? near_entries(last) * 4u : 0u, table_bytes = head_bytes * p.group;
     const bool table_here = BIAS && table_bytes <= kTableBytes;
     const int count = p.counts[1];
 
@@ -978,11 +981,11 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             if (table_here) {
                 const uint32_t slot = items & 1;
                 if (items >= 2 && !wait_warp(bar(B_TABFREE + slot), ((items >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar(B_TABFULL + slot), table_bytes);
-                    bulk_load(c.base + L::OFF_SMALL + kSmallKv + slot * kTableBytes,
-                              bias_row_of(p.bias_table, kvh * p.group, last) - kBiasPad, table_bytes, bar(B_TABFULL + slot));
-                }
+                if (lane == 0) mbar_arrive_expect_tx(bar(B_TABFULL + slot), table_bytes);
+                __syncwarp();
+                for (int g = lane; g < p.group; g += 32)
+                    bulk_load(c.base + L::OFF_SMALL + kSmallKv + slot * kTableBytes + g * head_bytes,
+                              bias_row_of(p.bias_table, kvh * p.group + g, last) - kNearPad, head_bytes, bar(B_TABFULL + slot));
                 __syncwarp();
             }
             ++items;
@@ -1109,12 +1112,14 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
         }
         const int pos_first = t.off + first_query(t) + 64 * wg;  // of this warpgroup's first query
         [[maybe_unused]] const float *bias_row = nullptr;  // entry of distance 0 of the item's first head
+        [[maybe_unused]] int bias_step = bias_stride(last);  // to the next head's
         if constexpr (BIAS) {
             bias_row = bias_row_of(p.bias_table, head0, last);
             if (table_here) {
                 ok = wait_warp(bar(B_TABFULL + (items & 1)), (items >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
                 if (!ok) break;
-                bias_row = reinterpret_cast<const float *>(c.sb + L::OFF_SMALL + kSmallKv + (items & 1) * kTableBytes) + kBiasPad;
+                bias_row = reinterpret_cast<const float *>(c.sb + L::OFF_SMALL + kSmallKv + (items & 1) * kTableBytes) + kNearPad;
+                bias_step = head_bytes / 4;
             }
         }
         for (int g = 0; ok && g < p.group; ++g)
@@ -1136,7 +1141,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             // (Lane 31 has the nearest key.)
             const bool near = BIAS && __shfl_sync(0xffffffffu, d0, 31) < last;
             if (near) {
-                const float *bt = bias_row + g * bias_stride(last) + d0;  // (-inf before distance 0)
+                const float *bt = bias_row + g * bias_step + d0;  // (-inf before distance 0)
                 const float4 *nl = reinterpret_cast<const float4 *>(stat(st) + 64 * wg);
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {

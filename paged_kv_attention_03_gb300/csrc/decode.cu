@@ -459,7 +459,7 @@ __device__ __forceinline__ void decode_split_body(const DecodeKernelParams &p, c
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int h = 8 * j + 2 * (lane & 3) + e;
-                far_bias[j][e] = h < rows_valid ? rb.b.bias[(rb.b.num_buckets - 1) * p.num_heads + h0 + h] * kLog2e : 0.f;
+                far_bias[j][e] = h < rows_valid ? bias_log2(rb.b.bias[(rb.b.num_buckets - 1) * p.num_heads + h0 + h]) : 0.f;
             }
     }
 
@@ -532,7 +532,7 @@ __device__ __forceinline__ void decode_split_body(const DecodeKernelParams &p, c
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int h = 8 * j + 2 * (lane & 3) + e;
-                            if (h < rows_valid) near_bias[j][2 * k + e] = row[h] * kLog2e;
+                            if (h < rows_valid) near_bias[j][2 * k + e] = bias_log2(row[h]);
                         }
                 }
             }

@@ -12,9 +12,10 @@ bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
 // A bias, given by table, number of buckets and largest distance: all or nothing.
-pa_status check_bias(const float *bias, int num_buckets, int max_distance, pa::RelativeBias *b) {
+pa_status check_bias(const float *bias, int num_buckets, int max_distance, float scale, pa::RelativeBias *b) {
     if (bias == nullptr) return num_buckets == 0 ? PA_OK : PA_ERR_INVALID_ARG;
     if (num_buckets < 2 || max_distance <= num_buckets / 2 || !aligned(bias, 4)) return PA_ERR_INVALID_ARG;
+    if (scale < 1e-20f) return PA_ERR_UNSUPPORTED;  // (biases are divided by it)
     if (!pa::plan_relative_bias(num_buckets, max_distance, b)) return PA_ERR_UNSUPPORTED;
     b->bias = bias;
     return PA_OK;
@@ -100,7 +101,7 @@ pa_status pa_varlen_attn(void *out, float *lse, const void *q, const void *k, co
     a.scale = scale;
     bool nothing = false;
     pa_status st = check_packed(a, &nothing);
-    if (st == PA_OK) st = check_bias(bias, num_buckets, max_distance, &a.bias);
+    if (st == PA_OK) st = check_bias(bias, num_buckets, max_distance, scale, &a.bias);
     if (st != PA_OK || nothing || total_q == 0 || max_seqlen_q == 0) return st;
     if (!out || !lse || !aligned(out, 16) || !aligned(lse, 4)) return PA_ERR_INVALID_ARG;
     const size_t need = bias ? pa::bias_table_bytes(num_heads, a.bias) : 0;
@@ -109,7 +110,7 @@ pa_status pa_varlen_attn(void *out, float *lse, const void *q, const void *k, co
     a.err = pa::device_error_word();
     if (bias) {
         a.bias_table = static_cast<float *>(workspace);
-        st = pa::cuda_status(pa::launch_bias_table(static_cast<float *>(workspace), num_heads, a.bias, s));
+        st = pa::cuda_status(pa::launch_bias_table(static_cast<float *>(workspace), num_heads, a.bias, true, s));
         if (st != PA_OK) return st;
     }
     return pa::cuda_status(pa::launch_packed_attn(a, out, lse, s));
@@ -144,7 +145,7 @@ pa_status pa_varlen_attn_backward(void *dq, void *dk, void *dv, float *dbias, in
     a.scale = scale;
     bool nothing = false;
     pa_status st = check_packed(a, &nothing);
-    if (st == PA_OK) st = check_bias(bias, num_buckets, max_distance, &a.bias);
+    if (st == PA_OK) st = check_bias(bias, num_buckets, max_distance, scale, &a.bias);
     if (st != PA_OK) return st;
     if (!row_stride_ok(dq_stride, num_heads, head_dim) || !row_stride_ok(dk_stride, num_kv_heads, head_dim) ||
         !row_stride_ok(dv_stride, num_kv_heads, head_dim))
@@ -164,7 +165,7 @@ pa_status pa_varlen_attn_backward(void *dq, void *dk, void *dv, float *dbias, in
     a.err = pa::device_error_word();
     if (bias) {
         a.bias_table = static_cast<float *>(workspace);
-        st = pa::cuda_status(pa::launch_bias_table(static_cast<float *>(workspace), num_heads, a.bias, s));
+        st = pa::cuda_status(pa::launch_bias_table(static_cast<float *>(workspace), num_heads, a.bias, false, s));
         if (st != PA_OK) return st;
     }
     g.out = out;
@@ -193,7 +194,7 @@ pa_status pa_decode_bias(void *out, const void *q, const void *key, const void *
     if (!is_pow2(block_size) || block_size > 1024 || batch > 65535) return PA_ERR_UNSUPPORTED;
     pa::DecodeArgs a{};
     if (!bias) return PA_ERR_INVALID_ARG;
-    st = check_bias(bias, num_buckets, max_distance, &a.bias);
+    st = check_bias(bias, num_buckets, max_distance, scale, &a.bias);
     if (st != PA_OK) return st;
     const bool has_new = key || value || slot_mapping;
     if (has_new && !(key && value && slot_mapping)) return PA_ERR_INVALID_ARG;
@@ -250,7 +251,7 @@ pa_status pa_varlen_prefill_bias(void *out, const void *q, const void *key, cons
     if (num_seqs > 65535 || total_q > 0x7fffff00 || num_blocks * block_size > 0x7fffff00LL) return PA_ERR_UNSUPPORTED;
     pa::PrefillArgs a{};
     if (!bias) return PA_ERR_INVALID_ARG;
-    st = check_bias(bias, num_buckets, max_distance, &a.bias);
+    st = check_bias(bias, num_buckets, max_distance, scale, &a.bias);
     if (st != PA_OK) return st;
     const bool has_new = key || value || slot_mapping;
     if (has_new && !(key && value && slot_mapping)) return PA_ERR_INVALID_ARG;
@@ -276,7 +277,7 @@ pa_status pa_varlen_prefill_bias(void *out, const void *q, const void *key, cons
     if (num_seqs == 0 || max_seqlen_q == 0) return PA_OK;
     // (The table serves the prefill kernel; single-row sequences alone go to the decode kernel.)
     if (!seq_lens || max_seqlen_q > 1) {
-        st = pa::cuda_status(pa::launch_bias_table(static_cast<float *>(workspace), num_heads, a.bias, s));
+        st = pa::cuda_status(pa::launch_bias_table(static_cast<float *>(workspace), num_heads, a.bias, true, s));
         if (st != PA_OK) return st;
     }
     a.bias_table = static_cast<float *>(workspace);

@@ -62,7 +62,7 @@ using namespace sm100;
 constexpr int BM = 128;                  // MMA rows per query tile
 constexpr int BN = 128;                  // keys per KV tile
 constexpr uint32_t HALF = 128u * 128u;   // [128 rows][64 bf16] = 16 KB (one swizzle span)
-constexpr int NSK = 3;                   // K stages
+constexpr int NSK = 3;                   // K stages (two with a bias: no slower, and its windows take the third's place)
 constexpr int NSV = 2;                   // V stages
 // Warpgroups 0 and 1 (warps 0-3, 4-7) are the softmax of query tiles 0 and 1 (a warp
 // reaches the TMEM lanes 32 * (warp % 4) ...); warpgroup 2 holds the producers and the
@@ -131,6 +131,10 @@ struct PrefillKernelParams {
     // one value.
     const float *bias_table;
     int bias_last;
+    // Entries of a head's bias that a tile's distances span (0: more heads than the shared memory has
+    // room for), and from one head's in shared memory to the next one's.
+    int bias_span;
+    int bias_step;
     unsigned *err;
 };
 
@@ -152,17 +156,23 @@ enum : int {
     B_LK = B_IEMPTY + kRing,     // [NSK]
     B_LV = B_LK + NSK,           // [NSV]
     B_QCONV = B_LV + NSV,
-    NBARS = B_QCONV + 1
+    // With a bias: a near tile's window of it landed, and read by the softmax warps.
+    B_WFULL = B_QCONV + 1,   // [2]
+    B_WEMPTY = B_WFULL + 2,  // [2]
+    NBARS = B_WEMPTY + 2
 };
 
-template <int HD>
+constexpr uint32_t kWindowBytes = 16384;  // of one of two windows
+template <int HD, bool BIAS = false>
 struct Layout {
+    static constexpr int NS_K = BIAS ? 2 : NSK;
     static constexpr int NHALF = HD / 64;
     static constexpr uint32_t TILE = NHALF * HALF;  // one [128][HD] bf16 tile
     static constexpr uint32_t OFF_Q = 0;             // Q0, Q1
     static constexpr uint32_t OFF_K = OFF_Q + 2 * TILE;
-    static constexpr uint32_t OFF_V = OFF_K + NSK * TILE;
-    static constexpr uint32_t OFF_BAR = OFF_V + NSV * TILE;
+    static constexpr uint32_t OFF_V = OFF_K + NS_K * TILE;
+    static constexpr uint32_t OFF_W = OFF_V + NSV * TILE;  // windows of the bias
+    static constexpr uint32_t OFF_BAR = OFF_W + (BIAS ? 2 * kWindowBytes : 0u);
     // 16-byte aligned: the item-info slots after it are read as 16-byte vectors.
     static constexpr uint32_t OFF_MISC = (OFF_BAR + NBARS * 8 + 15u) & ~15u;
     static constexpr uint32_t OFF_INFO = OFF_MISC + 16;   // item-info ring, kRing x 64 bytes
@@ -518,7 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr bool PV16 = CACHE != kCacheBf16 && !PACKED;  // P and V in f16
     static_assert(CACHE != kCacheE4m3 || HD == 128, "the E4M3 cache path is built for head_dim 128");
     static_assert(!CODES || !PREFIX, "the shared-prefix mode is built for bf16 caches");
-    using L = Layout<HD>;
+    using L = Layout<HD, BIAS>;
+    constexpr int NS_K = L::NS_K;
     constexpr int NHALF = L::NHALF;
     constexpr int KSTEPS_S = HD / 16;  // MMAs per S tile
     constexpr int KSTEPS_O = BN / 16;  // MMAs per PV tile
@@ -569,6 +580,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < NSK; ++s) mbar_init(bar(B_LK + s), 1);
         for (int s = 0; s < NSV; ++s) mbar_init(bar(B_LV + s), 1);
         mbar_init(bar(B_QCONV), 8);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar(B_WFULL + s), 1);
+            mbar_init(bar(B_WEMPTY + s), 8);
+        }
         *abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
@@ -614,6 +629,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_3d(dst + h * HALF + u * 2048, map, h * 64, it.kvh, row, full);
         }
     };
+
+    // With a bias: whether tile j of the item holds a distance below bias_last, and the distance with
+    // which its window begins (a multiple of 4 at or below its smallest one).
+    auto tile_distance = [&](const Item &it, int j) -> int {  // the smallest one
+        return it.sk - it.sq + it.q0 - ((it.kt0 + j) * BN + BN - 1);
+    };
+    [[maybe_unused]] auto near_tile = [&](const Item &it, int j) -> bool { return tile_distance(it, j) < p.bias_last; };
+    [[maybe_unused]] auto window_start = [&](const Item &it, int j) -> int { return tile_distance(it, j) & ~3; };
 
     // One tile of 4-bit rows at dst: a bulk copy for each 16-key piece, a lane each; a piece past
     // the sequence, or of an invalid block, is zeros.
@@ -691,7 +714,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr bool is_k = decltype(is_k_tag)::value;
             [[maybe_unused]] const CUtensorMap *map = is_k ? &p.tmap_k : &p.tmap_v;
             const uint32_t sbase = is_k ? sK : sV;
-            constexpr uint32_t NS = is_k ? NSK : NSV;
+            constexpr uint32_t NS = is_k ? NS_K : NSV;
+            [[maybe_unused]] uint32_t nw = 0;  // windows loaded
             constexpr int b_full = is_k ? B_KFULL : B_VFULL, b_empty = is_k ? B_KEMPTY : B_VEMPTY;
             if constexpr (!FP4)
                 if (lane == 0) prefetch_tmap(map);
@@ -710,6 +734,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane == 0) mbar_arrive_expect_tx(bar(b_full + st), L::TILE);
                         __syncwarp();
                         load_kv(map, it, (it.kt0 + j) * BN, sbase + st * L::TILE, bar(b_full + st));
+                        if constexpr (BIAS && is_k) {
+                            if (p.bias_span > 0 && near_tile(it, j)) {
+                                const uint32_t ws = nw & 1;
+                                if (nw >= 2 && !wait_warp(bar(B_WEMPTY + ws), ((nw >> 1) - 1) & 1, abort_flag, p.err, p.wait_ns)) {
+                                    ok = false;
+                                    break;
+                                }
+                                if (lane == 0) mbar_arrive_expect_tx(bar(B_WFULL + ws), G * p.bias_span * 4);
+                                __syncwarp();
+                                for (int h = lane; h < G; h += 32)
+                                    bulk_load(base + L::OFF_W + ws * kWindowBytes + h * p.bias_step * 4,
+                                              bias_row_of(p.bias_table, it.kvh * G + h, p.bias_last) + window_start(it, j),
+                                              p.bias_span * 4, bar(B_WFULL + ws));
+                                ++nw;
+                            }
+                        }
                     }
                 }
             } else {
@@ -844,7 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto issue_s = [&](int i, uint32_t gk, bool half) {
                 if (elect_one()) {
                     const uint64_t a0 = smem_desc_sw128(sQ + i * L::TILE, 16, 1024);
-                    const uint64_t b0 = smem_desc_sw128(sK + (gk % NSK) * L::TILE, 16, 1024);
+                    const uint64_t b0 = smem_desc_sw128(sK + (gk % NS_K) * L::TILE, 16, 1024);
                     const uint32_t id = half ? idesc_s_half : idesc_s;
 #pragma unroll
                     for (int k = 0; k < KSTEPS_S; ++k) {
@@ -873,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 for (int j = 0; j < it.n_tiles; ++j, ++g) {
-                    const int st = g % NSK;
+                    const int st = g % NS_K;
                     // query tile 0: P0 V of the previous tile needs no K, so it goes to
                     // the tensor core before the wait for K(g)
                     const bool half = it.half_last && j == it.n_tiles - 1;
@@ -881,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ok = false;
                         break;
                     }
-                    if (!wait(B_KFULL + st, (g / NSK) & 1)) {
+                    if (!wait(B_KFULL + st, (g / NS_K) & 1)) {
                         ok = false;
                         break;
                     }
@@ -922,6 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool row_in_tile = row < G * T;
         const float sl2 = p.scale_log2;
         const int w = p.window;
+        [[maybe_unused]] uint32_t nw = 0;  // windows of the bias taken
         uint32_t gt = 0;   // global KV tile counter
         uint32_t c = 0;    // tiles this warpgroup has processed
         bool ok = true;
@@ -960,6 +1001,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (wg == 1 && !it.has1) {
                 gt += it.n_tiles;
+                if constexpr (BIAS) {  // (a window is free when all softmax warps say so)
+                    for (int j = 0; ok && p.bias_span > 0 && j < it.n_tiles; ++j)
+                        if (near_tile(it, j)) {
+                            ok = wait_warp(bar(B_WFULL + (nw & 1)), (nw >> 1) & 1, abort_flag, p.err, p.wait_ns);
+                            if (ok && lane == 0) mbar_arrive(bar(B_WEMPTY + (nw & 1)));
+                            ++nw;
+                        }
+                }
                 continue;
             }
             const bool valid = row_in_tile && tok < it.rows0 + it.rows1;
@@ -975,10 +1024,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lo = w > 0 ? pos - w + 1 : INT_MIN;
             }
             [[maybe_unused]] const float *bias_row = nullptr;  // entry of distance 0
-            [[maybe_unused]] float far_bias = 0.f;
+            [[maybe_unused]] float far_bias = 0.f, ref_bias = 0.f, inv_sl2 = 0.f;
+            [[maybe_unused]] bool all_chunks = false;  // far chunks of near tiles take entries too
             if constexpr (BIAS) {
                 bias_row = bias_row_of(p.bias_table, min(it.kvh * G + g, p.num_heads - 1), p.bias_last);
-                far_bias = __ldg(bias_row + p.bias_last);
+                far_bias = __ldg(bias_row - kBiasPad);
+                ref_bias = bias_ref(far_bias);
+                all_chunks = __any_sync(0xffffffffu, ref_bias != far_bias);
+                inv_sl2 = 1.f / sl2;
             }
             float m_ref = -INFINITY;  // reference max (base-2 units) the weights use
             float l_sum = 0.f;
@@ -988,6 +1041,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 tc_fence_after();
+                const int key0 = (it.kt0 + j) * BN;
+                // x = sl2 * s + add is the logit in base 2: a far tile's bias is added to the row's maximum
+                // and to the exponents' offset, instead of its logits.  In a near tile add is what the
+                // table's entries are relative to, and chunks of 32 keys nearer than bias_last get those:
+                // in tensor memory, chunk by chunk, which keeps the code of all other tiles as small as
+                // without a bias.
+                [[maybe_unused]] float add = 0.f;
+                if constexpr (BIAS) {
+                    add = far_bias;
+                    if (near_tile(it, j)) {
+                        add = ref_bias;
+                        const float *near = bias_row;  // entry of distance 0
+                        if (p.bias_span > 0) {
+                            if (!wait_warp(bar(B_WFULL + (nw & 1)), (nw >> 1) & 1, abort_flag, p.err, p.wait_ns)) {
+                                ok = false;
+                                break;
+                            }
+                            near = reinterpret_cast<const float *>(sb + L::OFF_W + (nw & 1) * kWindowBytes) + g * p.bias_step -
+                                   window_start(it, j);
+                        }
+                        const int d0 = pos - key0;  // distance to the tile's first key
+#pragma unroll 1
+                        for (int cc = 0; cc < BN / 32; ++cc) {
+                            const int dc = d0 - cc * 32;
+                            if (__shfl_sync(0xffffffffu, dc, 31) < 0) break;  // (and later ones are future keys')
+                            if (!all_chunks && __shfl_sync(0xffffffffu, dc, 0) - 31 >= p.bias_last) continue;
+                            const float *bt = near + dc;
+                            float v[32];
+                            tmem_ld_32x32b_x32(scol + cc * 32, v);
+                            tmem_wait_ld_regs(v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = fmaf(bt[-i], inv_sl2, v[i]);
+                            tmem_st_32x32b_x32(scol + cc * 32, v);
+                        }
+                        tmem_wait_st();
+                        if (p.bias_span > 0) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(B_WEMPTY + (nw & 1)));
+                            ++nw;
+                        }
+                    }
+                }
                 float sc[BN / 32][32];
 #pragma unroll
                 for (int cc = 0; cc < BN / 32; ++cc) tmem_ld_32x32b_x32(scol + cc * 32, sc[cc]);
@@ -996,33 +1091,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int cc = 0; cc < BN / 32; ++cc) tmem_wait_ld_regs(sc[cc]);
                 float *s = &sc[0][0];
 
-                const int key0 = (it.kt0 + j) * BN;
-                // x = mul * s + add is the logit in base 2.  With a bias, chunks of 32 keys nearer than
-                // bias_last take it from the table (future keys' entries are whatever stands
-                // before the distance 0 and are masked below); a tile without any such chunk
-                // has one bias, which is added to the row's maximum instead of its logits.
-                float mul = sl2, add = 0.f;
-                if constexpr (BIAS) {
-                    add = far_bias;
-                    const int d0 = pos - key0;  // distance to the tile's first key
-                    if (__shfl_sync(0xffffffffu, d0, 0) - (BN - 1) < p.bias_last) {
-                        mul = 1.f;
-                        add = 0.f;
-#pragma unroll
-                        for (int cc = 0; cc < BN / 32; ++cc) {
-                            const int dc = d0 - cc * 32;
-                            const bool future = __shfl_sync(0xffffffffu, dc, 31) < 0;
-                            if (future || __shfl_sync(0xffffffffu, dc, 0) - 31 >= p.bias_last) {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) sc[cc][i] = fmaf(sc[cc][i], sl2, far_bias);
-                            } else {
-                                const float *bt = bias_row + dc;
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) sc[cc][i] = fmaf(sc[cc][i], sl2, __ldg(bt - i));
-                            }
-                        }
-                    }
-                }
                 // Row maximum as 8 independent 3-input max chains, then a tree (a single
                 // dependent chain of 128 maxima would cost ~4 cycles per element).
                 // Edge tiles: the causal bound and the window's lower bound are masked
@@ -1053,7 +1121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int a = 0; a < 8; ++a) mx8[a] = fmaxf(mx8[a], s[a + 120]);
                 const float mx = fmaxf(fmaxf(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5])),
                                        fmaxf(mx8[6], mx8[7]));
-                const float m_new = fmaxf(m_ref, BIAS ? fmaf(mx, mul, add) : mx * sl2);
+                const float m_new = fmaxf(m_ref, BIAS ? fmaf(mx, sl2, add) : mx * sl2);
                 if (j == 0) {
                     m_ref = m_new;  // O holds nothing of this item yet
                 } else {
@@ -1083,7 +1151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (moving part of it to a polynomial on the FMA pipe measured slower: the
                 // softmax is bound by instruction issue).
                 const float neg = BIAS ? add - m_use : -m_use;
-                const uint64_t sl2x2 = f2_pack(mul, mul);
+                const uint64_t sl2x2 = f2_pack(sl2, sl2);
                 const uint64_t negm2 = f2_pack(neg, neg);
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};  // partial sums of the bf16 weights
 #pragma unroll
@@ -1441,7 +1509,7 @@ namespace {
 
 template <int HD, bool PREFIX, int CACHE = kCacheBf16, bool BIAS = false>
 cudaError_t launch_prefill_d(PrefillKernelParams &kp, const PrefillArgs &a, cudaStream_t stream) {
-    using L = Layout<HD>;
+    using L = Layout<HD, BIAS>;
     const int64_t slots = a.num_blocks * a.block_size;
     const int64_t q_stride = a.q_stride > 0 ? a.q_stride : static_cast<int64_t>(a.num_heads) * HD;
     const int64_t kv_stride = static_cast<int64_t>(a.num_kv_heads) * HD;
@@ -1458,6 +1526,17 @@ cudaError_t launch_prefill_d(PrefillKernelParams &kp, const PrefillArgs &a, cuda
                        a.num_kv_heads, static_cast<uint64_t>(slots), HD * eb,
                        (CACHE != kCachePacked ? kv_stride : kv ? a.v_stride : a.k_stride) * eb, FP8 ? HD : 64, 1, 16, FP8))
             return cudaErrorInvalidValue;
+    }
+    if (BIAS) {
+        // A tile's rows span 2 T tokens, its columns 128 keys; begun on a multiple of 4.  A head's step is
+        // such that the tokens and heads of a warp fall on different banks.
+        const int span = (2 * kp.tok_per_tile + BN - 1 + 3 + 3) & ~3;
+        int heads = 1;
+        while (heads < kp.group && heads < 8) heads *= 2;
+        int step = span;
+        while (heads > 1 && step % 32 != 32 / heads) step += 4;
+        kp.bias_span = static_cast<uint32_t>(kp.group * step) * 4 <= kWindowBytes ? span : 0;
+        kp.bias_step = step;
     }
     auto kern = prefill_kernel<HD, PREFIX, CACHE, BIAS>;
     static std::atomic<uint64_t> smem_set;

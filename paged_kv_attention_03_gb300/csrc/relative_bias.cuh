@@ -6,13 +6,26 @@
 // distances without clamping each one.
 #pragma once
 
+#include <math.h>
+
+#include "pa_common.cuh"
 #include "pa_internal.h"
 
 namespace pa {
 
-constexpr int kBiasPad = 256, kBiasTail = 128;
+// (Both cover a prefill item's tile: 256 tokens against 128 keys.)
+constexpr int kBiasPad = 384, kBiasTail = 392;
 
 __host__ __device__ inline int bias_stride(int last) { return (last + kBiasPad + kBiasTail + 3) & ~3; }
+
+// A bias in base-2 units.  What lies below -1e30 hides its keys as -inf does: a row that saw nothing else
+// would have a log-sum-exp whose last place is larger than any logit.
+__device__ __forceinline__ float bias_log2(float b) { return b < -1e30f ? -INFINITY : b * kLog2e; }
+
+// The form for the prefill kernel (relative): entries are what is left over bias_ref, which is the last
+// bucket's bias unless that is so large that the difference would lose the others' digits; a row's first
+// entry is the last bucket's bias itself.  Logits of far keys then need no change of their own.
+__device__ __forceinline__ float bias_ref(float far) { return fabsf(far) <= 64.f ? far : 0.f; }
 
 // Entry of distance 0 of a head's row.
 __device__ __forceinline__ const float *bias_row_of(const float *table, int head, int last) {

@@ -25,9 +25,9 @@ def test_buckets_of_the_common_sizes():
 
 @pytest.mark.parametrize("num_buckets,max_distance", [(2, 2), (3, 7), (8, 9), (32, 17), (32, 128), (33, 500), (128, 32768)])
 def test_the_table_knows_the_last_bucket(num_buckets, max_distance):
-    """The library's table has bytes for last + 384 entries a head, a multiple of 4: its `last` is the oracle's."""
+    """The library's table has bytes for last + 776 entries a head, a multiple of 4: its `last` is the oracle's."""
     last = relative.first_distances(num_buckets, max_distance)[-1]
-    row = (last + 384 + 3) // 4 * 4
+    row = (last + 776 + 3) // 4 * 4
     assert pa.pa_relative_bias_workspace_size(64, num_buckets, max_distance) == 64 * row * 4
     m = num_buckets // 2
     r = num_buckets - m
