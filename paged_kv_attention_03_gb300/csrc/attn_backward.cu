@@ -745,15 +745,19 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             float d_sum = 0.f;
             [[maybe_unused]] float d_far = 0.f, w_far = 0.f;  // sums of P dP and of P over the first n_far tiles
             [[maybe_unused]] const float *bias_row = nullptr;  // entry of distance 0
-            float far = -lse2;  // x = sl2 s + far, where the bias is that of the last bucket
+            // x = sl2 s + far where the bias is that of the last bucket, else sl2 s + (entry + near_add).
+            float far = -lse2;
+            [[maybe_unused]] float near_add = -lse2;
             if constexpr (BIAS) {
                 bias_row = bias_row_of(p.bias_table, head, last);
+                const float last_bias = __ldg(bias_row - kBiasPad);
+                far = last_bias - lse2;
+                near_add = bias_ref(last_bias) - lse2;
                 if (table_here) {
                     ok = wait_warp(bar(B_TABFULL + (items & 1)), (items >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
                     if (!ok) break;
                     bias_row = small + kSmallQ / 4 + (items & 1) * (kTableBytes / 4) + kNearPad;
                 }
-                far = bias_row[last] - lse2;
             }
             const uint64_t far2 = f2_pack(far, far);
             for (int j = 0; j < s.n_all; ++j, ++J) {
@@ -778,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 if (near) {
                     const float *bt = bias_row + d0;  // (-inf before distance 0)
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = fmaf(w[i >> 5][i & 31], sl2, bt[-i]) - lse2;
+                    for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = fmaf(w[i >> 5][i & 31], sl2, bt[-i]) + near_add;
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
@@ -957,7 +961,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
     const uint32_t sK = c.base + L::OFF_RES, sV = sK + L::TILE;
     auto sQ = [&](int st) -> uint32_t { return c.base + L::OFF_A + st * L::TILE; };
     auto sDo = [&](int st) -> uint32_t { return c.base + L::OFF_B + st * L::TILE; };
-    // Per stage: -lse2, -D and (BIAS) the last bucket's bias - lse2 of the tile's queries.
+    // Per stage and query of the tile: -lse2 (BIAS: plus what the table is relative to), -D and (BIAS) the
+    // last bucket's bias - lse2.
     auto stat = [&](int st) -> float * { return reinterpret_cast<float *>(c.sb + L::OFF_SMALL) + st * 384; };
     const int last = p.bias.last();
 
@@ -1005,15 +1010,18 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
                 ok = J < 2 || wait_warp(bar(B_AEMPTY + st), ((J >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs);
                 if (!ok) break;
                 load_tile<HD>(p.tmap_q, sQ(st), head, t.q_start, r, t.sq, land);
-                float far = 0.f;
-                if constexpr (BIAS) far = __ldg(bias_row_of(p.bias_table, head, last) + last);
+                float far = 0.f, ref = 0.f;
+                if constexpr (BIAS) {
+                    far = __ldg(bias_row_of(p.bias_table, head, last) - kBiasPad);
+                    ref = bias_ref(far);
+                }
                 const int64_t at = static_cast<int64_t>(head) * p.total_q + t.q_start + r;
 #pragma unroll
                 for (int x4 = 0; x4 < 4; ++x4) {
                     const int x = lane + 32 * x4;
                     const bool in = r + x < t.sq;
                     const float l2 = in ? p.lse2[at + x] : INFINITY;
-                    stat(st)[x] = -l2;
+                    stat(st)[x] = ref - l2;
                     stat(st)[128 + x] = in ? -p.delta[at + x] : 0.f;
                     if constexpr (BIAS) stat(st)[256 + x] = far - l2;
                 }

@@ -110,7 +110,7 @@ pa_status pa_varlen_attn(void *out, float *lse, const void *q, const void *k, co
     a.err = pa::device_error_word();
     if (bias) {
         a.bias_table = static_cast<float *>(workspace);
-        st = pa::cuda_status(pa::launch_bias_table(static_cast<float *>(workspace), num_heads, a.bias, true, s));
+        st = pa::cuda_status(pa::launch_bias_table(static_cast<float *>(workspace), num_heads, a.bias, s));
         if (st != PA_OK) return st;
     }
     return pa::cuda_status(pa::launch_packed_attn(a, out, lse, s));
@@ -165,7 +165,7 @@ pa_status pa_varlen_attn_backward(void *dq, void *dk, void *dv, float *dbias, in
     a.err = pa::device_error_word();
     if (bias) {
         a.bias_table = static_cast<float *>(workspace);
-        st = pa::cuda_status(pa::launch_bias_table(static_cast<float *>(workspace), num_heads, a.bias, false, s));
+        st = pa::cuda_status(pa::launch_bias_table(static_cast<float *>(workspace), num_heads, a.bias, s));
         if (st != PA_OK) return st;
     }
     g.out = out;
@@ -277,7 +277,7 @@ pa_status pa_varlen_prefill_bias(void *out, const void *q, const void *key, cons
     if (num_seqs == 0 || max_seqlen_q == 0) return PA_OK;
     // (The table serves the prefill kernel; single-row sequences alone go to the decode kernel.)
     if (!seq_lens || max_seqlen_q > 1) {
-        st = pa::cuda_status(pa::launch_bias_table(static_cast<float *>(workspace), num_heads, a.bias, true, s));
+        st = pa::cuda_status(pa::launch_bias_table(static_cast<float *>(workspace), num_heads, a.bias, s));
         if (st != PA_OK) return st;
     }
     a.bias_table = static_cast<float *>(workspace);

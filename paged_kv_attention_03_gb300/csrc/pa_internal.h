@@ -29,8 +29,7 @@ struct RelativeBias {
 bool plan_relative_bias(int num_buckets, int max_distance, RelativeBias *b);
 // The bias by distance in base-2 units, for every head: relative_bias.cuh.
 size_t bias_table_bytes(int num_heads, const RelativeBias &b);
-// (relative: the prefill kernel's form of it)
-cudaError_t launch_bias_table(float *table, int num_heads, const RelativeBias &b, bool relative, cudaStream_t stream);
+cudaError_t launch_bias_table(float *table, int num_heads, const RelativeBias &b, cudaStream_t stream);
 
 // ------------------------------------------------------------------ store ---
 struct StoreArgs {

@@ -1065,7 +1065,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                         for (int cc = 0; cc < BN / 32; ++cc) {
                             const int dc = d0 - cc * 32;
-                            if (__shfl_sync(0xffffffffu, dc, 31) < 0) break;  // (and later ones are future keys')
                             if (!all_chunks && __shfl_sync(0xffffffffu, dc, 0) - 31 >= p.bias_last) continue;
                             const float *bt = near + dc;
                             float v[32];
@@ -1073,6 +1072,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_wait_ld_regs(v);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) v[i] = fmaf(bt[-i], inv_sl2, v[i]);
+                            if (__shfl_sync(0xffffffffu, dc, 0) < 31) {  // (whatever a half tile's other columns hold)
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (i > dc) v[i] = -INFINITY;
+                            }
                             tmem_st_32x32b_x32(scol + cc * 32, v);
                         }
                         tmem_wait_st();
@@ -1095,7 +1099,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // dependent chain of 128 maxima would cost ~4 cycles per element).
                 // Edge tiles: the causal bound and the window's lower bound are masked
                 // separately, so a diagonal tile pays for one compare per element.
-                if (key0 + BN - 1 > pos) {
+                if (!BIAS && key0 + BN - 1 > pos) {  // (near tiles hide future keys with their bias)
                     const int last = pos - key0;  // columns past it lie in the future
 #pragma unroll
                     for (int i = 0; i < BN; ++i)

@@ -41,7 +41,7 @@ bool reaches(int n, int m, int d, int r, int j) {
 
 // One thread an entry; a bucket's first distances are read through the kernel's parameters.
 __global__ void __launch_bounds__(128)
-    bias_table_kernel(float *__restrict__ table, const __grid_constant__ RelativeBias b, int num_heads, int relative) {
+    bias_table_kernel(float *__restrict__ table, const __grid_constant__ RelativeBias b, int num_heads) {
     const int stride = bias_stride(b.last());
     const int i = blockIdx.x * 128 + threadIdx.x;
     if (i >= stride) return;
@@ -50,9 +50,7 @@ __global__ void __launch_bounds__(128)
     for (int h = blockIdx.y; h < num_heads; h += gridDim.y) {
         const float far = bias_log2(b.bias[static_cast<int64_t>(b.num_buckets - 1) * num_heads + h]);
         const float v = bias_log2(b.bias[static_cast<int64_t>(k) * num_heads + h]);
-        table[static_cast<int64_t>(h) * stride + i] = relative && i == 0 ? far
-                                                      : i < kBiasPad     ? -INFINITY
-                                                                         : v - (relative ? bias_ref(far) : 0.f);
+        table[static_cast<int64_t>(h) * stride + i] = i == 0 ? far : i < kBiasPad ? -INFINITY : v - bias_ref(far);
     }
 }
 
@@ -83,9 +81,9 @@ size_t bias_table_bytes(int num_heads, const RelativeBias &b) {
     return (static_cast<size_t>(num_heads) * bias_stride(b.last()) * sizeof(float) + 255) / 256 * 256;
 }
 
-cudaError_t launch_bias_table(float *table, int num_heads, const RelativeBias &b, bool relative, cudaStream_t stream) {
+cudaError_t launch_bias_table(float *table, int num_heads, const RelativeBias &b, cudaStream_t stream) {
     const dim3 grid((bias_stride(b.last()) + 127) / 128, num_heads < 64 ? num_heads : 64);
-    bias_table_kernel<<<grid, 128, 0, stream>>>(table, b, num_heads, relative ? 1 : 0);
+    bias_table_kernel<<<grid, 128, 0, stream>>>(table, b, num_heads);
     return cudaGetLastError();
 }
 

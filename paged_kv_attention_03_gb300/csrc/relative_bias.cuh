@@ -1,9 +1,9 @@
 // relative_bias.cuh - the table of a learned relative position bias by distance.
 //
-// Row h holds head h's bias times log2(e) for the distances -kBiasPad .. last + kBiasTail - 1 (last:
-// the first distance of the last bucket).  Entries below 0 are -inf, which hides future keys, and those
-// from last on are all the last bucket's, so that a kernel may read whole runs around a tile's
-// distances without clamping each one.
+// Row h holds head h's bias in base-2 units (times log2 e) for the distances 0 .. last + kBiasTail - 1
+// (last: the first distance of the last bucket), less bias_ref.  Entries before distance 0 are -inf, which
+// hides future keys; those from last on are all the last bucket's.  So a kernel may read whole runs
+// around a tile's distances without clamping each one.
 #pragma once
 
 #include <math.h>
@@ -14,7 +14,7 @@
 namespace pa {
 
 // (Both cover a prefill item's tile: 256 tokens against 128 keys.)
-constexpr int kBiasPad = 384, kBiasTail = 392;
+constexpr int kBiasPad = 384, kBiasTail = 392;  // (entries before distance 0, and from last on)
 
 __host__ __device__ inline int bias_stride(int last) { return (last + kBiasPad + kBiasTail + 3) & ~3; }
 
@@ -22,9 +22,9 @@ __host__ __device__ inline int bias_stride(int last) { return (last + kBiasPad +
 // would have a log-sum-exp whose last place is larger than any logit.
 __device__ __forceinline__ float bias_log2(float b) { return b < -1e30f ? -INFINITY : b * kLog2e; }
 
-// The form for the prefill kernel (relative): entries are what is left over bias_ref, which is the last
-// bucket's bias unless that is so large that the difference would lose the others' digits; a row's first
-// entry is the last bucket's bias itself.  Logits of far keys then need no change of their own.
+// Entries are what is left over bias_ref, which is the last bucket's bias unless that is so large that the
+// difference would lose the others' digits; then far keys' logits need no change of their own.  A row's
+// first entry is the last bucket's bias itself.
 __device__ __forceinline__ float bias_ref(float far) { return fabsf(far) <= 64.f ? far : 0.f; }
 
 // Entry of distance 0 of a head's row.
