@@ -7,17 +7,17 @@
 //     dV = P^T dout,   dQ = scale dS K,   dK = scale dS^T Q,   dbias_b = sum of dS over bucket b.
 // D_i also equals dout_i out_i, but out is bf16 there: good enough inside dQ, whose terms are rounded
 // to bf16 anyway, unless a row's dS nearly cancel, as they do in rows of few keys; and not for sums
-// of dS.  So the dQ kernel starts from dout_i out_i, goes twice over the tiles that need the sum
-// itself, first for D alone, and leaves D in fp32 for dK.
+// of dS.  So the dQ kernel starts from dout_i out_i, visits the tiles that need the sum itself once
+// for D and once with it, and leaves D in fp32 for dK.
 //
 // Two kernels share the work, each with its accumulators in tensor memory and no atomics, so equal
 // calls give equal bits:
 //  * grad_q_kernel: 128 queries of one head against their keys in turn (3 products a tile).  dbias: the
 //    tiles whose distances all belong to the last bucket add sum_j P dP - D sum_j P to it; the others,
-//    the nearest ones, come last, once for D and once more with it, and their dS are summed along
-//    diagonals into buckets;
+//    the nearest ones, come last, and their dS, with the exact D, are summed along diagonals into
+//    buckets;
 //  * grad_kv_kernel: 128 keys of one kv head against the queries of every head that shares it
-//    (4 products a tile), so the sum over the heads happens in the accumulator;
+//    (4 products a tile), so the sum over the heads happens in the accumulator.
 // The products count 7 for the 5 of the formula (S and dP are formed twice); dQ added up across
 // the CTAs of one pass over the keys would need atomics, whose order changes the result.
 //
@@ -27,8 +27,16 @@
 //
 // Roles in a CTA: warps 0-7 are two warpgroups of element-wise work, each on 64 of a tile's 128
 // columns (a thread owns a TMEM lane, i.e. an accumulator row); warp 8 loads tiles by TMA, warp 9
-// issues the products.  P and dS go back to tensor memory as bf16, over the fp32 tile they came
-// from, and are the first operand of the next product from there.
+// (in dQ with warp 10) issues the products.  P and dS go back to tensor memory as bf16, over the fp32
+// tile they came from, and are the first operand of the next product from there.
+//
+// Measured (packed sequences, 32/8 heads of 128; the products of each kernel over its time):
+//  * two of 6000-8192 tokens, no bias: dQ 665 us (1.69 PFLOP/s of three products, 0.87 of the bf16
+//    peak), dK/dV 895 us (1.68): products nearly back to back; the rest are the waits between them;
+//  * sixteen of 128-2048 tokens, 32 buckets to 128: dQ 379 us (0.63), dK/dV 286 us (1.11): a third of
+//    dQ's steps are near tiles, whose bias and diagonal sums (64 shuffles an element row, two cycles
+//    each) take 2100 cycles beside 1600 of the softmax; loops grow past the instruction cache when
+//    such code is unrolled further.
 #include <cuda.h>
 
 #include <atomic>
@@ -1106,140 +1114,143 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
         KTile next{};
         if (more) next = load_entry(p.k_list, e);
         for (int k = 0; ok && more; ++k) {
-        const KTile t = next;
-        const int head0 = kvh * p.group;
-        const int rows = min(t.left, BM), key = t.key + row;
-        __nv_bfloat16 *dk = p.dk + static_cast<int64_t>(t.row) * p.dk_stride + kvh * HD;
-        __nv_bfloat16 *dv = p.dv + static_cast<int64_t>(t.row) * p.dv_stride + kvh * HD;
-        more = item_of(k + 1, count, p.num_kv_heads, e, kvh);
-        if (more) next = load_entry(p.k_list, e);
-        if (t.n == 0) {  // no row sees these keys
-            zero_rows<HD>(dk, p.dk_stride, rows);
-            zero_rows<HD>(dv, p.dv_stride, rows);
-            continue;
-        }
-        const int pos_first = t.off + first_query(t) + 64 * wg;  // of this warpgroup's first query
-        [[maybe_unused]] const float *bias_row = nullptr;  // entry of distance 0 of the item's first head
-        [[maybe_unused]] int bias_step = bias_stride(last);  // to the next head's
-        if constexpr (BIAS) {
-            bias_row = bias_row_of(p.bias_table, head0, last);
-            if (table_here) {
-                ok = wait_warp(bar(B_TABFULL + (items & 1)), (items >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
-                if (!ok) break;
-                bias_row = reinterpret_cast<const float *>(c.sb + L::OFF_SMALL + kSmallKv + (items & 1) * kTableBytes) + kNearPad;
-                bias_step = head_bytes / 4;
+            const KTile t = next;
+            const int head0 = kvh * p.group;
+            const int rows = min(t.left, BM), key = t.key + row;
+            __nv_bfloat16 *dk = p.dk + static_cast<int64_t>(t.row) * p.dk_stride + kvh * HD;
+            __nv_bfloat16 *dv = p.dv + static_cast<int64_t>(t.row) * p.dv_stride + kvh * HD;
+            more = item_of(k + 1, count, p.num_kv_heads, e, kvh);
+            if (more) next = load_entry(p.k_list, e);
+            if (t.n == 0) {  // no row sees these keys
+                zero_rows<HD>(dk, p.dk_stride, rows);
+                zero_rows<HD>(dv, p.dv_stride, rows);
+                continue;
             }
-        }
-        for (int g = 0; ok && g < p.group; ++g)
-        for (int q = 0; q < t.n; ++q, ++J) {
-            const uint32_t st = J & 1;
-            const int pos0 = pos_first + q * BN;
-            if (!wait_warp(bar(B_AFULL + st), (J >> 1) & 1, c.abort_flag, p.err, kTimeoutNs) ||
-                !wait_warp(bar(B_SFULL), J & 1, c.abort_flag, p.err, kTimeoutNs)) {
-                ok = false;
-                break;
+            const int pos_first = t.off + first_query(t) + 64 * wg;  // of this warpgroup's first query
+            [[maybe_unused]] const float *bias_row = nullptr;  // entry of distance 0 of the item's first head
+            [[maybe_unused]] int bias_step = bias_stride(last);  // to the next head's
+            if constexpr (BIAS) {
+                bias_row = bias_row_of(p.bias_table, head0, last);
+                if (table_here) {
+                    ok = wait_warp(bar(B_TABFULL + (items & 1)), (items >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
+                    if (!ok) break;
+                    bias_row = reinterpret_cast<const float *>(c.sb + L::OFF_SMALL + kSmallKv + (items & 1) * kTableBytes) + kNearPad;
+                    bias_step = head_bytes / 4;
+                }
             }
+            for (int g = 0, q = 0; g < p.group; ++J) {
+                const uint32_t st = J & 1;
+                const int pos0 = pos_first + q * BN;
+                if (!wait_warp(bar(B_AFULL + st), (J >> 1) & 1, c.abort_flag, p.err, kTimeoutNs) ||
+                    !wait_warp(bar(B_SFULL), J & 1, c.abort_flag, p.err, kTimeoutNs)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float w[2][32];
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) tmem_ld_32x32b_x32(sc + 32u * cc, w[cc]);
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) tmem_wait_ld_regs(w[cc]);
+                const int d0 = pos0 - key;  // distance from the first query
+                // (Lane 31 has the nearest key.)
+                const bool near = BIAS && __shfl_sync(0xffffffffu, d0, 31) < last;
+                if (near) {
+                    const float *bt = bias_row + g * bias_step + d0;  // (-inf before distance 0)
+                    const float4 *nl = reinterpret_cast<const float4 *>(stat(st) + 64 * wg);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        const float4 l = nl[x];
+                        float *v = &w[x >> 3][4 * (x & 7)];
+                        v[0] = fmaf(v[0], sl2, bt[4 * x]) + l.x;
+                        v[1] = fmaf(v[1], sl2, bt[4 * x + 1]) + l.y;
+                        v[2] = fmaf(v[2], sl2, bt[4 * x + 2]) + l.z;
+                        v[3] = fmaf(v[3], sl2, bt[4 * x + 3]) + l.w;
+                    }
+                } else {
+                    const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(stat(st) + (BIAS ? 256 : 0) + 64 * wg);
+                    const uint64_t sl2x2 = f2_pack(sl2, sl2);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        const ulonglong2 l = nl[x];
+                        float *v = &w[x >> 3][4 * (x & 7)];
+                        f2_unpack(f2_fma(f2_pack(v[0], v[1]), sl2x2, l.x), v[0], v[1]);
+                        f2_unpack(f2_fma(f2_pack(v[2], v[3]), sl2x2, l.y), v[2], v[3]);
+                    }
+                }
+                if (!BIAS && d0 < 0) {  // (the table hides future keys)
+#pragma unroll
+                    for (int x = 0; x < 64; ++x)
+                        if (x < -d0) w[x >> 5][x & 31] = -INFINITY;
+                }
+                if (p.window > 0 && d0 + 63 >= p.window) {
+                    const int end = p.window - d0;  // queries from here on are too far
+#pragma unroll
+                    for (int x = 0; x < 64; ++x)
+                        if (x >= end) w[x >> 5][x & 31] = -INFINITY;
+                }
+                uint32_t pk[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) {
+                    float &a = w[x >> 4][2 * (x & 15)], &b = w[x >> 4][2 * (x & 15) + 1];
+                    a = ex2_approx(a);
+                    b = ex2_approx(b);
+                    pk[x] = pack_bf16x2(a, b);
+                }
+                tmem_st_32x32b_x32_u(sc, pk);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_PFULL));
+                if (!wait_warp(bar(B_DPFULL), J & 1, c.abort_flag, p.err, kTimeoutNs)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const ulonglong2 *dl = reinterpret_cast<const ulonglong2 *>(stat(st) + 128 + 64 * wg);
+#pragma unroll
+                for (int cc = 0; cc < 2; ++cc) {
+                    float d[32];
+                    tmem_ld_32x32b_x32(dp + 32u * cc, d);
+                    tmem_wait_ld_regs(d);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const ulonglong2 l = dl[8 * cc + x];
+                        float *v = &d[4 * x];
+                        const float *pw = &w[cc][4 * x];
+                        f2_unpack(f2_mul(f2_pack(pw[0], pw[1]), f2_add(f2_pack(v[0], v[1]), l.x)), v[0], v[1]);
+                        f2_unpack(f2_mul(f2_pack(pw[2], pw[3]), f2_add(f2_pack(v[2], v[3]), l.y)), v[2], v[3]);
+                        pk[16 * cc + 2 * x] = pack_bf16x2(v[0], v[1]);
+                        pk[16 * cc + 2 * x + 1] = pack_bf16x2(v[2], v[3]);
+                    }
+                }
+                tmem_st_32x32b_x32_u(dp, pk);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_DSFULL));
+                if (++q == t.n) {
+                    q = 0;
+                    ++g;
+                }
+            }
+            if (BIAS && ok) {
+                __syncwarp();
+                if (table_here && lane == 0) mbar_arrive(bar(B_TABFREE + (items & 1)));
+            }
+            ok = ok && wait_warp(bar(B_DONE), items & 1, c.abort_flag, p.err, kTimeoutNs);
+            if (!ok) break;
             tc_fence_after();
-            float w[2][32];
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc) tmem_ld_32x32b_x32(sc + 32u * cc, w[cc]);
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc) tmem_wait_ld_regs(w[cc]);
-            const int d0 = pos0 - key;  // distance from the first query
-            // (Lane 31 has the nearest key.)
-            const bool near = BIAS && __shfl_sync(0xffffffffu, d0, 31) < last;
-            if (near) {
-                const float *bt = bias_row + g * bias_step + d0;  // (-inf before distance 0)
-                const float4 *nl = reinterpret_cast<const float4 *>(stat(st) + 64 * wg);
-#pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const float4 l = nl[x];
-                    float *v = &w[x >> 3][4 * (x & 7)];
-                    v[0] = fmaf(v[0], sl2, bt[4 * x]) + l.x;
-                    v[1] = fmaf(v[1], sl2, bt[4 * x + 1]) + l.y;
-                    v[2] = fmaf(v[2], sl2, bt[4 * x + 2]) + l.z;
-                    v[3] = fmaf(v[3], sl2, bt[4 * x + 3]) + l.w;
-                }
-            } else {
-                const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(stat(st) + (BIAS ? 256 : 0) + 64 * wg);
-                const uint64_t sl2x2 = f2_pack(sl2, sl2);
-#pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    const ulonglong2 l = nl[x];
-                    float *v = &w[x >> 3][4 * (x & 7)];
-                    f2_unpack(f2_fma(f2_pack(v[0], v[1]), sl2x2, l.x), v[0], v[1]);
-                    f2_unpack(f2_fma(f2_pack(v[2], v[3]), sl2x2, l.y), v[2], v[3]);
-                }
-            }
-            if (!BIAS && d0 < 0) {  // (the table hides future keys)
-#pragma unroll
-                for (int x = 0; x < 64; ++x)
-                    if (x < -d0) w[x >> 5][x & 31] = -INFINITY;
-            }
-            if (p.window > 0 && d0 + 63 >= p.window) {
-                const int end = p.window - d0;  // queries from here on are too far
-#pragma unroll
-                for (int x = 0; x < 64; ++x)
-                    if (x >= end) w[x >> 5][x & 31] = -INFINITY;
-            }
-            uint32_t pk[32];
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-                float &a = w[x >> 4][2 * (x & 15)], &b = w[x >> 4][2 * (x & 15) + 1];
-                a = ex2_approx(a);
-                b = ex2_approx(b);
-                pk[x] = pack_bf16x2(a, b);
-            }
-            tmem_st_32x32b_x32_u(sc, pk);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_PFULL));
-            if (!wait_warp(bar(B_DPFULL), J & 1, c.abort_flag, p.err, kTimeoutNs)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            const ulonglong2 *dl = reinterpret_cast<const ulonglong2 *>(stat(st) + 128 + 64 * wg);
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-                float d[32];
-                tmem_ld_32x32b_x32(dp + 32u * cc, d);
-                tmem_wait_ld_regs(d);
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    const ulonglong2 l = dl[8 * cc + x];
-                    float *v = &d[4 * x];
-                    const float *pw = &w[cc][4 * x];
-                    f2_unpack(f2_mul(f2_pack(pw[0], pw[1]), f2_add(f2_pack(v[0], v[1]), l.x)), v[0], v[1]);
-                    f2_unpack(f2_mul(f2_pack(pw[2], pw[3]), f2_add(f2_pack(v[2], v[3]), l.y)), v[2], v[3]);
-                    pk[16 * cc + 2 * x] = pack_bf16x2(v[0], v[1]);
-                    pk[16 * cc + 2 * x + 1] = pack_bf16x2(v[2], v[3]);
-                }
-            }
-            tmem_st_32x32b_x32_u(dp, pk);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_DSFULL));
-        }
-        if (BIAS && ok) {
-            __syncwarp();
-            if (table_here && lane == 0) mbar_arrive(bar(B_TABFREE + (items & 1)));
-        }
-        ok = ok && wait_warp(bar(B_DONE), items & 1, c.abort_flag, p.err, kTimeoutNs);
-        if (!ok) break;
-        tc_fence_after();
-        const int64_t stride = wg ? p.dk_stride : p.dv_stride;
-        __nv_bfloat16 *dst = (wg ? dk : dv) + static_cast<int64_t>(row) * stride;
-        const bool v8 = aligned32(wg ? p.dk : p.dv, stride);
+            const int64_t stride = wg ? p.dk_stride : p.dv_stride;
+            __nv_bfloat16 *dst = (wg ? dk : dv) + static_cast<int64_t>(row) * stride;
+            const bool v8 = aligned32(wg ? p.dk : p.dv, stride);
 #pragma unroll 1
-        for (int cc = 0; cc < HD / 32; ++cc)
-            store_chunk(c.tmem + t_lane + (wg ? kDk : kDv) + cc * 32, wg ? p.scale : 1.f, dst + cc * 32, row < rows, v8);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_ACCFREE));
-        ++items;
+            for (int cc = 0; cc < HD / 32; ++cc)
+                store_chunk(c.tmem + t_lane + (wg ? kDk : kDv) + cc * 32, wg ? p.scale : 1.f, dst + cc * 32, row < rows, v8);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_ACCFREE));
+            ++items;
         }
     }
     teardown(c);

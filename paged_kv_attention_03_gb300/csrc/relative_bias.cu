@@ -8,8 +8,6 @@
 // in whole numbers.
 #include <math.h>
 
-#include <vector>
-
 #include "pa_common.cuh"
 #include "relative_bias.cuh"
 
@@ -17,25 +15,30 @@ namespace pa {
 
 namespace {
 
-// x *= f, least significant word first.
-void multiply(std::vector<uint32_t> &x, uint32_t f) {
-    uint64_t carry = 0;
-    for (uint32_t &w : x) {
-        carry += static_cast<uint64_t>(w) * f;
-        w = static_cast<uint32_t>(carry);
-        carry >>= 32;
+// A whole number below 2^1152, least significant word first: n^r for distances below 2^16 and at most 64
+// factors.
+struct Whole {
+    uint32_t w[36] = {1u};
+    void multiply(uint32_t f) {
+        uint64_t carry = 0;
+        for (uint32_t &x : w) {
+            carry += static_cast<uint64_t>(x) * f;
+            x = static_cast<uint32_t>(carry);
+            carry >>= 32;
+        }
     }
-    if (carry != 0) x.push_back(static_cast<uint32_t>(carry));
-}
+};
+static_assert(kMaxBuckets - kMaxBuckets / 2 <= 64 && kMaxBiasDistance < 1 << 16, "powers fit in a Whole");
 
 // n^r >= m^(r - j) d^j
 bool reaches(int n, int m, int d, int r, int j) {
-    std::vector<uint32_t> a{1}, b{1};
-    for (int i = 0; i < r; ++i) multiply(a, n);
-    for (int i = 0; i < r; ++i) multiply(b, i < j ? d : m);
-    if (a.size() != b.size()) return a.size() > b.size();
-    for (size_t i = a.size(); i-- > 0;)
-        if (a[i] != b[i]) return a[i] > b[i];
+    Whole a, b;
+    for (int i = 0; i < r; ++i) {
+        a.multiply(n);
+        b.multiply(i < j ? d : m);
+    }
+    for (int i = 35; i >= 0; --i)
+        if (a.w[i] != b.w[i]) return a.w[i] > b.w[i];
     return true;
 }
 

@@ -69,7 +69,7 @@ def within(got, want, tol, what):
     got = f64(got)
     fine = np.isfinite(want)
     np.testing.assert_array_equal(np.where(fine, 0.0, want), np.where(fine, 0.0, np.where(np.isnan(want), np.nan, got)), err_msg=what)
-    off = np.abs(got - want)[fine] - tol[fine] - 2.0 ** -96
+    off = np.abs(got[fine] - want[fine]) - tol[fine] - 2.0 ** -96
     assert not np.isnan(off).any() and off.max(initial=-1.0) <= 0.0, f"{what}: {off.max()} beyond the bound"
 
 
@@ -134,6 +134,51 @@ def test_many_tiles_a_block(heads, hkv, dim, window, buckets, distance):
         assert (a is None and b is None) or torch.equal(a, b)
 
 
+def test_thousands_of_short_sequences():
+    """More sequences than the list's block takes in one round; most of them empty or of a token or two."""
+    g = np.random.default_rng(8)
+    sq = g.integers(0, 4, 5000)
+    sk = np.maximum(sq + g.integers(-1, 3, 5000), 0)
+    c = Case(sq.tolist(), sk.tolist(), 2, 1, 64, 0, 8, 9)
+    out, lse, grads = both(c)
+    check(c, out, lse, grads)
+
+
+def test_rows_far_apart():
+    """Rows of q, k, v and of the gradients so far apart that offsets pass 2^32 bytes and 2^31 elements."""
+    heads, hkv, d, step = 4, 2, 64, 1 << 23
+    c = Case([200, 77], [200, 77], heads, hkv, d, 0, 32, 128)
+    out, lse, grads = both(c)
+    base = torch.empty(277 * step, dtype=torch.bfloat16, device="cuda").view(277, step)
+    split = lambda t: (t[:, : heads * d].view(-1, heads, d), t[:, heads * d:(heads + hkv) * d].view(-1, hkv, d),  # noqa: E731
+                       t[:, (heads + hkv) * d:(heads + 2 * hkv) * d].view(-1, hkv, d))
+    wide = split(base)
+    for mine, theirs in zip(wide, (c.q, c.k, c.v)):
+        mine.copy_(theirs)
+    c.q, c.k, c.v = wide
+    out2, lse2 = c.forward()
+    dq, dk, dv = split(base[:, step // 2:])
+    grads2 = c.backward(out2, lse2, dq=dq, dk=dk, dv=dv)
+    for a, b in zip((out, lse, *grads), (out2, lse2, *grads2)):
+        assert torch.equal(a, b)
+
+
+def test_sequences_that_begin_behind_row_0():
+    """Rows before the first sequence are left as they were too."""
+    c = Case([50, 90], [70, 90], 4, 2, 64, 0, 16, 64)
+    want = both(c)
+    pad = lambda t: torch.cat([torch.full_like(t[:13], float("nan")), t])  # noqa: E731
+    moved = Case([50, 90], [70, 90], 4, 2, 64, 0, 16, 64)
+    moved.q, moved.k, moved.v, moved.dout = pad(c.q), pad(c.k), pad(c.v), pad(c.dout)
+    moved.cu_q, moved.cu_k = c.cu_q + 13, c.cu_k + 13
+    fill = lambda t: torch.full_like(t, 7.0)  # noqa: E731
+    out, lse = moved.forward(out=fill(moved.q), lse=torch.full(moved.q.shape[:2], 7.0, device="cuda"))
+    dq, dk, dv, dbias = moved.backward(out, lse, dq=fill(moved.q), dk=fill(moved.k), dv=fill(moved.v))
+    for got, ref in zip((out, lse, dq, dk, dv), (want[0], want[1], *want[2])):
+        assert (got[:13] == 7.0).all() and torch.equal(got[13:], ref)
+    assert torch.equal(dbias, want[2][3])
+
+
 @pytest.mark.parametrize("heads,hkv", [(64, 1), (32, 2), (33, 1), (3, 3), (128, 2)])
 def test_head_layouts(heads, hkv):
     c = Case([70, 9], [70, 30], heads, hkv, 128, 0, 32, 128)
@@ -173,24 +218,24 @@ def test_the_bias_gradient_keeps_fp32():
     assert np.linalg.norm(f64(grads[3]) - want) <= 1e-5 * np.linalg.norm(want)
 
 
-@pytest.mark.parametrize("how", ["minus infinity", "lowest", "large", "all hidden"])
+@pytest.mark.parametrize("how", ["minus infinity", "lowest", "large", "large and far", "all hidden"])
 def test_bias_values(how):
     c = Case([200, 30], [260, 30], 4, 2, 64, 0, 16, 64)
     if how == "large":
         c.bias *= 40.0
+    elif how == "large and far":  # the last bucket's far beyond the others'
+        c.bias[-1] = torch.tensor([-9000.0, 700.0, -65.0, 63.0])
     elif how == "all hidden":
         c.bias[:, 1] = float("-inf")
         c.bias[0, 2] = float("-inf")
     else:
-        c.bias[::3] = float("-inf") if how == "minus infinity" else torch.finfo(torch.float32).min / 2
+        c.bias[::3] = float("-inf") if how == "minus infinity" else torch.finfo(torch.float32).min
     out, lse, grads = both(c)
-    if how == "lowest":  # below every other logit: as if hidden, and an own bucket's rows aside
+    if how == "lowest":  # hides keys as -inf does
         hidden = Case([200, 30], [260, 30], 4, 2, 64, 0, 16, 64)
         hidden.bias[::3] = float("-inf")
-        # (rows that see a single key, in bucket 0, have it)
-        want = hidden.forward()[0]
-        rows = torch.arange(230, device="cuda") != 200
-        assert torch.equal(out[rows], want[rows])
+        for a, b in zip((out, lse, *grads), (lambda r: (r[0], r[1], *r[2]))(both(hidden))):
+            assert torch.equal(a, b)
         return
     if how == "all hidden":
         assert (out[:, 1] == 0).all() and torch.isneginf(lse[:, 1]).all()
@@ -382,7 +427,7 @@ def paged_tolerance(c, r):
     return (U + 2 * e) * r["out_abs"] + 2 * U * np.abs(r["out"])
 
 
-@pytest.mark.parametrize("heads,hkv,dim,block", [(8, 2, 64, 16), (32, 8, 128, 16), (5, 1, 128, 64), (32, 2, 64, 32), (40, 1, 128, 16)])
+@pytest.mark.parametrize("heads,hkv,dim,block", [(8, 2, 64, 16), (32, 8, 128, 16), (5, 1, 128, 64), (32, 2, 64, 4), (40, 1, 128, 16)])
 @pytest.mark.parametrize("window,buckets,distance", [(0, 32, 128), (0, 64, 2000), (90, 8, 300), (0, 2, 2)])
 @pytest.mark.parametrize("splits", [0, 1, 3])
 def test_decode(heads, hkv, dim, block, window, buckets, distance, splits):

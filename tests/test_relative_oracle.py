@@ -121,7 +121,7 @@ def test_paged_refusals():
         for bad in (dict(bias=None), dict(nb=0), dict(md=16), dict(scale=0.0), dict(H=9), dict(q=None), dict(key=FAKE), dict(out=MISALIGNED),
                     dict(blocks=-1)):
             assert call(**bad) == INVALID, bad
-        for bad in (dict(nb=200, md=1000), dict(md=40000), dict(D=96), dict(H=130), dict(bs=24)):
+        for bad in (dict(nb=200, md=1000), dict(md=40000), dict(scale=1e-21), dict(D=96), dict(H=130), dict(bs=24)):
             assert call(**bad) == UNSUPPORTED, bad
     assert decode(splits=4, most=4096) == INVALID  # needs a workspace
     assert prefill(ws=None) == INVALID and prefill(ws_bytes=100) == INVALID and prefill(ws=FAKE + 16) == INVALID
