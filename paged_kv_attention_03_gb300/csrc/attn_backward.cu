@@ -139,7 +139,7 @@ __device__ __forceinline__ Tile load_entry(const Tile *list, int i) {
 // Shared memory: two resident tiles (Q and dout, or K and V), rings of the tiles that pass by (K
 // and V, or Q and dout), small arrays, barriers.  K outlives V by the time from dP to dQ, so it has
 // three stages there.  With a bias the element-wise work is what bounds dQ, V's second stage gives
-// nothing (train varlen 414 us with and without it), and its place holds the bias of two items' heads.
+// nothing (16 sequences of 128-2048 tokens, 32/8 heads: 414 us with and without it), and its place holds the bias of two items' heads.
 template <int HD, int STAGES_A, int STAGES_B, uint32_t SMALL_BYTES>
 struct Layout {
     static constexpr int NHALF = HD / 64;
@@ -162,7 +162,7 @@ constexpr uint32_t kTableBytes = 15360;
 // What is kept of a head's row: distances -kNearPad .. last + 127.
 constexpr int kNearPad = 256;
 __host__ __device__ constexpr int near_entries(int last) { return (last + kNearPad + 128 + 3) & ~3; }
-constexpr uint32_t kSmallQ = 1024 + 528;
+constexpr uint32_t kSmallQ = 2048 + 528;  // two items' halves of D, the buckets' first distances
 template <int HD, bool BIAS>
 using LayoutQ = Layout<HD, 3, BIAS ? 1 : 2, kSmallQ + (BIAS ? 2 * kTableBytes : 0u)>;
 constexpr uint32_t kSmallKv = 2u * 3 * 512;
@@ -368,11 +368,13 @@ __device__ __forceinline__ void teardown(const Cta &c) {
 // ------------------------------------------------- lists and rows' statistics ---
 // The tiles of all sequences, sorted by their number of steps (the longest first), by one block.  A
 // warp takes 32 sequences at a time, a lane a tile; the order of equal tiles is left to chance (no
-// result depends on it).  Bad sequences are flagged and have no tiles.
+// result depends on it).  Bad sequences are flagged and have no tiles; offsets that go back and forth can
+// give sequences that share rows more tiles than the lists hold, and then none has any.
 struct PlanParams {
     const int32_t *cu_q;
     const int32_t *cu_k;
     int num_seqs, total_q, total_k, max_q, max_k, window;
+    int most[2];  // entries that the lists have room for
     int *counts;
     QTile *q_list;
     KTile *k_list;
@@ -471,6 +473,7 @@ __device__ __forceinline__ int exclusive_sums(int *x, int n) {
 __device__ __forceinline__ void plan_lists(const PlanParams &p) {
     __shared__ int bins[kPlanBins];
     __shared__ int before[65536 / 32];  // tiles of the chunks of 32 sequences before
+    __shared__ bool fits;
     const int chunks = (p.num_seqs + 31) / 32;
     for (int keys = 0; keys < 2; ++keys) {
         auto bin = [](int n) { return kPlanBins - 1 - min(n, kPlanBins - 1); };
@@ -486,9 +489,13 @@ __device__ __forceinline__ void plan_lists(const PlanParams &p) {
         if (threadIdx.x < 32) {
             const int count = exclusive_sums(bins, kPlanBins);
             exclusive_sums(before, chunks);
-            if (threadIdx.x == 0) p.counts[keys] = count;
+            if (threadIdx.x == 0) {
+                fits = count <= p.most[keys];
+                p.counts[keys] = fits ? count : 0;
+            }
         }
         __syncthreads();
+        if (!fits) continue;
         plan_tiles(
             p, keys, false,
             [&](int chunk, int i, int t, int a, int b, int c, int d) {
@@ -566,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
     constexpr uint32_t kDp = 128, kDq = 384;
     if constexpr (BIAS) {  // the buckets' first distances, behind the rows' sums
         extern __shared__ __align__(1024) uint8_t smem_raw[];
-        int *first = reinterpret_cast<int *>(smem_raw + L::OFF_SMALL + 1024);
+        int *first = reinterpret_cast<int *>(smem_raw + L::OFF_SMALL + 2048);
         for (int i = threadIdx.x; i <= p.bias.num_buckets; i += kThreads) first[i] = p.bias.first[i];
     }
     const Cta c = setup<L>();
@@ -712,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
         const uint64_t sl2x2 = f2_pack(sl2, sl2);
         // The rows' half sums, and the buckets' first distances.
         float *small = reinterpret_cast<float *>(c.sb + L::OFF_SMALL);
-        [[maybe_unused]] const int *first = reinterpret_cast<const int *>(small + 256);
+        [[maybe_unused]] const int *first = reinterpret_cast<const int *>(small + 512);
         const bool v8 = aligned32(p.dq, p.dq_stride);
         uint32_t items = 0, J = 0;
         bool ok = true;
@@ -824,11 +831,13 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 tc_fence_after();
                 // D of the row: this warpgroup's half and the other's.
                 auto exchange = [&]() -> bool {
-                    small[128 * wg + row] = d_sum;
+                    // (Two places: a warpgroup may be an item ahead of the other's reading.)
+                    float *sums = small + 256 * (items & 1) + row;
+                    sums[128 * wg] = d_sum;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_SUMS));
                     if (!wait_warp(bar(B_SUMS), items & 1, c.abort_flag, p.err, kTimeoutNs)) return false;
-                    delta = small[row] + small[128 + row];
+                    delta = sums[0] + sums[128];
                     if (wg == 0 && row < rows) p.delta[stat_row + row] = delta;
                     return true;
                 };
@@ -1381,6 +1390,8 @@ cudaError_t launch_packed_attn_backward(const PackedGradArgs &g, cudaStream_t st
     plan.max_q = a.max_seqlen_q;
     plan.max_k = a.max_seqlen_k;
     plan.window = a.sliding_window;
+    plan.most[0] = static_cast<int>(most_tiles(a.total_q, a.num_seqs));
+    plan.most[1] = static_cast<int>(most_tiles(a.total_k, a.num_seqs));
     plan.counts = reinterpret_cast<int *>(take(256));
     plan.q_list = reinterpret_cast<QTile *>(take(w.q_list));
     plan.k_list = reinterpret_cast<KTile *>(take(w.k_list));

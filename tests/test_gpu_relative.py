@@ -306,6 +306,26 @@ def test_bad_offsets_are_flagged_and_left_out():
         assert torch.equal(a, b)
 
 
+def test_offsets_that_go_back_and_forth():
+    """Sequences over the same rows, between others of negative length, have more tiles than the rows have."""
+    c = Case([1000], [1000], 4, 2, 64, 0, 32, 128)
+    good = both(c)
+    back = [0] + [1000, 0] * 40
+    fill = lambda x: torch.full_like(x, 7.0)  # noqa: E731
+    cu_q, cu_k = c.cu_q, c.cu_k
+    for cu in ((back, back), (back, [0] + [30, 60] * 40), ([0] + [30, 60] * 40, back)):
+        c.cu_q, c.cu_k = np.array(cu[0]), np.array(cu[1])
+        dq, dk, dv, dbias = c.backward(good[0], good[1], dq=fill(c.q), dk=fill(c.k), dv=fill(c.v))
+        assert pa.pa_read_device_error() & (pa.DEVERR_QUERY_LEN | pa.DEVERR_SEQ_RANGE)
+        if cu[0] is back and cu[1] is back:
+            assert (dq == 7.0).all() and (dk == 7.0).all() and (dv == 7.0).all() and (dbias == 0).all()
+    c.cu_q, c.cu_k = cu_q, cu_k
+    again = both(c)
+    assert pa.pa_read_device_error() == 0
+    for a, b in zip((good[0], good[1], *good[2]), (again[0], again[1], *again[2])):
+        assert torch.equal(a, b)
+
+
 def test_nothing_to_do():
     for sq, sk in (([], []), ([0, 0], [0, 0]), ([0], [30]), ([30], [0])):
         c = Case(sq, sk, 4, 2, 64, 0, 32, 128)
