@@ -136,21 +136,22 @@ __device__ __forceinline__ Tile load_entry(const Tile *list, int i) {
     return t;
 }
 
-// Shared memory: two resident tiles (Q and dout, or K and V), rings of the tiles that pass by (K
-// and V, or Q and dout), small arrays, barriers.  K outlives V by the time from dP to dQ, so it has
+// Shared memory: two resident tiles (Q and dout, or K and V; with heads of 64 there is room for the next
+// item's, whose loads then hide behind this one's work), rings of the tiles that pass by (K and V, or Q
+// and dout), small arrays, barriers.  K outlives V by the time from dP to dQ, so it has
 // three stages there.  With a bias the element-wise work is what bounds dQ, V's second stage gives
 // nothing (16 sequences of 128-2048 tokens, 32/8 heads: 414 us with and without it), and its place holds the bias of two items' heads.
 template <int HD, int STAGES_A, int STAGES_B, uint32_t SMALL_BYTES>
 struct Layout {
     static constexpr int NHALF = HD / 64;
     static constexpr uint32_t TILE = NHALF * HALF;
-    static constexpr int NA = STAGES_A, NB = STAGES_B;
+    static constexpr int NR = HD == 64 ? 2 : 1, NA = STAGES_A, NB = STAGES_B;
     static constexpr uint32_t OFF_RES = 0;
-    static constexpr uint32_t OFF_A = 2 * TILE;          // Q (dK, dV) or K (dQ)
+    static constexpr uint32_t OFF_A = 2 * NR * TILE;     // Q (dK, dV) or K (dQ)
     static constexpr uint32_t OFF_B = OFF_A + NA * TILE;  // dout (dK, dV) or V (dQ)
     static constexpr uint32_t OFF_SMALL = OFF_B + NB * TILE;
     static constexpr uint32_t OFF_BAR = OFF_SMALL + SMALL_BYTES;
-    static constexpr uint32_t OFF_MISC = OFF_BAR + 224;
+    static constexpr uint32_t OFF_MISC = OFF_BAR + 240;
     static constexpr uint32_t BYTES = OFF_MISC + 16;
     // At least 116 KB so a single CTA owns an SM (and all of its TMEM).
     static constexpr uint32_t SMEM = (BYTES > 118784u ? BYTES : 118784u);
@@ -164,18 +165,18 @@ constexpr int kNearPad = 256;
 __host__ __device__ constexpr int near_entries(int last) { return (last + kNearPad + 128 + 3) & ~3; }
 constexpr uint32_t kSmallQ = 2048 + 528;  // two items' halves of D, the buckets' first distances
 template <int HD, bool BIAS>
-using LayoutQ = Layout<HD, 3, BIAS ? 1 : 2, kSmallQ + (BIAS ? 2 * kTableBytes : 0u)>;
+using LayoutQ = Layout<HD, 3, BIAS && HD == 128 ? 1 : 2, kSmallQ + (BIAS ? 2 * kTableBytes : 0u)>;
 constexpr uint32_t kSmallKv = 2u * 3 * 512;
 template <int HD, bool BIAS>
 using LayoutKv = Layout<HD, 2, 2, kSmallKv + (BIAS ? 2 * kTableBytes : 0u)>;
 
 enum : int {
-    B_RES = 0,      // resident tiles loaded
-    B_RESEMPTY = 20,  // resident tiles read
+    B_RES = 0,        // [2] resident tiles loaded (the second one's at 28)
+    B_RESEMPTY = 20,  // [2] resident tiles read (the second one's at 29)
     B_ACCFREE = 21,   // accumulators stored (8 warps)
-    B_AFULL = 1,    // [3] tile of ring A ready (two arrivals: the copies, and the loading warp; dK, dV: for both rings)
+    B_AFULL = 1,    // [3] tile of ring A ready (dK, dV: of both rings, and a second arrival for the rows' statistics)
     B_AEMPTY = 4,   // [3] read
-    B_BFULL = 7,    // [2] ring B, likewise
+    B_BFULL = 7,    // [2] ring B
     B_BEMPTY = 9,   // [2]
     B_LAND = 11,    // copies of a tile that the loading warp edits
     B_SFULL = 12,   // logits of a tile ready
@@ -187,8 +188,10 @@ enum : int {
     B_DQDONE = 22,    // [2] dQ's product of a step done
     B_TABFULL = 24,   // [2] an item's bias in shared memory
     B_TABFREE = 26,   // [2] read (8 warps)
-    NBARS = 28
+    NBARS = 30
 };
+__device__ __forceinline__ int res_full(uint32_t slot) { return slot ? 28 : B_RES; }
+__device__ __forceinline__ int res_empty(uint32_t slot) { return slot ? 29 : B_RESEMPTY; }
 
 // A [128][HD] tile from row0 of a sequence that ends at row `end`: a box a lane.  A tile that the
 // sequence fills comes in boxes of 128 rows (a pair of tiles in 16-row pieces took 2900 cycles to land,
@@ -221,29 +224,6 @@ __device__ __forceinline__ void clear_rows(uint32_t tile, int from) {
     fence_proxy_async_smem();
 }
 __device__ __forceinline__ bool ragged(int left) { return left < BM && (left & 15) != 0; }
-
-// Tile -> stage, by the loading warp; `full` expects two arrivals.  `lands` counts the edited tiles.
-// False: a wait ran out.
-template <int HD>
-__device__ __forceinline__ bool load_stage(const CUtensorMap *map, uint32_t dst, int head, int start, int row0, int end,
-                                           uint32_t full, uint32_t land, uint32_t &lands, volatile int *abort_flag,
-                                           unsigned *err) {
-    const int lane = threadIdx.x & 31;
-    const bool cut = ragged(end - row0);
-    if (lane == 0) mbar_arrive_expect_tx(cut ? land : full, (HD / 64) * HALF);
-    __syncwarp();
-    load_tile<HD>(map, dst, head, start, row0, end, cut ? land : full);
-    if (cut) {
-        if (!wait_warp(land, lands++ & 1, abort_flag, err, kTimeoutNs)) return false;
-        clear_rows<HD>(dst, end - row0);
-    }
-    __syncwarp();
-    if (lane == 0) {
-        if (cut) mbar_arrive(full);
-        mbar_arrive(full);
-    }
-    return true;
-}
 
 // D[128 x 128] = A B^T over HD dims, both tiles [128][HD].
 template <int HD>
@@ -305,7 +285,7 @@ struct Cta {
     volatile int *abort_flag;
 };
 template <class L>
-__device__ __forceinline__ Cta setup() {
+__device__ __forceinline__ Cta setup(int full_arrivals) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];  // (swizzled tiles start on 1024 bytes)
     Cta c;
     c.base = smem_u32(smem_raw);
@@ -313,15 +293,15 @@ __device__ __forceinline__ Cta setup() {
     c.abort_flag = reinterpret_cast<volatile int *>(c.sb + L::OFF_MISC + 4);
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     if (threadIdx.x == 0) {
-        mbar_init(bar(B_RES), 1);
-        mbar_init(bar(B_RESEMPTY), 1);
         mbar_init(bar(B_ACCFREE), 8);
         for (int s = 0; s < 3; ++s) {
-            mbar_init(bar(B_AFULL + s), 2);
+            mbar_init(bar(B_AFULL + s), full_arrivals);
             mbar_init(bar(B_AEMPTY + s), 1);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(bar(B_BFULL + s), 2);
+            mbar_init(bar(res_full(s)), 1);
+            mbar_init(bar(res_empty(s)), 1);
+            mbar_init(bar(B_BFULL + s), full_arrivals);
             mbar_init(bar(B_BEMPTY + s), 1);
             mbar_init(bar(B_DPFULL + s), 1);
             mbar_init(bar(B_DSFULL + s), 8);
@@ -569,17 +549,18 @@ __global__ void __launch_bounds__(256)
 template <int HD, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_constant__ GradParams p) {
     using L = LayoutQ<HD, BIAS>;
-    constexpr int NA = L::NA, NB = L::NB;
+    constexpr int NR = L::NR, NA = L::NA, NB = L::NB;
     constexpr uint32_t kDp = 128, kDq = 384;
     if constexpr (BIAS) {  // the buckets' first distances, behind the rows' sums
         extern __shared__ __align__(1024) uint8_t smem_raw[];
         int *first = reinterpret_cast<int *>(smem_raw + L::OFF_SMALL + 2048);
         for (int i = threadIdx.x; i <= p.bias.num_buckets; i += kThreads) first[i] = p.bias.first[i];
     }
-    const Cta c = setup<L>();
+    const Cta c = setup<L>(1);
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t sQ = c.base + L::OFF_RES, sDo = sQ + L::TILE;
+    auto sQ = [&](uint32_t slot) -> uint32_t { return c.base + L::OFF_RES + slot * 2 * L::TILE; };
+    auto sDo = [&](uint32_t slot) -> uint32_t { return sQ(slot) + L::TILE; };
     auto sK = [&](uint32_t st) -> uint32_t { return c.base + L::OFF_A + st * L::TILE; };
     auto sV = [&](uint32_t st) -> uint32_t { return c.base + L::OFF_B + st * L::TILE; };
     const int last = p.bias.last();
@@ -616,20 +597,21 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             const QTile t = load_entry(p.q_list, e);
             if (t.n == 0) continue;
             const Steps s = steps_of(t);
-            if (items > 0 && !wait_warp(bar(B_RESEMPTY), (items - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+            const uint32_t res = items % NR;
+            if (items >= NR && !wait_warp(bar(res_empty(res)), (items / NR - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
             // (Sums along diagonals run across rows; in all else a row behind the sequence stays on its own.)
             const bool edit = BIAS && ragged(t.left);
-            const uint32_t land = bar(edit ? B_LAND : B_RES);
+            const uint32_t land = bar(edit ? B_LAND : res_full(res));
             if (lane == 0) mbar_arrive_expect_tx(land, 2 * L::TILE);
             __syncwarp();
-            load_tile<HD>(p.tmap_q, sQ, h, t.row, 0, t.left, land);
-            load_tile<HD>(p.tmap_do, sDo, h, t.row, 0, t.left, land);
+            load_tile<HD>(p.tmap_q, sQ(res), h, t.row, 0, t.left, land);
+            load_tile<HD>(p.tmap_do, sDo(res), h, t.row, 0, t.left, land);
             if (edit) {
                 if (!wait_warp(land, lands++ & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-                clear_rows<HD>(sQ, t.left);
-                clear_rows<HD>(sDo, t.left);
+                clear_rows<HD>(sQ(res), t.left);
+                clear_rows<HD>(sDo(res), t.left);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_RES));
+                if (lane == 0) mbar_arrive(bar(res_full(res)));
             }
             if (table_here) {
                 const uint32_t slot = items & 1;
@@ -643,16 +625,28 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             }
             ++items;
             const int kvh = h / p.group;
-            auto load = [&](const CUtensorMap *map, uint32_t dst, int j, uint32_t full) -> bool {
-                return load_stage<HD>(map, dst, kvh, t.k_start, (s.kt0 + s.tile(j)) * BN, t.sk, full, bar(B_LAND), lands,
-                                      c.abort_flag, p.err);
-            };
-            for (int j = 0; ok && j < s.n_all; ++j, ++J) {
-                const uint32_t sb = J % NB;
-                ok = (J < NA || wait_warp(bar(B_AEMPTY + sa), pa, c.abort_flag, p.err, kTimeoutNs)) &&
-                     load(p.tmap_k, sK(sa), j, bar(B_AFULL + sa)) &&
-                     (J < NB || wait_warp(bar(B_BEMPTY + sb), (J / NB - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) &&
-                     load(p.tmap_v, sV(sb), j, bar(B_BFULL + sb));
+            for (int j = 0; j < s.n_all; ++j, ++J) {
+                const uint32_t sb = J % NB, full_k = bar(B_AFULL + sa), full_v = bar(B_BFULL + sb);
+                const int row0 = (s.kt0 + s.tile(j)) * BN;
+                const bool cut = ragged(t.sk - row0);  // (the copies of tiles that are edited land together)
+                ok = J < NA || wait_warp(bar(B_AEMPTY + sa), pa, c.abort_flag, p.err, kTimeoutNs);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(cut ? bar(B_LAND) : full_k, cut ? 2 * L::TILE : L::TILE);
+                __syncwarp();
+                load_tile<HD>(p.tmap_k, sK(sa), kvh, t.k_start, row0, t.sk, cut ? bar(B_LAND) : full_k);
+                ok = J < NB || wait_warp(bar(B_BEMPTY + sb), (J / NB - 1) & 1, c.abort_flag, p.err, kTimeoutNs);
+                if (!ok) break;
+                if (lane == 0 && !cut) mbar_arrive_expect_tx(full_v, L::TILE);
+                __syncwarp();
+                load_tile<HD>(p.tmap_v, sV(sb), kvh, t.k_start, row0, t.sk, cut ? bar(B_LAND) : full_v);
+                if (cut) {
+                    ok = wait_warp(bar(B_LAND), lands++ & 1, c.abort_flag, p.err, kTimeoutNs);
+                    if (!ok) break;
+                    clear_rows<HD>(sK(sa), t.sk - row0);
+                    clear_rows<HD>(sV(sb), t.sk - row0);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full_k), mbar_arrive(full_v);
+                }
                 if (++sa == NA) sa = 0, pa ^= 1u;
             }
         }
@@ -672,13 +666,14 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             if (t.n == 0) continue;
             const Steps s = steps_of(t);
             if (warp == kWarpMma) {
-                ok = wait(B_RES, items & 1);
+                const uint32_t res = items % NR;
+                ok = wait(res_full(res), (items / NR) & 1);
                 for (int j = 0; ok && j < s.n_all; ++j, ++J) {
                     const uint32_t sb = J % NB, sd = J & 1;  // stage of V, place of dP
                     ok = wait(B_AFULL + sa, pa) && (J == 0 || wait(B_PFULL, (J - 1) & 1));
                     if (!ok) break;
                     if (elect_one()) {
-                        issue_abt<HD>(c.tmem, sQ, sK(sa));
+                        issue_abt<HD>(c.tmem, sQ(res), sK(sa));
                         mma_commit(bar(B_SFULL));
                     }
                     __syncwarp();
@@ -686,10 +681,10 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                     ok = wait(B_BFULL + sb, (J / NB) & 1) && (J < 2 || wait(B_DQDONE + sd, ((J >> 1) - 1) & 1));
                     if (!ok) break;
                     if (elect_one()) {
-                        issue_abt<HD>(c.tmem + kDp + 128u * sd, sDo, sV(sb));
+                        issue_abt<HD>(c.tmem + kDp + 128u * sd, sDo(res), sV(sb));
                         mma_commit(bar(B_DPFULL + sd));
                         mma_commit(bar(B_BEMPTY + sb));
-                        if (j + 1 == s.n_all) mma_commit(bar(B_RESEMPTY));
+                        if (j + 1 == s.n_all) mma_commit(bar(res_empty(res)));
                     }
                     __syncwarp();
                     if (++sa == NA) sa = 0, pa ^= 1u;
@@ -971,11 +966,13 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
 template <int HD, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_constant__ GradParams p) {
     using L = LayoutKv<HD, BIAS>;
+    constexpr int NR = L::NR;
     constexpr uint32_t kS = 0, kDp = 128, kDv = 256, kDk = 384;
-    const Cta c = setup<L>();
+    const Cta c = setup<L>(2);
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t sK = c.base + L::OFF_RES, sV = sK + L::TILE;
+    auto sK = [&](uint32_t slot) -> uint32_t { return c.base + L::OFF_RES + slot * 2 * L::TILE; };
+    auto sV = [&](uint32_t slot) -> uint32_t { return sK(slot) + L::TILE; };
     auto sQ = [&](int st) -> uint32_t { return c.base + L::OFF_A + st * L::TILE; };
     auto sDo = [&](int st) -> uint32_t { return c.base + L::OFF_B + st * L::TILE; };
     // Per stage and query of the tile: -lse2 (BIAS: plus what the table is relative to), -D and (BIAS) the
@@ -995,11 +992,12 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
         for (int k = 0; ok && item_of(k, count, p.num_kv_heads, e, kvh); ++k) {
             const KTile t = load_entry(p.k_list, e);
             if (t.n == 0) continue;
-            if (items > 0 && !wait_warp(bar(B_RESEMPTY), (items - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-            if (lane == 0) mbar_arrive_expect_tx(bar(B_RES), 2 * L::TILE);
+            const uint32_t res = items % NR;
+            if (items >= NR && !wait_warp(bar(res_empty(res)), (items / NR - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+            if (lane == 0) mbar_arrive_expect_tx(bar(res_full(res)), 2 * L::TILE);
             __syncwarp();
-            load_tile<HD>(p.tmap_k, sK, kvh, t.row, 0, t.left, bar(B_RES));
-            load_tile<HD>(p.tmap_v, sV, kvh, t.row, 0, t.left, bar(B_RES));
+            load_tile<HD>(p.tmap_k, sK(res), kvh, t.row, 0, t.left, bar(res_full(res)));
+            load_tile<HD>(p.tmap_v, sV(res), kvh, t.row, 0, t.left, bar(res_full(res)));
             if (table_here) {
                 const uint32_t slot = items & 1;
                 if (items >= 2 && !wait_warp(bar(B_TABFREE + slot), ((items >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
@@ -1067,19 +1065,20 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
         for (int k = 0; ok && item_of(k, count, p.num_kv_heads, e, kvh); ++k) {
             const int n = load_entry(p.k_list, e).n * p.group;
             if (n == 0) continue;
-            ok = wait(B_RES, items & 1) && wait(B_AFULL + (J & 1), (J >> 1) & 1);
+            const uint32_t res = items % NR;
+            ok = wait(res_full(res), (items / NR) & 1) && wait(B_AFULL + (J & 1), (J >> 1) & 1);
             if (!ok) break;
             if (elect_one()) {
-                issue_abt<HD>(c.tmem + kS, sK, sQ(J & 1));
+                issue_abt<HD>(c.tmem + kS, sK(res), sQ(J & 1));
                 mma_commit(bar(B_SFULL));
             }
             __syncwarp();
             for (int i = 0; i < n; ++i, ++J) {
                 const uint32_t st = J & 1, sn = st ^ 1u;
                 if (elect_one()) {
-                    issue_abt<HD>(c.tmem + kDp, sV, sDo(st));
+                    issue_abt<HD>(c.tmem + kDp, sV(res), sDo(st));
                     mma_commit(bar(B_DPFULL));
-                    if (i + 1 == n) mma_commit(bar(B_RESEMPTY));
+                    if (i + 1 == n) mma_commit(bar(res_empty(res)));
                 }
                 __syncwarp();
                 // (The item before's accumulators are stored before they are overwritten.)
@@ -1094,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
                     ok = wait(B_AFULL + sn, ((J + 1) >> 1) & 1);
                     if (!ok) break;
                     if (elect_one()) {
-                        issue_abt<HD>(c.tmem + kS, sK, sQ(sn));
+                        issue_abt<HD>(c.tmem + kS, sK(res), sQ(sn));
                         mma_commit(bar(B_SFULL));
                     }
                     __syncwarp();
