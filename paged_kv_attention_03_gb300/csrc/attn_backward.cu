@@ -135,7 +135,6 @@ __device__ __forceinline__ Tile load_entry(const Tile *list, int i) {
     d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
     return t;
 }
-
 // Shared memory: two resident tiles (Q and dout, or K and V; with heads of 64 there is room for the next
 // item's, whose loads then hide behind this one's work), rings of the tiles that pass by (K and V, or Q
 // and dout), small arrays, barriers.  K outlives V by the time from dP to dQ, so it has
@@ -159,13 +158,16 @@ struct Layout {
 };
 
 // An item's bias (dK, dV: of its kv head's heads) in shared memory; a longer one is read from global memory.
-constexpr uint32_t kTableBytes = 15360;
+constexpr uint32_t kTableBytesQ = 13312, kTableBytes = 15360;
 // What is kept of a head's row: distances -kNearPad .. last + 127.
 constexpr int kNearPad = 256;
 __host__ __device__ constexpr int near_entries(int last) { return (last + kNearPad + 128 + 3) & ~3; }
-constexpr uint32_t kSmallQ = 2048 + 528;  // two items' halves of D, the buckets' first distances
+// dQ's small arrays, as floats: two items' halves of D; with a bias, the buckets' first distances and each
+// warp's sums along diagonals.
+constexpr int kFirstAt = 512, kDiagAt = kFirstAt + 132;
+constexpr uint32_t kSmallQ = 4u * kFirstAt, kSmallQBias = 4u * (kDiagAt + 8 * 96);
 template <int HD, bool BIAS>
-using LayoutQ = Layout<HD, 3, BIAS && HD == 128 ? 1 : 2, kSmallQ + (BIAS ? 2 * kTableBytes : 0u)>;
+using LayoutQ = Layout<HD, 3, BIAS && HD == 128 ? 1 : 2, BIAS ? kSmallQBias + 2 * kTableBytesQ : kSmallQ>;
 constexpr uint32_t kSmallKv = 2u * 3 * 512;
 template <int HD, bool BIAS>
 using LayoutKv = Layout<HD, 2, 2, kSmallKv + (BIAS ? 2 * kTableBytes : 0u)>;
@@ -275,6 +277,31 @@ __device__ __forceinline__ void zero_rows(__nv_bfloat16 *dst, int64_t stride, in
     for (int i = threadIdx.x; i < rows * (HD / 8); i += 256)
         *reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(i / (HD / 8)) * stride + i % (HD / 8) * 8) =
             make_uint4(0u, 0u, 0u, 0u);
+}
+
+// A warp's 32 x 64 block of a tile as the element-wise warps hold it: thread t has the rows t / 4 + 8 a
+// (a = 0 .. 3) and of each the columns 8 b + 2 (t % 4) + e (b = 0 .. 7, e = 0, 1), from two loads of 16 lanes.
+// Row - column is then the same for all (a, b) with the same a - b, 11 pairs of distances for 64 elements:
+// a bias costs a thread 22 reads, masks are 22 comparisons, and sums along diagonals begin with additions in
+// registers.  (A thread a row needs 64 reads, comparisons and shuffles: dQ of 16 sequences of 128-2048 tokens,
+// 32/8 heads of 128 took 375 us that way.)
+__device__ __forceinline__ int pair_at(int a, int b) { return 4 * b + 2 * (a & 1); }
+__device__ __forceinline__ uint64_t block_pair(const float (&w)[2][32], int a, int b) {
+    return f2_pack(w[a >> 1][pair_at(a, b)], w[a >> 1][pair_at(a, b) + 1]);
+}
+__device__ __forceinline__ void set_pair(float (&w)[2][32], int a, int b, uint64_t x) {
+    f2_unpack(x, w[a >> 1][pair_at(a, b)], w[a >> 1][pair_at(a, b) + 1]);
+}
+__device__ __forceinline__ void load_block(uint32_t taddr, float (&w)[2][32]) {
+    tmem_ld_16x256b_x8(taddr, w[0]);
+    tmem_ld_16x256b_x8(taddr + (16u << 16), w[1]);
+    tmem_wait_ld_regs(w[0]);
+    tmem_wait_ld_regs(w[1]);
+}
+__device__ __forceinline__ float pair_sum(uint64_t x) {
+    float a, b;
+    f2_unpack(x, a, b);
+    return a + b;
 }
 
 // Shared set-up of both kernels.
@@ -553,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
     constexpr uint32_t kDp = 128, kDq = 384;
     if constexpr (BIAS) {  // the buckets' first distances, behind the rows' sums
         extern __shared__ __align__(1024) uint8_t smem_raw[];
-        int *first = reinterpret_cast<int *>(smem_raw + L::OFF_SMALL + 2048);
+        int *first = reinterpret_cast<int *>(smem_raw + L::OFF_SMALL) + kFirstAt;
         for (int i = threadIdx.x; i <= p.bias.num_buckets; i += kThreads) first[i] = p.bias.first[i];
     }
     const Cta c = setup<L>(1);
@@ -565,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
     auto sV = [&](uint32_t st) -> uint32_t { return c.base + L::OFF_B + st * L::TILE; };
     const int last = p.bias.last();
     const uint32_t table_bytes = BIAS ? near_entries(last) * 4u : 0u;
-    const bool table_here = BIAS && table_bytes <= kTableBytes;
+    const bool table_here = BIAS && table_bytes <= kTableBytesQ;
     const int count = *p.counts;
     // An item's steps: the tiles 0 .. n_pre - 1 with D from dout . out; tiles n_pre .. n - 2 for D alone;
     // the last tile, where D is complete before its dS is formed; then tiles n_pre .. n - 2 with D.
@@ -618,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 if (items >= 2 && !wait_warp(bar(B_TABFREE + slot), ((items >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar(B_TABFULL + slot), table_bytes);
-                    bulk_load(c.base + L::OFF_SMALL + kSmallQ + slot * kTableBytes, bias_row_of(p.bias_table, h, last) - kNearPad,
+                    bulk_load(c.base + L::OFF_SMALL + kSmallQBias + slot * kTableBytesQ, bias_row_of(p.bias_table, h, last) - kNearPad,
                               table_bytes, bar(B_TABFULL + slot));
                 }
                 __syncwarp();
@@ -708,36 +735,43 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
         }
     } else if (warp < 8) {
         const int wg = warp >> 2, quarter = warp & 3;
-        const int row = quarter * 32 + lane;
+        const int row = quarter * 32 + lane;  // (of D and dQ)
+        const int r0 = quarter * 32 + (lane >> 2), c0 = lane & 3;  // first row of the block, columns 2 c0, 2 c0 + 1
         const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
         const float sl2 = p.scale_log2;
         const uint64_t sl2x2 = f2_pack(sl2, sl2);
-        // The rows' half sums, and the buckets' first distances.
         float *small = reinterpret_cast<float *>(c.sb + L::OFF_SMALL);
-        [[maybe_unused]] const int *first = reinterpret_cast<const int *>(small + 512);
+        [[maybe_unused]] const int *first = reinterpret_cast<const int *>(small) + kFirstAt;
         const bool v8 = aligned32(p.dq, p.dq_stride);
         uint32_t items = 0, J = 0;
         bool ok = true;
         int e, h;
         bool more = item_of(0, count, p.num_heads, e, h);
         QTile next{};
-        float next_lse = 0.f, next_delta = 0.f;
-        auto prefetch = [&] {  // what the next item needs of the rows
+        float next_lse[4] = {}, next_delta[4] = {}, next_far = 0.f;
+        auto prefetch = [&] {  // what the next item needs of its rows and its head
             next = load_entry(p.q_list, e);
-            const int64_t at = static_cast<int64_t>(h) * p.total_q + next.row + row;
-            next_lse = row < next.left ? p.lse2[at] : INFINITY;
-            next_delta = row < next.left ? p.delta[at] : 0.f;
+            const int64_t at = static_cast<int64_t>(h) * p.total_q + next.row;
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const int x = r0 + 8 * a;
+                next_lse[a] = x < next.left ? p.lse2[at + x] : INFINITY;
+                next_delta[a] = x < next.left ? p.delta[at + x] : 0.f;
+            }
+            if (BIAS) next_far = __ldg(bias_row_of(p.bias_table, h, last) - kBiasPad);
         };
         if (more) prefetch();
         for (int k = 0; ok && more; ++k) {
             const QTile t = next;
             const int head = h;
-            const float lse2 = next_lse;
-            float delta = next_delta;
+            float lse2[4], delta[4];
+#pragma unroll
+            for (int a = 0; a < 4; ++a) lse2[a] = next_lse[a], delta[a] = next_delta[a];
+            [[maybe_unused]] const float last_bias = next_far;
+            more = item_of(k + 1, count, p.num_heads, e, h);
             const int rows = min(t.left, BM);
             const int64_t stat_row = static_cast<int64_t>(head) * p.total_q + t.row;
             __nv_bfloat16 *dq = p.dq + static_cast<int64_t>(t.row) * p.dq_stride + head * HD;
-            more = item_of(k + 1, count, p.num_heads, e, h);
             [[maybe_unused]] float by_bucket[4] = {0.f, 0.f, 0.f, 0.f};
             float *partial = nullptr;
             if constexpr (BIAS)
@@ -751,129 +785,141 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 continue;
             }
             const Steps s = steps_of(t);
-            const int pos = t.pos + row;
-            float d_sum = 0.f;
-            [[maybe_unused]] float d_far = 0.f, w_far = 0.f;  // sums of P dP and of P over the first n_far tiles
+            float d_sum[4] = {0.f, 0.f, 0.f, 0.f};
+            // Sums of P dP and of P over the first n_far tiles (d_far: and of the last bucket's dS in the others).
+            [[maybe_unused]] float d_far = 0.f, w_far[4] = {0.f, 0.f, 0.f, 0.f};
             [[maybe_unused]] const float *bias_row = nullptr;  // entry of distance 0
-            // x = sl2 s + far where the bias is that of the last bucket, else sl2 s + (entry + near_add).
-            float far = -lse2;
-            [[maybe_unused]] float near_add = -lse2;
             if constexpr (BIAS) {
                 bias_row = bias_row_of(p.bias_table, head, last);
-                const float last_bias = __ldg(bias_row - kBiasPad);
-                far = last_bias - lse2;
-                near_add = bias_ref(last_bias) - lse2;
                 if (table_here) {
                     ok = wait_warp(bar(B_TABFULL + (items & 1)), (items >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
                     if (!ok) break;
-                    bias_row = small + kSmallQ / 4 + (items & 1) * (kTableBytes / 4) + kNearPad;
+                    bias_row = small + kSmallQBias / 4 + (items & 1) * (kTableBytesQ / 4) + kNearPad;
                 }
             }
-            const uint64_t far2 = f2_pack(far, far);
             for (int j = 0; j < s.n_all; ++j, ++J) {
                 const uint32_t dp = c.tmem + t_lane + kDp + 128u * (J & 1) + 64u * wg;
                 const bool sum_only = s.sum_only(j);
                 const int tile = s.tile(j);
-                const int key0 = (s.kt0 + tile) * BN + 64 * wg;  // this warpgroup's first key
                 ok = wait_warp(bar(B_SFULL), J & 1, c.abort_flag, p.err, kTimeoutNs);
                 if (!ok) break;
                 tc_fence_after();
                 float w[2][32];  // logits, then weights P
-#pragma unroll
-                for (int cc = 0; cc < 2; ++cc) tmem_ld_32x32b_x32(c.tmem + t_lane + 64u * wg + 32u * cc, w[cc]);
-#pragma unroll
-                for (int cc = 0; cc < 2; ++cc) tmem_wait_ld_regs(w[cc]);
+                load_block(c.tmem + t_lane + 64u * wg, w);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_PFULL));
-                const int d0 = pos - key0;  // distance to the first key
-                const int d00 = __shfl_sync(0xffffffffu, d0, 0);  // the warp's first row's: its block has d00 - 63 .. d00 + 31
+                // The distance of the warp's first row to its first key: its block has d00 - 63 .. d00 + 31.
+                const int d00 = t.pos + quarter * 32 - (s.kt0 + tile) * BN - 64 * wg;
                 const bool near = BIAS && d00 - 63 < last;
-                if (near) {
-                    const float *bt = bias_row + d0;  // (-inf before distance 0)
+                const float add = BIAS ? near ? bias_ref(last_bias) : last_bias : 0.f;
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = fmaf(w[i >> 5][i & 31], sl2, bt[-i]) + near_add;
-                } else {
+                for (int a = 0; a < 4; ++a) {
+                    const float x = add - lse2[a];
+                    const uint64_t x2 = f2_pack(x, x);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float &a = w[i >> 4][2 * (i & 15)], &b = w[i >> 4][2 * (i & 15) + 1];
-                        f2_unpack(f2_fma(f2_pack(a, b), sl2x2, far2), a, b);
+                    for (int b = 0; b < 8; ++b) set_pair(w, a, b, f2_fma(block_pair(w, a, b), sl2x2, x2));
+                }
+                if (near || (!BIAS && d00 < 63) || (p.window > 0 && d00 + 31 >= p.window)) {
+                    const int n0 = d00 + (lane >> 2) - 2 * c0 - 56;
+                    auto entry = [&](int n) -> float {
+                        float x = 0.f;
+                        if (near)
+                            x = bias_row[n];  // (-inf before distance 0)
+                        else if (!BIAS && n < 0)
+                            x = -INFINITY;
+                        return p.window > 0 && n >= p.window ? -INFINITY : x;
+                    };
+#pragma unroll
+                    for (int g = 0; g < 11; ++g) {  // a - b + 7
+                        const uint64_t x2 = f2_pack(entry(n0 + 8 * g), entry(n0 + 8 * g - 1));
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {
+                            const int b = a + 7 - g;
+                            if (b >= 0 && b < 8) set_pair(w, a, b, f2_add(block_pair(w, a, b), x2));
+                        }
                     }
-                }
-                if (!BIAS && d0 < 63) {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (i > d0) w[i >> 5][i & 31] = -INFINITY;
-                }
-                if (p.window > 0 && d0 >= p.window) {
-                    const int hidden = d0 - p.window + 1;
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (i < hidden) w[i >> 5][i & 31] = -INFINITY;
                 }
 #pragma unroll
                 for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = ex2_approx(w[i >> 5][i & 31]);
                 if (BIAS && !sum_only && tile < s.n_far) {
-                    uint64_t a[2] = {0ull, 0ull};
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) a[i & 1] = f2_add(a[i & 1], f2_pack(w[i >> 4][2 * (i & 15)], w[i >> 4][2 * (i & 15) + 1]));
-                    float a0, a1;
-                    f2_unpack(f2_add(a[0], a[1]), a0, a1);
-                    w_far += a0 + a1;
+                    for (int a = 0; a < 4; ++a) {
+                        uint64_t x = block_pair(w, a, 0);
+#pragma unroll
+                        for (int b = 1; b < 8; ++b) x = f2_add(x, block_pair(w, a, b));
+                        w_far[a] += pair_sum(x);
+                    }
                 }
                 ok = wait_warp(bar(B_DPFULL + (J & 1)), (J >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
                 if (!ok) break;
                 tc_fence_after();
-                // D of the row: this warpgroup's half and the other's.
+                // D of the rows: a thread's columns, its four threads', this warpgroup's half and the other's.
                 auto exchange = [&]() -> bool {
+                    const bool odd = c0 & 1, high = c0 & 2;
+                    const float x0 = (odd ? d_sum[1] : d_sum[0]) + __shfl_xor_sync(0xffffffffu, odd ? d_sum[0] : d_sum[1], 1);
+                    const float x1 = (odd ? d_sum[3] : d_sum[2]) + __shfl_xor_sync(0xffffffffu, odd ? d_sum[2] : d_sum[3], 1);
+                    const float mine = (high ? x1 : x0) + __shfl_xor_sync(0xffffffffu, high ? x0 : x1, 2);
                     // (Two places: a warpgroup may be an item ahead of the other's reading.)
-                    float *sums = small + 256 * (items & 1) + row;
-                    sums[128 * wg] = d_sum;
+                    float *sums = small + 256 * (items & 1);
+                    const int x = r0 + 8 * c0;
+                    sums[128 * wg + x] = mine;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_SUMS));
                     if (!wait_warp(bar(B_SUMS), items & 1, c.abort_flag, p.err, kTimeoutNs)) return false;
-                    delta = sums[0] + sums[128];
-                    if (wg == 0 && row < rows) p.delta[stat_row + row] = delta;
+#pragma unroll
+                    for (int a = 0; a < 4; ++a) delta[a] = sums[r0 + 8 * a] + sums[128 + r0 + 8 * a];
+                    if (wg == 0 && x < rows) p.delta[stat_row + x] = sums[x] + sums[128 + x];
                     return true;
                 };
                 const bool pivot = j + 1 == s.n && s.n_pre < s.n;
                 if (pivot) {
-                    float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int cc = 0; cc < 2; ++cc) {
+                    for (int half = 0; half < 2; ++half) {
                         float d[32];
-                        tmem_ld_32x32b_x32(dp + 32u * cc, d);
+                        tmem_ld_16x256b_x8(dp + static_cast<uint32_t>(half * 16 << 16), d);
                         tmem_wait_ld_regs(d);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) a[i & 3] = fmaf(w[cc][i], d[i], a[i & 3]);
+                        for (int u = 0; u < 2; ++u) {
+                            const int a = 2 * half + u;
+                            uint64_t x = 0ull;
+#pragma unroll
+                            for (int b = 0; b < 8; ++b)
+                                x = f2_fma(block_pair(w, a, b), f2_pack(d[pair_at(a, b)], d[pair_at(a, b) + 1]), x);
+                            d_sum[a] += pair_sum(x);
+                        }
                     }
-                    d_sum += (a[0] + a[1]) + (a[2] + a[3]);
                     ok = exchange();
                     if (!ok) break;
-                    d_sum = s.n_pre == 0 ? 0.f : d_sum;  // (the last bucket's tiles may still be to come)
-                }
-                uint32_t pk[32];
-                uint64_t acc[2] = {0ull, 0ull};
-                const uint64_t delta2 = f2_pack(-delta, -delta);
+                    if (s.n_pre == 0) {  // (the last bucket's tiles may still be to come)
 #pragma unroll
-                for (int cc = 0; cc < 2; ++cc) {
-                    float d[32];
-                    tmem_ld_32x32b_x32(dp + 32u * cc, d);
-                    tmem_wait_ld_regs(d);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint64_t w2 = f2_pack(w[cc][2 * i], w[cc][2 * i + 1]), d2 = f2_pack(d[2 * i], d[2 * i + 1]);
-                        acc[i & 1] = f2_fma(w2, d2, acc[i & 1]);
-                        f2_unpack(f2_mul(w2, f2_add(d2, delta2)), w[cc][2 * i], w[cc][2 * i + 1]);
-                        pk[16 * cc + i] = pack_bf16x2(w[cc][2 * i], w[cc][2 * i + 1]);
+                        for (int a = 0; a < 4; ++a) d_sum[a] = 0.f;
                     }
                 }
-                float a0, a1;
-                f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
-                if (!pivot) d_sum += a0 + a1;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    float d[32];
+                    tmem_ld_16x256b_x8(dp + static_cast<uint32_t>(half * 16 << 16), d);
+                    tmem_wait_ld_regs(d);
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int a = 2 * half + u;
+                        const uint64_t delta2 = f2_pack(-delta[a], -delta[a]);
+                        uint64_t x = 0ull;
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            const uint64_t w2 = block_pair(w, a, b), d2 = f2_pack(d[pair_at(a, b)], d[pair_at(a, b) + 1]);
+                            x = f2_fma(w2, d2, x);
+                            set_pair(w, a, b, f2_mul(w2, f2_add(d2, delta2)));
+                            pk[2 * b + u] = pack_bf16x2(w[half][pair_at(a, b)], w[half][pair_at(a, b) + 1]);
+                        }
+                        if (!pivot) d_sum[a] += pair_sum(x);
+                    }
+                    if (!sum_only) tmem_st_16x128b_x8(dp + static_cast<uint32_t>(half * 16 << 16), pk);
+                }
                 if (!sum_only) {
-                    if (BIAS && tile + 1 == s.n_far) d_far = d_sum;
-                    tmem_st_32x32b_x32_u(dp, pk);
+                    if (BIAS && tile + 1 == s.n_far) d_far += (d_sum[0] + d_sum[1]) + (d_sum[2] + d_sum[3]);
                     tmem_wait_st();
                 }
                 tc_fence_before();
@@ -884,57 +930,73 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                     if (!ok) break;
                 }
                 if (BIAS && j + 1 >= s.n && tile >= s.n_far) {
-                    // Sums along the diagonals row - column = lane, lane - 32, lane - 64 of the warp's 32 x
-                    // 64 block: at column i the lane fetches the element of row (lane + i) % 32.
-                    float a[3] = {0.f, 0.f, 0.f};
+                    // Sums along diagonals: a thread's own, 11 pairs; then thread (r, c), r = t / 4, fetches of the
+                    // threads (., c) those of distances r + 8 i (v[i], less d00 - 64); then the four threads of
+                    // an r share them out.
+                    float v[12];
 #pragma unroll
-                    for (int b = 0; b < 32; ++b) {
-                        const bool wrap = lane + b >= 32;
+                    for (int i = 0; i < 12; ++i) v[i] = 0.f;
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float v = __shfl_sync(0xffffffffu, w[x][b], lane + b);
-                            if (wrap)
-                                a[x + 1] += v;
+                    for (int g = 0; g < 11; ++g) {
+                        uint64_t x2 = 0ull;
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {
+                            const int b = a + 7 - g;
+                            if (b >= 0 && b < 8) x2 = f2_add(x2, block_pair(w, a, b));
+                        }
+                        float x[2];
+                        f2_unpack(x2, x[0], x[1]);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int src = (lane >> 2) + 2 * c0 + k;
+                            const float y = __shfl_sync(0xffffffffu, x[k], (src & 7) * 4 + c0);
+                            if (src >= 8)
+                                v[g] += y;
                             else
-                                a[x] += v;
+                                v[g + 1] += y;
                         }
                     }
-                    // 32 distances at a time: runs of a bucket's are added up from its first one on (`heads`
-                    // marks those), and the lane that has the bucket fetches the sum at its end.
+                    const int base = d00 - 64;
+                    float *diag = small + kDiagAt + 96 * warp;
 #pragma unroll
-                    for (int r = 0; r < 3; ++r) {
-                        const int base = d00 - 32 * r;
-                        uint32_t heads = 0u;
-                        for (int b = lane; b < p.bias.num_buckets; b += 32) {
-                            const int x = first[b] - base;
-                            if (x >= 0 && x < 32) heads |= 1u << x;
-                        }
-                        heads = __reduce_or_sync(0xffffffffu, heads);
-                        const uint32_t mine = heads & (0xffffffffu >> (31 - lane));
-                        const int from = mine != 0u ? 31 - __clz(mine) : 0;
-                        float v = a[r];
+                    for (int k = 0; k < 3; ++k) {
+                        float x[2];
 #pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) {
-                            const float x = __shfl_up_sync(0xffffffffu, v, o);
-                            if (lane - o >= from) v += x;
+                        for (int i = 0; i < 2; ++i) {
+                            const float even = v[4 * k + 2 * i], odd = v[4 * k + 2 * i + 1];
+                            x[i] = (c0 & 1 ? odd : even) + __shfl_xor_sync(0xffffffffu, c0 & 1 ? even : odd, 1);
                         }
-#pragma unroll
-                        for (int k4 = 0; k4 < 4; ++k4) {
-                            if (32 * k4 >= p.bias.num_buckets) break;
-                            const int b = lane + 32 * k4;
-                            const bool in = b < p.bias.num_buckets;
-                            const int lo = in ? first[b] - base : 32, hi = in ? min(first[b + 1] - base, 32) : 0;
-                            const float x = __shfl_sync(0xffffffffu, v, hi - 1);
-                            if (lo < 32 && hi > max(lo, 0)) by_bucket[k4] += x;
-                        }
+                        const float y = (c0 & 2 ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, c0 & 2 ? x[0] : x[1], 2);
+                        const int at = (lane >> 2) + 8 * c0 + 32 * k;
+                        diag[at] = y;
+                        if (base + at >= last) d_far += y;
                     }
+                    __syncwarp();
+                    // A lane adds up the distances of its buckets.
+#pragma unroll
+                    for (int k4 = 0; k4 < 4; ++k4) {
+                        if (32 * k4 >= p.bias.num_buckets - 1) break;
+                        const int b = lane + 32 * k4;
+                        if (b >= p.bias.num_buckets - 1) continue;
+                        const int hi = min(first[b + 1] - base, 96);
+                        float sum = 0.f;
+#pragma unroll 1
+                        for (int x = max(first[b] - base, 0); x < hi; x += 4) {
+                            float f[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) f[i] = x + i < hi ? diag[x + i] : 0.f;
+                            sum += (f[0] + f[1]) + (f[2] + f[3]);
+                        }
+                        by_bucket[k4] += sum;
+                    }
+                    __syncwarp();
                 }
             }
             if (!ok) break;
             if constexpr (BIAS) {
                 __syncwarp();
                 if (table_here && lane == 0) mbar_arrive(bar(B_TABFREE + (items & 1)));
-                const float t_far = warp_sum(d_far - delta * w_far);
+                const float t_far = warp_sum(d_far - ((delta[0] * w_far[0] + delta[1] * w_far[1]) + (delta[2] * w_far[2] + delta[3] * w_far[3])));
 #pragma unroll
                 for (int k4 = 0; k4 < 4; ++k4) {
                     const int b = lane + 32 * k4;
@@ -1114,6 +1176,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
         const int row = quarter * 32 + lane;
         const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
         const float sl2 = p.scale_log2;
+        const int c0 = lane & 3;  // columns 2 c0, 2 c0 + 1
         const uint32_t sc = c.tmem + t_lane + kS + 64u * wg, dp = c.tmem + t_lane + kDp + 64u * wg;
         uint32_t items = 0, J = 0;
         bool ok = true;
@@ -1124,7 +1187,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
         for (int k = 0; ok && more; ++k) {
             const KTile t = next;
             const int head0 = kvh * p.group;
-            const int rows = min(t.left, BM), key = t.key + row;
+            const int rows = min(t.left, BM);
             __nv_bfloat16 *dk = p.dk + static_cast<int64_t>(t.row) * p.dk_stride + kvh * HD;
             __nv_bfloat16 *dv = p.dv + static_cast<int64_t>(t.row) * p.dv_stride + kvh * HD;
             more = item_of(k + 1, count, p.num_kv_heads, e, kvh);
@@ -1156,56 +1219,51 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
                 }
                 tc_fence_after();
                 float w[2][32];
+                load_block(sc, w);
+                // The distance of the first query to the warp's first key: its block has d00 - 31 .. d00 + 63.
+                const int d00 = pos0 - t.key - quarter * 32;
+                const bool near = BIAS && d00 - 31 < last;
+                const uint64_t sl2x2 = f2_pack(sl2, sl2);
+                const float *nl = stat(st) + (BIAS && !near ? 256 : 0) + 64 * wg + 2 * c0;
 #pragma unroll
-                for (int cc = 0; cc < 2; ++cc) tmem_ld_32x32b_x32(sc + 32u * cc, w[cc]);
+                for (int b = 0; b < 8; ++b) {
+                    const uint64_t l2 = *reinterpret_cast<const uint64_t *>(nl + 8 * b);
 #pragma unroll
-                for (int cc = 0; cc < 2; ++cc) tmem_wait_ld_regs(w[cc]);
-                const int d0 = pos0 - key;  // distance from the first query
-                // (Lane 31 has the nearest key.)
-                const bool near = BIAS && __shfl_sync(0xffffffffu, d0, 31) < last;
-                if (near) {
-                    const float *bt = bias_row + g * bias_step + d0;  // (-inf before distance 0)
-                    const float4 *nl = reinterpret_cast<const float4 *>(stat(st) + 64 * wg);
+                    for (int a = 0; a < 4; ++a) set_pair(w, a, b, f2_fma(block_pair(w, a, b), sl2x2, l2));
+                }
+                if (near || (!BIAS && d00 < 31) || (p.window > 0 && d00 + 63 >= p.window)) {
+                    const int n0 = d00 - (lane >> 2) + 2 * c0 - 24;
+                    const float *bt = bias_row + g * bias_step;
+                    auto entry = [&](int n) -> float {
+                        float x = 0.f;
+                        if (near)
+                            x = bt[n];  // (-inf before distance 0)
+                        else if (!BIAS && n < 0)
+                            x = -INFINITY;
+                        return p.window > 0 && n >= p.window ? -INFINITY : x;
+                    };
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        const float4 l = nl[x];
-                        float *v = &w[x >> 3][4 * (x & 7)];
-                        v[0] = fmaf(v[0], sl2, bt[4 * x]) + l.x;
-                        v[1] = fmaf(v[1], sl2, bt[4 * x + 1]) + l.y;
-                        v[2] = fmaf(v[2], sl2, bt[4 * x + 2]) + l.z;
-                        v[3] = fmaf(v[3], sl2, bt[4 * x + 3]) + l.w;
+                    for (int x = 0; x < 11; ++x) {  // b - a + 3
+                        const uint64_t x2 = f2_pack(entry(n0 + 8 * x), entry(n0 + 8 * x + 1));
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {
+                            const int b = a + x - 3;
+                            if (b >= 0 && b < 8) set_pair(w, a, b, f2_add(block_pair(w, a, b), x2));
+                        }
                     }
-                } else {
-                    const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(stat(st) + (BIAS ? 256 : 0) + 64 * wg);
-                    const uint64_t sl2x2 = f2_pack(sl2, sl2);
+                }
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) {
-                        const ulonglong2 l = nl[x];
-                        float *v = &w[x >> 3][4 * (x & 7)];
-                        f2_unpack(f2_fma(f2_pack(v[0], v[1]), sl2x2, l.x), v[0], v[1]);
-                        f2_unpack(f2_fma(f2_pack(v[2], v[3]), sl2x2, l.y), v[2], v[3]);
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {  // pair 2 b + a % 2
+                        float &e0 = w[half][2 * x], &e1 = w[half][2 * x + 1];
+                        e0 = ex2_approx(e0);
+                        e1 = ex2_approx(e1);
+                        pk[x] = pack_bf16x2(e0, e1);
                     }
+                    tmem_st_16x128b_x8(sc + static_cast<uint32_t>(half * 16 << 16), pk);
                 }
-                if (!BIAS && d0 < 0) {  // (the table hides future keys)
-#pragma unroll
-                    for (int x = 0; x < 64; ++x)
-                        if (x < -d0) w[x >> 5][x & 31] = -INFINITY;
-                }
-                if (p.window > 0 && d0 + 63 >= p.window) {
-                    const int end = p.window - d0;  // queries from here on are too far
-#pragma unroll
-                    for (int x = 0; x < 64; ++x)
-                        if (x >= end) w[x >> 5][x & 31] = -INFINITY;
-                }
-                uint32_t pk[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                    float &a = w[x >> 4][2 * (x & 15)], &b = w[x >> 4][2 * (x & 15) + 1];
-                    a = ex2_approx(a);
-                    b = ex2_approx(b);
-                    pk[x] = pack_bf16x2(a, b);
-                }
-                tmem_st_32x32b_x32_u(sc, pk);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -1215,24 +1273,25 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
                     break;
                 }
                 tc_fence_after();
-                const ulonglong2 *dl = reinterpret_cast<const ulonglong2 *>(stat(st) + 128 + 64 * wg);
+                const float *dl = stat(st) + 128 + 64 * wg + 2 * c0;
 #pragma unroll
-                for (int cc = 0; cc < 2; ++cc) {
+                for (int half = 0; half < 2; ++half) {
                     float d[32];
-                    tmem_ld_32x32b_x32(dp + 32u * cc, d);
+                    tmem_ld_16x256b_x8(dp + static_cast<uint32_t>(half * 16 << 16), d);
                     tmem_wait_ld_regs(d);
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const ulonglong2 l = dl[8 * cc + x];
-                        float *v = &d[4 * x];
-                        const float *pw = &w[cc][4 * x];
-                        f2_unpack(f2_mul(f2_pack(pw[0], pw[1]), f2_add(f2_pack(v[0], v[1]), l.x)), v[0], v[1]);
-                        f2_unpack(f2_mul(f2_pack(pw[2], pw[3]), f2_add(f2_pack(v[2], v[3]), l.y)), v[2], v[3]);
-                        pk[16 * cc + 2 * x] = pack_bf16x2(v[0], v[1]);
-                        pk[16 * cc + 2 * x + 1] = pack_bf16x2(v[2], v[3]);
+                    for (int b = 0; b < 8; ++b) {
+                        const uint64_t l2 = *reinterpret_cast<const uint64_t *>(dl + 8 * b);
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            float *x = &d[4 * b + 2 * u];
+                            f2_unpack(f2_mul(block_pair(w, 2 * half + u, b), f2_add(f2_pack(x[0], x[1]), l2)), x[0], x[1]);
+                            pk[2 * b + u] = pack_bf16x2(x[0], x[1]);
+                        }
                     }
+                    tmem_st_16x128b_x8(dp + static_cast<uint32_t>(half * 16 << 16), pk);
                 }
-                tmem_st_32x32b_x32_u(dp, pk);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
