@@ -929,7 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                     ok = exchange();
                     if (!ok) break;
                 }
-                if (BIAS && j + 1 >= s.n && tile >= s.n_far) {
+                if (BIAS && j + 1 >= s.n && tile >= s.n_far && d00 > -32) {  // (else all of the block is hidden)
                     // Sums along diagonals: a thread's own, 11 pairs; then thread (r, c), r = t / 4, fetches of the
                     // threads (., c) those of distances r + 8 i (v[i], less d00 - 64); then the four threads of
                     // an r share them out.
