@@ -552,7 +552,9 @@ pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const
  * not see has weight 0: an infinite or NaN key or value of its sequence may reach the rows whose
  * 128-key tiles hold it (another sequence's never does).  Sequences with offsets outside the
  * arrays, or longer than max_seqlen_q / max_seqlen_k, are flagged (PA_DEVERR_QUERY_LEN,
- * PA_DEVERR_SEQ_RANGE) and left out.
+ * PA_DEVERR_SEQ_RANGE) and left out; where offsets that go back and forth make sequences share rows,
+ * those rows' results are unspecified, or left as they were.  Outputs may not overlap inputs or one
+ * another, but for key / value / slot_mapping's rows in the cache.
  *
  *   workspace  256-byte aligned, contents on entry do not matter; calls that may overlap on the
  *              GPU need one each.

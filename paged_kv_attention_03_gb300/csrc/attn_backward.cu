@@ -26,17 +26,18 @@
 // item's loads run during the end of the one before.
 //
 // Roles in a CTA: warps 0-7 are two warpgroups of element-wise work, each on 64 of a tile's 128
-// columns (a thread owns a TMEM lane, i.e. an accumulator row); warp 8 loads tiles by TMA, warp 9
+// columns (a warp on the 32 lanes of tensor memory that it can reach); warp 8 loads tiles by TMA, warp 9
 // (in dQ with warp 10) issues the products.  P and dS go back to tensor memory as bf16, over the fp32
 // tile they came from, and are the first operand of the next product from there.
 //
 // Measured (packed sequences, 32/8 heads of 128; the products of each kernel over its time):
-//  * two of 6000-8192 tokens, no bias: dQ 665 us (1.69 PFLOP/s of three products, 0.87 of the bf16
-//    peak), dK/dV 895 us (1.68): products nearly back to back; the rest are the waits between them;
-//  * sixteen of 128-2048 tokens, 32 buckets to 128: dQ 379 us (0.63), dK/dV 286 us (1.11): a third of
-//    dQ's steps are near tiles, whose bias and diagonal sums (64 shuffles an element row, two cycles
-//    each) take 2100 cycles beside 1600 of the softmax; loops grow past the instruction cache when
-//    such code is unrolled further.
+//  * two of 6000-8192 tokens, no bias: dQ 664 us (1.69 PFLOP/s of three products, 0.87 of the bf16
+//    peak), dK/dV 891 us (1.68): products nearly back to back; the rest are the waits between them;
+//  * sixteen of 128-2048 tokens, 32 buckets to 128: dQ 304 us (0.78), dK/dV 277 us (1.15).  A block of
+//    dQ takes 216 steps, 58 of them near tiles, in 30 items of which the last step's chain (logits, D,
+//    dS, diagonals, product, rows out) has nothing beside it;
+//  * 128 of 128 tokens, where an item is one step: dQ 96 us without a bias (the bytes alone take 69),
+//    131 with one, dK/dV 77 and 79 (59).
 #include <cuda.h>
 
 #include <atomic>
@@ -138,8 +139,9 @@ __device__ __forceinline__ Tile load_entry(const Tile *list, int i) {
 // Shared memory: two resident tiles (Q and dout, or K and V; with heads of 64 there is room for the next
 // item's, whose loads then hide behind this one's work), rings of the tiles that pass by (K and V, or Q
 // and dout), small arrays, barriers.  K outlives V by the time from dP to dQ, so it has
-// three stages there.  With a bias the element-wise work is what bounds dQ, V's second stage gives
-// nothing (16 sequences of 128-2048 tokens, 32/8 heads: 414 us with and without it), and its place holds the bias of two items' heads.
+// three stages there.  With a bias and heads of 128, V's second stage gives nothing (16 sequences of
+// 128-2048 tokens, 32/8 heads: the same time with and without it), and its place holds the bias of two
+// items' heads.
 template <int HD, int STAGES_A, int STAGES_B, uint32_t SMALL_BYTES>
 struct Layout {
     static constexpr int NHALF = HD / 64;
@@ -284,7 +286,8 @@ __device__ __forceinline__ void zero_rows(__nv_bfloat16 *dst, int64_t stride, in
 // Row - column is then the same for all (a, b) with the same a - b, 11 pairs of distances for 64 elements:
 // a bias costs a thread 22 reads, masks are 22 comparisons, and sums along diagonals begin with additions in
 // registers.  (A thread a row needs 64 reads, comparisons and shuffles: dQ of 16 sequences of 128-2048 tokens,
-// 32/8 heads of 128 took 375 us that way.)
+// 32/8 heads of 128 took 375 us that way, 304 this way; without a bias of two documents of 6000-8192 tokens
+// 648 against 664.)
 __device__ __forceinline__ int pair_at(int a, int b) { return 4 * b + 2 * (a & 1); }
 __device__ __forceinline__ uint64_t block_pair(const float (&w)[2][32], int a, int b) {
     return f2_pack(w[a >> 1][pair_at(a, b)], w[a >> 1][pair_at(a, b) + 1]);
@@ -519,6 +522,7 @@ __device__ __forceinline__ void plan_lists(const PlanParams &p) {
     }
 }
 
+// Bound by its bytes: 44 us for out and dout of 17400 tokens, 32 heads of 128 (285 MB, 6.5 TB/s).
 // lse in base 2 and dout_i out_i, both as [num_heads, total_q]: a block takes 8 tokens of 8 heads, half
 // a warp (128 dims) or a quarter (64) a row.  The first block makes the lists.
 template <int HD>
@@ -972,7 +976,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                         if (base + at >= last) d_far += y;
                     }
                     __syncwarp();
-                    // A lane adds up the distances of its buckets.
+                    // A lane adds up the distances of its buckets.  (Scans over the warp's 96 distances by bucket
+                    // took 60 us of 375 of sixteen sequences of 128-2048 tokens.)
 #pragma unroll
                     for (int k4 = 0; k4 < 4; ++k4) {
                         if (32 * k4 >= p.bias.num_buckets - 1) break;
@@ -1325,7 +1330,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
 
 // ---------------------------------------------------------------------- dbias ---
 // Sums the query tiles' partial sums, eight warps' for each, always in the same order: a block takes
-// eight buckets of a head (a sector of a row), 128 threads a bucket.
+// eight buckets of a head (a sector of a row), 128 threads a bucket.  4.5 us for 145 tiles of 32 heads, 32
+// buckets (4.8 MB): latency.
 constexpr int kBiasBuckets = 8;
 __global__ void __launch_bounds__(1024)
     grad_bias_kernel(float *__restrict__ dbias, const float *__restrict__ partial, const int *__restrict__ counts, int num_heads,

