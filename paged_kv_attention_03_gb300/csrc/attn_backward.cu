@@ -78,7 +78,8 @@ struct alignas(16) QTile {
     int id;       // place among all query tiles in the sequences' order
     int pad;
 };
-// 128 keys of a sequence.
+// 128 keys of a sequence, or a part of their steps: one for each head of the kv head and each tile of 128
+// queries that sees some of the keys.
 struct alignas(16) KTile {
     int row;      // first row of k
     int left;     // rows from there to the sequence's end (1 ..)
@@ -86,8 +87,10 @@ struct alignas(16) KTile {
     int off;      // position of the first query
     int q_start;  // first row of q
     int sq;       // queries
-    int n;        // tiles of 128 queries that see some of the keys
-    int pad;
+    int n;        // tiles of 128 queries
+    int from, to;  // steps of this part, of n times the heads of a kv head
+    int part, parts;
+    int slot;     // (parts > 1) of the first part of kv head 0
 };
 
 struct GradParams {
@@ -107,6 +110,8 @@ struct GradParams {
     const int *counts;  // [2]: query tiles, key tiles
     const QTile *q_list;
     const KTile *k_list;
+    float *split;       // [slots][dV, dK][HD / 4][128 rows][4]: sums of key tiles whose steps are split
+    int *arrived;       // [slots][8 warps]
     int total_q, total_k;
     int num_heads, num_kv_heads, group;
     int window;
@@ -130,12 +135,17 @@ __device__ __forceinline__ bool item_of(int k, int count, int heads, int &entry,
 }
 template <class Tile>
 __device__ __forceinline__ Tile load_entry(const Tile *list, int i) {
+    static_assert(sizeof(Tile) % 16 == 0, "entries are read as 16-byte vectors");
     Tile t;
-    const int4 a = __ldg(reinterpret_cast<const int4 *>(list + i)), b = __ldg(reinterpret_cast<const int4 *>(list + i) + 1);
     int *d = reinterpret_cast<int *>(&t);
-    d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
+#pragma unroll
+    for (int x = 0; x < static_cast<int>(sizeof(Tile) / 16); ++x) {
+        const int4 a = __ldg(reinterpret_cast<const int4 *>(list + i) + x);
+        d[4 * x] = a.x, d[4 * x + 1] = a.y, d[4 * x + 2] = a.z, d[4 * x + 3] = a.w;
+    }
     return t;
 }
+
 // Shared memory: two resident tiles (Q and dout, or K and V; with heads of 64 there is room for the next
 // item's, whose loads then hide behind this one's work), rings of the tiles that pass by (K and V, or Q
 // and dout), small arrays, barriers.  K outlives V by the time from dP to dQ, so it has
@@ -384,13 +394,22 @@ struct PlanParams {
     const int32_t *cu_q;
     const int32_t *cu_k;
     int num_seqs, total_q, total_k, max_q, max_k, window;
-    int most[2];  // entries that the lists have room for
+    int most[2];  // tiles that the lists have room for (the key tiles' also for the parts of those that are split)
+    int num_kv_heads, group;
+    int slots;    // places for the sums of split key tiles
+    int *arrived;
     int *counts;
     QTile *q_list;
     KTile *k_list;
     unsigned *err;
 };
 constexpr int kPlanBins = 1024;  // longer tiles share the last bin
+// Key tiles of more steps than an SM's share and 8 more are split: few kv heads with many queries each have
+// few long items (3 sequences of 293-2336 tokens, 40/4 heads: 180 steps for the longest, 55 for an SM's
+// share; one of 16384, 8/1 heads: 1024 and 434).  Parts leave their sums in fp32; the last one to arrive, warp
+// by warp, adds them up in the parts' order.  A part costs about five steps, for its keys and its sums.  So many
+// slots suffice: a split tile has fewer parts than twice its steps over an SM's share.
+constexpr int kMinSteps = 8, kMaxSlots = 2 * kPlanSms + 1;
 
 // emit(chunk of sequences, tile of the chunk, tile of the sequence, the sequence)
 template <class Emit, class Chunk>
@@ -458,7 +477,11 @@ __device__ __forceinline__ KTile k_tile(const PlanParams &p, int t, int q_start,
     int64_t to = sq;
     if (p.window > 0) to = min(to, static_cast<int64_t>(r.key) + min(r.left, BM) - 1 + p.window - r.off);
     r.n = to > from ? static_cast<int>((to - from + BN - 1) / BN) : 0;
-    r.pad = 0;
+    r.from = 0;
+    r.to = r.n * p.group;
+    r.part = 0;
+    r.parts = 1;
+    r.slot = 0;
     return r;
 }
 
@@ -481,26 +504,75 @@ __device__ __forceinline__ int exclusive_sums(int *x, int n) {
 }
 
 __device__ __forceinline__ void plan_lists(const PlanParams &p) {
-    __shared__ int bins[kPlanBins];
+    __shared__ __align__(16) int bins[kPlanBins];
+    __shared__ int warps[8];  // entries in a warp's bins
     __shared__ int before[65536 / 32];  // tiles of the chunks of 32 sequences before
     __shared__ bool fits;
+    __shared__ int slots;
+    __shared__ unsigned long long steps;  // of the key tiles, all kv heads
     const int chunks = (p.num_seqs + 31) / 32;
+    if (threadIdx.x == 0) slots = 0, steps = 0;
+    for (int i = threadIdx.x; i < 8 * p.slots; i += blockDim.x) p.arrived[i] = 0;
+    __syncthreads();
+    unsigned long long mine = 0;
+    plan_tiles(
+        p, true, false, [&](int, int, int t, int a, int b, int c, int d) { mine += k_tile(p, t, a, b, c, d).to; }, [](int, int) {});
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if ((threadIdx.x & 31) == 0 && mine > 0) atomicAdd(&steps, mine * p.num_kv_heads);
+    __syncthreads();
+    const int limit = static_cast<int>(min(steps / kPlanSms + kMinSteps, 1ull << 30));
+    // Bins of the list by the number of steps (key tiles: in units of a group's where those would not fit).
+    const int unit = p.group * ((p.max_q + BM - 1) / BM) < kPlanBins ? 1 : p.group;
+    auto bin = [](int n) { return kPlanBins - 1 - min(n, kPlanBins - 1); };
+    // A key tile's parts in turn: fill(entry).
+    auto parts_of = [&](KTile x, bool place, auto fill) {
+        const int all = x.to;
+        x.parts = max((all + limit - 1) / limit, 1);
+        const int per = (all + x.parts - 1) / x.parts;  // (at most limit, so no part is empty)
+        if (place && x.parts > 1) x.slot = atomicAdd(&slots, x.parts * p.num_kv_heads);
+        for (; x.part < x.parts; ++x.part) {
+            x.from = x.part * per;
+            x.to = min(x.from + per, all);
+            fill(x);
+        }
+    };
     for (int keys = 0; keys < 2; ++keys) {
-        auto bin = [](int n) { return kPlanBins - 1 - min(n, kPlanBins - 1); };
         for (int i = threadIdx.x; i < kPlanBins; i += blockDim.x) bins[i] = 0;
         __syncthreads();
         plan_tiles(
             p, keys, keys == 0,
             [&](int, int, int t, int a, int b, int c, int d) {
-                atomicAdd(&bins[bin(keys ? k_tile(p, t, a, b, c, d).n : q_tile(p, 0, t, a, b, c, d).n)], 1);
+                if (keys)
+                    parts_of(k_tile(p, t, a, b, c, d), false, [&](const KTile &x) { atomicAdd(&bins[bin((x.to - x.from + unit - 1) / unit)], 1); });
+                else
+                    atomicAdd(&bins[bin(q_tile(p, 0, t, a, b, c, d).n)], 1);
             },
             [&](int chunk, int tiles) { before[chunk] = tiles; });
         __syncthreads();
+        // (A thread four bins: by one warp the sums of all took 2.5 us.)
+        static_assert(kPlanBins == 4 * 256, "four bins a thread");
+        int4 &mine4 = reinterpret_cast<int4 *>(bins)[threadIdx.x];
+        const int4 n4 = mine4;
+        int end = n4.x + n4.y + n4.z + n4.w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, end, o);
+            if ((threadIdx.x & 31) >= o) end += x;
+        }
+        if ((threadIdx.x & 31) == 31) warps[threadIdx.x >> 5] = end;
+        __syncthreads();
+        int count = 0;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            if (w == threadIdx.x >> 5) end += count;
+            count += warps[w];
+        }
+        mine4 = make_int4(end - n4.x - n4.y - n4.z - n4.w, end - n4.y - n4.z - n4.w, end - n4.z - n4.w, end - n4.w);
         if (threadIdx.x < 32) {
-            const int count = exclusive_sums(bins, kPlanBins);
-            exclusive_sums(before, chunks);
+            const int tiles = exclusive_sums(before, chunks);
             if (threadIdx.x == 0) {
-                fits = count <= p.most[keys];
+                fits = tiles <= p.most[keys];
                 p.counts[keys] = fits ? count : 0;
             }
         }
@@ -510,8 +582,8 @@ __device__ __forceinline__ void plan_lists(const PlanParams &p) {
             p, keys, false,
             [&](int chunk, int i, int t, int a, int b, int c, int d) {
                 if (keys) {
-                    const KTile x = k_tile(p, t, a, b, c, d);
-                    p.k_list[atomicAdd(&bins[bin(x.n)], 1)] = x;
+                    parts_of(k_tile(p, t, a, b, c, d), true,
+                             [&](const KTile &x) { p.k_list[atomicAdd(&bins[bin((x.to - x.from + unit - 1) / unit)], 1)] = x; });
                 } else {
                     const QTile x = q_tile(p, before[chunk] + i, t, a, b, c, d);
                     p.q_list[atomicAdd(&bins[bin(x.n)], 1)] = x;
@@ -524,9 +596,10 @@ __device__ __forceinline__ void plan_lists(const PlanParams &p) {
 
 // Bound by its bytes: 44 us for out and dout of 17400 tokens, 32 heads of 128 (285 MB, 6.5 TB/s).
 // lse in base 2 and dout_i out_i, both as [num_heads, total_q]: a block takes 8 tokens of 8 heads, half
-// a warp (128 dims) or a quarter (64) a row.  The first block makes the lists.
+// a warp (128 dims) or a quarter (64) a row.  The first block makes the lists, for which it spills registers: with
+// the 48 that it would take the others are too few on an SM (44 us against 39 for 15000 tokens, 32 heads of 128).
 template <int HD>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 8)
     grad_stat_kernel(const uint4 *__restrict__ out, const uint4 *__restrict__ dout, const float *__restrict__ lse,
                      float *__restrict__ lse2, float *__restrict__ delta, int total_q, int num_heads,
                      const __grid_constant__ PlanParams plan) {
@@ -1077,7 +1150,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             }
             ++items;
             const int r_first = first_query(t);
-            for (int i = 0; ok && i < t.n * p.group; ++i, ++J) {
+            for (int i = t.from; ok && i < t.to; ++i, ++J) {
                 const uint32_t st = J & 1;
                 const int r = r_first + i % t.n * BN, head = kvh * p.group + i / t.n;
                 // (dout's stage is free first: dV comes before dK.  The copies of a tile that is edited
@@ -1130,7 +1203,8 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
         bool ok = true;
         int e, kvh;
         for (int k = 0; ok && item_of(k, count, p.num_kv_heads, e, kvh); ++k) {
-            const int n = load_entry(p.k_list, e).n * p.group;
+            const KTile t = load_entry(p.k_list, e);
+            const int n = t.to - t.from;
             if (n == 0) continue;
             const uint32_t res = items % NR;
             ok = wait(res_full(res), (items / NR) & 1) && wait(B_AFULL + (J & 1), (J >> 1) & 1);
@@ -1214,7 +1288,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
                     bias_step = head_bytes / 4;
                 }
             }
-            for (int g = 0, q = 0; g < p.group; ++J) {
+            for (int i = t.from, g = t.from / t.n, q = t.from % t.n; i < t.to; ++i, ++J) {
                 const uint32_t st = J & 1;
                 const int pos0 = pos_first + q * BN;
                 if (!wait_warp(bar(B_AFULL + st), (J >> 1) & 1, c.abort_flag, p.err, kTimeoutNs) ||
@@ -1316,9 +1390,54 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
             const int64_t stride = wg ? p.dk_stride : p.dv_stride;
             __nv_bfloat16 *dst = (wg ? dk : dv) + static_cast<int64_t>(row) * stride;
             const bool v8 = aligned32(wg ? p.dk : p.dv, stride);
+            const float f = wg ? p.scale : 1.f;
+            const uint32_t acc = c.tmem + t_lane + (wg ? kDk : kDv);
+            if (t.parts == 1) {
 #pragma unroll 1
-            for (int cc = 0; cc < HD / 32; ++cc)
-                store_chunk(c.tmem + t_lane + (wg ? kDk : kDv) + cc * 32, wg ? p.scale : 1.f, dst + cc * 32, row < rows, v8);
+                for (int cc = 0; cc < HD / 32; ++cc) store_chunk(acc + cc * 32, f, dst + cc * 32, row < rows, v8);
+            } else {
+                const int slot = t.slot + kvh * t.parts;
+                auto sums = [&](int part, int c4) -> float4 * {
+                    return reinterpret_cast<float4 *>(p.split) + (static_cast<int64_t>(2 * (slot + part) + wg) * (HD / 4) + c4) * 128 + row;
+                };
+#pragma unroll 1
+                for (int cc = 0; cc < HD / 32; ++cc) {
+                    float o[32];
+                    tmem_ld_32x32b_x32(acc + cc * 32, o);
+                    tmem_wait_ld_regs(o);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) *sums(t.part, 8 * cc + x) = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                }
+                // The last of the parts' warps w has all of their sums of its rows.
+                __threadfence();
+                __syncwarp();
+                int before = 0;
+                if (lane == 0) before = atomicAdd(p.arrived + 8 * slot + warp, 1);
+                before = __shfl_sync(0xffffffffu, before, 0);
+                if (before == t.parts - 1) {
+                    __threadfence();
+#pragma unroll 1
+                    for (int c4 = 0; c4 < HD / 4; c4 += 4) {
+                        float4 o[4] = {};
+#pragma unroll 4
+                        for (int part = 0; part < t.parts; ++part) {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const float4 s = __ldcg(sums(part, c4 + x));
+                                o[x].x += s.x, o[x].y += s.y, o[x].z += s.z, o[x].w += s.w;
+                            }
+                        }
+                        if (row < rows) {
+                            uint4 *d4 = reinterpret_cast<uint4 *>(dst + 4 * c4);
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                d4[x] = make_uint4(pack_bf16x2(o[2 * x].x * f, o[2 * x].y * f), pack_bf16x2(o[2 * x].z * f, o[2 * x].w * f),
+                                                   pack_bf16x2(o[2 * x + 1].x * f, o[2 * x + 1].y * f),
+                                                   pack_bf16x2(o[2 * x + 1].z * f, o[2 * x + 1].w * f));
+                        }
+                    }
+                }
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(B_ACCFREE));
@@ -1363,15 +1482,27 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // Most tiles that sequences of `total` rows in all can have.
 int64_t most_tiles(int total, int num_seqs) { return static_cast<int64_t>(total) / BM + num_seqs; }
 
-// The workspace: lse2, delta, counts, lists, partial sums.
+// Places for the sums of split key tiles: tiles of fewer steps than kMinSteps have none, others less than a
+// quarter of their steps.
+int split_slots(int total_q, int total_k, int num_seqs, int num_heads) {
+    const double steps = static_cast<double>(most_tiles(total_q, num_seqs)) * most_tiles(total_k, num_seqs) * num_heads;
+    return steps / 4 < kMaxSlots ? static_cast<int>(steps / 4) : kMaxSlots;
+}
+
+// The workspace: lse2, delta, counts, lists, partial sums of dbias, sums of split key tiles (for 128 dims) and
+// their counters.
 struct Workspace {
-    size_t stat, q_list, k_list, partial;
-    size_t bytes() const { return 2 * stat + 256 + q_list + k_list + partial; }
+    int slots;
+    size_t stat, q_list, k_list, partial, split, arrived;
+    size_t bytes() const { return 2 * stat + 256 + q_list + k_list + partial + split + arrived; }
     Workspace(int total_q, int total_k, int num_seqs, int num_heads, int num_buckets)
-        : stat(up256(static_cast<size_t>(total_q) * num_heads * sizeof(float))),
+        : slots(split_slots(total_q, total_k, num_seqs, num_heads)),
+          stat(up256(static_cast<size_t>(total_q) * num_heads * sizeof(float))),
           q_list(up256(most_tiles(total_q, num_seqs) * sizeof(QTile))),
-          k_list(up256(most_tiles(total_k, num_seqs) * sizeof(KTile))),
-          partial(up256(static_cast<size_t>(most_tiles(total_q, num_seqs)) * num_heads * 8 * num_buckets * sizeof(float))) {}
+          k_list(up256((most_tiles(total_k, num_seqs) + slots) * sizeof(KTile))),
+          partial(up256(static_cast<size_t>(most_tiles(total_q, num_seqs)) * num_heads * 8 * num_buckets * sizeof(float))),
+          split(static_cast<size_t>(slots) * 2 * BM * 128 * sizeof(float)),
+          arrived(up256(static_cast<size_t>(slots) * 8 * sizeof(int))) {}
 };
 
 template <class Kernel>
@@ -1407,7 +1538,7 @@ cudaError_t launch_backward_d(GradParams &p, const PlanParams &plan, const Packe
     cudaError_t e = cudaGetLastError();
     static std::atomic<uint64_t> set[2];
     const int64_t q_items = a.total_q > 0 ? most_tiles(a.total_q, a.num_seqs) * a.num_heads : 0;
-    const int64_t k_items = a.total_k > 0 ? most_tiles(a.total_k, a.num_seqs) * a.num_kv_heads : 0;
+    const int64_t k_items = a.total_k > 0 ? (most_tiles(a.total_k, a.num_seqs) + plan.slots) * a.num_kv_heads : 0;
     if (e == cudaSuccess) e = launch_tiles(grad_q_kernel<HD, BIAS>, LayoutQ<HD, BIAS>::SMEM, set[0], q_items, p, stream);
     if (e == cudaSuccess) e = launch_tiles(grad_kv_kernel<HD, BIAS>, LayoutKv<HD, BIAS>::SMEM, set[1], k_items, p, stream);
     if (BIAS && e == cudaSuccess) {
@@ -1456,6 +1587,9 @@ cudaError_t launch_packed_attn_backward(const PackedGradArgs &g, cudaStream_t st
     plan.window = a.sliding_window;
     plan.most[0] = static_cast<int>(most_tiles(a.total_q, a.num_seqs));
     plan.most[1] = static_cast<int>(most_tiles(a.total_k, a.num_seqs));
+    plan.num_kv_heads = a.num_kv_heads;
+    plan.group = a.num_heads / a.num_kv_heads;
+    plan.slots = w.slots;
     plan.counts = reinterpret_cast<int *>(take(256));
     plan.q_list = reinterpret_cast<QTile *>(take(w.q_list));
     plan.k_list = reinterpret_cast<KTile *>(take(w.k_list));
@@ -1464,6 +1598,8 @@ cudaError_t launch_packed_attn_backward(const PackedGradArgs &g, cudaStream_t st
     p.q_list = plan.q_list;
     p.k_list = plan.k_list;
     p.partial = reinterpret_cast<float *>(take(w.partial));
+    p.split = reinterpret_cast<float *>(take(w.split));
+    p.arrived = plan.arrived = reinterpret_cast<int *>(take(w.arrived));
     p.bias_table = a.bias_table;
     p.total_q = a.total_q;
     p.total_k = a.total_k;

@@ -280,6 +280,29 @@ def test_rows_behind_the_last_sequence_and_what_stands_beside_a_sequence():
             assert np.abs(f64(got[a:b]) - want[name][a:b]).max() < 0.1, name  # (bounds are the other tests')
 
 
+@pytest.mark.parametrize("heads,hkv,dim", [(16, 1, 64), (16, 1, 128), (27, 3, 128), (9, 1, 64)])
+@pytest.mark.parametrize("window,buckets,distance", [(0, 0, 0), (0, 32, 128), (333, 16, 500)])
+def test_few_kv_heads_of_many_queries(heads, hkv, dim, window, buckets, distance):
+    """Key tiles of many steps, which several blocks share: sums in parts, the same bits every time."""
+    c = Case([901, 0, 40, 128, 1], [901, 20, 300, 128, 700], heads, hkv, dim, window, buckets, distance, seed=8)
+    out, lse, grads = both(c)
+    check(c, out, lse, grads)
+    again = [torch.full_like(x, 7.0) for x in grads if x is not None]
+    kw = dict(zip(("dq", "dk", "dv", "dbias"), again))
+    graph = torch.cuda.CUDAGraph()
+    cu_q, cu_k = dev(c.cu_q), dev(c.cu_k)
+    with torch.cuda.graph(graph):
+        pa.pa_varlen_attn_backward(c.dout, c.q, c.k, c.v, out, lse, cu_q, cu_k, c.max_q, c.max_k, c.scale, c.window, bias=c.bias,
+                                   max_distance=c.distance, **kw)
+    for _ in range(3):
+        for x in again:
+            x.fill_(7.0)
+        graph.replay()
+        for x, y in zip(again, grads):
+            assert torch.equal(x, y)
+    assert pa.pa_read_device_error() == 0
+
+
 def test_bad_offsets_are_flagged_and_left_out():
     c = Case([40, 40, 40], [40, 40, 40], 4, 2, 64, 0, 32, 128)
     good = both(c)
