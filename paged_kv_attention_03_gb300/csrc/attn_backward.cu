@@ -405,8 +405,8 @@ struct PlanParams {
 };
 constexpr int kPlanBins = 1024;  // longer tiles share the last bin
 // Key tiles of more steps than an SM's share and 8 more are split: few kv heads with many queries each have
-// few long items (3 sequences of 293-2336 tokens, 40/4 heads: 180 steps for the longest, 55 for an SM's
-// share; one of 16384, 8/1 heads: 1024 and 434).  Parts leave their sums in fp32; the last one to arrive, warp
+// few long items.  dK/dV with and without: one sequence of 2048, 16/1 heads 59 and 367 us, of 4096, 8/2 heads 64
+// and 178, of 16384, 8/1 heads 820 and 1369.  Parts leave their sums in fp32; the last one to arrive, warp
 // by warp, adds them up in the parts' order.  A part costs about five steps, for its keys and its sums.  So many
 // slots suffice: a split tile has fewer parts than twice its steps over an SM's share.
 constexpr int kMinSteps = 8, kMaxSlots = 2 * kPlanSms + 1;
