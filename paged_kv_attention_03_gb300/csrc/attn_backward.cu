@@ -59,7 +59,7 @@ constexpr int BM = 128;                 // rows (TMEM lanes) of a tile
 constexpr int BN = 128;                 // columns of a tile
 constexpr uint32_t HALF = 128u * 128u;  // [128 rows][64 bf16]: one swizzle span
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpMma2 = 10;
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;  // (whole warpgroups: the last warp has no work)
 constexpr uint32_t kTmemCols = 512;
 // Rows of fewer keys get their D from the sum over the keys also for dQ.  dout . out is off by about
 // 2^-9 |dout . out|, and |dout . out| shrinks against dP as the root of the number of keys that share
@@ -692,125 +692,132 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
         return s;
     };
 
-    if (warp == kWarpLoad) {
-        if (lane < 4) prefetch_tmap(lane == 0 ? p.tmap_q : lane == 1 ? p.tmap_do : lane == 2 ? p.tmap_k : p.tmap_v);
-        uint32_t lands = 0, items = 0, J = 0, sa = 0, pa = 1;  // ring A: stage, phase of its emptying
-        bool ok = true;
-        int e, h;
-        for (int k = 0; ok && item_of(k, count, p.num_heads, e, h); ++k) {
-            const QTile t = load_entry(p.q_list, e);
-            if (t.n == 0) continue;
-            const Steps s = steps_of(t);
-            const uint32_t res = items % NR;
-            if (items >= NR && !wait_warp(bar(res_empty(res)), (items / NR - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-            // (Sums along diagonals run across rows; in all else a row behind the sequence stays on its own.)
-            const bool edit = BIAS && ragged(t.left);
-            const uint32_t land = bar(edit ? B_LAND : res_full(res));
-            if (lane == 0) mbar_arrive_expect_tx(land, 2 * L::TILE);
-            __syncwarp();
-            load_tile<HD>(p.tmap_q, sQ(res), h, t.row, 0, t.left, land);
-            load_tile<HD>(p.tmap_do, sDo(res), h, t.row, 0, t.left, land);
-            if (edit) {
-                if (!wait_warp(land, lands++ & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-                clear_rows<HD>(sQ(res), t.left);
-                clear_rows<HD>(sDo(res), t.left);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(res_full(res)));
-            }
-            if (table_here) {
-                const uint32_t slot = items & 1;
-                if (items >= 2 && !wait_warp(bar(B_TABFREE + slot), ((items >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bar(B_TABFULL + slot), table_bytes);
-                    bulk_load(c.base + L::OFF_SMALL + kSmallQBias + slot * kTableBytesQ, bias_row_of(p.bias_table, h, last) - kNearPad,
-                              table_bytes, bar(B_TABFULL + slot));
-                }
-                __syncwarp();
-            }
-            ++items;
-            const int kvh = h / p.group;
-            for (int j = 0; j < s.n_all; ++j, ++J) {
-                const uint32_t sb = J % NB, full_k = bar(B_AFULL + sa), full_v = bar(B_BFULL + sb);
-                const int row0 = (s.kt0 + s.tile(j)) * BN;
-                const bool cut = ragged(t.sk - row0);  // (the copies of tiles that are edited land together)
-                ok = J < NA || wait_warp(bar(B_AEMPTY + sa), pa, c.abort_flag, p.err, kTimeoutNs);
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(cut ? bar(B_LAND) : full_k, cut ? 2 * L::TILE : L::TILE);
-                __syncwarp();
-                load_tile<HD>(p.tmap_k, sK(sa), kvh, t.k_start, row0, t.sk, cut ? bar(B_LAND) : full_k);
-                ok = J < NB || wait_warp(bar(B_BEMPTY + sb), (J / NB - 1) & 1, c.abort_flag, p.err, kTimeoutNs);
-                if (!ok) break;
-                if (lane == 0 && !cut) mbar_arrive_expect_tx(full_v, L::TILE);
-                __syncwarp();
-                load_tile<HD>(p.tmap_v, sV(sb), kvh, t.k_start, row0, t.sk, cut ? bar(B_LAND) : full_v);
-                if (cut) {
-                    ok = wait_warp(bar(B_LAND), lands++ & 1, c.abort_flag, p.err, kTimeoutNs);
-                    if (!ok) break;
-                    clear_rows<HD>(sK(sa), t.sk - row0);
-                    clear_rows<HD>(sV(sb), t.sk - row0);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full_k), mbar_arrive(full_v);
-                }
-                if (++sa == NA) sa = 0, pa ^= 1u;
-            }
-        }
-    } else if (warp == kWarpMma || warp == kWarpMma2) {
-        // One warp issues S and dP, the other dQ, so that neither's waits hold up the other's products.
-        // The whole warp waits, one lane issues (always the same: a commit covers what its thread issued).
-        auto wait = [&](int b, uint32_t parity) {
-            const bool ok = wait_warp(bar(b), parity, c.abort_flag, p.err, kTimeoutNs);
-            tc_fence_after();
-            return ok;
-        };
-        uint32_t items = 0, J = 0, sa = 0, pa = 0;  // stage of ring A and its phase
-        bool ok = true;
-        int e, h;
-        for (int k = 0; ok && item_of(k, count, p.num_heads, e, h); ++k) {
-            const QTile t = load_entry(p.q_list, e);
-            if (t.n == 0) continue;
-            const Steps s = steps_of(t);
-            if (warp == kWarpMma) {
+    // With a bias, registers go from the warps that load and issue to the element-wise ones, which spill with
+    // 168 (304 us against 293 for 16 sequences of 128-2048 tokens, 32/8 heads; without a bias the split costs
+    // two documents of 6000-8192 tokens 12 us of 664): 384 threads of 168 are 256 of 208 and 128 of 88.
+    if (warp >= 8) {
+        if constexpr (BIAS) setmaxnreg_dec<88>();
+        if (warp == kWarpLoad) {
+            if (lane < 4) prefetch_tmap(lane == 0 ? p.tmap_q : lane == 1 ? p.tmap_do : lane == 2 ? p.tmap_k : p.tmap_v);
+            uint32_t lands = 0, items = 0, J = 0, sa = 0, pa = 1;  // ring A: stage, phase of its emptying
+            bool ok = true;
+            int e, h;
+            for (int k = 0; ok && item_of(k, count, p.num_heads, e, h); ++k) {
+                const QTile t = load_entry(p.q_list, e);
+                if (t.n == 0) continue;
+                const Steps s = steps_of(t);
                 const uint32_t res = items % NR;
-                ok = wait(res_full(res), (items / NR) & 1);
-                for (int j = 0; ok && j < s.n_all; ++j, ++J) {
-                    const uint32_t sb = J % NB, sd = J & 1;  // stage of V, place of dP
-                    ok = wait(B_AFULL + sa, pa) && (J == 0 || wait(B_PFULL, (J - 1) & 1));
-                    if (!ok) break;
-                    if (elect_one()) {
-                        issue_abt<HD>(c.tmem, sQ(res), sK(sa));
-                        mma_commit(bar(B_SFULL));
+                if (items >= NR && !wait_warp(bar(res_empty(res)), (items / NR - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+                // (Sums along diagonals run across rows; in all else a row behind the sequence stays on its own.)
+                const bool edit = BIAS && ragged(t.left);
+                const uint32_t land = bar(edit ? B_LAND : res_full(res));
+                if (lane == 0) mbar_arrive_expect_tx(land, 2 * L::TILE);
+                __syncwarp();
+                load_tile<HD>(p.tmap_q, sQ(res), h, t.row, 0, t.left, land);
+                load_tile<HD>(p.tmap_do, sDo(res), h, t.row, 0, t.left, land);
+                if (edit) {
+                    if (!wait_warp(land, lands++ & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+                    clear_rows<HD>(sQ(res), t.left);
+                    clear_rows<HD>(sDo(res), t.left);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(res_full(res)));
+                }
+                if (table_here) {
+                    const uint32_t slot = items & 1;
+                    if (items >= 2 && !wait_warp(bar(B_TABFREE + slot), ((items >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar(B_TABFULL + slot), table_bytes);
+                        bulk_load(c.base + L::OFF_SMALL + kSmallQBias + slot * kTableBytesQ, bias_row_of(p.bias_table, h, last) - kNearPad,
+                                  table_bytes, bar(B_TABFULL + slot));
                     }
                     __syncwarp();
-                    // (dP goes where dS of the step before the last one was: its dQ has to be done.)
-                    ok = wait(B_BFULL + sb, (J / NB) & 1) && (J < 2 || wait(B_DQDONE + sd, ((J >> 1) - 1) & 1));
+                }
+                ++items;
+                const int kvh = h / p.group;
+                for (int j = 0; j < s.n_all; ++j, ++J) {
+                    const uint32_t sb = J % NB, full_k = bar(B_AFULL + sa), full_v = bar(B_BFULL + sb);
+                    const int row0 = (s.kt0 + s.tile(j)) * BN;
+                    const bool cut = ragged(t.sk - row0);  // (the copies of tiles that are edited land together)
+                    ok = J < NA || wait_warp(bar(B_AEMPTY + sa), pa, c.abort_flag, p.err, kTimeoutNs);
                     if (!ok) break;
-                    if (elect_one()) {
-                        issue_abt<HD>(c.tmem + kDp + 128u * sd, sDo(res), sV(sb));
-                        mma_commit(bar(B_DPFULL + sd));
-                        mma_commit(bar(B_BEMPTY + sb));
-                        if (j + 1 == s.n_all) mma_commit(bar(res_empty(res)));
-                    }
+                    if (lane == 0) mbar_arrive_expect_tx(cut ? bar(B_LAND) : full_k, cut ? 2 * L::TILE : L::TILE);
                     __syncwarp();
+                    load_tile<HD>(p.tmap_k, sK(sa), kvh, t.k_start, row0, t.sk, cut ? bar(B_LAND) : full_k);
+                    ok = J < NB || wait_warp(bar(B_BEMPTY + sb), (J / NB - 1) & 1, c.abort_flag, p.err, kTimeoutNs);
+                    if (!ok) break;
+                    if (lane == 0 && !cut) mbar_arrive_expect_tx(full_v, L::TILE);
+                    __syncwarp();
+                    load_tile<HD>(p.tmap_v, sV(sb), kvh, t.k_start, row0, t.sk, cut ? bar(B_LAND) : full_v);
+                    if (cut) {
+                        ok = wait_warp(bar(B_LAND), lands++ & 1, c.abort_flag, p.err, kTimeoutNs);
+                        if (!ok) break;
+                        clear_rows<HD>(sK(sa), t.sk - row0);
+                        clear_rows<HD>(sV(sb), t.sk - row0);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(full_k), mbar_arrive(full_v);
+                    }
                     if (++sa == NA) sa = 0, pa ^= 1u;
                 }
-            } else {
-                for (int j = 0; j < s.n_all; ++j, ++J) {
-                    const bool first = s.first_dq(j);
-                    ok = wait(B_DSFULL + (J & 1), (J >> 1) & 1) && (!first || items == 0 || wait(B_ACCFREE, (items - 1) & 1));
-                    if (!ok) break;
-                    if (elect_one()) {
-                        if (!s.sum_only(j)) issue_ab<HD>(c.tmem + kDq, c.tmem + kDp + 128u * (J & 1), sK(sa), first);
-                        mma_commit(bar(B_DQDONE + (J & 1)));
-                        mma_commit(bar(B_AEMPTY + sa));
-                        if (j + 1 == s.n_all) mma_commit(bar(B_DONE));
-                    }
-                    __syncwarp();
-                    if (++sa == NA) sa = 0;
-                }
             }
-            ++items;
+        } else if (warp == kWarpMma || warp == kWarpMma2) {
+            // One warp issues S and dP, the other dQ, so that neither's waits hold up the other's products.
+            // The whole warp waits, one lane issues (always the same: a commit covers what its thread issued).
+            auto wait = [&](int b, uint32_t parity) {
+                const bool ok = wait_warp(bar(b), parity, c.abort_flag, p.err, kTimeoutNs);
+                tc_fence_after();
+                return ok;
+            };
+            uint32_t items = 0, J = 0, sa = 0, pa = 0;  // stage of ring A and its phase
+            bool ok = true;
+            int e, h;
+            for (int k = 0; ok && item_of(k, count, p.num_heads, e, h); ++k) {
+                const QTile t = load_entry(p.q_list, e);
+                if (t.n == 0) continue;
+                const Steps s = steps_of(t);
+                if (warp == kWarpMma) {
+                    const uint32_t res = items % NR;
+                    ok = wait(res_full(res), (items / NR) & 1);
+                    for (int j = 0; ok && j < s.n_all; ++j, ++J) {
+                        const uint32_t sb = J % NB, sd = J & 1;  // stage of V, place of dP
+                        ok = wait(B_AFULL + sa, pa) && (J == 0 || wait(B_PFULL, (J - 1) & 1));
+                        if (!ok) break;
+                        if (elect_one()) {
+                            issue_abt<HD>(c.tmem, sQ(res), sK(sa));
+                            mma_commit(bar(B_SFULL));
+                        }
+                        __syncwarp();
+                        // (dP goes where dS of the step before the last one was: its dQ has to be done.)
+                        ok = wait(B_BFULL + sb, (J / NB) & 1) && (J < 2 || wait(B_DQDONE + sd, ((J >> 1) - 1) & 1));
+                        if (!ok) break;
+                        if (elect_one()) {
+                            issue_abt<HD>(c.tmem + kDp + 128u * sd, sDo(res), sV(sb));
+                            mma_commit(bar(B_DPFULL + sd));
+                            mma_commit(bar(B_BEMPTY + sb));
+                            if (j + 1 == s.n_all) mma_commit(bar(res_empty(res)));
+                        }
+                        __syncwarp();
+                        if (++sa == NA) sa = 0, pa ^= 1u;
+                    }
+                } else {
+                    for (int j = 0; j < s.n_all; ++j, ++J) {
+                        const bool first = s.first_dq(j);
+                        ok = wait(B_DSFULL + (J & 1), (J >> 1) & 1) && (!first || items == 0 || wait(B_ACCFREE, (items - 1) & 1));
+                        if (!ok) break;
+                        if (elect_one()) {
+                            if (!s.sum_only(j)) issue_ab<HD>(c.tmem + kDq, c.tmem + kDp + 128u * (J & 1), sK(sa), first);
+                            mma_commit(bar(B_DQDONE + (J & 1)));
+                            mma_commit(bar(B_AEMPTY + sa));
+                            if (j + 1 == s.n_all) mma_commit(bar(B_DONE));
+                        }
+                        __syncwarp();
+                        if (++sa == NA) sa = 0;
+                    }
+                }
+                ++items;
+            }
         }
-    } else if (warp < 8) {
+    } else {
+        if constexpr (BIAS) setmaxnreg_inc<208>();
         const int wg = warp >> 2, quarter = warp & 3;
         const int row = quarter * 32 + lane;  // (of D and dQ)
         const int r0 = quarter * 32 + (lane >> 2), c0 = lane & 3;  // first row of the block, columns 2 c0, 2 c0 + 1
