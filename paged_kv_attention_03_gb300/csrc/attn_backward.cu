@@ -31,13 +31,13 @@
 // tile they came from, and are the first operand of the next product from there.
 //
 // Measured (packed sequences, 32/8 heads of 128; the products of each kernel over its time):
-//  * two of 6000-8192 tokens, no bias: dQ 664 us (1.69 PFLOP/s of three products, 0.87 of the bf16
-//    peak), dK/dV 891 us (1.68): products nearly back to back; the rest are the waits between them;
-//  * sixteen of 128-2048 tokens, 32 buckets to 128: dQ 304 us (0.78), dK/dV 277 us (1.15).  A block of
+//  * two of 6000-8192 tokens, no bias: dQ 658 us (1.70 PFLOP/s of three products, 0.88 of the bf16
+//    peak), dK/dV 896 us (1.67): products nearly back to back; the rest are the waits between them;
+//  * sixteen of 128-2048 tokens, 32 buckets to 128: dQ 294 us (0.81), dK/dV 280 us (1.14).  A block of
 //    dQ takes 216 steps, 58 of them near tiles, in 30 items of which the last step's chain (logits, D,
 //    dS, diagonals, product, rows out) has nothing beside it;
 //  * 128 of 128 tokens, where an item is one step: dQ 96 us without a bias (the bytes alone take 69),
-//    131 with one, dK/dV 77 and 79 (59).
+//    119 with one, dK/dV 77 and 79 (59).
 #include <cuda.h>
 
 #include <atomic>
@@ -296,7 +296,7 @@ __device__ __forceinline__ void zero_rows(__nv_bfloat16 *dst, int64_t stride, in
 // Row - column is then the same for all (a, b) with the same a - b, 11 pairs of distances for 64 elements:
 // a bias costs a thread 22 reads, masks are 22 comparisons, and sums along diagonals begin with additions in
 // registers.  (A thread a row needs 64 reads, comparisons and shuffles: dQ of 16 sequences of 128-2048 tokens,
-// 32/8 heads of 128 took 375 us that way, 304 this way; without a bias of two documents of 6000-8192 tokens
+// 32/8 heads of 128 took 375 us that way, 318 this way, 294 with what followed; without a bias of two documents of 6000-8192 tokens
 // 648 against 664.)
 __device__ __forceinline__ int pair_at(int a, int b) { return 4 * b + 2 * (a & 1); }
 __device__ __forceinline__ uint64_t block_pair(const float (&w)[2][32], int a, int b) {
