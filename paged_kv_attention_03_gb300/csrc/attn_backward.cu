@@ -596,20 +596,28 @@ __device__ __forceinline__ void plan_lists(const PlanParams &p) {
 
 // Bound by its bytes: 44 us for out and dout of 17400 tokens, 32 heads of 128 (285 MB, 6.5 TB/s).
 // lse in base 2 and dout_i out_i, both as [num_heads, total_q]: a block takes 8 tokens of 8 heads, half
-// a warp (128 dims) or a quarter (64) a row.  The first block makes the lists, for which it spills registers: with
-// the 48 that it would take the others are too few on an SM (44 us against 39 for 15000 tokens, 32 heads of 128).
+// a warp (128 dims) or a quarter (64) a row.  The blocks behind the first write the bias by distance (with a
+// launch of its own the smallest training step took 72 us, the host's, instead of 64-69).  The first block makes
+// the lists, for which it spills registers: with the 48 that it would take the others are too few on an SM
+// (44 us against 39 for 15000 tokens, 32 heads of 128).
 template <int HD>
 __global__ void __launch_bounds__(256, 8)
     grad_stat_kernel(const uint4 *__restrict__ out, const uint4 *__restrict__ dout, const float *__restrict__ lse,
                      float *__restrict__ lse2, float *__restrict__ delta, int total_q, int num_heads,
-                     const __grid_constant__ PlanParams plan) {
+                     const __grid_constant__ PlanParams plan, float *__restrict__ table, const __grid_constant__ RelativeBias bias,
+                     int table_blocks) {
     constexpr int LANES = HD / 8, ROWS = 256 / LANES;
     __shared__ float s_l[8][9], s_d[8][9];  // [head][token]
     if (blockIdx.x == 0) {
         if (blockIdx.y == 0) plan_lists(plan);
         return;
     }
-    const int t0 = (blockIdx.x - 1) * 8, h0 = blockIdx.y * 8;
+    const int h0 = blockIdx.y * 8;
+    if (static_cast<int>(blockIdx.x) <= table_blocks) {
+        bias_table_entry(table, bias, num_heads, (blockIdx.x - 1) * 256 + threadIdx.x, h0, 1, min(h0 + 8, num_heads));
+        return;
+    }
+    const int t0 = (blockIdx.x - 1 - table_blocks) * 8;
     const int l = threadIdx.x % LANES;
 #pragma unroll
     for (int r = threadIdx.x / LANES; r < 64; r += ROWS) {
@@ -1539,9 +1547,11 @@ cudaError_t launch_backward_d(GradParams &p, const PlanParams &plan, const Packe
         !rows_map(p.tmap_k, a.k, a.q, a.num_kv_heads, a.total_k, a.k_stride) ||
         !rows_map(p.tmap_v, a.v, a.q, a.num_kv_heads, a.total_k, a.v_stride))
         return cudaErrorInvalidValue;
-    const dim3 grid((a.total_q + 7) / 8 + 1, (a.num_heads + 7) / 8);
+    const int table_blocks = BIAS ? (bias_stride(a.bias.last()) + 255) / 256 : 0;
+    const dim3 grid((a.total_q + 7) / 8 + 1 + table_blocks, (a.num_heads + 7) / 8);
     grad_stat_kernel<HD><<<grid, 256, 0, stream>>>(static_cast<const uint4 *>(g.out), static_cast<const uint4 *>(g.dout), g.lse,
-                                                   const_cast<float *>(p.lse2), p.delta, a.total_q, a.num_heads, plan);
+                                                   const_cast<float *>(p.lse2), p.delta, a.total_q, a.num_heads, plan,
+                                                   const_cast<float *>(a.bias_table), a.bias, table_blocks);
     cudaError_t e = cudaGetLastError();
     static std::atomic<uint64_t> set[2];
     const int64_t q_items = a.total_q > 0 ? most_tiles(a.total_q, a.num_seqs) * a.num_heads : 0;

@@ -163,11 +163,7 @@ pa_status pa_varlen_attn_backward(void *dq, void *dk, void *dv, float *dbias, in
     const size_t table = bias ? pa::bias_table_bytes(num_heads, a.bias) : 0;
     if (need + table > 0 && (!workspace || workspace_bytes < need + table || !aligned(workspace, 256))) return PA_ERR_INVALID_ARG;
     a.err = pa::device_error_word();
-    if (bias) {
-        a.bias_table = static_cast<float *>(workspace);
-        st = pa::cuda_status(pa::launch_bias_table(static_cast<float *>(workspace), num_heads, a.bias, s));
-        if (st != PA_OK) return st;
-    }
+    if (bias) a.bias_table = static_cast<float *>(workspace);
     g.out = out;
     g.dout = dout;
     g.lse = lse;

@@ -259,7 +259,7 @@ struct PackedArgs {
     int sliding_window;
     float scale;
     RelativeBias bias;        // bias.bias null: none
-    const float *bias_table;  // its table (launch_bias_table), null without a bias
+    const float *bias_table;  // its table (launch_bias_table; the gradient writes it itself), null without a bias
     unsigned *err;
 };
 cudaError_t launch_packed_attn(const PackedArgs &a, void *out, float *lse, cudaStream_t stream);

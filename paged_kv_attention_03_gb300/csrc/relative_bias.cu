@@ -47,16 +47,7 @@ bool reaches(int n, int m, int d, int r, int j) {
 // an element where the bucket's search would take five steps.
 __global__ void __launch_bounds__(128)
     bias_table_kernel(float *__restrict__ table, const __grid_constant__ RelativeBias b, int num_heads) {
-    const int stride = bias_stride(b.last());
-    const int i = blockIdx.x * 128 + threadIdx.x;
-    if (i >= stride) return;
-    const int k = bucket_of(b, max(i - kBiasPad, 0));
-    // (A block's heads in turn: the search is shared.)
-    for (int h = blockIdx.y; h < num_heads; h += gridDim.y) {
-        const float far = bias_log2(b.bias[static_cast<int64_t>(b.num_buckets - 1) * num_heads + h]);
-        const float v = bias_log2(b.bias[static_cast<int64_t>(k) * num_heads + h]);
-        table[static_cast<int64_t>(h) * stride + i] = i == 0 ? far : i < kBiasPad ? -INFINITY : v - bias_ref(far);
-    }
+    bias_table_entry(table, b, num_heads, blockIdx.x * 128 + threadIdx.x, blockIdx.y, gridDim.y, num_heads);
 }
 
 }  // namespace

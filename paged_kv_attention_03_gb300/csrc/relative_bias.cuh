@@ -45,4 +45,17 @@ __device__ __forceinline__ int bucket_of(const RelativeBias &b, int n) {
     return lo;
 }
 
+// Entry i of the rows of heads h, h + step, ... below end.  (The heads share the search.)
+__device__ __forceinline__ void bias_table_entry(float *__restrict__ table, const RelativeBias &b, int num_heads, int i, int h, int step,
+                                                 int end) {
+    const int stride = bias_stride(b.last());
+    if (i >= stride) return;
+    const int k = bucket_of(b, max(i - kBiasPad, 0));
+    for (; h < end; h += step) {
+        const float far = bias_log2(b.bias[static_cast<int64_t>(b.num_buckets - 1) * num_heads + h]);
+        const float v = bias_log2(b.bias[static_cast<int64_t>(k) * num_heads + h]);
+        table[static_cast<int64_t>(h) * stride + i] = i == 0 ? far : i < kBiasPad ? -INFINITY : v - bias_ref(far);
+    }
+}
+
 }  // namespace pa
