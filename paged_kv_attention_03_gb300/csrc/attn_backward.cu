@@ -837,30 +837,30 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
         const bool v8 = aligned32(p.dq, p.dq_stride);
         uint32_t items = 0, J = 0;
         bool ok = true;
-        int e, h;
-        bool more = item_of(0, count, p.num_heads, e, h);
+        int next_entry, next_head;
+        bool more = item_of(0, count, p.num_heads, next_entry, next_head);
         QTile next{};
         float next_lse[4] = {}, next_delta[4] = {}, next_far = 0.f;
         auto prefetch = [&] {  // what the next item needs of its rows and its head
-            next = load_entry(p.q_list, e);
-            const int64_t at = static_cast<int64_t>(h) * p.total_q + next.row;
+            next = load_entry(p.q_list, next_entry);
+            const int64_t at = static_cast<int64_t>(next_head) * p.total_q + next.row;
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
                 const int x = r0 + 8 * a;
                 next_lse[a] = x < next.left ? p.lse2[at + x] : INFINITY;
                 next_delta[a] = x < next.left ? p.delta[at + x] : 0.f;
             }
-            if (BIAS) next_far = __ldg(bias_row_of(p.bias_table, h, last) - kBiasPad);
+            if (BIAS) next_far = __ldg(bias_row_of(p.bias_table, next_head, last) - kBiasPad);
         };
         if (more) prefetch();
         for (int k = 0; ok && more; ++k) {
             const QTile t = next;
-            const int head = h;
+            const int head = next_head;
             float lse2[4], delta[4];
 #pragma unroll
             for (int a = 0; a < 4; ++a) lse2[a] = next_lse[a], delta[a] = next_delta[a];
             [[maybe_unused]] const float last_bias = next_far;
-            more = item_of(k + 1, count, p.num_heads, e, h);
+            more = item_of(k + 1, count, p.num_heads, next_entry, next_head);
             const int rows = min(t.left, BM);
             const int64_t stat_row = static_cast<int64_t>(head) * p.total_q + t.row;
             __nv_bfloat16 *dq = p.dq + static_cast<int64_t>(t.row) * p.dq_stride + head * HD;
@@ -1274,18 +1274,19 @@ __global__ void __launch_bounds__(kThreads, 1) grad_kv_kernel(const __grid_const
         const uint32_t sc = c.tmem + t_lane + kS + 64u * wg, dp = c.tmem + t_lane + kDp + 64u * wg;
         uint32_t items = 0, J = 0;
         bool ok = true;
-        int e, kvh;
-        bool more = item_of(0, count, p.num_kv_heads, e, kvh);
+        int next_entry, next_kvh;
+        bool more = item_of(0, count, p.num_kv_heads, next_entry, next_kvh);
         KTile next{};
-        if (more) next = load_entry(p.k_list, e);
+        if (more) next = load_entry(p.k_list, next_entry);
         for (int k = 0; ok && more; ++k) {
             const KTile t = next;
+            const int kvh = next_kvh;  // (the place of a split tile's sums goes by it, at the item's end)
             const int head0 = kvh * p.group;
             const int rows = min(t.left, BM);
             __nv_bfloat16 *dk = p.dk + static_cast<int64_t>(t.row) * p.dk_stride + kvh * HD;
             __nv_bfloat16 *dv = p.dv + static_cast<int64_t>(t.row) * p.dv_stride + kvh * HD;
-            more = item_of(k + 1, count, p.num_kv_heads, e, kvh);
-            if (more) next = load_entry(p.k_list, e);
+            more = item_of(k + 1, count, p.num_kv_heads, next_entry, next_kvh);
+            if (more) next = load_entry(p.k_list, next_entry);
             if (t.n == 0) {  // no row sees these keys
                 zero_rows<HD>(dk, p.dk_stride, rows);
                 zero_rows<HD>(dv, p.dv_stride, rows);
