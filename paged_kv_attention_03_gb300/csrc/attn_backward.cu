@@ -6,9 +6,10 @@
 //     dP = dout V^T,   D_i = sum_j P_ij dP_ij,   dS = P (dP - D),
 //     dV = P^T dout,   dQ = scale dS K,   dK = scale dS^T Q,   dbias_b = sum of dS over bucket b.
 // D_i also equals dout_i out_i, but out is bf16 there: good enough inside dQ, whose terms are rounded
-// to bf16 anyway, unless a row's dS nearly cancel, as they do in rows of few keys; and not for sums
-// of dS.  So the dQ kernel starts from dout_i out_i, visits the tiles that need the sum itself once
-// for D and once with it, and leaves D in fp32 for dK.
+// to bf16 anyway, unless a row's dS nearly cancel, as they do where few keys have the weight; and not
+// for sums of dS.  So the dQ kernel starts from dout_i out_i, visits the tiles that need the sum itself once
+// for D and once with it, and leaves D in fp32 for dK.  What dout_i out_i was off by is known at an item's
+// end; where that is more than the rounding of dS may be, for any row, the item is done again with D.
 //
 // Two kernels share the work, each with its accumulators in tensor memory and no atomics, so equal
 // calls give equal bits:
@@ -61,10 +62,14 @@ constexpr uint32_t HALF = 128u * 128u;  // [128 rows][64 bf16]: one swizzle span
 constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpMma2 = 10;
 constexpr int kThreads = 384;  // (whole warpgroups: the last warp has no work)
 constexpr uint32_t kTmemCols = 512;
-// Rows of fewer keys get their D from the sum over the keys also for dQ.  dout . out is off by about
-// 2^-9 |dout . out|, and |dout . out| shrinks against dP as the root of the number of keys that share
-// the weight: from 128 on the error is below a tenth of that of dS in bf16.
+// Rows of fewer keys get their D from the sum over the keys at once also for dQ: few keys share their weight, so
+// that dout . out would mostly have to be done again, and they have two tiles at most.
 constexpr int kFewKeys = 128;
+// A row is done again with D if dout . out, off by x, moves its dS by more in all (x times the weights of
+// the tiles that took it) than half a step of bf16 of each: dout . out is off by about 2^-9 of the root of its terms'
+// squares, so that a weight spread over ten keys or more never is.  Items (128 rows of a head) done again with 2048 keys: none
+// with logits of standard deviation 1, 12 % with 2, nearly all from 3 on, which take twice the products then.
+constexpr float kMoved = 0.00390625f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
 
 // 128 queries of a sequence.
@@ -112,6 +117,7 @@ struct GradParams {
     const KTile *k_list;
     float *split;       // [slots][dV, dK][HD / 4][128 rows][4]: sums of key tiles whose steps are split
     int *arrived;       // [slots][8 warps]
+    uint8_t *again;     // [query tiles, num_heads][4 warps]: whether a warp's rows are done again with D
     int total_q, total_k;
     int num_heads, num_kv_heads, group;
     int window;
@@ -132,6 +138,18 @@ __device__ __forceinline__ bool item_of(int k, int count, int heads, int &entry,
     entry = static_cast<int>(v / heads);
     head = static_cast<int>(v - static_cast<int64_t>(entry) * heads);
     return true;
+}
+// The first item from k on that is done again (by a whole warp); beyond all items: none.
+__device__ __forceinline__ int next_again(int k, int count, int heads, const uint8_t *again) {
+    for (;; k += 32) {
+        int entry, head;
+        const bool have = item_of(k + (threadIdx.x & 31), count, heads, entry, head);
+        const uint32_t f =
+            have ? __ldcg(reinterpret_cast<const unsigned *>(again) + static_cast<int64_t>(entry) * heads + head) : 0u;
+        const uint32_t m = __ballot_sync(0xffffffffu, f != 0u);
+        if (m != 0u) return k + __ffs(m) - 1;
+        if (!__all_sync(0xffffffffu, have)) return INT_MAX;
+    }
 }
 template <class Tile>
 __device__ __forceinline__ Tile load_entry(const Tile *list, int i) {
@@ -174,10 +192,11 @@ constexpr uint32_t kTableBytesQ = 13312, kTableBytes = 15360;
 // What is kept of a head's row: distances -kNearPad .. last + 127.
 constexpr int kNearPad = 256;
 __host__ __device__ constexpr int near_entries(int last) { return (last + kNearPad + 128 + 3) & ~3; }
-// dQ's small arrays, as floats: two items' halves of D; with a bias, the buckets' first distances and each
-// warp's sums along diagonals.
-constexpr int kFirstAt = 512, kDiagAt = kFirstAt + 132;
-constexpr uint32_t kSmallQ = 4u * kFirstAt, kSmallQBias = 4u * (kDiagAt + 8 * 96);
+// dQ's small arrays, as floats: two items' halves of D, and of the second half of the columns (in bf16, rounded to the safe side) the
+// sums of |dS|; with a bias those of P, the buckets' first distances and each warp's sums along diagonals.
+constexpr int kAbsAt = 512, kWeightAt = kAbsAt + 128, kFirstAt = kWeightAt + 128, kDiagAt = kFirstAt + 132;
+constexpr uint32_t kSmallQ = 4u * kWeightAt, kSmallQBias = 4u * (kDiagAt + 8 * 96);
+static_assert(kSmallQBias % 16 == 0, "the bias behind it comes by bulk copies");
 template <int HD, bool BIAS>
 using LayoutQ = Layout<HD, 3, BIAS && HD == 128 ? 1 : 2, BIAS ? kSmallQBias + 2 * kTableBytesQ : kSmallQ>;
 constexpr uint32_t kSmallKv = 2u * 3 * 512;
@@ -323,6 +342,7 @@ struct Cta {
     uint8_t *sb;
     uint32_t tmem;
     volatile int *abort_flag;
+    volatile int *again;  // (dQ) some item is done again
 };
 template <class L>
 __device__ __forceinline__ Cta setup(int full_arrivals) {
@@ -331,6 +351,7 @@ __device__ __forceinline__ Cta setup(int full_arrivals) {
     c.base = smem_u32(smem_raw);
     c.sb = smem_raw;
     c.abort_flag = reinterpret_cast<volatile int *>(c.sb + L::OFF_MISC + 4);
+    c.again = reinterpret_cast<volatile int *>(c.sb + L::OFF_MISC + 8);
     auto bar = [&](int i) -> uint32_t { return c.base + L::OFF_BAR + 8u * static_cast<uint32_t>(i); };
     if (threadIdx.x == 0) {
         mbar_init(bar(B_ACCFREE), 8);
@@ -355,6 +376,7 @@ __device__ __forceinline__ Cta setup(int full_arrivals) {
         mbar_init(bar(B_DONE), 1);
         mbar_init(bar(B_SUMS), 8);
         *c.abort_flag = 0;
+        *c.again = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
     }
@@ -681,13 +703,14 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
     const int count = *p.counts;
     // An item's steps: the tiles 0 .. n_pre - 1 with D from dout . out; tiles n_pre .. n - 2 for D alone;
     // the last tile, where D is complete before its dS is formed; then tiles n_pre .. n - 2 with D.
+    // In the second pass, over the items that are done again, all tiles with D.
     struct Steps {
         int n, n_far, n_pre, n_all, kt0;
         __device__ int tile(int j) const { return j < n ? j : j - (n - n_pre); }
         __device__ bool sum_only(int j) const { return j >= n_pre && j + 1 < n; }
         __device__ bool first_dq(int j) const { return j == (n_pre > 0 ? 0 : n - 1); }
     };
-    auto steps_of = [&](const QTile &t) -> Steps {
+    auto steps_of = [&](const QTile &t, int pass) -> Steps {
         Steps s;
         const int kmin = first_key(t.pos, p.window);
         s.n = t.n;
@@ -695,10 +718,17 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
         // (tiles of the last bucket alone)
         s.n_far = BIAS ? min(max(kmin, t.pos - last + 1) / BN - s.kt0, t.n) : t.n;
         const bool few = t.pos + 1 < kFewKeys || (p.window > 0 && p.window < kFewKeys);
-        s.n_pre = few ? 0 : s.n_far;
+        s.n_pre = pass > 0 ? t.n : few ? 0 : s.n_far;
         s.n_all = s.n + max(s.n - 1 - s.n_pre, 0);
         return s;
     };
+    // Between the passes the roles meet: all of the block's items have their D, and whether they are done again is known.
+    auto second_pass = [&]() -> bool {
+        asm volatile("bar.sync 1, 352;" ::: "memory");
+        return *c.again != 0 && *c.abort_flag == 0;
+    };
+    auto first_item = [&](int pass) -> int { return pass > 0 ? next_again(0, count, p.num_heads, p.again) : 0; };
+    auto item_after = [&](int k, int pass) -> int { return pass > 0 ? next_again(k + 1, count, p.num_heads, p.again) : k + 1; };
 
     // With a bias, registers go from the warps that load and issue to the element-wise ones, which spill with
     // 168 (304 us against 293 for 16 sequences of 128-2048 tokens, 32/8 heads; without a bias the split costs
@@ -710,61 +740,64 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             uint32_t lands = 0, items = 0, J = 0, sa = 0, pa = 1;  // ring A: stage, phase of its emptying
             bool ok = true;
             int e, h;
-            for (int k = 0; ok && item_of(k, count, p.num_heads, e, h); ++k) {
-                const QTile t = load_entry(p.q_list, e);
-                if (t.n == 0) continue;
-                const Steps s = steps_of(t);
-                const uint32_t res = items % NR;
-                if (items >= NR && !wait_warp(bar(res_empty(res)), (items / NR - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-                // (Sums along diagonals run across rows; in all else a row behind the sequence stays on its own.)
-                const bool edit = BIAS && ragged(t.left);
-                const uint32_t land = bar(edit ? B_LAND : res_full(res));
-                if (lane == 0) mbar_arrive_expect_tx(land, 2 * L::TILE);
-                __syncwarp();
-                load_tile<HD>(p.tmap_q, sQ(res), h, t.row, 0, t.left, land);
-                load_tile<HD>(p.tmap_do, sDo(res), h, t.row, 0, t.left, land);
-                if (edit) {
-                    if (!wait_warp(land, lands++ & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-                    clear_rows<HD>(sQ(res), t.left);
-                    clear_rows<HD>(sDo(res), t.left);
+            for (int pass = 0; pass < 2; ++pass) {
+                if (pass > 0 && !second_pass()) break;
+                for (int k = first_item(pass); ok && item_of(k, count, p.num_heads, e, h); k = item_after(k, pass)) {
+                    const QTile t = load_entry(p.q_list, e);
+                    if (t.n == 0) continue;
+                    const Steps s = steps_of(t, pass);
+                    const uint32_t res = items % NR;
+                    if (items >= NR && !wait_warp(bar(res_empty(res)), (items / NR - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+                    // (Sums along diagonals run across rows; in all else a row behind the sequence stays on its own.)
+                    const bool edit = BIAS && ragged(t.left);
+                    const uint32_t land = bar(edit ? B_LAND : res_full(res));
+                    if (lane == 0) mbar_arrive_expect_tx(land, 2 * L::TILE);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(res_full(res)));
-                }
-                if (table_here) {
-                    const uint32_t slot = items & 1;
-                    if (items >= 2 && !wait_warp(bar(B_TABFREE + slot), ((items >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(bar(B_TABFULL + slot), table_bytes);
-                        bulk_load(c.base + L::OFF_SMALL + kSmallQBias + slot * kTableBytesQ, bias_row_of(p.bias_table, h, last) - kNearPad,
-                                  table_bytes, bar(B_TABFULL + slot));
-                    }
-                    __syncwarp();
-                }
-                ++items;
-                const int kvh = h / p.group;
-                for (int j = 0; j < s.n_all; ++j, ++J) {
-                    const uint32_t sb = J % NB, full_k = bar(B_AFULL + sa), full_v = bar(B_BFULL + sb);
-                    const int row0 = (s.kt0 + s.tile(j)) * BN;
-                    const bool cut = ragged(t.sk - row0);  // (the copies of tiles that are edited land together)
-                    ok = J < NA || wait_warp(bar(B_AEMPTY + sa), pa, c.abort_flag, p.err, kTimeoutNs);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(cut ? bar(B_LAND) : full_k, cut ? 2 * L::TILE : L::TILE);
-                    __syncwarp();
-                    load_tile<HD>(p.tmap_k, sK(sa), kvh, t.k_start, row0, t.sk, cut ? bar(B_LAND) : full_k);
-                    ok = J < NB || wait_warp(bar(B_BEMPTY + sb), (J / NB - 1) & 1, c.abort_flag, p.err, kTimeoutNs);
-                    if (!ok) break;
-                    if (lane == 0 && !cut) mbar_arrive_expect_tx(full_v, L::TILE);
-                    __syncwarp();
-                    load_tile<HD>(p.tmap_v, sV(sb), kvh, t.k_start, row0, t.sk, cut ? bar(B_LAND) : full_v);
-                    if (cut) {
-                        ok = wait_warp(bar(B_LAND), lands++ & 1, c.abort_flag, p.err, kTimeoutNs);
-                        if (!ok) break;
-                        clear_rows<HD>(sK(sa), t.sk - row0);
-                        clear_rows<HD>(sV(sb), t.sk - row0);
+                    load_tile<HD>(p.tmap_q, sQ(res), h, t.row, 0, t.left, land);
+                    load_tile<HD>(p.tmap_do, sDo(res), h, t.row, 0, t.left, land);
+                    if (edit) {
+                        if (!wait_warp(land, lands++ & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+                        clear_rows<HD>(sQ(res), t.left);
+                        clear_rows<HD>(sDo(res), t.left);
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(full_k), mbar_arrive(full_v);
+                        if (lane == 0) mbar_arrive(bar(res_full(res)));
                     }
-                    if (++sa == NA) sa = 0, pa ^= 1u;
+                    if (table_here) {
+                        const uint32_t slot = items & 1;
+                        if (items >= 2 && !wait_warp(bar(B_TABFREE + slot), ((items >> 1) - 1) & 1, c.abort_flag, p.err, kTimeoutNs)) break;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(bar(B_TABFULL + slot), table_bytes);
+                            bulk_load(c.base + L::OFF_SMALL + kSmallQBias + slot * kTableBytesQ, bias_row_of(p.bias_table, h, last) - kNearPad,
+                                      table_bytes, bar(B_TABFULL + slot));
+                        }
+                        __syncwarp();
+                    }
+                    ++items;
+                    const int kvh = h / p.group;
+                    for (int j = 0; j < s.n_all; ++j, ++J) {
+                        const uint32_t sb = J % NB, full_k = bar(B_AFULL + sa), full_v = bar(B_BFULL + sb);
+                        const int row0 = (s.kt0 + s.tile(j)) * BN;
+                        const bool cut = ragged(t.sk - row0);  // (the copies of tiles that are edited land together)
+                        ok = J < NA || wait_warp(bar(B_AEMPTY + sa), pa, c.abort_flag, p.err, kTimeoutNs);
+                        if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(cut ? bar(B_LAND) : full_k, cut ? 2 * L::TILE : L::TILE);
+                        __syncwarp();
+                        load_tile<HD>(p.tmap_k, sK(sa), kvh, t.k_start, row0, t.sk, cut ? bar(B_LAND) : full_k);
+                        ok = J < NB || wait_warp(bar(B_BEMPTY + sb), (J / NB - 1) & 1, c.abort_flag, p.err, kTimeoutNs);
+                        if (!ok) break;
+                        if (lane == 0 && !cut) mbar_arrive_expect_tx(full_v, L::TILE);
+                        __syncwarp();
+                        load_tile<HD>(p.tmap_v, sV(sb), kvh, t.k_start, row0, t.sk, cut ? bar(B_LAND) : full_v);
+                        if (cut) {
+                            ok = wait_warp(bar(B_LAND), lands++ & 1, c.abort_flag, p.err, kTimeoutNs);
+                            if (!ok) break;
+                            clear_rows<HD>(sK(sa), t.sk - row0);
+                            clear_rows<HD>(sV(sb), t.sk - row0);
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(full_k), mbar_arrive(full_v);
+                        }
+                        if (++sa == NA) sa = 0, pa ^= 1u;
+                    }
                 }
             }
         } else if (warp == kWarpMma || warp == kWarpMma2) {
@@ -778,50 +811,53 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             uint32_t items = 0, J = 0, sa = 0, pa = 0;  // stage of ring A and its phase
             bool ok = true;
             int e, h;
-            for (int k = 0; ok && item_of(k, count, p.num_heads, e, h); ++k) {
-                const QTile t = load_entry(p.q_list, e);
-                if (t.n == 0) continue;
-                const Steps s = steps_of(t);
-                if (warp == kWarpMma) {
-                    const uint32_t res = items % NR;
-                    ok = wait(res_full(res), (items / NR) & 1);
-                    for (int j = 0; ok && j < s.n_all; ++j, ++J) {
-                        const uint32_t sb = J % NB, sd = J & 1;  // stage of V, place of dP
-                        ok = wait(B_AFULL + sa, pa) && (J == 0 || wait(B_PFULL, (J - 1) & 1));
-                        if (!ok) break;
-                        if (elect_one()) {
-                            issue_abt<HD>(c.tmem, sQ(res), sK(sa));
-                            mma_commit(bar(B_SFULL));
+            for (int pass = 0; pass < 2; ++pass) {
+                if (pass > 0 && !second_pass()) break;
+                for (int k = first_item(pass); ok && item_of(k, count, p.num_heads, e, h); k = item_after(k, pass)) {
+                    const QTile t = load_entry(p.q_list, e);
+                    if (t.n == 0) continue;
+                    const Steps s = steps_of(t, pass);
+                    if (warp == kWarpMma) {
+                        const uint32_t res = items % NR;
+                        ok = wait(res_full(res), (items / NR) & 1);
+                        for (int j = 0; ok && j < s.n_all; ++j, ++J) {
+                            const uint32_t sb = J % NB, sd = J & 1;  // stage of V, place of dP
+                            ok = wait(B_AFULL + sa, pa) && (J == 0 || wait(B_PFULL, (J - 1) & 1));
+                            if (!ok) break;
+                            if (elect_one()) {
+                                issue_abt<HD>(c.tmem, sQ(res), sK(sa));
+                                mma_commit(bar(B_SFULL));
+                            }
+                            __syncwarp();
+                            // (dP goes where dS of the step before the last one was: its dQ has to be done.)
+                            ok = wait(B_BFULL + sb, (J / NB) & 1) && (J < 2 || wait(B_DQDONE + sd, ((J >> 1) - 1) & 1));
+                            if (!ok) break;
+                            if (elect_one()) {
+                                issue_abt<HD>(c.tmem + kDp + 128u * sd, sDo(res), sV(sb));
+                                mma_commit(bar(B_DPFULL + sd));
+                                mma_commit(bar(B_BEMPTY + sb));
+                                if (j + 1 == s.n_all) mma_commit(bar(res_empty(res)));
+                            }
+                            __syncwarp();
+                            if (++sa == NA) sa = 0, pa ^= 1u;
                         }
-                        __syncwarp();
-                        // (dP goes where dS of the step before the last one was: its dQ has to be done.)
-                        ok = wait(B_BFULL + sb, (J / NB) & 1) && (J < 2 || wait(B_DQDONE + sd, ((J >> 1) - 1) & 1));
-                        if (!ok) break;
-                        if (elect_one()) {
-                            issue_abt<HD>(c.tmem + kDp + 128u * sd, sDo(res), sV(sb));
-                            mma_commit(bar(B_DPFULL + sd));
-                            mma_commit(bar(B_BEMPTY + sb));
-                            if (j + 1 == s.n_all) mma_commit(bar(res_empty(res)));
+                    } else {
+                        for (int j = 0; j < s.n_all; ++j, ++J) {
+                            const bool first = s.first_dq(j);
+                            ok = wait(B_DSFULL + (J & 1), (J >> 1) & 1) && (!first || items == 0 || wait(B_ACCFREE, (items - 1) & 1));
+                            if (!ok) break;
+                            if (elect_one()) {
+                                if (!s.sum_only(j)) issue_ab<HD>(c.tmem + kDq, c.tmem + kDp + 128u * (J & 1), sK(sa), first);
+                                mma_commit(bar(B_DQDONE + (J & 1)));
+                                mma_commit(bar(B_AEMPTY + sa));
+                                if (j + 1 == s.n_all) mma_commit(bar(B_DONE));
+                            }
+                            __syncwarp();
+                            if (++sa == NA) sa = 0;
                         }
-                        __syncwarp();
-                        if (++sa == NA) sa = 0, pa ^= 1u;
                     }
-                } else {
-                    for (int j = 0; j < s.n_all; ++j, ++J) {
-                        const bool first = s.first_dq(j);
-                        ok = wait(B_DSFULL + (J & 1), (J >> 1) & 1) && (!first || items == 0 || wait(B_ACCFREE, (items - 1) & 1));
-                        if (!ok) break;
-                        if (elect_one()) {
-                            if (!s.sum_only(j)) issue_ab<HD>(c.tmem + kDq, c.tmem + kDp + 128u * (J & 1), sK(sa), first);
-                            mma_commit(bar(B_DQDONE + (J & 1)));
-                            mma_commit(bar(B_AEMPTY + sa));
-                            if (j + 1 == s.n_all) mma_commit(bar(B_DONE));
-                        }
-                        __syncwarp();
-                        if (++sa == NA) sa = 0;
-                    }
+                    ++items;
                 }
-                ++items;
             }
         }
     } else {
@@ -838,7 +874,6 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
         uint32_t items = 0, J = 0;
         bool ok = true;
         int next_entry, next_head;
-        bool more = item_of(0, count, p.num_heads, next_entry, next_head);
         QTile next{};
         float next_lse[4] = {}, next_delta[4] = {}, next_far = 0.f;
         auto prefetch = [&] {  // what the next item needs of its rows and its head
@@ -852,262 +887,312 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
             }
             if (BIAS) next_far = __ldg(bias_row_of(p.bias_table, next_head, last) - kBiasPad);
         };
-        if (more) prefetch();
-        for (int k = 0; ok && more; ++k) {
-            const QTile t = next;
-            const int head = next_head;
-            float lse2[4], delta[4];
+        for (int pass = 0; pass < 2; ++pass) {
+            if (pass > 0 && !second_pass()) break;
+            int k = first_item(pass);
+            bool more = ok && item_of(k, count, p.num_heads, next_entry, next_head);
+            if (more) prefetch();
+            while (ok && more) {
+                const QTile t = next;
+                const int head = next_head;
+                // (wg 0) where it says whether the item is done again
+                uint8_t *const again = p.again + (static_cast<int64_t>(next_entry) * p.num_heads + head) * 4 + quarter;
+                float lse2[4], delta[4];
 #pragma unroll
-            for (int a = 0; a < 4; ++a) lse2[a] = next_lse[a], delta[a] = next_delta[a];
-            [[maybe_unused]] const float last_bias = next_far;
-            more = item_of(k + 1, count, p.num_heads, next_entry, next_head);
-            const int rows = min(t.left, BM);
-            const int64_t stat_row = static_cast<int64_t>(head) * p.total_q + t.row;
-            __nv_bfloat16 *dq = p.dq + static_cast<int64_t>(t.row) * p.dq_stride + head * HD;
-            [[maybe_unused]] float by_bucket[4] = {0.f, 0.f, 0.f, 0.f};
-            float *partial = nullptr;
-            if constexpr (BIAS)
-                partial = p.partial + ((static_cast<int64_t>(t.id) * p.num_heads + head) * 8 + warp) * p.bias.num_buckets;
-            if (t.n == 0) {
-                zero_rows<HD>(dq, p.dq_stride, rows);
-                if (wg == 0 && row < rows) p.delta[stat_row + row] = 0.f;
+                for (int a = 0; a < 4; ++a) lse2[a] = next_lse[a], delta[a] = next_delta[a];
+                [[maybe_unused]] const float last_bias = next_far;
+                k = item_after(k, pass);
+                more = item_of(k, count, p.num_heads, next_entry, next_head);
+                const int rows = min(t.left, BM);
+                const int64_t stat_row = static_cast<int64_t>(head) * p.total_q + t.row;
+                __nv_bfloat16 *dq = p.dq + static_cast<int64_t>(t.row) * p.dq_stride + head * HD;
+                [[maybe_unused]] float by_bucket[4] = {0.f, 0.f, 0.f, 0.f};
+                float *partial = nullptr;
                 if constexpr (BIAS)
-                    for (int b = lane; b < p.bias.num_buckets; b += 32) partial[b] = 0.f;
-                if (more) prefetch();
-                continue;
-            }
-            const Steps s = steps_of(t);
-            float d_sum[4] = {0.f, 0.f, 0.f, 0.f};
-            // Sums of P dP and of P over the first n_far tiles (d_far: and of the last bucket's dS in the others).
-            [[maybe_unused]] float d_far = 0.f, w_far[4] = {0.f, 0.f, 0.f, 0.f};
-            [[maybe_unused]] const float *bias_row = nullptr;  // entry of distance 0
-            if constexpr (BIAS) {
-                bias_row = bias_row_of(p.bias_table, head, last);
-                if (table_here) {
-                    ok = wait_warp(bar(B_TABFULL + (items & 1)), (items >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
-                    if (!ok) break;
-                    bias_row = small + kSmallQBias / 4 + (items & 1) * (kTableBytesQ / 4) + kNearPad;
+                    partial = p.partial + ((static_cast<int64_t>(t.id) * p.num_heads + head) * 8 + warp) * p.bias.num_buckets;
+                if (t.n == 0) {
+                    zero_rows<HD>(dq, p.dq_stride, rows);
+                    if (wg == 0 && row < rows) p.delta[stat_row + row] = 0.f;
+                    if (wg == 0 && lane == 0) *again = 0;
+                    if constexpr (BIAS)
+                        for (int b = lane; b < p.bias.num_buckets; b += 32) partial[b] = 0.f;
+                    if (more) prefetch();
+                    continue;
                 }
-            }
-            for (int j = 0; j < s.n_all; ++j, ++J) {
-                const uint32_t dp = c.tmem + t_lane + kDp + 128u * (J & 1) + 64u * wg;
-                const bool sum_only = s.sum_only(j);
-                const int tile = s.tile(j);
-                ok = wait_warp(bar(B_SFULL), J & 1, c.abort_flag, p.err, kTimeoutNs);
-                if (!ok) break;
-                tc_fence_after();
-                float w[2][32];  // logits, then weights P
-                load_block(c.tmem + t_lane + 64u * wg, w);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_PFULL));
-                // The distance of the warp's first row to its first key: its block has d00 - 63 .. d00 + 31.
-                const int d00 = t.pos + quarter * 32 - (s.kt0 + tile) * BN - 64 * wg;
-                const bool near = BIAS && d00 - 63 < last;
-                const float add = BIAS ? near ? bias_ref(last_bias) : last_bias : 0.f;
-#pragma unroll
-                for (int a = 0; a < 4; ++a) {
-                    const float x = add - lse2[a];
-                    const uint64_t x2 = f2_pack(x, x);
-#pragma unroll
-                    for (int b = 0; b < 8; ++b) set_pair(w, a, b, f2_fma(block_pair(w, a, b), sl2x2, x2));
-                }
-                if (near || (!BIAS && d00 < 63) || (p.window > 0 && d00 + 31 >= p.window)) {
-                    const int n0 = d00 + (lane >> 2) - 2 * c0 - 56;
-                    auto entry = [&](int n) -> float {
-                        float x = 0.f;
-                        if (near)
-                            x = bias_row[n];  // (-inf before distance 0)
-                        else if (!BIAS && n < 0)
-                            x = -INFINITY;
-                        return p.window > 0 && n >= p.window ? -INFINITY : x;
-                    };
-#pragma unroll
-                    for (int g = 0; g < 11; ++g) {  // a - b + 7
-                        const uint64_t x2 = f2_pack(entry(n0 + 8 * g), entry(n0 + 8 * g - 1));
-#pragma unroll
-                        for (int a = 0; a < 4; ++a) {
-                            const int b = a + 7 - g;
-                            if (b >= 0 && b < 8) set_pair(w, a, b, f2_add(block_pair(w, a, b), x2));
-                        }
+                const Steps s = steps_of(t, pass);
+                float d_sum[4] = {0.f, 0.f, 0.f, 0.f}, abs_sum[4] = {0.f, 0.f, 0.f, 0.f};  // of P dP, of |dS| with dout . out
+                // Sums of P dP and of P over the first n_far tiles (d_far: and of the last bucket's dS in the others).
+                [[maybe_unused]] float d_far = 0.f, w_far[4] = {0.f, 0.f, 0.f, 0.f};
+                [[maybe_unused]] const float *bias_row = nullptr;  // entry of distance 0
+                if constexpr (BIAS) {
+                    bias_row = bias_row_of(p.bias_table, head, last);
+                    if (table_here) {
+                        ok = wait_warp(bar(B_TABFULL + (items & 1)), (items >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
+                        if (!ok) break;
+                        bias_row = small + kSmallQBias / 4 + (items & 1) * (kTableBytesQ / 4) + kNearPad;
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = ex2_approx(w[i >> 5][i & 31]);
-                if (BIAS && !sum_only && tile < s.n_far) {
+                bool moved = false;  // (wg 0) dout . out moved a row of the warp too far
+                for (int j = 0; j < s.n_all; ++j, ++J) {
+                    const uint32_t dp = c.tmem + t_lane + kDp + 128u * (J & 1) + 64u * wg;
+                    const bool sum_only = s.sum_only(j);
+                    const int tile = s.tile(j);
+                    ok = wait_warp(bar(B_SFULL), J & 1, c.abort_flag, p.err, kTimeoutNs);
+                    if (!ok) break;
+                    tc_fence_after();
+                    float w[2][32];  // logits, then weights P
+                    load_block(c.tmem + t_lane + 64u * wg, w);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_PFULL));
+                    // The distance of the warp's first row to its first key: its block has d00 - 63 .. d00 + 31.
+                    const int d00 = t.pos + quarter * 32 - (s.kt0 + tile) * BN - 64 * wg;
+                    const bool near = BIAS && d00 - 63 < last;
+                    const float add = BIAS ? near ? bias_ref(last_bias) : last_bias : 0.f;
 #pragma unroll
                     for (int a = 0; a < 4; ++a) {
-                        uint64_t x = block_pair(w, a, 0);
+                        const float x = add - lse2[a];
+                        const uint64_t x2 = f2_pack(x, x);
 #pragma unroll
-                        for (int b = 1; b < 8; ++b) x = f2_add(x, block_pair(w, a, b));
-                        w_far[a] += pair_sum(x);
+                        for (int b = 0; b < 8; ++b) set_pair(w, a, b, f2_fma(block_pair(w, a, b), sl2x2, x2));
                     }
-                }
-                ok = wait_warp(bar(B_DPFULL + (J & 1)), (J >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
-                if (!ok) break;
-                tc_fence_after();
-                // D of the rows: a thread's columns, its four threads', this warpgroup's half and the other's.
-                auto exchange = [&]() -> bool {
-                    const bool odd = c0 & 1, high = c0 & 2;
-                    const float x0 = (odd ? d_sum[1] : d_sum[0]) + __shfl_xor_sync(0xffffffffu, odd ? d_sum[0] : d_sum[1], 1);
-                    const float x1 = (odd ? d_sum[3] : d_sum[2]) + __shfl_xor_sync(0xffffffffu, odd ? d_sum[2] : d_sum[3], 1);
-                    const float mine = (high ? x1 : x0) + __shfl_xor_sync(0xffffffffu, high ? x0 : x1, 2);
-                    // (Two places: a warpgroup may be an item ahead of the other's reading.)
-                    float *sums = small + 256 * (items & 1);
-                    const int x = r0 + 8 * c0;
-                    sums[128 * wg + x] = mine;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_SUMS));
-                    if (!wait_warp(bar(B_SUMS), items & 1, c.abort_flag, p.err, kTimeoutNs)) return false;
+                    if (near || (!BIAS && d00 < 63) || (p.window > 0 && d00 + 31 >= p.window)) {
+                        const int n0 = d00 + (lane >> 2) - 2 * c0 - 56;
+                        auto entry = [&](int n) -> float {
+                            float x = 0.f;
+                            if (near)
+                                x = bias_row[n];  // (-inf before distance 0)
+                            else if (!BIAS && n < 0)
+                                x = -INFINITY;
+                            return p.window > 0 && n >= p.window ? -INFINITY : x;
+                        };
 #pragma unroll
-                    for (int a = 0; a < 4; ++a) delta[a] = sums[r0 + 8 * a] + sums[128 + r0 + 8 * a];
-                    if (wg == 0 && x < rows) p.delta[stat_row + x] = sums[x] + sums[128 + x];
-                    return true;
-                };
-                const bool pivot = j + 1 == s.n && s.n_pre < s.n;
-                if (pivot) {
+                        for (int g = 0; g < 11; ++g) {  // a - b + 7
+                            const uint64_t x2 = f2_pack(entry(n0 + 8 * g), entry(n0 + 8 * g - 1));
+#pragma unroll
+                            for (int a = 0; a < 4; ++a) {
+                                const int b = a + 7 - g;
+                                if (b >= 0 && b < 8) set_pair(w, a, b, f2_add(block_pair(w, a, b), x2));
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) w[i >> 5][i & 31] = ex2_approx(w[i >> 5][i & 31]);
+                    if (BIAS && !sum_only && tile < s.n_far) {
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {
+                            uint64_t x = block_pair(w, a, 0);
+#pragma unroll
+                            for (int b = 1; b < 8; ++b) x = f2_add(x, block_pair(w, a, b));
+                            w_far[a] += pair_sum(x);
+                        }
+                    }
+                    ok = wait_warp(bar(B_DPFULL + (J & 1)), (J >> 1) & 1, c.abort_flag, p.err, kTimeoutNs);
+                    if (!ok) break;
+                    tc_fence_after();
+                    // D of the rows: a thread's columns, its four threads', this warpgroup's half and the other's.
+                    auto exchange = [&]() -> bool {
+                        const bool odd = c0 & 1, high = c0 & 2;
+                        auto own = [&](const float (&f)[4]) -> float {  // that of the thread's row r0 + 8 c0
+                            return high ? (odd ? f[3] : f[2]) : (odd ? f[1] : f[0]);
+                        };
+                        auto across = [&](const float (&f)[4]) -> float {
+                            const float x0 = (odd ? f[1] : f[0]) + __shfl_xor_sync(0xffffffffu, odd ? f[0] : f[1], 1);
+                            const float x1 = (odd ? f[3] : f[2]) + __shfl_xor_sync(0xffffffffu, odd ? f[2] : f[3], 1);
+                            return (high ? x1 : x0) + __shfl_xor_sync(0xffffffffu, high ? x0 : x1, 2);
+                        };
+                        // (Two places: a warpgroup may be an item ahead of the other's reading.)
+                        float *sums = small + 256 * (items & 1);
+                        __nv_bfloat16 *abs_of = reinterpret_cast<__nv_bfloat16 *>(small + kAbsAt) + 128 * (items & 1);
+                        [[maybe_unused]] __nv_bfloat16 *weight_of = reinterpret_cast<__nv_bfloat16 *>(small + kWeightAt) + 128 * (items & 1);
+                        const int x = r0 + 8 * c0;
+                        sums[128 * wg + x] = across(d_sum);
+                        float abs_all = across(abs_sum);
+                        [[maybe_unused]] float weight = 1.f;
+                        if constexpr (BIAS) weight = across(w_far);
+                        if (wg == 1) {
+                            abs_of[x] = __float2bfloat16_rd(abs_all);
+                            if constexpr (BIAS) weight_of[x] = __float2bfloat16_ru(weight);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(B_SUMS));
+                        if (!wait_warp(bar(B_SUMS), items & 1, c.abort_flag, p.err, kTimeoutNs)) return false;
+                        const float before = own(delta);
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) delta[a] = sums[r0 + 8 * a] + sums[128 + r0 + 8 * a];
+                        if (wg == 0) {
+                            const float d = own(delta);
+                            if (x < rows) p.delta[stat_row + x] = d;
+                            abs_all += __bfloat162float(abs_of[x]);
+                            if constexpr (BIAS) weight += __bfloat162float(weight_of[x]);
+                            const bool off = s.n_pre > 0 && x < rows && fabsf(d - before) * weight > kMoved * abs_all;
+                            moved = __any_sync(0xffffffffu, off);
+                        }
+                        return true;
+                    };
+                    const bool pivot = j + 1 == s.n && s.n_pre < s.n;
+                    if (pivot) {
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            float d[32];
+                            tmem_ld_16x256b_x8(dp + static_cast<uint32_t>(half * 16 << 16), d);
+                            tmem_wait_ld_regs(d);
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int a = 2 * half + u;
+                                uint64_t x = 0ull;
+#pragma unroll
+                                for (int b = 0; b < 8; ++b)
+                                    x = f2_fma(block_pair(w, a, b), f2_pack(d[pair_at(a, b)], d[pair_at(a, b) + 1]), x);
+                                d_sum[a] += pair_sum(x);
+                            }
+                        }
+                        ok = exchange();
+                        if (!ok) break;
+                        if (s.n_pre == 0) {  // (the last bucket's tiles may still be to come)
+#pragma unroll
+                            for (int a = 0; a < 4; ++a) d_sum[a] = 0.f;
+                        }
+                    }
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         float d[32];
                         tmem_ld_16x256b_x8(dp + static_cast<uint32_t>(half * 16 << 16), d);
                         tmem_wait_ld_regs(d);
+                        uint32_t pk[16];
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             const int a = 2 * half + u;
+                            const uint64_t delta2 = f2_pack(-delta[a], -delta[a]);
                             uint64_t x = 0ull;
 #pragma unroll
-                            for (int b = 0; b < 8; ++b)
-                                x = f2_fma(block_pair(w, a, b), f2_pack(d[pair_at(a, b)], d[pair_at(a, b) + 1]), x);
-                            d_sum[a] += pair_sum(x);
+                            for (int b = 0; b < 8; ++b) {
+                                const uint64_t w2 = block_pair(w, a, b), d2 = f2_pack(d[pair_at(a, b)], d[pair_at(a, b) + 1]);
+                                x = f2_fma(w2, d2, x);
+                                set_pair(w, a, b, f2_mul(w2, f2_add(d2, delta2)));
+                                pk[2 * b + u] = pack_bf16x2(w[half][pair_at(a, b)], w[half][pair_at(a, b) + 1]);
+                            }
+                            if (!pivot) d_sum[a] += pair_sum(x);
                         }
+                        if (!sum_only) tmem_st_16x128b_x8(dp + static_cast<uint32_t>(half * 16 << 16), pk);
                     }
-                    ok = exchange();
-                    if (!ok) break;
-                    if (s.n_pre == 0) {  // (the last bucket's tiles may still be to come)
-#pragma unroll
-                        for (int a = 0; a < 4; ++a) d_sum[a] = 0.f;
+                    if (!sum_only) {
+                        if (BIAS && tile + 1 == s.n_far) d_far += (d_sum[0] + d_sum[1]) + (d_sum[2] + d_sum[3]);
+                        tmem_wait_st();
                     }
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    float d[32];
-                    tmem_ld_16x256b_x8(dp + static_cast<uint32_t>(half * 16 << 16), d);
-                    tmem_wait_ld_regs(d);
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int a = 2 * half + u;
-                        const uint64_t delta2 = f2_pack(-delta[a], -delta[a]);
-                        uint64_t x = 0ull;
-#pragma unroll
-                        for (int b = 0; b < 8; ++b) {
-                            const uint64_t w2 = block_pair(w, a, b), d2 = f2_pack(d[pair_at(a, b)], d[pair_at(a, b) + 1]);
-                            x = f2_fma(w2, d2, x);
-                            set_pair(w, a, b, f2_mul(w2, f2_add(d2, delta2)));
-                            pk[2 * b + u] = pack_bf16x2(w[half][pair_at(a, b)], w[half][pair_at(a, b) + 1]);
-                        }
-                        if (!pivot) d_sum[a] += pair_sum(x);
-                    }
-                    if (!sum_only) tmem_st_16x128b_x8(dp + static_cast<uint32_t>(half * 16 << 16), pk);
-                }
-                if (!sum_only) {
-                    if (BIAS && tile + 1 == s.n_far) d_far += (d_sum[0] + d_sum[1]) + (d_sum[2] + d_sum[3]);
-                    tmem_wait_st();
-                }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_DSFULL + (J & 1)));
-                if (j + 1 == s.n && s.n_pre == s.n) {
-                    ok = exchange();
-                    if (!ok) break;
-                }
-                if (BIAS && j + 1 >= s.n && tile >= s.n_far && d00 > -32) {  // (else all of the block is hidden)
-                    // Sums along diagonals: a thread's own, 11 pairs; then thread (r, c), r = t / 4, fetches of the
-                    // threads (., c) those of distances r + 8 i (v[i], less d00 - 64); then the four threads of
-                    // an r share them out.
-                    float v[12];
-#pragma unroll
-                    for (int i = 0; i < 12; ++i) v[i] = 0.f;
-#pragma unroll
-                    for (int g = 0; g < 11; ++g) {
-                        uint64_t x2 = 0ull;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_DSFULL + (J & 1)));
+                    if (pass == 0 && j < s.n_pre) {
 #pragma unroll
                         for (int a = 0; a < 4; ++a) {
-                            const int b = a + 7 - g;
-                            if (b >= 0 && b < 8) x2 = f2_add(x2, block_pair(w, a, b));
-                        }
-                        float x[2];
-                        f2_unpack(x2, x[0], x[1]);
+                            float x = 0.f, y = 0.f;
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int src = (lane >> 2) + 2 * c0 + k;
-                            const float y = __shfl_sync(0xffffffffu, x[k], (src & 7) * 4 + c0);
-                            if (src >= 8)
-                                v[g] += y;
-                            else
-                                v[g + 1] += y;
+                            for (int b = 0; b < 8; ++b) {
+                                x += fabsf(w[a >> 1][pair_at(a, b)]);
+                                y += fabsf(w[a >> 1][pair_at(a, b) + 1]);
+                            }
+                            abs_sum[a] += x + y;
                         }
                     }
-                    const int base = d00 - 64;
-                    float *diag = small + kDiagAt + 96 * warp;
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        float x[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float even = v[4 * k + 2 * i], odd = v[4 * k + 2 * i + 1];
-                            x[i] = (c0 & 1 ? odd : even) + __shfl_xor_sync(0xffffffffu, c0 & 1 ? even : odd, 1);
-                        }
-                        const float y = (c0 & 2 ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, c0 & 2 ? x[0] : x[1], 2);
-                        const int at = (lane >> 2) + 8 * c0 + 32 * k;
-                        diag[at] = y;
-                        if (base + at >= last) d_far += y;
+                    if (pass == 0 && j + 1 == s.n && s.n_pre == s.n) {
+                        ok = exchange();
+                        if (!ok) break;
                     }
-                    __syncwarp();
-                    // A lane adds up the distances of its buckets.  (Scans over the warp's 96 distances by bucket
-                    // took 60 us of 375 of sixteen sequences of 128-2048 tokens.)
+                    if (BIAS && pass == 0 && j + 1 >= s.n && tile >= s.n_far && d00 > -32) {  // (else all of the block is hidden)
+                        // Sums along diagonals: a thread's own, 11 pairs; then thread (r, c), r = t / 4, fetches of the
+                        // threads (., c) those of distances r + 8 i (v[i], less d00 - 64); then the four threads of
+                        // an r share them out.
+                        float v[12];
 #pragma unroll
-                    for (int k4 = 0; k4 < 4; ++k4) {
-                        if (32 * k4 >= p.bias.num_buckets - 1) break;
-                        const int b = lane + 32 * k4;
-                        if (b >= p.bias.num_buckets - 1) continue;
-                        const int hi = min(first[b + 1] - base, 96);
-                        float sum = 0.f;
+                        for (int i = 0; i < 12; ++i) v[i] = 0.f;
+#pragma unroll
+                        for (int g = 0; g < 11; ++g) {
+                            uint64_t x2 = 0ull;
+#pragma unroll
+                            for (int a = 0; a < 4; ++a) {
+                                const int b = a + 7 - g;
+                                if (b >= 0 && b < 8) x2 = f2_add(x2, block_pair(w, a, b));
+                            }
+                            float x[2];
+                            f2_unpack(x2, x[0], x[1]);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int src = (lane >> 2) + 2 * c0 + k;
+                                const float y = __shfl_sync(0xffffffffu, x[k], (src & 7) * 4 + c0);
+                                if (src >= 8)
+                                    v[g] += y;
+                                else
+                                    v[g + 1] += y;
+                            }
+                        }
+                        const int base = d00 - 64;
+                        float *diag = small + kDiagAt + 96 * warp;
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) {
+                            float x[2];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float even = v[4 * k + 2 * i], odd = v[4 * k + 2 * i + 1];
+                                x[i] = (c0 & 1 ? odd : even) + __shfl_xor_sync(0xffffffffu, c0 & 1 ? even : odd, 1);
+                            }
+                            const float y = (c0 & 2 ? x[1] : x[0]) + __shfl_xor_sync(0xffffffffu, c0 & 2 ? x[0] : x[1], 2);
+                            const int at = (lane >> 2) + 8 * c0 + 32 * k;
+                            diag[at] = y;
+                            if (base + at >= last) d_far += y;
+                        }
+                        __syncwarp();
+                        // A lane adds up the distances of its buckets.  (Scans over the warp's 96 distances by bucket
+                        // took 60 us of 375 of sixteen sequences of 128-2048 tokens.)
+#pragma unroll
+                        for (int k4 = 0; k4 < 4; ++k4) {
+                            if (32 * k4 >= p.bias.num_buckets - 1) break;
+                            const int b = lane + 32 * k4;
+                            if (b >= p.bias.num_buckets - 1) continue;
+                            const int hi = min(first[b + 1] - base, 96);
+                            float sum = 0.f;
 #pragma unroll 1
-                        for (int x = max(first[b] - base, 0); x < hi; x += 4) {
-                            float f[4];
+                            for (int x = max(first[b] - base, 0); x < hi; x += 4) {
+                                float f[4];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) f[i] = x + i < hi ? diag[x + i] : 0.f;
-                            sum += (f[0] + f[1]) + (f[2] + f[3]);
+                                for (int i = 0; i < 4; ++i) f[i] = x + i < hi ? diag[x + i] : 0.f;
+                                sum += (f[0] + f[1]) + (f[2] + f[3]);
+                            }
+                            by_bucket[k4] += sum;
                         }
-                        by_bucket[k4] += sum;
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
-            }
-            if (!ok) break;
-            if constexpr (BIAS) {
+                if (!ok) break;
+                if constexpr (BIAS) {
+                    __syncwarp();
+                    if (table_here && lane == 0) mbar_arrive(bar(B_TABFREE + (items & 1)));
+    if (pass == 0) {
+                        const float t_far = warp_sum(d_far - ((delta[0] * w_far[0] + delta[1] * w_far[1]) + (delta[2] * w_far[2] + delta[3] * w_far[3])));
+#pragma unroll
+                        for (int k4 = 0; k4 < 4; ++k4) {
+                            const int b = lane + 32 * k4;
+                            if (b < p.bias.num_buckets) partial[b] = by_bucket[k4] + (b == p.bias.num_buckets - 1 ? t_far : 0.f);
+                        }
+                    }
+                }
+                if (pass == 0 && wg == 0 && lane == 0) {
+                    *again = moved;
+                    if (moved) *c.again = 1;
+                }
+                if (more) prefetch();
+                ok = wait_warp(bar(B_DONE), items & 1, c.abort_flag, p.err, kTimeoutNs);
+                if (!ok) break;
+                tc_fence_after();
+                __nv_bfloat16 *dst = dq + static_cast<int64_t>(row) * p.dq_stride + wg * (HD / 2);
+#pragma unroll 1
+                for (int cc = 0; cc < HD / 64; ++cc)
+                    store_chunk(c.tmem + t_lane + kDq + wg * (HD / 2) + cc * 32, p.scale, dst + cc * 32, row < rows, v8);
+                tc_fence_before();
                 __syncwarp();
-                if (table_here && lane == 0) mbar_arrive(bar(B_TABFREE + (items & 1)));
-                const float t_far = warp_sum(d_far - ((delta[0] * w_far[0] + delta[1] * w_far[1]) + (delta[2] * w_far[2] + delta[3] * w_far[3])));
-#pragma unroll
-                for (int k4 = 0; k4 < 4; ++k4) {
-                    const int b = lane + 32 * k4;
-                    if (b < p.bias.num_buckets) partial[b] = by_bucket[k4] + (b == p.bias.num_buckets - 1 ? t_far : 0.f);
-                }
+                if (lane == 0) mbar_arrive(bar(B_ACCFREE));
+                ++items;
             }
-            if (more) prefetch();
-            ok = wait_warp(bar(B_DONE), items & 1, c.abort_flag, p.err, kTimeoutNs);
-            if (!ok) break;
-            tc_fence_after();
-            __nv_bfloat16 *dst = dq + static_cast<int64_t>(row) * p.dq_stride + wg * (HD / 2);
-#pragma unroll 1
-            for (int cc = 0; cc < HD / 64; ++cc)
-                store_chunk(c.tmem + t_lane + kDq + wg * (HD / 2) + cc * 32, p.scale, dst + cc * 32, row < rows, v8);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_ACCFREE));
-            ++items;
         }
     }
     teardown(c);
@@ -1506,11 +1591,11 @@ int split_slots(int total_q, int total_k, int num_seqs, int num_heads) {
 }
 
 // The workspace: lse2, delta, counts, lists, partial sums of dbias, sums of split key tiles (for 128 dims) and
-// their counters.
+// their counters, which of dQ's items are done again.
 struct Workspace {
     int slots;
-    size_t stat, q_list, k_list, partial, split, arrived;
-    size_t bytes() const { return 2 * stat + 256 + q_list + k_list + partial + split + arrived; }
+    size_t stat, q_list, k_list, partial, split, arrived, again;
+    size_t bytes() const { return 2 * stat + 256 + q_list + k_list + partial + split + arrived + again; }
     Workspace(int total_q, int total_k, int num_seqs, int num_heads, int num_buckets)
         : slots(split_slots(total_q, total_k, num_seqs, num_heads)),
           stat(up256(static_cast<size_t>(total_q) * num_heads * sizeof(float))),
@@ -1518,7 +1603,8 @@ struct Workspace {
           k_list(up256((most_tiles(total_k, num_seqs) + slots) * sizeof(KTile))),
           partial(up256(static_cast<size_t>(most_tiles(total_q, num_seqs)) * num_heads * 8 * num_buckets * sizeof(float))),
           split(static_cast<size_t>(slots) * 2 * BM * 128 * sizeof(float)),
-          arrived(up256(static_cast<size_t>(slots) * 8 * sizeof(int))) {}
+          arrived(up256(static_cast<size_t>(slots) * 8 * sizeof(int))),
+          again(up256(static_cast<size_t>(most_tiles(total_q, num_seqs)) * num_heads * 4)) {}
 };
 
 template <class Kernel>
@@ -1618,6 +1704,7 @@ cudaError_t launch_packed_attn_backward(const PackedGradArgs &g, cudaStream_t st
     p.partial = reinterpret_cast<float *>(take(w.partial));
     p.split = reinterpret_cast<float *>(take(w.split));
     p.arrived = plan.arrived = reinterpret_cast<int *>(take(w.arrived));
+    p.again = take(w.again);
     p.bias_table = a.bias_table;
     p.total_q = a.total_q;
     p.total_k = a.total_k;

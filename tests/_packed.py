@@ -16,14 +16,15 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 
 
 def values(q, k, v, cu_q, cu_k, window, scale, bias=None, max_distance=0, dout=None):
-    """A dict as oracle.relative.attention's, of float64 tensors on q's device; and `ds_abs` [Tq, H] = sum_j |dS_ij|."""
+    """A dict as oracle.relative.attention's, of float64 tensors on q's device; and `ds_abs` [Tq, H] = sum_j |dS_ij|,
+    `mean` [Tq, H] = sum_j P_ij N_ij."""
     d = q.device
     wide = lambda t: torch.zeros(t.shape, dtype=torch.float64, device=d)  # noqa: E731
     heads, hkv = q.shape[1], k.shape[1]
     group = heads // hkv
     r = {"out": wide(q), "out_abs": wide(q), "lse": wide(q[..., 0]), "logit": wide(q[..., 0])}
     if dout is not None:
-        r["ds_abs"] = wide(q[..., 0])
+        r |= {"ds_abs": wide(q[..., 0]), "mean": wide(q[..., 0])}
         r |= {n + e: wide(like) for n, like in (("dq", q), ("dk", k), ("dv", v)) for e in ("", "_abs", "_terms", "_rows")}
         if bias is not None:
             r |= {"dbias": wide(bias), "dbias_terms": wide(bias)}
@@ -56,7 +57,7 @@ def values(q, k, v, cu_q, cu_k, window, scale, bias=None, max_distance=0, dout=N
             dp, n = o @ z.T, o.abs() @ z.abs().T
             ds = p * (dp - (p * dp).sum(1, keepdim=True))
             terms = p * (n + (p * n).sum(1, keepdim=True))
-            r["ds_abs"][a:b, h] = ds.abs().sum(1)
+            r["ds_abs"][a:b, h], r["mean"][a:b, h] = ds.abs().sum(1), (p * n).sum(1)
             r["dq"][a:b, h] = scale * (ds @ y)
             r["dk"][c:e, g] += scale * (ds.T @ x)
             r["dv"][c:e, g] += p.T @ o
