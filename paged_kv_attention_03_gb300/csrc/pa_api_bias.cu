@@ -34,6 +34,10 @@ bool row_stride_ok(int64_t stride, int heads, int head_dim) {
     return stride >= static_cast<int64_t>(heads) * head_dim && stride % 8 == 0 && stride < (1ll << 38);
 }
 
+bool packed_sizes_ok(int total_q, int total_k, int num_seqs) {
+    return total_q < (1 << 30) && total_k < (1 << 30) && num_seqs <= 65535;
+}
+
 // What both directions of packed attention check.  PA_OK with *nothing set: no row to compute.
 pa_status check_packed(const pa::PackedArgs &a, bool *nothing) {
     if (a.num_seqs < 0 || a.total_q < 0 || a.total_k < 0 || a.max_seqlen_q < 0 || a.max_seqlen_k < 0) return PA_ERR_INVALID_ARG;
@@ -42,7 +46,7 @@ pa_status check_packed(const pa::PackedArgs &a, bool *nothing) {
     if (!row_stride_ok(a.q_stride, a.num_heads, a.head_dim) || !row_stride_ok(a.k_stride, a.num_kv_heads, a.head_dim) ||
         !row_stride_ok(a.v_stride, a.num_kv_heads, a.head_dim))
         return PA_ERR_INVALID_ARG;
-    if (a.total_q >= (1 << 30) || a.total_k >= (1 << 30) || a.num_seqs > 65535) return PA_ERR_UNSUPPORTED;
+    if (!packed_sizes_ok(a.total_q, a.total_k, a.num_seqs)) return PA_ERR_UNSUPPORTED;
     // The kernels count tiles of at least two tokens (queries) or 128 rows in 32 bits.
     const int64_t tiles_q = (static_cast<int64_t>(a.max_seqlen_q) + 127) / 128 * a.num_seqs * a.num_heads;
     const int64_t tiles_k = (static_cast<int64_t>(a.max_seqlen_k) + 127) / 128 * a.num_seqs * a.num_kv_heads;
@@ -69,10 +73,12 @@ size_t pa_relative_bias_workspace_size(int num_heads, int num_buckets, int max_d
 
 size_t pa_varlen_attn_backward_workspace_size(int total_q, int total_k, int num_seqs, int num_heads, int num_buckets,
                                               int max_distance) {
-    if (total_q < 0 || total_k < 0 || num_seqs < 0 || num_heads <= 0 || num_buckets < 0 || num_buckets > pa::kMaxBuckets) return 0;
+    if (total_q < 0 || total_k < 0 || num_seqs < 0 || num_heads <= 0 || !packed_sizes_ok(total_q, total_k, num_seqs)) return 0;
+    pa::RelativeBias b{};
+    if (num_buckets != 0 && !pa::plan_relative_bias(num_buckets, max_distance, &b)) return 0;
     size_t bytes = 0;
     if (!pa::packed_grad_workspace(total_q, total_k, num_seqs, num_heads, num_buckets, &bytes)) return 0;
-    return bytes + (num_buckets > 0 ? pa_relative_bias_workspace_size(num_heads, num_buckets, max_distance) : 0);
+    return bytes + (num_buckets > 0 ? pa::bias_table_bytes(num_heads, b) : 0);
 }
 
 pa_status pa_varlen_attn(void *out, float *lse, const void *q, const void *k, const void *v, int64_t q_stride,
