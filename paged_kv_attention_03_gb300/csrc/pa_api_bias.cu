@@ -51,7 +51,8 @@ pa_status check_packed(const pa::PackedArgs &a, bool *nothing) {
     const int64_t tiles_q = (static_cast<int64_t>(a.max_seqlen_q) + 127) / 128 * a.num_seqs * a.num_heads;
     const int64_t tiles_k = (static_cast<int64_t>(a.max_seqlen_k) + 127) / 128 * a.num_seqs * a.num_kv_heads;
     if (tiles_q > 0x7fffffffLL || tiles_k > 0x7fffffffLL || a.max_seqlen_q > (1 << 30) || a.max_seqlen_k > (1 << 30) ||
-        (a.num_seqs > 0 && !pa::prefill_fits(a.num_seqs, a.num_kv_heads, a.num_heads / a.num_kv_heads, a.total_q, a.max_seqlen_q, a.total_k)))
+        (a.num_seqs > 0 && !pa::prefill_fits(a.num_seqs, a.num_kv_heads, a.num_heads / a.num_kv_heads, a.total_q,
+                                             a.max_seqlen_q > 0 ? a.max_seqlen_q : 1, a.total_k)))
         return PA_ERR_UNSUPPORTED;
     *nothing = a.num_seqs == 0 || (a.total_q == 0 && a.total_k == 0);
     if (*nothing) return PA_OK;
@@ -108,7 +109,7 @@ pa_status pa_varlen_attn(void *out, float *lse, const void *q, const void *k, co
     bool nothing = false;
     pa_status st = check_packed(a, &nothing);
     if (st == PA_OK) st = check_bias(bias, num_buckets, max_distance, scale, &a.bias);
-    if (st != PA_OK || nothing || total_q == 0 || max_seqlen_q == 0) return st;
+    if (st != PA_OK || nothing || total_q == 0) return st;
     if (!out || !lse || !aligned(out, 16) || !aligned(lse, 4)) return PA_ERR_INVALID_ARG;
     const size_t need = bias ? pa::bias_table_bytes(num_heads, a.bias) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return PA_ERR_INVALID_ARG;

@@ -1745,7 +1745,8 @@ cudaError_t launch_packed_attn(const PackedArgs &a, void *out, float *lse, cudaS
     kp.num_kv_heads = a.num_kv_heads;
     kp.group = a.num_heads / a.num_kv_heads;
     kp.tok_per_tile = BM / kp.group;
-    kp.q_items = static_cast<int>(query_items(kp.group, a.max_seqlen_q));
+    // (One at least: a sequence that is longer than a maximum of 0 is looked at too, and flagged.)
+    kp.q_items = static_cast<int>(query_items(kp.group, a.max_seqlen_q > 0 ? a.max_seqlen_q : 1));
     kp.n_items = kp.q_items * a.num_kv_heads * a.num_seqs;
     kp.window = a.sliding_window;
     kp.kv_scale = 1.f;
