@@ -552,7 +552,8 @@ pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const
  *
  * In all of them rows behind the last sequence are left as they were, and a key that a row does
  * not see has weight 0: an infinite or NaN key or value of its sequence may reach the rows whose
- * 128-key tiles hold it (another sequence's never does).  Sequences with offsets outside the
+ * 128-key tiles hold it, and in the gradient the keys of their tiles (another sequence's never
+ * does).  A row with a NaN among the logits that it sees has NaN in out and in lse.  Sequences with offsets outside the
  * arrays, or longer than max_seqlen_q / max_seqlen_k, are flagged (PA_DEVERR_QUERY_LEN,
  * PA_DEVERR_SEQ_RANGE) and left out; where offsets that go back and forth make sequences share rows,
  * those rows' results are unspecified, or left as they were.  Outputs may not overlap inputs or one

@@ -1225,7 +1225,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     continue;
                 }
-                if (valid) p.lse[r] = l_sum > 0.f ? (m_ref + log2f(l_sum)) * kLn2 : -INFINITY;
+                // (0 where all keys are hidden; a NaN, of a row with one among its logits, stays one.)
+                if (valid) p.lse[r] = l_sum == 0.f ? -INFINITY : (m_ref + log2f(l_sum)) * kLn2;
             }
             // ---- epilogue: O / l -> bf16 rows (P V of the item's last tile is number c-1) ----
             if (!wait_warp(bar(B_ODONE + wg), (c - 1) & 1, abort_flag, p.err, p.wait_ns)) {

@@ -58,3 +58,18 @@ def test_rows_beyond_a_maximum_of_zero_are_flagged(buckets):
     c.cu_q = np.array([0, 0, 0])  # no row is in a sequence: nothing is wrong
     c.forward(out=out, lse=lse)
     assert pa.pa_read_device_error() == 0 and (out == 7.0).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("buckets", [0, 16])
+def test_a_nan_query_is_no_row_without_keys(dim, buckets):
+    c = Call([50, 200], [50, 260], 4, 2, dim, buckets, 64)
+    c.q[7, 1] = float("nan")
+    c.q[90, 3] = float("nan")
+    out, lse = c.forward()
+    bad = torch.zeros(c.q.shape[:2], dtype=torch.bool, device="cuda")
+    bad[7, 1] = bad[90, 3] = True
+    assert torch.equal(lse.isnan(), bad) and torch.equal(out.isnan().all(-1), bad) and torch.equal(out.isnan().any(-1), bad)
+    dq = c.backward(out, lse)[0]
+    assert dq[7, 1].isnan().all() and dq[90, 3].isnan().all()
+    assert pa.pa_read_device_error() == 0
