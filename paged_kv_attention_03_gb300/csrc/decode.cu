@@ -703,7 +703,7 @@ __device__ __forceinline__ void decode_split_body(const DecodeKernelParams &p, c
             acc += f * o_s[(w * 16 + row) * OSTRIDE + d];
         }
         float res = acc / L;
-        if constexpr (BIAS) res = L > 0.f ? res : 0.f;  // (a bias of -inf can hide every key)
+        if constexpr (BIAS) res = L == 0.f ? 0.f : res;  // (a bias of -inf can hide every key; a NaN stays one)
         if constexpr (FP8) res *= p.kv_scale;  // V elements read code * kv_scale
         const int64_t bh = static_cast<int64_t>(b) * p.num_heads + h0 + row;
         if (p.ws_o == nullptr) {

@@ -73,3 +73,59 @@ def test_a_nan_query_is_no_row_without_keys(dim, buckets):
     dq = c.backward(out, lse)[0]
     assert dq[7, 1].isnan().all() and dq[90, 3].isnan().all()
     assert pa.pa_read_device_error() == 0
+
+
+def _paged(c, block, behind_the_ends=0.0, seed=0):
+    """The case's keys in shuffled blocks.  Every other row of the cache is NaN, but those behind the end of a sequence in its last
+    block, which are read with weight 0."""
+    lens = np.diff(c.cu_k)
+    blocks = -(-lens // block)
+    total = int(blocks.sum()) + 5
+    order = np.random.default_rng(seed).permutation(total)
+    table = np.full((len(lens), max(int(blocks.max()), 1)), -1)
+    hkv, d = c.k.shape[1:]
+    caches = [torch.full((total, block, hkv, d), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for i, n in enumerate(lens):
+        table[i, :blocks[i]], order = order[:blocks[i]], order[blocks[i]:]
+        for cache, rows in zip(caches, (c.k, c.v)):
+            for b in range(blocks[i]):
+                part = rows[c.cu_k[i] + b * block:min(c.cu_k[i] + (b + 1) * block, c.cu_k[i + 1])]
+                cache[table[i, b], :len(part)] = part
+                cache[table[i, b], len(part):] = behind_the_ends
+    assert sum(int(x.isnan().all(dim=3).all(dim=2).all(dim=1).sum()) for x in caches) == 10
+    return *caches, dev(table), dev(lens)
+
+
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("heads,hkv,dim", [(8, 2, 64), (20, 1, 128)])
+def test_blocks_of_nobody_are_not_read(heads, hkv, dim, block):
+    new, lens = [70, 1, 33, 1], [70, 600, 300, 17]
+    c = Call(new, lens, heads, hkv, dim, 32, 128)
+    k, v, table, seq_lens = _paged(c, block)
+    r = c.values()
+    e = 2.0 ** -22 * (600 + 64 + 128 * float(r["logit"].max()))
+    tol = (U + 2 * e) * r["out_abs"] + 2 * U * r["out"].abs()
+    out = pa.pa_varlen_prefill_bias(c.q, k, v, dev(c.cu_q), seq_lens, table, 70, 600, c.scale, c.bias, 128)
+    assert torch.isfinite(out).all() and ((out.double() - r["out"]).abs() <= tol).all()
+    last = torch.as_tensor(c.cu_q[1:] - 1).cuda()
+    for splits in (0, 1, 4):
+        out = pa.pa_decode_bias(c.q[last], k, v, table, seq_lens, 600, c.scale, c.bias, 128, 0, splits)
+        assert torch.isfinite(out).all() and ((out.double() - r["out"][last]).abs() <= tol[last]).all()
+    assert pa.pa_read_device_error() == 0
+
+
+@pytest.mark.parametrize("splits", [0, 1, 3])
+def test_decode_keeps_nan(splits):
+    """A NaN query, key or bias gives NaN with the bias as without it, however the keys are split."""
+    lens = [40, 300, 90]
+    c = Call([1, 1, 1], lens, 4, 2, 64, 16, 64)
+    k, v, table, seq_lens = _paged(c, 16)
+    c.q[0, 2] = float("nan")
+    k[table[2, 1], 3, 1] = float("nan")
+    c.bias[5, 0] = float("nan")
+    out = pa.pa_decode_bias(c.q, k, v, table, seq_lens, 300, c.scale, c.bias, 64, 0, splits)
+    nan = out.isnan().all(-1)
+    want = torch.zeros(3, 4, dtype=torch.bool, device="cuda")
+    want[0, 2] = want[2, 2] = want[2, 3] = True
+    want[:, 0] = True  # distance 5 is in every sequence
+    assert torch.equal(nan, want) and torch.equal(out.isnan().any(-1), want)
