@@ -542,11 +542,12 @@ pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const
  *         P = e^{s - lse},  dP = dout V^T,  dS = P (dP - sum_j P_j dP_j),
  *         dq = scale dS K,  dk = scale dS^T q,  dv = P^T dout,  dbias[b] = sum of dS over bucket b,
  *     dk and dv summed over the query heads of a kv head.  Keys and rows that nothing pairs get
- *     zeros, and so do buckets that no pair reaches.  No atomics: equal calls
- *     give equal bits.  P and dS are rounded to bf16 for the products, all sums are fp32; dbias
- *     is summed from unrounded terms.  In dq a row's sum_j P_j dP_j is exact to 2^-8 sum_j |dS_j|:
- *     it is taken from dout . out where that holds, and the rows where it does not (a sharp softmax)
- *     are computed a second time, with the sum itself, as dk and dbias are.
+ *     zeros, and so do buckets that no pair reaches.  Rows with lse below -1e6 (their keys all have
+ *     biases like -1e9) count as rows without keys: fp32 leaves e^{s - lse} no digit there.
+ *     No atomics: equal calls give equal bits.  P and dS are rounded to bf16 for the products, all
+ *     sums are fp32; dbias is summed from unrounded terms.  In dq a row's sum_j P_j dP_j is exact to
+ *     2^-8 sum_j |dS_j|: it is taken from dout . out where that holds, and the rows where it does
+ *     not (a sharp softmax) are computed a second time, with the sum itself, as dk and dbias are.
  * pa_decode_bias, pa_varlen_prefill_bias: pa_decode and pa_varlen_prefill (optional store of new
  *     tokens included) with the bias, which is required.
  *

@@ -70,6 +70,9 @@ constexpr int kFewKeys = 128;
 // squares, so that a weight spread over ten keys or more never is.  Items (128 rows of a head) done again with 2048 keys: none
 // with logits of standard deviation 1, 12 % with 2, nearly all from 3 on, which take twice the products then.
 constexpr float kMoved = 0.00390625f;
+// Rows whose lse lies below see nothing but keys with biases that stand for hiding them (-1e9, say).  P = e^(s - lse) is off by
+// a factor of up to e^(2^-22 |lse|), 1.3 here and anything from 0 to infinity at -1e9: they have no gradient, as rows without keys.
+constexpr float kNoDigits = -1.0e6f;
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
 
 // 128 queries of a sequence.
@@ -108,7 +111,7 @@ struct GradParams {
     __nv_bfloat16 *dk;
     __nv_bfloat16 *dv;
     int64_t dq_stride, dk_stride, dv_stride;
-    const float *lse2;  // [num_heads, total_q]: lse in base 2, +inf for a row without keys
+    const float *lse2;  // [num_heads, total_q]: lse in base 2, +inf for a row without keys (or with an lse below kNoDigits)
     float *delta;       // [num_heads, total_q]: D
     const float *bias_table;
     float *partial;     // [query tiles, num_heads, 8 warps, num_buckets]
@@ -659,7 +662,7 @@ __global__ void __launch_bounds__(256, 8)
         for (int o = LANES / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
         if (l == 0 && in) {
             const float e = lse[row];
-            s_l[r % 8][r / 8] = e == -INFINITY ? INFINITY : e * kLog2e;
+            s_l[r % 8][r / 8] = e < kNoDigits ? INFINITY : e * kLog2e;
             s_d[r % 8][r / 8] = d;
         }
     }

@@ -129,3 +129,29 @@ def test_decode_keeps_nan(splits):
     want[0, 2] = want[2, 2] = want[2, 3] = True
     want[:, 0] = True  # distance 5 is in every sequence
     assert torch.equal(nan, want) and torch.equal(out.isnan().any(-1), want)
+
+
+@pytest.mark.parametrize("low", [-1e9, -3e7])
+@pytest.mark.parametrize("heads,hkv,dim", [(4, 2, 64), (8, 1, 128)])
+def test_rows_of_nothing_but_very_low_biases_have_no_gradient(low, heads, hkv, dim):
+    """lse of such rows has no digits left for e^(s - lse).  Keys with such a bias beside others have weight 0."""
+    c = Call([200, 1, 30], [260, 1, 30], heads, hkv, dim, 16, 64)
+    c.bias[0, 1] = low  # a position does not see itself: the first one of a sequence sees nothing else
+    c.bias[:, 3] = low
+    c.bias[9:, 2] = low
+    out, lse = c.forward()
+    grads = c.backward(out, lse)
+    assert pa.pa_read_device_error() == 0
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    dout = c.dout.clone()
+    dout[lse < -1e6] = 0.0
+    assert (dout[:, 3] == 0).all() and (dout[200, 1] == 0).all() and (dout[:, 0] == c.dout[:, 0]).all()
+    c.bias[c.bias == low] = float("-inf")
+    r = c.values(dout)
+    e = 2.0 ** -22 * (260 + 64 + 128 * float(r["logit"].max()))
+    moved = U * r["ds_abs"] + 2 * e * r["mean"]
+    tols = {"dq": (U + 2 * e) * r["dq_abs"] + 2 * e * r["dq_terms"] + moved[..., None] * r["dq_rows"], "dk": (U + 2 * e) * r["dk_abs"] + 2 * e * r["dk_terms"],
+            "dv": (U + 2 * e) * r["dv_abs"], "dbias": 2 * e * r["dbias_terms"]}
+    for name, got in zip(("dq", "dk", "dv", "dbias"), grads):
+        assert torch.isfinite(got).all(), name
+        assert ((got.double() - r[name]).abs() <= tols[name] + U * r[name].abs() + 2.0 ** -96).all(), name
