@@ -12,6 +12,7 @@ import ctypes
 import functools
 import os
 import threading
+import warnings
 
 import torch
 
@@ -647,9 +648,16 @@ def pa_varlen_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens
                    ) -> tuple[torch.Tensor, torch.Tensor]:
     """Causal attention of packed sequences on plain rows: q [Tq, H, D], k / v [Tk, Hkv, D] ->
     (out [Tq, H, D] bf16, lse [Tq, H] fp32).  q, k and v may be slices of a wider row.  bias
-    [num_buckets, H] fp32: a learned bias by relative position, in buckets up to max_distance."""
+    [num_buckets, H] fp32: a learned bias by relative position, in buckets up to max_distance.
+
+    No autograd graph is recorded, and a call that would need one warns: a model wraps this call and
+    pa_varlen_attn_backward in a torch.autograd.Function."""
     lib = _lib or load()
     dev = _device_of(q, "q")
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or
+                                    (bias is not None and bias.requires_grad)):
+        warnings.warn("pa_varlen_attn records no autograd graph: out has no gradient but by "
+                      "pa_varlen_attn_backward", RuntimeWarning, stacklevel=2)
     total_q, heads, d = q.shape
     total_k, hkv, _ = k.shape
     n = cu_seqlens_q.shape[0] - 1

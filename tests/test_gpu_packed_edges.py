@@ -155,3 +155,48 @@ def test_rows_of_nothing_but_very_low_biases_have_no_gradient(low, heads, hkv, d
     for name, got in zip(("dq", "dk", "dv", "dbias"), grads):
         assert torch.isfinite(got).all(), name
         assert ((got.double() - r[name]).abs() <= tols[name] + U * r[name].abs() + 2.0 ** -96).all(), name
+
+
+def test_a_call_that_records_no_graph_says_so():
+    import warnings
+    c = Call([20], [20], 4, 2, 64, 16, 64)
+    for name in ("q", "k", "v", "bias"):
+        t = getattr(c, name)
+        t.requires_grad_(True)
+        with pytest.warns(RuntimeWarning, match="pa_varlen_attn_backward"):
+            out, lse = c.forward()
+        assert not out.requires_grad and not lse.requires_grad
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            with torch.no_grad():
+                c.forward()
+            t.requires_grad_(False)
+            c.forward()
+
+
+def test_an_autograd_function_of_the_two_calls():
+    """What a model wraps the two calls in: no warning, and the gradients of the calls."""
+    import warnings
+    c = Call([70, 130], [70, 130], 4, 2, 64, 16, 64)
+
+    class Attention(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, v, bias):
+            c.q, c.k, c.v, c.bias = q, k, v, bias
+            out, lse = c.forward()
+            ctx.save_for_backward(q, k, v, bias, out, lse)
+            return out
+
+        @staticmethod
+        def backward(ctx, dout):
+            q, k, v, bias, out, lse = ctx.saved_tensors
+            return pa.pa_varlen_attn_backward(dout.contiguous(), q, k, v, out, lse, *c.args(), bias=bias, max_distance=64)
+
+    out, lse = c.forward()
+    want = c.backward(out, lse)
+    leaves = [t.clone().requires_grad_(True) for t in (c.q, c.k, c.v, c.bias)]
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        Attention.apply(*leaves).backward(c.dout)
+    for t, g in zip(leaves, want):
+        assert torch.equal(t.grad, g)
