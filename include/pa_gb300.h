@@ -570,8 +570,9 @@ pa_status pa_varlen_prefill_fp4(void *out, const void *q, const void *key, const
  * (with a bias also at least 1e-20, and bias / scale inside the fp32 range); total_q and
  * total_k below 2^30; num_seqs <= 65535; the 128-row tiles of max_seqlen_q (max_seqlen_k) times
  * num_seqs times num_heads (num_kv_heads) below 2^31; in the backward call also (total_q / 128 +
- * num_seqs) num_heads and (total_k / 128 + num_seqs) num_heads.  Sizes of the paged calls as pa_decode and pa_varlen_prefill, but at
- * most 64 query heads a kv head.  Size functions return 0 for what is not supported.
+ * num_seqs) num_heads and (total_k / 128 + num_seqs) num_heads.  Sizes of the paged calls as
+ * pa_decode and pa_varlen_prefill, but at most 64 query heads a kv head; their caches are bf16 (the
+ * E4M3 and the 4-bit cache have no form with the bias).  Size functions return 0 for what is not supported.
  */
 size_t pa_relative_bias_workspace_size(int num_heads, int num_buckets, int max_distance);
 size_t pa_varlen_attn_backward_workspace_size(int total_q, int total_k, int num_seqs,

@@ -32,13 +32,14 @@
 // tile they came from, and are the first operand of the next product from there.
 //
 // Measured (packed sequences, 32/8 heads of 128; the products of each kernel over its time):
-//  * two of 6000-8192 tokens, no bias: dQ 658 us (1.70 PFLOP/s of three products, 0.88 of the bf16
-//    peak), dK/dV 896 us (1.67): products nearly back to back; the rest are the waits between them;
-//  * sixteen of 128-2048 tokens, 32 buckets to 128: dQ 294 us (0.81), dK/dV 280 us (1.14).  A block of
+//  * two of 6000-8192 tokens, no bias: dQ 717 us (1.57 PFLOP/s of three products, 0.81 of the bf16
+//    peak; 657 us without the sums of |dS| that tell which rows are done again, 1380-1420 where nearly all
+//    are, with queries three or four times as large), dK/dV 900 us (1.67);
+//  * sixteen of 128-2048 tokens, 32 buckets to 128: dQ 316 us (0.75; 295 and 590), dK/dV 281 us (1.14).  A block of
 //    dQ takes 216 steps, 58 of them near tiles, in 30 items of which the last step's chain (logits, D,
 //    dS, diagonals, product, rows out) has nothing beside it;
-//  * 128 of 128 tokens, where an item is one step: dQ 96 us without a bias (the bytes alone take 69),
-//    119 with one, dK/dV 77 and 79 (59).
+//  * 128 of 128 tokens, where an item is one step: dQ 104 us without a bias (the bytes alone take 69),
+//    130 with one, dK/dV 77 and 79 (59).
 #include <cuda.h>
 
 #include <atomic>
@@ -318,8 +319,8 @@ __device__ __forceinline__ void zero_rows(__nv_bfloat16 *dst, int64_t stride, in
 // Row - column is then the same for all (a, b) with the same a - b, 11 pairs of distances for 64 elements:
 // a bias costs a thread 22 reads, masks are 22 comparisons, and sums along diagonals begin with additions in
 // registers.  (A thread a row needs 64 reads, comparisons and shuffles: dQ of 16 sequences of 128-2048 tokens,
-// 32/8 heads of 128 took 375 us that way, 318 this way, 294 with what followed; without a bias of two documents of 6000-8192 tokens
-// 648 against 664.)
+// 32/8 heads of 128 took 375 us that way, 318 this way; without a bias of two documents of 6000-8192 tokens
+// 648 against 664.  Both before what followed.)
 __device__ __forceinline__ int pair_at(int a, int b) { return 4 * b + 2 * (a & 1); }
 __device__ __forceinline__ uint64_t block_pair(const float (&w)[2][32], int a, int b) {
     return f2_pack(w[a >> 1][pair_at(a, b)], w[a >> 1][pair_at(a, b) + 1]);
@@ -430,8 +431,9 @@ struct PlanParams {
 };
 constexpr int kPlanBins = 1024;  // longer tiles share the last bin
 // Key tiles of more steps than an SM's share and 8 more are split: few kv heads with many queries each have
-// few long items.  dK/dV with and without: one sequence of 2048, 16/1 heads 59 and 367 us, of 4096, 8/2 heads 64
-// and 178, of 16384, 8/1 heads 820 and 1369.  Parts leave their sums in fp32; the last one to arrive, warp
+// few long items.  dK/dV with and without, us: one sequence of 2048, 32/8 heads of 128 71 and 97, 16/1 57 and 348; of 4096,
+// 32/4 heads of 64 184 and 301, 8/2 of 128 65 and 177; of 16384, 8/1 of 128 820 and 1367; of 3000 and 1100, 16/2 of 64 60 and 219.  Where
+// the share of an SM is nearly a tile's steps the parts cost more than they even out: 4096, 32/8 of 128 204 and 181.  Parts leave their sums in fp32; the last one to arrive, warp
 // by warp, adds them up in the parts' order.  A part costs about five steps, for its keys and its sums.  So many
 // slots suffice: a split tile has fewer parts than twice its steps over an SM's share.
 constexpr int kMinSteps = 8, kMaxSlots = 2 * kPlanSms + 1;
@@ -622,7 +624,7 @@ __device__ __forceinline__ void plan_lists(const PlanParams &p) {
 // Bound by its bytes: 44 us for out and dout of 17400 tokens, 32 heads of 128 (285 MB, 6.5 TB/s).
 // lse in base 2 and dout_i out_i, both as [num_heads, total_q]: a block takes 8 tokens of 8 heads, half
 // a warp (128 dims) or a quarter (64) a row.  The blocks behind the first write the bias by distance (with a
-// launch of its own the smallest training step took 72 us, the host's, instead of 64-69).  The first block makes
+// launch of its own the smallest training step took 72 us, the host's, instead of 64-69; 64-74 across boxes).  The first block makes
 // the lists, for which it spills registers: with the 48 that it would take the others are too few on an SM
 // (44 us against 39 for 15000 tokens, 32 heads of 128).
 template <int HD>
