@@ -431,10 +431,11 @@ struct PlanParams {
 };
 constexpr int kPlanBins = 1024;  // longer tiles share the last bin
 // Key tiles of more steps than an SM's share and 8 more are split: few kv heads with many queries each have
-// few long items.  dK/dV with and without, us: one sequence of 2048, 32/8 heads of 128 71 and 97, 16/1 57 and 348; of 4096,
-// 32/4 heads of 64 184 and 301, 8/2 of 128 65 and 177; of 16384, 8/1 of 128 820 and 1367; of 3000 and 1100, 16/2 of 64 60 and 219.  Where
-// the share of an SM is nearly a tile's steps the parts cost more than they even out: 4096, 32/8 of 128 204 and 181.  Parts leave their sums in fp32; the last one to arrive, warp
-// by warp, adds them up in the parts' order.  A part costs about five steps, for its keys and its sums.  So many
+// few long items.  dK/dV with and without, us: one sequence of 2048, 32/8 heads of 128 71 and 97, 16/1 57 and
+// 348; of 4096, 32/4 heads of 64 184 and 301, 8/2 of 128 65 and 177; of 16384, 8/1 of 128 820 and 1367; of 3000
+// and 1100, 16/2 of 64 60 and 219.  Where an SM's share is nearly a tile's steps the parts cost more than they even
+// out: 4096, 32/8 of 128 204 and 181.  Parts leave their sums in fp32; the last one to arrive, warp by warp,
+// adds them up in the parts' order.  A part costs about five steps, for its keys and its sums.  So many
 // slots suffice: a split tile has fewer parts than twice its steps over an SM's share.
 constexpr int kMinSteps = 8, kMaxSlots = 2 * kPlanSms + 1;
 
@@ -1172,7 +1173,7 @@ __global__ void __launch_bounds__(kThreads, 1) grad_q_kernel(const __grid_consta
                 if constexpr (BIAS) {
                     __syncwarp();
                     if (table_here && lane == 0) mbar_arrive(bar(B_TABFREE + (items & 1)));
-    if (pass == 0) {
+                    if (pass == 0) {
                         const float t_far = warp_sum(d_far - ((delta[0] * w_far[0] + delta[1] * w_far[1]) + (delta[2] * w_far[2] + delta[3] * w_far[3])));
 #pragma unroll
                         for (int k4 = 0; k4 < 4; ++k4) {
